@@ -384,6 +384,112 @@ moe_status_t moe_get_plan(const moe_problem_t* p, moe_plan_t* plan);
 /* Plan for a device with `num_sms` SMs; pure host computation, needs no GPU. */
 moe_status_t moe_get_plan_for_sms(const moe_problem_t* p, int32_t num_sms, moe_plan_t* plan);
 
+/* ------------------------------------------------------------------------
+ * The operators around the layer: one pre-norm MoE block is residual add + RMS
+ * norm, router scores, the routed experts (moe_forward, or moe_forward_few for
+ * a few tokens) and a shared expert or dense layer in 8-bit floating point with
+ * a scale per block of 128 (the weight format of the DeepSeek-V3 checkpoints).
+ * The conventions at the top hold.  Strides count elements between rows (the
+ * elements of a row are adjacent); rows of one tensor must not overlap.  These
+ * calls use only the 256-byte error header of a workspace, so any workspace
+ * will do, and one of MOE_OP_WORKSPACE_BYTES. */
+
+typedef enum { MOE_T_BF16 = 0, MOE_T_F16 = 1, MOE_T_F32 = 2 } moe_dtype_t;
+typedef enum { MOE_QUANT_NONE = 0, MOE_QUANT_BLOCK128 = 1, MOE_QUANT_TOKEN = 2 } moe_quant_t;
+
+#define MOE_OP_WORKSPACE_BYTES 256
+
+/* T rows of H columns, 1 <= H <= 16384, eps >= 0. */
+typedef struct {
+  int32_t T, H;
+  int32_t dtype;        /* moe_dtype_t of x, residual, residual_out and y */
+  int32_t weight_dtype; /* moe_dtype_t of weight: dtype or MOE_T_F32 */
+  int32_t quant;        /* moe_quant_t */
+  float eps;
+} moe_norm_t;
+
+/* Residual add + RMS norm, optionally with an 8-bit copy of the result:
+ *   s = x + residual (x alone where residual is NULL), in float
+ *   residual_out = s rounded to dtype (needs residual; NULL: not written)
+ *   v = s * weight / sqrt(mean(s^2) + eps), in float over the unrounded s
+ *   y = v rounded to dtype (NULL: not written)
+ *   scales, codes (quant other than NONE): per block of 128 columns (float
+ *     [T, ceil(H / 128)], the last block may be short) or per row (float [T]),
+ *     scale = max |v| / 448, or 1 where every v is 0; codes uint8 e4m3 [T, H],
+ *     contiguous, the code of v / scale (round to nearest even, saturating),
+ *     from the unrounded v.  NaN propagates to its row (y, and e4m3 NaN codes).
+ * residual_out may be the residual itself (same stride); otherwise inputs and
+ * outputs do not overlap.  Any row alignment of at least one element is taken;
+ * rows that all start on 16-byte boundaries with H % 8 == 0 are read in
+ * 16-byte pieces. */
+moe_status_t moe_add_rms_norm(const moe_norm_t* n, const void* x, int64_t x_stride,
+                              const void* residual, int64_t residual_stride, const void* weight,
+                              void* residual_out, int64_t residual_out_stride, void* y,
+                              int64_t y_stride, void* codes, float* scales, moe_stream_t stream);
+
+/* T tokens of H channels against E experts: H % 8 == 0, 1 <= E <= 1024. */
+typedef struct {
+  int32_t T, H, E;
+  int32_t dtype; /* MOE_T_BF16 or MOE_T_F16, of x and w */
+} moe_router_t;
+
+/* Router scores: logits[t, e] = sum_h x[t, h] w[e, h], float [T, E] contiguous,
+ * accumulated in float.  x [T, H] and w [E, H]: 16-byte aligned, strides
+ * multiples of 8. */
+moe_status_t moe_router_logits(const moe_router_t* r, const void* x, int64_t x_stride, const void* w,
+                               int64_t w_stride, float* logits, void* ws, size_t ws_bytes,
+                               moe_stream_t stream);
+
+/* M rows against N weight rows of depth K: M, N >= 0 rows, K % 16 == 0, K >= 16. */
+typedef struct {
+  int32_t M, N, K;
+  int32_t out_dtype;  /* moe_dtype_t of out (moe_gemm_fp8_block) */
+  int32_t accumulate; /* 1: out += product, 0: out = product (moe_gemm_fp8_block) */
+} moe_fp8_gemm_t;
+
+/* Product in 8-bit floating point with a scale per block of 128 along K:
+ *   out[m, n] = sum_b a_scale[m, b] * w_scale[n / 128, b] *
+ *               sum_{k in block b} a[m, k] * w[n, k]
+ *   a        e4m3 [M, K], a_scale float [M, ceil(K / 128)] (as moe_add_rms_norm
+ *            and moe_gemm_fp8_block_swiglu write them)
+ *   w        e4m3 [N, K], w_scale float [ceil(N / 128), ceil(K / 128)] contiguous
+ *   out      out_dtype [M, N]; with accumulate its old values are added in float
+ * Each block's product and the sum over blocks are formed in float, rounded
+ * once at the end.  a and w: 16-byte aligned, strides multiples of 16. */
+moe_status_t moe_gemm_fp8_block(const moe_fp8_gemm_t* g, const void* a, int64_t a_stride,
+                                const float* a_scale, int64_t a_scale_stride, const void* w,
+                                int64_t w_stride, const float* w_scale, void* out,
+                                int64_t out_stride, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* The gate and up projections with SwiGLU and the requantisation that the down
+ * projection reads: with h = the product above of a and w13 [2N, K] (rows
+ * [0, N) gate, [N, 2N) up; w13_scale [2N / 128, ceil(K / 128)]), N % 128 == 0,
+ *   v[m, n] = silu(h[m, n]) * h[m, N + n]   (float, not rounded)
+ *   scales[m, b] = max |v| over columns [128 b, 128 b + 128) / 448 (1 if all 0)
+ *   codes[m, n]  = e4m3(v / scale), uint8 [M, N] contiguous; scales float [M, N / 128].
+ * out_dtype is not used; accumulate must be 0. */
+moe_status_t moe_gemm_fp8_block_swiglu(const moe_fp8_gemm_t* g, const void* a, int64_t a_stride,
+                                       const float* a_scale, int64_t a_scale_stride, const void* w13,
+                                       int64_t w13_stride, const float* w13_scale, void* codes,
+                                       float* scales, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* The whole layer for a few tokens (p->T <= MOE_FEW_MAX_TOKENS, else
+ * MOE_ERR_UNSUPPORTED): arguments, weight formats and meaning of moe_forward,
+ * in two launches that stream the chosen experts' weights once.  All sums are
+ * held in float and nothing is rounded between the gate and out: the SwiGLU
+ * output stays float, int4 / int8 weights enter as (code - zero) * scale
+ * unrounded, and y is not rounded per expert, so results differ from
+ * moe_forward's by its roundings.  fp8 experts take activations as their codes,
+ * e4m3(x / a1) and e4m3(act / a2); dynamic scales are max |x| / 448 and
+ * max |act| / 448 over the call (1 for all zeros).  The workspace holds
+ * moe_few_workspace_size() bytes (0 for an invalid problem or T above the
+ * limit). */
+#define MOE_FEW_MAX_TOKENS 8
+size_t moe_few_workspace_size(const moe_problem_t* p);
+moe_status_t moe_forward_few(const moe_problem_t* p, const moe_weights_t* w, const void* x,
+                             const float* logits, const float* bias, void* out, void* ws,
+                             size_t ws_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

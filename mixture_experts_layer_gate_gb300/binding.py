@@ -24,7 +24,14 @@ EXPORTED = ("moe_scratch_size", "moe_workspace_size", "moe_padded_capacity", "mo
             "moe_align_permute", "moe_align_block_size", "moe_grouped_gemm_swiglu",
             "moe_grouped_gemm_down", "moe_unpermute_reduce", "moe_forward", "moe_get_device_error",
             "moe_status_string", "moe_get_plan", "moe_get_plan_for_sms", "moe_align_permute_noalloc",
-            "moe_dynamic_scales", "moe_launch_count", "moe_set_tuning", "moe_repack_int4")
+            "moe_dynamic_scales", "moe_launch_count", "moe_set_tuning", "moe_repack_int4",
+            "moe_add_rms_norm", "moe_router_logits", "moe_gemm_fp8_block", "moe_gemm_fp8_block_swiglu",
+            "moe_few_workspace_size", "moe_forward_few")
+
+DTYPES = {"bf16": 0, "f16": 1, "f32": 2}
+QUANTS = {"none": 0, "block": 1, "token": 2}
+OP_WORKSPACE_BYTES = 256
+FEW_MAX_TOKENS = 8
 
 
 class MoEError(RuntimeError):
@@ -71,6 +78,20 @@ class Tuning(ctypes.Structure):
                                              "epi_warps", "acc_bufs")]
 
 
+class NormProblem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("quant", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class RouterProblem(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("E", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class Fp8GemmProblem(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32)]
+
+
 TUNING_KNOBS = tuple(n for n, _ in Tuning._fields_)
 
 _lib = None
@@ -86,6 +107,7 @@ def load(path: str = LIB_PATH):
     lib = ctypes.CDLL(path)
     P = ctypes.POINTER(Problem)
     vp, sz, i32, st = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int
+    i64 = ctypes.c_int64
     sig = {
         "moe_scratch_size": (sz, [P]),
         "moe_workspace_size": (sz, [P]),
@@ -106,6 +128,14 @@ def load(path: str = LIB_PATH):
         "moe_launch_count": (ctypes.c_uint64, []),
         "moe_set_tuning": (st, [ctypes.POINTER(Tuning)]),
         "moe_repack_int4": (st, [vp, vp, sz, vp]),
+        "moe_add_rms_norm": (st, [ctypes.POINTER(NormProblem), vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp]),
+        "moe_router_logits": (st, [ctypes.POINTER(RouterProblem), vp, i64, vp, i64, vp, vp, sz, vp]),
+        "moe_gemm_fp8_block": (st, [ctypes.POINTER(Fp8GemmProblem), vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, sz,
+                                    vp]),
+        "moe_gemm_fp8_block_swiglu": (st, [ctypes.POINTER(Fp8GemmProblem), vp, i64, vp, i64, vp, i64, vp, vp, vp, vp,
+                                           sz, vp]),
+        "moe_few_workspace_size": (sz, [P]),
+        "moe_forward_few": (st, [P, ctypes.POINTER(WeightsStruct), vp, vp, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -296,6 +326,124 @@ class tuning:
 
     def __exit__(self, *exc):
         set_tuning()
+
+
+# ------------------------------------------------------- operators around the layer
+
+
+def norm_problem(T, H, dtype="bf16", weight_dtype=None, eps=1e-6, quant="none") -> NormProblem:
+    """T rows of H columns for add_rms_norm; quant: "none", "block" (a scale per 128 columns) or "token"."""
+    return NormProblem(int(T), int(H), DTYPES[dtype], DTYPES[weight_dtype or dtype], QUANTS[quant], float(eps))
+
+
+def router_problem(T, H, E, dtype="bf16") -> RouterProblem:
+    return RouterProblem(int(T), int(H), int(E), DTYPES[dtype])
+
+
+def fp8_gemm_problem(M, N, K, out_dtype="bf16", accumulate=False) -> Fp8GemmProblem:
+    """M rows, N output columns, depth K; for gemm_fp8_block_swiglu the weight has 2N rows.  accumulate: the
+    product is added to out."""
+    return Fp8GemmProblem(int(M), int(N), int(K), DTYPES[out_dtype], int(bool(accumulate)))
+
+
+def alloc_op_workspace(device):
+    """Zeroed error header for router_logits and the gemm_fp8_block calls (any workspace serves as well)."""
+    import torch
+    return torch.zeros(OP_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+
+
+def _rows(t, rows, cols, size, what):
+    """Device pointer and row stride of a [rows, cols] tensor of `size`-byte elements; None stays None."""
+    if t is None:
+        return None, 0
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols or t.element_size() != size or not t.is_cuda \
+            or (stride[1] != 1 and cols > 1):
+        raise ValueError(f"{what}: a CUDA tensor [{rows}, {cols}] of {size}-byte elements with adjacent columns")
+    return t.data_ptr(), stride[0] if rows > 1 else max(stride[0], cols)
+
+
+def _flat(t, n, size, what):
+    """Device pointer of a contiguous tensor of n elements of `size` bytes; None stays None."""
+    if t is None:
+        return None
+    if t.numel() != n or t.element_size() != size or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous CUDA tensor of {n} elements of {size} bytes")
+    return t.data_ptr()
+
+
+_SIZE = (2, 2, 4)  # bytes of a moe_dtype_t
+
+
+def add_rms_norm(n: NormProblem, x, weight, residual=None, residual_out=None, y=None, codes=None, scales=None,
+                 stream=None):
+    """moe_add_rms_norm.  x, residual, residual_out, y: [T, H] of n's dtype (rows may be strided; residual_out may
+    be residual); weight [H]; codes [T, H] (uint8 or float8_e4m3fn) and scales (float32, [T, ceil(H / 128)] or
+    [T]) exactly where n quantises."""
+    T, H, b = n.T, n.H, _SIZE[n.dtype]
+    px, sx = _rows(x, T, H, b, "x")
+    pr, sr = _rows(residual, T, H, b, "residual")
+    po, so = _rows(residual_out, T, H, b, "residual_out")
+    py, sy = _rows(y, T, H, b, "y")
+    _check(load().moe_add_rms_norm(
+        ctypes.byref(n), px, sx, pr, sr, _flat(weight, H, _SIZE[n.weight_dtype], "weight"), po, so, py, sy,
+        _flat(codes, T * H, 1, "codes"), _flat(scales, T * (-(-H // 128) if n.quant == 1 else 1), 4, "scales"),
+        _stream(stream)), "moe_add_rms_norm")
+
+
+def router_logits(r: RouterProblem, x, w, logits, ws, stream=None):
+    """moe_router_logits: x [T, H] and w [E, H] (rows may be strided) -> logits float32 [T, E]."""
+    px, sx = _rows(x, r.T, r.H, 2, "x")
+    pw, sw = _rows(w, r.E, r.H, 2, "w")
+    _check(load().moe_router_logits(ctypes.byref(r), px, sx, pw, sw, _flat(logits, r.T * r.E, 4, "logits"),
+                                    ws.data_ptr(), ws.numel(), _stream(stream)), "moe_router_logits")
+
+
+def gemm_fp8_block(g: Fp8GemmProblem, a, a_scale, w, w_scale, out, ws, stream=None):
+    """moe_gemm_fp8_block: a [M, K], w [N, K] (uint8 or float8_e4m3fn), a_scale [M, ceil(K / 128)] and w_scale
+    [ceil(N / 128), ceil(K / 128)] float32 -> out [M, N] of g's out_dtype."""
+    M, N, K = g.M, g.N, g.K
+    kb = -(-K // 128)
+    pa, sa = _rows(a, M, K, 1, "a")
+    ps, ss = _rows(a_scale, M, kb, 4, "a_scale")
+    pw, sw = _rows(w, N, K, 1, "w")
+    po, so = _rows(out, M, N, _SIZE[g.out_dtype], "out")
+    _check(load().moe_gemm_fp8_block(ctypes.byref(g), pa, sa, ps, ss, pw, sw,
+                                     _flat(w_scale, -(-N // 128) * kb, 4, "w_scale"), po, so, ws.data_ptr(),
+                                     ws.numel(), _stream(stream)), "moe_gemm_fp8_block")
+
+
+def gemm_fp8_block_swiglu(g: Fp8GemmProblem, a, a_scale, w13, w13_scale, codes, scales, ws, stream=None):
+    """moe_gemm_fp8_block_swiglu: a [M, K], w13 [2N, K] with their scales -> codes [M, N], scales [M, N / 128]."""
+    M, N, K = g.M, g.N, g.K
+    kb = -(-K // 128)
+    pa, sa = _rows(a, M, K, 1, "a")
+    ps, ss = _rows(a_scale, M, kb, 4, "a_scale")
+    pw, sw = _rows(w13, 2 * N, K, 1, "w13")
+    _check(load().moe_gemm_fp8_block_swiglu(ctypes.byref(g), pa, sa, ps, ss, pw, sw,
+                                            _flat(w13_scale, -(-2 * N // 128) * kb, 4, "w13_scale"),
+                                            _flat(codes, M * N, 1, "codes"), _flat(scales, M * (N // 128), 4, "scales"),
+                                            ws.data_ptr(), ws.numel(), _stream(stream)), "moe_gemm_fp8_block_swiglu")
+
+
+def few_workspace_size(p: Problem) -> int:
+    return int(load().moe_few_workspace_size(ctypes.byref(p)))
+
+
+def alloc_few_workspace(p: Problem, device):
+    """Zeroed workspace for forward_few."""
+    import torch
+    n = few_workspace_size(p)
+    if n == 0:
+        raise MoEError(2 if p.T > FEW_MAX_TOKENS else 1, "few workspace size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def forward_few(p: Problem, w: Weights, x, logits, bias, out, ws, stream=None):
+    """moe_forward_few: the whole layer for at most FEW_MAX_TOKENS tokens in two launches."""
+    _check(load().moe_forward_few(ctypes.byref(p), ctypes.byref(w.struct), x.data_ptr(), logits.data_ptr(),
+                                  _ptr(bias), out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)),
+           "moe_forward_few")
 
 
 class MoELayer:

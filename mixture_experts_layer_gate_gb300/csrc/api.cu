@@ -650,7 +650,23 @@ moe_status_t run_gemm(const moe_problem_t& p, const moe_weights_t& wt, bool up, 
   return cuda_status(err);
 }
 
-moe_status_t check_weights(const moe_problem_t& p, const moe_weights_t* w) {
+moe_status_t check_ws(const moe_problem_t& p, void* ws, size_t ws_bytes, bool full) {
+  if (ws == nullptr || !aligned(ws, 256)) return MOE_ERR_WORKSPACE;
+  const Layout L = layout_of(p);
+  if (ws_bytes < (full ? L.total : L.scratch_end)) return MOE_ERR_WORKSPACE;
+  return MOE_OK;
+}
+
+#define MOE_TRY(x)                       \
+  do {                                   \
+    const moe_status_t st__ = (x);       \
+    if (st__ != MOE_OK) return st__;     \
+  } while (0)
+
+}  // namespace
+
+moe_status_t moe::validate_weights(const moe_problem_t* pp, const moe_weights_t* w) {
+  const moe_problem_t& p = *pp;
   if (w == nullptr || w->w13 == nullptr || w->w2 == nullptr) return MOE_ERR_INVALID_ARG;
   if (!aligned(w->w13, 16) || !aligned(w->w2, 16)) return MOE_ERR_INVALID_ARG;
   if (p.wdtype == MOE_W_FP8_E4M3) {
@@ -668,21 +684,6 @@ moe_status_t check_weights(const moe_problem_t& p, const moe_weights_t* w) {
   }
   return MOE_OK;
 }
-
-moe_status_t check_ws(const moe_problem_t& p, void* ws, size_t ws_bytes, bool full) {
-  if (ws == nullptr || !aligned(ws, 256)) return MOE_ERR_WORKSPACE;
-  const Layout L = layout_of(p);
-  if (ws_bytes < (full ? L.total : L.scratch_end)) return MOE_ERR_WORKSPACE;
-  return MOE_OK;
-}
-
-#define MOE_TRY(x)                       \
-  do {                                   \
-    const moe_status_t st__ = (x);       \
-    if (st__ != MOE_OK) return st__;     \
-  } while (0)
-
-}  // namespace
 
 extern "C" {
 
@@ -753,7 +754,7 @@ moe_status_t moe_grouped_gemm_swiglu(const moe_problem_t* p, const moe_weights_t
                                      const void* x_perm, const int32_t* offsets, void* act,
                                      void* ws, size_t ws_bytes, moe_stream_t stream) {
   MOE_TRY(validate_problem(p));
-  MOE_TRY(check_weights(*p, w));
+  MOE_TRY(validate_weights(p, w));
   MOE_TRY(check_ws(*p, ws, ws_bytes, false));
   if (p->T == 0) return MOE_OK;
   if (!x_perm || !offsets || !act || !aligned(x_perm, 16) || !aligned(act, 16) || !aligned(offsets, 4))
@@ -765,7 +766,7 @@ moe_status_t moe_grouped_gemm_down(const moe_problem_t* p, const moe_weights_t* 
                                    const void* act, const int32_t* offsets, void* y_perm,
                                    void* ws, size_t ws_bytes, moe_stream_t stream) {
   MOE_TRY(validate_problem(p));
-  MOE_TRY(check_weights(*p, w));
+  MOE_TRY(validate_weights(p, w));
   MOE_TRY(check_ws(*p, ws, ws_bytes, false));
   if (p->T == 0) return MOE_OK;
   if (!act || !offsets || !y_perm || !aligned(act, 16) || !aligned(y_perm, 16) || !aligned(offsets, 4))
@@ -790,7 +791,7 @@ moe_status_t moe_forward(const moe_problem_t* p, const moe_weights_t* w, const v
                          const float* logits, const float* bias, void* out, void* ws,
                          size_t ws_bytes, moe_stream_t stream) {
   MOE_TRY(validate_problem(p));
-  MOE_TRY(check_weights(*p, w));
+  MOE_TRY(validate_weights(p, w));
   MOE_TRY(check_ws(*p, ws, ws_bytes, true));
   if (p->T == 0) return MOE_OK;
   if (!x || !logits || !out || !aligned(x, 16) || !aligned(out, 16) || !aligned(logits, 4) ||

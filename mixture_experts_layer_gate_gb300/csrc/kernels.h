@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -13,6 +14,8 @@ namespace moe {
 // Problem checks shared by every entry point: MOE_OK, MOE_ERR_INVALID_ARG for a
 // malformed problem, MOE_ERR_UNSUPPORTED for one beyond the library's limits.
 moe_status_t validate_problem(const moe_problem_t* p);
+// Checks of the weight pointers for a valid problem, shared likewise.
+moe_status_t validate_weights(const moe_problem_t* p, const moe_weights_t* w);
 #endif
 
 // ------------------------------------------------------------------- gate
@@ -168,5 +171,72 @@ cudaError_t launch_grouped_gemm(int wkind, const GemmMaps& maps, const GemmParam
 // int4 codes from the packed order (low nibble = even K index) to the paired
 // order (per 4-byte word: even K indices in the low 16 bits, odd in the high).
 cudaError_t launch_repack_int4(const uint32_t* in, uint32_t* out, size_t n_words, cudaStream_t s);
+
+// ------------------------------------------- operators around the layer
+struct NormArgs {
+  const void* x;
+  const void* residual;   // or null
+  const void* weight;     // [H]
+  void* residual_out;     // or null
+  void* y;                // or null
+  uint8_t* codes;         // [T, H]
+  float* scales;          // [T, ceil(H / 128)] or [T]
+  int64_t x_stride, residual_stride, residual_out_stride, y_stride;  // elements
+  int T, H;
+  int quant;              // moe_quant_t
+  int vec;                // rows are 16-byte aligned and H % 8 == 0
+  float eps;
+};
+// dtype: moe_dtype_t; weight_f32: the weight is float (else dtype)
+cudaError_t launch_add_rms_norm(const NormArgs& a, int dtype, int weight_f32, cudaStream_t s);
+
+struct RouterArgs {
+  const void* x;          // [T, H]
+  const void* w;          // [E, H]
+  float* logits;          // [T, E]
+  int64_t x_stride, w_stride;
+  int T, H, E;
+  int dtype;              // moe_dtype_t: bf16 or f16
+  uint32_t* err;
+};
+cudaError_t launch_router(const RouterArgs& a, cudaStream_t s);
+
+struct Fp8GemmArgs {
+  const uint8_t* a;       // [M, K] e4m3
+  const uint8_t* w;       // [N, K], or [2N, K] for SwiGLU
+  const float* a_scale;   // [M, KB]
+  const float* w_scale;   // [ceil(rows / 128), KB]
+  void* out;              // [M, N] (SwiGLU: null)
+  uint8_t* codes;         // SwiGLU: [M, N] e4m3, else null
+  float* scales;          // SwiGLU: [M, N / 128]
+  int64_t a_stride, a_scale_stride, w_stride, out_stride;
+  int M, N, K;
+  int out_dtype;          // moe_dtype_t
+  int accumulate;         // out += product
+  uint32_t* err;
+};
+cudaError_t launch_fp8_block(const Fp8GemmArgs& g, cudaStream_t s);
+
+constexpr int kFewMaxTokens = 8;
+struct FewArgs {
+  const __nv_bfloat16* x;  // [T, H]
+  const void* w13;
+  const void* w2;
+  const void* w13_scale;
+  const void* w2_scale;
+  const uint8_t* w13_zero;
+  const uint8_t* w2_zero;
+  const float* a1;         // fp8 static scales, or null (dynamic)
+  const float* a2;
+  const int32_t* ids;      // [T, k]
+  const float* topk_w;     // [T, k]
+  float* act;              // [T * k, I]
+  uint32_t* amax;          // bits of max |act| (fp8 dynamic)
+  __nv_bfloat16* out;      // [T, H]
+  int T, H, I, E, k;
+  int wkind;               // WKind
+  int paired;              // int4 code order
+};
+cudaError_t launch_few(const GateArgs& g, const FewArgs& a, cudaStream_t s);
 
 }  // namespace moe
