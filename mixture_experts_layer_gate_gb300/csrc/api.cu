@@ -75,12 +75,23 @@ namespace {
 
 // ------------------------------------------------------------ device facts
 
-struct DeviceInfo {
-  int sms = 0;
-  bool ok = false;
-};
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static std::once_flag once;
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
 
-cudaError_t device_info(DeviceInfo* out) {
+}  // namespace
+
+cudaError_t moe::device_info(DeviceInfo* out) {
   static std::mutex mu;
   static DeviceInfo cache[64];
   int dev = 0;
@@ -99,21 +110,7 @@ cudaError_t device_info(DeviceInfo* out) {
   return cudaSuccess;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static std::once_flag once;
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
-  return fn;
-}
-
-bool encode_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* ptr,
+bool moe::encode_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* ptr,
                 const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
                 CUtensorMapSwizzle swz) {
   auto fn = encode_fn();
@@ -126,6 +123,8 @@ bool encode_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* pt
                   swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
+
+namespace {
 
 // ---------------------------------------------------------------- planning
 

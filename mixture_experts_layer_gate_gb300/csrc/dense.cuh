@@ -1,0 +1,673 @@
+// Dense matrix product out[m, n] = sum_k a[m, k] w[n, k] on the tensor cores,
+// shared by the block-scaled 8-bit product and the router scores: tcgen05 MMAs
+// fed by TMA, accumulators in tensor memory, sums in registers.
+//
+// Tiles of 128 rows (token rows on the M side) by BN columns, K in k-blocks of
+// 128 bytes (128 e4m3 or 64 bf16 / f16 values).  Every `group` k-blocks the MMA
+// thread turns to the other of two accumulators, and the eight joining warps
+// (two per tensor-memory lane quarter: warp w holds rows 32 (w % 4) .. + 31,
+// one per lane, and one half of the columns) add the finished one, times the
+// scales of its block, to the tile's sums, which stay in registers.  The 8-bit
+// product joins every k-block, which is its scale block; the 16-bit one every
+// 16 (1024 values), which only bounds the length of the tensor core's own sums.
+//
+// PAIR: two CTAs share MMAs of M = 256 (cta_group::2): each loads its own 128
+// rows and half of the columns' weights, which halves the weight traffic from
+// L2 per product.  Else P CTAs of a cluster take P ranges of K of one tile and
+// join their sums through distributed shared memory in rank order (no atomics:
+// the order is fixed).
+#pragma once
+
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace moe {
+namespace dense {
+
+constexpr int kJoinWarps = 8;
+constexpr int kFirstJoin = 4;  // warp 0 issues TMA, warp 1 MMAs; 2 and 3 fill their warpgroup
+constexpr int kThreads = 32 * (kFirstJoin + kJoinWarps);
+// Registers a thread: the launch gives 168 x 384 (three warps per sub-partition);
+// 256-column tiles hold 128 sums per joining thread, so the first warpgroup
+// hands most of its share over (128 x (40 + 2 x 224) <= 168 x 384).
+constexpr int kLeanRegs = 40, kJoinRegs = 224, kLaunchRegs = 168;
+// two accumulators
+__host__ __device__ constexpr uint32_t tmem_cols(int bn) { return 2u * static_cast<uint32_t>(bn); }
+constexpr int kMaxStages = 12;
+constexpr int kMiscBytes = 4096;        // barriers, flags and the row maxima
+constexpr int kTileABytes = 128 * 128;  // what an MMA reads of A: 128 rows of a k-block
+
+enum Kind : int { kE4M3 = 0, kHalf = 1 };
+
+struct Params {
+  const float* a_scale;  // [M, KB] (8-bit)
+  const float* w_scale;  // [ceil(N / 128) or 2N / 128, KB] (8-bit)
+  void* out;
+  uint8_t* codes;        // SwiGLU
+  float* scales;         // SwiGLU
+  uint32_t* err;
+  int64_t a_scale_stride, out_stride;
+  int M, N, KB;
+  int group;             // k-blocks per accumulator
+  int P;                 // CTAs of a cluster that split K (not PAIR)
+  int mt, nt;            // tiles
+  int arows;             // rows of an A load: a multiple of 8, at most 128
+  int stages;
+  int fmt;               // 16-bit operands: 1 bf16, 0 f16
+  int out_dtype;         // moe_dtype_t
+  int accumulate;
+  int vec;               // out rows take 16-byte stores
+};
+
+struct Maps {
+  CUtensorMap a, w;
+};
+
+__host__ __device__ constexpr int wrows(int bn, bool pair) { return pair ? 128 : (bn < 128 ? bn : 128); }
+__host__ __device__ constexpr int stage_bytes(int arows, int bn, bool pair) {
+  return arows * 128 + (pair ? 128 : bn) * 128;
+}
+// shared row of a split-K partial, padded so that 8 lanes' 16-byte stores of 8
+// rows fall into different banks
+__host__ __device__ constexpr int part_ld(int bn) { return bn + 4; }
+
+// 32 columns of this lane, complete on return
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
+      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// 16 columns of this lane, complete on return
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// acc += d * s, two floats at a time
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t d0, uint32_t d1, uint64_t s) {
+  asm("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\tfma.rn.f32x2 %0, d, %3, %0;\n\t}"
+      : "+l"(acc)
+      : "r"(d0), "r"(d1), "l"(s));
+}
+__device__ __forceinline__ uint64_t pair2(float v) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "r"(__float_as_uint(v)));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  return make_float2(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32)));
+}
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// one arrival whose earlier shared-memory writes the waiters see
+__device__ __forceinline__ void mbar_arrive_cta(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// mbar_wait without a call (a function call leaves no room for a warp to change
+// its register count).
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* err,
+                                     uint32_t info) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 0u) {
+      if (abort_flag != nullptr && *abort_flag != 0) return false;
+      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        if (abort_flag != nullptr) *abort_flag = 1;
+        record_error(err, kErrTimeout, info);
+        return false;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) { return (a > b || a != a) ? a : b; }
+__device__ __forceinline__ float quant_scale(float amax) { return amax == 0.f ? 1.0f : __fdiv_rn(amax, 448.0f); }
+__device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float scale) {
+  return f32x2_to_e4m3x2(__fdiv_rn(a, scale), __fdiv_rn(b, scale)) |
+         (static_cast<uint32_t>(f32x2_to_e4m3x2(__fdiv_rn(c, scale), __fdiv_rn(d, scale))) << 16);
+}
+
+// out[row, col .. col + 3] of four sums
+__device__ __forceinline__ void store4(const Params& p, int64_t row, int col, float4 v) {
+  const int64_t at = row * p.out_stride + col;
+  float f[4] = {v.x, v.y, v.z, v.w};
+  if (p.vec && col + 4 <= p.N) {
+    if (p.out_dtype == 2) {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+      if (p.accumulate) {
+        const float4 u = *o;
+        v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+      }
+      *o = v;
+    } else {
+      uint2* o = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at);
+      uint2 u = make_uint2(0, 0);
+      if (p.accumulate) u = *o;
+      if (p.out_dtype == 0) {
+        if (p.accumulate) {
+          f[0] += bf16_lo(u.x);
+          f[1] += bf16_hi(u.x);
+          f[2] += bf16_lo(u.y);
+          f[3] += bf16_hi(u.y);
+        }
+        u = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+      } else {
+        if (p.accumulate) {
+          const float2 a = __half22float2(*reinterpret_cast<__half2*>(&u.x));
+          const float2 b = __half22float2(*reinterpret_cast<__half2*>(&u.y));
+          f[0] += a.x;
+          f[1] += a.y;
+          f[2] += b.x;
+          f[3] += b.y;
+        }
+        __half2 a = __floats2half2_rn(f[0], f[1]), b = __floats2half2_rn(f[2], f[3]);
+        u = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+      }
+      *o = u;
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (col + j >= p.N) return;
+    if (p.out_dtype == 0) {
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at + j;
+      *o = __float2bfloat16_rn(p.accumulate ? f[j] + __bfloat162float(*o) : f[j]);
+    } else if (p.out_dtype == 1) {
+      __half* o = static_cast<__half*>(p.out) + at + j;
+      *o = __float2half_rn(p.accumulate ? f[j] + __half2float(*o) : f[j]);
+    } else {
+      float* o = static_cast<float*>(p.out) + at + j;
+      *o = p.accumulate ? f[j] + *o : f[j];
+    }
+  }
+}
+
+template <int KIND, bool SWIGLU, bool PAIR, int BN>
+__global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constant__ Maps maps, const Params p) {
+  static_assert(!SWIGLU || BN == 256, "gate and up halves of 128 columns");
+  static_assert(!PAIR || BN == 256, "a pair's halves are 128 weight rows");
+  constexpr int W = BN / 2;              // columns per joining warp
+  constexpr int CH = W < 32 ? W : 32;    // columns per tensor-memory load
+  constexpr int NCH = W / CH;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw_u32 = smem_u32(smem_raw);
+  const uint32_t base_u32 = (raw_u32 + 1023u) & ~1023u;
+  uint8_t* base = smem_raw + (base_u32 - raw_u32);
+  const int ns = p.stages;
+  const uint32_t abytes = static_cast<uint32_t>(p.arows) * 128u;
+  const uint32_t sbytes = static_cast<uint32_t>(stage_bytes(p.arows, BN, PAIR));
+  // barriers first, then the ring
+  const uint32_t bars = base_u32;
+  const uint32_t ring = base_u32 + kMiscBytes;
+#define FULL(s) (bars + 8u * static_cast<uint32_t>(s))
+#define EMPTY(s) (bars + 8u * static_cast<uint32_t>(kMaxStages + (s)))
+  const uint32_t dfull = bars + 16u * kMaxStages, dempty = dfull + 16u, drain = dfull + 32u;
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(base + 16 * kMaxStages + 40);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(base + 16 * kMaxStages + 44);
+  const uint32_t pairs = bars + 16u * kMaxStages + 48u;    // one per lane quarter
+  float* row_max = reinterpret_cast<float*>(base + 1024);  // [2][2][128]: tile parity, column half, row
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = (PAIR || p.P > 1) ? cluster_ctarank() : 0u;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ns; ++s) {
+      mbar_init(FULL(s), 1u);
+      mbar_init(EMPTY(s), 1u);
+    }
+    for (uint32_t b = 0; b < 2; ++b) {
+      mbar_init(dfull + 8u * b, 1u);
+      mbar_init(dempty + 8u * b, kJoinWarps * (PAIR ? 2u : 1u));
+    }
+    mbar_init(drain, 1u);
+    for (uint32_t q = 0; q < 4; ++q) mbar_init(pairs + 8u * q, 2u);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&maps.a);
+    tma_prefetch_desc(&maps.w);
+  }
+  if (warp == 1) {
+    if (PAIR) {
+      tmem_alloc_pair(smem_u32(const_cast<uint32_t*>(tmem_slot)), tmem_cols(BN));
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), tmem_cols(BN));
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (PAIR) cluster_sync_all();  // the peer's barriers are initialised before anyone signals them
+  tc_fence_after();
+  pdl_wait();
+  pdl_trigger();
+  const uint32_t tmem = *tmem_slot;
+
+  // tiles of this cluster (PAIR) or CTA; a K-splitting cluster has one
+  const int tiles = p.mt * p.nt;
+  const int width = PAIR ? 2 : p.P;
+  const int first = static_cast<int>(blockIdx.x) / width;
+  const int step = static_cast<int>(gridDim.x) / width;
+  const int kb0 = PAIR ? 0 : static_cast<int>(static_cast<int64_t>(p.KB) * rank / p.P);
+  const int kb1 = PAIR ? p.KB : static_cast<int>(static_cast<int64_t>(p.KB) * (rank + 1) / p.P);
+  constexpr int kTileM = PAIR ? 256 : 128;
+  constexpr int kElems = KIND == kE4M3 ? 128 : 64;
+
+  if (warp < kFirstJoin) {
+    if (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLeanRegs));
+    if (warp == 0) {
+    // ------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      const uint64_t pol = l2_policy_evict_normal();
+      int st = 0, issued = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += step) {
+        const int m0 = (t % p.mt) * kTileM + (PAIR ? 128 * static_cast<int>(rank) : 0);
+        const int n0 = (t / p.mt) * (SWIGLU ? 128 : BN);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!wait(EMPTY(st), ph ^ 1u, abort_flag, p.err, 0x600u)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = ring + static_cast<uint32_t>(st) * sbytes;
+          if (PAIR) {
+            const uint32_t bar = map_to_rank(FULL(st), 0);
+            if (rank == 0) mbar_expect_tx(FULL(st), 2u * sbytes);
+            tma_load_2d_pair(dst, &maps.a, bar, kb * kElems, m0, pol);
+            const int row = SWIGLU ? n0 + static_cast<int>(rank) * p.N : n0 + 128 * static_cast<int>(rank);
+            tma_load_2d_pair(dst + abytes, &maps.w, bar, kb * kElems, row, pol);
+          } else {
+            mbar_expect_tx(FULL(st), sbytes);
+            tma_load_2d_hint(dst, &maps.a, FULL(st), kb * kElems, m0, pol);
+            tma_load_2d_hint(dst + abytes, &maps.w, FULL(st), kb * kElems, n0, pol);
+            if (BN == 256)
+              tma_load_2d_hint(dst + abytes + 128u * 128u, &maps.w, FULL(st), kb * kElems,
+                               SWIGLU ? n0 + p.N : n0 + 128, pol);
+          }
+          ++issued;
+          if (++st == ns) {
+            st = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (!ok && rank == (PAIR ? 0u : rank)) {
+        // after an abort the loads in flight land before the CTA (or its pair,
+        // whose leader counts both CTAs' bytes) may leave
+        for (int i = min(issued, ns); i > 0; --i) {
+          st = st == 0 ? ns - 1 : st - 1;
+          if (st == ns - 1) ph ^= 1u;
+          wait(FULL(st), ph, nullptr, p.err, 0x601u);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // --------------------------------------------- MMA issuer (leader CTA)
+    if (lane == 0 && (!PAIR || rank == 0)) {
+      const uint32_t idesc = make_idesc(kTileM, BN, KIND == kE4M3 ? 0u : static_cast<uint32_t>(p.fmt));
+      int st = 0;
+      uint32_t ph = 0, buf = 0, dph = 0;
+      bool ok = true, any = false;
+      for (int t = first; t < tiles && ok; t += step) {
+        for (int kb = kb0; kb < kb1 && ok;) {
+          if (!wait(dempty + 8u * buf, dph ^ 1u, abort_flag, p.err, 0x610u)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem + buf * static_cast<uint32_t>(BN);
+          const int end = min(kb + p.group, kb1);
+          for (bool fresh = true; kb < end; ++kb, fresh = false) {
+            if (!wait(FULL(st), ph, abort_flag, p.err, 0x620u)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t src = ring + static_cast<uint32_t>(st) * sbytes;
+            const uint64_t ad = sw128_kmajor_desc(src), wd = sw128_kmajor_desc(src + abytes);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint32_t accum = (fresh && kk == 0) ? 0u : 1u;
+              if (KIND == kE4M3) {
+                if (PAIR) mma_f8_pair(d, ad + 2u * kk, wd + 2u * kk, idesc, accum);
+                else mma_f8(d, ad + 2u * kk, wd + 2u * kk, idesc, accum);
+              } else {
+                if (PAIR) mma_f16_pair(d, ad + 2u * kk, wd + 2u * kk, idesc, accum);
+                else mma_f16(d, ad + 2u * kk, wd + 2u * kk, idesc, accum);
+              }
+            }
+            if (PAIR) mma_commit_pair(EMPTY(st), 0x3);
+            else mma_commit(EMPTY(st));
+            any = true;
+            if (++st == ns) {
+              st = 0;
+              ph ^= 1u;
+            }
+          }
+          if (!ok) break;
+          if (PAIR) mma_commit_pair(dfull + 8u * buf, 0x3);
+          else mma_commit(dfull + 8u * buf);
+          buf ^= 1u;
+          if (buf == 0u) dph ^= 1u;
+        }
+      }
+      if (!ok && any) {  // MMAs in flight end before tensor memory is freed
+        if (PAIR) mma_commit_pair(drain, 0x1);
+        else mma_commit(drain);
+        wait(drain, 0u, nullptr, p.err, 0x630u);
+      }
+    }
+    }
+    // Every warp leaves its role with the registers of the launch.  The joining
+    // warps give theirs back before this warpgroup takes its own again: a warp
+    // without a role that took them at once could leave a joining warp waiting
+    // for registers that nobody returns.
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kLaunchRegs));
+  } else {
+    if (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kJoinRegs));
+    // ------------------------------------------------------- joining warps
+    const int quarter = warp & 3, half = (warp - kFirstJoin) >> 2;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * quarter) << 16;
+    const uint32_t dempty_to = PAIR ? map_to_rank(dempty, 0) : dempty;
+    uint32_t buf = 0, dph = 0, tile = 0;
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += step) {
+      const int m0 = (t % p.mt) * kTileM + (PAIR ? 128 * static_cast<int>(rank) : 0);
+      const int n0 = (t / p.mt) * (SWIGLU ? 128 : BN);
+      const int row = m0 + 32 * quarter + lane;
+      const bool live = m0 + 32 * quarter < p.M;  // some row of this warp exists
+      const float* as = p.a_scale + static_cast<int64_t>(min(row, p.M - 1)) * p.a_scale_stride;
+      // the weight scales of this warp's columns (SwiGLU: gate's and up's)
+      const int sb = SWIGLU ? n0 / 128 : min((n0 + half * W) / 128, (p.N - 1) / 128);
+      const float* ws0 = p.w_scale + static_cast<int64_t>(sb) * p.KB;
+      const float* ws1 = SWIGLU ? ws0 + static_cast<int64_t>(p.N / 128) * p.KB : ws0;
+      uint64_t acc[W / 2];
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i) acc[i] = 0;
+      float s_a = 1.f, s_0 = 1.f, s_1 = 1.f;
+      if (KIND == kE4M3) {
+        s_a = as[kb0];
+        s_0 = ws0[kb0];
+        s_1 = SWIGLU ? ws1[kb0] : s_0;
+      }
+      for (int kb = kb0; kb < kb1; kb += p.group) {
+        const uint64_t f0 = pair2(s_a * s_0), f1 = pair2(s_a * s_1);
+        if (KIND == kE4M3 && kb + 1 < kb1) {  // the next block's scales, while its product is formed
+          s_a = as[kb + 1];
+          s_0 = ws0[kb + 1];
+          s_1 = SWIGLU ? ws1[kb + 1] : s_0;
+        }
+        if (!wait(dfull + 8u * buf, dph, abort_flag, p.err, 0x640u)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (live) {
+          const uint32_t src = tmem + lane_base + buf * static_cast<uint32_t>(BN);
+#pragma unroll
+          for (int c = 0; c < NCH; ++c) {
+            // SwiGLU: 64 gate columns, then the 64 up columns that go with them
+            const uint32_t col = SWIGLU ? static_cast<uint32_t>(64 * half + (c & 1) * 32 + (c >> 1) * 128)
+                                        : static_cast<uint32_t>(W * half + CH * c);
+            if constexpr (CH == 32) {
+              uint32_t r[32];
+              tmem_ld32(src + col, r);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) fma2(acc[16 * c + j], r[2 * j], r[2 * j + 1], (SWIGLU && c >= 2) ? f1 : f0);
+            } else {
+              uint32_t r[16];
+              tmem_ld16_wait(src + col, r);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) fma2(acc[j], r[2 * j], r[2 * j + 1], f0);
+            }
+          }
+        }
+        tc_fence_before();
+        if (lane == 0) mbar_arrive_cluster(dempty_to + 8u * buf);
+        buf ^= 1u;
+        if (buf == 0u) dph ^= 1u;
+      }
+      if (!ok) break;
+
+      if (!PAIR && p.P > 1) {
+        // partial sums into this CTA's shared memory (the ring is drained: the
+        // last accumulator was finished by the last MMA that read it)
+        if (row < p.M) {
+          float* dst = reinterpret_cast<float*>(base + kMiscBytes) + (32 * quarter + lane) * part_ld(BN);
+#pragma unroll
+          for (int c = 0; c < NCH; ++c) {
+            const int col = SWIGLU ? 64 * half + (c & 1) * 32 + (c >> 1) * 128 : W * half + CH * c;
+#pragma unroll
+            for (int j = 0; j < CH / 4; ++j) {
+              const float2 u = unpair(acc[CH / 2 * c + 2 * j]), v = unpair(acc[CH / 2 * c + 2 * j + 1]);
+              *reinterpret_cast<float4*>(dst + col + 4 * j) = make_float4(u.x, u.y, v.x, v.y);
+            }
+          }
+        }
+      } else if (SWIGLU) {
+        float v[W / 2];
+        float amax = 0.f;
+#pragma unroll
+        for (int j = 0; j < W / 4; ++j) {
+          const float2 g = unpair(acc[j]), u = unpair(acc[W / 4 + j]);
+          v[2 * j] = swiglu(g.x, u.x);
+          v[2 * j + 1] = swiglu(g.y, u.y);
+          amax = max_nan(amax, max_nan(fabsf(v[2 * j]), fabsf(v[2 * j + 1])));
+        }
+        // the other half of the row's block is held by the warp four further on
+        // (or back); a warp writes a buffer again two tiles later, when the
+        // other has read it before arriving for the tile between
+        float* mine = row_max + (tile & 1u) * 256 + 32 * quarter + lane;
+        mine[half * 128] = amax;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cta(pairs + 8u * quarter);
+        if (!wait(pairs + 8u * quarter, tile & 1u, abort_flag, p.err, 0x650u)) {
+          ok = false;
+          break;
+        }
+        amax = max_nan(amax, mine[(half ^ 1) * 128]);
+        ++tile;
+        if (row < p.M) {
+          const float scale = quant_scale(amax);
+          if (half == 0) p.scales[static_cast<int64_t>(row) * (p.N / 128) + n0 / 128] = scale;
+          uint4* dst = reinterpret_cast<uint4*>(p.codes + static_cast<int64_t>(row) * p.N + n0 + 64 * half);
+#pragma unroll
+          for (int j = 0; j < W / 32; ++j)
+            dst[j] = make_uint4(codes4(v[16 * j], v[16 * j + 1], v[16 * j + 2], v[16 * j + 3], scale),
+                                codes4(v[16 * j + 4], v[16 * j + 5], v[16 * j + 6], v[16 * j + 7], scale),
+                                codes4(v[16 * j + 8], v[16 * j + 9], v[16 * j + 10], v[16 * j + 11], scale),
+                                codes4(v[16 * j + 12], v[16 * j + 13], v[16 * j + 14], v[16 * j + 15], scale));
+        }
+      } else if (row < p.M) {
+#pragma unroll
+        for (int j = 0; j < W / 4; ++j) {
+          const float2 u = unpair(acc[2 * j]), v = unpair(acc[2 * j + 1]);
+          store4(p, row, n0 + W * half + 4 * j, make_float4(u.x, u.y, v.x, v.y));
+        }
+      }
+    }
+    __syncwarp();
+    if (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLaunchRegs));
+    tc_fence_before();
+    __syncthreads();
+  }
+#undef FULL
+#undef EMPTY
+
+  if (PAIR || p.P > 1) cluster_sync_all();  // signals and partial sums have arrived
+  if (!PAIR && p.P > 1) {
+    // a warp per row of this rank's share, a lane per four columns
+    const int m0 = (first % p.mt) * 128, n0 = (first / p.mt) * (SWIGLU ? 128 : BN);
+    const int rows = min(128, p.M - m0);
+    for (int r = static_cast<int>(rank) + p.P * warp; r < rows; r += p.P * (kThreads / 32)) {
+      const uint32_t src = ring + static_cast<uint32_t>(r * part_ld(BN)) * 4u;
+      auto joined = [&](int col) {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int q = 0; q < p.P; ++q) {
+          const float4 v = ld_cluster_f4(map_to_rank(src + static_cast<uint32_t>(col) * 4u, static_cast<uint32_t>(q)));
+          s.x += v.x;
+          s.y += v.y;
+          s.z += v.z;
+          s.w += v.w;
+        }
+        return s;
+      };
+      if (SWIGLU) {
+        const float4 g = joined(4 * lane), u = joined(128 + 4 * lane);
+        const float a = swiglu(g.x, u.x), b = swiglu(g.y, u.y), c = swiglu(g.z, u.z), d = swiglu(g.w, u.w);
+        float amax = max_nan(max_nan(fabsf(a), fabsf(b)), max_nan(fabsf(c), fabsf(d)));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const float scale = quant_scale(amax);
+        if (lane == 0) p.scales[static_cast<int64_t>(m0 + r) * (p.N / 128) + n0 / 128] = scale;
+        reinterpret_cast<uint32_t*>(p.codes + static_cast<int64_t>(m0 + r) * p.N + n0)[lane] = codes4(a, b, c, d, scale);
+      } else {
+        for (int col = 4 * lane; col < BN; col += 128) store4(p, m0 + r, n0 + col, joined(col));
+      }
+    }
+    cluster_sync_all();  // no CTA leaves while a peer reads its sums
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    if (PAIR) tmem_dealloc_pair(tmem, tmem_cols(BN));
+    else tmem_dealloc(tmem, tmem_cols(BN));
+  }
+}
+
+// ------------------------------------------------------------------ launch
+
+constexpr size_t kMaxSmem = 232448;
+
+// Dynamic shared memory for `stages` ring stages: what an MMA of a short A tile
+// reads past its rows, and a split-K partial, stay inside.
+inline size_t smem_bytes(const Params& p, int bn, bool pair) {
+  size_t ring = static_cast<size_t>(p.stages) * stage_bytes(p.arows, bn, pair) + (kTileABytes - p.arows * 128);
+  if (!pair && p.P > 1) {
+    const int rows = p.M < 128 ? p.M : 128;
+    const size_t part = static_cast<size_t>(rows) * part_ld(bn) * 4;
+    if (part > ring) ring = part;
+  }
+  // CTAs that share an SM share its 512 tensor-memory columns: as many fit by
+  // shared memory as by columns, so that no CTA waits for another's
+  // columns while its cluster waits for it
+  const size_t floor = bn >= 256 ? 120 * 1024 : bn >= 128 ? 80 * 1024 : bn >= 64 ? 48 * 1024 : 0;
+  const size_t need = 1024 + kMiscBytes + ring;
+  return need > floor ? need : floor;
+}
+
+template <int KIND, bool SWIGLU, bool PAIR, int BN>
+cudaError_t launch(const Maps& maps, const Params& p, int grid, cudaStream_t s) {
+  static int configured[64] = {};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  auto kernel = dense_kernel<KIND, SWIGLU, PAIR, BN>;
+  if (dev < 0 || dev >= 64 || configured[dev] == 0) {
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxSmem));
+    if (err != cudaSuccess) return err;
+    cudaFuncAttributes attr;
+    err = cudaFuncGetAttributes(&attr, kernel);
+    if (err != cudaSuccess) return err;
+    // the warps' register counts add up to the launch's only if it has these
+    if (BN == 256 && attr.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+    if (dev >= 0 && dev < 64) configured[dev] = 1;
+  }
+  return launch_pdl_cluster(kernel, dim3(grid), dim3(kThreads), smem_bytes(p, BN, PAIR), s,
+                            static_cast<unsigned>(PAIR ? 2 : p.P), maps, p);
+}
+
+// Descriptors, tile counts and ring depth, then the launch.  p: everything but
+// mt, nt, arows and stages.  a [M, K] and w [wrows_total, K] of 1-byte (kE4M3)
+// or 2-byte elements, strides in elements.
+template <int KIND>
+cudaError_t plan_and_launch(Params p, int bn, bool pair, bool swiglu, const void* a, int64_t a_stride, const void* w,
+                            int64_t w_stride, int64_t w_total, int64_t K, int sms, cudaStream_t s) {
+  const uint64_t esz = KIND == kE4M3 ? 1 : 2;
+  const CUtensorMapDataType dt = KIND == kE4M3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                 : p.fmt == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const int tile_m = pair ? 256 : 128;
+  p.mt = (p.M + tile_m - 1) / tile_m;
+  p.nt = (p.N + (swiglu ? 128 : bn) - 1) / (swiglu ? 128 : bn);
+  p.arows = pair || p.M >= 128 ? 128 : (p.M + 7) / 8 * 8;
+  const int sb = stage_bytes(p.arows, bn, pair);
+  const size_t room = kMaxSmem - 1024 - kMiscBytes - (kTileABytes - p.arows * 128);
+  const int per_cta = pair ? p.KB : (p.KB + p.P - 1) / p.P;
+  const int most = static_cast<int>(room / sb);
+  p.stages = most < kMaxStages ? most : kMaxStages;
+  // a K-splitting CTA has one tile: no more stages than k-blocks
+  if (p.P > 1 && p.stages > per_cta) p.stages = per_cta;
+  Maps maps;
+  {
+    const uint64_t dims[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(p.M)};
+    const uint64_t str[1] = {static_cast<uint64_t>(a_stride) * esz};
+    const uint32_t box[2] = {static_cast<uint32_t>(128 / esz), static_cast<uint32_t>(p.arows)};
+    if (!encode_map(&maps.a, dt, 2, a, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
+  }
+  {
+    const uint64_t dims[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(w_total)};
+    const uint64_t str[1] = {static_cast<uint64_t>(w_stride) * esz};
+    const uint32_t box[2] = {static_cast<uint32_t>(128 / esz), static_cast<uint32_t>(wrows(bn, pair))};
+    if (!encode_map(&maps.w, dt, 2, w, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B)) return cudaErrorInvalidValue;
+  }
+  const long long tiles = static_cast<long long>(p.mt) * p.nt;
+  if (tiles * 16 > (1ll << 30)) return cudaErrorInvalidValue;
+  int grid;
+  if (pair) {
+    grid = 2 * static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
+    if constexpr (KIND == kE4M3) {
+      if (swiglu) return launch<KIND, true, true, 256>(maps, p, grid, s);
+    }
+    return launch<KIND, false, true, 256>(maps, p, grid, s);
+  }
+  if (p.P > 1) grid = static_cast<int>(tiles) * p.P;
+  else grid = static_cast<int>(tiles < sms ? tiles : sms);
+  if constexpr (KIND == kE4M3) {
+    if (swiglu) return launch<KIND, true, false, 256>(maps, p, grid, s);
+  }
+  switch (bn) {
+    case 32: return launch<KIND, false, false, 32>(maps, p, grid, s);
+    case 64: return launch<KIND, false, false, 64>(maps, p, grid, s);
+    case 128: return launch<KIND, false, false, 128>(maps, p, grid, s);
+    default: return launch<KIND, false, false, 256>(maps, p, grid, s);
+  }
+}
+
+}  // namespace dense
+}  // namespace moe

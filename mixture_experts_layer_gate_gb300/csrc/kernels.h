@@ -18,6 +18,17 @@ moe_status_t validate_problem(const moe_problem_t* p);
 moe_status_t validate_weights(const moe_problem_t* p, const moe_weights_t* w);
 #endif
 
+// Constants of the current device, looked up once per device.
+struct DeviceInfo {
+  int sms = 0;
+  bool ok = false;
+};
+cudaError_t device_info(DeviceInfo* out);
+
+// A tiled TMA descriptor (out-of-range elements read as zero); false if the driver refuses it.
+bool encode_map(CUtensorMap* m, CUtensorMapDataType dt, int rank, const void* ptr, const uint64_t* dims,
+                const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapSwizzle swz);
+
 // ------------------------------------------------------------------- gate
 struct GateArgs {
   const float* logits;  // [T, E]

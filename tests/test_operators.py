@@ -301,6 +301,30 @@ def test_router_nan_stays_in_its_token(dev, T):
     assert torch.isnan(logits[T - 1]).all() and torch.isfinite(logits[:T - 1]).all()
 
 
+@gpu
+def test_products_back_to_back(dev):
+    """Launches that follow each other without a wait, over long sums, wide tiles and split ones."""
+    g = gen(21)
+    x, w = randn(g, 1024, 7168).to(torch.bfloat16), randn(g, 256, 7168).to(torch.bfloat16)
+    logits = torch.full((1024, 256), float("nan"), device=dev)
+    ws = moe.alloc_op_workspace(dev)
+    xd, wd = x.to(dev), w.to(dev)
+    a, sa, b, sb = product_inputs(1, 4096, 7168, 2)
+    ad = [t.to(dev) for t in (a, sa, b, sb)]
+    codes, scales = torch.empty((1, 2048), dtype=torch.uint8, device=dev), torch.empty((1, 16), device=dev)
+    out = torch.empty((1, 4096), device=dev)
+    for _ in range(40):
+        moe.router_logits(moe.router_problem(1024, 7168, 256), xd, wd, logits, ws)
+        moe.gemm_fp8_block_swiglu(moe.fp8_gemm_problem(1, 2048, 7168), *ad, codes, scales, ws)
+        moe.gemm_fp8_block(moe.fp8_gemm_problem(1, 4096, 7168, out_dtype="f32"), *ad, out, ws)
+    assert moe.get_device_error(ws) == 0
+    want, tol = ref.router(x, w)
+    ref.check(logits, want, tol, "logits")
+    h, dh = ref.product(a, sa, b, sb)
+    ref.check(out, h, 1.01 * dh + ref.EPS32 * h.abs(), "out")
+    ref.check_quantised(codes, scales, *ref.swiglu(h, dh), 128, "swiglu")
+
+
 # ------------------------------------------------------------------ block-scaled 8-bit product
 
 
