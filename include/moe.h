@@ -473,17 +473,17 @@ moe_status_t moe_gemm_fp8_block_swiglu(const moe_fp8_gemm_t* g, const void* a, i
                                        int64_t w13_stride, const float* w13_scale, void* codes,
                                        float* scales, void* ws, size_t ws_bytes, moe_stream_t stream);
 
-/* The whole layer for a few tokens (p->T <= MOE_FEW_MAX_TOKENS, else
- * MOE_ERR_UNSUPPORTED): arguments, weight formats and meaning of moe_forward,
+/* The whole layer for a few tokens (T <= MOE_FEW_MAX_TOKENS and T * (H + 32) <=
+ * 65792, which any H <= 8192 meets, else MOE_ERR_UNSUPPORTED): arguments, weight formats and meaning of moe_forward,
  * in two launches that stream the chosen experts' weights once.  All sums are
  * held in float and nothing is rounded between the gate and out: the SwiGLU
  * output stays float, int4 / int8 weights enter as (code - zero) * scale
  * unrounded, and y is not rounded per expert, so results differ from
  * moe_forward's by its roundings.  fp8 experts take activations as their codes,
  * e4m3(x / a1) and e4m3(act / a2); dynamic scales are max |x| / 448 and
- * max |act| / 448 over the call (1 for all zeros).  The workspace holds
- * moe_few_workspace_size() bytes (0 for an invalid problem or T above the
- * limit). */
+ * max |act| / 448 over the call (1 for all zeros).  int4 / int8 scales and zero
+ * points are 4-byte aligned.  The workspace holds moe_few_workspace_size()
+ * bytes (0 for an invalid problem or one beyond the limit). */
 #define MOE_FEW_MAX_TOKENS 8
 size_t moe_few_workspace_size(const moe_problem_t* p);
 moe_status_t moe_forward_few(const moe_problem_t* p, const moe_weights_t* w, const void* x,

@@ -229,6 +229,9 @@ struct Fp8GemmArgs {
 cudaError_t launch_fp8_block(const Fp8GemmArgs& g, cudaStream_t s);
 
 constexpr int kFewMaxTokens = 8;
+constexpr int kFewMaxCtas = 1024;
+// T * (H + 32) at most: the tokens stay in shared memory beside the weights' ring
+constexpr int kFewMaxTokenValues = 8 * (8192 + 32);
 struct FewArgs {
   const __nv_bfloat16* x;  // [T, H]
   const void* w13;
@@ -239,14 +242,15 @@ struct FewArgs {
   const uint8_t* w2_zero;
   const float* a1;         // fp8 static scales, or null (dynamic)
   const float* a2;
-  const int32_t* ids;      // [T, k]
-  const float* topk_w;     // [T, k]
-  float* act;              // [T * k, I]
-  uint32_t* amax;          // bits of max |act| (fp8 dynamic)
+  int32_t* ids;            // [T, k]
+  float* topk_w;           // [T, k]
+  uint16_t* act;           // [T * k, 2, I]: two 16-bit parts of each activation
+  float* amax;             // fp8 dynamic: largest |act| of each CTA of the first kernel
   __nv_bfloat16* out;      // [T, H]
   int T, H, I, E, k;
   int wkind;               // WKind
   int paired;              // int4 code order
+  uint32_t* err;
 };
 cudaError_t launch_few(const GateArgs& g, const FewArgs& a, cudaStream_t s);
 

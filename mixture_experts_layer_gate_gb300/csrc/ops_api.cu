@@ -46,11 +46,15 @@ FewLayout few_layout(const moe_problem_t& p) {
   L.w = o;
   o = align256(o + S * 4);
   L.amax = o;
-  o = align256(o + 4);
+  o = align256(o + kFewMaxCtas * 4);
   L.act = o;
   o = align256(o + S * p.I * 4);
   L.total = o;
   return L;
+}
+
+bool few_fits(const moe_problem_t& p) {
+  return p.T <= kFewMaxTokens && static_cast<long long>(p.T) * (p.H + 32) <= kFewMaxTokenValues;
 }
 
 moe_status_t check_fp8_gemm(const moe_fp8_gemm_t* g, const void* a, int64_t a_stride, const float* a_scale,
@@ -201,20 +205,21 @@ moe_status_t moe_gemm_fp8_block_swiglu(const moe_fp8_gemm_t* g, const void* a, i
 }
 
 size_t moe_few_workspace_size(const moe_problem_t* p) {
-  if (validate_problem(p) != MOE_OK || p->T > kFewMaxTokens) return 0;
+  if (validate_problem(p) != MOE_OK || !few_fits(*p)) return 0;
   return few_layout(*p).total;
 }
 
 moe_status_t moe_forward_few(const moe_problem_t* p, const moe_weights_t* w, const void* x, const float* logits,
                              const float* bias, void* out, void* ws, size_t ws_bytes, moe_stream_t stream) {
   MOE_TRY(validate_problem(p));
-  if (p->T > kFewMaxTokens) return MOE_ERR_UNSUPPORTED;
+  if (!few_fits(*p)) return MOE_ERR_UNSUPPORTED;
   MOE_TRY(validate_weights(p, w));
   const FewLayout L = few_layout(*p);
   if (ws == nullptr || !aligned(ws, 256) || ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   if (p->T == 0) return MOE_OK;
   if (!x || !logits || !out || !aligned(x, 16) || !aligned(out, 16) || !aligned(logits, 4) ||
-      (bias && !aligned(bias, 4)))
+      (bias && !aligned(bias, 4)) || !aligned(w->w13_scale, 4) || !aligned(w->w2_scale, 4) ||
+      !aligned(w->w13_zero, 4) || !aligned(w->w2_zero, 4))
     return MOE_ERR_INVALID_ARG;
   uint8_t* base = static_cast<uint8_t*>(ws);
   GateArgs g;
@@ -242,8 +247,9 @@ moe_status_t moe_forward_few(const moe_problem_t* p, const moe_weights_t* w, con
   a.a2 = w->a2_scale;
   a.ids = g.ids;
   a.topk_w = g.w;
-  a.act = reinterpret_cast<float*>(base + L.act);
-  a.amax = reinterpret_cast<uint32_t*>(base + L.amax);
+  a.act = reinterpret_cast<uint16_t*>(base + L.act);
+  a.amax = reinterpret_cast<float*>(base + L.amax);
+  a.err = reinterpret_cast<uint32_t*>(base);
   a.out = static_cast<__nv_bfloat16*>(out);
   a.T = p->T;
   a.H = p->H;

@@ -155,6 +155,12 @@ def test_few_refusals(lib):
     for kw in (dict(ws=None), dict(ws=P + 16), dict(n=size - 1)):
         assert call(p, **kw) == WORKSPACE, kw
     assert call(moe.problem(9, 256, 512, 8, 2)) == UNSUPPORTED
+    assert call(moe.problem(8, 8320, 128, 8, 2)) == UNSUPPORTED
+    assert moe.few_workspace_size(moe.problem(8, 8320, 128, 8, 2)) == 0
+    assert moe.few_workspace_size(moe.problem(8, 8192, 128, 8, 2)) > 0
+    p4 = moe.problem(4, 256, 512, 8, 2, wdtype="int4")
+    assert call(p4, w=binding.WeightsStruct(P, P, P + 2, P)) == INVALID
+    assert call(p4, w=binding.WeightsStruct(P, P, P, P, None, None, P + 2, P)) == INVALID
     assert moe.few_workspace_size(moe.problem(9, 256, 512, 8, 2)) == 0
     assert moe.few_workspace_size(moe.problem(4, 100, 512, 8, 2)) == 0
     assert call(moe.problem(4, 256, 512, 8, 2, wdtype="fp8")) == INVALID  # no scales
@@ -486,6 +492,21 @@ def test_few_formats(dev, wdtype, zero, act, T):
                                        (4, 128, 1408, 16, 8), (1, 2048, 1024, 32, 8), (7, 640, 384, 33, 5)])
 def test_few_shapes(dev, wdtype, T, H, I, E, k):
     run_few(dev, T, H, I, E, k, wdtype=wdtype, renormalize=(T % 2 == 0))
+
+
+@gpu
+@pytest.mark.parametrize("wdtype", ["bf16", "fp8", "int4", "int8"])
+def test_few_widest_tokens(dev, wdtype):
+    run_few(dev, 8, 8192, 128, 4, 2, zero=wdtype.startswith("int"), wdtype=wdtype)
+    run_few(dev, 1, 16384, 128, 4, 2, wdtype=wdtype)
+
+
+@gpu
+@pytest.mark.parametrize("wdtype,zero,act", FORMATS)
+def test_few_all_tokens_on_the_same_experts(dev, wdtype, zero, act):
+    logits = torch.zeros(8, 16)
+    logits[:, 5], logits[:, 11] = 3.0, 2.0
+    run_few(dev, 8, 256, 640, 16, 2, zero=zero, wdtype=wdtype, act_scale=act, logits=logits)
 
 
 @gpu
