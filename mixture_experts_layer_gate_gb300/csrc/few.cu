@@ -21,36 +21,42 @@
 // experts needs no second pass.  The activations pass between the two in 32
 // bits: as a bf16 and the bf16 of what that left over (two MMAs), or for fp8
 // as the format's codes.
-#include "gate_token.cuh"
+#include <float.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
 
 namespace moe {
 namespace {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxSlots = kFewMaxTokens * gate_detail::kMaxTopK;
+constexpr int kMaxTopK = 32;
+constexpr int kMaxSlots = kFewMaxTokens * kMaxTopK;
 constexpr int kMaxDepth = 8;
 
 // K per lane load of 16 bytes by four lanes, 16-byte slices of a token's
-// fragment per load, and loads per step of the two kernels.  A step lies within
-// one scale group of 128 (int4, int8).
+// fragment per load, and loads per step of the second kernel (one in the first).
+// A step lies within one scale group of 128 (int4, int8).
 template <int FMT>
 struct Fmt;
 template <>
 struct Fmt<kW_BF16> {
-  static constexpr int KC = 32, NS = 1, UP = 1, DOWN = 2;
+  static constexpr int KC = 32, NS = 1, DOWN = 2;
 };
 template <>
 struct Fmt<kW_FP8> {
-  static constexpr int KC = 64, NS = 2, UP = 1, DOWN = 2;
+  static constexpr int KC = 64, NS = 2, DOWN = 2;
 };
 template <>
 struct Fmt<kW_INT8> {
-  static constexpr int KC = 64, NS = 2, UP = 1, DOWN = 2;
+  static constexpr int KC = 64, NS = 2, DOWN = 2;
 };
 template <>
 struct Fmt<kW_INT4> {
-  static constexpr int KC = 128, NS = 4, UP = 1, DOWN = 1;
+  static constexpr int KC = 128, NS = 4, DOWN = 1;
 };
 template <int FMT>
 constexpr bool kGrouped = FMT == kW_INT4 || FMT == kW_INT8;
@@ -99,6 +105,12 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   return v;
 }
 
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
 template <bool F16>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -116,6 +128,24 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// the same from zero
+template <bool F16>
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, "
+        "%10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, "
+        "%10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(v)));
@@ -130,15 +160,18 @@ struct Offset {
   uint32_t flip;
   uint32_t pair;   // int4: bf16x2 of 128 + offset
   float magic;     // int8: 2^23 + offset
+  float plus;      // int4: 128 + offset
 };
 
 // The A registers (one row) of MMA m of a 16-byte load.
-//   int4: a nibble in the low bits of the bf16 128.0 is 128 + code; a pair of
-//     them is one shift, one masked xor and one exact subtraction (1.4
-//     operations a code)
+//   int4: a nibble in the low bits of the bf16 128.0 is 128 + code: a pair is a
+//     shift and a masked xor; the 128 and the offset are taken off the pair
+//     (SUB, exact), or by the caller off the product: sum (128 + c - p) x =
+//     sum (128 + c) x - p sum x, a multiply-add per group of 128 instead of a
+//     subtraction per pair (0.9 operations a code instead of 1.4)
 //   int8: a byte in the low bits of the float 2^23 is 2^23 + code
 //   fp8: the converter's f16 pairs
-template <int FMT>
+template <int FMT, bool SUB>
 __device__ __forceinline__ void convert(const uint4& w, int m, const Offset& o, uint32_t& lo, uint32_t& hi) {
   if (FMT == kW_BF16) {
     lo = word(w, 2 * m);
@@ -156,31 +189,33 @@ __device__ __forceinline__ void convert(const uint4& w, int m, const Offset& o, 
     hi = pack_bf16x2(f[2], f[3]);
   } else {
     const uint32_t v = word(w, m >> 1) >> (8 * (m & 1));
-    uint32_t a = (v & 0x000F000Fu) ^ o.flip, b = ((v >> 4) & 0x000F000Fu) ^ o.flip;
-    const __nv_bfloat162 off = *reinterpret_cast<const __nv_bfloat162*>(&o.pair);
-    __nv_bfloat162 pa = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a), off);
-    __nv_bfloat162 pb = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&b), off);
-    lo = *reinterpret_cast<uint32_t*>(&pa);
-    hi = *reinterpret_cast<uint32_t*>(&pb);
+    lo = (v & 0x000F000Fu) ^ o.flip;
+    hi = ((v >> 4) & 0x000F000Fu) ^ o.flip;
+    if (SUB) {
+      const __nv_bfloat162 off = *reinterpret_cast<const __nv_bfloat162*>(&o.pair);
+      __nv_bfloat162 pa = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&lo), off);
+      __nv_bfloat162 pb = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&hi), off);
+      lo = *reinterpret_cast<uint32_t*>(&pa);
+      hi = *reinterpret_cast<uint32_t*>(&pb);
+    }
   }
 }
 
-// Scale and offset of one row's group, from the copied words that hold them.
+// Scale and offset of one row's group, from the 4-byte words that hold them
+// (index: the group's place in its tensor, modulo 4).
 template <int FMT>
-__device__ __forceinline__ void group_of(uint32_t saddr, uint32_t zaddr, int64_t index, bool zero, float& scale,
+__device__ __forceinline__ void group_of(uint32_t sword, uint32_t zword, uint32_t index, bool zero, float& scale,
                                          Offset& o) {
-  uint16_t h;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(saddr + 2u * static_cast<uint32_t>(index & 1)) : "memory");
-  scale = __half2float(__ushort_as_half(h));
+  scale = __half2float(__ushort_as_half(static_cast<uint16_t>((index & 1u) ? sword >> 16 : sword)));
   uint32_t z = FMT == kW_INT4 ? 8u : 128u;
-  if (zero)
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(z) : "r"(zaddr + static_cast<uint32_t>(index & 3)) : "memory");
+  if (zero) z = (zword >> (8u * (index & 3u))) & 255u;
   if (FMT == kW_INT4) {
     o.flip = zero ? 0x43004300u : 0x43084308u;
     o.pair = 0x43004300u | z | (z << 16);
+    o.plus = static_cast<float>(128u + z);
   } else {
     o.flip = zero ? 0u : 0x80808080u;
-    o.magic = 8388608.0f + static_cast<float>(z);
+    o.magic = static_cast<float>(8388608u + z);
   }
 }
 
@@ -193,7 +228,7 @@ struct Routing {
   uint32_t seen[32];                   // bit per expert
   int16_t expert[kMaxSlots];
   uint8_t tokens[kMaxSlots];           // bit per token
-  int16_t slot[kMaxSlots][kFewMaxTokens];
+  uint8_t slot[kMaxSlots][kFewMaxTokens];
   int most;                            // tokens of the expert with the most
 };
 // per chosen expert and token: the weight of the sum, 0 where the token did not choose it
@@ -215,7 +250,7 @@ __device__ __forceinline__ void build_routing(Routing& r, const FewArgs& a, Weig
     int at = __popc(r.seen[e >> 5] & ((1u << (e & 31)) - 1u));
     for (int i = 0; i < (e >> 5); ++i) at += __popc(r.seen[i]);
     r.expert[at] = static_cast<int16_t>(e);
-    r.slot[at][t] = static_cast<int16_t>(s);
+    r.slot[at][t] = static_cast<uint8_t>(s);
     if (weight != nullptr) weight[at][t] = r.w[s];
     atomicOr(reinterpret_cast<uint32_t*>(r.tokens) + (at >> 2), 1u << (8 * (at & 3) + t));
   }
@@ -245,202 +280,395 @@ __device__ __forceinline__ float act_scale_of(float amax) { return amax > 0.f ? 
 __device__ __forceinline__ uint32_t quantised_f16x2(float a, float b) { return e4m3x2_f16x2(f32x2_to_e4m3x2(a, b)); }
 
 constexpr size_t kRoutingBytes = (sizeof(Routing) + 127) / 128 * 128;
+static_assert(kMaxSlots <= 256, "slots in a byte");
+constexpr size_t kDownRedBytes = 2 * kWarps * 128 * 4;
 constexpr size_t kWeightBytes = sizeof(float) * kMaxSlots * kFewMaxTokens;
-constexpr size_t kRedBytes = static_cast<size_t>(kWarps) * 32 * 8 * 4;
+// a warp's sums of 32 rows and 8 tokens; the up half starts in other banks
+constexpr int kRedHalf = 16 * 8 + 16, kRedWarp = 2 * 16 * 8 + 16;
+constexpr size_t kRedBytes = static_cast<size_t>(kWarps) * kRedWarp * 4;
 // row stride of a token in shared memory: 64 bytes over a multiple of 128, so
 // that the lanes of two tokens read different banks
 __host__ __device__ constexpr int token_stride(int H) { return 2 * H + 64; }
 
 template <int FMT>
 constexpr int up_stage() {
-  return Fmt<FMT>::UP * 4 * 512 + (kGrouped<FMT> ? 256 : 0);
+  return 4 * 512 + (kGrouped<FMT> ? 256 : 0);
 }
+
+// A float's order as an unsigned one (-0 as +0); 0 is below every number.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t u = __float_as_uint(v + 0.f);
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+// The k best of the warp's keys (32 strided experts per register, 0: out of the
+// running), ties to the lower expert: lane j returns the j-th expert.  Two warp
+// reductions a round.
+template <int EPL>
+__device__ __forceinline__ int best_k(uint32_t (&key)[EPL], int k, int lane) {
+  int mine = 0;
+#pragma unroll 1
+  for (int j = 0; j < k; ++j) {
+    uint32_t m = key[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) m = max(m, key[i]);
+    m = __reduce_max_sync(0xffffffffu, m);
+    uint32_t at = 0xffffffffu;
+#pragma unroll
+    for (int i = EPL - 1; i >= 0; --i)
+      if (key[i] == m) at = static_cast<uint32_t>(lane + 32 * i);
+    at = __reduce_min_sync(0xffffffffu, at);
+    if (lane == j) mine = static_cast<int>(at);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (at == static_cast<uint32_t>(lane + 32 * i)) key[i] = 0;
+  }
+  return mine;
+}
+
+// The gate of one token by one warp: moe_gate_topk's rule (gate_token.cuh), with
+// reductions by the warp's integer unit, because here a single token's latency
+// counts (DeepSeek-V3 gate of one token: 2 us against 8).  scratch: 32 * EPL floats.
+template <int EPL>
+__device__ __forceinline__ void gate_one(const GateArgs& a, int t, int lane, float* scratch, int32_t* ids, float* w) {
+  const float* row = a.logits + static_cast<size_t>(t) * a.E;
+  float val[EPL], bias[EPL];
+  uint32_t key[EPL];
+  float top = -FLT_MAX;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {  // (every load before the first use: their latencies overlap)
+    const int e = lane + 32 * i;
+    val[i] = e < a.E ? row[e] : -INFINITY;
+    bias[i] = a.bias != nullptr && e < a.E ? a.bias[e] : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    float l = val[i];
+    if (l != l) l = -INFINITY;  // a NaN logit is read as -inf
+    val[i] = l;
+    top = fmaxf(top, l);
+  }
+  float inv_z = 1.0f;
+  if (!a.sigmoid) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      key[i] = ordered(val[i]);
+      val[i] = lane + 32 * i < a.E ? expf(val[i] - top) : 0.f;
+      z += val[i];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    inv_z = 1.0f / z;
+  } else {
+    const bool raw = a.n_group == 0 && a.bias == nullptr;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = lane + 32 * i;
+      const float s = 1.0f / (1.0f + expf(-val[i]));
+      const float kk = raw ? val[i] : s + bias[i];
+      key[i] = ordered(kk);
+      val[i] = s;
+      if (a.n_group > 0 && e < a.E) scratch[e] = kk;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i)
+    if (lane + 32 * i >= a.E) key[i] = 0;
+  if (a.n_group > 0) {
+    // a group's two largest keys, by `per` lanes a group
+    __syncwarp();
+    const int gs = a.E / a.n_group;
+    const int shift = 31 - __clz(32 / a.n_group), per = 1 << shift;
+    const int g = lane >> shift, p = lane & (per - 1);
+    float m1 = -INFINITY, m2 = -INFINITY;
+    if (g < a.n_group)
+      for (int j = p; j < gs; j += per) {
+        const float v = scratch[g * gs + j];
+        m2 = fmaxf(m2, fminf(m1, v));
+        m1 = fmaxf(m1, v);
+      }
+    for (int o = per / 2; o > 0; o >>= 1) {
+      const float b1 = __shfl_xor_sync(0xffffffffu, m1, o), b2 = __shfl_xor_sync(0xffffffffu, m2, o);
+      m2 = fmaxf(fminf(m1, b1), fmaxf(m2, b2));
+      m1 = fmaxf(m1, b1);
+    }
+    const float score = gs >= 2 ? m1 + m2 : m1;
+    // lane g takes group g's score
+    const float mine = __shfl_sync(0xffffffffu, score, (lane * per) & 31);
+    uint32_t gkey[1] = {lane < a.n_group ? ordered(mine) : 0u};
+    const int picked = best_k<1>(gkey, a.topk_group, lane);
+    const uint32_t allowed = __reduce_or_sync(0xffffffffu, lane < a.topk_group ? 1u << (picked & 31) : 0u);
+    const float inv_gs = 1.0f / static_cast<float>(gs);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      // (e + 0.5) / gs is at least 1 / 2048 from every integer: its float is on the same side
+      const int e = lane + 32 * i, eg = static_cast<int>((static_cast<float>(e) + 0.5f) * inv_gs);
+      if (e < a.E && !(allowed >> (eg & 31) & 1u)) key[i] = 0;
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) scratch[lane + 32 * i] = val[i];
+  const int id = best_k<EPL>(key, a.k, lane);
+  __syncwarp();
+  float v = 0.f;
+  if (lane < a.k) v = scratch[static_cast<unsigned>(id) < static_cast<unsigned>(a.E) ? id : 0] * inv_z;
+  float total = v;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane < a.k) {
+    const float inv = a.renormalize ? (total > 0.f ? 1.0f / total : 0.f) : 1.0f;
+    ids[t * a.k + lane] = id;
+    w[t * a.k + lane] = (v * inv) * a.scale;
+  }
+}
+
+// The gate (warps 0 .. T - 1, one token each), while the other warps run
+// `meanwhile`; then the routing tables.
+template <int EPL, typename Fn>
+__device__ __forceinline__ void route(const GateArgs& gate, const FewArgs& a, Routing& r, Weights weight, float* scratch,
+                                      Fn&& meanwhile) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp < a.T) {
+    gate_one<EPL>(gate, warp, lane, scratch + warp * (32 * EPL), r.ids, r.w);
+    // (a NaN bias can leave the gate without a choice)
+    if (lane < a.k && static_cast<unsigned>(r.ids[warp * a.k + lane]) >= static_cast<unsigned>(a.E)) {
+      if (blockIdx.x == 0) record_error(a.err, kErrBadIndex, static_cast<uint32_t>(warp * a.k + lane));
+      r.ids[warp * a.k + lane] = 0;
+    }
+  } else {
+    meanwhile();
+  }
+  build_routing(r, a, weight);
+}
+
+// Part of K of warp w, as step w' of kWarps: where 16 does not divide the steps
+// the longer parts are spread over the SM's four sub-partitions.
+__device__ __forceinline__ int part_of(int warp) { return (warp & ~3) + ((warp + (warp >> 2)) & 3); }
 
 // ------------------------------------------------------------------- up
 
 template <int FMT, int EPL>
-__global__ void __launch_bounds__(kThreads, 1) few_up_kernel(GateArgs gate, FewArgs a, int depth) {
+__global__ void __launch_bounds__(kThreads, 1) few_up_kernel(GateArgs gate, FewArgs a, int depth, int reds) {
   extern __shared__ __align__(128) uint8_t few_smem[];
   using F = Fmt<FMT>;
+  constexpr bool kCorrect = FMT == kW_INT4;  // offsets are taken off the products
   Routing& r = *reinterpret_cast<Routing*>(few_smem);
-  float* red = reinterpret_cast<float*>(few_smem + kRoutingBytes);  // [warp][row 0-15 gate, 16-31 up][token]
-  uint8_t* xs = few_smem + kRoutingBytes + kRedBytes;
+  float* red = reinterpret_cast<float*>(few_smem + kRoutingBytes);  // [reds][warp][gate, up][16 rows][token]
+  float* xsum = red + reds * (kRedBytes / 4);                       // int4: [group][token] sums of x
+  uint8_t* xs = reinterpret_cast<uint8_t*>(xsum) + (kCorrect ? a.H / 128 * 32 : 0);
   const int xstride = token_stride(a.H);
   uint8_t* rings = xs + (static_cast<size_t>(a.T) * xstride + 127) / 128 * 128;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   pdl_wait();
   pdl_trigger();
 
-  // the gate, one warp per token, with the reduction buffer (up to 4 KB a token
-  // would not fit there for E > 512) and rings as its scratch
-  {
-    GateArgs gl = gate;
-    gl.ids = r.ids;
-    gl.w = r.w;
-    if (warp < a.T) gate_detail::gate_token<EPL>(gl, warp, lane, reinterpret_cast<float*>(rings) + warp * (32 * EPL));
-  }
-  __syncthreads();
-  for (int s = tid; s < a.T * a.k; s += kThreads) {
-    // (a NaN bias can leave the gate without a choice)
-    if (static_cast<unsigned>(r.ids[s]) >= static_cast<unsigned>(a.E)) {
-      if (blockIdx.x == 0) record_error(a.err, kErrBadIndex, static_cast<uint32_t>(s));
-      r.ids[s] = 0;
-    }
-    if (blockIdx.x == 0) {
-      a.ids[s] = r.ids[s];
-      a.topk_w[s] = r.w[s];
-    }
-  }
-  build_routing(r, a, nullptr);
-
   // tokens into shared memory in fragment order; fp8: as codes of x / a1
-  float a1 = 1.f;
   const uint4* xg = reinterpret_cast<const uint4*>(a.x);
-  if (FMT == kW_FP8) {
-    if (a.a1 != nullptr) {
-      a1 = a.a1[0];
-    } else {
-      float m = 0.f;
-      for (int i = tid; i < a.T * a.H / 8; i += kThreads) {
-        const uint4 v = xg[i];
+  const int nvec = a.T * a.H / 8;
+  auto stage = [&](int t0, int n, float a1) {
+    for (int c = tid - t0; c - lane < a.H / 8; c += n) {
+      const bool live = c < a.H / 8;
+      const int k = c * 8;
+#pragma unroll 1
+      for (int t0 = 0; t0 < a.T; t0 += 4) {
+        uint4 vs[4];  // four tokens' loads in flight
 #pragma unroll
-        for (int j = 0; j < 4; ++j) m = fmaxf(m, fmaxf(fabsf(bf16_lo(word(v, j))), fabsf(bf16_hi(word(v, j)))));
+        for (int u = 0; u < 4; ++u)
+          vs[u] = live && t0 + u < a.T ? xg[static_cast<size_t>(t0 + u) * (a.H / 8) + c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int t = t0 + u;
+          if (t >= a.T) break;
+          uint4 v = vs[u];
+          if (kCorrect) {  // a group of 128 is 16 adjacent lanes
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum += bf16_lo(word(v, j)) + bf16_hi(word(v, j));
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (live && (lane & 15) == 0) xsum[k / 128 * 8 + t] = sum;
+          }
+          if (FMT == kW_FP8) {
+            uint32_t q[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              q[j] = quantised_f16x2(__fdiv_rn(bf16_lo(word(v, j)), a1), __fdiv_rn(bf16_hi(word(v, j)), a1));
+            v = make_uint4(q[0], q[1], q[2], q[3]);
+          } else if (FMT == kW_INT4 && !a.paired) {
+            v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                           __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+          }
+          if (live) *reinterpret_cast<uint4*>(xs + static_cast<size_t>(t) * xstride + 2 * frag_pos<FMT>(k, 0)) = v;
+        }
       }
-      a1 = act_scale_of(block_max(m, red));
     }
+  };
+  const bool dynamic = FMT == kW_FP8 && a.a1 == nullptr;
+  float a1 = FMT == kW_FP8 && !dynamic ? a.a1[0] : 1.f;
+  if (kCorrect) {
+    for (int i = tid; i < a.H / 128 * 8; i += kThreads)
+      if ((i & 7) >= a.T) xsum[i] = 0.f;
   }
-  for (int i = tid; i < a.T * a.H / 8; i += kThreads) {
-    const int t = i / (a.H / 8), k = (i - t * (a.H / 8)) * 8;
-    uint4 v = xg[i];
-    if (FMT == kW_FP8) {
-      uint32_t q[4];
+  route<EPL>(gate, a, r, nullptr, reinterpret_cast<float*>(rings), [&] {
+    if (!dynamic) stage(32 * a.T, kThreads - 32 * a.T, a1);
+  });
+  if (dynamic) {
+    float m = 0.f;
+    for (int i = tid; i < nvec; i += kThreads) {
+      const uint4 v = xg[i];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        q[j] = quantised_f16x2(__fdiv_rn(bf16_lo(word(v, j)), a1), __fdiv_rn(bf16_hi(word(v, j)), a1));
-      v = make_uint4(q[0], q[1], q[2], q[3]);
-    } else if (FMT == kW_INT4 && !a.paired) {
-      v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                     __byte_perm(v.y, v.w, 0x7632));
+      for (int j = 0; j < 4; ++j) m = fmaxf(m, fmaxf(fabsf(bf16_lo(word(v, j))), fabsf(bf16_hi(word(v, j)))));
     }
-    *reinterpret_cast<uint4*>(xs + static_cast<size_t>(t) * xstride + 2 * frag_pos<FMT>(k, 0)) = v;
+    a1 = act_scale_of(block_max(m, red));
+    stage(0, kThreads, a1);
+    __syncthreads();
   }
-  __syncthreads();
 
-  constexpr int STEP = F::KC * F::UP;  // K of a step
+  constexpr int STEP = F::KC;  // K of a step
   constexpr int kStage = up_stage<FMT>();
-  const int tiles = a.I / 16;
-  const int units = r.count * tiles;
+  const int tiles = a.I / 16, count = r.count;
   const int nsteps = a.H / STEP;
-  const int s0 = nsteps * warp / kWarps, s1 = nsteps * (warp + 1) / kWarps;
+  const int part_no = part_of(warp);
+  const int s0 = nsteps * part_no / kWarps, s1 = nsteps * (part_no + 1) / kWarps;
   const uint32_t ring = smem_u32(rings) + static_cast<uint32_t>(warp * depth * kStage);
-  const int64_t rb = row_bytes<FMT>(a.H);
+  const int64_t rb = row_bytes<FMT>(a.H), to8 = 8 * rb, to_up = a.I * rb;
   const int G = a.H / 128;
   const bool zero = a.w13_zero != nullptr;
+  const uint8_t* w13 = static_cast<const uint8_t*>(a.w13);
 
-  // issue side: unit iu, step is
-  int iu = blockIdx.x, is = s0, islot = 0;
+  // issue side: its unit (expert ix, tile it), step is, pointers of the step
+  int ix = static_cast<int>(blockIdx.x) / tiles, it = static_cast<int>(blockIdx.x) % tiles, is = s0;
+  uint32_t idst = ring + lane * 16;
+  const uint32_t iend = ring + static_cast<uint32_t>(depth * kStage);
+  const uint8_t* isrc = nullptr;
+  int64_t iat = 0;  // row `lane`'s scale (16 gate rows, 16 up rows), first group
+  auto start_unit = [&] {
+    const int64_t row = static_cast<int64_t>(r.expert[ix]) * 2 * a.I + it * 16;
+    isrc = w13 + (row + g) * rb + row_bytes<FMT>(static_cast<int64_t>(s0) * STEP) + t4 * 16;
+    if (kGrouped<FMT>) iat = (row + (lane & 15) + static_cast<int64_t>(lane >> 4) * a.I) * G;
+    is = s0;
+  };
+  bool more = ix < count && s0 < s1;
+  if (more) start_unit();
   auto issue = [&] {
-    if (iu < units && s0 < s1) {
-      const int x = iu / tiles;
-      const int64_t row = static_cast<int64_t>(r.expert[x]) * 2 * a.I + (iu - x * tiles) * 16;
-      const uint8_t* src = static_cast<const uint8_t*>(a.w13) + (row + g) * rb + row_bytes<FMT>(static_cast<int64_t>(is) * STEP) + t4 * 16;
-      const uint32_t dst = ring + static_cast<uint32_t>(islot * kStage + lane * 16);
-#pragma unroll
-      for (int u = 0; u < F::UP; ++u)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)  // gate rows g and g + 8, up rows g and g + 8
-          cp_async16(dst + static_cast<uint32_t>((4 * u + q) * 512),
-                     src + u * 64 + ((q & 1) * 8 + static_cast<int64_t>(q >> 1) * a.I) * rb);
+    if (more) {
+      cp_async16(idst, isrc);  // gate rows g and g + 8, up rows g and g + 8
+      cp_async16(idst + 512, isrc + to8);
+      cp_async16(idst + 1024, isrc + to_up);
+      cp_async16(idst + 1536, isrc + to_up + to8);
       if (kGrouped<FMT>) {
         // the 4-byte words that hold row `lane`'s scale and zero point
-        const int64_t at = (row + (lane & 15) + static_cast<int64_t>(lane >> 4) * a.I) * G + is * STEP / 128;
-        const uint32_t d = ring + static_cast<uint32_t>(islot * kStage + F::UP * 2048 + lane * 4);
+        const int64_t at = iat + is * STEP / 128;
+        const uint32_t d = idst + 2048 - lane * 16 + (lane & 7) * 16 + (lane >> 3) * 4;
         cp_async4(d, static_cast<const uint16_t*>(a.w13_scale) + (at & ~1ll));
         if (zero) cp_async4(d + 128, a.w13_zero + (at & ~3ll));
       }
+      isrc += 64;
       if (++is == s1) {
-        is = s0;
-        iu += gridDim.x;
+        it += gridDim.x;
+        while (it >= tiles) {
+          it -= tiles;
+          ++ix;
+        }
+        more = ix < count;
+        if (more) start_unit();
       }
     }
     cp_async_commit();
-    if (++islot == depth) islot = 0;
+    idst += kStage;
+    if (idst >= iend) idst -= static_cast<uint32_t>(depth * kStage);
   };
   for (int i = 0; i < depth - 1; ++i) issue();
 
-  int slot = 0;
+  uint32_t src = ring;
   float amax = 0.f;
-  for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int x = unit / tiles, i0 = (unit - x * tiles) * 16;
-    const int64_t row0 = static_cast<int64_t>(r.expert[x]) * 2 * a.I + i0;
+  int buf = 0;
+  int x = static_cast<int>(blockIdx.x) / tiles, tile = static_cast<int>(blockIdx.x) % tiles;
+  // (columns past the last token repeat it; nobody reads their sums)
+  const uint8_t* xlane = xs + static_cast<size_t>(min(g, a.T - 1)) * xstride + t4 * 16;
+  while (x < count) {
+    const int i0 = tile * 16;
+    uint32_t at[4];  // the four rows' scales: index modulo 4
+    if (kGrouped<FMT>) {
+      const uint32_t row = static_cast<uint32_t>(r.expert[x]) * 2u * static_cast<uint32_t>(a.I) + static_cast<uint32_t>(i0 + g);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        at[q] = ((row + 8u * (q & 1) + static_cast<uint32_t>(q >> 1) * static_cast<uint32_t>(a.I)) * static_cast<uint32_t>(G)) & 3u;
+    }
     float acc[2][4] = {};
     for (int s = s0; s < s1; ++s) {
       __syncwarp();
       issue();
       cp_async_wait(depth - 1);
       __syncwarp();
-      const uint32_t src = ring + static_cast<uint32_t>(slot * kStage);
-      if (++slot == depth) slot = 0;
-      float sc[4] = {1.f, 1.f, 1.f, 1.f};
+      float sc[4];
       Offset off[4] = {};
-      float part[2][4] = {};
+      float part[2][4];
+      const int group = s * STEP / 128;
       if (kGrouped<FMT>) {
+        const uint4 sw = lds128(src + 2048 + g * 16);  // rows g, g + 8 (gate), g, g + 8 (up)
+        uint4 zw = make_uint4(0, 0, 0, 0);
+        if (zero) zw = lds128(src + 2176 + g * 16);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int rr = g + 8 * q;  // gate g, gate g + 8, up g, up g + 8
-          const int64_t at = (row0 + (rr & 15) + static_cast<int64_t>(rr >> 4) * a.I) * G + s * STEP / 128;
-          group_of<FMT>(src + F::UP * 2048 + rr * 4, src + F::UP * 2048 + 128 + rr * 4, at, zero, sc[q], off[q]);
-        }
+        for (int q = 0; q < 4; ++q)
+          group_of<FMT>(word(sw, q), word(zw, q), at[q] + static_cast<uint32_t>(group), zero, sc[q], off[q]);
       }
+      uint4 w[4];
 #pragma unroll
-      for (int u = 0; u < F::UP; ++u) {
-        uint4 w[4];
+      for (int q = 0; q < 4; ++q) w[q] = lds128(src + static_cast<uint32_t>(q * 512 + lane * 16));
 #pragma unroll
-        for (int q = 0; q < 4; ++q) w[q] = lds128(src + static_cast<uint32_t>((4 * u + q) * 512 + lane * 16));
+      for (int n = 0; n < F::NS; ++n) {
+        const uint4 b = *reinterpret_cast<const uint4*>(xlane + 2 * s * F::KC + n * 64);
 #pragma unroll
-        for (int n = 0; n < F::NS; ++n) {
-          uint4 b = make_uint4(0, 0, 0, 0);
-          if (g < a.T)
-            b = *reinterpret_cast<const uint4*>(xs + static_cast<size_t>(g) * xstride +
-                                                2 * ((s * F::UP + u) * F::KC) + n * 64 + t4 * 16);
+        for (int h = 0; h < 2; ++h) {
+          const int m = 2 * n + h;
+          const uint32_t b0 = h ? b.z : b.x, b1 = h ? b.w : b.y;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int m = 2 * n + h;
-            const uint32_t b0 = h ? b.z : b.x, b1 = h ? b.w : b.y;
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              uint32_t a0, a1r, a2, a3;
-              convert<FMT>(w[2 * y], m, off[2 * y], a0, a2);
-              convert<FMT>(w[2 * y + 1], m, off[2 * y + 1], a1r, a3);
-              mma16816<FMT == kW_FP8>(kGrouped<FMT> ? part[y] : acc[y], a0, a1r, a2, a3, b0, b1);
-            }
+          for (int y = 0; y < 2; ++y) {
+            uint32_t r0, r1, r2, r3;
+            convert<FMT, !kCorrect>(w[2 * y], m, off[2 * y], r0, r2);
+            convert<FMT, !kCorrect>(w[2 * y + 1], m, off[2 * y + 1], r1, r3);
+            if (kGrouped<FMT> && m == 0) mma16816_first<false>(part[y], r0, r1, r2, r3, b0, b1);
+            else mma16816<FMT == kW_FP8>(kGrouped<FMT> ? part[y] : acc[y], r0, r1, r2, r3, b0, b1);
           }
         }
       }
       if (kGrouped<FMT>) {
+        float2 xv = make_float2(0.f, 0.f);
+        if (kCorrect) xv = *reinterpret_cast<const float2*>(xsum + group * 8 + 2 * t4);
 #pragma unroll
         for (int y = 0; y < 2; ++y)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[y][j] = fmaf(part[y][j], sc[2 * y + (j >> 1)], acc[y][j]);
+          for (int j = 0; j < 4; ++j) {
+            const int q = 2 * y + (j >> 1);
+            if (kCorrect) part[y][j] = fmaf(-off[q].plus, j & 1 ? xv.y : xv.x, part[y][j]);
+            acc[y][j] = fmaf(part[y][j], sc[q], acc[y][j]);
+          }
       }
+      src += kStage;
+      if (src >= iend) src -= static_cast<uint32_t>(depth * kStage);
     }
-    // join the warps' sums: thread (i, token, gate or up)
+    // Join the warps' sums: thread (row, token, gate or up) of the first eight
+    // warps.  With two buffers the other warps go on to the next unit.
+    float* rd = red + buf * (kRedBytes / 4);
 #pragma unroll
     for (int y = 0; y < 2; ++y)
 #pragma unroll
       for (int j = 0; j < 4; j += 2)
-        *reinterpret_cast<float2*>(red + (warp * 32 + y * 16 + g + 4 * j) * 8 + 2 * t4) =
+        *reinterpret_cast<float2*>(rd + warp * kRedWarp + y * kRedHalf + (g + 4 * j) * 8 + 2 * t4) =
             make_float2(acc[y][j], acc[y][j + 1]);
     __syncthreads();
     if (tid < 256) {
-      const int half = tid >> 7 & 1, i = tid >> 3 & 15, t = tid & 7;
+      const int half = tid & 1, t = (tid >> 1) & 7, i = tid >> 4;
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += red[(w * 32 + half * 16 + i) * 8 + t];
-      if (half) red[(16 + i) * 8 + t] = v;  // (row of warp 0, read by this thread alone)
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      for (int w = 0; w < kWarps; ++w) v += rd[w * kRedWarp + half * kRedHalf + i * 8 + t];
+      float up = __shfl_xor_sync(0xffffffffu, v, 1);
       if (!half && t < a.T && (r.tokens[x] >> t & 1)) {
-        float up = red[(16 + i) * 8 + t];
         if (FMT == kW_FP8) {
           const float s = a1 * static_cast<const float*>(a.w13_scale)[r.expert[x]];
           v *= s;
@@ -461,7 +689,13 @@ __global__ void __launch_bounds__(kThreads, 1) few_up_kernel(GateArgs gate, FewA
         }
       }
     }
-    __syncthreads();
+    if (reds == 2) buf ^= 1;
+    else __syncthreads();
+    tile += gridDim.x;
+    while (tile >= tiles) {
+      tile -= tiles;
+      ++x;
+    }
   }
   if (FMT == kW_FP8 && a.a2 == nullptr) {
     amax = block_max(amax, red);
@@ -478,23 +712,126 @@ __host__ __device__ constexpr int down_stage(int tokens) {
   return Fmt<FMT>::DOWN * 1024 + (kGrouped<FMT> ? 128 : 0) + tokens * Fmt<FMT>::DOWN * Fmt<FMT>::KC * 4;
 }
 
-template <int FMT>
-__global__ void __launch_bounds__(kThreads, 1) few_down_kernel(FewArgs a, int up_ctas, int ring_bytes) {
+template <int FMT, int EPL>
+__global__ void __launch_bounds__(kThreads, 1) few_down_kernel(GateArgs gate, FewArgs a, int up_ctas, int ring_bytes) {
   extern __shared__ __align__(128) uint8_t few_smem[];
   using F = Fmt<FMT>;
   Routing& r = *reinterpret_cast<Routing*>(few_smem);
-  float* red = reinterpret_cast<float*>(few_smem + kRoutingBytes);  // [warp][16 rows][token]
-  Weights weight = reinterpret_cast<Weights>(few_smem + kRoutingBytes + kRedBytes / 2);
-  uint8_t* rings = few_smem + kRoutingBytes + kRedBytes / 2 + kWeightBytes;
+  float* red = reinterpret_cast<float*>(few_smem + kRoutingBytes);  // [2][warp][16 rows][token]
+  Weights weight = reinterpret_cast<Weights>(few_smem + kRoutingBytes + kDownRedBytes);
+  uint8_t* rings = few_smem + kRoutingBytes + kDownRedBytes + kWeightBytes;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+
+  // Before the first kernel is waited for: the gate once more and the first
+  // weights.  (It lets this one start when its own CTAs have passed their wait,
+  // so the scores and weights, which precede it, are there.)
+  route<EPL>(gate, a, r, weight, reinterpret_cast<float*>(rings), [] {});
+
+  constexpr int STEP = F::KC * F::DOWN;
+  constexpr int kActs = F::DOWN * 1024 + (kGrouped<FMT> ? 128 : 0);
+  constexpr int kTok = F::DOWN * F::KC * 4;  // a token's activations in a stage
+  const int stage = down_stage<FMT>(r.most);
+  const int depth = min(kMaxDepth, ring_bytes / (kWarps * stage));
+  const int per = a.I / STEP;  // steps of an expert
+  const int nsteps = r.count * per;
+  const int part_no = part_of(warp);
+  const int s0 = static_cast<int>(static_cast<int64_t>(nsteps) * part_no / kWarps);
+  const int s1 = static_cast<int>(static_cast<int64_t>(nsteps) * (part_no + 1) / kWarps);
+  const uint32_t ring = smem_u32(rings) + static_cast<uint32_t>(warp * depth * stage);
+  const uint32_t iend = ring + static_cast<uint32_t>(depth * stage);
+  const int64_t rb = row_bytes<FMT>(a.I), to8 = 8 * rb;
+  const int G = a.I / 128;
+  const bool zero = a.w2_zero != nullptr;
+  const bool dynamic = FMT == kW_FP8 && a.a2 == nullptr;
+  const bool both = FMT != kW_FP8 || dynamic;  // two halves of an activation
+  const int units = a.H / 16;
+  const int x0 = s0 / per, c0 = s0 - x0 * per;  // where this warp's part begins
+
+  // Where a stage holds the activations of this lane's token: one place for each
+  // token that chose the expert (a lane whose token did not reads the last one,
+  // and its sums are left out).
+  auto place_of = [&](uint32_t mask) {
+    const int at = min(__popc(mask & ((1u << g) - 1u)), __popc(mask) - 1);
+    return kActs + static_cast<uint32_t>(at * kTok + t4 * 16);
+  };
+  struct Cursor {  // of the issue side
+    int unit, left, x, c;       // unit, steps left of the part, expert, its step
+    uint32_t dst;
+    const uint8_t* w;           // weights of the step, row g
+    const uint16_t* act;        // this lane's token, or null
+    uint32_t place;             // where its activations go in a stage
+    int64_t at;                 // row `lane`'s scale
+  };
+  auto start_expert = [&](Cursor& c) {
+    const int64_t row = static_cast<int64_t>(r.expert[c.x]) * a.H + c.unit * 16;
+    c.w = static_cast<const uint8_t*>(a.w2) + (row + g) * rb + row_bytes<FMT>(c.c * STEP) + t4 * 16;
+    c.at = (row + (lane & 15)) * G + c.c * STEP / 128;
+    const uint32_t mask = r.tokens[c.x];
+    c.act = (mask >> g & 1) ? a.act + static_cast<size_t>(r.slot[c.x][g]) * 2 * a.I + c.c * STEP + t4 * 8 : nullptr;
+    c.place = place_of(mask);
+  };
+  auto start_unit = [&](Cursor& c) {
+    c.left = s1 - s0;
+    c.x = x0;
+    c.c = c0;
+    if (c.left > 0 && c.unit < units) start_expert(c);
+    else c.unit = units;
+  };
+  auto issue = [&](Cursor& c, bool weights, bool acts) {
+    if (c.unit < units) {
+      if (weights) {
+#pragma unroll
+        for (int u = 0; u < F::DOWN; ++u) {
+          cp_async16(c.dst + u * 1024 + lane * 16, c.w + u * 64);
+          cp_async16(c.dst + u * 1024 + 512 + lane * 16, c.w + u * 64 + to8);
+        }
+        if (kGrouped<FMT> && lane < 16) {
+          const uint32_t d = c.dst + F::DOWN * 1024 + (lane & 7) * 8 + (lane >> 3) * 4;
+          cp_async4(d, static_cast<const uint16_t*>(a.w2_scale) + (c.at & ~1ll));
+          if (zero) cp_async4(d + 64, a.w2_zero + (c.at & ~3ll));
+        }
+      }
+      if (acts && c.act != nullptr) {
+        // this lane's token: its slices of both halves
+        const uint32_t d = c.dst + c.place;
+#pragma unroll
+        for (int n = 0; n < F::DOWN * F::NS; ++n) {
+          cp_async16(d + n * 64, c.act + n * 32);
+          if (both) cp_async16(d + kTok / 2 + n * 64, c.act + a.I + n * 32);
+        }
+      }
+      c.w += F::DOWN * 64;
+      c.at += 1;
+      if (c.act != nullptr) c.act += STEP;
+      ++c.c;
+      if (--c.left == 0) {
+        c.unit += gridDim.x;
+        start_unit(c);
+      } else if (c.c == per) {
+        c.c = 0;
+        ++c.x;
+        start_expert(c);
+      }
+    }
+    c.dst += stage;
+    if (c.dst >= iend) c.dst -= static_cast<uint32_t>(depth * stage);
+  };
+  static_assert(!kGrouped<FMT> || STEP == 128, "a step is a group");
+  Cursor cur;
+  cur.unit = blockIdx.x;
+  cur.dst = ring;
+  start_unit(cur);
+  {
+    Cursor early = cur;
+    for (int i = 0; i < depth - 1; ++i) issue(early, true, false);
+  }
   pdl_wait();
   pdl_trigger();
-  for (int s = tid; s < a.T * a.k; s += kThreads) {
-    r.ids[s] = a.ids[s];
-    r.w[s] = a.topk_w[s];
+  for (int i = 0; i < depth - 1; ++i) {
+    issue(cur, false, true);
+    cp_async_commit();
   }
   float a2 = 1.f;
-  const bool dynamic = FMT == kW_FP8 && a.a2 == nullptr;
   if (FMT == kW_FP8) {
     if (dynamic) {
       float m = 0.f;
@@ -503,145 +840,111 @@ __global__ void __launch_bounds__(kThreads, 1) few_down_kernel(FewArgs a, int up
     } else {
       a2 = a.a2[0];
     }
-  }
-  __syncthreads();
-  build_routing(r, a, weight);
-  if (FMT == kW_FP8) {  // the experts' scales go with the weights of the sum
+    // the experts' scales go with the weights of the sum
     for (int i = tid; i < r.count * kFewMaxTokens; i += kThreads)
       (&weight[0][0])[i] *= a2 * static_cast<const float*>(a.w2_scale)[r.expert[i / kFewMaxTokens]];
     __syncthreads();
   }
-
-  constexpr int STEP = F::KC * F::DOWN;
-  const int stage = down_stage<FMT>(r.most);
-  const int depth = min(kMaxDepth, ring_bytes / (kWarps * stage));
-  const int per = a.I / STEP;  // steps of an expert
-  const int nsteps = r.count * per;
-  const int s0 = static_cast<int>(static_cast<int64_t>(nsteps) * warp / kWarps);
-  const int s1 = static_cast<int>(static_cast<int64_t>(nsteps) * (warp + 1) / kWarps);
-  const uint32_t ring = smem_u32(rings) + static_cast<uint32_t>(warp * depth * stage);
-  const int64_t rb = row_bytes<FMT>(a.I);
-  const int G = a.I / 128;
-  const bool zero = a.w2_zero != nullptr;
-  constexpr int kActs = F::DOWN * 1024 + (kGrouped<FMT> ? 128 : 0);
-  constexpr int kTok = F::DOWN * F::KC * 4;  // a token's activations in a stage
   const float rs = 1.0f / a2;
-  const int units = a.H / 16;
 
-  int iu = blockIdx.x, is = s0, islot = 0;
-  auto issue = [&] {
-    if (iu < units && s0 < s1) {
-      const int x = is / per, k0 = (is - x * per) * STEP;
-      const int64_t row = static_cast<int64_t>(r.expert[x]) * a.H + iu * 16;
-      const uint8_t* src = static_cast<const uint8_t*>(a.w2) + (row + g) * rb + row_bytes<FMT>(k0) + t4 * 16;
-      const uint32_t dst = ring + static_cast<uint32_t>(islot * stage);
-#pragma unroll
-      for (int u = 0; u < F::DOWN; ++u)
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          cp_async16(dst + static_cast<uint32_t>((2 * u + q) * 512 + lane * 16), src + u * 64 + q * 8 * rb);
-      if (kGrouped<FMT> && lane < 16) {
-        const int64_t at = (row + lane) * G + k0 / 128;
-        cp_async4(dst + F::DOWN * 1024 + lane * 4, static_cast<const uint16_t*>(a.w2_scale) + (at & ~1ll));
-        if (zero) cp_async4(dst + F::DOWN * 1024 + 64 + lane * 4, a.w2_zero + (at & ~3ll));
-      }
-      const uint32_t mask = r.tokens[x];
-      if (mask >> g & 1) {
-        // this lane's token: its slices of both halves
-        const uint32_t d = dst + kActs + static_cast<uint32_t>(__popc(mask & ((1u << g) - 1u)) * kTok + t4 * 16);
-        const uint16_t* act = a.act + static_cast<size_t>(r.slot[x][g]) * 2 * a.I + k0 + t4 * 8;
-#pragma unroll
-        for (int n = 0; n < F::DOWN * F::NS; ++n) {
-          cp_async16(d + n * 64, act + n * 32);
-          if (FMT != kW_FP8 || dynamic) cp_async16(d + kTok / 2 + n * 64, act + a.I + n * 32);
-        }
-      }
-      if (++is == s1) {
-        is = s0;
-        iu += gridDim.x;
-      }
-    }
-    cp_async_commit();
-    if (++islot == depth) islot = 0;
-  };
-  for (int i = 0; i < depth - 1; ++i) issue();
-
-  int slot = 0;
+  uint32_t src = ring;
+  int buf = 0;
   for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
     float acc[4] = {};
-    float part[4] = {};
-    for (int s = s0; s < s1; ++s) {
-      const int x = s / per, k0 = (s - x * per) * STEP;
-      __syncwarp();
-      issue();
-      cp_async_wait(depth - 1);
-      __syncwarp();
-      const uint32_t src = ring + static_cast<uint32_t>(slot * stage);
-      if (++slot == depth) slot = 0;
-      float sc[2] = {1.f, 1.f};
-      Offset off[2] = {};
-      if (kGrouped<FMT>) {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int rr = g + 8 * q;
-          const int64_t at = (static_cast<int64_t>(r.expert[x]) * a.H + unit * 16 + rr) * G + k0 / 128;
-          group_of<FMT>(src + F::DOWN * 1024 + rr * 4, src + F::DOWN * 1024 + 64 + rr * 4, at, zero, sc[q], off[q]);
-        }
-      }
+    float part[2][4] = {};  // of the activations' two halves
+    int x = x0, c = c0;
+    for (int s = s0; s < s1; c = 0, ++x) {
+      const int end = min(s1, s + per - c);  // of this expert's part
       const uint32_t mask = r.tokens[x];
-      const bool mine = mask >> g & 1;
-      const uint32_t acts = src + kActs + static_cast<uint32_t>(__popc(mask & ((1u << g) - 1u)) * kTok + t4 * 16);
+      const uint32_t place = place_of(mask);
+      const bool use0 = mask >> (2 * t4) & 1, use1 = mask >> (2 * t4 + 1) & 1;
+      const float2 wt = *reinterpret_cast<const float2*>(&weight[x][2 * t4]);
+      uint32_t at[2];
 #pragma unroll
-      for (int u = 0; u < F::DOWN; ++u) {
-        uint4 w[2];
+      for (int q = 0; q < 2; ++q)
+        at[q] = (static_cast<uint32_t>(r.expert[x]) * static_cast<uint32_t>(a.H) +
+                 static_cast<uint32_t>(unit * 16 + g + 8 * q)) * static_cast<uint32_t>(G) + static_cast<uint32_t>(c);
+      auto join = [&](const float (&sc)[2]) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) w[q] = lds128(src + static_cast<uint32_t>((2 * u + q) * 512 + lane * 16));
+        for (int j = 0; j < 4; ++j) {
+          if (j & 1 ? use1 : use0) acc[j] = fmaf(part[0][j] + part[1][j], sc[j >> 1] * (j & 1 ? wt.y : wt.x), acc[j]);
+          if (!kGrouped<FMT>) part[0][j] = part[1][j] = 0.f;
+        }
+      };
+      for (; s < end; ++s) {
+        __syncwarp();
+        issue(cur, true, true);
+        cp_async_commit();
+        cp_async_wait(depth - 1);
+        __syncwarp();
+        float sc[2] = {1.f, 1.f};
+        Offset off[2] = {};
+        if (kGrouped<FMT>) {
+          const uint2 sw = lds64(src + F::DOWN * 1024 + g * 8);  // rows g, g + 8
+          uint2 zw = make_uint2(0, 0);
+          if (zero) zw = lds64(src + F::DOWN * 1024 + 64 + g * 8);
 #pragma unroll
-        for (int n = 0; n < F::NS; ++n) {
-          uint4 hi = make_uint4(0, 0, 0, 0), lo = make_uint4(0, 0, 0, 0);
-          if (mine) {
-            hi = lds128(acts + (u * F::NS + n) * 64);
-            if (FMT != kW_FP8 || dynamic) lo = lds128(acts + kTok / 2 + (u * F::NS + n) * 64);
-            if (FMT == kW_FP8 && dynamic) {
+          for (int q = 0; q < 2; ++q) {
+            group_of<FMT>(q ? sw.y : sw.x, q ? zw.y : zw.x, at[q], zero, sc[q], off[q]);
+            ++at[q];
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < F::DOWN; ++u) {
+          uint4 w[2];
+#pragma unroll
+          for (int q = 0; q < 2; ++q) w[q] = lds128(src + static_cast<uint32_t>((2 * u + q) * 512 + lane * 16));
+#pragma unroll
+          for (int n = 0; n < F::NS; ++n) {
+            uint4 hi = lds128(src + place + (u * F::NS + n) * 64), lo = make_uint4(0, 0, 0, 0);
+            if (both) lo = lds128(src + place + kTok / 2 + (u * F::NS + n) * 64);
+            if (dynamic) {
               auto q2 = [&](uint32_t h, uint32_t l) {
                 return quantised_f16x2(__uint_as_float(__byte_perm(l, h, 0x5410)) * rs,
                                        __uint_as_float(__byte_perm(l, h, 0x7632)) * rs);
               };
               hi = make_uint4(q2(hi.x, lo.x), q2(hi.y, lo.y), q2(hi.z, lo.z), q2(hi.w, lo.w));
             }
-          }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t a0, a1, a2r, a3;
-            convert<FMT>(w[0], 2 * n + h, off[0], a0, a2r);
-            convert<FMT>(w[1], 2 * n + h, off[1], a1, a3);
-            mma16816<FMT == kW_FP8>(part, a0, a1, a2r, a3, h ? hi.z : hi.x, h ? hi.w : hi.y);
-            if (FMT != kW_FP8) mma16816<false>(part, a0, a1, a2r, a3, h ? lo.z : lo.x, h ? lo.w : lo.y);
+            for (int h = 0; h < 2; ++h) {
+              uint32_t r0, r1, r2, r3;
+              convert<FMT, true>(w[0], 2 * n + h, off[0], r0, r2);
+              convert<FMT, true>(w[1], 2 * n + h, off[1], r1, r3);
+              const uint32_t b0 = h ? hi.z : hi.x, b1 = h ? hi.w : hi.y, l0 = h ? lo.z : lo.x, l1 = h ? lo.w : lo.y;
+              if (FMT == kW_FP8) {
+                mma16816<true>(part[h], r0, r1, r2, r3, b0, b1);
+              } else if (kGrouped<FMT> && u == 0 && n == 0 && h == 0) {
+                mma16816_first<false>(part[0], r0, r1, r2, r3, b0, b1);
+                mma16816_first<false>(part[1], r0, r1, r2, r3, l0, l1);
+              } else {
+                mma16816<false>(part[0], r0, r1, r2, r3, b0, b1);
+                mma16816<false>(part[1], r0, r1, r2, r3, l0, l1);
+              }
+            }
           }
         }
+        if (kGrouped<FMT>) join(sc);  // the group's scales
+        src += stage;
+        if (src >= iend) src -= static_cast<uint32_t>(depth * stage);
       }
-      // the group's or expert's end: times the row's scale and the tokens' weights
-      if (kGrouped<FMT> || s + 1 == s1 || (s + 1) / per != x) {
-        const float w0 = weight[x][2 * t4], w1 = weight[x][2 * t4 + 1];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[j] = fmaf(part[j], sc[j >> 1] * (j & 1 ? w1 : w0), acc[j]);
-          part[j] = 0.f;
-        }
+      if (!kGrouped<FMT>) {
+        const float one[2] = {1.f, 1.f};
+        join(one);
       }
     }
+    float* rd = red + buf * (kWarps * 128);
+    buf ^= 1;
 #pragma unroll
     for (int j = 0; j < 4; j += 2)
-      *reinterpret_cast<float2*>(red + (warp * 16 + g + 4 * j) * 8 + 2 * t4) = make_float2(acc[j], acc[j + 1]);
+      *reinterpret_cast<float2*>(rd + (warp * 16 + g + 4 * j) * 8 + 2 * t4) = make_float2(acc[j], acc[j + 1]);
     __syncthreads();
     if (tid < 128) {
       const int row = tid & 15, t = tid >> 4;
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += red[(w * 16 + row) * 8 + t];
+      for (int w = 0; w < kWarps; ++w) v += rd[(w * 16 + row) * 8 + t];
       if (t < a.T) a.out[static_cast<size_t>(t) * a.H + unit * 16 + row] = __float2bfloat16_rn(v);
     }
-    __syncthreads();
   }
 }
 
@@ -661,41 +964,41 @@ cudaError_t allow_smem(K kernel, int* configured) {
 }
 
 template <int FMT, int EPL>
-cudaError_t launch_up(const GateArgs& g, const FewArgs& a, int grid, cudaStream_t s) {
-  static int configured[64] = {};
-  cudaError_t err = allow_smem(few_up_kernel<FMT, EPL>, configured);
+cudaError_t launch_both(const GateArgs& g, const FewArgs& a, int sms, cudaStream_t s) {
+  static int configured_up[64] = {}, configured_down[64] = {};
+  cudaError_t err = allow_smem(few_up_kernel<FMT, EPL>, configured_up);
+  if (err == cudaSuccess) err = allow_smem(few_down_kernel<FMT, EPL>, configured_down);
   if (err != cudaSuccess) return err;
-  const size_t fixed = kRoutingBytes + kRedBytes + (static_cast<size_t>(a.T) * token_stride(a.H) + 127) / 128 * 128;
   const size_t gate = static_cast<size_t>(a.T) * 32 * EPL * 4;
-  int depth = static_cast<int>((kMaxSmem - std::min(fixed, kMaxSmem)) / (kWarps * up_stage<FMT>()));
-  if (depth > kMaxDepth) depth = kMaxDepth;
-  if (depth < 2) return cudaErrorInvalidValue;  // (refused before: kFewMaxTokenValues)
-  size_t smem = static_cast<size_t>(depth) * kWarps * up_stage<FMT>();
-  smem = fixed + (smem > gate ? smem : gate);
-  return launch_pdl(few_up_kernel<FMT, EPL>, dim3(grid), dim3(kThreads), smem, s, g, a, depth);
+  const size_t tokens = (static_cast<size_t>(a.T) * token_stride(a.H) + 127) / 128 * 128;
+  const size_t sums = FMT == kW_INT4 ? static_cast<size_t>(a.H) / 128 * 32 : 0;
+  const size_t stage = static_cast<size_t>(kWarps) * up_stage<FMT>();
+  // a second reduction buffer where it leaves four stages
+  const int reds = kRoutingBytes + 2 * kRedBytes + sums + tokens + 4 * stage <= kMaxSmem ? 2 : 1;
+  const size_t fixed = kRoutingBytes + reds * kRedBytes + sums + tokens;
+  if (fixed + 2 * stage > kMaxSmem) return cudaErrorInvalidValue;  // (refused before: kFewMaxTokenValues)
+  const int depth = static_cast<int>(std::min<size_t>(kMaxDepth, (kMaxSmem - fixed) / stage));
+  const int up_grid = std::min(sms, std::min(a.E, a.T * a.k) * (a.I / 16));
+  err = launch_pdl(few_up_kernel<FMT, EPL>, dim3(up_grid), dim3(kThreads), fixed + std::max(depth * stage, gate), s, g,
+                   a, depth, reds);
+  if (err != cudaSuccess) return err;
+  constexpr size_t down_fixed = kRoutingBytes + kDownRedBytes + kWeightBytes;
+  static_assert(kWarps * 2 * down_stage<FMT>(kFewMaxTokens) + down_fixed <= kMaxSmem,
+                "two stages a warp for every routing");
+  return launch_pdl(few_down_kernel<FMT, EPL>, dim3(std::min(sms, a.H / 16)), dim3(kThreads), kMaxSmem, s, g, a,
+                    up_grid, static_cast<int>(kMaxSmem - down_fixed));
 }
 
 template <int FMT>
-cudaError_t launch_both(const GateArgs& g, const FewArgs& a, int sms, cudaStream_t s) {
-  const int up_units = std::min(a.E, a.T * a.k) * (a.I / 16);
-  const int up_grid = std::min(sms, up_units);
-  cudaError_t err = a.E <= 64    ? launch_up<FMT, 2>(g, a, up_grid, s)
-                    : a.E <= 256 ? launch_up<FMT, 8>(g, a, up_grid, s)
-                                 : launch_up<FMT, 32>(g, a, up_grid, s);
-  if (err != cudaSuccess) return err;
-  static int configured[64] = {};
-  err = allow_smem(few_down_kernel<FMT>, configured);
-  if (err != cudaSuccess) return err;
-  const size_t fixed = kRoutingBytes + kRedBytes / 2 + kWeightBytes;
-  const int ring = static_cast<int>(kMaxSmem - fixed);
-  static_assert(kWarps * 2 * down_stage<FMT>(kFewMaxTokens) + kRoutingBytes + kRedBytes / 2 + kWeightBytes <= kMaxSmem,
-                "two stages a warp for every routing");
-  return launch_pdl(few_down_kernel<FMT>, dim3(std::min(sms, a.H / 16)), dim3(kThreads), kMaxSmem, s, a, up_grid, ring);
+cudaError_t launch_gate_width(const GateArgs& g, const FewArgs& a, int sms, cudaStream_t s) {
+  if (a.E <= 64) return launch_both<FMT, 2>(g, a, sms, s);
+  if (a.E <= 256) return launch_both<FMT, 8>(g, a, sms, s);
+  return launch_both<FMT, 32>(g, a, sms, s);
 }
 
 }  // namespace
 
-static_assert(kRoutingBytes + kRedBytes + 2 * static_cast<size_t>(kFewMaxTokenValues) + 128 +
+static_assert(kRoutingBytes + kRedBytes + 2 * static_cast<size_t>(kFewMaxTokenValues) + 128 + 8192 / 4 +
                       2 * kWarps * up_stage<kW_INT4>() <=
                   kMaxSmem,
               "two stages a warp beside the most tokens");
@@ -705,10 +1008,10 @@ cudaError_t launch_few(const GateArgs& g, const FewArgs& a, cudaStream_t s) {
   cudaError_t err = device_info(&di);
   if (err != cudaSuccess) return err;
   switch (a.wkind) {
-    case kW_BF16: return launch_both<kW_BF16>(g, a, di.sms, s);
-    case kW_FP8: return launch_both<kW_FP8>(g, a, di.sms, s);
-    case kW_INT8: return launch_both<kW_INT8>(g, a, di.sms, s);
-    default: return launch_both<kW_INT4>(g, a, di.sms, s);
+    case kW_BF16: return launch_gate_width<kW_BF16>(g, a, di.sms, s);
+    case kW_FP8: return launch_gate_width<kW_FP8>(g, a, di.sms, s);
+    case kW_INT8: return launch_gate_width<kW_INT8>(g, a, di.sms, s);
+    default: return launch_gate_width<kW_INT4>(g, a, di.sms, s);
   }
 }
 

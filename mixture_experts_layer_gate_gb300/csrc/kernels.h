@@ -242,8 +242,6 @@ struct FewArgs {
   const uint8_t* w2_zero;
   const float* a1;         // fp8 static scales, or null (dynamic)
   const float* a2;
-  int32_t* ids;            // [T, k]
-  float* topk_w;           // [T, k]
   uint16_t* act;           // [T * k, 2, I]: two 16-bit parts of each activation
   float* amax;             // fp8 dynamic: largest |act| of each CTA of the first kernel
   __nv_bfloat16* out;      // [T, H]

@@ -34,17 +34,13 @@ bool rows_ok(const void* p, int64_t stride, int64_t cols, size_t align) {
   } while (0)
 
 struct FewLayout {
-  size_t ids, w, amax, act, total;
+  size_t amax, act, total;
 };
 
 FewLayout few_layout(const moe_problem_t& p) {
   const size_t S = static_cast<size_t>(p.T) * p.top_k;
   FewLayout L;
   size_t o = kHeaderBytes;
-  L.ids = o;
-  o = align256(o + S * 4);
-  L.w = o;
-  o = align256(o + S * 4);
   L.amax = o;
   o = align256(o + kFewMaxCtas * 4);
   L.act = o;
@@ -225,8 +221,8 @@ moe_status_t moe_forward_few(const moe_problem_t* p, const moe_weights_t* w, con
   GateArgs g;
   g.logits = logits;
   g.bias = p->scoring == MOE_SCORE_SIGMOID ? bias : nullptr;
-  g.ids = reinterpret_cast<int32_t*>(base + L.ids);
-  g.w = reinterpret_cast<float*>(base + L.w);
+  g.ids = nullptr;  // the kernels keep them to themselves
+  g.w = nullptr;
   g.T = p->T;
   g.E = p->E;
   g.k = p->top_k;
@@ -245,8 +241,6 @@ moe_status_t moe_forward_few(const moe_problem_t* p, const moe_weights_t* w, con
   a.w2_zero = static_cast<const uint8_t*>(w->w2_zero);
   a.a1 = w->a1_scale;
   a.a2 = w->a2_scale;
-  a.ids = g.ids;
-  a.topk_w = g.w;
   a.act = reinterpret_cast<uint16_t*>(base + L.act);
   a.amax = reinterpret_cast<float*>(base + L.amax);
   a.err = reinterpret_cast<uint32_t*>(base);
