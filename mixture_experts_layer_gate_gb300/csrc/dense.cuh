@@ -29,16 +29,27 @@ namespace moe {
 namespace dense {
 
 constexpr int kJoinWarps = 8;
-constexpr int kFirstJoin = 4;  // warp 0 issues TMA, warp 1 MMAs; 2 and 3 fill their warpgroup
+constexpr int kFirstJoin = 4;  // warp 0 issues TMA, warp 1 MMAs, 2 and 3 fetch scales
 constexpr int kThreads = 32 * (kFirstJoin + kJoinWarps);
 // Registers a thread: the launch gives 168 x 384 (three warps per sub-partition);
 // 256-column tiles hold 128 sums per joining thread, so the first warpgroup
-// hands most of its share over (128 x (40 + 2 x 224) <= 168 x 384).
-constexpr int kLeanRegs = 40, kJoinRegs = 224, kLaunchRegs = 168;
+// hands most of its share over (128 x (56 + 2 x 224) = 168 x 384).
+constexpr int kLeanRegs = 56, kJoinRegs = 224, kLaunchRegs = 168;
 // two accumulators
 __host__ __device__ constexpr uint32_t tmem_cols(int bn) { return 2u * static_cast<uint32_t>(bn); }
 constexpr int kMaxStages = 12;
 constexpr int kMiscBytes = 4096;        // barriers, flags and the row maxima
+// Products of scales, 8-bit operands: groups of four k-blocks x 128 rows x two
+// weight-scale rows.
+constexpr uint32_t kScaleSlots = 4, kScaleSlotBytes = 2 * 4 * 128 * 4;
+// Transposition of the stored sums: per joining warp 32 rows of 16 floats, rows
+// 80 bytes apart (eight lanes' 16-byte stores fall into different banks).
+constexpr int kStageRow = 80, kStageBytes = 32 * kStageRow;
+template <int KIND, bool SWIGLU>
+__host__ __device__ constexpr int fixed_bytes() {
+  return kMiscBytes + (KIND == 0 ? static_cast<int>(kScaleSlots * kScaleSlotBytes) : 0) +
+         (SWIGLU ? 0 : kJoinWarps * kStageBytes);
+}
 constexpr int kTileABytes = 128 * 128;  // what an MMA reads of A: 128 rows of a k-block
 
 enum Kind : int { kE4M3 = 0, kHalf = 1 };
@@ -61,6 +72,7 @@ struct Params {
   int out_dtype;         // moe_dtype_t
   int accumulate;
   int vec;               // out rows take 16-byte stores
+  int vec_scale;         // rows of a_scale take 16-byte loads at multiples of four blocks
 };
 
 struct Maps {
@@ -75,19 +87,29 @@ __host__ __device__ constexpr int stage_bytes(int arows, int bn, bool pair) {
 // rows fall into different banks
 __host__ __device__ constexpr int part_ld(int bn) { return bn + 4; }
 
-// 32 columns of this lane, complete on return
+// 32 columns of this lane; r is there after tmem_ld32_wait(r)
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32"
       " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
-      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
+}
+
+// waits for this thread's loads; r passes through, so that nothing reads it earlier
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 
 // 16 columns of this lane, complete on return
@@ -100,6 +122,21 @@ __device__ __forceinline__ void tmem_ld16_wait(uint32_t taddr, uint32_t (&r)[16]
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
+}
+
+__device__ __forceinline__ float lds_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_f4(uint32_t a, float4 v) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
 
 // acc += d * s, two floats at a time
@@ -231,9 +268,13 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
   const uint32_t sbytes = static_cast<uint32_t>(stage_bytes(p.arows, BN, PAIR));
   // barriers first, then the ring
   const uint32_t bars = base_u32;
-  const uint32_t ring = base_u32 + kMiscBytes;
+  const uint32_t ring0 = base_u32 + kMiscBytes;  // scale products
+  const uint32_t ring = base_u32 + fixed_bytes<KIND, SWIGLU>();
+  const uint32_t stage0 = ring - kJoinWarps * kStageBytes;
 #define FULL(s) (bars + 8u * static_cast<uint32_t>(s))
 #define EMPTY(s) (bars + 8u * static_cast<uint32_t>(kMaxStages + (s)))
+#define SFULL(s) (bars + 16u * kMaxStages + 80u + 8u * (s))
+#define SEMPTY(s) (bars + 16u * kMaxStages + 80u + 8u * (kScaleSlots + (s)))
   const uint32_t dfull = bars + 16u * kMaxStages, dempty = dfull + 16u, drain = dfull + 32u;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(base + 16 * kMaxStages + 40);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(base + 16 * kMaxStages + 44);
@@ -253,6 +294,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     }
     mbar_init(drain, 1u);
     for (uint32_t q = 0; q < 4; ++q) mbar_init(pairs + 8u * q, 2u);
+    for (uint32_t q = 0; q < kScaleSlots; ++q) {
+      mbar_init(SFULL(q), 1u);
+      mbar_init(SEMPTY(q), kJoinWarps);
+    }
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&maps.a);
@@ -391,6 +436,57 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
       }
     }
     }
+    if (KIND == kE4M3 && warp >= 2) {
+      // ------------------------------------------------------- scale warps
+      // A row's scale times its weight block's, for four k-blocks at a time and
+      // up to kScaleSlots such groups ahead of the joining warps (a load from L2
+      // takes longer than a block's product).  The two warps take turns.
+      uint32_t n = 0;
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += step) {
+        const int m0 = (t % p.mt) * kTileM + (PAIR ? 128 * static_cast<int>(rank) : 0);
+        const int n0 = (t / p.mt) * (SWIGLU ? 128 : BN);
+        // the tile's two weight-scale rows: gate and up, or the column halves
+        const int last = (p.N - 1) / 128;
+        const float* ws0 = p.w_scale + static_cast<int64_t>(n0 / 128) * p.KB;
+        const float* ws1 = p.w_scale + static_cast<int64_t>(SWIGLU ? (n0 + p.N) / 128 : min(n0 / 128 + 1, last)) * p.KB;
+        for (int kq = kb0; kq < kb1; kq += 4, ++n) {
+          if ((n & 1u) != static_cast<uint32_t>(warp & 1)) continue;
+          const uint32_t slot = n & (kScaleSlots - 1);
+          if (!wait(SEMPTY(slot), (n / kScaleSlots & 1u) ^ 1u, abort_flag, p.err, 0x670u)) {
+            ok = false;
+            break;
+          }
+          float4 sa[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float* as = p.a_scale + static_cast<int64_t>(min(m0 + 32 * q + lane, p.M - 1)) * p.a_scale_stride;
+            if (p.vec_scale && kq + 4 <= kb1) {
+              sa[q] = *reinterpret_cast<const float4*>(as + kq);
+            } else {
+              sa[q].x = as[kq];
+              sa[q].y = as[min(kq + 1, kb1 - 1)];
+              sa[q].z = as[min(kq + 2, kb1 - 1)];
+              sa[q].w = as[min(kq + 3, kb1 - 1)];
+            }
+          }
+          float* dst = reinterpret_cast<float*>(base + kMiscBytes) + slot * (kScaleSlotBytes / 4) + lane;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int kb = min(kq + j, kb1 - 1);
+            const float w0 = ws0[kb], w1 = ws1[kb];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float v = j == 0 ? sa[q].x : j == 1 ? sa[q].y : j == 2 ? sa[q].z : sa[q].w;
+              dst[j * 128 + 32 * q] = v * w0;
+              dst[512 + j * 128 + 32 * q] = v * w1;
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cta(SFULL(slot));
+        }
+      }
+    }
     // Every warp leaves its role with the registers of the launch.  The joining
     // warps give theirs back before this warpgroup takes its own again: a warp
     // without a role that took them at once could leave a joining warp waiting
@@ -405,63 +501,83 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     const int quarter = warp & 3, half = (warp - kFirstJoin) >> 2;
     const uint32_t lane_base = static_cast<uint32_t>(32 * quarter) << 16;
     const uint32_t dempty_to = PAIR ? map_to_rank(dempty, 0) : dempty;
-    uint32_t buf = 0, dph = 0, tile = 0;
+    uint32_t buf = 0, dph = 0, tile = 0, quad = 0;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
       const int m0 = (t % p.mt) * kTileM + (PAIR ? 128 * static_cast<int>(rank) : 0);
       const int n0 = (t / p.mt) * (SWIGLU ? 128 : BN);
       const int row = m0 + 32 * quarter + lane;
       const bool live = m0 + 32 * quarter < p.M;  // some row of this warp exists
-      const float* as = p.a_scale + static_cast<int64_t>(min(row, p.M - 1)) * p.a_scale_stride;
-      // the weight scales of this warp's columns (SwiGLU: gate's and up's)
-      const int sb = SWIGLU ? n0 / 128 : min((n0 + half * W) / 128, (p.N - 1) / 128);
-      const float* ws0 = p.w_scale + static_cast<int64_t>(sb) * p.KB;
-      const float* ws1 = SWIGLU ? ws0 + static_cast<int64_t>(p.N / 128) * p.KB : ws0;
+      // columns of load c: SwiGLU takes 64 gate columns, then the 64 up columns
+      // that go with them
+      auto column_of = [&](int c) {
+        return static_cast<uint32_t>(SWIGLU ? 64 * half + (c & 1) * 32 + (c >> 1) * 128 : W * half + CH * c);
+      };
       uint64_t acc[W / 2];
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) acc[i] = 0;
-      float s_a = 1.f, s_0 = 1.f, s_1 = 1.f;
-      if (KIND == kE4M3) {
-        s_a = as[kb0];
-        s_0 = ws0[kb0];
-        s_1 = SWIGLU ? ws1[kb0] : s_0;
-      }
-      for (int kb = kb0; kb < kb1; kb += p.group) {
-        const uint64_t f0 = pair2(s_a * s_0), f1 = pair2(s_a * s_1);
-        if (KIND == kE4M3 && kb + 1 < kb1) {  // the next block's scales, while its product is formed
-          s_a = as[kb + 1];
-          s_0 = ws0[kb + 1];
-          s_1 = SWIGLU ? ws1[kb + 1] : s_0;
-        }
-        if (!wait(dfull + 8u * buf, dph, abort_flag, p.err, 0x640u)) {
+      for (int kq = kb0; kq < kb1 && ok; kq += 4 * p.group) {
+        const uint32_t slot = quad & (kScaleSlots - 1);
+        const uint32_t factors = ring0 + slot * kScaleSlotBytes + static_cast<uint32_t>(32 * quarter + lane) * 4u;
+        if (KIND == kE4M3 && !wait(SFULL(slot), quad / kScaleSlots & 1u, abort_flag, p.err, 0x660u)) {
           ok = false;
           break;
         }
-        tc_fence_after();
-        if (live) {
-          const uint32_t src = tmem + lane_base + buf * static_cast<uint32_t>(BN);
 #pragma unroll
-          for (int c = 0; c < NCH; ++c) {
-            // SwiGLU: 64 gate columns, then the 64 up columns that go with them
-            const uint32_t col = SWIGLU ? static_cast<uint32_t>(64 * half + (c & 1) * 32 + (c >> 1) * 128)
-                                        : static_cast<uint32_t>(W * half + CH * c);
-            if constexpr (CH == 32) {
-              uint32_t r[32];
-              tmem_ld32(src + col, r);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) fma2(acc[16 * c + j], r[2 * j], r[2 * j + 1], (SWIGLU && c >= 2) ? f1 : f0);
-            } else {
-              uint32_t r[16];
-              tmem_ld16_wait(src + col, r);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) fma2(acc[j], r[2 * j], r[2 * j + 1], f0);
-            }
+        for (int j4 = 0; j4 < 4; ++j4) {
+          if (kq + j4 * p.group >= kb1) break;
+          if (!wait(dfull + 8u * buf, dph, abort_flag, p.err, 0x640u)) {
+            ok = false;
+            break;
           }
+          tc_fence_after();
+          uint64_t g0, g1;
+          if (KIND == kE4M3) {
+            g0 = pair2(lds_f32(factors + static_cast<uint32_t>(SWIGLU || BN < 256 ? 0 : half) * 2048u + j4 * 512u));
+            g1 = SWIGLU ? pair2(lds_f32(factors + 2048u + j4 * 512u)) : g0;
+          } else {
+            g0 = g1 = pair2(1.f);
+          }
+          const uint32_t src = tmem + lane_base + buf * static_cast<uint32_t>(BN);
+          if constexpr (CH == 32) {
+            // a load of 32 columns runs while the 32 before are added
+            uint32_t r[2][32];
+            if (live) {
+              tmem_ld32(src + column_of(0), r[0]);
+#pragma unroll
+              for (int c = 0; c < NCH; ++c) {
+                tmem_ld32_wait(r[c & 1]);
+                if (c + 1 < NCH) tmem_ld32(src + column_of(c + 1), r[(c + 1) & 1]);
+                if (c + 1 == NCH) {
+                  tc_fence_before();
+                  if (lane == 0) mbar_arrive_cluster(dempty_to + 8u * buf);
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  fma2(acc[16 * c + j], r[c & 1][2 * j], r[c & 1][2 * j + 1], (SWIGLU && c >= 2) ? g1 : g0);
+              }
+            } else {
+              tc_fence_before();
+              if (lane == 0) mbar_arrive_cluster(dempty_to + 8u * buf);
+            }
+          } else {
+            if (live) {
+              uint32_t r[16];
+              tmem_ld16_wait(src + column_of(0), r);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) fma2(acc[j], r[2 * j], r[2 * j + 1], g0);
+            }
+            tc_fence_before();
+            if (lane == 0) mbar_arrive_cluster(dempty_to + 8u * buf);
+          }
+          buf ^= 1u;
+          if (buf == 0u) dph ^= 1u;
         }
-        tc_fence_before();
-        if (lane == 0) mbar_arrive_cluster(dempty_to + 8u * buf);
-        buf ^= 1u;
-        if (buf == 0u) dph ^= 1u;
+        if (KIND == kE4M3) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cta(SEMPTY(slot));
+          ++quad;
+        }
       }
       if (!ok) break;
 
@@ -469,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
         // partial sums into this CTA's shared memory (the ring is drained: the
         // last accumulator was finished by the last MMA that read it)
         if (row < p.M) {
-          float* dst = reinterpret_cast<float*>(base + kMiscBytes) + (32 * quarter + lane) * part_ld(BN);
+          float* dst = reinterpret_cast<float*>(base + fixed_bytes<KIND, SWIGLU>()) + (32 * quarter + lane) * part_ld(BN);
 #pragma unroll
           for (int c = 0; c < NCH; ++c) {
             const int col = SWIGLU ? 64 * half + (c & 1) * 32 + (c >> 1) * 128 : W * half + CH * c;
@@ -514,11 +630,28 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
                                 codes4(v[16 * j + 8], v[16 * j + 9], v[16 * j + 10], v[16 * j + 11], scale),
                                 codes4(v[16 * j + 12], v[16 * j + 13], v[16 * j + 14], v[16 * j + 15], scale));
         }
-      } else if (row < p.M) {
+      } else {
+        // 16 columns at a time through shared memory, so that four lanes write 16
+        // adjacent columns of a row: whole 32-byte sectors (one row per lane
+        // wrote 8 bytes of 32 rows at a time and took twice the product's time
+        // at M = 4096, N = 7168, K = 2048)
+        const uint32_t mine = stage0 + static_cast<uint32_t>(4 * half + quarter) * kStageBytes;
 #pragma unroll
-        for (int j = 0; j < W / 4; ++j) {
-          const float2 u = unpair(acc[2 * j]), v = unpair(acc[2 * j + 1]);
-          store4(p, row, n0 + W * half + 4 * j, make_float4(u.x, u.y, v.x, v.y));
+        for (int c = 0; c < W / 16; ++c) {
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 u = unpair(acc[8 * c + 2 * j]), v = unpair(acc[8 * c + 2 * j + 1]);
+            sts_f4(mine + static_cast<uint32_t>(lane * kStageRow + 16 * j), make_float4(u.x, u.y, v.x, v.y));
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2);
+            const float4 v = lds_f4(mine + static_cast<uint32_t>(r * kStageRow + 16 * (lane & 3)));
+            const int to = m0 + 32 * quarter + r;
+            if (to < p.M) store4(p, to, n0 + W * half + 16 * c + 4 * (lane & 3), v);
+          }
         }
       }
     }
@@ -529,6 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
   }
 #undef FULL
 #undef EMPTY
+#undef SFULL
+#undef SEMPTY
 
   if (PAIR || p.P > 1) cluster_sync_all();  // signals and partial sums have arrived
   if (!PAIR && p.P > 1) {
@@ -576,7 +711,8 @@ constexpr size_t kMaxSmem = 232448;
 
 // Dynamic shared memory for `stages` ring stages: what an MMA of a short A tile
 // reads past its rows, and a split-K partial, stay inside.
-inline size_t smem_bytes(const Params& p, int bn, bool pair) {
+template <int KIND, bool SWIGLU>
+size_t smem_bytes(const Params& p, int bn, bool pair) {
   size_t ring = static_cast<size_t>(p.stages) * stage_bytes(p.arows, bn, pair) + (kTileABytes - p.arows * 128);
   if (!pair && p.P > 1) {
     const int rows = p.M < 128 ? p.M : 128;
@@ -587,7 +723,7 @@ inline size_t smem_bytes(const Params& p, int bn, bool pair) {
   // shared memory as by columns, so that no CTA waits for another's
   // columns while its cluster waits for it
   const size_t floor = bn >= 256 ? 120 * 1024 : bn >= 128 ? 80 * 1024 : bn >= 64 ? 48 * 1024 : 0;
-  const size_t need = 1024 + kMiscBytes + ring;
+  const size_t need = 1024 + fixed_bytes<KIND, SWIGLU>() + ring;
   return need > floor ? need : floor;
 }
 
@@ -608,7 +744,7 @@ cudaError_t launch(const Maps& maps, const Params& p, int grid, cudaStream_t s) 
     if (BN == 256 && attr.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
     if (dev >= 0 && dev < 64) configured[dev] = 1;
   }
-  return launch_pdl_cluster(kernel, dim3(grid), dim3(kThreads), smem_bytes(p, BN, PAIR), s,
+  return launch_pdl_cluster(kernel, dim3(grid), dim3(kThreads), smem_bytes<KIND, SWIGLU>(p, BN, PAIR), s,
                             static_cast<unsigned>(PAIR ? 2 : p.P), maps, p);
 }
 
@@ -627,7 +763,8 @@ cudaError_t plan_and_launch(Params p, int bn, bool pair, bool swiglu, const void
   p.nt = (p.N + (swiglu ? 128 : bn) - 1) / (swiglu ? 128 : bn);
   p.arows = pair || p.M >= 128 ? 128 : (p.M + 7) / 8 * 8;
   const int sb = stage_bytes(p.arows, bn, pair);
-  const size_t room = kMaxSmem - 1024 - kMiscBytes - (kTileABytes - p.arows * 128);
+  const int fixed = swiglu ? fixed_bytes<KIND, true>() : fixed_bytes<KIND, false>();
+  const size_t room = kMaxSmem - 1024 - fixed - (kTileABytes - p.arows * 128);
   const int per_cta = pair ? p.KB : (p.KB + p.P - 1) / p.P;
   const int most = static_cast<int>(room / sb);
   p.stages = most < kMaxStages ? most : kMaxStages;

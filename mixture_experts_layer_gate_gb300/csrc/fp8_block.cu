@@ -67,6 +67,7 @@ cudaError_t launch_fp8_block(const Fp8GemmArgs& g, cudaStream_t s) {
   p.accumulate = g.accumulate;
   const int64_t osz = g.out_dtype == 2 ? 4 : 2;
   p.vec = reinterpret_cast<uintptr_t>(g.out) % 16 == 0 && g.out_stride * osz % 16 == 0;
+  p.vec_scale = reinterpret_cast<uintptr_t>(g.a_scale) % 16 == 0 && g.a_scale_stride % 4 == 0 && c.P == 1;
   return dense::plan_and_launch<dense::kE4M3>(p, c.bn, c.pair, swiglu, g.a, g.a_stride, g.w, g.w_stride,
                                               swiglu ? 2 * g.N : g.N, g.K, di.sms, s);
 }
