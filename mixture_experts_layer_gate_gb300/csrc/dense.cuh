@@ -252,6 +252,88 @@ __device__ __forceinline__ void store4(const Params& p, int64_t row, int col, fl
   }
 }
 
+// ---- Single-thread instructions of a whole warp.  The TMA and MMA roles run
+// their loops with all 32 lanes and predicate the instructions themselves on one
+// lane: in code that only one lane enters, every descriptor has to be moved from
+// a vector register to a uniform one, and a k-block's four MMAs and two commits
+// took 450 cycles to issue, with their waits twice as long as the tensor pipe.
+
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+  return p;
+}
+
+// The four MMAs of a k-block (32 bytes of K each); descriptors as (low, high)
+// words, the low one advancing by 32 bytes >> 4.
+template <int KIND, bool PAIR>
+__device__ __forceinline__ void mma_kblock(uint32_t leader, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
+                                           uint32_t idesc, uint32_t accumulate_first) {
+#define MOE_DENSE_MMA4(GROUP, TYPE)                                                                                  \
+  asm volatile(                                                                                                      \
+      "{\n\t.reg .pred l, p, q;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t"                                           \
+      "setp.ne.b32 l, %0, 0;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 q, %4, %4;\n\t"                                 \
+      "mov.b64 a, {%2, %4};\n\tmov.b64 b, {%3, %4};\n\t"                                                             \
+      "@l tcgen05.mma.cta_group::" GROUP ".kind::" TYPE " [%1], a, b, %5, p;\n\t"                                    \
+      "add.u32 x, %2, 2;\n\tadd.u32 y, %3, 2;\n\tmov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t"                     \
+      "@l tcgen05.mma.cta_group::" GROUP ".kind::" TYPE " [%1], a, b, %5, q;\n\t"                                    \
+      "add.u32 x, %2, 4;\n\tadd.u32 y, %3, 4;\n\tmov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t"                     \
+      "@l tcgen05.mma.cta_group::" GROUP ".kind::" TYPE " [%1], a, b, %5, q;\n\t"                                    \
+      "add.u32 x, %2, 6;\n\tadd.u32 y, %3, 6;\n\tmov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t"                     \
+      "@l tcgen05.mma.cta_group::" GROUP ".kind::" TYPE " [%1], a, b, %5, q;\n\t}" ::"r"(leader),                    \
+      "r"(d), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate_first)                                       \
+      : "memory")
+  if (KIND == 0) {
+    if (PAIR) MOE_DENSE_MMA4("2", "f8f6f4");
+    else MOE_DENSE_MMA4("1", "f8f6f4");
+  } else {
+    if (PAIR) MOE_DENSE_MMA4("2", "f16");
+    else MOE_DENSE_MMA4("1", "f16");
+  }
+#undef MOE_DENSE_MMA4
+}
+
+// Arrives on the barrier (PAIR: of both CTAs) when the MMAs issued so far complete.
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint32_t leader, uint32_t bar) {
+  if (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred l;\n\t.reg .b16 m;\n\tsetp.ne.b32 l, %0, 0;\n\tmov.b16 m, 3;\n\t"
+        "@l tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%1], m;\n\t}" ::"r"(
+            leader),
+        "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %0, 0;\n\t"
+        "@l tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(leader),
+        "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void expect_tx(uint32_t leader, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %0, 0;\n\t"
+      "@l mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%1], %2;\n\t}" ::"r"(leader),
+      "r"(bar), "r"(bytes)
+      : "memory");
+}
+
+// One box into this CTA's shared memory, counted on `bar` (PAIR: a barrier of the pair's leader).
+template <bool PAIR>
+__device__ __forceinline__ void load_box(uint32_t leader, uint32_t dst, const void* map, uint32_t bar, int c0, int c1) {
+#define MOE_DENSE_LOAD(GROUP)                                                                                   \
+  asm volatile(                                                                                                 \
+      "{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %0, 0;\n\t"                                                         \
+      "@l cp.async.bulk.tensor.2d" GROUP ".shared::cluster.global.tile.mbarrier::complete_tx::bytes"            \
+      " [%1], [%2, {%4, %5}], [%3];\n\t}" ::"r"(leader),                                                        \
+      "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)                                \
+      : "memory")
+  if (PAIR) MOE_DENSE_LOAD(".cta_group::2");
+  else MOE_DENSE_LOAD("");
+#undef MOE_DENSE_LOAD
+}
+
 template <int KIND, bool SWIGLU, bool PAIR, int BN>
 __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constant__ Maps maps, const Params p) {
   static_assert(!SWIGLU || BN == 256, "gate and up halves of 128 columns");
@@ -333,15 +415,16 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
   if (warp < kFirstJoin) {
     if (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLeanRegs));
     if (warp == 0) {
-    // ------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      const uint64_t pol = l2_policy_evict_normal();
+      // ------------------------------------------------------ TMA producer
+      const uint32_t leader = elect_one();
       int st = 0, issued = 0;
       uint32_t ph = 0;
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step) {
         const int m0 = (t % p.mt) * kTileM + (PAIR ? 128 * static_cast<int>(rank) : 0);
         const int n0 = (t / p.mt) * (SWIGLU ? 128 : BN);
+        // the weight rows: PAIR loads one half here, the peer the other
+        const int second = SWIGLU ? n0 + p.N : n0 + 128;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait(EMPTY(st), ph ^ 1u, abort_flag, p.err, 0x600u)) {
             ok = false;
@@ -350,17 +433,14 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
           const uint32_t dst = ring + static_cast<uint32_t>(st) * sbytes;
           if (PAIR) {
             const uint32_t bar = map_to_rank(FULL(st), 0);
-            if (rank == 0) mbar_expect_tx(FULL(st), 2u * sbytes);
-            tma_load_2d_pair(dst, &maps.a, bar, kb * kElems, m0, pol);
-            const int row = SWIGLU ? n0 + static_cast<int>(rank) * p.N : n0 + 128 * static_cast<int>(rank);
-            tma_load_2d_pair(dst + abytes, &maps.w, bar, kb * kElems, row, pol);
+            if (rank == 0) expect_tx(leader, FULL(st), 2u * sbytes);
+            load_box<true>(leader, dst, &maps.a, bar, kb * kElems, m0);
+            load_box<true>(leader, dst + abytes, &maps.w, bar, kb * kElems, rank == 0 ? n0 : second);
           } else {
-            mbar_expect_tx(FULL(st), sbytes);
-            tma_load_2d_hint(dst, &maps.a, FULL(st), kb * kElems, m0, pol);
-            tma_load_2d_hint(dst + abytes, &maps.w, FULL(st), kb * kElems, n0, pol);
-            if (BN == 256)
-              tma_load_2d_hint(dst + abytes + 128u * 128u, &maps.w, FULL(st), kb * kElems,
-                               SWIGLU ? n0 + p.N : n0 + 128, pol);
+            expect_tx(leader, FULL(st), sbytes);
+            load_box<false>(leader, dst, &maps.a, FULL(st), kb * kElems, m0);
+            load_box<false>(leader, dst + abytes, &maps.w, FULL(st), kb * kElems, n0);
+            if (BN == 256) load_box<false>(leader, dst + abytes + 128u * 128u, &maps.w, FULL(st), kb * kElems, second);
           }
           ++issued;
           if (++st == ns) {
@@ -369,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
           }
         }
       }
-      if (!ok && rank == (PAIR ? 0u : rank)) {
+      if (!ok && (!PAIR || rank == 0)) {
         // after an abort the loads in flight land before the CTA (or its pair,
         // whose leader counts both CTAs' bytes) may leave
         for (int i = min(issued, ns); i > 0; --i) {
@@ -378,44 +458,30 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
           wait(FULL(st), ph, nullptr, p.err, 0x601u);
         }
       }
-    }
-  } else if (warp == 1) {
-    // --------------------------------------------- MMA issuer (leader CTA)
-    if (lane == 0 && (!PAIR || rank == 0)) {
+    } else if (warp == 1 && (!PAIR || rank == 0)) {
+      // --------------------------------------------- MMA issuer (leader CTA)
+      const uint32_t leader = elect_one();
       const uint32_t idesc = make_idesc(kTileM, BN, KIND == kE4M3 ? 0u : static_cast<uint32_t>(p.fmt));
+      const uint64_t desc0 = sw128_kmajor_desc(ring);
+      const uint32_t desc_lo = static_cast<uint32_t>(desc0), desc_hi = static_cast<uint32_t>(desc0 >> 32);
       int st = 0;
       uint32_t ph = 0, buf = 0, dph = 0;
       bool ok = true, any = false;
       for (int t = first; t < tiles && ok; t += step) {
         for (int kb = kb0; kb < kb1 && ok;) {
-          if (!wait(dempty + 8u * buf, dph ^ 1u, abort_flag, p.err, 0x610u)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
           const uint32_t d = tmem + buf * static_cast<uint32_t>(BN);
           const int end = min(kb + p.group, kb1);
-          for (bool fresh = true; kb < end; ++kb, fresh = false) {
-            if (!wait(FULL(st), ph, abort_flag, p.err, 0x620u)) {
+          for (uint32_t accum = 0; kb < end; ++kb, accum = 1) {
+            // the operands first: they are there by the time the accumulator is
+            if (!wait(FULL(st), ph, abort_flag, p.err, 0x620u) ||
+                (accum == 0 && !wait(dempty + 8u * buf, dph ^ 1u, abort_flag, p.err, 0x610u))) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t src = ring + static_cast<uint32_t>(st) * sbytes;
-            const uint64_t ad = sw128_kmajor_desc(src), wd = sw128_kmajor_desc(src + abytes);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint32_t accum = (fresh && kk == 0) ? 0u : 1u;
-              if (KIND == kE4M3) {
-                if (PAIR) mma_f8_pair(d, ad + 2u * kk, wd + 2u * kk, idesc, accum);
-                else mma_f8(d, ad + 2u * kk, wd + 2u * kk, idesc, accum);
-              } else {
-                if (PAIR) mma_f16_pair(d, ad + 2u * kk, wd + 2u * kk, idesc, accum);
-                else mma_f16(d, ad + 2u * kk, wd + 2u * kk, idesc, accum);
-              }
-            }
-            if (PAIR) mma_commit_pair(EMPTY(st), 0x3);
-            else mma_commit(EMPTY(st));
+            const uint32_t a_lo = desc_lo + ((static_cast<uint32_t>(st) * sbytes) >> 4);
+            mma_kblock<KIND, PAIR>(leader, d, a_lo, a_lo + (abytes >> 4), desc_hi, idesc, accum);
+            commit<PAIR>(leader, EMPTY(st));
             any = true;
             if (++st == ns) {
               st = 0;
@@ -423,18 +489,18 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
             }
           }
           if (!ok) break;
-          if (PAIR) mma_commit_pair(dfull + 8u * buf, 0x3);
-          else mma_commit(dfull + 8u * buf);
+          commit<PAIR>(leader, dfull + 8u * buf);
           buf ^= 1u;
           if (buf == 0u) dph ^= 1u;
         }
       }
       if (!ok && any) {  // MMAs in flight end before tensor memory is freed
-        if (PAIR) mma_commit_pair(drain, 0x1);
-        else mma_commit(drain);
+        if (leader != 0u) {
+          if (PAIR) mma_commit_pair(drain, 0x1);
+          else mma_commit(drain);
+        }
         wait(drain, 0u, nullptr, p.err, 0x630u);
       }
-    }
     }
     if (KIND == kE4M3 && warp >= 2) {
       // ------------------------------------------------------- scale warps
@@ -540,21 +606,28 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
           }
           const uint32_t src = tmem + lane_base + buf * static_cast<uint32_t>(BN);
           if constexpr (CH == 32) {
-            // a load of 32 columns runs while the 32 before are added
+            // two loads of 32 columns at a time
             uint32_t r[2][32];
+            auto add = [&](int c) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                fma2(acc[16 * c + j], r[c & 1][2 * j], r[c & 1][2 * j + 1], (SWIGLU && c >= 2) ? g1 : g0);
+            };
             if (live) {
               tmem_ld32(src + column_of(0), r[0]);
+              if (NCH > 1) tmem_ld32(src + column_of(1), r[1]);
 #pragma unroll
-              for (int c = 0; c < NCH; ++c) {
-                tmem_ld32_wait(r[c & 1]);
-                if (c + 1 < NCH) tmem_ld32(src + column_of(c + 1), r[(c + 1) & 1]);
-                if (c + 1 == NCH) {
+              for (int c = 0; c < NCH; c += 2) {
+                tmem_ld32_wait(r[0]);
+                if (c + 1 < NCH) tmem_ld32_wait(r[1]);
+                if (c + 2 >= NCH) {
                   tc_fence_before();
                   if (lane == 0) mbar_arrive_cluster(dempty_to + 8u * buf);
                 }
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  fma2(acc[16 * c + j], r[c & 1][2 * j], r[c & 1][2 * j + 1], (SWIGLU && c >= 2) ? g1 : g0);
+                add(c);
+                if (c + 2 < NCH) tmem_ld32(src + column_of(c + 2), r[0]);
+                if (c + 1 < NCH) add(c + 1);
+                if (c + 3 < NCH) tmem_ld32(src + column_of(c + 3), r[1]);
               }
             } else {
               tc_fence_before();
@@ -636,22 +709,44 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
         // wrote 8 bytes of 32 rows at a time and took twice the product's time
         // at M = 4096, N = 7168, K = 2048)
         const uint32_t mine = stage0 + static_cast<uint32_t>(4 * half + quarter) * kStageBytes;
+        const int to0 = m0 + 32 * quarter + (lane >> 2), col0 = n0 + W * half + 4 * (lane & 3);
+        auto store_all = [&](auto store) {
 #pragma unroll
-        for (int c = 0; c < W / 16; ++c) {
-          __syncwarp();
+          for (int c = 0; c < W / 16; ++c) {
+            __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 u = unpair(acc[8 * c + 2 * j]), v = unpair(acc[8 * c + 2 * j + 1]);
-            sts_f4(mine + static_cast<uint32_t>(lane * kStageRow + 16 * j), make_float4(u.x, u.y, v.x, v.y));
+            for (int j = 0; j < 4; ++j) {
+              const float2 u = unpair(acc[8 * c + 2 * j]), v = unpair(acc[8 * c + 2 * j + 1]);
+              sts_f4(mine + static_cast<uint32_t>(lane * kStageRow + 16 * j), make_float4(u.x, u.y, v.x, v.y));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 v = lds_f4(mine + static_cast<uint32_t>((8 * i + (lane >> 2)) * kStageRow + 16 * (lane & 3)));
+              if (to0 + 8 * i < p.M) store(i, c, v);
+            }
           }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = 8 * i + (lane >> 2);
-            const float4 v = lds_f4(mine + static_cast<uint32_t>(r * kStageRow + 16 * (lane & 3)));
-            const int to = m0 + 32 * quarter + r;
-            if (to < p.M) store4(p, to, n0 + W * half + 16 * c + 4 * (lane & 3), v);
+        };
+        if (p.vec && !p.accumulate && n0 + BN <= p.N) {  // a whole tile's columns: one aligned store each
+          const int64_t at = static_cast<int64_t>(to0) * p.out_stride + col0, eight = 8 * p.out_stride;
+          if (p.out_dtype == 0) {
+            uint16_t* o = static_cast<uint16_t*>(p.out) + at;
+            store_all([&](int i, int c, float4 v) {
+              *reinterpret_cast<uint2*>(o + i * eight + 16 * c) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+            });
+          } else if (p.out_dtype == 1) {
+            uint16_t* o = static_cast<uint16_t*>(p.out) + at;
+            store_all([&](int i, int c, float4 v) {
+              __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
+              *reinterpret_cast<uint2*>(o + i * eight + 16 * c) =
+                  make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+            });
+          } else {
+            float* o = static_cast<float*>(p.out) + at;
+            store_all([&](int i, int c, float4 v) { *reinterpret_cast<float4*>(o + i * eight + 16 * c) = v; });
           }
+        } else {
+          store_all([&](int i, int c, float4 v) { store4(p, to0 + 8 * i, col0 + 16 * c, v); });
         }
       }
     }
