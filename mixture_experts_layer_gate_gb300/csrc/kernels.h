@@ -196,6 +196,7 @@ struct NormArgs {
   int T, H;
   int quant;              // moe_quant_t
   int vec;                // rows are 16-byte aligned and H % 8 == 0
+  int sms;
   float eps;
 };
 // dtype: moe_dtype_t; weight_f32: the weight is float (else dtype)

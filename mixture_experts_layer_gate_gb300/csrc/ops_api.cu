@@ -82,7 +82,7 @@ moe_status_t moe_add_rms_norm(const moe_norm_t* n, const void* x, int64_t x_stri
   if (n->weight_dtype != n->dtype && n->weight_dtype != MOE_T_F32) return MOE_ERR_INVALID_ARG;
   if (n->quant < MOE_QUANT_NONE || n->quant > MOE_QUANT_TOKEN) return MOE_ERR_INVALID_ARG;
   if (!(n->eps >= 0.f) || !std::isfinite(n->eps)) return MOE_ERR_INVALID_ARG;
-  if (n->H > 16384) return MOE_ERR_UNSUPPORTED;
+  if (n->H > 16384 || n->T > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   if (n->T == 0) return MOE_OK;
   const size_t b = size_of(n->dtype), wb = size_of(n->weight_dtype);
   if (!rows_ok(x, x_stride, n->H, b) || weight == nullptr || !aligned(weight, wb)) return MOE_ERR_INVALID_ARG;
@@ -111,6 +111,9 @@ moe_status_t moe_add_rms_norm(const moe_norm_t* n, const void* x, int64_t x_stri
   a.H = n->H;
   a.quant = n->quant;
   a.eps = n->eps;
+  DeviceInfo di;
+  if (device_info(&di) != cudaSuccess) return MOE_ERR_CUDA;
+  a.sms = di.sms;
   auto wide = [&](const void* p, int64_t stride) {
     return p == nullptr || (aligned(p, 16) && stride * static_cast<int64_t>(b) % 16 == 0);
   };
