@@ -850,6 +850,47 @@ cudaError_t launch(const Maps& maps, const Params& p, int grid, cudaStream_t s) 
                             static_cast<unsigned>(PAIR ? 2 : p.P), maps, p);
 }
 
+// Tile width, CTA pairs and the split of K.
+struct Choice {
+  int bn;
+  bool pair;
+  int P;
+};
+
+// The candidate with the least estimated time in cycles: rounds of the SMs times
+// (k-blocks of a CTA times a k-block's time, and the tile's end).  The k-block
+// times are measured ones of the whole loop (16-bit: H = 7168, 256 experts, 1 to
+// 4096 tokens; 8-bit: 1 to 4096 rows of the DeepSeek-V3 shared expert).  Eight
+// CTAs a cluster only for eight tiles at most: more such clusters do not all fit
+// on the SMs at once (one row, N = 2048, K = 7168 with SwiGLU: 24 us by eights,
+// 18 us by fours).
+inline Choice choose(int M, int N, int KB, bool swiglu, bool e4m3, int sms) {
+  Choice best{256, false, 1};
+  double best_time = 1e30;
+  const double arows = std::min(128, (M + 7) / 8 * 8);
+  for (int w = 0; w < 5; ++w) {
+    constexpr int width[5] = {32, 64, 128, 256, 256};
+    constexpr double half_block[5] = {250, 340, 560, 1150, 1150}, e4m3_block[5] = {600, 690, 800, 1250, 950};
+    const int bn = width[w];
+    const bool pair = w == 4;
+    if ((swiglu && bn != 256) || (pair && (M <= 128 || !e4m3))) continue;
+    const int tm = pair ? 256 : 128, tn = swiglu ? 128 : bn;
+    const long long tiles = static_cast<long long>((M + tm - 1) / tm) * ((N + tn - 1) / tn);
+    for (int P = 1; P <= 8 && P <= KB; P *= 2) {
+      if (P > 1 && (pair || tiles * P > sms || (P == 8 && tiles > 8))) break;
+      const long long slots = pair ? sms / 2 : sms / P;
+      const double rounds = static_cast<double>((tiles + slots - 1) / slots);
+      const double end = (P > 1 ? 2500.0 : 300.0) + arows * bn / 7.0;
+      const double time = rounds * ((KB + P - 1) / P * (e4m3 ? e4m3_block[w] : half_block[w]) + end);
+      if (time < best_time) {
+        best_time = time;
+        best = {bn, pair, P};
+      }
+    }
+  }
+  return best;
+}
+
 // Descriptors, tile counts and ring depth, then the launch.  p: everything but
 // mt, nt, arows and stages.  a [M, K] and w [wrows_total, K] of 1-byte (kE4M3)
 // or 2-byte elements, strides in elements.

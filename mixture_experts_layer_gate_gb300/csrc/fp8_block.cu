@@ -6,49 +6,13 @@
 #include "dense.cuh"
 
 namespace moe {
-namespace {
-
-struct Choice {
-  int bn, pair, P;
-};
-
-// Tiles, pairs and the split of K.  Large batches: CTA pairs on 256 x 256 tiles.
-// Else the width and split that spread the tile's weights over the SMs.
-Choice choose(const Fp8GemmArgs& g, bool swiglu, int KB, int sms) {
-  const int cols = g.N;
-  const int bn_full = swiglu ? 128 : 256;
-  const int mt = (g.M + 127) / 128;
-  const long long pair_tiles = static_cast<long long>((g.M + 255) / 256) * ((cols + bn_full - 1) / bn_full);
-  if (g.M > 128 && pair_tiles * 2 >= sms * 3 / 4) return {256, 1, 1};
-  Choice best{256, 0, 1};
-  double best_time = 1e30;
-  for (int bn : {32, 64, 128, 256}) {
-    if (swiglu && bn != 256) continue;
-    const long long tiles = static_cast<long long>(mt) * ((cols + (swiglu ? 128 : bn) - 1) / (swiglu ? 128 : bn));
-    for (int P : {1, 2, 4, 8}) {
-      if (P > KB) continue;
-      const long long waves = (tiles * P + sms - 1) / sms;
-      const double load = 128.0 * (bn + std::min(128, g.M)) / 48.0;  // cycles to load a k-block
-      const double time = static_cast<double>(waves) * (((KB + P - 1) / P) * std::max(load, 2.0 * bn) + 1500.0) +
-                          (P > 1 ? 1200.0 + 4.0 * P * std::min(128, g.M) / P : 0.0);
-      if (time < best_time * 0.999) {
-        best_time = time;
-        best = {bn, 0, P};
-      }
-    }
-  }
-  return best;
-}
-
-}  // namespace
-
 cudaError_t launch_fp8_block(const Fp8GemmArgs& g, cudaStream_t s) {
   const bool swiglu = g.codes != nullptr;
   DeviceInfo di;
   cudaError_t err = device_info(&di);
   if (err != cudaSuccess) return err;
   const int KB = (g.K + 127) / 128;
-  const Choice c = choose(g, swiglu, KB, di.sms);
+  const dense::Choice c = dense::choose(g.M, g.N, KB, swiglu, true, di.sms);
   dense::Params p = {};
   p.a_scale = g.a_scale;
   p.w_scale = g.w_scale;
