@@ -8,6 +8,7 @@
 namespace moe {
 cudaError_t launch_fp8_block(const Fp8GemmArgs& g, cudaStream_t s) {
   const bool swiglu = g.codes != nullptr;
+  if (fp8_few_fits(g)) return launch_fp8_few(g, s);
   DeviceInfo di;
   cudaError_t err = device_info(&di);
   if (err != cudaSuccess) return err;

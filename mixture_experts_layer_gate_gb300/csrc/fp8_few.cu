@@ -1,0 +1,241 @@
+// The block-scaled 8-bit product for at most 8 rows of activations (decode):
+// bound by the rate at which the weights stream in, so no tile of 128 rows, but
+// the rings and mma.sync of the few-token layer (stream.cuh): a warp multiplies
+// 16 weight rows with all activation rows (the 8 columns) by m16n8k16 on e4m3
+// turned into f16 (exact), and joins each k-step's product, times its block's
+// scales, to its sums in registers.
+//
+// SwiGLU: a CTA takes 16 gate rows and the 16 up rows that go with them, its 8
+// warps each a part of K; the 8 CTAs of a cluster make up a quantisation block
+// of 128 columns and exchange each row's largest value through distributed
+// shared memory.  Else a CTA goes through blocks of 16 rows.  At most 110 KB of
+// shared memory, so that two CTAs live on an SM and every cluster finds its
+// place (clusters of eight one-per-SM CTAs did not all fit at once).
+//
+// One row, K = 7168, N = 2048 (29 MB): see launch_fp8_few.
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "stream.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kFewWarps = 8;
+constexpr int kFewThreads = 32 * kFewWarps;
+constexpr int kStage = 2048 + 32;  // 4 loads of 16 bytes a lane, and two weight scales
+constexpr int kFewSmem = 110 * 1024;
+constexpr int kMaxFewDepth = 8;
+constexpr int kRed = kFewWarps * 32 * 8 * 4;  // the warps' sums
+
+__host__ __device__ constexpr int code_stride(int K) { return (K + 127) / 128 * 128 + 64; }
+
+__device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16u : 0u) : "memory");
+}
+__device__ __forceinline__ float max_nan(float a, float b) { return (a > b || a != a) ? a : b; }
+
+// SWIGLU: a step is 64 k of 16 gate and 16 up rows; else 128 k of 16 rows.
+template <bool SWIGLU>
+__global__ void __launch_bounds__(kFewThreads, 2) fp8_few_kernel(Fp8GemmArgs p, int depth) {
+  extern __shared__ __align__(128) uint8_t fp8_few_smem[];
+  constexpr int STEP = SWIGLU ? 64 : 128, SETS = SWIGLU ? 2 : 1;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  const int KB = (p.K + 127) / 128, stride = code_stride(p.K);
+  float* red = reinterpret_cast<float*>(fp8_few_smem);                   // [warp][set, row][8]
+  float* as = red + kRed / 4;                                            // [block][8] activation scales
+  uint8_t* codes = reinterpret_cast<uint8_t*>(as + KB * 8);              // [row][stride]
+  const uint32_t rings = smem_u32(codes) + static_cast<uint32_t>((p.M * stride + 127) / 128 * 128);
+  const uint32_t ring = rings + static_cast<uint32_t>(warp * depth * kStage);
+  const uint32_t iend = ring + static_cast<uint32_t>(depth * kStage);
+  const int units = SWIGLU ? p.N / 16 : (p.N + 15) / 16;
+  const int nsteps = (p.K + STEP - 1) / STEP;
+  const int s0 = nsteps * warp / kFewWarps, s1 = nsteps * (warp + 1) / kFewWarps;
+  pdl_wait();
+  pdl_trigger();
+
+  int iu = blockIdx.x, is = s0;
+  uint32_t idst = ring;
+  auto issue = [&] {
+    if (iu < units && s0 < s1) {
+      const int64_t n0 = static_cast<int64_t>(iu) * 16;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        // SWIGLU: gate rows g and g + 8, up rows g and g + 8; else rows g and g +
+        // 8 of the step's first 64 k and of its second
+        const int64_t n = n0 + g + 8 * (q & 1);
+        const int64_t row = n + (SWIGLU && q >= 2 ? p.N : 0);
+        const int k = is * STEP + t4 * 16 + (SWIGLU ? 0 : 64 * (q >> 1));
+        const bool there = k < p.K && n < p.N;
+        cp_async16_if(idst + static_cast<uint32_t>(q * 512 + lane * 16), there ? p.w + row * p.w_stride + k : p.w, there);
+      }
+      if (lane < SETS)
+        cp_async4(idst + 2048 + lane * 4, p.w_scale + ((n0 + static_cast<int64_t>(lane) * p.N) / 128) * KB + is * STEP / 128);
+      if (++is == s1) {
+        is = s0;
+        iu += gridDim.x;
+      }
+    }
+    cp_async_commit();
+    idst += kStage;
+    if (idst >= iend) idst = ring;
+  };
+  for (int i = 0; i < depth - 1; ++i) issue();  // (before the activations: they take as long to arrive)
+
+  for (int i = tid; i < p.M * (stride / 16); i += kFewThreads) {
+    const int m = i / (stride / 16), k = (i - m * (stride / 16)) * 16;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (k < p.K) v = *reinterpret_cast<const uint4*>(p.a + m * p.a_stride + k);
+    *reinterpret_cast<uint4*>(codes + m * stride + k) = v;
+  }
+  for (int i = tid; i < KB * 8; i += kFewThreads)
+    as[i] = p.a_scale[static_cast<int64_t>(min(i & 7, p.M - 1)) * p.a_scale_stride + (i >> 3)];
+  __syncthreads();
+
+  uint32_t src = ring;
+  // (columns past the last row repeat it; nobody reads their sums)
+  const uint32_t mine = smem_u32(codes) + static_cast<uint32_t>(min(g, p.M - 1) * stride + t4 * 16);
+  for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    float acc[SETS][4] = {};
+    for (int s = s0; s < s1; ++s) {
+      __syncwarp();
+      issue();
+      cp_async_wait(depth - 1);
+      __syncwarp();
+      float part[2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {  // SWIGLU: gate and up of the same k; else two runs of k
+        const uint4 wa = lds128(src + static_cast<uint32_t>(2 * u * 512 + lane * 16));
+        const uint4 wb = lds128(src + static_cast<uint32_t>((2 * u + 1) * 512 + lane * 16));
+        const uint4 b = lds128(mine + static_cast<uint32_t>(s * STEP + (SWIGLU ? 0 : 64 * u)));
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const uint32_t a0 = e4m3x2_f16x2(word(wa, m) & 0xFFFFu), a2 = e4m3x2_f16x2(word(wa, m) >> 16);
+          const uint32_t a1 = e4m3x2_f16x2(word(wb, m) & 0xFFFFu), a3 = e4m3x2_f16x2(word(wb, m) >> 16);
+          const uint32_t b0 = e4m3x2_f16x2(word(b, m) & 0xFFFFu), b1 = e4m3x2_f16x2(word(b, m) >> 16);
+          if (m == 0) mma16816_first<true>(part[u], a0, a1, a2, a3, b0, b1);
+          else mma16816<true>(part[u], a0, a1, a2, a3, b0, b1);
+        }
+      }
+      const float2 sa = *reinterpret_cast<const float2*>(as + (s * STEP / 128) * 8 + 2 * t4);
+      const uint2 sw = lds64(src + 2048);
+      const float w0 = __uint_as_float(sw.x), w1 = SWIGLU ? __uint_as_float(sw.y) : w0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float f = j & 1 ? sa.y : sa.x;
+        if (SWIGLU) {
+          acc[0][j] = fmaf(part[0][j], f * w0, acc[0][j]);
+          acc[SETS - 1][j] = fmaf(part[1][j], f * w1, acc[SETS - 1][j]);
+        } else {
+          acc[0][j] = fmaf(part[0][j] + part[1][j], f * w0, acc[0][j]);
+        }
+      }
+      src += kStage;
+      if (src >= iend) src = ring;
+    }
+#pragma unroll
+    for (int y = 0; y < SETS; ++y)
+#pragma unroll
+      for (int j = 0; j < 4; j += 2)
+        *reinterpret_cast<float2*>(red + ((warp * SETS + y) * 16 + g + 4 * j) * 8 + 2 * t4) =
+            make_float2(acc[y][j], acc[y][j + 1]);
+    __syncthreads();
+    if (!SWIGLU) {
+      if (tid < 128) {
+        const int row = tid & 15, t = tid >> 4;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) v += red[(w * 16 + row) * 8 + t];
+        const int n = unit * 16 + row;
+        if (t < p.M && n < p.N) {
+          const int64_t at = t * p.out_stride + n;
+          if (p.out_dtype == 0) {
+            __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at;
+            *o = __float2bfloat16_rn(p.accumulate ? v + __bfloat162float(*o) : v);
+          } else if (p.out_dtype == 1) {
+            __half* o = static_cast<__half*>(p.out) + at;
+            *o = __float2half_rn(p.accumulate ? v + __half2float(*o) : v);
+          } else {
+            float* o = static_cast<float*>(p.out) + at;
+            *o = p.accumulate ? v + *o : v;
+          }
+        }
+      }
+      __syncthreads();
+      continue;
+    }
+    // SWIGLU: thread (row of the 16, activation row); one unit a CTA
+    const int i = tid & 15, t = tid >> 4 & 7;
+    float v = 0.f;
+    if (tid < 128) {
+      float gate = 0.f, up = 0.f;
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) {
+        gate += red[((w * SETS) * 16 + i) * 8 + t];
+        up += red[((w * SETS + SETS - 1) * 16 + i) * 8 + t];
+      }
+      v = __fdividef(gate, 1.0f + __expf(-gate)) * up;
+      float m = fabsf(v);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (i == 0) as[t] = m;  // (the scales have been read)
+    }
+    cluster_sync_all();
+    float amax = 0.f;
+    if (tid < 128) {
+#pragma unroll
+      for (uint32_t r = 0; r < 8; ++r) {
+        float q;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q) : "r"(map_to_rank(smem_u32(as + t), r)) : "memory");
+        amax = max_nan(amax, q);
+      }
+      const float scale = amax == 0.f ? 1.0f : __fdiv_rn(amax, 448.0f);
+      if (t < p.M) {
+        p.codes[static_cast<int64_t>(t) * p.N + unit * 16 + i] =
+            static_cast<uint8_t>(f32x2_to_e4m3x2(__fdiv_rn(v, scale), 0.f));
+        if (i == 0 && unit % 8 == 0) p.scales[static_cast<int64_t>(t) * (p.N / 128) + unit / 8] = scale;
+      }
+    }
+    cluster_sync_all();  // no CTA leaves while a peer reads its maxima
+  }
+}
+
+// smem before the rings
+int fixed_bytes(const Fp8GemmArgs& p) {
+  return kRed + (p.K + 127) / 128 * 32 + (p.M * code_stride(p.K) + 127) / 128 * 128;
+}
+int depth_of(const Fp8GemmArgs& p) {
+  return std::min(kMaxFewDepth, (kFewSmem - fixed_bytes(p)) / (kFewWarps * kStage));
+}
+
+template <bool SWIGLU>
+cudaError_t launch(const Fp8GemmArgs& p, int grid, cudaStream_t s) {
+  static int configured[64] = {};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64 || configured[dev] == 0) {
+    err = cudaFuncSetAttribute(fp8_few_kernel<SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
+    if (err != cudaSuccess) return err;
+    if (dev >= 0 && dev < 64) configured[dev] = 1;
+  }
+  const int depth = depth_of(p);
+  const size_t smem = static_cast<size_t>(fixed_bytes(p)) + static_cast<size_t>(depth) * kFewWarps * kStage;
+  return launch_pdl_cluster(fp8_few_kernel<SWIGLU>, dim3(grid), dim3(kFewThreads), smem, s, SWIGLU ? 8u : 1u, p, depth);
+}
+
+}  // namespace
+
+// At most 8 rows whose codes leave room for a ring of two stages a warp.
+bool fp8_few_fits(const Fp8GemmArgs& p) { return p.M <= 8 && p.K <= 65536 && depth_of(p) >= 2; }
+
+cudaError_t launch_fp8_few(const Fp8GemmArgs& p, cudaStream_t s) {
+  DeviceInfo di;
+  cudaError_t err = device_info(&di);
+  if (err != cudaSuccess) return err;
+  if (p.codes != nullptr) return launch<true>(p, p.N / 16, s);
+  return launch<false>(p, std::min((p.N + 15) / 16, 2 * di.sms), s);
+}
+
+}  // namespace moe

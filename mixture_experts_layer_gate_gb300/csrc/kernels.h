@@ -228,6 +228,9 @@ struct Fp8GemmArgs {
   uint32_t* err;
 };
 cudaError_t launch_fp8_block(const Fp8GemmArgs& g, cudaStream_t s);
+// The same for a few rows; whether they fit its shared memory.
+bool fp8_few_fits(const Fp8GemmArgs& g);
+cudaError_t launch_fp8_few(const Fp8GemmArgs& g, cudaStream_t s);
 
 constexpr int kFewMaxTokens = 8;
 constexpr int kFewMaxCtas = 1024;
