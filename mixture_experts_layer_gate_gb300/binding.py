@@ -30,7 +30,7 @@ EXPORTED = ("moe_scratch_size", "moe_workspace_size", "moe_padded_capacity", "mo
 
 DTYPES = {"bf16": 0, "f16": 1, "f32": 2}
 QUANTS = {"none": 0, "block": 1, "token": 2}
-OP_WORKSPACE_BYTES = 256
+OP_WORKSPACE_BYTES = 256 + 512 + 4 * 8 * 16384
 FEW_MAX_TOKENS = 8
 
 
@@ -359,7 +359,7 @@ def fp8_gemm_problem(M, N, K, out_dtype="bf16", accumulate=False) -> Fp8GemmProb
 
 
 def alloc_op_workspace(device):
-    """Zeroed error header for router_logits and the gemm_fp8_block calls (any workspace serves as well)."""
+    """Zeroed workspace (error header and scratch) for router_logits and the gemm_fp8_block calls of one stream."""
     import torch
     return torch.zeros(OP_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
 

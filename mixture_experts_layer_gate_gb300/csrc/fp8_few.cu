@@ -5,12 +5,14 @@
 // turned into f16 (exact), and joins each k-step's product, times its block's
 // scales, to its sums in registers.
 //
-// SwiGLU: a CTA takes 16 gate rows and the 16 up rows that go with them, its 8
-// warps each a part of K; the 8 CTAs of a cluster make up a quantisation block
-// of 128 columns and exchange each row's largest value through distributed
-// shared memory.  Else a CTA goes through blocks of 16 rows.  At most 110 KB of
-// shared memory, so that two CTAs live on an SM and every cluster finds its
-// place (clusters of eight one-per-SM CTAs did not all fit at once).
+// SwiGLU: a CTA takes 16 gate rows and the 16 up rows that go with them, its
+// warps each a part of K.  A quantisation block of 128 columns is 8 CTAs' work:
+// each leaves its values (float) in scratch and counts itself, and the last of
+// the eight takes the block's maxima and writes scales and codes (the same
+// whichever is last).  A cluster of eight that exchanged the maxima through
+// distributed shared memory took 13.6 us for one row, K = 7168, N = 2048 (such
+// clusters start late and did not all fit with 16 warps a CTA).
+// Else a CTA goes through blocks of 16 rows.
 //
 // One row, K = 7168, N = 2048 (29 MB): see launch_fp8_few.
 #include <algorithm>
@@ -22,12 +24,15 @@
 namespace moe {
 namespace {
 
-constexpr int kFewWarps = 8;
-constexpr int kFewThreads = 32 * kFewWarps;
+// Warps of a CTA: one CTA an SM with SwiGLU, whose units are few, else two.
+template <bool SWIGLU>
+constexpr int kFewWarps = SWIGLU ? 16 : 8;
 constexpr int kStage = 2048 + 32;  // 4 loads of 16 bytes a lane, and two weight scales
-constexpr int kFewSmem = 110 * 1024;
 constexpr int kMaxFewDepth = 8;
-constexpr int kRed = kFewWarps * 32 * 8 * 4;  // the warps' sums
+template <bool SWIGLU>
+constexpr int kFewSmem = SWIGLU ? 200 * 1024 : 110 * 1024;
+template <bool SWIGLU>
+constexpr int kRed = kFewWarps<SWIGLU> * (SWIGLU ? 32 : 16) * 8 * 4;  // the warps' sums
 
 __host__ __device__ constexpr int code_stride(int K) { return (K + 127) / 128 * 128 + 64; }
 
@@ -38,20 +43,22 @@ __device__ __forceinline__ float max_nan(float a, float b) { return (a > b || a 
 
 // SWIGLU: a step is 64 k of 16 gate and 16 up rows; else 128 k of 16 rows.
 template <bool SWIGLU>
-__global__ void __launch_bounds__(kFewThreads, 2) fp8_few_kernel(Fp8GemmArgs p, int depth) {
+__global__ void __launch_bounds__(32 * kFewWarps<SWIGLU>, SWIGLU ? 1 : 2) fp8_few_kernel(Fp8GemmArgs p, int depth) {
   extern __shared__ __align__(128) uint8_t fp8_few_smem[];
+  __shared__ bool last;
+  constexpr int kWarps = kFewWarps<SWIGLU>, kThreads = 32 * kWarps;
   constexpr int STEP = SWIGLU ? 64 : 128, SETS = SWIGLU ? 2 : 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   const int KB = (p.K + 127) / 128, stride = code_stride(p.K);
   float* red = reinterpret_cast<float*>(fp8_few_smem);                   // [warp][set, row][8]
-  float* as = red + kRed / 4;                                            // [block][8] activation scales
+  float* as = red + kRed<SWIGLU> / 4;                                            // [block][8] activation scales
   uint8_t* codes = reinterpret_cast<uint8_t*>(as + KB * 8);              // [row][stride]
   const uint32_t rings = smem_u32(codes) + static_cast<uint32_t>((p.M * stride + 127) / 128 * 128);
   const uint32_t ring = rings + static_cast<uint32_t>(warp * depth * kStage);
   const uint32_t iend = ring + static_cast<uint32_t>(depth * kStage);
   const int units = SWIGLU ? p.N / 16 : (p.N + 15) / 16;
   const int nsteps = (p.K + STEP - 1) / STEP;
-  const int s0 = nsteps * warp / kFewWarps, s1 = nsteps * (warp + 1) / kFewWarps;
+  const int s0 = nsteps * warp / kWarps, s1 = nsteps * (warp + 1) / kWarps;
   pdl_wait();
   pdl_trigger();
 
@@ -83,13 +90,13 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp8_few_kernel(Fp8GemmArgs p, 
   };
   for (int i = 0; i < depth - 1; ++i) issue();  // (before the activations: they take as long to arrive)
 
-  for (int i = tid; i < p.M * (stride / 16); i += kFewThreads) {
+  for (int i = tid; i < p.M * (stride / 16); i += kThreads) {
     const int m = i / (stride / 16), k = (i - m * (stride / 16)) * 16;
     uint4 v = make_uint4(0, 0, 0, 0);
     if (k < p.K) v = *reinterpret_cast<const uint4*>(p.a + m * p.a_stride + k);
     *reinterpret_cast<uint4*>(codes + m * stride + k) = v;
   }
-  for (int i = tid; i < KB * 8; i += kFewThreads)
+  for (int i = tid; i < KB * 8; i += kThreads)
     as[i] = p.a_scale[static_cast<int64_t>(min(i & 7, p.M - 1)) * p.a_scale_stride + (i >> 3)];
   __syncthreads();
 
@@ -146,7 +153,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp8_few_kernel(Fp8GemmArgs p, 
         const int row = tid & 15, t = tid >> 4;
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) v += red[(w * 16 + row) * 8 + t];
+        for (int w = 0; w < kWarps; ++w) v += red[(w * 16 + row) * 8 + t];
         const int n = unit * 16 + row;
         if (t < p.M && n < p.N) {
           const int64_t at = t * p.out_stride + n;
@@ -165,48 +172,52 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp8_few_kernel(Fp8GemmArgs p, 
       __syncthreads();
       continue;
     }
-    // SWIGLU: thread (row of the 16, activation row); one unit a CTA
-    const int i = tid & 15, t = tid >> 4 & 7;
-    float v = 0.f;
+    // SWIGLU: thread (row of the 16, activation row)
     if (tid < 128) {
+      const int i = tid & 15, t = tid >> 4;
       float gate = 0.f, up = 0.f;
 #pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         gate += red[((w * SETS) * 16 + i) * 8 + t];
         up += red[((w * SETS + SETS - 1) * 16 + i) * 8 + t];
       }
-      v = __fdividef(gate, 1.0f + __expf(-gate)) * up;
-      float m = fabsf(v);
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (i == 0) as[t] = m;  // (the scales have been read)
+      if (t < p.M) __stcg(p.act + static_cast<int64_t>(t) * p.N + unit * 16 + i, __fdividef(gate, 1.0f + __expf(-gate)) * up);
+      __threadfence();
     }
-    cluster_sync_all();
-    float amax = 0.f;
-    if (tid < 128) {
+    __syncthreads();
+    if (tid == 0) {
+      last = atomicAdd(p.tickets + unit / 8, 1u) == 7u;
+      if (last) p.tickets[unit / 8] = 0;  // for the next call
+    }
+    __syncthreads();
+    if (last) {
+      // warp t: row t of the block, four columns a lane
+      __threadfence();
+      if (warp < p.M) {
+        const int64_t n0 = static_cast<int64_t>(unit / 8) * 128;
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(p.act + static_cast<int64_t>(warp) * p.N + n0) + lane);
+        float m = max_nan(max_nan(fabsf(v.x), fabsf(v.y)), max_nan(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
-      for (uint32_t r = 0; r < 8; ++r) {
-        float q;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q) : "r"(map_to_rank(smem_u32(as + t), r)) : "memory");
-        amax = max_nan(amax, q);
-      }
-      const float scale = amax == 0.f ? 1.0f : __fdiv_rn(amax, 448.0f);
-      if (t < p.M) {
-        p.codes[static_cast<int64_t>(t) * p.N + unit * 16 + i] =
-            static_cast<uint8_t>(f32x2_to_e4m3x2(__fdiv_rn(v, scale), 0.f));
-        if (i == 0 && unit % 8 == 0) p.scales[static_cast<int64_t>(t) * (p.N / 128) + unit / 8] = scale;
+        for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float scale = m == 0.f ? 1.0f : __fdiv_rn(m, 448.0f);
+        if (lane == 0) p.scales[static_cast<int64_t>(warp) * (p.N / 128) + unit / 8] = scale;
+        reinterpret_cast<uint32_t*>(p.codes + static_cast<int64_t>(warp) * p.N + n0)[lane] =
+            f32x2_to_e4m3x2(__fdiv_rn(v.x, scale), __fdiv_rn(v.y, scale)) |
+            (static_cast<uint32_t>(f32x2_to_e4m3x2(__fdiv_rn(v.z, scale), __fdiv_rn(v.w, scale))) << 16);
       }
     }
-    cluster_sync_all();  // no CTA leaves while a peer reads its maxima
+    __syncthreads();
   }
 }
 
 // smem before the rings
+template <bool SWIGLU>
 int fixed_bytes(const Fp8GemmArgs& p) {
-  return kRed + (p.K + 127) / 128 * 32 + (p.M * code_stride(p.K) + 127) / 128 * 128;
+  return kRed<SWIGLU> + (p.K + 127) / 128 * 32 + (p.M * code_stride(p.K) + 127) / 128 * 128;
 }
+template <bool SWIGLU>
 int depth_of(const Fp8GemmArgs& p) {
-  return std::min(kMaxFewDepth, (kFewSmem - fixed_bytes(p)) / (kFewWarps * kStage));
+  return std::min(kMaxFewDepth, (kFewSmem<SWIGLU> - fixed_bytes<SWIGLU>(p)) / (kFewWarps<SWIGLU> * kStage));
 }
 
 template <bool SWIGLU>
@@ -216,25 +227,31 @@ cudaError_t launch(const Fp8GemmArgs& p, int grid, cudaStream_t s) {
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev < 0 || dev >= 64 || configured[dev] == 0) {
-    err = cudaFuncSetAttribute(fp8_few_kernel<SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
+    err = cudaFuncSetAttribute(fp8_few_kernel<SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem<SWIGLU>);
     if (err != cudaSuccess) return err;
     if (dev >= 0 && dev < 64) configured[dev] = 1;
   }
-  const int depth = depth_of(p);
-  const size_t smem = static_cast<size_t>(fixed_bytes(p)) + static_cast<size_t>(depth) * kFewWarps * kStage;
-  return launch_pdl_cluster(fp8_few_kernel<SWIGLU>, dim3(grid), dim3(kFewThreads), smem, s, SWIGLU ? 8u : 1u, p, depth);
+  const int depth = depth_of<SWIGLU>(p);
+  const size_t smem = static_cast<size_t>(fixed_bytes<SWIGLU>(p)) + static_cast<size_t>(depth) * kFewWarps<SWIGLU> * kStage;
+  return launch_pdl(fp8_few_kernel<SWIGLU>, dim3(grid), dim3(32 * kFewWarps<SWIGLU>), smem, s, p, depth);
 }
 
 }  // namespace
 
-// At most 8 rows whose codes leave room for a ring of two stages a warp.
-bool fp8_few_fits(const Fp8GemmArgs& p) { return p.M <= 8 && p.K <= 65536 && depth_of(p) >= 2; }
+size_t fp8_few_scratch(int M, int N) { return (static_cast<size_t>(N) / 128 * 4 + 255) / 256 * 256 + static_cast<size_t>(M) * N * 4; }
+
+// At most 8 rows whose codes leave room for a ring of two stages a warp, and
+// with SwiGLU scratch for them.
+bool fp8_few_fits(const Fp8GemmArgs& p) {
+  if (p.M > 8 || p.K > 65536) return false;
+  return p.codes != nullptr ? p.tickets != nullptr && depth_of<true>(p) >= 2 : depth_of<false>(p) >= 2;
+}
 
 cudaError_t launch_fp8_few(const Fp8GemmArgs& p, cudaStream_t s) {
   DeviceInfo di;
   cudaError_t err = device_info(&di);
   if (err != cudaSuccess) return err;
-  if (p.codes != nullptr) return launch<true>(p, p.N / 16, s);
+  if (p.codes != nullptr) return launch<true>(p, std::min(p.N / 16, di.sms), s);
   return launch<false>(p, std::min((p.N + 15) / 16, 2 * di.sms), s);
 }
 

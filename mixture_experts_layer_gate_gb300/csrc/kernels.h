@@ -221,6 +221,8 @@ struct Fp8GemmArgs {
   void* out;              // [M, N] (SwiGLU: null)
   uint8_t* codes;         // SwiGLU: [M, N] e4m3, else null
   float* scales;          // SwiGLU: [M, N / 128]
+  uint32_t* tickets;      // SwiGLU of a few rows: [N / 128] counters, zero between calls (null: no scratch)
+  float* act;             // and [M, N] values
   int64_t a_stride, a_scale_stride, w_stride, out_stride;
   int M, N, K;
   int out_dtype;          // moe_dtype_t
@@ -230,6 +232,7 @@ struct Fp8GemmArgs {
 cudaError_t launch_fp8_block(const Fp8GemmArgs& g, cudaStream_t s);
 // The same for a few rows; whether they fit its shared memory.
 bool fp8_few_fits(const Fp8GemmArgs& g);
+size_t fp8_few_scratch(int M, int N);  // bytes of tickets and act
 cudaError_t launch_fp8_few(const Fp8GemmArgs& g, cudaStream_t s);
 
 constexpr int kFewMaxTokens = 8;
