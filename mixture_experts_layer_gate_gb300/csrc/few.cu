@@ -127,21 +127,36 @@ __device__ __forceinline__ void convert(const uint4& w, int m, const Offset& o, 
   }
 }
 
-// Scale and offset of one row's group, from the 4-byte words that hold them
-// (index: the group's place in its tensor, modulo 4).
+// Where a row's group lies in the 4-byte words that are copied for it: index =
+// (row * groups + group) modulo 4.  Rows of a tile are 16 r + g (+ 8, + I) with
+// every other term a multiple of 4 groups, so index = g * groups + group for all
+// the rows of a lane.
+struct Place {
+  uint32_t half;   // byte selector of the scale
+  uint32_t shift;  // of the zero point
+  __device__ __forceinline__ explicit Place(uint32_t index) {
+    half = (index & 1u) ? 0x4432u : 0x4410u;
+    shift = 8u * (index & 3u);
+  }
+};
+
+// Scale and offset of one row's group.
 template <int FMT>
-__device__ __forceinline__ void group_of(uint32_t sword, uint32_t zword, uint32_t index, bool zero, float& scale,
-                                         Offset& o) {
-  scale = __half2float(__ushort_as_half(static_cast<uint16_t>((index & 1u) ? sword >> 16 : sword)));
-  uint32_t z = FMT == kW_INT4 ? 8u : 128u;
-  if (zero) z = (zword >> (8u * (index & 3u))) & 255u;
+__device__ __forceinline__ void group_of(uint32_t sword, uint32_t zword, const Place& at, bool zero, float& scale, Offset& o) {
+  scale = __half2float(__ushort_as_half(static_cast<uint16_t>(__byte_perm(sword, 0u, at.half))));
   if (FMT == kW_INT4) {
     o.flip = zero ? 0x43004300u : 0x43084308u;
-    o.pair = 0x43004300u | z | (z << 16);
-    o.plus = static_cast<float>(128u + z);
+    o.pair = 0x43084308u;
+    o.plus = 136.0f;
+    if (zero) {
+      const uint32_t z = (zword >> at.shift) & 255u;
+      o.pair = 0x43004300u | z | (z << 16);
+      o.plus = static_cast<float>(128u + z);
+    }
   } else {
     o.flip = zero ? 0u : 0x80808080u;
-    o.magic = static_cast<float>(8388608u + z);
+    o.magic = 8388736.0f;
+    if (zero) o.magic = static_cast<float>(8388608u + ((zword >> at.shift) & 255u));
   }
 }
 
@@ -469,13 +484,19 @@ __global__ void __launch_bounds__(kThreads, 1) few_up_kernel(GateArgs gate, FewA
   // issue side: its unit (expert ix, tile it), step is, pointers of the step
   int ix = static_cast<int>(blockIdx.x) / tiles, it = static_cast<int>(blockIdx.x) % tiles, is = s0;
   uint32_t idst = ring + lane * 16;
+  const uint32_t wpos = static_cast<uint32_t>(2048 - lane * 16 + (lane & 7) * 16 + (lane >> 3) * 4);
   const uint32_t iend = ring + static_cast<uint32_t>(depth * kStage);
   const uint8_t* isrc = nullptr;
-  int64_t iat = 0;  // row `lane`'s scale (16 gate rows, 16 up rows), first group
+  // addresses of row `lane`'s scale and zero point (16 gate rows, 16 up rows)
+  uint64_t isc = 0, izp = 0;
   auto start_unit = [&] {
     const int64_t row = static_cast<int64_t>(r.expert[ix]) * 2 * a.I + it * 16;
     isrc = w13 + (row + g) * rb + row_bytes<FMT>(static_cast<int64_t>(s0) * STEP) + t4 * 16;
-    if (kGrouped<FMT>) iat = (row + (lane & 15) + static_cast<int64_t>(lane >> 4) * a.I) * G;
+    if (kGrouped<FMT>) {
+      const int64_t at = (row + (lane & 15) + static_cast<int64_t>(lane >> 4) * a.I) * G + s0 * STEP / 128;
+      isc = reinterpret_cast<uint64_t>(a.w13_scale) + 2 * at;
+      izp = reinterpret_cast<uint64_t>(a.w13_zero) + at;
+    }
     is = s0;
   };
   bool more = ix < count && s0 < s1;
@@ -488,10 +509,12 @@ __global__ void __launch_bounds__(kThreads, 1) few_up_kernel(GateArgs gate, FewA
       cp_async16(idst + 1536, isrc + to_up + to8);
       if (kGrouped<FMT>) {
         // the 4-byte words that hold row `lane`'s scale and zero point
-        const int64_t at = iat + is * STEP / 128;
-        const uint32_t d = idst + 2048 - lane * 16 + (lane & 7) * 16 + (lane >> 3) * 4;
-        cp_async4(d, static_cast<const uint16_t*>(a.w13_scale) + (at & ~1ll));
-        if (zero) cp_async4(d + 128, a.w13_zero + (at & ~3ll));
+        cp_async4(idst + wpos, reinterpret_cast<const void*>(isc & ~3ull));
+        if (zero) cp_async4(idst + wpos + 128, reinterpret_cast<const void*>(izp & ~3ull));
+        if (STEP == 128 || (is & 1)) {
+          isc += 2;
+          izp += 1;
+        }
       }
       isrc += 64;
       if (++is == s1) {
@@ -518,13 +541,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_up_kernel(GateArgs gate, FewA
   const uint8_t* xlane = xs + static_cast<size_t>(min(g, a.T - 1)) * xstride + t4 * 16;
   while (x < count) {
     const int i0 = tile * 16;
-    uint32_t at[4];  // the four rows' scales: index modulo 4
-    if (kGrouped<FMT>) {
-      const uint32_t row = static_cast<uint32_t>(r.expert[x]) * 2u * static_cast<uint32_t>(a.I) + static_cast<uint32_t>(i0 + g);
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        at[q] = ((row + 8u * (q & 1) + static_cast<uint32_t>(q >> 1) * static_cast<uint32_t>(a.I)) * static_cast<uint32_t>(G)) & 3u;
-    }
     float acc[2][4] = {};
     for (int s = s0; s < s1; ++s) {
       __syncwarp();
@@ -539,9 +555,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_up_kernel(GateArgs gate, FewA
         const uint4 sw = lds128(src + 2048 + g * 16);  // rows g, g + 8 (gate), g, g + 8 (up)
         uint4 zw = make_uint4(0, 0, 0, 0);
         if (zero) zw = lds128(src + 2176 + g * 16);
+        const Place at(static_cast<uint32_t>(g * G + group));
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          group_of<FMT>(word(sw, q), word(zw, q), at[q] + static_cast<uint32_t>(group), zero, sc[q], off[q]);
+        for (int q = 0; q < 4; ++q) group_of<FMT>(word(sw, q), word(zw, q), at, zero, sc[q], off[q]);
       }
       uint4 w[4];
 #pragma unroll
@@ -686,12 +702,16 @@ __global__ void __launch_bounds__(kThreads, 1) few_down_kernel(GateArgs gate, Fe
     const uint8_t* w;           // weights of the step, row g
     const uint16_t* act;        // this lane's token, or null
     uint32_t place;             // where its activations go in a stage
-    int64_t at;                 // row `lane`'s scale
+    uint64_t sc, zp;            // row `lane`'s scale and zero point
   };
   auto start_expert = [&](Cursor& c) {
     const int64_t row = static_cast<int64_t>(r.expert[c.x]) * a.H + c.unit * 16;
     c.w = static_cast<const uint8_t*>(a.w2) + (row + g) * rb + row_bytes<FMT>(c.c * STEP) + t4 * 16;
-    c.at = (row + (lane & 15)) * G + c.c * STEP / 128;
+    if (kGrouped<FMT>) {
+      const int64_t at = (row + (lane & 15)) * G + c.c;
+      c.sc = reinterpret_cast<uint64_t>(a.w2_scale) + 2 * at;
+      c.zp = reinterpret_cast<uint64_t>(a.w2_zero) + at;
+    }
     const uint32_t mask = r.tokens[c.x];
     c.act = (mask >> g & 1) ? a.act + static_cast<size_t>(r.slot[c.x][g]) * 2 * a.I + c.c * STEP + t4 * 8 : nullptr;
     c.place = place_of(mask);
@@ -713,8 +733,8 @@ __global__ void __launch_bounds__(kThreads, 1) few_down_kernel(GateArgs gate, Fe
         }
         if (kGrouped<FMT> && lane < 16) {
           const uint32_t d = c.dst + F::DOWN * 1024 + (lane & 7) * 8 + (lane >> 3) * 4;
-          cp_async4(d, static_cast<const uint16_t*>(a.w2_scale) + (c.at & ~1ll));
-          if (zero) cp_async4(d + 64, a.w2_zero + (c.at & ~3ll));
+          cp_async4(d, reinterpret_cast<const void*>(c.sc & ~3ull));
+          if (zero) cp_async4(d + 64, reinterpret_cast<const void*>(c.zp & ~3ull));
         }
       }
       if (acts && c.act != nullptr) {
@@ -727,7 +747,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_down_kernel(GateArgs gate, Fe
         }
       }
       c.w += F::DOWN * 64;
-      c.at += 1;
+      if (kGrouped<FMT>) {
+        c.sc += 2;
+        c.zp += 1;
+      }
       if (c.act != nullptr) c.act += STEP;
       ++c.c;
       if (--c.left == 0) {
@@ -780,16 +803,11 @@ __global__ void __launch_bounds__(kThreads, 1) few_down_kernel(GateArgs gate, Fe
     float part[2][4] = {};  // of the activations' two halves
     int x = x0, c = c0;
     for (int s = s0; s < s1; c = 0, ++x) {
-      const int end = min(s1, s + per - c);  // of this expert's part
+      const int from = s, end = min(s1, s + per - c);  // of this expert's part
       const uint32_t mask = r.tokens[x];
       const uint32_t place = place_of(mask);
       const bool use0 = mask >> (2 * t4) & 1, use1 = mask >> (2 * t4 + 1) & 1;
       const float2 wt = *reinterpret_cast<const float2*>(&weight[x][2 * t4]);
-      uint32_t at[2];
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-        at[q] = (static_cast<uint32_t>(r.expert[x]) * static_cast<uint32_t>(a.H) +
-                 static_cast<uint32_t>(unit * 16 + g + 8 * q)) * static_cast<uint32_t>(G) + static_cast<uint32_t>(c);
       auto join = [&](const float (&sc)[2]) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -809,11 +827,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_down_kernel(GateArgs gate, Fe
           const uint2 sw = lds64(src + F::DOWN * 1024 + g * 8);  // rows g, g + 8
           uint2 zw = make_uint2(0, 0);
           if (zero) zw = lds64(src + F::DOWN * 1024 + 64 + g * 8);
+          const Place at(static_cast<uint32_t>(g * G + c + s - from));
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            group_of<FMT>(q ? sw.y : sw.x, q ? zw.y : zw.x, at[q], zero, sc[q], off[q]);
-            ++at[q];
-          }
+          for (int q = 0; q < 2; ++q) group_of<FMT>(q ? sw.y : sw.x, q ? zw.y : zw.x, at, zero, sc[q], off[q]);
         }
 #pragma unroll
         for (int u = 0; u < F::DOWN; ++u) {
