@@ -167,6 +167,7 @@ struct Routing {
   int32_t ids[kMaxSlots];              // per slot
   float w[kMaxSlots];                  // per slot
   uint32_t seen[32];                   // bit per expert
+  int before[32];                      // chosen experts before each word's
   int16_t expert[kMaxSlots];
   uint8_t tokens[kMaxSlots];           // bit per token
   uint8_t slot[kMaxSlots][kFewMaxTokens];
@@ -186,23 +187,31 @@ __device__ __forceinline__ void build_routing(Routing& r, const FewArgs& a, Weig
   __syncthreads();
   for (int s = threadIdx.x; s < S; s += kThreads) atomicOr(&r.seen[r.ids[s] >> 5], 1u << (r.ids[s] & 31));
   __syncthreads();
+  if (threadIdx.x < 32) {
+    const int n = __popc(r.seen[threadIdx.x]);
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (static_cast<int>(threadIdx.x) >= o) sum += v;
+    }
+    r.before[threadIdx.x] = sum - n;
+    if (threadIdx.x == 31) r.count = sum;
+  }
+  __syncthreads();
   for (int s = threadIdx.x; s < S; s += kThreads) {
     const int e = r.ids[s], t = s / a.k;
-    int at = __popc(r.seen[e >> 5] & ((1u << (e & 31)) - 1u));
-    for (int i = 0; i < (e >> 5); ++i) at += __popc(r.seen[i]);
+    const int at = r.before[e >> 5] + __popc(r.seen[e >> 5] & ((1u << (e & 31)) - 1u));
     r.expert[at] = static_cast<int16_t>(e);
     r.slot[at][t] = static_cast<uint8_t>(s);
     if (weight != nullptr) weight[at][t] = r.w[s];
     atomicOr(reinterpret_cast<uint32_t*>(r.tokens) + (at >> 2), 1u << (8 * (at & 3) + t));
   }
-  if (threadIdx.x == 0) {
-    int n = 0;
-    for (int i = 0; i < 32; ++i) n += __popc(r.seen[i]);
-    r.count = n;
+  __syncthreads();
+  if (weight != nullptr) {  // (only the second kernel's ring goes by it)
+    if (threadIdx.x < r.count) atomicMax(&r.most, __popc(r.tokens[threadIdx.x]));
+    __syncthreads();
   }
-  __syncthreads();
-  if (threadIdx.x < r.count) atomicMax(&r.most, __popc(r.tokens[threadIdx.x]));
-  __syncthreads();
 }
 
 __device__ __forceinline__ float block_max(float v, float* part) {
@@ -236,6 +245,10 @@ constexpr int up_stage() {
   return 4 * 512 + (kGrouped<FMT> ? 256 : 0);
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
+}
+
 // A float's order as an unsigned one (-0 as +0); 0 is below every number.
 __device__ __forceinline__ uint32_t ordered(float v) {
   const uint32_t u = __float_as_uint(v + 0.f);
@@ -243,26 +256,33 @@ __device__ __forceinline__ uint32_t ordered(float v) {
 }
 
 // The k best of the warp's keys (32 strided experts per register, 0: out of the
-// running), ties to the lower expert: lane j returns the j-th expert.  Two warp
-// reductions a round.
+// running), ties to the lower expert: lane j returns the j-th expert.  A lane
+// keeps the best of its own; a round is two warp reductions, after which the
+// winner's lane looks for its next.
 template <int EPL>
 __device__ __forceinline__ int best_k(uint32_t (&key)[EPL], int k, int lane) {
   int mine = 0;
-#pragma unroll 1
-  for (int j = 0; j < k; ++j) {
-    uint32_t m = key[0];
+  uint32_t top = 0, at = 0;
+  auto look = [&] {
+    top = key[0];
 #pragma unroll
-    for (int i = 1; i < EPL; ++i) m = max(m, key[i]);
-    m = __reduce_max_sync(0xffffffffu, m);
-    uint32_t at = 0xffffffffu;
+    for (int i = 1; i < EPL; ++i) top = max(top, key[i]);
 #pragma unroll
     for (int i = EPL - 1; i >= 0; --i)
-      if (key[i] == m) at = static_cast<uint32_t>(lane + 32 * i);
-    at = __reduce_min_sync(0xffffffffu, at);
-    if (lane == j) mine = static_cast<int>(at);
+      if (key[i] == top) at = static_cast<uint32_t>(lane + 32 * i);
+  };
+  look();
+#pragma unroll 1
+  for (int j = 0; j < k; ++j) {
+    const uint32_t m = __reduce_max_sync(0xffffffffu, top);
+    const uint32_t best = __reduce_min_sync(0xffffffffu, top == m ? at : 0xffffffffu);
+    if (lane == j) mine = static_cast<int>(best);
+    if (top == m && at == best) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      if (at == static_cast<uint32_t>(lane + 32 * i)) key[i] = 0;
+      for (int i = 0; i < EPL; ++i)
+        if (best == static_cast<uint32_t>(lane + 32 * i)) key[i] = 0;
+      look();
+    }
   }
   return mine;
 }
@@ -404,6 +424,14 @@ __global__ void __launch_bounds__(kThreads, 1) few_up_kernel(GateArgs gate, FewA
   const int xstride = token_stride(a.H);
   uint8_t* rings = xs + (static_cast<size_t>(a.T) * xstride + 127) / 128 * 128;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  // While the kernel before still runs: what the gate reads towards L2 (a hint
+  // only: nothing is read before the wait)
+  if (blockIdx.x == 0) {
+    for (int i = tid * 32; i < a.T * a.E; i += kThreads * 32) prefetch_l2(gate.logits + i);
+    if (gate.bias != nullptr)
+      for (int i = tid * 32; i < a.E; i += kThreads * 32) prefetch_l2(gate.bias + i);
+    for (int i = tid * 64; i < a.T * a.H; i += kThreads * 64) prefetch_l2(a.x + i);
+  }
   pdl_wait();
   pdl_trigger();
 
