@@ -932,9 +932,10 @@ cudaError_t plan_and_launch(Params p, int bn, bool pair, bool swiglu, const void
   if (pair) {
     grid = 2 * static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
     if constexpr (KIND == kE4M3) {
-      if (swiglu) return launch<KIND, true, true, 256>(maps, p, grid, s);
+      return swiglu ? launch<KIND, true, true, 256>(maps, p, grid, s) : launch<KIND, false, true, 256>(maps, p, grid, s);
+    } else {
+      return cudaErrorInvalidValue;  // (choose() pairs CTAs for 8-bit operands only)
     }
-    return launch<KIND, false, true, 256>(maps, p, grid, s);
   }
   if (p.P > 1) grid = static_cast<int>(tiles) * p.P;
   else grid = static_cast<int>(tiles < sms ? tiles : sms);

@@ -4,6 +4,9 @@
 // With at most 8 tokens the chosen experts' weights are read once and nothing
 // else is large, so the layer is bound by the rate at which the weights stream
 // in (int4: nearly by the integer work that unpacks them, see convert()).
+// Measured in a graph: Mixtral bf16, 8 tokens 386 us = 6.6 TB/s, one token 106 us;
+// DeepSeek-V3 int4, one token 59 us for 182 MB (the first kernel 4.9 TB/s, the
+// second 3.1 TB/s), 8 tokens 312 us; Qwen2 fp8, one token 43 us.
 //
 // Every warp streams its own part of the weights through a private ring in
 // shared memory (cp.async, 16 bytes a lane; a lane reads back what it copied

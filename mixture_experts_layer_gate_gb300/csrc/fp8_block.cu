@@ -2,7 +2,10 @@
 // moe_gemm_fp8_block_swiglu): out[m, n] = sum_b a_scale[m, b] w_scale[n / 128, b]
 // sum_{k in b} a[m, k] w[n, k].  A k-block of the dense kernel is a scale block,
 // so each accumulator is one block's product and is joined to the sums in
-// registers with one multiply-add per value.
+// registers with one multiply-add per value.  Measured in a graph: SwiGLU, M = 4096,
+// K = 7168, N = 2048 105 us = 2.3 PFLOP/s; M = 4096, K = 2048, N = 7168 62 us = 1.95
+// PFLOP/s (bound by the joining warps: a k-block of a CTA pair takes ~800 cycles,
+// its MMAs ~690; and by storing a tile every 16 k-blocks).
 #include "dense.cuh"
 
 namespace moe {

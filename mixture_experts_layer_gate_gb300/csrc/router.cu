@@ -4,7 +4,7 @@
 // 256 experts 20 us, of which x is 8.6 us of DRAM time).  Up to 4 tokens, where
 // only latency counts, a CTA takes an expert: all of its row is in flight at
 // once, and the threads' sums are joined in a fixed order (T = 1, H = 7168, 256
-// experts: see launch_router).
+// experts: 1.8 us in a graph; 2 and 4 tokens see launch_router).
 #include "dense.cuh"
 
 namespace moe {
