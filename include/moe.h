@@ -393,15 +393,15 @@ moe_status_t moe_get_plan_for_sms(const moe_problem_t* p, int32_t num_sms, moe_p
  * elements of a row are adjacent); rows of one tensor must not overlap.  These
  * calls need the 256-byte error header of a workspace; moe_gemm_fp8_block_swiglu
  * with at most 8 rows also uses what follows it as scratch where that is large
- * enough (256 + 512 * ceil(N / 16384) + 4 * M * N bytes always are; without it
- * the general kernel runs).  The workspace is theirs (not one that moe_forward
+ * enough (256 + 4096 + 4 * M * N bytes, for N <= 131072; without it the general
+ * kernel runs).  The workspace is theirs (not one that moe_forward
  * or the stage calls write), all zero when first used, and serves one stream's
  * calls at a time.  MOE_OP_WORKSPACE_BYTES are enough up to N = 16384. */
 
 typedef enum { MOE_T_BF16 = 0, MOE_T_F16 = 1, MOE_T_F32 = 2 } moe_dtype_t;
 typedef enum { MOE_QUANT_NONE = 0, MOE_QUANT_BLOCK128 = 1, MOE_QUANT_TOKEN = 2 } moe_quant_t;
 
-#define MOE_OP_WORKSPACE_BYTES (256 + 512 + 4 * 8 * 16384)
+#define MOE_OP_WORKSPACE_BYTES (256 + 4096 + 4 * 8 * 16384)
 
 /* T rows of H columns, 1 <= H <= 16384, eps >= 0. */
 typedef struct {

@@ -30,7 +30,7 @@ EXPORTED = ("moe_scratch_size", "moe_workspace_size", "moe_padded_capacity", "mo
 
 DTYPES = {"bf16": 0, "f16": 1, "f32": 2}
 QUANTS = {"none": 0, "block": 1, "token": 2}
-OP_WORKSPACE_BYTES = 256 + 512 + 4 * 8 * 16384
+OP_WORKSPACE_BYTES = 256 + 4096 + 4 * 8 * 16384
 FEW_MAX_TOKENS = 8
 
 

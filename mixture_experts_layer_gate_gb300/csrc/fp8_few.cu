@@ -241,10 +241,10 @@ cudaError_t launch(const Fp8GemmArgs& p, int grid, cudaStream_t s) {
 
 }  // namespace
 
-size_t fp8_few_scratch(int M, int N) { return (static_cast<size_t>(N) / 128 * 4 + 255) / 256 * 256 + static_cast<size_t>(M) * N * 4; }
+size_t fp8_few_scratch(int M, int N) { return kFewTicketBytes + static_cast<size_t>(M) * N * 4; }
 
 // At most 8 rows whose codes leave room for a ring of two stages a warp, and
-// with SwiGLU scratch for them.
+// with SwiGLU scratch for them and a ticket for each block.
 bool fp8_few_fits(const Fp8GemmArgs& p) {
   if (p.M > 8 || p.K > 65536) return false;
   return p.codes != nullptr ? p.tickets != nullptr && depth_of<true>(p) >= 2 : depth_of<false>(p) >= 2;

@@ -232,6 +232,9 @@ struct Fp8GemmArgs {
 cudaError_t launch_fp8_block(const Fp8GemmArgs& g, cudaStream_t s);
 // The same for a few rows; whether they fit its shared memory.
 bool fp8_few_fits(const Fp8GemmArgs& g);
+// Tickets take the same bytes whatever N is: the values after them are left there,
+// and another call's tickets must find zeros.
+constexpr size_t kFewTicketBytes = 4096;
 size_t fp8_few_scratch(int M, int N);  // bytes of tickets and act
 cudaError_t launch_fp8_few(const Fp8GemmArgs& g, cudaStream_t s);
 

@@ -193,10 +193,11 @@ moe_status_t moe_gemm_fp8_block_swiglu(const moe_fp8_gemm_t* g, const void* a, i
   f.w_scale = w13_scale;
   f.codes = static_cast<uint8_t*>(codes);
   f.scales = scales;
-  if (g->M <= 8 && ws_bytes >= kHeaderBytes + fp8_few_scratch(g->M, g->N)) {
+  if (g->M <= 8 && static_cast<size_t>(g->N) / 128 * 4 <= kFewTicketBytes &&
+      ws_bytes >= kHeaderBytes + fp8_few_scratch(g->M, g->N)) {
     uint8_t* scratch = static_cast<uint8_t*>(ws) + kHeaderBytes;
     f.tickets = reinterpret_cast<uint32_t*>(scratch);
-    f.act = reinterpret_cast<float*>(scratch + align256(static_cast<size_t>(g->N) / 128 * 4));
+    f.act = reinterpret_cast<float*>(scratch + kFewTicketBytes);
   }
   f.a_stride = a_stride;
   f.a_scale_stride = a_scale_stride;

@@ -387,11 +387,11 @@ def test_gemm_many_tiles(dev):
     run_gemm(dev, 700, 1000, 7168, "f32")
 
 
-def run_swiglu(dev, M, N, K, pad=0):
+def run_swiglu(dev, M, N, K, pad=0, ws=None):
     a, sa, w, sw = product_inputs(M, 2 * N, K, M + N + K)
     codes = torch.full((M, N), 0xAA, dtype=torch.uint8, device=dev)
     scales = torch.full((M, N // 128), -1.0, device=dev)
-    ws = moe.alloc_op_workspace(dev)
+    ws = moe.alloc_op_workspace(dev) if ws is None else ws
     moe.gemm_fp8_block_swiglu(moe.fp8_gemm_problem(M, N, K), wide(a, pad, dev, fill=127), wide(sa, pad, dev),
                               wide(w, pad, dev, fill=127), sw.to(dev), codes, scales, ws)
     assert moe.get_device_error(ws) == 0
@@ -410,6 +410,20 @@ def test_swiglu_sizes(dev, M, N, K, pad):
 def test_swiglu_many_tiles(dev):
     run_swiglu(dev, 1, 2048, 7168)
     run_swiglu(dev, 1500, 1280, 384)
+
+
+@gpu
+def test_swiglu_of_few_rows_shares_a_workspace(dev):
+    """Widths in turn, and each again: every call finds the counters of the workspace at zero."""
+    ws = moe.alloc_op_workspace(dev)
+    for M, N, K in ((8, 256, 128), (1, 16384, 128), (8, 256, 128), (3, 9088, 144), (8, 16384, 16)):
+        run_swiglu(dev, M, N, K, ws=ws)
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", [(1, 2048, 7168), (8, 128, 272)])
+def test_swiglu_of_few_rows_without_scratch(dev, M, N, K):
+    run_swiglu(dev, M, N, K, ws=torch.zeros(256, dtype=torch.uint8, device=dev))
 
 
 @gpu
