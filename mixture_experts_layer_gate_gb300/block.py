@@ -20,8 +20,9 @@ class SharedExpert:
 class MoEBlock:
     """`block(x, residual)` -> (out, residual + x), both bf16 [T, H]; the next block adds out to the residual.
 
-    `gate` takes problem()'s keywords (scoring, n_group, wdtype, ...).  Batches of
-    at most FEW_MAX_TOKENS tokens run moe_forward_few, others moe_forward.  Calls
+    `gate` takes problem()'s keywords (scoring, n_group, wdtype, ...).  Batches that
+    moe_forward_few takes (FEW_MAX_TOKENS tokens up to H = 8192, fewer beyond) run
+    there, others in moe_forward.  Calls
     of one block share its workspaces: order them on one stream.
     """
 
@@ -31,7 +32,11 @@ class MoEBlock:
         self.norm_weight, self.router_weight, self.router_bias = norm_weight, router_weight, router_bias
         self.shared, self.weights = shared, weights
         self.layer = b.MoELayer(H, I, E, top_k, weights, max_tokens, device, **gate)
-        self.few_ws = b.alloc_few_workspace(self.layer.problem(min(max_tokens, b.FEW_MAX_TOKENS)), device)
+        self.few_ws = None
+        for T in range(min(max_tokens, b.FEW_MAX_TOKENS), 0, -1):
+            if b.few_workspace_size(self.layer.problem(T)):
+                self.few_ws = b.alloc_few_workspace(self.layer.problem(T), device)
+                break
         self.op_ws = b.alloc_op_workspace(device)
 
     def __call__(self, x, residual=None, stream=None):
@@ -50,8 +55,9 @@ class MoEBlock:
         logits = new(T, p.E, dtype=torch.float32)
         b.router_logits(b.router_problem(T, H, p.E), y, self.router_weight, logits, self.op_ws, stream)
         out = new(T, H)
-        if 0 < T <= b.FEW_MAX_TOKENS:
-            if b.few_workspace_size(p) > self.few_ws.numel():
+        few = b.few_workspace_size(p) if 0 < T <= b.FEW_MAX_TOKENS else 0
+        if few:
+            if self.few_ws is None or few > self.few_ws.numel():
                 self.few_ws = b.alloc_few_workspace(p, dev)
             b.forward_few(p, self.weights, y, logits, self.router_bias, out, self.few_ws, stream)
         else:
@@ -68,5 +74,5 @@ class MoEBlock:
 
     def device_error(self, stream=None) -> int:
         """First error that a kernel of the block recorded (0: none), cleared; synchronises the stream."""
-        found = [b.get_device_error(ws, stream) for ws in (self.op_ws, self.few_ws, self.layer.ws)]
+        found = [b.get_device_error(ws, stream) for ws in (self.op_ws, self.few_ws, self.layer.ws) if ws is not None]
         return next((e for e in found if e), 0)

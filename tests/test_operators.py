@@ -621,3 +621,25 @@ def test_block(dev, T, shared):
     # two quantisations to e4m3 (2^-4 at most, a fifth of that on average) and bf16 roundings between the stages
     err = float((out.cpu().double() - want).norm() / want.norm())
     assert err <= 4e-2, err
+
+
+@gpu
+@pytest.mark.parametrize("max_tokens,T", [(8, 8), (8, 3), (2, 4), (0, 1)])
+def test_block_of_wide_rows(dev, max_tokens, T):
+    """H = 16384: the few-token layer takes 4 tokens at most, and the block calls the general one beyond."""
+    H, I, E, k = 16384, 128, 4, 2
+    g = gen(T)
+    w = few_weights(moe.problem(T, H, I, E, k), False, 9)
+    nw, rw = torch.ones(H, dtype=torch.bfloat16), (0.01 * randn(g, E, H)).to(torch.bfloat16)
+    wd = moe.Weights(*[None if t is None else t.to(dev) for t in w])
+    block = moe.MoEBlock(H, I, E, k, wd, nw.to(dev), rw.to(dev), None, max_tokens, dev)
+    x = randn(g, T, H).to(torch.bfloat16).to(dev)
+    out, _ = block(x)
+    assert block.device_error() == 0
+    y, logits = torch.empty_like(x), torch.empty((T, E), device=dev)
+    moe.add_rms_norm(moe.norm_problem(T, H), x, nw.to(dev), y=y)
+    moe.router_logits(moe.router_problem(T, H, E), y, rw.to(dev), logits, moe.alloc_op_workspace(dev))
+    want, _ = few_reference.few(moe.problem(T, H, I, E, k), w, y.cpu(), logits.cpu(), None)
+    # moe_forward rounds the activations and each expert's output to bf16
+    err = float((out.cpu().double() - want).norm() / want.norm())
+    assert err <= 1e-2, err
