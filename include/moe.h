@@ -419,7 +419,7 @@ typedef struct {
  *   y = v rounded to dtype (NULL: not written)
  *   scales, codes (quant other than NONE): per block of 128 columns (float
  *     [T, ceil(H / 128)], the last block may be short) or per row (float [T]),
- *     scale = max |v| / 448, or 1 where every v is 0; codes uint8 e4m3 [T, H],
+ *     scale = max |v| / 448, or 1 where that is 0; codes uint8 e4m3 [T, H],
  *     contiguous, the code of v / scale (round to nearest even, saturating),
  *     from the unrounded v.  NaN propagates to its row (y, and e4m3 NaN codes).
  * residual_out may be the residual itself (same stride); otherwise inputs and
@@ -469,7 +469,7 @@ moe_status_t moe_gemm_fp8_block(const moe_fp8_gemm_t* g, const void* a, int64_t 
  * projection reads: with h = the product above of a and w13 [2N, K] (rows
  * [0, N) gate, [N, 2N) up; w13_scale [2N / 128, ceil(K / 128)]), N % 128 == 0,
  *   v[m, n] = silu(h[m, n]) * h[m, N + n]   (float, not rounded)
- *   scales[m, b] = max |v| over columns [128 b, 128 b + 128) / 448 (1 if all 0)
+ *   scales[m, b] = max |v| over columns [128 b, 128 b + 128) / 448 (1 if 0)
  *   codes[m, n]  = e4m3(v / scale), uint8 [M, N] contiguous; scales float [M, N / 128].
  * out_dtype is not used; accumulate must be 0. */
 moe_status_t moe_gemm_fp8_block_swiglu(const moe_fp8_gemm_t* g, const void* a, int64_t a_stride,

@@ -203,7 +203,10 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
 }
 
 __device__ __forceinline__ float max_nan(float a, float b) { return (a > b || a != a) ? a : b; }
-__device__ __forceinline__ float quant_scale(float amax) { return amax == 0.f ? 1.0f : __fdiv_rn(amax, 448.0f); }
+__device__ __forceinline__ float quant_scale(float amax) {
+  const float s = __fdiv_rn(amax, 448.0f);
+  return s == 0.f ? 1.0f : s;
+}
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float scale) {

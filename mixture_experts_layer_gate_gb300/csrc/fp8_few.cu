@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(32 * kFewWarps<SWIGLU>, SWIGLU ? 1 : 2) fp8_fe
         float m = max_nan(max_nan(fabsf(v.x), fabsf(v.y)), max_nan(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float scale = m == 0.f ? 1.0f : __fdiv_rn(m, 448.0f);
+        const float whole = __fdiv_rn(m, 448.0f), scale = whole == 0.f ? 1.0f : whole;
         if (lane == 0) p.scales[static_cast<int64_t>(warp) * (p.N / 128) + unit / 8] = scale;
         reinterpret_cast<uint32_t*>(p.codes + static_cast<int64_t>(warp) * p.N + n0)[lane] =
             f32x2_to_e4m3x2(__fdiv_rn(v.x, scale), __fdiv_rn(v.y, scale)) |

@@ -135,8 +135,10 @@ struct Quotient {
 };
 
 __device__ __forceinline__ float scale_of(float amax) {
-  // 1 for a block of zeros; a NaN (or infinite) maximum stays one
-  return amax == 0.f ? 1.0f : __fdiv_rn(amax, 448.0f);
+  // 1 for a block of zeros, or of values so small that the scale would be zero; a
+  // NaN (or infinite) maximum stays one
+  const float s = __fdiv_rn(amax, 448.0f);
+  return s == 0.f ? 1.0f : s;
 }
 
 template <typename T, typename W, bool VEC, bool WIDE, int CH>

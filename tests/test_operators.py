@@ -265,6 +265,22 @@ def test_norm_nan_stays_in_its_row(dev, quant, H):
     assert torch.isfinite(y[keep]).all() and torch.isfinite(scales[keep]).all()
 
 
+@gpu
+@pytest.mark.parametrize("quant", ["block", "token"])
+@pytest.mark.parametrize("H", [256, 259, 1280])
+def test_norm_values_below_any_scale(dev, quant, H):
+    """max |v| / 448 below the smallest float: scale 1 and codes of zero, no division by zero."""
+    x = torch.full((3, H), 3e-43)
+    x[1] = 0.5
+    n = moe.norm_problem(3, H, dtype="f32", eps=1.0, quant=quant)
+    nb = -(-H // 128) if quant == "block" else 1
+    codes, scales = torch.full((3, H), 0xAA, dtype=torch.uint8, device=dev), torch.zeros(3, nb, device=dev)
+    moe.add_rms_norm(n, x.to(dev), torch.ones(H, device=dev), codes=codes, scales=scales)
+    for t in (0, 2):
+        assert bool((scales[t] == 1).all()) and bool((codes[t] == 0).all())
+    assert bool((codes[1] == 0x7E).all())  # each value is its block's largest: 448
+
+
 # ------------------------------------------------------------------ router scores
 
 
@@ -444,6 +460,20 @@ def test_product_of_zeros_and_nan(dev):
     assert bool(((codes[3] & 127) == 0).all()) and bool((scales[3] == 1).all())
     assert torch.isnan(scales[7]).all() and bool(((codes[7] & 127) == 127).all())
     assert torch.isfinite(scales[others]).all()
+
+
+@gpu
+@pytest.mark.parametrize("M,scratch", [(1, True), (8, True), (8, False), (130, False)])
+def test_swiglu_values_below_any_scale(dev, M, scratch):
+    N, K = 256, 16
+    ones = lambda *s: torch.full(s, 0x38, dtype=torch.uint8, device=dev)  # noqa: E731
+    ws = moe.alloc_op_workspace(dev)[:None if scratch else 256]
+    codes, scales = torch.full((M, N), 0xAA, dtype=torch.uint8, device=dev), torch.zeros(M, N // 128, device=dev)
+    w_scale = torch.full((2 * N // 128, 1), 2e-23, device=dev)  # gate and up 3.2e-22 each, silu(gate) up 5e-44
+    moe.gemm_fp8_block_swiglu(moe.fp8_gemm_problem(M, N, K), ones(M, K), torch.ones(M, 1, device=dev), ones(2 * N, K),
+                              w_scale, codes, scales, ws)
+    assert moe.get_device_error(ws) == 0
+    assert bool((scales == 1).all()) and bool((codes == 0).all())
 
 
 # ------------------------------------------------------------------ the layer for a few tokens
