@@ -32,6 +32,14 @@ def dev():
     return torch.device("cuda:0")
 
 
+def far(t, stride, dev):
+    """t on the device with rows `stride` elements apart (memory between them as it is)."""
+    w = torch.empty((t.shape[0] - 1) * stride + t.shape[1], dtype=t.dtype, device=dev)
+    v = torch.as_strided(w, t.shape, (stride, 1))
+    v.copy_(t)
+    return v
+
+
 def gen(seed):
     return torch.Generator().manual_seed(seed)
 
@@ -228,6 +236,30 @@ def test_norm_rows(dev, T, H):
 
 
 @gpu
+@pytest.mark.parametrize("T,H,dtype,wdtype", [(700, 1032, "bf16", "bf16"), (1900, 1536, "f16", "f32"),
+                                              (901, 8191, "bf16", "f32"), (305, 2048, "f32", "f32"),
+                                              (320, 16384, "bf16", "bf16")])
+@pytest.mark.parametrize("quant", ["none", "block", "token"])
+def test_norm_more_rows_than_ctas(dev, T, H, dtype, wdtype, quant):
+    run_norm(dev, T, H, dtype, wdtype, True, quant, 0, in_place=quant == "block")
+    if quant == "none":
+        run_norm(dev, T, H, dtype, wdtype, False, quant, 0)
+
+
+@gpu
+def test_norm_offsets_past_32_bits(dev):
+    g, H, far_apart = gen(8), 520, 2 ** 30 + 8
+    x, r, w = randn(g, 3, H).to(torch.bfloat16), randn(g, 3, H).to(torch.bfloat16), torch.ones(H, dtype=torch.bfloat16)
+    n = moe.norm_problem(3, H)
+    want, total = torch.empty_like(x, device=dev), torch.empty_like(x, device=dev)
+    moe.add_rms_norm(n, x.to(dev), w.to(dev), residual=r.to(dev), residual_out=total, y=want)
+    xd, rd = far(x, far_apart, dev), far(r, far_apart + 8, dev)
+    yd = far(torch.zeros_like(x), far_apart + 16, dev)
+    moe.add_rms_norm(n, xd, w.to(dev), residual=rd, residual_out=rd, y=yd)
+    assert torch.equal(yd, want) and torch.equal(rd, total)
+
+
+@gpu
 def test_norm_in_place_and_without_y(dev):
     run_norm(dev, 9, 1100, "bf16", "bf16", True, "block", 0, in_place=True)
     run_norm(dev, 9, 1024, "bf16", "bf16", True, "block", 8, in_place=True, y=False)
@@ -313,6 +345,32 @@ def test_router_most_experts_and_many_tokens(dev):
 
 
 @gpu
+@pytest.mark.parametrize("T,H,E", [(1, 24, 1024), (2, 2056, 1024), (3, 1032, 683), (3, 1032, 682), (4, 9000, 512),
+                                   (4, 512, 513), (2, 32768, 5), (130, 32768, 40)])
+def test_router_few_tokens_and_long_rows(dev, T, H, E):
+    g = gen(E)
+    x, w = randn(g, T, H).to(torch.float16), (0.02 * randn(g, E, H)).to(torch.float16)
+    logits = torch.full((T, E), float("nan"), device=dev)
+    ws = moe.alloc_op_workspace(dev)
+    moe.router_logits(moe.router_problem(T, H, E, dtype="f16"), wide(x, 8, dev), wide(w, 8, dev), logits, ws)
+    want, tol = ref.router(x, w)
+    ref.check(logits, want, tol, "logits")
+    assert moe.get_device_error(ws) == 0
+
+
+@gpu
+@pytest.mark.parametrize("T", [3, 9])
+def test_router_offsets_past_32_bits(dev, T):
+    g, H, E = gen(T), 520, 3
+    x, w = randn(g, T, H).to(torch.bfloat16), randn(g, E, H).to(torch.bfloat16)
+    ws, r = moe.alloc_op_workspace(dev), moe.router_problem(T, H, E)
+    want, got = torch.zeros((T, E), device=dev), torch.zeros((T, E), device=dev)
+    moe.router_logits(r, x.to(dev), w.to(dev), want, ws)
+    moe.router_logits(r, far(x, 2 ** 31 // (T - 1) + 8, dev), far(w, 2 ** 30 + 8, dev), got, ws)
+    assert moe.get_device_error(ws) == 0 and torch.equal(got, want)
+
+
+@gpu
 @pytest.mark.parametrize("T", [1, 40])
 def test_router_nan_stays_in_its_token(dev, T):
     g = gen(9)
@@ -395,6 +453,25 @@ def test_gemm_sizes(dev, M, N, K):
 def test_gemm_types_strides_and_accumulation(dev, out, M, N, K, pad):
     run_gemm(dev, M, N, K, out, pad)
     run_gemm(dev, M, N, K, out, pad, accumulate=True)
+
+
+@gpu
+@pytest.mark.parametrize("M,N,K", [(8, 40, 16384), (3, 130, 30000), (1, 20, 65552), (5, 4900, 400), (8, 9000, 272)])
+def test_gemm_few_rows_long_sums_and_many_columns(dev, M, N, K):
+    run_gemm(dev, M, N, K, "f32")
+
+
+@gpu
+@pytest.mark.parametrize("M", [3, 20])
+def test_gemm_offsets_past_32_bits(dev, M):
+    N, K = 40, 272
+    far_apart, far_w = (2 ** 31 // (n - 1) // 16 * 16 + 16 for n in (M, N))
+    a, sa, w, sw = [t.to(dev) for t in product_inputs(M, N, K, M)]
+    ws, p = moe.alloc_op_workspace(dev), moe.fp8_gemm_problem(M, N, K, out_dtype="f32")
+    want, got = torch.zeros((M, N), device=dev), far(torch.zeros(M, N), far_apart, dev)
+    moe.gemm_fp8_block(p, a, sa, w, sw, want, ws)
+    moe.gemm_fp8_block(p, far(a, far_apart, dev), far(sa, far_apart, dev), far(w, far_w, dev), sw, got, ws)
+    assert moe.get_device_error(ws) == 0 and torch.equal(got, want)
 
 
 @gpu
@@ -673,3 +750,36 @@ def test_block_of_wide_rows(dev, max_tokens, T):
     # moe_forward rounds the activations and each expert's output to bf16
     err = float((out.cpu().double() - want).norm() / want.norm())
     assert err <= 1e-2, err
+
+
+@gpu
+@pytest.mark.parametrize("T", [3, 20])
+def test_block_in_a_graph_and_on_another_stream(dev, T):
+    H, I, E, k = 512, 256, 16, 4
+    g = gen(T)
+    rand = lambda *s: torch.rand(s, generator=g)  # noqa: E731
+    w = few_weights(moe.problem(T, H, I, E, k, wdtype="int8"), False, 7)
+    wd = moe.Weights(*[None if t is None else t.to(dev) for t in w])
+    sh = (codes_of(g, 2 * I, H), rand(2 * I // 128, H // 128) * 4e-4, codes_of(g, H, I), rand(H // 128, I // 128) * 4e-4)
+    block = moe.MoEBlock(H, I, E, k, wd, torch.ones(H, dtype=torch.bfloat16, device=dev),
+                         (0.05 * randn(g, E, H)).to(torch.bfloat16).to(dev), moe.SharedExpert(*[t.to(dev) for t in sh]), 64,
+                         dev, wdtype="int8")
+    x, r = randn(g, T, H).to(torch.bfloat16).to(dev), randn(g, T, H).to(torch.bfloat16).to(dev)
+    block(x, r)
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out, total = block(x, r)
+    for seed in (1, 2, 3):
+        x.copy_(randn(gen(seed), T, H).to(torch.bfloat16))
+        torch.cuda.synchronize()
+        want, sums = block(x, r)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(total, sums)
+    with torch.cuda.stream(side):
+        again, sums = block(x, r)
+    side.synchronize()
+    assert torch.equal(again, want) and torch.equal(sums, total)
+    assert block.device_error() == 0
