@@ -43,12 +43,13 @@ constexpr int kMiscBytes = 4096;        // barriers, flags and the row maxima
 // weight-scale rows.
 constexpr uint32_t kScaleSlots = 4, kScaleSlotBytes = 2 * 4 * 128 * 4;
 // Transposition of the stored sums: per joining warp 32 rows of 16 floats, rows
-// 80 bytes apart (eight lanes' 16-byte stores fall into different banks).
-constexpr int kStageRow = 80, kStageBytes = 32 * kStageRow;
-template <int KIND, bool SWIGLU>
-__host__ __device__ constexpr int fixed_bytes() {
-  return kMiscBytes + (KIND == 0 ? static_cast<int>(kScaleSlots * kScaleSlotBytes) : 0) +
-         (SWIGLU ? 0 : kJoinWarps * kStageBytes);
+// 80 bytes apart (eight lanes' 16-byte stores fall into different banks); of
+// 256-column tiles that TMA stores, two boxes of 32 rows by 64 bytes.
+constexpr int kStageRow = 80, kBoxBytes = 32 * 64;
+__host__ __device__ constexpr int out_stage_bytes(int bn) { return bn == 256 ? 2 * kBoxBytes : 32 * kStageRow; }
+__host__ __device__ constexpr int fixed_bytes(int kind, bool swiglu, int bn) {
+  return kMiscBytes + (kind == 0 ? static_cast<int>(kScaleSlots * kScaleSlotBytes) : 0) +
+         (swiglu ? 0 : kJoinWarps * out_stage_bytes(bn));
 }
 constexpr int kTileABytes = 128 * 128;  // what an MMA reads of A: 128 rows of a k-block
 
@@ -72,11 +73,12 @@ struct Params {
   int out_dtype;         // moe_dtype_t
   int accumulate;
   int vec;               // out rows take 16-byte stores
+  int tma_out;           // 256-column tiles are stored by TMA
   int vec_scale;         // rows of a_scale take 16-byte loads at multiples of four blocks
 };
 
 struct Maps {
-  CUtensorMap a, w;
+  CUtensorMap a, w, out;
 };
 
 __host__ __device__ constexpr int wrows(int bn, bool pair) { return pair ? 128 : (bn < 128 ? bn : 128); }
@@ -135,8 +137,20 @@ __device__ __forceinline__ float4 lds_f4(uint32_t a) {
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ void sts_u4(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 __device__ __forceinline__ void sts_f4(uint32_t a, float4 v) {
   asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+
+// A box of shared memory to `map` at (x, y); rows and columns past the tensor's
+// are left out.
+__device__ __forceinline__ void tma_store_box(const void* map, uint32_t src, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y), "r"(src)
+      : "memory");
 }
 
 // acc += d * s, two floats at a time
@@ -369,8 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
   // barriers first, then the ring
   const uint32_t bars = base_u32;
   const uint32_t ring0 = base_u32 + kMiscBytes;  // scale products
-  const uint32_t ring = base_u32 + fixed_bytes<KIND, SWIGLU>();
-  const uint32_t stage0 = ring - kJoinWarps * kStageBytes;
+  const uint32_t ring = base_u32 + fixed_bytes(KIND, SWIGLU, BN);
+  const uint32_t stage0 = ring - kJoinWarps * out_stage_bytes(BN);
 #define FULL(s) (bars + 8u * static_cast<uint32_t>(s))
 #define EMPTY(s) (bars + 8u * static_cast<uint32_t>(kMaxStages + (s)))
 #define SFULL(s) (bars + 16u * kMaxStages + 80u + 8u * (s))
@@ -402,6 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     fence_mbar_init();
     tma_prefetch_desc(&maps.a);
     tma_prefetch_desc(&maps.w);
+    if (p.tma_out) tma_prefetch_desc(&maps.out);
   }
   if (warp == 1) {
     if (PAIR) {
@@ -669,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
         // partial sums into this CTA's shared memory (the ring is drained: the
         // last accumulator was finished by the last MMA that read it)
         if (row < p.M) {
-          float* dst = reinterpret_cast<float*>(base + fixed_bytes<KIND, SWIGLU>()) + (32 * quarter + lane) * part_ld(BN);
+          float* dst = reinterpret_cast<float*>(base + fixed_bytes(KIND, SWIGLU, BN)) + (32 * quarter + lane) * part_ld(BN);
 #pragma unroll
           for (int c = 0; c < NCH; ++c) {
             const int col = SWIGLU ? 64 * half + (c & 1) * 32 + (c >> 1) * 128 : W * half + CH * c;
@@ -714,14 +729,59 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
                                 codes4(v[16 * j + 8], v[16 * j + 9], v[16 * j + 10], v[16 * j + 11], scale),
                                 codes4(v[16 * j + 12], v[16 * j + 13], v[16 * j + 14], v[16 * j + 15], scale));
         }
+      } else if (BN == 256 && p.tma_out) {
+        // 64 bytes of a row at a time: boxes in shared memory (16-byte pieces swizzled
+        // so that eight lanes' stores fall into different banks), which TMA
+        // writes while the next box is filled and the next tile's blocks are joined
+        // (M = 4096, N = 7168, K = 2048, bf16: 51.5 us; plain stores of the tile 61.6)
+        if (live) {
+          const uint32_t boxes = stage0 + static_cast<uint32_t>(4 * half + quarter) * out_stage_bytes(BN);
+          auto box = [&](int i, int x, auto&& piece) {  // piece(j): 16 bytes
+            const uint32_t dst = boxes + static_cast<uint32_t>(i & 1) * kBoxBytes;
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the last one but one is read
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              sts_u4(dst + static_cast<uint32_t>(lane * 64 + 16 * (j ^ (lane >> 1 & 3))), piece(j));
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+              if (n0 + W * half + x < p.N) tma_store_box(&maps.out, dst, n0 + W * half + x, m0 + 32 * quarter);
+              asm volatile("cp.async.bulk.commit_group;" ::: "memory");  // (a group for every box)
+            }
+          };
+          if (p.out_dtype == 2) {
+#pragma unroll
+            for (int i = 0; i < W / 16; ++i)
+              box(i, 16 * i, [&](int j) {
+                const uint64_t u = acc[8 * i + 2 * j], v = acc[8 * i + 2 * j + 1];
+                return make_uint4(static_cast<uint32_t>(u), static_cast<uint32_t>(u >> 32), static_cast<uint32_t>(v),
+                                  static_cast<uint32_t>(v >> 32));
+              });
+          } else {
+            const bool f16 = p.out_dtype == 1;
+            auto two = [&](uint64_t a) {
+              const float2 v = unpair(a);
+              const __half2 h = __floats2half2_rn(v.x, v.y);
+              return f16 ? *reinterpret_cast<const uint32_t*>(&h) : pack_bf16x2(v.x, v.y);
+            };
+#pragma unroll
+            for (int i = 0; i < W / 32; ++i)
+              box(i, 32 * i, [&](int j) {
+                const uint64_t* q = acc + 16 * i + 4 * j;
+                return make_uint4(two(q[0]), two(q[1]), two(q[2]), two(q[3]));
+              });
+          }
+        }
       } else {
         // 16 columns at a time through shared memory, so that four lanes write 16
         // adjacent columns of a row: whole 32-byte sectors (one row per lane
         // wrote 8 bytes of 32 rows at a time and took twice the product's time
         // at M = 4096, N = 7168, K = 2048)
-        const uint32_t mine = stage0 + static_cast<uint32_t>(4 * half + quarter) * kStageBytes;
+        const uint32_t mine = stage0 + static_cast<uint32_t>(4 * half + quarter) * out_stage_bytes(BN);
         const int to0 = m0 + 32 * quarter + (lane >> 2), col0 = n0 + W * half + 4 * (lane & 3);
-        const bool fast = p.vec && !p.accumulate && n0 + BN <= p.N;  // a whole tile's columns, aligned stores
+        // a whole tile's columns, aligned stores (of 256-column tiles those are TMA's)
+        const bool fast = BN < 256 && p.vec && !p.accumulate && n0 + BN <= p.N;
         const int64_t at = static_cast<int64_t>(to0) * p.out_stride + col0, eight = 8 * p.out_stride;
 #pragma unroll
         for (int c = 0; c < W / 16; ++c) {
@@ -760,6 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
         }
       }
     }
+    if (BN == 256 && !SWIGLU && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // stored
     __syncwarp();
     if (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLaunchRegs));
     tc_fence_before();
@@ -828,7 +889,7 @@ size_t smem_bytes(const Params& p, int bn, bool pair) {
   // shared memory as by columns, so that no CTA waits for another's
   // columns while its cluster waits for it
   const size_t floor = bn >= 256 ? 120 * 1024 : bn >= 128 ? 80 * 1024 : bn >= 64 ? 48 * 1024 : 0;
-  const size_t need = 1024 + fixed_bytes<KIND, SWIGLU>() + ring;
+  const size_t need = 1024 + fixed_bytes(KIND, SWIGLU, bn) + ring;
   return need > floor ? need : floor;
 }
 
@@ -909,14 +970,24 @@ cudaError_t plan_and_launch(Params p, int bn, bool pair, bool swiglu, const void
   p.nt = (p.N + (swiglu ? 128 : bn) - 1) / (swiglu ? 128 : bn);
   p.arows = pair || p.M >= 128 ? 128 : (p.M + 7) / 8 * 8;
   const int sb = stage_bytes(p.arows, bn, pair);
-  const int fixed = swiglu ? fixed_bytes<KIND, true>() : fixed_bytes<KIND, false>();
+  const int fixed = fixed_bytes(KIND, swiglu, bn);
   const size_t room = kMaxSmem - 1024 - fixed - (kTileABytes - p.arows * 128);
   const int per_cta = pair ? p.KB : (p.KB + p.P - 1) / p.P;
   const int most = static_cast<int>(room / sb);
   p.stages = most < kMaxStages ? most : kMaxStages;
   // a K-splitting CTA has one tile: no more stages than k-blocks
   if (p.P > 1 && p.stages > per_cta) p.stages = per_cta;
-  Maps maps;
+  Maps maps = {};
+  p.tma_out = bn == 256 && !swiglu && p.P == 1 && p.vec && !p.accumulate;
+  if (p.tma_out) {
+    const uint64_t osz = p.out_dtype == 2 ? 4 : 2;
+    const uint64_t dims[2] = {static_cast<uint64_t>(p.N), static_cast<uint64_t>(p.M)};
+    const uint64_t str[1] = {static_cast<uint64_t>(p.out_stride) * osz};
+    const uint32_t box[2] = {static_cast<uint32_t>(64 / osz), 32};
+    if (!encode_map(&maps.out, osz == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.out,
+                    dims, str, box, CU_TENSOR_MAP_SWIZZLE_64B))
+      return cudaErrorInvalidValue;
+  }
   {
     const uint64_t dims[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(p.M)};
     const uint64_t str[1] = {static_cast<uint64_t>(a_stride) * esz};

@@ -456,6 +456,15 @@ def test_gemm_types_strides_and_accumulation(dev, out, M, N, K, pad):
 
 
 @gpu
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("M,N,K,pad", [(1030, 5000, 144, 16), (2049, 4360, 272, 0), (131, 40000, 144, 8), (100, 40008, 144, 8)])
+def test_gemm_wide_tiles(dev, out, M, N, K, pad):
+    """Tiles of 256 columns, whole and cut, several per CTA: stored as rows of 16-byte pieces where the strides allow it."""
+    run_gemm(dev, M, N, K, out, 2 * pad)
+    run_gemm(dev, M, N, K, out, 2 * pad + 16, accumulate=True)
+
+
+@gpu
 @pytest.mark.parametrize("M,N,K", [(8, 40, 16384), (3, 130, 30000), (1, 20, 65552), (5, 4900, 400), (8, 9000, 272)])
 def test_gemm_few_rows_long_sums_and_many_columns(dev, M, N, K):
     run_gemm(dev, M, N, K, "f32")
