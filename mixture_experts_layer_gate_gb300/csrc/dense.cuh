@@ -44,12 +44,16 @@ constexpr int kMiscBytes = 4096;        // barriers, flags and the row maxima
 constexpr uint32_t kScaleSlots = 4, kScaleSlotBytes = 2 * 4 * 128 * 4;
 // Transposition of the stored sums: per joining warp 32 rows of 16 floats, rows
 // 80 bytes apart (eight lanes' 16-byte stores fall into different banks); of
-// 256-column tiles that TMA stores, two boxes of 32 rows by 64 bytes.
-constexpr int kStageRow = 80, kBoxBytes = 32 * 64;
-__host__ __device__ constexpr int out_stage_bytes(int bn) { return bn == 256 ? 2 * kBoxBytes : 32 * kStageRow; }
-__host__ __device__ constexpr int fixed_bytes(int kind, bool swiglu, int bn) {
+// 256-column tiles that TMA stores, two boxes of 32 rows by 64 bytes, or four
+// where it also fetches what the sums are added to and the ring keeps its stages
+// (CTA pairs).
+constexpr int kStageRow = 80, kBoxBytes = 32 * 64, kMaxBoxes = 4;
+__host__ __device__ constexpr int out_stage_bytes(int bn, int boxes) {
+  return bn == 256 ? boxes * kBoxBytes : 32 * kStageRow;
+}
+__host__ __device__ constexpr int fixed_bytes(int kind, bool swiglu, int bn, int boxes) {
   return kMiscBytes + (kind == 0 ? static_cast<int>(kScaleSlots * kScaleSlotBytes) : 0) +
-         (swiglu ? 0 : kJoinWarps * out_stage_bytes(bn));
+         (swiglu ? 0 : kJoinWarps * out_stage_bytes(bn, boxes));
 }
 constexpr int kTileABytes = 128 * 128;  // what an MMA reads of A: 128 rows of a k-block
 
@@ -74,6 +78,7 @@ struct Params {
   int accumulate;
   int vec;               // out rows take 16-byte stores
   int tma_out;           // 256-column tiles are stored by TMA
+  int boxes;             // of each joining warp, for that: 2 or 4
   int vec_scale;         // rows of a_scale take 16-byte loads at multiples of four blocks
 };
 
@@ -137,6 +142,12 @@ __device__ __forceinline__ float4 lds_f4(uint32_t a) {
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ uint4 lds_u4(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ void sts_u4(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -366,10 +377,14 @@ __device__ __forceinline__ void load_box(uint32_t leader, uint32_t dst, const vo
 #undef MOE_DENSE_LOAD
 }
 
-template <int KIND, bool SWIGLU, bool PAIR, int BN>
+// ADD: 256-column tiles that are added to what out holds (a kernel of its own: what
+// fetches the old values costs the storing one 51 -> 57 us at M = 4096, N = 7168,
+// K = 2048); of narrower tiles p.accumulate tells.
+template <int KIND, bool SWIGLU, bool PAIR, int BN, bool ADD>
 __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constant__ Maps maps, const Params p) {
   static_assert(!SWIGLU || BN == 256, "gate and up halves of 128 columns");
   static_assert(!PAIR || BN == 256, "a pair's halves are 128 weight rows");
+  static_assert(!ADD || (BN == 256 && !SWIGLU), "narrower tiles add at run time");
   constexpr int W = BN / 2;              // columns per joining warp
   constexpr int CH = W < 32 ? W : 32;    // columns per tensor-memory load
   constexpr int NCH = W / CH;
@@ -383,11 +398,12 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
   // barriers first, then the ring
   const uint32_t bars = base_u32;
   const uint32_t ring0 = base_u32 + kMiscBytes;  // scale products
-  const uint32_t ring = base_u32 + fixed_bytes(KIND, SWIGLU, BN);
-  const uint32_t stage0 = ring - kJoinWarps * out_stage_bytes(BN);
+  const uint32_t ring = base_u32 + fixed_bytes(KIND, SWIGLU, BN, p.boxes);
+  const uint32_t stage0 = ring - kJoinWarps * out_stage_bytes(BN, p.boxes);
 #define FULL(s) (bars + 8u * static_cast<uint32_t>(s))
 #define EMPTY(s) (bars + 8u * static_cast<uint32_t>(kMaxStages + (s)))
 #define SFULL(s) (bars + 16u * kMaxStages + 80u + 8u * (s))
+#define BOX(s) (bars + 512u + 8u * (static_cast<uint32_t>(warp - kFirstJoin) * kMaxBoxes + (s)))
 #define SEMPTY(s) (bars + 16u * kMaxStages + 80u + 8u * (kScaleSlots + (s)))
   const uint32_t dfull = bars + 16u * kMaxStages, dempty = dfull + 16u, drain = dfull + 32u;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(base + 16 * kMaxStages + 40);
@@ -412,6 +428,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
       mbar_init(SFULL(q), 1u);
       mbar_init(SEMPTY(q), kJoinWarps);
     }
+    if (ADD)
+      for (uint32_t q = 0; q < kJoinWarps * kMaxBoxes; ++q) mbar_init(bars + 512u + 8u * q, 1u);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&maps.a);
@@ -601,10 +619,25 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     const uint32_t lane_base = static_cast<uint32_t>(32 * quarter) << 16;
     const uint32_t dempty_to = PAIR ? map_to_rank(dempty, 0) : dempty;
     uint32_t buf = 0, dph = 0, tile = 0, quad = 0;
+    // boxes that TMA fetches: the parity of each one's next arrival, and those on their way
+    uint32_t box_phase = 0, box_loads = 0;
+    const bool fetch = ADD && p.tma_out;
+    const uint32_t boxes0 = stage0 + static_cast<uint32_t>(warp - kFirstJoin) * out_stage_bytes(BN, p.boxes);
+    const int box_cols = p.out_dtype == 2 ? 16 : 32;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
       const int m0 = (t % p.mt) * kTileM + (PAIR ? 128 * static_cast<int>(rank) : 0);
       const int n0 = (t / p.mt) * (SWIGLU ? 128 : BN);
+      // what chunk i of the warp's columns is added to, into its box; the box's
+      // last store has read it
+      auto fetch_box = [&](int i) {
+        const uint32_t slot = static_cast<uint32_t>(i & (p.boxes - 1));
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        expect_tx(lane == 0, BOX(slot), kBoxBytes);
+        load_box<false>(lane == 0, boxes0 + slot * kBoxBytes, &maps.out, BOX(slot), n0 + W * half + i * box_cols,
+                        m0 + 32 * quarter);
+        box_loads |= 1u << slot;
+      };
       const int row = m0 + 32 * quarter + lane;
       const bool live = m0 + 32 * quarter < p.M;  // some row of this warp exists
       // columns of load c: SwiGLU takes 64 gate columns, then the 64 up columns
@@ -612,6 +645,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
       auto column_of = [&](int c) {
         return static_cast<uint32_t>(SWIGLU ? 64 * half + (c & 1) * 32 + (c >> 1) * 128 : W * half + CH * c);
       };
+      if (fetch && live)
+        for (int i = 0; i < p.boxes; ++i) fetch_box(i);
       uint64_t acc[W / 2];
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) acc[i] = 0;
@@ -684,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
         // partial sums into this CTA's shared memory (the ring is drained: the
         // last accumulator was finished by the last MMA that read it)
         if (row < p.M) {
-          float* dst = reinterpret_cast<float*>(base + fixed_bytes(KIND, SWIGLU, BN)) + (32 * quarter + lane) * part_ld(BN);
+          float* dst = reinterpret_cast<float*>(base + fixed_bytes(KIND, SWIGLU, BN, p.boxes)) + (32 * quarter + lane) * part_ld(BN);
 #pragma unroll
           for (int c = 0; c < NCH; ++c) {
             const int col = SWIGLU ? 64 * half + (c & 1) * 32 + (c >> 1) * 128 : W * half + CH * c;
@@ -732,53 +767,72 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
       } else if (BN == 256 && p.tma_out) {
         // 64 bytes of a row at a time: boxes in shared memory (16-byte pieces swizzled
         // so that eight lanes' stores fall into different banks), which TMA
-        // writes while the next box is filled and the next tile's blocks are joined
-        // (M = 4096, N = 7168, K = 2048, bf16: 51.5 us; plain stores of the tile 61.6)
+        // writes while the next box is filled and the next tile's blocks are joined.
+        // What the sums are added to is there by then (fetch_box).  M = 4096, N =
+        // 7168, K = 2048, bf16: 51 us, added 62; plain stores of the tile 62 and 130.
         if (live) {
-          const uint32_t boxes = stage0 + static_cast<uint32_t>(4 * half + quarter) * out_stage_bytes(BN);
-          auto box = [&](int i, int x, auto&& piece) {  // piece(j): 16 bytes
-            const uint32_t dst = boxes + static_cast<uint32_t>(i & 1) * kBoxBytes;
-            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the last one but one is read
-            __syncwarp();
+          auto box = [&](int i, auto&& piece) {  // piece(j, old): 16 bytes
+            const uint32_t slot = static_cast<uint32_t>(i & (p.boxes - 1));
+            const uint32_t dst = boxes0 + slot * kBoxBytes, mine = dst + static_cast<uint32_t>(lane * 64);
+            if (fetch) {
+              ok = ok && wait(BOX(slot), box_phase >> slot & 1u, abort_flag, p.err, 0x680u);
+              if (!ok) return;
+              box_phase ^= 1u << slot;
+              box_loads &= ~(1u << slot);
+            } else {
+              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the last one but one is read
+              __syncwarp();
+            }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              sts_u4(dst + static_cast<uint32_t>(lane * 64 + 16 * (j ^ (lane >> 1 & 3))), piece(j));
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t at = mine + static_cast<uint32_t>(16 * (j ^ (lane >> 1 & 3)));
+              sts_u4(at, piece(j, fetch ? lds_u4(at) : make_uint4(0u, 0u, 0u, 0u)));
+            }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
+            const int x = n0 + W * half + i * box_cols;
             if (lane == 0) {
-              if (n0 + W * half + x < p.N) tma_store_box(&maps.out, dst, n0 + W * half + x, m0 + 32 * quarter);
+              if (x < p.N) tma_store_box(&maps.out, dst, x, m0 + 32 * quarter);
               asm volatile("cp.async.bulk.commit_group;" ::: "memory");  // (a group for every box)
             }
+            if (fetch && (i + p.boxes) * box_cols < W) fetch_box(i + p.boxes);
           };
           if (p.out_dtype == 2) {
 #pragma unroll
             for (int i = 0; i < W / 16; ++i)
-              box(i, 16 * i, [&](int j) {
-                const uint64_t u = acc[8 * i + 2 * j], v = acc[8 * i + 2 * j + 1];
-                return make_uint4(static_cast<uint32_t>(u), static_cast<uint32_t>(u >> 32), static_cast<uint32_t>(v),
-                                  static_cast<uint32_t>(v >> 32));
+              box(i, [&](int j, uint4 old) {
+                const float2 u = unpair(acc[8 * i + 2 * j]), v = unpair(acc[8 * i + 2 * j + 1]);
+                if (!ADD) return make_uint4(__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(v.x), __float_as_uint(v.y));
+                return make_uint4(__float_as_uint(u.x + __uint_as_float(old.x)), __float_as_uint(u.y + __uint_as_float(old.y)),
+                                  __float_as_uint(v.x + __uint_as_float(old.z)), __float_as_uint(v.y + __uint_as_float(old.w)));
               });
           } else {
             const bool f16 = p.out_dtype == 1;
-            auto two = [&](uint64_t a) {
-              const float2 v = unpair(a);
+            auto two = [&](uint64_t a, uint32_t old) {
+              float2 v = unpair(a);
+              if (ADD) {
+                const float2 o = f16 ? __half22float2(*reinterpret_cast<const __half2*>(&old))
+                                     : make_float2(bf16_lo(old), bf16_hi(old));
+                v = make_float2(v.x + o.x, v.y + o.y);
+              }
               const __half2 h = __floats2half2_rn(v.x, v.y);
               return f16 ? *reinterpret_cast<const uint32_t*>(&h) : pack_bf16x2(v.x, v.y);
             };
 #pragma unroll
             for (int i = 0; i < W / 32; ++i)
-              box(i, 32 * i, [&](int j) {
+              box(i, [&](int j, uint4 old) {
                 const uint64_t* q = acc + 16 * i + 4 * j;
-                return make_uint4(two(q[0]), two(q[1]), two(q[2]), two(q[3]));
+                return make_uint4(two(q[0], old.x), two(q[1], old.y), two(q[2], old.z), two(q[3], old.w));
               });
           }
         }
+        if (!ok) break;
       } else {
         // 16 columns at a time through shared memory, so that four lanes write 16
         // adjacent columns of a row: whole 32-byte sectors (one row per lane
         // wrote 8 bytes of 32 rows at a time and took twice the product's time
         // at M = 4096, N = 7168, K = 2048)
-        const uint32_t mine = stage0 + static_cast<uint32_t>(4 * half + quarter) * out_stage_bytes(BN);
+        const uint32_t mine = stage0 + static_cast<uint32_t>(4 * half + quarter) * out_stage_bytes(BN, p.boxes);
         const int to0 = m0 + 32 * quarter + (lane >> 2), col0 = n0 + W * half + 4 * (lane & 3);
         // a whole tile's columns, aligned stores (of 256-column tiles those are TMA's)
         const bool fast = BN < 256 && p.vec && !p.accumulate && n0 + BN <= p.N;
@@ -820,7 +874,11 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
         }
       }
     }
-    if (BN == 256 && !SWIGLU && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // stored
+    if (BN == 256 && !SWIGLU) {
+      for (uint32_t i = 0; ADD && i < kMaxBoxes; ++i)  // (after an abort only)
+        if (box_loads >> i & 1u) wait(BOX(i), box_phase >> i & 1u, nullptr, p.err, 0x681u);
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // stored
+    }
     __syncwarp();
     if (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLaunchRegs));
     tc_fence_before();
@@ -830,6 +888,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
 #undef EMPTY
 #undef SFULL
 #undef SEMPTY
+#undef BOX
 
   if (PAIR || p.P > 1) cluster_sync_all();  // signals and partial sums have arrived
   if (!PAIR && p.P > 1) {
@@ -889,17 +948,17 @@ size_t smem_bytes(const Params& p, int bn, bool pair) {
   // shared memory as by columns, so that no CTA waits for another's
   // columns while its cluster waits for it
   const size_t floor = bn >= 256 ? 120 * 1024 : bn >= 128 ? 80 * 1024 : bn >= 64 ? 48 * 1024 : 0;
-  const size_t need = 1024 + fixed_bytes(KIND, SWIGLU, bn) + ring;
+  const size_t need = 1024 + fixed_bytes(KIND, SWIGLU, bn, p.boxes) + ring;
   return need > floor ? need : floor;
 }
 
-template <int KIND, bool SWIGLU, bool PAIR, int BN>
+template <int KIND, bool SWIGLU, bool PAIR, int BN, bool ADD = false>
 cudaError_t launch(const Maps& maps, const Params& p, int grid, cudaStream_t s) {
   static int configured[64] = {};
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
-  auto kernel = dense_kernel<KIND, SWIGLU, PAIR, BN>;
+  auto kernel = dense_kernel<KIND, SWIGLU, PAIR, BN, ADD>;
   if (dev < 0 || dev >= 64 || configured[dev] == 0) {
     err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxSmem));
     if (err != cudaSuccess) return err;
@@ -970,7 +1029,9 @@ cudaError_t plan_and_launch(Params p, int bn, bool pair, bool swiglu, const void
   p.nt = (p.N + (swiglu ? 128 : bn) - 1) / (swiglu ? 128 : bn);
   p.arows = pair || p.M >= 128 ? 128 : (p.M + 7) / 8 * 8;
   const int sb = stage_bytes(p.arows, bn, pair);
-  const int fixed = fixed_bytes(KIND, swiglu, bn);
+  p.tma_out = bn == 256 && !swiglu && p.P == 1 && p.vec;
+  p.boxes = p.tma_out && p.accumulate && pair ? kMaxBoxes : 2;
+  const int fixed = fixed_bytes(KIND, swiglu, bn, p.boxes);
   const size_t room = kMaxSmem - 1024 - fixed - (kTileABytes - p.arows * 128);
   const int per_cta = pair ? p.KB : (p.KB + p.P - 1) / p.P;
   const int most = static_cast<int>(room / sb);
@@ -978,7 +1039,6 @@ cudaError_t plan_and_launch(Params p, int bn, bool pair, bool swiglu, const void
   // a K-splitting CTA has one tile: no more stages than k-blocks
   if (p.P > 1 && p.stages > per_cta) p.stages = per_cta;
   Maps maps = {};
-  p.tma_out = bn == 256 && !swiglu && p.P == 1 && p.vec && !p.accumulate;
   if (p.tma_out) {
     const uint64_t osz = p.out_dtype == 2 ? 4 : 2;
     const uint64_t dims[2] = {static_cast<uint64_t>(p.N), static_cast<uint64_t>(p.M)};
@@ -1006,7 +1066,9 @@ cudaError_t plan_and_launch(Params p, int bn, bool pair, bool swiglu, const void
   if (pair) {
     grid = 2 * static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
     if constexpr (KIND == kE4M3) {
-      return swiglu ? launch<KIND, true, true, 256>(maps, p, grid, s) : launch<KIND, false, true, 256>(maps, p, grid, s);
+      if (swiglu) return launch<KIND, true, true, 256>(maps, p, grid, s);
+      return p.accumulate ? launch<KIND, false, true, 256, true>(maps, p, grid, s)
+                          : launch<KIND, false, true, 256>(maps, p, grid, s);
     } else {
       return cudaErrorInvalidValue;  // (choose() pairs CTAs for 8-bit operands only)
     }
@@ -1015,6 +1077,7 @@ cudaError_t plan_and_launch(Params p, int bn, bool pair, bool swiglu, const void
   else grid = static_cast<int>(tiles < sms ? tiles : sms);
   if constexpr (KIND == kE4M3) {
     if (swiglu) return launch<KIND, true, false, 256>(maps, p, grid, s);
+    if (bn == 256 && p.accumulate) return launch<KIND, false, false, 256, true>(maps, p, grid, s);
   }
   switch (bn) {
     case 32: return launch<KIND, false, false, 32>(maps, p, grid, s);
