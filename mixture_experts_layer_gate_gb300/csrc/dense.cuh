@@ -171,9 +171,10 @@ __device__ __forceinline__ void fma2(uint64_t& acc, uint32_t d0, uint32_t d1, ui
       : "r"(d0), "r"(d1), "l"(s));
 }
 // The same as two scalar multiply-adds where PACKED is false: the packed form
-// needs its operands in register pairs, which the storing kernels pay for with
-// spills (down projection, M = 4096: 70 us packed, 51.5 us scalar; SwiGLU, which
-// spills in neither form: 109 packed, 118 scalar).
+// needs its operands in register pairs and is the slower one in the storing
+// kernels, with 124 bytes of spills a thread or (16 columns a load) without (down
+// projection, M = 4096: 70 and 60 us packed, 51 us scalar), the faster one with
+// SwiGLU (103 us packed, 107 us scalar).
 template <bool PACKED>
 __device__ __forceinline__ void add2(uint64_t& acc, uint32_t d0, uint32_t d1, uint64_t s) {
   if (PACKED) {

@@ -3,9 +3,9 @@
 // sum_{k in b} a[m, k] w[n, k].  A k-block of the dense kernel is a scale block,
 // so each accumulator is one block's product and is joined to the sums in
 // registers with one multiply-add per value.  Measured in a graph: SwiGLU, M = 4096,
-// K = 7168, N = 2048 105 us = 2.3 PFLOP/s; M = 4096, K = 2048, N = 7168 62 us = 1.95
-// PFLOP/s (bound by the joining warps: a k-block of a CTA pair takes ~800 cycles,
-// its MMAs ~690; and by storing a tile every 16 k-blocks).
+// K = 7168, N = 2048 103 us = 2.3 PFLOP/s; M = 4096, K = 2048, N = 7168 51 us = 2.3
+// PFLOP/s, added to out 62 us (bound by the joining warps, which take ~800 cycles
+// for a k-block of a CTA pair, its MMAs ~690, and by the last round of tiles).
 #include "dense.cuh"
 
 namespace moe {
