@@ -364,28 +364,18 @@ def alloc_op_workspace(device):
     return torch.zeros(OP_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
 
 
-def _rows(t, rows, cols, size, what):
-    """Device pointer and row stride of a [rows, cols] tensor of `size`-byte elements; None stays None."""
-    if t is None:
-        return None, 0
-    if t.shape != (rows, cols) or t.element_size() != size or not t.is_cuda:
-        raise ValueError(f"{what}: a CUDA tensor [{rows}, {cols}] of {size}-byte elements")
-    step, column = t.stride()
-    if column != 1 and cols > 1:
-        raise ValueError(f"{what}: adjacent columns")
-    return t.data_ptr(), step if rows > 1 else cols
+_ops = None
 
 
-def _flat(t, n, size, what):
-    """Device pointer of a contiguous tensor of n elements of `size` bytes; None stays None."""
-    if t is None:
-        return None
-    if t.numel() != n or t.element_size() != size or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what}: a contiguous CUDA tensor of {n} elements of {size} bytes")
-    return t.data_ptr()
-
-
-_SIZE = (2, 2, 4)  # bytes of a moe_dtype_t
+def _native():
+    """The compiled entries of the operators below (csrc/binding.cpp): they check tensors against the problem."""
+    global _ops
+    if _ops is None:
+        load()
+        import torch  # noqa: F401  (its libraries first)
+        from . import _ops as module
+        _ops = module
+    return _ops
 
 
 def add_rms_norm(n: NormProblem, x, weight, residual=None, residual_out=None, y=None, codes=None, scales=None,
@@ -393,50 +383,25 @@ def add_rms_norm(n: NormProblem, x, weight, residual=None, residual_out=None, y=
     """moe_add_rms_norm.  x, residual, residual_out, y: [T, H] of n's dtype (rows may be strided; residual_out may
     be residual); weight [H]; codes [T, H] (uint8 or float8_e4m3fn) and scales (float32, [T, ceil(H / 128)] or
     [T]) exactly where n quantises."""
-    T, H, b = n.T, n.H, _SIZE[n.dtype]
-    px, sx = _rows(x, T, H, b, "x")
-    pr, sr = _rows(residual, T, H, b, "residual")
-    po, so = _rows(residual_out, T, H, b, "residual_out")
-    py, sy = _rows(y, T, H, b, "y")
-    _check(load().moe_add_rms_norm(
-        ctypes.byref(n), px, sx, pr, sr, _flat(weight, H, _SIZE[n.weight_dtype], "weight"), po, so, py, sy,
-        _flat(codes, T * H, 1, "codes"), _flat(scales, T * (-(-H // 128) if n.quant == 1 else 1), 4, "scales"),
-        _stream(stream)), "moe_add_rms_norm")
+    _check((_ops or _native()).add_rms_norm(n, x, weight, residual, residual_out, y, codes, scales, stream),
+           "moe_add_rms_norm")
 
 
 def router_logits(r: RouterProblem, x, w, logits, ws, stream=None):
     """moe_router_logits: x [T, H] and w [E, H] (rows may be strided) -> logits float32 [T, E]."""
-    px, sx = _rows(x, r.T, r.H, 2, "x")
-    pw, sw = _rows(w, r.E, r.H, 2, "w")
-    _check(load().moe_router_logits(ctypes.byref(r), px, sx, pw, sw, _flat(logits, r.T * r.E, 4, "logits"),
-                                    ws.data_ptr(), ws.numel(), _stream(stream)), "moe_router_logits")
+    _check((_ops or _native()).router_logits(r, x, w, logits, ws, stream), "moe_router_logits")
 
 
 def gemm_fp8_block(g: Fp8GemmProblem, a, a_scale, w, w_scale, out, ws, stream=None):
     """moe_gemm_fp8_block: a [M, K], w [N, K] (uint8 or float8_e4m3fn), a_scale [M, ceil(K / 128)] and w_scale
     [ceil(N / 128), ceil(K / 128)] float32 -> out [M, N] of g's out_dtype."""
-    M, N, K = g.M, g.N, g.K
-    kb = -(-K // 128)
-    pa, sa = _rows(a, M, K, 1, "a")
-    ps, ss = _rows(a_scale, M, kb, 4, "a_scale")
-    pw, sw = _rows(w, N, K, 1, "w")
-    po, so = _rows(out, M, N, _SIZE[g.out_dtype], "out")
-    _check(load().moe_gemm_fp8_block(ctypes.byref(g), pa, sa, ps, ss, pw, sw,
-                                     _flat(w_scale, -(-N // 128) * kb, 4, "w_scale"), po, so, ws.data_ptr(),
-                                     ws.numel(), _stream(stream)), "moe_gemm_fp8_block")
+    _check((_ops or _native()).gemm_fp8_block(g, a, a_scale, w, w_scale, out, ws, stream), "moe_gemm_fp8_block")
 
 
 def gemm_fp8_block_swiglu(g: Fp8GemmProblem, a, a_scale, w13, w13_scale, codes, scales, ws, stream=None):
     """moe_gemm_fp8_block_swiglu: a [M, K], w13 [2N, K] with their scales -> codes [M, N], scales [M, N / 128]."""
-    M, N, K = g.M, g.N, g.K
-    kb = -(-K // 128)
-    pa, sa = _rows(a, M, K, 1, "a")
-    ps, ss = _rows(a_scale, M, kb, 4, "a_scale")
-    pw, sw = _rows(w13, 2 * N, K, 1, "w13")
-    _check(load().moe_gemm_fp8_block_swiglu(ctypes.byref(g), pa, sa, ps, ss, pw, sw,
-                                            _flat(w13_scale, -(-2 * N // 128) * kb, 4, "w13_scale"),
-                                            _flat(codes, M * N, 1, "codes"), _flat(scales, M * (N // 128), 4, "scales"),
-                                            ws.data_ptr(), ws.numel(), _stream(stream)), "moe_gemm_fp8_block_swiglu")
+    _check((_ops or _native()).gemm_fp8_block_swiglu(g, a, a_scale, w13, w13_scale, codes, scales, ws, stream),
+           "moe_gemm_fp8_block_swiglu")
 
 
 def few_workspace_size(p: Problem) -> int:

@@ -2,7 +2,9 @@
 
 Each .cu file is compiled in its own nvcc process (in parallel), then linked
 into one shared library with the CUDA runtime linked statically, so the library
-loads on a machine without a GPU (calls then fail with MOE_ERR_CUDA).
+loads on a machine without a GPU (calls then fail with MOE_ERR_CUDA).  Beside it,
+_ops.so: the Python entries of the operators around the layer, against the
+installed PyTorch's headers.
 """
 from __future__ import annotations
 
@@ -18,6 +20,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
 SOURCES = ["gemm.cu", "api.cu", "gate.cu", "align.cu", "route.cu", "reduce.cu", "noalloc.cu", "scale.cu",
            "repack.cu", "ops_api.cu", "norm.cu", "router.cu", "fp8_block.cu", "fp8_few.cu", "few.cu"]
+OPS = os.path.join(PKG, "_ops.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -37,6 +40,24 @@ def _stale(obj: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _ops_command(obj: str) -> list[str]:
+    import sysconfig
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    include = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[f"-isystem{i}" for i in include], "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+
+
+def _link_ops(obj: str) -> list[str]:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ["g++", "-shared", "-o", OPS, obj, LIB, "-Wl,-rpath,$ORIGIN", "-L" + lib, "-ltorch_python", "-ltorch_cpu",
+            "-lc10_cuda", "-lc10"]
+
+
 def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -52,6 +73,12 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
             if verbose:
                 print(" ".join(cmd), flush=True)
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    ops_obj = os.path.join(BUILD, "binding.o")
+    if _stale(ops_obj, [os.path.join(CSRC, "binding.cpp"), headers[-1]]):
+        cmd = _ops_command(ops_obj)
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        procs.append(("binding.cpp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for src, pr in procs:
         out, _ = pr.communicate()
@@ -62,9 +89,14 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
             print(text, flush=True)
     if failed:
         msg = "\n".join(f"--- {s}\n{t}" for s, t in failed)
-        raise RuntimeError(f"nvcc failed:\n{msg}")
-    if _stale(LIB, objs):
-        cmd = [cc, *ARCH, "-shared", "-o", LIB, *objs, "-cudart", "static"]
+        raise RuntimeError(f"compilation failed:\n{msg}")
+    links = [(LIB, objs, lambda: [cc, *ARCH, "-shared", "-Xlinker", "-soname=libmoe_gb300.so", "-o", LIB, *objs, "-cudart",
+                                  "static"]),
+             (OPS, [ops_obj, LIB], lambda: _link_ops(ops_obj))]
+    for target, deps, command in links:
+        if not _stale(target, deps):
+            continue
+        cmd = command()
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)

@@ -187,6 +187,48 @@ def test_binding_refuses_tensors_that_are_not_what_the_problem_says():
         moe.router_logits(moe.router_problem(4, 256, 8), x, x, x, x)
 
 
+def test_binding_refuses_what_is_no_tensor_or_problem():
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    n = moe.norm_problem(4, 256)
+    with pytest.raises(TypeError):
+        moe.add_rms_norm(n, [1.0], x)
+    with pytest.raises((TypeError, BufferError)):
+        moe.add_rms_norm(None, x, x)
+    with pytest.raises(ValueError):
+        moe.add_rms_norm(moe.router_problem(4, 256, 8), x, x)
+    with pytest.raises(TypeError):
+        moe.router_logits(moe.router_problem(0, 256, 0), None, None, None, None)
+
+
+@gpu
+def test_binding_refuses_shapes_types_and_strides(dev):
+    n = moe.norm_problem(4, 256, quant="block")
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device=dev)  # noqa: E731
+    x, w = bf(4, 256), bf(256)
+    codes, scales = torch.zeros(4, 256, dtype=torch.uint8, device=dev), torch.zeros(4, 2, device=dev)
+    moe.add_rms_norm(n, x, w, codes=codes, scales=scales)
+    for bad in (dict(x=bf(4, 255)), dict(x=bf(5, 256)), dict(x=bf(4 * 256)), dict(x=x.float()), dict(x=bf(256, 4).T),
+                dict(x=x.cpu()), dict(weight=bf(255)), dict(weight=bf(512)[::2]), dict(codes=codes[:3]),
+                dict(scales=scales.half()), dict(residual=bf(3, 256)), dict(y=bf(4, 8))):
+        args = dict(dict(x=x, weight=w, codes=codes, scales=scales), **bad)
+        with pytest.raises(ValueError):
+            moe.add_rms_norm(n, **args)
+    with pytest.raises(moe.MoEError):
+        moe.add_rms_norm(n, x, w, y=x.clone())   # quantises, but has nowhere to put the codes
+    ws = moe.alloc_op_workspace(dev)
+    logits = torch.zeros(4, 8, device=dev)
+    with pytest.raises(ValueError):
+        moe.router_logits(moe.router_problem(4, 256, 8), x, bf(7, 256), logits, ws)
+    with pytest.raises(ValueError):
+        moe.router_logits(moe.router_problem(4, 256, 8), x, bf(8, 256), logits, ws.cpu())
+    with pytest.raises(moe.MoEError):
+        moe.router_logits(moe.router_problem(4, 256, 8), x, bf(8, 256), logits, ws[:128])
+    stream = torch.cuda.current_stream().cuda_stream
+    moe.router_logits(moe.router_problem(4, 256, 8), x, bf(8, 256), logits, ws, stream)
+    moe.router_logits(moe.router_problem(1, 256, 8), x[:1], bf(8, 256), logits[:1], ws, stream=stream)
+    torch.cuda.synchronize()
+
+
 # ------------------------------------------------------------------ residual + RMS norm
 
 
