@@ -419,9 +419,7 @@ def alloc_few_workspace(p: Problem, device):
 
 def forward_few(p: Problem, w: Weights, x, logits, bias, out, ws, stream=None):
     """moe_forward_few: the whole layer for at most FEW_MAX_TOKENS tokens in two launches."""
-    _check(load().moe_forward_few(ctypes.byref(p), ctypes.byref(w.struct), x.data_ptr(), logits.data_ptr(),
-                                  _ptr(bias), out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)),
-           "moe_forward_few")
+    _check((_ops or _native()).forward_few(p, w.struct, x, logits, bias, out, ws, stream), "moe_forward_few")
 
 
 class MoELayer:

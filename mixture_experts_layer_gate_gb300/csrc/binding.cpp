@@ -70,7 +70,7 @@ struct Workspace {
   }
 };
 
-// A copy of the problem, a ctypes structure.
+// A copy of a ctypes structure: the problem, or pointers to weights.
 template <typename T>
 T problem(PyObject* o) {
   Py_buffer b;
@@ -79,7 +79,7 @@ T problem(PyObject* o) {
   T v{};
   if (fits) v = *static_cast<const T*>(b.buf);
   PyBuffer_Release(&b);
-  if (!fits) refuse("not the problem structure of this call");
+  if (!fits) refuse("not the structure of this call");
   return v;
 }
 
@@ -192,9 +192,27 @@ PyObject* gemm_fp8_block_swiglu(PyObject*, PyObject* const* v, Py_ssize_t n) {
   });
 }
 
+// problem, weights, x, logits, bias, out, ws, stream
+PyObject* forward_few(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return run(n, 8, [&] {
+    const moe_problem_t p = problem<moe_problem_t>(v[0]);
+    const moe_weights_t w = problem<moe_weights_t>(v[1]);
+    const int64_t T = p.T;
+    void* x = flat(v[2], T * p.H, 2, "x");
+    void* logits = flat(v[3], T * p.E, 4, "logits");
+    void* bias = flat(v[4], p.E, 4, "bias");
+    void* out = flat(v[5], T * p.H, 2, "out");
+    const Workspace ws(v[6]);
+    const moe_stream_t s = stream_of(v[7]);
+    return unlocked([&] {
+      return moe_forward_few(&p, &w, x, static_cast<float*>(logits), static_cast<float*>(bias), out, ws.p, ws.bytes, s);
+    });
+  });
+}
+
 #define ENTRY(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(add_rms_norm), ENTRY(router_logits), ENTRY(gemm_fp8_block), ENTRY(gemm_fp8_block_swiglu),
-                         {nullptr, nullptr, 0, nullptr}};
+                         ENTRY(forward_few), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -708,6 +708,24 @@ def test_few_ties_nan_logits_and_zero_tokens(dev):
 
 
 @gpu
+def test_few_binding_refuses_what_does_not_fit(dev):
+    p = moe.problem(2, 256, 128, 8, 2, scoring="sigmoid")
+    w = moe.Weights(*[None if t is None else t.to(dev) for t in few_weights(p, False, 1)])
+    x, logits = torch.zeros(2, 256, dtype=torch.bfloat16, device=dev), torch.zeros(2, 8, device=dev)
+    ws = moe.alloc_few_workspace(p, dev)
+    out = torch.empty_like(x)
+    moe.forward_few(p, w, x, logits, None, out, ws)
+    for bad in (dict(x=x[:1]), dict(x=x.float()), dict(x=x.cpu()), dict(logits=logits[:, :7]), dict(logits=logits.half()),
+                dict(bias=torch.zeros(7, device=dev)), dict(out=torch.zeros(2, 512, dtype=torch.bfloat16, device=dev)[:, ::2])):
+        with pytest.raises(ValueError):
+            moe.forward_few(p, w, **dict(dict(x=x, logits=logits, bias=None, out=out, ws=ws), **bad))
+    with pytest.raises(moe.MoEError):
+        moe.forward_few(p, w, x, logits, None, out, ws[:256])
+    torch.cuda.synchronize()
+    assert moe.get_device_error(ws) == 0
+
+
+@gpu
 def test_few_in_a_graph_and_on_another_stream(dev):
     p = moe.problem(3, 512, 256, 8, 2, wdtype="fp8", act_scale="dynamic")
     w = few_weights(p, False, 3)
