@@ -289,6 +289,14 @@ def test_norm_more_rows_than_ctas(dev, T, H, dtype, wdtype, quant):
 
 
 @gpu
+@pytest.mark.parametrize("T,H,dtype", [(1500, 1032, "bf16"), (1000, 2048, "f32"), (160, 7168, "bf16"), (400, 7168, "f16"),
+                                       (500, 7167, "bf16"), (153, 8192, "bf16")])
+@pytest.mark.parametrize("quant", ["none", "block", "token"])
+def test_norm_rows_that_fit_the_sms_and_more(dev, T, H, dtype, quant):
+    run_norm(dev, T, H, dtype, dtype, quant != "token", quant, 0)
+
+
+@gpu
 def test_norm_offsets_past_32_bits(dev):
     g, H, far_apart = gen(8), 520, 2 ** 30 + 8
     x, r, w = randn(g, 3, H).to(torch.bfloat16), randn(g, 3, H).to(torch.bfloat16), torch.ones(H, dtype=torch.bfloat16)
