@@ -1,16 +1,16 @@
 // Router scores (moe_router_logits): logits[t, e] = sum_h x[t, h] w[e, h], in
 // float.  A batch goes through the dense kernel with 16-bit operands (bound by
 // the reads of x and the tiles' repeated reads through L2: T = 4096, H = 7168,
-// 256 experts 20 us, of which x is 8.6 us of DRAM time).  Up to 4 tokens, where
+// 256 experts 20 us, of which x is 8.6 us of DRAM time).  Up to 8 tokens, where
 // only latency counts, a CTA takes an expert: all of its row is in flight at
 // once, and the threads' sums are joined in a fixed order (T = 1, H = 7168, 256
-// experts: 1.8 us in a graph; 2 and 4 tokens see launch_router).
+// experts: 1.8 us in a graph, 2 tokens 2.0, 4 tokens 2.8, 8 tokens 4.3).
 #include "dense.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kFewTokens = 4;
+constexpr int kFewTokens = 8;
 constexpr int kFewThreads = 128;
 
 template <typename T2>
@@ -24,68 +24,65 @@ __device__ __forceinline__ float2 pair_f32<__half2>(uint32_t v) {
   return __half22float2(*reinterpret_cast<__half2*>(&v));
 }
 
-template <typename T2, int T>
-__global__ void __launch_bounds__(kFewThreads) router_few_kernel(RouterArgs a) {
-  __shared__ float part[kFewThreads / 32][T];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+// Threads kFewThreads t .. take token t; the weight row that they share comes from
+// L2 once a CTA.  At most TMAX tokens: the fewer, the more registers for loads in
+// flight (one token, H = 7168, 256 experts: 1.8 us; as one of eight 2.3 us).
+template <typename T2, int TMAX>
+__global__ void __launch_bounds__(kFewThreads * TMAX) router_few_kernel(RouterArgs a) {
+  __shared__ float part[TMAX][kFewThreads / 32];
+  const int token = threadIdx.x / kFewThreads, tid = threadIdx.x % kFewThreads, warp = tid >> 5, lane = tid & 31;
   const int64_t e = blockIdx.x;
   const uint4* w = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.w) + e * a.w_stride);
+  const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + token * a.x_stride);
   const int nvec = a.H / 8;
   pdl_wait();
   pdl_trigger();
-  float sum[T] = {};
+  float sum = 0.f;
   for (int i0 = tid; i0 < nvec; i0 += 8 * kFewThreads) {
-    uint4 q[8];
+    uint4 q[8], v[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) q[u] = i0 + u * kFewThreads < nvec ? w[i0 + u * kFewThreads] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int t = 0; t < T; ++t) {
-      const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + t * a.x_stride);
-      uint4 v[8];
+    for (int u = 0; u < 8; ++u) v[u] = i0 + u * kFewThreads < nvec ? x[i0 + u * kFewThreads] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = i0 + u * kFewThreads < nvec ? x[i0 + u * kFewThreads] : make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < 8; ++u) {
+      const uint32_t p[4] = {q[u].x, q[u].y, q[u].z, q[u].w}, r[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const uint32_t p[4] = {q[u].x, q[u].y, q[u].z, q[u].w}, r[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = pair_f32<T2>(p[j]), g = pair_f32<T2>(r[j]);
-          sum[t] = fmaf(f.x, g.x, sum[t]);
-          sum[t] = fmaf(f.y, g.y, sum[t]);
-        }
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = pair_f32<T2>(p[j]), g = pair_f32<T2>(r[j]);
+        sum = fmaf(f.x, g.x, sum);
+        sum = fmaf(f.y, g.y, sum);
       }
     }
   }
 #pragma unroll
-  for (int t = 0; t < T; ++t) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum[t] += __shfl_xor_sync(0xffffffffu, sum[t], o);
-    if (lane == 0) part[warp][t] = sum[t];
-  }
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) part[token][warp] = sum;
   __syncthreads();
-  if (tid < T) {
-    float s = part[0][tid];
+  if (tid == 0) {
+    float s = part[token][0];
 #pragma unroll
-    for (int i = 1; i < kFewThreads / 32; ++i) s += part[i][tid];
-    a.logits[static_cast<int64_t>(tid) * a.E + e] = s;
+    for (int i = 1; i < kFewThreads / 32; ++i) s += part[token][i];
+    a.logits[static_cast<int64_t>(token) * a.E + e] = s;
   }
 }
 
 template <typename T2>
 cudaError_t launch_few(const RouterArgs& a, cudaStream_t s) {
-  switch (a.T) {
-    case 1: return launch_pdl(router_few_kernel<T2, 1>, dim3(a.E), dim3(kFewThreads), 0, s, a);
-    case 2: return launch_pdl(router_few_kernel<T2, 2>, dim3(a.E), dim3(kFewThreads), 0, s, a);
-    case 3: return launch_pdl(router_few_kernel<T2, 3>, dim3(a.E), dim3(kFewThreads), 0, s, a);
-    default: return launch_pdl(router_few_kernel<T2, kFewTokens>, dim3(a.E), dim3(kFewThreads), 0, s, a);
-  }
+  const dim3 grid(a.E), block(kFewThreads * a.T);
+  if (a.T == 1) return launch_pdl(router_few_kernel<T2, 1>, grid, block, 0, s, a);
+  if (a.T == 2) return launch_pdl(router_few_kernel<T2, 2>, grid, block, 0, s, a);
+  if (a.T <= 4) return launch_pdl(router_few_kernel<T2, 4>, grid, block, 0, s, a);
+  return launch_pdl(router_few_kernel<T2, kFewTokens>, grid, block, 0, s, a);
 }
 
 }  // namespace
 
 cudaError_t launch_router(const RouterArgs& a, cudaStream_t s) {
-  // the few-token kernel reads the tokens once per expert: T = 1, 2, 4 of 256 experts
-  // 1.8, 2.5, 4.1 us against 5.2 us, but 4 of 1024 experts 7.8 against 6.8
+  // the few-token kernel reads the tokens once per expert, so its time grows with T * E
+  // (few / dense, in a graph): H = 7168, 256 experts, 8 tokens 4.3 / 5.2 us; H = 4096,
+  // 512 experts, 4 tokens 4.1 / 4.8, 5 tokens 5.1 / 4.8; 1024 experts, 2 tokens 4.1 /
+  // 5.4, 4 tokens 6.5 / 5.4; 8 experts, 8 tokens 2.6 / 4.2
   if (a.T <= kFewTokens && a.T * a.E <= 2048) return a.dtype == 0 ? launch_few<__nv_bfloat162>(a, s) : launch_few<__half2>(a, s);
   DeviceInfo di;
   cudaError_t err = device_info(&di);

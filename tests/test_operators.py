@@ -396,7 +396,8 @@ def test_router_most_experts_and_many_tokens(dev):
 
 @gpu
 @pytest.mark.parametrize("T,H,E", [(1, 24, 1024), (2, 2056, 1024), (3, 1032, 683), (3, 1032, 682), (4, 9000, 512),
-                                   (4, 512, 513), (2, 32768, 5), (130, 32768, 40)])
+                                   (4, 512, 513), (2, 32768, 5), (130, 32768, 40), (8, 7168, 256), (8, 1032, 257),
+                                   (5, 4096, 409), (6, 264, 8), (7, 9000, 292), (7, 512, 293)])
 def test_router_few_tokens_and_long_rows(dev, T, H, E):
     g = gen(E)
     x, w = randn(g, T, H).to(torch.float16), (0.02 * randn(g, E, H)).to(torch.float16)
