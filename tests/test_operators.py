@@ -18,8 +18,8 @@ INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
 @pytest.fixture(scope="module")
 def lib():
     import os
-    if not os.path.exists(moe.LIB_PATH):
-        from mixture_experts_layer_gate_gb300 import build
+    from mixture_experts_layer_gate_gb300 import build
+    if not os.path.exists(moe.LIB_PATH) or not os.path.exists(build.OPS):
         build.build()
     return moe.load()
 
@@ -178,7 +178,7 @@ def test_few_refusals(lib):
         moe.alloc_few_workspace(moe.problem(9, 256, 512, 8, 2), "cpu")
 
 
-def test_binding_refuses_tensors_that_are_not_what_the_problem_says():
+def test_binding_refuses_tensors_that_are_not_what_the_problem_says(lib):
     x = torch.zeros(4, 256, dtype=torch.bfloat16)
     w = torch.zeros(256, dtype=torch.bfloat16)
     with pytest.raises(ValueError):  # not on a GPU
@@ -187,7 +187,7 @@ def test_binding_refuses_tensors_that_are_not_what_the_problem_says():
         moe.router_logits(moe.router_problem(4, 256, 8), x, x, x, x)
 
 
-def test_binding_refuses_what_is_no_tensor_or_problem():
+def test_binding_refuses_what_is_no_tensor_or_problem(lib):
     x = torch.zeros(4, 256, dtype=torch.bfloat16)
     n = moe.norm_problem(4, 256)
     with pytest.raises(TypeError):
