@@ -373,7 +373,11 @@ def _native():
     if _ops is None:
         load()
         import torch  # noqa: F401  (its libraries first)
-        from . import _ops as module
+        try:
+            from . import _ops as module
+        except ImportError as e:
+            raise RuntimeError("_ops.so is missing or does not fit this PyTorch: build it first "
+                               "(python -m mixture_experts_layer_gate_gb300.build)") from e
         _ops = module
     return _ops
 

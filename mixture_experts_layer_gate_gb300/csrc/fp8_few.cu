@@ -27,13 +27,14 @@
 namespace moe {
 namespace {
 
-// Warps of a CTA: one CTA an SM with SwiGLU, whose units are few, else two.
+// Warps of a CTA: one CTA an SM with SwiGLU, whose units are few, else two or three.
 template <bool SWIGLU>
 constexpr int kFewWarps = SWIGLU ? 16 : 8;
 constexpr int kStage = 2048 + 32;  // 4 loads of 16 bytes a lane, and two weight scales
 constexpr int kMaxFewDepth = 8;
 template <bool SWIGLU>
 constexpr int kFewSmem = SWIGLU ? 200 * 1024 : 110 * 1024;
+constexpr int kThirdSmem = 73 * 1024;  // of three CTAs an SM
 template <bool SWIGLU>
 constexpr int kRed = kFewWarps<SWIGLU> * (SWIGLU ? 32 : 16) * 8 * 4;  // the warps' sums
 
@@ -219,12 +220,12 @@ int fixed_bytes(const Fp8GemmArgs& p) {
   return kRed<SWIGLU> + (p.K + 127) / 128 * 32 + (p.M * code_stride(p.K) + 127) / 128 * 128;
 }
 template <bool SWIGLU>
-int depth_of(const Fp8GemmArgs& p) {
-  return std::min(kMaxFewDepth, (kFewSmem<SWIGLU> - fixed_bytes<SWIGLU>(p)) / (kFewWarps<SWIGLU> * kStage));
+int depth_of(const Fp8GemmArgs& p, int smem = kFewSmem<SWIGLU>) {
+  return std::min(kMaxFewDepth, (smem - fixed_bytes<SWIGLU>(p)) / (kFewWarps<SWIGLU> * kStage));
 }
 
 template <bool SWIGLU>
-cudaError_t launch(const Fp8GemmArgs& p, int grid, cudaStream_t s) {
+cudaError_t launch(const Fp8GemmArgs& p, int depth, int grid, cudaStream_t s) {
   static int configured[64] = {};
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
@@ -234,7 +235,6 @@ cudaError_t launch(const Fp8GemmArgs& p, int grid, cudaStream_t s) {
     if (err != cudaSuccess) return err;
     if (dev >= 0 && dev < 64) configured[dev] = 1;
   }
-  const int depth = depth_of<SWIGLU>(p);
   const size_t smem = static_cast<size_t>(fixed_bytes<SWIGLU>(p)) + static_cast<size_t>(depth) * kFewWarps<SWIGLU> * kStage;
   return launch_pdl(fp8_few_kernel<SWIGLU>, dim3(grid), dim3(32 * kFewWarps<SWIGLU>), smem, s, p, depth);
 }
@@ -254,8 +254,17 @@ cudaError_t launch_fp8_few(const Fp8GemmArgs& p, cudaStream_t s) {
   DeviceInfo di;
   cudaError_t err = device_info(&di);
   if (err != cudaSuccess) return err;
-  if (p.codes != nullptr) return launch<true>(p, std::min(p.N / 16, di.sms), s);
-  return launch<false>(p, std::min((p.N + 15) / 16, 2 * di.sms), s);
+  if (p.codes != nullptr) return launch<true>(p, depth_of<true>(p), std::min(p.N / 16, di.sms), s);
+  const int units = (p.N + 15) / 16;
+  const int third = depth_of<false>(p, kThirdSmem);
+  // Three CTAs an SM where that takes an SM's units in better balance, or nearly as
+  // good: 3 / 2 CTAs, one row, N x K = 7168 x 2048 (3 / 4 units an SM) 5.2 / 6.1 us,
+  // 14336 x 4096 (6 / 6) 11.9 / 13.1, 16384 x 7168 (9 / 8) 22.9 / 24.0, 9000 x 1104 (6 /
+  // 4) 5.5 / 5.1
+  const int on3 = 3 * ((units + 3 * di.sms - 1) / (3 * di.sms)), on2 = 2 * ((units + 2 * di.sms - 1) / (2 * di.sms));
+  if (units > 2 * di.sms && 4 * on3 <= 5 * on2 && third >= 3)
+    return launch<false>(p, third, std::min(units, 3 * di.sms), s);
+  return launch<false>(p, depth_of<false>(p), std::min(units, 2 * di.sms), s);
 }
 
 }  // namespace moe
