@@ -14,10 +14,10 @@
 // clusters start late and did not all fit with 16 warps a CTA).
 // Else a CTA goes through blocks of 16 rows.
 //
-// One row in a graph: SwiGLU, K = 7168, N = 2048 (29 MB) 9.8 us, 3 TB/s, the
-// general kernel 14; K = 2048, N = 7168 (14.7 MB) 5.2 us, 2.8 TB/s, the general one
-// 6.  Eight rows take 11.0 us with SwiGLU: the stream, not the products, sets the
-// time, and of it the start of the loads and the join at the end are half.
+// In a graph: SwiGLU, K = 7168, N = 2048 (29 MB) one row 9.5 us, 3.1 TB/s, eight rows
+// 10.3, the general kernel 13; K = 2048, N = 7168 (14.7 MB) one row 4.0 us, 3.7 TB/s,
+// the general kernel 6: the stream, not the products, sets the time, and of it the
+// start of the loads and the join at the end are half.
 #include <algorithm>
 
 #include "common.cuh"
