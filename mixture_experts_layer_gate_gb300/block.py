@@ -23,7 +23,11 @@ class MoEBlock:
     `gate` takes problem()'s keywords (scoring, n_group, wdtype, ...).  Batches that
     moe_forward_few takes (FEW_MAX_TOKENS tokens up to H = 8192, fewer beyond) run
     there, others in moe_forward.  Calls
-    of one block share its workspaces: order them on one stream.
+    of one block share its workspaces: order them on one stream, the given raw one or
+    PyTorch's current one.  What a call allocates belongs to that stream.  With a
+    stream other than the current one the block and the inputs have to be ready on it
+    (wait_stream), and the outputs are once its work is; the memory of neither is reused
+    before both streams are done with it.
     """
 
     def __init__(self, H, I, E, top_k, weights: b.Weights, norm_weight, router_weight, shared: SharedExpert | None,
@@ -40,6 +44,9 @@ class MoEBlock:
         self.op_ws = b.alloc_op_workspace(device)
 
     def __call__(self, x, residual=None, stream=None):
+        return b.run_on(stream, self._run, x, residual)
+
+    def _run(self, x, residual):
         import torch
         T, H = x.shape
         dev = x.device
@@ -50,26 +57,26 @@ class MoEBlock:
         scales = new(T, -(-H // 128), dtype=torch.float32) if self.shared else None
         wdt = "f32" if self.norm_weight.dtype == torch.float32 else "bf16"
         b.add_rms_norm(b.norm_problem(T, H, weight_dtype=wdt, eps=self.eps, quant="block" if self.shared else "none"),
-                       x, self.norm_weight, residual, total, y, codes, scales, stream)
+                       x, self.norm_weight, residual, total, y, codes, scales)
         p = self.layer.problem(T)
         logits = new(T, p.E, dtype=torch.float32)
-        b.router_logits(b.router_problem(T, H, p.E), y, self.router_weight, logits, self.op_ws, stream)
+        b.router_logits(b.router_problem(T, H, p.E), y, self.router_weight, logits, self.op_ws)
         out = new(T, H)
         few = b.few_workspace_size(p) if 0 < T <= b.FEW_MAX_TOKENS else 0
         if few:
             if self.few_ws is None or few > self.few_ws.numel():
                 self.few_ws = b.alloc_few_workspace(p, dev)
-            b.forward_few(p, self.weights, y, logits, self.router_bias, out, self.few_ws, stream)
+            b.forward_few(p, self.weights, y, logits, self.router_bias, out, self.few_ws)
         else:
-            self.layer(y, logits, self.router_bias, out, stream)
+            self.layer(y, logits, self.router_bias, out)
         if self.shared:
             s = self.shared
             act = new(T, s.I, dtype=torch.uint8)
             act_scales = new(T, s.I // 128, dtype=torch.float32)
             b.gemm_fp8_block_swiglu(b.fp8_gemm_problem(T, s.I, H), codes, scales, s.w13, s.w13_scale, act, act_scales,
-                                    self.op_ws, stream)
+                                    self.op_ws)
             b.gemm_fp8_block(b.fp8_gemm_problem(T, H, s.I, accumulate=True), act, act_scales, s.w2, s.w2_scale, out,
-                             self.op_ws, stream)
+                             self.op_ws)
         return out, total if total is not None else x
 
     def device_error(self, stream=None) -> int:
