@@ -447,7 +447,8 @@ def forward_few(p: Problem, w: Weights, x, logits, bias, out, ws, stream=None):
 
 class MoELayer:
     """Convenience wrapper: one problem shape (up to a token budget), its weights
-    and a workspace; `__call__` runs moe_forward on the current stream."""
+    and a workspace; `__call__` runs moe_forward on the given raw stream or the current
+    one, and allocates there what it needs."""
 
     def __init__(self, H, I, E, top_k, weights: Weights, max_tokens: int, device, **gate):
         self.shape = dict(H=H, I=I, E=E, top_k=top_k, **gate)
@@ -458,6 +459,9 @@ class MoELayer:
         return problem(T, **self.shape)
 
     def __call__(self, x, logits, bias=None, out=None, stream=None):
+        return run_on(stream, self._run, x, logits, bias, out)
+
+    def _run(self, x, logits, bias, out):
         import torch
         T = x.shape[0]
         if out is None:
@@ -465,5 +469,5 @@ class MoELayer:
         p = self.problem(T)
         if workspace_size(p) > self.ws.numel():
             self.ws = alloc_workspace(p, x.device)
-        forward(p, self.weights, x, logits, bias, out, self.ws, stream)
+        forward(p, self.weights, x, logits, bias, out, self.ws)
         return out

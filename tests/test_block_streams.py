@@ -1,4 +1,4 @@
-"""MoEBlock on a stream that it is given: what a call allocates belongs to the stream of its kernels."""
+"""MoEBlock and MoELayer on a stream that they are given: what a call allocates belongs to the stream of its kernels."""
 import contextlib
 
 import pytest
@@ -79,6 +79,21 @@ def test_block_allocates_on_the_stream_of_its_kernels(monkeypatch, T, max_tokens
     assert fake.current == 16
     if used != 16:  # what crosses streams is kept for both
         assert {(x.data_ptr(), 48), (r.data_ptr(), 48), (out.data_ptr(), 16), (total.data_ptr(), 16)} <= set(fake.recorded)
+
+
+@pytest.mark.parametrize("given", [True, False])
+def test_layer_allocates_on_the_stream_of_its_kernels(monkeypatch, given):
+    H, I, E = 256, 128, 8
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    layer = moe.MoELayer(H, I, E, 2, moe.Weights(bf(E, 2 * I, H), bf(E, H, I)), 1, "cpu")
+    fake = FakeStreams(monkeypatch, 16)
+    x, logits = bf(40, H), torch.empty(40, E)
+    fake.log.clear()
+    out = bf(40, H) if given else None
+    fake.log.clear()
+    got = layer(x, logits, None, out, stream=48)
+    assert fake.log and {s for _, s in fake.log} == {48}, fake.log
+    assert got.shape == (40, H) and (out is None or got is out)
 
 
 @gpu
