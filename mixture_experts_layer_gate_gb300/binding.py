@@ -445,6 +445,26 @@ def forward_few(p: Problem, w: Weights, x, logits, bias, out, ws, stream=None):
     _check((_ops or _native()).forward_few(p, w.struct, x, logits, bias, out, ws, stream), "moe_forward_few")
 
 
+def workspace_of(owner, name: str, n: int, allocate):
+    """A workspace of at least n bytes for a call: owner's attribute `name`, which allocate() replaces where it is too
+    small.  One that a captured graph uses stays alive in owner.kept, and one whose zero fill is being captured
+    serves that capture alone."""
+    import torch
+    ws, capturing = getattr(owner, name), torch.cuda.is_current_stream_capturing()
+    if ws is not None and n <= ws.numel():
+        if capturing and not any(w is ws for w in owner.kept):
+            owner.kept.append(ws)
+        return ws
+    new = allocate()
+    if capturing:
+        owner.kept.append(new)
+        return new
+    if ws is not None and not any(w is ws for w in owner.kept):
+        ws.record_stream(torch.cuda.current_stream())  # its calls may still run there
+    setattr(owner, name, new)
+    return new
+
+
 class MoELayer:
     """Convenience wrapper: one problem shape (up to a token budget), its weights
     and a workspace; `__call__` runs moe_forward on the given raw stream or the current
@@ -453,6 +473,7 @@ class MoELayer:
     def __init__(self, H, I, E, top_k, weights: Weights, max_tokens: int, device, **gate):
         self.shape = dict(H=H, I=I, E=E, top_k=top_k, **gate)
         self.weights = weights
+        self.kept = []  # workspaces that captured graphs use
         self.ws = alloc_workspace(problem(max_tokens, H, I, E, top_k, **gate), device)
 
     def problem(self, T: int) -> Problem:
@@ -467,7 +488,6 @@ class MoELayer:
         if out is None:
             out = torch.empty((T, self.shape["H"]), dtype=torch.bfloat16, device=x.device)
         p = self.problem(T)
-        if workspace_size(p) > self.ws.numel():
-            self.ws = alloc_workspace(p, x.device)
-        forward(p, self.weights, x, logits, bias, out, self.ws)
+        ws = workspace_of(self, "ws", workspace_size(p), lambda: alloc_workspace(p, x.device))
+        forward(p, self.weights, x, logits, bias, out, ws)
         return out

@@ -36,7 +36,7 @@ class MoEBlock:
         self.norm_weight, self.router_weight, self.router_bias = norm_weight, router_weight, router_bias
         self.shared, self.weights = shared, weights
         self.layer = b.MoELayer(H, I, E, top_k, weights, max_tokens, device, **gate)
-        self.few_ws = None
+        self.few_ws, self.kept = None, []  # kept: workspaces that captured graphs use
         for T in range(min(max_tokens, b.FEW_MAX_TOKENS), 0, -1):
             if b.few_workspace_size(self.layer.problem(T)):
                 self.few_ws = b.alloc_few_workspace(self.layer.problem(T), device)
@@ -64,9 +64,8 @@ class MoEBlock:
         out = new(T, H)
         few = b.few_workspace_size(p) if 0 < T <= b.FEW_MAX_TOKENS else 0
         if few:
-            if self.few_ws is None or few > self.few_ws.numel():
-                self.few_ws = b.alloc_few_workspace(p, dev)
-            b.forward_few(p, self.weights, y, logits, self.router_bias, out, self.few_ws)
+            ws = b.workspace_of(self, "few_ws", few, lambda: b.alloc_few_workspace(p, dev))
+            b.forward_few(p, self.weights, y, logits, self.router_bias, out, ws)
         else:
             self.layer(y, logits, self.router_bias, out)
         if self.shared:
@@ -81,5 +80,6 @@ class MoEBlock:
 
     def device_error(self, stream=None) -> int:
         """First error that a kernel of the block recorded (0: none), cleared; synchronises the stream."""
-        found = [b.get_device_error(ws, stream) for ws in (self.op_ws, self.few_ws, self.layer.ws) if ws is not None]
+        all_ws = (self.op_ws, self.few_ws, self.layer.ws, *self.kept, *self.layer.kept)
+        found = [b.get_device_error(ws, stream) for ws in all_ws if ws is not None]
         return next((e for e in found if e), 0)

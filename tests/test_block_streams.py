@@ -1,5 +1,7 @@
-"""MoEBlock and MoELayer on a stream that they are given: what a call allocates belongs to the stream of its kernels."""
+"""MoEBlock and MoELayer on a stream that they are given and in captured graphs: what a call allocates belongs to the
+stream of its kernels, and a workspace lives as long as a graph that uses it."""
 import contextlib
+import weakref
 
 import pytest
 import torch
@@ -15,7 +17,7 @@ class FakeStreams:
     """Stands in for PyTorch's streams, allocations and the kernels, on the CPU: notes on which stream each runs."""
 
     def __init__(self, monkeypatch, caller):
-        self.current, self.log, self.recorded = caller, [], []
+        self.current, self.log, self.recorded, self.capturing, self.passed = caller, [], [], False, []
         fake = self
 
         class Stream:
@@ -34,7 +36,7 @@ class FakeStreams:
         monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream(self.current))
         monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
         monkeypatch.setattr(torch.cuda, "stream", switch)
-        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: self.capturing)
         monkeypatch.setattr(torch.Tensor, "record_stream",
                             lambda t, s: self.recorded.append((t.data_ptr(), s.cuda_stream)))
         monkeypatch.setattr(binding, "_stream", lambda s: self.current if s is None else int(s))
@@ -44,6 +46,8 @@ class FakeStreams:
             def op(*a, name=name, i=i, stream=None):
                 given = a[i] if len(a) > i else stream
                 self.log.append((name, self.current if given is None else int(given)))
+                if name.startswith("forward"):
+                    self.passed.append(a[6])  # its workspace
             monkeypatch.setattr(binding, name, op)
 
 
@@ -96,6 +100,32 @@ def test_layer_allocates_on_the_stream_of_its_kernels(monkeypatch, given):
     assert got.shape == (40, H) and (out is None or got is out)
 
 
+@pytest.mark.parametrize("T", [3, 20])
+def test_workspaces_live_as_long_as_the_graphs_that_use_them(monkeypatch, T):
+    """Capture a small batch, then call a larger one: the graph's workspace stays.  Captured while too small: the zero
+    fill belongs to the graph, so a later call does not take that workspace for a zeroed one."""
+    bf = lambda n: torch.zeros(n, 256, dtype=torch.bfloat16)  # noqa: E731
+    small = 1 if T <= 8 else 9
+    b = cpu_block(small, shared=False)
+    fake = FakeStreams(monkeypatch, 16)
+    fake.capturing = True
+    b(bf(small))
+    fake.capturing = False
+    graphs = weakref.ref(fake.passed.pop())
+    b(bf(T))                                   # grows
+    assert graphs() is not None and fake.passed.pop() is not graphs()
+    fake.capturing = True
+    b(bf(T + 5 if T <= 8 else 2 * T))          # too small again, within a capture
+    fake.capturing = False
+    graphs = weakref.ref(fake.passed.pop())
+    b(bf(T + 5 if T <= 8 else 2 * T))
+    assert graphs() is not None and fake.passed.pop() is not graphs()
+    before = len(b.kept) + len(b.layer.kept)
+    for n in range(2 * T + 1, 2 * T + 4):      # without a capture outgrown ones go
+        b(bf(n))
+    assert len(b.kept) + len(b.layer.kept) == before
+
+
 @gpu
 @pytest.mark.parametrize("T", [3, 20])
 def test_block_on_a_given_stream_while_the_current_one_allocates_and_writes(T):
@@ -127,3 +157,33 @@ def test_block_on_a_given_stream_while_the_current_one_allocates_and_writes(T):
     assert b.device_error() == 0
     for (out, total), (o, t) in zip(got, want):
         assert torch.equal(out, o) and torch.equal(total, t)
+
+
+@gpu
+@pytest.mark.parametrize("small,large", [(1, 8), (9, 300)])
+def test_a_graph_replays_after_the_workspace_has_grown(small, large):
+    dev = torch.device("cuda:0")
+    H, I, E, k = 512, 256, 16, 4
+    p = moe.problem(large, H, I, E, k, wdtype="int8")
+    wd = moe.Weights(*[None if t is None else t.to(dev) for t in few_weights(p, False, 7)])
+    nw, rw = torch.ones(H, dtype=torch.bfloat16, device=dev), (0.05 * randn(gen(1), E, H)).to(torch.bfloat16).to(dev)
+    b, other = (moe.MoEBlock(H, I, E, k, wd, nw, rw, None, n, dev, wdtype="int8") for n in (0, large))
+    x, y = (randn(gen(n), n, H).to(torch.bfloat16).to(dev) for n in (small, large))
+    graphs = []
+    other(x)  # the kernels' first launches, outside of a capture
+    torch.cuda.synchronize()
+    for eager in (False, True):  # the first capture grows the workspace itself, the second uses the eager one
+        if eager:
+            want, _ = b(x)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            graphs.append((graph, b(x)[0]))
+    large_want = b(y)[0].clone()
+    junk = [torch.full((1 << 16,), 0x7F, dtype=torch.uint8, device=dev) for _ in range(64)]
+    torch.cuda.synchronize()
+    for graph, out in graphs:
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert all(bool((j == 0x7F).all()) for j in junk)
+    assert torch.equal(b(y)[0], large_want) and b.device_error() == 0
