@@ -373,7 +373,7 @@ GemmPlan plan_gemm(const moe_problem_t& p, bool up, int sms) {
   // whole-stage slots: converters wait on the stage ring for slot reuse, which
   // needs at least as many ring stages as slots (parity-wait rule)
   if (converts(wk) && g.slot_kb == kSuper && g.astages > g.stages) g.astages = g.stages;
-  g.smem = gemm_smem_bytes(wk, brows, g.stages, g.astages, p.E, g.epi_warps);
+  g.smem = std::max(kTensorMemorySmem, gemm_smem_bytes(wk, brows, g.stages, g.astages, p.E, g.epi_warps));
   return g;
 }
 

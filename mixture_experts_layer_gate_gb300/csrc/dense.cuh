@@ -945,12 +945,7 @@ size_t smem_bytes(const Params& p, int bn, bool pair) {
     const size_t part = static_cast<size_t>(rows) * part_ld(bn) * 4;
     if (part > ring) ring = part;
   }
-  // CTAs that share an SM share its 512 tensor-memory columns: as many fit by
-  // shared memory as by columns, so that no CTA waits for another's
-  // columns while its cluster waits for it
-  const size_t floor = bn >= 256 ? 120 * 1024 : bn >= 128 ? 80 * 1024 : bn >= 64 ? 48 * 1024 : 0;
-  const size_t need = 1024 + fixed_bytes(KIND, SWIGLU, bn, p.boxes) + ring;
-  return need > floor ? need : floor;
+  return std::max(kTensorMemorySmem, 1024 + fixed_bytes(KIND, SWIGLU, bn, p.boxes) + ring);
 }
 
 template <int KIND, bool SWIGLU, bool PAIR, int BN, bool ADD = false>

@@ -171,6 +171,11 @@ struct GemmMaps {
   CUtensorMap b16;  // the same rows, 16-row box (ragged last tile of an expert)
 };
 
+// Least dynamic shared memory of a CTA that takes tensor memory: more than half of
+// an SM's, so that no two share one.  tcgen05.alloc waits without a limit, and of two
+// clusters on two streams each could hold columns that the other waits for.
+constexpr size_t kTensorMemorySmem = 116 * 1024;
+
 constexpr int kMaxEpiWarps = 8;
 size_t gemm_smem_bytes(int wkind, int bn_max, int stages, int astages, int E, int epi_warps);
 int gemm_threads(int wkind, int conv_groups, int dual, int epi_warps);
