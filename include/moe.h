@@ -485,7 +485,8 @@ moe_status_t moe_gemm_fp8_block_swiglu(const moe_fp8_gemm_t* g, const void* a, i
  * unrounded, and y is not rounded per expert, so results differ from
  * moe_forward's by its roundings.  fp8 experts take activations as their codes,
  * e4m3(x / a1) and e4m3(act / a2); dynamic scales are max |x| / 448 and
- * max |act| / 448 over the call (1 for all zeros).  int4 / int8 scales and zero
+ * max |act| / 448 over the call (1 where that is 0), the quotient by the latter to
+ * within a float's last bits.  int4 / int8 scales and zero
  * points are 4-byte aligned.  The workspace holds moe_few_workspace_size()
  * bytes (0 for an invalid problem or one beyond the limit). */
 #define MOE_FEW_MAX_TOKENS 8

@@ -227,7 +227,11 @@ __device__ __forceinline__ float block_max(float v, float* part) {
   return v;
 }
 
-__device__ __forceinline__ float act_scale_of(float amax) { return amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f; }
+// 1 for zeros, and for values so small that the scale would be zero
+__device__ __forceinline__ float act_scale_of(float amax) {
+  const float s = __fdiv_rn(amax, 448.0f);
+  return s == 0.f ? 1.0f : s;
+}
 
 // e4m3 of two values as the f16 pair that they stand for
 __device__ __forceinline__ uint32_t quantised_f16x2(float a, float b) { return e4m3x2_f16x2(f32x2_to_e4m3x2(a, b)); }
@@ -820,12 +824,18 @@ __global__ void __launch_bounds__(kThreads, 1) few_down_kernel(GateArgs gate, Fe
     } else {
       a2 = a.a2[0];
     }
-    // the experts' scales go with the weights of the sum
+    // the experts' scales go with the weights of the sum; a2 follows it, because its
+    // product with a scale may be too small for a float where the sum's is not
     for (int i = tid; i < r.count * kFewMaxTokens; i += kThreads)
-      (&weight[0][0])[i] *= a2 * static_cast<const float*>(a.w2_scale)[r.expert[i / kFewMaxTokens]];
+      (&weight[0][0])[i] *= static_cast<const float*>(a.w2_scale)[r.expert[i / kFewMaxTokens]];
     __syncthreads();
   }
-  const float rs = 1.0f / a2;
+  // act / a2 by the reciprocal, which is within the quotient's last bits (an IEEE
+  // division per value: Qwen2 fp8, one token 69 us, eight 326; the reciprocal 51 and
+  // 227); of a scale so small that it would overflow, with both sides times 2^64 (in a
+  // step of its own below: as part of every value's product 52 and 234)
+  const bool tiny = a2 < 0x1p-64f;
+  const float rs = __fdiv_rn(1.0f, tiny ? a2 * 0x1p64f : a2);
 
   uint32_t src = ring;
   int buf = 0;
@@ -873,9 +883,21 @@ __global__ void __launch_bounds__(kThreads, 1) few_down_kernel(GateArgs gate, Fe
             if (both) lo = lds128(src + place + kTok / 2 + (u * F::NS + n) * 64);
             if (dynamic) {
               auto q2 = [&](uint32_t h, uint32_t l) {
-                return quantised_f16x2(__uint_as_float(__byte_perm(l, h, 0x5410)) * rs,
-                                       __uint_as_float(__byte_perm(l, h, 0x7632)) * rs);
+                float v0 = __uint_as_float(__byte_perm(l, h, 0x5410)), v1 = __uint_as_float(__byte_perm(l, h, 0x7632));
+                return quantised_f16x2(v0 * rs, v1 * rs);
               };
+              if (tiny) {
+                auto up = [](uint32_t& h, uint32_t& l) {
+                  const uint32_t v0 = __float_as_uint(__uint_as_float(__byte_perm(l, h, 0x5410)) * 0x1p64f);
+                  const uint32_t v1 = __float_as_uint(__uint_as_float(__byte_perm(l, h, 0x7632)) * 0x1p64f);
+                  l = __byte_perm(v0, v1, 0x5410);
+                  h = __byte_perm(v0, v1, 0x7632);
+                };
+                up(hi.x, lo.x);
+                up(hi.y, lo.y);
+                up(hi.z, lo.z);
+                up(hi.w, lo.w);
+              }
               hi = make_uint4(q2(hi.x, lo.x), q2(hi.y, lo.y), q2(hi.z, lo.z), q2(hi.w, lo.w));
             }
 #pragma unroll
@@ -916,7 +938,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_down_kernel(GateArgs gate, Fe
       float v = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) v += rd[(w * 16 + row) * 8 + t];
-      if (t < a.T) a.out[static_cast<size_t>(t) * a.H + unit * 16 + row] = __float2bfloat16_rn(v);
+      if (t < a.T) a.out[static_cast<size_t>(t) * a.H + unit * 16 + row] = __float2bfloat16_rn(FMT == kW_FP8 ? v * a2 : v);
     }
   }
 }
