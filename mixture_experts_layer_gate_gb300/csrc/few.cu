@@ -179,7 +179,7 @@ struct Routing {
 // per chosen expert and token: the weight of the sum, 0 where the token did not choose it
 typedef float (*Weights)[kFewMaxTokens];
 
-// From r.ids and r.w; every thread of the CTA.  weight: null where it is not needed.
+// From r.ids (-1: no expert) and r.w; every thread of the CTA.  weight: null where it is not needed.
 __device__ __forceinline__ void build_routing(Routing& r, const FewArgs& a, Weights weight) {
   const int S = a.T * a.k;
   if (threadIdx.x == 0) r.most = 1;
@@ -188,7 +188,8 @@ __device__ __forceinline__ void build_routing(Routing& r, const FewArgs& a, Weig
     for (int i = threadIdx.x; i < S * kFewMaxTokens; i += kThreads) (&weight[0][0])[i] = 0.f;
   for (int i = threadIdx.x; i < (S + 3) / 4; i += kThreads) reinterpret_cast<uint32_t*>(r.tokens)[i] = 0;
   __syncthreads();
-  for (int s = threadIdx.x; s < S; s += kThreads) atomicOr(&r.seen[r.ids[s] >> 5], 1u << (r.ids[s] & 31));
+  for (int s = threadIdx.x; s < S; s += kThreads)
+    if (r.ids[s] >= 0) atomicOr(&r.seen[r.ids[s] >> 5], 1u << (r.ids[s] & 31));
   __syncthreads();
   if (threadIdx.x < 32) {
     const int n = __popc(r.seen[threadIdx.x]);
@@ -204,6 +205,7 @@ __device__ __forceinline__ void build_routing(Routing& r, const FewArgs& a, Weig
   __syncthreads();
   for (int s = threadIdx.x; s < S; s += kThreads) {
     const int e = r.ids[s], t = s / a.k;
+    if (e < 0) continue;
     const int at = r.before[e >> 5] + __popc(r.seen[e >> 5] & ((1u << (e & 31)) - 1u));
     r.expert[at] = static_cast<int16_t>(e);
     r.slot[at][t] = static_cast<uint8_t>(s);
@@ -256,15 +258,16 @@ __device__ __forceinline__ void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
 }
 
-// A float's order as an unsigned one (-0 as +0); 0 is below every number.
+// A float's order as an unsigned one (-0 as +0); 0, below every number, for NaN,
+// which is never chosen.
 __device__ __forceinline__ uint32_t ordered(float v) {
   const uint32_t u = __float_as_uint(v + 0.f);
-  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+  return v != v ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
 // The k best of the warp's keys (32 strided experts per register, 0: out of the
-// running), ties to the lower expert: lane j returns the j-th expert.  A lane
-// keeps the best of its own; a round is two warp reductions, after which the
+// running), ties to the lower expert: lane j returns the j-th expert, -1 where
+// fewer were in the running.  A lane keeps the best of its own; a round is two warp reductions, after which the
 // winner's lane looks for its next.
 template <int EPL>
 __device__ __forceinline__ int best_k(uint32_t (&key)[EPL], int k, int lane) {
@@ -282,7 +285,7 @@ __device__ __forceinline__ int best_k(uint32_t (&key)[EPL], int k, int lane) {
 #pragma unroll 1
   for (int j = 0; j < k; ++j) {
     const uint32_t m = __reduce_max_sync(0xffffffffu, top);
-    const uint32_t best = __reduce_min_sync(0xffffffffu, top == m ? at : 0xffffffffu);
+    const uint32_t best = __reduce_min_sync(0xffffffffu, top == m && m != 0 ? at : 0xffffffffu);
     if (lane == j) mine = static_cast<int>(best);
     if (top == m && at == best) {
 #pragma unroll
@@ -339,7 +342,7 @@ __device__ __forceinline__ void gate_one(const GateArgs& a, int t, int lane, flo
       const float kk = raw ? val[i] : s + bias[i];
       key[i] = ordered(kk);
       val[i] = s;
-      if (a.n_group > 0 && e < a.E) scratch[e] = kk;
+      if (a.n_group > 0 && e < a.E) scratch[e] = kk == kk ? kk : -INFINITY;
     }
   }
 #pragma unroll
@@ -368,7 +371,7 @@ __device__ __forceinline__ void gate_one(const GateArgs& a, int t, int lane, flo
     const float mine = __shfl_sync(0xffffffffu, score, (lane * per) & 31);
     uint32_t gkey[1] = {lane < a.n_group ? ordered(mine) : 0u};
     const int picked = best_k<1>(gkey, a.topk_group, lane);
-    const uint32_t allowed = __reduce_or_sync(0xffffffffu, lane < a.topk_group ? 1u << (picked & 31) : 0u);
+    const uint32_t allowed = __reduce_or_sync(0xffffffffu, lane < a.topk_group && picked >= 0 ? 1u << (picked & 31) : 0u);
     const float inv_gs = 1.0f / static_cast<float>(gs);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
@@ -383,7 +386,7 @@ __device__ __forceinline__ void gate_one(const GateArgs& a, int t, int lane, flo
   const int id = best_k<EPL>(key, a.k, lane);
   __syncwarp();
   float v = 0.f;
-  if (lane < a.k) v = scratch[static_cast<unsigned>(id) < static_cast<unsigned>(a.E) ? id : 0] * inv_z;
+  if (lane < a.k && id >= 0) v = scratch[id] * inv_z;
   float total = v;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -403,10 +406,8 @@ __device__ __forceinline__ void route(const GateArgs& gate, const FewArgs& a, Ro
   if (warp < a.T) {
     gate_one<EPL>(gate, warp, lane, scratch + warp * (32 * EPL), r.ids, r.w);
     // (a NaN bias can leave the gate without a choice)
-    if (lane < a.k && static_cast<unsigned>(r.ids[warp * a.k + lane]) >= static_cast<unsigned>(a.E)) {
-      if (blockIdx.x == 0) record_error(a.err, kErrBadIndex, static_cast<uint32_t>(warp * a.k + lane));
-      r.ids[warp * a.k + lane] = 0;
-    }
+    if (blockIdx.x == 0 && lane < a.k && r.ids[warp * a.k + lane] < 0)
+      record_error(a.err, kErrBadIndex, static_cast<uint32_t>(warp * a.k + lane));
   } else {
     meanwhile();
   }

@@ -5,7 +5,7 @@ import torch
 import mixture_experts_layer_gate_gb300 as moe
 from tests import op_reference as ref
 from tests.few_reference import _quantised
-from tests.test_operators import codes_of, gen, randn
+from tests.test_operators import codes_of, few_weights, gen, randn
 
 gpu = pytest.mark.gpu
 
@@ -70,3 +70,58 @@ def test_dynamic_scale_that_would_be_zero(dev):
     # every gate and up value is 128 * 2^-72 * 2^-7 = 2^-72, their product's half 2^-145: 16 steps of a float
     out = one_fp8_expert(dev, x, w13, torch.tensor([2.0 ** -7]), w2, torch.tensor([1.0]))
     assert bool((out == 0).all())
+
+
+# ------------------------------------------------------------------ a NaN in the gate's correction bias
+
+
+def few_of(dev, p, w, x, logits, bias):
+    out, ws = torch.full((p.T, p.H), float("nan"), dtype=torch.bfloat16, device=dev), moe.alloc_few_workspace(p, dev)
+    moe.forward_few(p, w, x, logits, bias, out, ws)
+    return out, moe.get_device_error(ws)
+
+
+@gpu
+@pytest.mark.parametrize("E,k,gate", [(8, 2, {}), (64, 6, {}), (300, 4, dict(renormalize=False)),
+                                      (64, 8, dict(n_group=8, topk_group=4)), (64, 8, dict(n_group=8, topk_group=2)),
+                                      (256, 8, dict(n_group=8, topk_group=4, routed_scaling_factor=2.5))])
+@pytest.mark.parametrize("T", [1, 5])
+def test_an_expert_with_a_nan_bias_is_not_chosen(dev, T, E, k, gate):
+    H, I = 256, 128
+    p = moe.problem(T, H, I, E, k, scoring="sigmoid", **gate)
+    g = gen(E + T)
+    wd = moe.Weights(*[None if t is None else t.to(dev) for t in few_weights(p, False, 5)])
+    x, logits = randn(g, T, H).to(torch.bfloat16).to(dev), (1.5 * randn(g, T, E)).to(dev)
+    bias = (0.2 * torch.rand(E, generator=g) - 0.1).to(dev)
+    out = [1] if E == 8 else [1, 3, E - 1]
+    bias[out] = float("nan")
+    ids, weights = torch.empty((T, k), dtype=torch.int32, device=dev), torch.empty((T, k), device=dev)
+    moe.gate_topk(p, logits, bias, ids, weights)
+    assert not any(bool((ids == e).any()) for e in out)
+    low = torch.where(torch.isnan(bias), torch.full_like(bias, -1e30), bias)  # the last of all, and chosen by nobody
+    got, err = few_of(dev, p, wd, x, logits, bias)
+    want, _ = few_of(dev, p, wd, x, logits, low)
+    assert err == 0 and torch.equal(got, want)
+
+
+@gpu
+@pytest.mark.parametrize("wdtype", ["bf16", "int4"])
+@pytest.mark.parametrize("n_group", [0, 2])
+def test_fewer_experts_than_choices(dev, wdtype, n_group):
+    """Two of four experts usable for three choices: the third is reported and counts nothing."""
+    T, H, I, E, k = 3, 256, 128, 4, 3
+    gate = dict(scoring="sigmoid", wdtype=wdtype, n_group=n_group, topk_group=n_group)
+    p, p2 = moe.problem(T, H, I, E, k, **gate), moe.problem(T, H, I, E, 2, **gate)
+    g = gen(2)
+    wd = moe.Weights(*[None if t is None else t.to(dev) for t in few_weights(p, False, 5)])
+    x, logits = randn(g, T, H).to(torch.bfloat16).to(dev), randn(g, T, E).to(dev)
+    nan = float("nan")
+    bias, low = torch.tensor([nan, 0.1, nan, 0.0], device=dev), torch.tensor([-1e30, 0.1, -1e30, 0.0], device=dev)
+    ids, weights = torch.empty((T, k), dtype=torch.int32, device=dev), torch.empty((T, k), device=dev)
+    moe.gate_topk(p, logits, bias, ids, weights)
+    assert bool((weights[:, 2] == 0).all()) and bool(((ids[:, 2] < 0) | (ids[:, 2] >= E)).all())
+    got, err = few_of(dev, p, wd, x, logits, bias)
+    want, none = few_of(dev, p2, wd, x, logits, low)
+    assert err == 5 and none == 0 and torch.equal(got, want)
+    got, err = few_of(dev, p, wd, x, logits, torch.full_like(bias, nan))  # no expert at all
+    assert err == 5 and bool((got == 0).all())
