@@ -478,7 +478,8 @@ moe_status_t moe_gemm_fp8_block_swiglu(const moe_fp8_gemm_t* g, const void* a, i
                                        float* scales, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /* The whole layer for a few tokens (T <= MOE_FEW_MAX_TOKENS and T * (H + 32) <=
- * 65792, which any H <= 8192 meets, else MOE_ERR_UNSUPPORTED): arguments, weight formats and meaning of moe_forward,
+ * 65792, with int4 weights also T * (H + 32) + H / 8 <= 68000, which any H <= 8192
+ * meets, else MOE_ERR_UNSUPPORTED): arguments, weight formats and meaning of moe_forward,
  * in two launches that stream the chosen experts' weights once.  All sums are
  * held in float and nothing is rounded between the gate and out: the SwiGLU
  * output stays float, int4 / int8 weights enter as (code - zero) * scale

@@ -972,7 +972,7 @@ cudaError_t launch_both(const GateArgs& g, const FewArgs& a, int sms, cudaStream
   // a second reduction buffer where it leaves four stages
   const int reds = kRoutingBytes + 2 * kRedBytes + sums + tokens + 4 * stage <= kMaxSmem ? 2 : 1;
   const size_t fixed = kRoutingBytes + reds * kRedBytes + sums + tokens;
-  if (fixed + 2 * stage > kMaxSmem) return cudaErrorInvalidValue;  // (refused before: kFewMaxTokenValues)
+  if (fixed + 2 * stage > kMaxSmem) return cudaErrorInvalidValue;  // (refused before, by the limits asserted below)
   const int depth = static_cast<int>(std::min<size_t>(kMaxDepth, (kMaxSmem - fixed) / stage));
   const int up_grid = std::min(sms, std::min(a.E, a.T * a.k) * (a.I / 16));
   err = launch_pdl(few_up_kernel<FMT, EPL>, dim3(up_grid), dim3(kThreads), fixed + std::max(depth * stage, gate), s, g,
@@ -994,10 +994,15 @@ cudaError_t launch_gate_width(const GateArgs& g, const FewArgs& a, int sms, cuda
 
 }  // namespace
 
-static_assert(kRoutingBytes + kRedBytes + 2 * static_cast<size_t>(kFewMaxTokenValues) + 128 + 8192 / 4 +
-                      2 * kWarps * up_stage<kW_INT4>() <=
+// (a token's row takes 2 * (H + 32) bytes, all of them rounded up to 128; int4's sums H / 4)
+static_assert(kRoutingBytes + kRedBytes + 2 * static_cast<size_t>(kFewMaxTokenValues) + 127 +
+                      2 * kWarps * std::max(up_stage<kW_INT8>(), std::max(up_stage<kW_BF16>(), up_stage<kW_FP8>())) <=
                   kMaxSmem,
               "two stages a warp beside the most tokens");
+static_assert(kRoutingBytes + kRedBytes + 2 * static_cast<size_t>(kFewMaxInt4Values) + 64 +
+                      2 * kWarps * up_stage<kW_INT4>() <=
+                  kMaxSmem,
+              "two stages a warp beside the most tokens and their sums (rows of a multiple of 64 bytes)");
 
 cudaError_t launch_few(const GateArgs& g, const FewArgs& a, cudaStream_t s) {
   DeviceInfo di;

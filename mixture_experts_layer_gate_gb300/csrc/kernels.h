@@ -247,6 +247,8 @@ constexpr int kFewMaxTokens = 8;
 constexpr int kFewMaxCtas = 1024;
 // T * (H + 32) at most: the tokens stay in shared memory beside the weights' ring
 constexpr int kFewMaxTokenValues = 8 * (8192 + 32);
+// and with int4 weights T * (H + 32) + H / 8: the sums of x over groups of 128 beside them
+constexpr int kFewMaxInt4Values = 68000;
 struct FewArgs {
   const __nv_bfloat16* x;  // [T, H]
   const void* w13;

@@ -50,7 +50,9 @@ FewLayout few_layout(const moe_problem_t& p) {
 }
 
 bool few_fits(const moe_problem_t& p) {
-  return p.T <= kFewMaxTokens && static_cast<long long>(p.T) * (p.H + 32) <= kFewMaxTokenValues;
+  const long long values = static_cast<long long>(p.T) * (p.H + 32);
+  const bool int4 = p.wdtype == MOE_W_INT4_G128 || p.wdtype == MOE_W_INT4_G128_PAIRED;
+  return p.T <= kFewMaxTokens && values <= kFewMaxTokenValues && (!int4 || values + p.H / 8 <= kFewMaxInt4Values);
 }
 
 moe_status_t check_fp8_gemm(const moe_fp8_gemm_t* g, const void* a, int64_t a_stride, const float* a_scale,

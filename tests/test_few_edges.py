@@ -1,11 +1,13 @@
 """moe_forward_few at the ends of its ranges, against plain 64-bit forms."""
+import ctypes
+
 import pytest
 import torch
 
 import mixture_experts_layer_gate_gb300 as moe
 from tests import op_reference as ref
 from tests.few_reference import _quantised
-from tests.test_operators import codes_of, few_weights, gen, randn
+from tests.test_operators import codes_of, few_weights, gen, randn, run_few
 
 gpu = pytest.mark.gpu
 
@@ -125,3 +127,35 @@ def test_fewer_experts_than_choices(dev, wdtype, n_group):
     assert err == 5 and none == 0 and torch.equal(got, want)
     got, err = few_of(dev, p, wd, x, logits, torch.full_like(bias, nan))  # no expert at all
     assert err == 5 and bool((got == 0).all())
+
+
+# ------------------------------------------------------------------ the widest tokens of each format
+
+
+WIDEST = {"int4": {1: 60416, 2: 31872, 3: 21632, 4: 16384, 8: 8192}, "bf16": {1: 65664, 2: 32768, 3: 21888, 8: 8192}}
+WIDEST["int4_paired"], WIDEST["fp8"], WIDEST["int8"] = WIDEST["int4"], WIDEST["bf16"], WIDEST["bf16"]
+
+
+@pytest.mark.parametrize("wdtype", list(WIDEST))
+def test_limits_of_the_token_width(wdtype):
+    moe.load()
+    for T, H in WIDEST[wdtype].items():
+        p, over = moe.problem(T, H, 128, 2, 1, wdtype=wdtype), moe.problem(T, H + 128, 128, 2, 1, wdtype=wdtype)
+        assert moe.few_workspace_size(p) > 0 and moe.few_workspace_size(over) == 0, (T, H)
+        w, lib = moe.binding.WeightsStruct(4096, 4096, 4096, 4096, 4096, 4096), moe.load()
+        if wdtype != "fp8":
+            w.a1_scale = w.a2_scale = None
+        if wdtype == "bf16":
+            w.w13_scale = w.w2_scale = None
+        assert lib.moe_forward_few(ctypes.byref(over), ctypes.byref(w), 4096, 4096, None, 4096, 4096, 1 << 30, None) == 2
+    for T in range(1, 9):
+        for H in range(128, 8193, 128):
+            assert moe.few_workspace_size(moe.problem(T, H, 128, 2, 1, wdtype=wdtype)) > 0
+
+
+@gpu
+@pytest.mark.parametrize("wdtype,zero", [("int4", False), ("int4", True), ("int4_paired", False), ("bf16", False),
+                                         ("fp8", False), ("int8", True)])
+@pytest.mark.parametrize("T", [1, 2, 3])
+def test_widest_tokens(dev, wdtype, zero, T):
+    run_few(dev, T, WIDEST[wdtype][T], 128, 2, 1, zero=zero, wdtype=wdtype)
