@@ -5,6 +5,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -29,33 +30,63 @@ const at::Tensor& tensor(PyObject* o, const char* what) {
   return THPVariable_Unpack(o);
 }
 
+// What the elements have to be.
+struct Type {
+  at::ScalarType first, second;
+  Type(at::ScalarType t) : first(t), second(t) {}
+  Type(at::ScalarType t, at::ScalarType u) : first(t), second(u) {}
+};
+const Type kFloat(at::ScalarType::Float), kBf16(at::ScalarType::BFloat16);
+const Type kCodes(at::ScalarType::Byte, at::ScalarType::Float8_e4m3fn);
+
+// of a moe_dtype_t; one that is none is left to the C call, which refuses it
+Type type_of(int dtype) {
+  switch (dtype) {
+    case MOE_T_BF16: return kBf16;
+    case MOE_T_F16: return at::ScalarType::Half;
+    case MOE_T_F32: return kFloat;
+    default: return at::ScalarType::Undefined;
+  }
+}
+
+std::string name_of(const Type& type) {
+  const std::string s = at::toString(type.first);
+  return type.first == type.second ? s : s + " or " + at::toString(type.second);
+}
+bool is_of(const at::Tensor& t, const Type& type) {
+  const at::ScalarType s = t.scalar_type();
+  return s == type.first || s == type.second || type.first == at::ScalarType::Undefined;
+}
+// the kernels are launched on the current device
+bool is_here(const at::Tensor& t) { return t.is_cuda() && t.device().index() == c10::cuda::current_device(); }
+
 struct Rows {
   void* p = nullptr;
   int64_t stride = 0;
   float* f32() const { return static_cast<float*>(p); }
 };
 
-// [rows, cols] of `size`-byte elements; None stays null
-Rows rows(PyObject* o, int64_t n, int64_t cols, size_t size, const char* what) {
+// [rows, cols]; None stays null
+Rows rows(PyObject* o, int64_t n, int64_t cols, const Type& type, const char* what) {
   Rows r;
   if (o == Py_None) return r;
   const at::Tensor& t = tensor(o, what);
-  if (t.dim() != 2 || t.size(0) != n || t.size(1) != cols || t.itemsize() != size || !t.is_cuda())
-    refuse(std::string(what) + ": a CUDA tensor [" + std::to_string(n) + ", " + std::to_string(cols) + "] of " +
-           std::to_string(size) + "-byte elements");
+  if (t.dim() != 2 || t.size(0) != n || t.size(1) != cols || !is_of(t, type) || !is_here(t))
+    refuse(std::string(what) + ": a tensor [" + std::to_string(n) + ", " + std::to_string(cols) + "] of " +
+           name_of(type) + " on the current CUDA device");
   if (t.stride(1) != 1 && cols > 1) refuse(std::string(what) + ": adjacent columns");
   r.p = t.data_ptr();
   r.stride = n > 1 ? t.stride(0) : cols;
   return r;
 }
 
-// a contiguous tensor of n elements of `size` bytes; None stays null
-void* flat(PyObject* o, int64_t n, size_t size, const char* what) {
+// a contiguous tensor of n elements; None stays null
+void* flat(PyObject* o, int64_t n, const Type& type, const char* what) {
   if (o == Py_None) return nullptr;
   const at::Tensor& t = tensor(o, what);
-  if (t.numel() != n || t.itemsize() != size || !t.is_cuda() || !t.is_contiguous())
-    refuse(std::string(what) + ": a contiguous CUDA tensor of " + std::to_string(n) + " elements of " +
-           std::to_string(size) + " bytes");
+  if (t.numel() != n || !is_of(t, type) || !is_here(t) || !t.is_contiguous())
+    refuse(std::string(what) + ": a contiguous tensor of " + std::to_string(n) + " elements of " + name_of(type) +
+           " on the current CUDA device");
   return t.data_ptr();
 }
 
@@ -64,7 +95,7 @@ struct Workspace {
   size_t bytes;
   explicit Workspace(PyObject* o) {
     const at::Tensor& t = tensor(o, "ws");
-    if (!t.is_cuda() || !t.is_contiguous()) refuse("ws: a contiguous CUDA tensor");
+    if (!is_here(t) || !t.is_contiguous()) refuse("ws: a contiguous tensor on the current CUDA device");
     p = t.data_ptr();
     bytes = t.nbytes();
   }
@@ -94,7 +125,6 @@ moe_stream_t stream_of(PyObject* o) {
   return reinterpret_cast<moe_stream_t>(v);
 }
 
-size_t size_of(int dtype) { return dtype == MOE_T_F32 ? 4 : 2; }
 int64_t blocks(int64_t n) { return (n + 127) / 128; }
 
 // Runs f(arguments, ...) -> moe_status_t; C++ exceptions become Python's.
@@ -128,12 +158,12 @@ PyObject* add_rms_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return run(n, 9, [&] {
     const moe_norm_t p = problem<moe_norm_t>(v[0]);
     const int64_t T = p.T, H = p.H;
-    const size_t b = size_of(p.dtype);
+    const Type b = type_of(p.dtype);
     const Rows x = rows(v[1], T, H, b, "x"), r = rows(v[3], T, H, b, "residual");
     const Rows o = rows(v[4], T, H, b, "residual_out"), y = rows(v[5], T, H, b, "y");
-    void* w = flat(v[2], H, size_of(p.weight_dtype), "weight");
-    void* codes = flat(v[6], T * H, 1, "codes");
-    void* scales = flat(v[7], T * (p.quant == MOE_QUANT_BLOCK128 ? blocks(H) : 1), 4, "scales");
+    void* w = flat(v[2], H, type_of(p.weight_dtype), "weight");
+    void* codes = flat(v[6], T * H, kCodes, "codes");
+    void* scales = flat(v[7], T * (p.quant == MOE_QUANT_BLOCK128 ? blocks(H) : 1), kFloat, "scales");
     const moe_stream_t s = stream_of(v[8]);
     return unlocked([&] {
       return moe_add_rms_norm(&p, x.p, x.stride, r.p, r.stride, w, o.p, o.stride, y.p, y.stride, codes,
@@ -146,8 +176,9 @@ PyObject* add_rms_norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
 PyObject* router_logits(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return run(n, 6, [&] {
     const moe_router_t p = problem<moe_router_t>(v[0]);
-    const Rows x = rows(v[1], p.T, p.H, 2, "x"), w = rows(v[2], p.E, p.H, 2, "w");
-    void* logits = flat(v[3], static_cast<int64_t>(p.T) * p.E, 4, "logits");
+    const Type b = type_of(p.dtype);
+    const Rows x = rows(v[1], p.T, p.H, b, "x"), w = rows(v[2], p.E, p.H, b, "w");
+    void* logits = flat(v[3], static_cast<int64_t>(p.T) * p.E, kFloat, "logits");
     const Workspace ws(v[4]);
     const moe_stream_t s = stream_of(v[5]);
     return unlocked([&] {
@@ -161,9 +192,9 @@ PyObject* gemm_fp8_block(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return run(n, 8, [&] {
     const moe_fp8_gemm_t p = problem<moe_fp8_gemm_t>(v[0]);
     const int64_t kb = blocks(p.K);
-    const Rows a = rows(v[1], p.M, p.K, 1, "a"), as = rows(v[2], p.M, kb, 4, "a_scale");
-    const Rows w = rows(v[3], p.N, p.K, 1, "w"), o = rows(v[5], p.M, p.N, size_of(p.out_dtype), "out");
-    void* sw = flat(v[4], blocks(p.N) * kb, 4, "w_scale");
+    const Rows a = rows(v[1], p.M, p.K, kCodes, "a"), as = rows(v[2], p.M, kb, kFloat, "a_scale");
+    const Rows w = rows(v[3], p.N, p.K, kCodes, "w"), o = rows(v[5], p.M, p.N, type_of(p.out_dtype), "out");
+    void* sw = flat(v[4], blocks(p.N) * kb, kFloat, "w_scale");
     const Workspace ws(v[6]);
     const moe_stream_t s = stream_of(v[7]);
     return unlocked([&] {
@@ -178,11 +209,11 @@ PyObject* gemm_fp8_block_swiglu(PyObject*, PyObject* const* v, Py_ssize_t n) {
   return run(n, 9, [&] {
     const moe_fp8_gemm_t p = problem<moe_fp8_gemm_t>(v[0]);
     const int64_t kb = blocks(p.K), N = p.N;
-    const Rows a = rows(v[1], p.M, p.K, 1, "a"), as = rows(v[2], p.M, kb, 4, "a_scale");
-    const Rows w = rows(v[3], 2 * N, p.K, 1, "w13");
-    void* sw = flat(v[4], blocks(2 * N) * kb, 4, "w13_scale");
-    void* codes = flat(v[5], p.M * N, 1, "codes");
-    void* scales = flat(v[6], p.M * (N / 128), 4, "scales");
+    const Rows a = rows(v[1], p.M, p.K, kCodes, "a"), as = rows(v[2], p.M, kb, kFloat, "a_scale");
+    const Rows w = rows(v[3], 2 * N, p.K, kCodes, "w13");
+    void* sw = flat(v[4], blocks(2 * N) * kb, kFloat, "w13_scale");
+    void* codes = flat(v[5], p.M * N, kCodes, "codes");
+    void* scales = flat(v[6], p.M * (N / 128), kFloat, "scales");
     const Workspace ws(v[7]);
     const moe_stream_t s = stream_of(v[8]);
     return unlocked([&] {
@@ -198,10 +229,10 @@ PyObject* forward_few(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const moe_problem_t p = problem<moe_problem_t>(v[0]);
     const moe_weights_t w = problem<moe_weights_t>(v[1]);
     const int64_t T = p.T;
-    void* x = flat(v[2], T * p.H, 2, "x");
-    void* logits = flat(v[3], T * p.E, 4, "logits");
-    void* bias = flat(v[4], p.E, 4, "bias");
-    void* out = flat(v[5], T * p.H, 2, "out");
+    void* x = flat(v[2], T * p.H, kBf16, "x");
+    void* logits = flat(v[3], T * p.E, kFloat, "logits");
+    void* bias = flat(v[4], p.E, kFloat, "bias");
+    void* out = flat(v[5], T * p.H, kBf16, "out");
     const Workspace ws(v[6]);
     const moe_stream_t s = stream_of(v[7]);
     return unlocked([&] {
