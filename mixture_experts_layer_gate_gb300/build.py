@@ -3,11 +3,13 @@
 Each .cu file is compiled in its own nvcc process (in parallel), then linked
 into one shared library with the CUDA runtime linked statically, so the library
 loads on a machine without a GPU (calls then fail with MOE_ERR_CUDA).  Beside it,
-_ops.so: the Python entries of the operators around the layer, against the
-installed PyTorch's headers.
+where PyTorch is installed, _ops.so: the Python entries of the operators around the
+layer, against its headers.
 """
 from __future__ import annotations
 
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -40,6 +42,13 @@ def _stale(obj: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_version() -> str | None:
+    """Of the installed PyTorch, None without one."""
+    if importlib.util.find_spec("torch") is None:
+        return None
+    return importlib.metadata.version("torch")
+
+
 def _ops_command(obj: str) -> list[str]:
     import sysconfig
     import torch
@@ -58,6 +67,25 @@ def _link_ops(obj: str) -> list[str]:
             "-lc10_cuda", "-lc10"]
 
 
+def _start(cmd: list[str], verbose: bool) -> subprocess.Popen:
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
+def _finish(procs: list[tuple[str, subprocess.Popen]], verbose: bool) -> None:
+    failed = []
+    for src, pr in procs:
+        out, _ = pr.communicate()
+        text = out.decode(errors="replace")
+        if pr.returncode != 0:
+            failed.append(f"--- {src}\n{text}")
+        elif verbose and text.strip():
+            print(text, flush=True)
+    if failed:
+        raise RuntimeError("build failed:\n" + "\n".join(failed))
+
+
 def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -69,39 +97,29 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None) -> str:
         o = os.path.join(BUILD, src.replace(".cu", ".o"))
         objs.append(o)
         if _stale(o, [s] + headers):
-            cmd = [cc, *ARCH, *FLAGS, *(extra_flags or []), "-c", s, "-o", o]
-            if verbose:
-                print(" ".join(cmd), flush=True)
-            procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    ops_obj = os.path.join(BUILD, "binding.o")
-    if _stale(ops_obj, [os.path.join(CSRC, "binding.cpp"), headers[-1]]):
-        cmd = _ops_command(ops_obj)
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        procs.append(("binding.cpp", subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    failed = []
-    for src, pr in procs:
-        out, _ = pr.communicate()
-        text = out.decode(errors="replace")
-        if pr.returncode != 0:
-            failed.append((src, text))
-        elif verbose and text.strip():
-            print(text, flush=True)
-    if failed:
-        msg = "\n".join(f"--- {s}\n{t}" for s, t in failed)
-        raise RuntimeError(f"compilation failed:\n{msg}")
-    links = [(LIB, objs, lambda: [cc, *ARCH, "-shared", "-Xlinker", "-soname=libmoe_gb300.so", "-o", LIB, *objs, "-cudart",
-                                  "static"]),
-             (OPS, [ops_obj, LIB], lambda: _link_ops(ops_obj))]
-    for target, deps, command in links:
-        if not _stale(target, deps):
-            continue
-        cmd = command()
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-        if r.returncode != 0:
-            raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
+            procs.append((src, _start([cc, *ARCH, *FLAGS, *(extra_flags or []), "-c", s, "-o", o], verbose)))
+    # The Python entries need PyTorch and fit the one (and the Python) whose headers they saw; the library needs neither.
+    torch_version = _torch_version()
+    ops_obj = os.path.join(BUILD, f"binding-{torch_version}-{sys.implementation.cache_tag}.o")
+    ops_procs = []
+    if torch_version is not None and _stale(ops_obj, [os.path.join(CSRC, "binding.cpp"), headers[-1]]):
+        ops_procs.append(("binding.cpp", _start(_ops_command(ops_obj), verbose)))
+    try:
+        _finish(procs, verbose)
+        if _stale(LIB, objs):
+            _finish([(LIB, _start([cc, *ARCH, "-shared", "-Xlinker", "-soname=libmoe_gb300.so", "-o", LIB, *objs, "-cudart",
+                                   "static"], verbose))], verbose)
+    finally:
+        _finish(ops_procs, verbose)
+    if torch_version is None:
+        print(f"no PyTorch: {os.path.basename(OPS)} is not built", file=sys.stderr)
+        return LIB
+    stamp = os.path.join(BUILD, "_ops.for")
+    fits = os.path.exists(stamp) and open(stamp).read() == os.path.basename(ops_obj)
+    if not fits or _stale(OPS, [ops_obj, LIB]):
+        _finish([(OPS, _start(_link_ops(ops_obj), verbose))], verbose)
+        with open(stamp, "w") as f:
+            f.write(os.path.basename(ops_obj))
     return LIB
 
 
