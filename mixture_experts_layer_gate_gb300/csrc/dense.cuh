@@ -233,6 +233,9 @@ __device__ __forceinline__ float quant_scale(float amax) {
   const float s = __fdiv_rn(amax, 448.0f);
   return s == 0.f ? 1.0f : s;
 }
+// By the fast exponential and division: within (8 + |g|) * 2^-23 of the value (zero
+// below g = -87.3, where it is under 1e-36 u).  With expf M = 4096, K = 7168, N = 2048
+// takes 104.7 us instead of 101.9, with an IEEE division too 113.7.
 __device__ __forceinline__ float swiglu(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float scale) {

@@ -652,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_up_kernel(GateArgs gate, FewA
           v *= s;
           up *= s;
         }
+        // (to about 16 bits, as it is kept: the fast exponential is off by |v| * 2^-23)
         const float act = __fdividef(v, 1.0f + __expf(-v)) * up;
         uint16_t* dst = a.act + static_cast<size_t>(r.slot[x][t]) * 2 * a.I + frag_pos<FMT>(i0 + i, !a.paired);
         if (FMT == kW_FP8 && a.a2 != nullptr) {

@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(32 * kFewWarps<SWIGLU>, SWIGLU ? 1 : 2) fp8_fe
         gate += red[((w * SETS) * 16 + i) * 8 + t];
         up += red[((w * SETS + SETS - 1) * 16 + i) * 8 + t];
       }
-      if (t < p.M) __stcg(p.act + static_cast<int64_t>(t) * p.N + unit * 16 + i, __fdividef(gate, 1.0f + __expf(-gate)) * up);
+      // (the fast exponential's error grows with |gate|; here the full one costs nothing)
+      if (t < p.M) __stcg(p.act + static_cast<int64_t>(t) * p.N + unit * 16 + i, __fdiv_rn(gate, 1.0f + expf(-gate)) * up);
       __threadfence();
     }
     __syncthreads();
