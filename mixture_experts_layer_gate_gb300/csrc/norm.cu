@@ -286,9 +286,10 @@ cudaError_t launch_wide(const NormArgs& a, cudaStream_t s) {
 //   12.9 and 5.6 / 5.4; H = 4096: 456 rows 3.6 / 4.4 and 2.2 / 2.5, 608 rows 5.2 /
 //   4.6 and 3.1 / 2.5; H = 7168: 152 rows 2.7 / 3.3 and 1.9 / 2.0, 304 rows 4.9 / 4.1
 //   and 3.2 / 2.5.
-// Rows that are not 16-byte aligned take one chunk always: two take twice as many
-// small loads to start (H = 2571: 333 rows 4.1 / 7.4 us and 2.4 / 3.7, 4096 rows 30 /
-// 53 and 17 / 22; H = 7167: 4096 rows 103 / 119, but 60 / 49).
+// Rows that are not 16-byte aligned take one chunk whatever their number: two take
+// twice as many small loads to start (H = 2571: 333 rows 4.1 / 7.4 us and 2.4 / 3.7,
+// 4096 rows 30 / 53 and 17 / 22; H = 7167: 4096 rows 103 / 119).  Of long rows for y
+// alone two would be faster (H = 7167: 4096 rows 60 / 49).
 // T = 4096, H = 7168, residual and block codes, event times with 4 us of launch: two
 // chunks, two CTAs an SM 50 us, three 61 (spills), one chunk 52, four chunks 85 (14
 // warps an SM); without the next row's loads in flight 54.  H = 4096: four CTAs an SM
@@ -299,10 +300,12 @@ cudaError_t launch_shape(const NormArgs& a, cudaStream_t s) {
   if (chunks <= 32) return launch_warp<T, W, VEC, 1>(a, s);
   if (chunks <= 64) return launch_warp<T, W, VEC, 2>(a, s);
   if (chunks <= 128) return launch_warp<T, W, VEC, 4>(a, s);
-  const int rows = 1536 / ((chunks + 31) / 32 * 32);  // of one chunk a thread that an SM holds
-  if (chunks <= 1024 && (!VEC || a.T <= rows * a.sms)) return launch_wide<T, W, VEC, 1>(a, s);
-  if (chunks <= 1024) return launch_wide<T, W, VEC, 2>(a, s);
-  return launch_wide<T, W, VEC, 4>(a, s);
+  if (chunks > 1024) return launch_wide<T, W, VEC, 4>(a, s);
+  if constexpr (VEC) {
+    const int rows = 1536 / ((chunks + 31) / 32 * 32);  // of one chunk a thread that an SM holds
+    if (a.T > rows * a.sms) return launch_wide<T, W, VEC, 2>(a, s);
+  }
+  return launch_wide<T, W, VEC, 1>(a, s);
 }
 
 template <typename T, typename W>
