@@ -2,9 +2,9 @@
 // float.  A batch goes through the dense kernel with 16-bit operands (bound by
 // the reads of x and the tiles' repeated reads through L2: T = 4096, H = 7168,
 // 256 experts 20 us, of which x is 8.6 us of DRAM time).  Up to 8 tokens, where
-// only latency counts, a CTA takes an expert: all of its row is in flight at
-// once, and the threads' sums are joined in a fixed order (T = 1, H = 7168, 256
-// experts: 1.8 us in a graph, 2 tokens 2.0, 4 tokens 2.8, 8 tokens 4.3).
+// only latency counts, a CTA takes an expert, 128 threads a token, and the threads'
+// sums are joined in a fixed order (T = 1, H = 7168, 256 experts: 2.0 us in a graph, 2
+// tokens 2.2, 4 tokens 2.9, 8 tokens 4.4).
 #include "dense.cuh"
 
 namespace moe {
@@ -25,8 +25,10 @@ __device__ __forceinline__ float2 pair_f32<__half2>(uint32_t v) {
 }
 
 // Threads kFewThreads t .. take token t; the weight row that they share comes from
-// L2 once a CTA.  At most TMAX tokens: the fewer, the more registers for loads in
-// flight (one token, H = 7168, 256 experts: 1.8 us; as one of eight 2.3 us).
+// L2 once a CTA.  At most TMAX tokens: bounded to a CTA of one or two tokens the
+// kernel is faster than bounded to eight (H = 7168, 256 experts: one token 2.0 and
+// 2.5 us, two 2.2 and 2.6, in a graph), to four it is not (2.9 both), with about 32
+// registers a thread in each, so that the sixteen loads are not all in flight at once.
 template <typename T2, int TMAX>
 __global__ void __launch_bounds__(kFewThreads * TMAX) router_few_kernel(RouterArgs a) {
   __shared__ float part[TMAX][kFewThreads / 32];
@@ -72,7 +74,6 @@ cudaError_t launch_few(const RouterArgs& a, cudaStream_t s) {
   const dim3 grid(a.E), block(kFewThreads * a.T);
   if (a.T == 1) return launch_pdl(router_few_kernel<T2, 1>, grid, block, 0, s, a);
   if (a.T == 2) return launch_pdl(router_few_kernel<T2, 2>, grid, block, 0, s, a);
-  if (a.T <= 4) return launch_pdl(router_few_kernel<T2, 4>, grid, block, 0, s, a);
   return launch_pdl(router_few_kernel<T2, kFewTokens>, grid, block, 0, s, a);
 }
 
