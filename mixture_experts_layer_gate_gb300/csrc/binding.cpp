@@ -57,8 +57,14 @@ bool is_of(const at::Tensor& t, const Type& type) {
   const at::ScalarType s = t.scalar_type();
   return s == type.first || s == type.second || type.first == at::ScalarType::Undefined;
 }
-// the kernels are launched on the current device
-bool is_here(const at::Tensor& t) { return t.is_cuda() && t.device().index() == c10::cuda::current_device(); }
+// The kernels are launched on the current device, which a call looks up once (for
+// each of seven tensors: 0.3 us).
+thread_local int device_of_call = -1;
+int current_device() {
+  if (device_of_call < 0) device_of_call = c10::cuda::current_device();
+  return device_of_call;
+}
+bool is_here(const at::Tensor& t) { return t.is_cuda() && t.get_device() == current_device(); }
 
 struct Rows {
   void* p = nullptr;
@@ -116,7 +122,7 @@ T problem(PyObject* o) {
 
 // the given raw stream, or the current one of the current device
 moe_stream_t stream_of(PyObject* o) {
-  if (o == Py_None) return reinterpret_cast<moe_stream_t>(c10::cuda::getCurrentCUDAStream().stream());
+  if (o == Py_None) return reinterpret_cast<moe_stream_t>(c10::cuda::getCurrentCUDAStream(current_device()).stream());
   PyObject* i = PyNumber_Long(o);
   if (i == nullptr) throw Refused();
   const unsigned long long v = PyLong_AsUnsignedLongLong(i);
@@ -134,6 +140,7 @@ PyObject* run(Py_ssize_t given, Py_ssize_t wanted, Fn&& f) {
     PyErr_Format(PyExc_TypeError, "%zd arguments", wanted);
     return nullptr;
   }
+  device_of_call = -1;
   try {
     return PyLong_FromLong(f());
   } catch (const Refused&) {
