@@ -478,18 +478,19 @@ moe_status_t moe_gemm_fp8_block_swiglu(const moe_fp8_gemm_t* g, const void* a, i
                                        float* scales, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /* The whole layer for a few tokens (T <= MOE_FEW_MAX_TOKENS and T * (H + 32) <=
- * 65792, with int4 weights also T * (H + 32) + H / 8 <= 68000, which any H <= 8192
- * meets, else MOE_ERR_UNSUPPORTED): arguments, weight formats and meaning of moe_forward,
- * in two launches that stream the chosen experts' weights once.  All sums are
- * held in float and nothing is rounded between the gate and out: the SwiGLU
- * output stays float, int4 / int8 weights enter as (code - zero) * scale
- * unrounded, and y is not rounded per expert, so results differ from
- * moe_forward's by its roundings.  fp8 experts take activations as their codes,
- * e4m3(x / a1) and e4m3(act / a2); dynamic scales are max |x| / 448 and
- * max |act| / 448 over the call (1 where that is 0), the quotient by the latter to
- * within a float's last bits.  int4 / int8 scales and zero
- * points are 4-byte aligned.  The workspace holds moe_few_workspace_size()
- * bytes (0 for an invalid problem or one beyond the limit). */
+ * 65792, with int4 weights also T * (H + 32) + H / 8 <= 68000, which any H <=
+ * 8192 meets, else MOE_ERR_UNSUPPORTED): arguments, weight formats and meaning
+ * of moe_forward, in two launches that stream the chosen experts' weights once.
+ * All sums are held in float and nothing is rounded to bf16 between the gate
+ * and out: the SwiGLU output is kept as two bf16 that add up to it within
+ * 2^-16, int4 / int8 weights enter as (code - zero) * scale unrounded, and y is
+ * not rounded per expert, so results differ from moe_forward's by its
+ * roundings.  fp8 experts take activations as their codes, e4m3(x / a1) and
+ * e4m3(act / a2); dynamic scales are max |x| / 448 and max |act| / 448 over the
+ * call (1 where that is 0), the quotient by the latter to within a float's last
+ * bits.  int4 / int8 scales and zero points are 4-byte aligned.  The workspace
+ * holds moe_few_workspace_size() bytes (0 for an invalid problem or one beyond
+ * the limit). */
 #define MOE_FEW_MAX_TOKENS 8
 size_t moe_few_workspace_size(const moe_problem_t* p);
 moe_status_t moe_forward_few(const moe_problem_t* p, const moe_weights_t* w, const void* x,

@@ -22,8 +22,9 @@
 // gate for itself (one warp per token).  down: a CTA takes 16 rows of H and its
 // warps the chosen experts' K axes laid end to end, so the weighted sum over
 // experts needs no second pass.  The activations pass between the two in 32
-// bits: as a bf16 and the bf16 of what that left over (two MMAs), or for fp8
-// as the format's codes.
+// bits, but not as a float: as a bf16 and the bf16 of what that left over (two MMAs
+// and no conversion; together within 2^-16 of the value, where out is rounded to
+// 2^-8 in the end), or for fp8 as the format's codes.
 #include <float.h>
 
 #include <algorithm>
@@ -267,8 +268,8 @@ __device__ __forceinline__ uint32_t ordered(float v) {
 
 // The k best of the warp's keys (32 strided experts per register, 0: out of the
 // running), ties to the lower expert: lane j returns the j-th expert, -1 where
-// fewer were in the running.  A lane keeps the best of its own; a round is two warp reductions, after which the
-// winner's lane looks for its next.
+// fewer were in the running.  A lane keeps the best of its own; a round is two warp
+// reductions, after which the winner's lane looks for its next.
 template <int EPL>
 __device__ __forceinline__ int best_k(uint32_t (&key)[EPL], int k, int lane) {
   int mine = 0;

@@ -14,10 +14,12 @@
 // clusters start late and did not all fit with 16 warps a CTA).
 // Else a CTA goes through blocks of 16 rows.
 //
-// In a graph: SwiGLU, K = 7168, N = 2048 (29 MB) one row 9.5 us, 3.1 TB/s, eight rows
-// 10.3, the general kernel 13; K = 2048, N = 7168 (14.7 MB) one row 4.0 us, 3.7 TB/s,
-// the general kernel 6: the stream, not the products, sets the time, and of it the
-// start of the loads and the join at the end are half.
+// In a graph, the weights in L2 / from memory (as many copies in turn as L2 does not
+// hold): SwiGLU, K = 7168, N = 2048 (29 MB) one row 9.5 / 10.7 us, 2.7 TB/s, eight rows
+// 10.2 / 10.8, the general kernel 13 (in L2); K = 2048, N = 7168 (14.7 MB) one row 4.1 /
+// 4.5 us, 3.3 TB/s, eight rows 5.2 / 5.8, the general kernel 7 (16 rows, in L2): the
+// stream, not the products, sets the time, and of it the start of the loads and the
+// join at the end are half.
 #include <algorithm>
 
 #include "common.cuh"
@@ -262,9 +264,9 @@ cudaError_t launch_fp8_few(const Fp8GemmArgs& p, cudaStream_t s) {
   const int units = (p.N + 15) / 16;
   const int third = depth_of<false>(p, kThirdSmem);
   // Three CTAs an SM where that takes an SM's units in better balance, or nearly as
-  // good: 3 / 2 CTAs, one row, N x K = 7168 x 2048 (3 / 4 units an SM) 5.2 / 6.1 us,
-  // 14336 x 4096 (6 / 6) 11.9 / 13.1, 16384 x 7168 (9 / 8) 22.9 / 24.0, 9000 x 1104 (6 /
-  // 4) 5.5 / 5.1
+  // good: 3 / 2 CTAs, one row, weights from memory, N x K = 7168 x 2048 (3 / 4 units an
+  // SM) 4.5 / 5.7 us, 14336 x 4096 (6 / 6) 12.0 / 13.1, 16384 x 7168 (9 / 8) 23.4 / 24.3,
+  // 9000 x 1104 (6 / 4) 5.4 / 4.7
   const int on3 = 3 * ((units + 3 * di.sms - 1) / (3 * di.sms)), on2 = 2 * ((units + 2 * di.sms - 1) / (2 * di.sms));
   if (units > 2 * di.sms && 4 * on3 <= 5 * on2 && third >= 3)
     return launch<false>(p, third, std::min(units, 3 * di.sms), s);
