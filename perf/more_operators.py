@@ -74,6 +74,11 @@ def _heads(rng):
     return Hkv * rng.choice([1, 2, 4, 5, 7, 8]), Hkv, rng.choice([64, 128, 128, 128, _log(rng, 1, 16) * 8])
 
 
+def _depth(D, cache):
+    """Rows of a cache are whole pieces of 16 bytes."""
+    return -(-D // 16) * 16 if cache == "e4m3" else D
+
+
 def draw(rng):
     op = rng.choice(["linear", "rope", "paged", "paged", "paged", "prompt"])
     dtype = rng.choice(["bf16", "f16"])
@@ -86,12 +91,13 @@ def draw(rng):
     if op == "rope":
         layout = rng.choice(["half", "interleaved"])
         rot = max(16, D // rng.choice([1, 1, 2, 4]) // 16 * 16)
-        D = max(D, rot)
+        cache = rng.choice([dtype, "e4m3"])
+        D = _depth(max(D, rot), cache)
         T = min(_log(rng, 1, 4096), 4096 * 40 * 128 // ((Hq + Hkv) * D))
         return dict(op=op, T=T, Hq=Hq, Hkv=Hkv, D=D, rot=rot, layout=layout, dtype=dtype, norm=rng.random() < 0.7,
                     wdtype=rng.choice(["f32", dtype]), far=rng.choice([0, 0, 5000, 1_000_000]),
                     factor=rng.choice([1.0, 8.0, 32.0]), page=rng.choice([16, 32, 64, 256]),
-                    cache=rng.choice([dtype, "e4m3"]), order=rng.choice(["token", "head"]), skip=rng.random() < 0.3)
+                    cache=cache, order=rng.choice(["token", "head"]), skip=rng.random() < 0.3)
     if op == "prompt":
         hi = _log(rng, 1, 7001)
         return dict(op=op, B=rng.randint(1, 4), new=_log(rng, 1, hi), new_hi=hi, Hq=Hq // Hkv * min(Hkv, 4),
@@ -103,8 +109,9 @@ def draw(rng):
         B //= 2
     most = min(131071, 1_600_000 // (B * Hkv), int(1.7e9 / (B * new_hi * Hq)))
     past_hi = _log(rng, 1, max(1, most))
+    cache = rng.choice([dtype, "e4m3"])
     return dict(op=op, B=B, new=_log(rng, 1, new_hi), new_hi=new_hi, past=_log(rng, 1, past_hi), past_hi=past_hi,
-                Hq=Hq, Hkv=Hkv, D=D, dtype=dtype, cache=rng.choice([dtype, "e4m3"]),
+                Hq=Hq, Hkv=Hkv, D=_depth(D, cache), dtype=dtype, cache=cache,
                 page=rng.choice([16, 32, 64, 256]), order=rng.choice(["token", "head"]), spare=rng.choice([0, 0, 3]))
 
 
