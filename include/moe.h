@@ -497,6 +497,72 @@ moe_status_t moe_forward_few(const moe_problem_t* p, const moe_weights_t* w, con
                              const float* logits, const float* bias, void* out, void* ws,
                              size_t ws_bytes, moe_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The attention half of a decoder block: projections (moe_linear), norms of the
+ * query and key heads with the rotation of their positions, which write the new
+ * keys and values into a paged cache (moe_qk_norm_rope), and attention of the new
+ * tokens over that cache (moe_paged_attention) or over the packed prompts
+ * themselves (moe_prompt_attention).  The conventions at the top hold; a
+ * workspace serves one stream's calls at a time. */
+
+/* A paged cache of num_pages pages of page_size tokens (a power of two, 16 to
+ * 1024), Hkv heads of D values each.  k and v point to [num_pages, page_size, Hkv,
+ * D] values of the cache's type, with strides in elements between pages, tokens
+ * and heads (a head's D values are adjacent; every stride and the base are
+ * multiples of 16 bytes; any order in memory, e.g. [num_pages, Hkv, page_size, D]).
+ * 8-bit caches hold e4m3 codes (D % 16 == 0) and k_scale, v_scale: float
+ * [num_pages, Hkv, page_size], contiguous, 16-byte aligned; a value is code *
+ * scale.  Else k_scale and v_scale are NULL. */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t k_page_stride, k_token_stride, k_head_stride;
+  int64_t v_page_stride, v_token_stride, v_head_stride;
+} moe_kv_t;
+
+#define MOE_CACHE_SAME 0 /* values of the problem's dtype */
+#define MOE_CACHE_E4M3 1 /* e4m3 codes with a scale per token and head */
+
+/* T tokens with Hq query heads and Hkv key and value heads of D values (D % 8 ==
+ * 0, 8 <= D <= 256), of which the first rot (even, 0 <= rot <= D) are rotated. */
+typedef struct {
+  int32_t T, Hq, Hkv, D, rot;
+  int32_t interleaved;  /* rotated pairs: 0 (i, i + rot / 2), 1 (2 i, 2 i + 1) */
+  int32_t dtype;        /* MOE_T_BF16 or MOE_T_F16, of q, k, v and the outputs */
+  int32_t weight_dtype; /* of the norms' weights: dtype or MOE_T_F32 */
+  int32_t cache_dtype;  /* MOE_CACHE_SAME or MOE_CACHE_E4M3 */
+  int32_t page_size;    /* 0: no cache */
+  int32_t num_pages;
+  float eps;            /* >= 0 */
+  float magnitude;      /* factor of the rotated values (1: none) */
+} moe_rope_t;
+
+/* For each token t and query or key head:
+ *   v = x / sqrt(mean(x^2) + eps) * weight  (x itself where the weight is NULL)
+ *   (a, b) = (a cos - b sin, b cos + a sin) * magnitude over the rotated pairs i,
+ *     angle = 2 pi * (positions[t] * turns[i] mod 2^64) / 2^64
+ * in float, rounded once into q_out, k_out and the cache.  turns (uint64 [rot /
+ * 2]) holds what a pair turns a position in 2^-64 of a full turn, so that angles
+ * of any position are exact to float; positions int32 [T].
+ *   q, q_out   [T, Hq * D] rows (q_out may be q with its stride)
+ *   k, v       [T, Hkv * D] rows; k_out likewise or NULL (may be k)
+ *   cache      or NULL (then page_size is 0, and v and slots are not read):
+ *     token t's keys and values go to slot slots[t] = page * page_size + place
+ *     (int32 [T]; negative: not stored; one beyond the cache is recorded as
+ *     MOE_ERR_DEVICE_BAD_INDEX and not stored; two tokens of a call have
+ *     different slots).  8-bit: scale = max |v| / 448 over the head's values, 1
+ *     where that is 0, code = e4m3(v / scale), from the unrounded v.
+ * At least one of k_out and cache is given.  Rows are 16-byte aligned, strides
+ * multiples of 8.  ws: 256 bytes (the error header). */
+moe_status_t moe_qk_norm_rope(const moe_rope_t* r, const void* q, int64_t q_stride, const void* k,
+                              int64_t k_stride, const void* v, int64_t v_stride, const int32_t* positions,
+                              const uint64_t* turns, const void* q_weight, const void* k_weight,
+                              void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                              const moe_kv_t* cache, const int32_t* slots, void* ws, size_t ws_bytes,
+                              moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

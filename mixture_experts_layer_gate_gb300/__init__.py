@@ -11,5 +11,6 @@ from .binding import (MoEError, Problem, Plan, Weights, MoELayer, load, problem,
                       LIB_PATH, set_tuning, tuning, TUNING_KNOBS, repack_int4, NormProblem, RouterProblem, Fp8GemmProblem,
                       norm_problem, router_problem, fp8_gemm_problem, alloc_op_workspace, add_rms_norm,
                       router_logits, gemm_fp8_block, gemm_fp8_block_swiglu, few_workspace_size,
-                      alloc_few_workspace, forward_few, FEW_MAX_TOKENS)
+                      alloc_few_workspace, forward_few, FEW_MAX_TOKENS, RopeProblem, rope_problem, rope_table,
+                      qk_norm_rope)
 from .block import MoEBlock, SharedExpert

@@ -26,12 +26,13 @@ EXPORTED = ("moe_scratch_size", "moe_workspace_size", "moe_padded_capacity", "mo
             "moe_status_string", "moe_get_plan", "moe_get_plan_for_sms", "moe_align_permute_noalloc",
             "moe_dynamic_scales", "moe_launch_count", "moe_set_tuning", "moe_repack_int4",
             "moe_add_rms_norm", "moe_router_logits", "moe_gemm_fp8_block", "moe_gemm_fp8_block_swiglu",
-            "moe_few_workspace_size", "moe_forward_few")
+            "moe_few_workspace_size", "moe_forward_few", "moe_qk_norm_rope")
 
 DTYPES = {"bf16": 0, "f16": 1, "f32": 2}
 QUANTS = {"none": 0, "block": 1, "token": 2}
 OP_WORKSPACE_BYTES = 256 + 4096 + 4 * 8 * 16384
 FEW_MAX_TOKENS = 8
+LAYOUTS = {"half": 0, "interleaved": 1}
 
 
 class MoEError(RuntimeError):
@@ -92,6 +93,19 @@ class Fp8GemmProblem(ctypes.Structure):
                 ("accumulate", ctypes.c_int32)]
 
 
+class KvStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in (
+                    "k_page_stride", "k_token_stride", "k_head_stride", "v_page_stride", "v_token_stride",
+                    "v_head_stride")]
+
+
+class RopeProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "Hq", "Hkv", "D", "rot", "interleaved", "dtype", "weight_dtype",
+                                             "cache_dtype", "page_size", "num_pages")] + [
+        ("eps", ctypes.c_float), ("magnitude", ctypes.c_float)]
+
+
 TUNING_KNOBS = tuple(n for n, _ in Tuning._fields_)
 
 _lib = None
@@ -136,6 +150,8 @@ def load(path: str = LIB_PATH):
                                            sz, vp]),
         "moe_few_workspace_size": (sz, [P]),
         "moe_forward_few": (st, [P, ctypes.POINTER(WeightsStruct), vp, vp, vp, vp, vp, sz, vp]),
+        "moe_qk_norm_rope": (st, [ctypes.POINTER(RopeProblem), vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp,
+                                  i64, ctypes.POINTER(KvStruct), vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -443,6 +459,68 @@ def alloc_few_workspace(p: Problem, device):
 def forward_few(p: Problem, w: Weights, x, logits, bias, out, ws, stream=None):
     """moe_forward_few: the whole layer for at most FEW_MAX_TOKENS tokens in two launches."""
     _check((_ops or _native()).forward_few(p, w.struct, x, logits, bias, out, ws, stream), "moe_forward_few")
+
+
+# ------------------------------------------------- the attention half of a block
+
+
+def _cache_code(cache_dtype, dtype) -> int:
+    """MOE_CACHE_SAME or MOE_CACHE_E4M3 of a cache of dtype's values or "e4m3"."""
+    if cache_dtype == "e4m3":
+        return 1
+    if cache_dtype not in (None, dtype):
+        raise ValueError(f"cache_dtype: {dtype!r} or 'e4m3'")
+    return 0
+
+
+def rope_problem(T, Hq, Hkv, D, rot=None, layout="half", dtype="bf16", weight_dtype=None, eps=1e-6, magnitude=1.0,
+                 cache_dtype=None, page_size=0, num_pages=0) -> RopeProblem:
+    """T tokens of Hq query and Hkv key and value heads of D values for qk_norm_rope; rot (all D without it) of them
+    are rotated, as pairs (i, i + rot / 2) ("half") or (2 i, 2 i + 1) ("interleaved").  With page_size and num_pages
+    keys and values go to a paged cache, of dtype's values or "e4m3"."""
+    return RopeProblem(int(T), int(Hq), int(Hkv), int(D), int(D if rot is None else rot), LAYOUTS[layout],
+                       DTYPES[dtype], DTYPES[weight_dtype or dtype], _cache_code(cache_dtype, dtype), int(page_size),
+                       int(num_pages), float(eps), float(magnitude))
+
+
+def rope_table(rot, theta=10000.0, factor=1.0, original=0, low=1.0, high=1.0, inv_freq=None, device=None):
+    """The turns of qk_norm_rope (int64 [rot / 2], in 2^-64 of a turn a position): pair i turns theta^(-2 i / rot)
+    radians a position (or inv_freq[i], float64), for a context stretched `factor` times as g f + (1 - g) f / factor.
+    Without `original` g = 0: every frequency is divided.  With it, g goes from 0 for pairs of at most `low` turns over
+    the `original` positions to 1 for those of `high` and more."""
+    import math
+
+    import torch
+    if rot < 0 or rot % 2 or not (factor > 0 and math.isfinite(factor)):
+        raise ValueError("rope_table: an even rot and a positive factor")
+    if inv_freq is None:
+        freq = [float(theta) ** (-2.0 * i / rot) for i in range(rot // 2)]
+    else:
+        freq = [float(f) for f in inv_freq]
+    if len(freq) != rot // 2 or not all(math.isfinite(f) for f in freq):
+        raise ValueError("rope_table: rot / 2 finite frequencies")
+    table = []
+    for f in freq:
+        keep = 0.0
+        if factor == 1.0:
+            keep = 1.0
+        elif original:
+            seen = original * f / (2.0 * math.pi)
+            keep = min(1.0, max(0.0, (seen - low) / (high - low))) if high > low else float(seen >= high)
+        turn = (keep * f + (1.0 - keep) * f / factor) / (2.0 * math.pi)
+        whole = int((turn - math.floor(turn)) * 2.0 ** 64) % 2 ** 64
+        table.append(whole - 2 ** 64 if whole >= 2 ** 63 else whole)
+    return torch.tensor(table, dtype=torch.int64, device=device)
+
+
+def qk_norm_rope(r: RopeProblem, q, k, positions, turns, q_out, ws, k_out=None, v=None, k_cache=None, v_cache=None,
+                 slots=None, k_scale=None, v_scale=None, q_weight=None, k_weight=None, stream=None):
+    """moe_qk_norm_rope.  q, q_out [T, Hq * D] and k, v, k_out [T, Hkv * D] of r's dtype (rows may be strided; outputs
+    may be the inputs), positions int32 [T], turns of rope_table; weights [D] or None; k_cache, v_cache [num_pages,
+    page_size, Hkv, D] of any order in memory with slots int32 [T], and for "e4m3" k_scale, v_scale float32 [num_pages,
+    Hkv, page_size]."""
+    _check((_ops or _native()).qk_norm_rope(r, q, k, v, positions, turns, q_weight, k_weight, q_out, k_out, k_cache,
+                                            v_cache, k_scale, v_scale, slots, ws, stream), "moe_qk_norm_rope")
 
 
 def workspace_of(owner, name: str, n: int, allocate):

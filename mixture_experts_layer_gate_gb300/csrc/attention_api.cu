@@ -1,0 +1,118 @@
+// Host side of the attention half's operators declared in include/moe.h: argument
+// checks and launches.
+#include <cmath>
+
+#include "../../include/moe.h"
+#include "checks.h"
+#include "common.cuh"
+#include "kernels.h"
+
+using namespace moe;
+
+namespace {
+
+bool page_size_ok(int n) { return n >= 16 && n <= 1024 && (n & (n - 1)) == 0; }
+int shift_of(int n) {
+  int s = 0;
+  while ((1 << s) < n) ++s;
+  return s;
+}
+
+// The cache's pointers and strides; of one page, token or head the stride is not used.
+moe_status_t check_cache(const moe_kv_t* c, int cache_dtype, int Hkv, int D, int page_size, int num_pages, KvCache* out) {
+  if (c == nullptr || cache_dtype < MOE_CACHE_SAME || cache_dtype > MOE_CACHE_E4M3) return MOE_ERR_INVALID_ARG;
+  if (!page_size_ok(page_size) || num_pages < 1) return MOE_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(num_pages) * page_size > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  const bool e4m3 = cache_dtype == MOE_CACHE_E4M3;
+  const int64_t unit = e4m3 ? 16 : 8;
+  if (D % unit != 0 || !aligned(c->k, 16) || !aligned(c->v, 16) || c->k == nullptr || c->v == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  const int64_t strides[2][3] = {{c->k_page_stride, c->k_token_stride, c->k_head_stride},
+                                 {c->v_page_stride, c->v_token_stride, c->v_head_stride}};
+  const int64_t counts[3] = {num_pages, page_size, Hkv};
+  for (const auto& s : strides)
+    for (int i = 0; i < 3; ++i)
+      if (counts[i] > 1 && (s[i] < D || s[i] % unit != 0 || s[i] > (1ll << 37))) return MOE_ERR_INVALID_ARG;
+  if (e4m3 != (c->k_scale != nullptr) || e4m3 != (c->v_scale != nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(c->k_scale, 16) || !aligned(c->v_scale, 16)) return MOE_ERR_INVALID_ARG;
+  auto used = [&](int i, int64_t s) { return counts[i] > 1 ? s : static_cast<int64_t>(unit); };
+  *out = {static_cast<uint8_t*>(c->k),  static_cast<uint8_t*>(c->v),  c->k_scale,
+          c->v_scale,                   used(0, c->k_page_stride),    used(1, c->k_token_stride),
+          used(2, c->k_head_stride),    used(0, c->v_page_stride),    used(1, c->v_token_stride),
+          used(2, c->v_head_stride)};
+  return MOE_OK;
+}
+
+bool half_dtype(int d) { return d == MOE_T_BF16 || d == MOE_T_F16; }
+
+// 16-byte aligned rows of 16-bit values
+bool wide_rows(const void* p, int64_t stride, int64_t cols) { return rows_ok(p, stride, cols, 16) && stride % 8 == 0; }
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_qk_norm_rope(const moe_rope_t* r, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                              const void* v, int64_t v_stride, const int32_t* positions, const uint64_t* turns,
+                              const void* q_weight, const void* k_weight, void* q_out, int64_t q_out_stride,
+                              void* k_out, int64_t k_out_stride, const moe_kv_t* cache, const int32_t* slots, void* ws,
+                              size_t ws_bytes, moe_stream_t stream) {
+  if (r == nullptr || r->T < 0 || r->Hq < 1 || r->Hkv < 1 || r->D < 8 || r->D % 8 != 0) return MOE_ERR_INVALID_ARG;
+  if (r->rot < 0 || r->rot > r->D || r->rot % 2 != 0) return MOE_ERR_INVALID_ARG;
+  if (r->interleaved != 0 && r->interleaved != 1) return MOE_ERR_INVALID_ARG;
+  if (!half_dtype(r->dtype) || (r->weight_dtype != r->dtype && r->weight_dtype != MOE_T_F32)) return MOE_ERR_INVALID_ARG;
+  if (!(r->eps >= 0.f) || !std::isfinite(r->eps) || !std::isfinite(r->magnitude)) return MOE_ERR_INVALID_ARG;
+  if (r->D > 256 || r->Hq > 4096 || r->Hkv > 4096 || r->T > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+  MOE_TRY(check_header(ws, ws_bytes));
+  RopeArgs a = {};
+  if (cache != nullptr) {
+    MOE_TRY(check_cache(cache, r->cache_dtype, r->Hkv, r->D, r->page_size, r->num_pages, &a.cache));
+  } else if (r->page_size != 0 || k_out == nullptr) {
+    return MOE_ERR_INVALID_ARG;
+  }
+  if (r->T == 0) return MOE_OK;
+  const int64_t nq = static_cast<int64_t>(r->Hq) * r->D, nk = static_cast<int64_t>(r->Hkv) * r->D;
+  if (!wide_rows(q, q_stride, nq) || !wide_rows(k, k_stride, nk) || !wide_rows(q_out, q_out_stride, nq))
+    return MOE_ERR_INVALID_ARG;
+  if (k_out != nullptr && !wide_rows(k_out, k_out_stride, nk)) return MOE_ERR_INVALID_ARG;
+  if ((q_out == q && q_out_stride != q_stride) || (k_out == k && k_out_stride != k_stride)) return MOE_ERR_INVALID_ARG;
+  if (cache != nullptr && (!wide_rows(v, v_stride, nk) || slots == nullptr || !aligned(slots, 4)))
+    return MOE_ERR_INVALID_ARG;
+  if (r->rot > 0 && (positions == nullptr || !aligned(positions, 4) || turns == nullptr || !aligned(turns, 8)))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(q_weight, 16) || !aligned(k_weight, 16)) return MOE_ERR_INVALID_ARG;
+  DeviceInfo di;
+  if (device_info(&di) != cudaSuccess) return MOE_ERR_CUDA;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.positions = positions;
+  a.turns = turns;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.slots = slots;
+  a.err = static_cast<uint32_t*>(ws);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_out_stride = q_out_stride;
+  a.k_out_stride = k_out_stride;
+  a.capacity = static_cast<int64_t>(r->num_pages) * r->page_size;
+  a.T = r->T;
+  a.Hq = r->Hq;
+  a.Hkv = r->Hkv;
+  a.D = r->D;
+  a.rot = r->rot;
+  a.interleaved = r->interleaved;
+  a.weight_f32 = r->weight_dtype == MOE_T_F32;
+  a.e4m3 = cache != nullptr && r->cache_dtype == MOE_CACHE_E4M3;
+  a.page_shift = cache != nullptr ? shift_of(r->page_size) : 0;
+  a.sms = di.sms;
+  a.eps = r->eps;
+  a.magnitude = r->magnitude;
+  return cuda_status(launch_rope(a, r->dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -37,6 +37,7 @@ struct Type {
   Type(at::ScalarType t, at::ScalarType u) : first(t), second(u) {}
 };
 const Type kFloat(at::ScalarType::Float), kBf16(at::ScalarType::BFloat16);
+const Type kInt32(at::ScalarType::Int), kInt64(at::ScalarType::Long);
 const Type kCodes(at::ScalarType::Byte, at::ScalarType::Float8_e4m3fn);
 
 // of a moe_dtype_t; one that is none is left to the C call, which refuses it
@@ -248,9 +249,66 @@ PyObject* forward_few(PyObject*, PyObject* const* v, Py_ssize_t n) {
   });
 }
 
+// A paged cache: k and v [num_pages, page_size, Hkv, D] of any order in memory, the
+// scales [num_pages, Hkv, page_size]; false where there is none.
+bool cache_of(PyObject* const* o, int dtype, int cache_dtype, int64_t pages, int64_t page, int64_t heads, int64_t D,
+              moe_kv_t* c) {
+  if (o[0] == Py_None && o[1] == Py_None) {
+    if (o[2] != Py_None || o[3] != Py_None) refuse("k_scale, v_scale: only with a cache");
+    return false;
+  }
+  const bool e4m3 = cache_dtype == MOE_CACHE_E4M3;
+  const Type type = e4m3 ? kCodes : type_of(dtype);
+  int64_t strides[2][3];
+  void* p[2];
+  const char* names[2] = {"k_cache", "v_cache"};
+  for (int i = 0; i < 2; ++i) {
+    const at::Tensor& t = tensor(o[i], names[i]);
+    if (t.dim() != 4 || t.size(0) != pages || t.size(1) != page || t.size(2) != heads || t.size(3) != D ||
+        !is_of(t, type) || !is_here(t))
+      refuse(std::string(names[i]) + ": a tensor [" + std::to_string(pages) + ", " + std::to_string(page) + ", " +
+             std::to_string(heads) + ", " + std::to_string(D) + "] of " + name_of(type) + " on the current CUDA device");
+    if (t.stride(3) != 1) refuse(std::string(names[i]) + ": adjacent values of a head");
+    for (int d = 0; d < 3; ++d) strides[i][d] = t.stride(d);
+    p[i] = t.data_ptr();
+  }
+  *c = {p[0],
+        p[1],
+        static_cast<float*>(flat(o[2], pages * heads * page, kFloat, "k_scale")),
+        static_cast<float*>(flat(o[3], pages * heads * page, kFloat, "v_scale")),
+        strides[0][0], strides[0][1], strides[0][2], strides[1][0], strides[1][1], strides[1][2]};
+  return true;
+}
+
+// problem, q, k, v, positions, turns, q_weight, k_weight, q_out, k_out, k_cache, v_cache, k_scale, v_scale, slots,
+// ws, stream
+PyObject* qk_norm_rope(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return run(n, 17, [&] {
+    const moe_rope_t p = problem<moe_rope_t>(v[0]);
+    const int64_t T = p.T, nq = static_cast<int64_t>(p.Hq) * p.D, nk = static_cast<int64_t>(p.Hkv) * p.D;
+    const Type b = type_of(p.dtype), wt = type_of(p.weight_dtype);
+    const Rows q = rows(v[1], T, nq, b, "q"), k = rows(v[2], T, nk, b, "k"), val = rows(v[3], T, nk, b, "v");
+    void* pos = flat(v[4], T, kInt32, "positions");
+    void* turns = flat(v[5], p.rot / 2, kInt64, "turns");
+    void* qw = flat(v[6], p.D, wt, "q_weight");
+    void* kw = flat(v[7], p.D, wt, "k_weight");
+    const Rows qo = rows(v[8], T, nq, b, "q_out"), ko = rows(v[9], T, nk, b, "k_out");
+    moe_kv_t c{};
+    const bool cached = cache_of(v + 10, p.dtype, p.cache_dtype, p.num_pages, p.page_size, p.Hkv, p.D, &c);
+    void* slots = flat(v[14], T, kInt32, "slots");
+    const Workspace ws(v[15]);
+    const moe_stream_t s = stream_of(v[16]);
+    return unlocked([&] {
+      return moe_qk_norm_rope(&p, q.p, q.stride, k.p, k.stride, val.p, val.stride, static_cast<int32_t*>(pos),
+                              static_cast<uint64_t*>(turns), qw, kw, qo.p, qo.stride, ko.p, ko.stride,
+                              cached ? &c : nullptr, static_cast<int32_t*>(slots), ws.p, ws.bytes, s);
+    });
+  });
+}
+
 #define ENTRY(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(add_rms_norm), ENTRY(router_logits), ENTRY(gemm_fp8_block), ENTRY(gemm_fp8_block_swiglu),
-                         ENTRY(forward_few), {nullptr, nullptr, 0, nullptr}};
+                         ENTRY(forward_few), ENTRY(qk_norm_rope), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -269,4 +269,37 @@ struct FewArgs {
 };
 cudaError_t launch_few(const GateArgs& g, const FewArgs& a, cudaStream_t s);
 
+// ------------------------------------------- the attention half of a block
+// A paged cache as the kernels read it (moe_kv_t, strides in elements).
+struct KvCache {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t k_page, k_token, k_head, v_page, v_token, v_head;
+};
+
+struct RopeArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const int32_t* positions;
+  const uint64_t* turns;   // [rot / 2]
+  const void* q_weight;    // [D] or null
+  const void* k_weight;
+  void* q_out;
+  void* k_out;             // or null
+  const int32_t* slots;
+  uint32_t* err;
+  KvCache cache;           // k null: none
+  int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+  int64_t capacity;        // slots of the cache
+  int T, Hq, Hkv, D, rot;
+  int interleaved, weight_f32, e4m3;
+  int page_shift;
+  int sms;
+  float eps, magnitude;
+};
+cudaError_t launch_rope(const RopeArgs& a, int dtype, cudaStream_t s);
+
 }  // namespace moe

@@ -1,0 +1,50 @@
+"""Plain 64-bit forms of the attention half's operators, for their tests, with how far 32-bit arithmetic may be from
+them (tests/op_reference.py: a rounded step is off by at most half a step of its type)."""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from tests.op_reference import EPS32
+
+
+def frequencies(rot, theta=10000.0, factor=1.0, original=0, low=1.0, high=1.0):
+    """Radians a position of each pair, pair by pair."""
+    out = []
+    for i in range(rot // 2):
+        f = theta ** (-2.0 * i / rot)
+        if factor != 1.0:
+            seen = original * f / (2.0 * math.pi)
+            keep = 0.0 if not original else min(1.0, max(0.0, (seen - low) / (high - low)))
+            f = keep * f + (1.0 - keep) * f / factor
+        out.append(f)
+    return torch.tensor(out, dtype=torch.float64)
+
+
+def norm_rotate(x, weight, positions, freq, interleaved, eps, magnitude):
+    """x [T, heads, D] -> the normed and rotated heads in float64, and how far float arithmetic may be from them."""
+    x = x.double()
+    D, rot = x.shape[2], 2 * freq.numel()
+    dx = torch.zeros_like(x)
+    if weight is not None:
+        x = x / torch.sqrt((x * x).mean(dim=2, keepdim=True) + eps) * weight.double()
+        # a sum of D squares: 8 steps a lane and up to 5 joins (halved by the root); the mean, eps, root, quotient and
+        # two products round once each
+        dx = x.abs() * (13 / 2 + 6) * EPS32
+    out, dout = x.clone(), dx.clone()
+    if rot:
+        # angles are reduced in whole numbers of 2^-64 of a turn; their upper half rounds to float (2^-26 of a turn),
+        # sine and cosine are off by 2 ulp at most, the magnitude's product by half a one
+        angle = positions.double()[:, None] * freq[None, :]
+        cos, sin = (f(angle)[:, None, :] * magnitude for f in (torch.cos, torch.sin))
+        dturn = abs(magnitude) * (2 * math.pi * 2.0 ** -26 + 5 * EPS32)
+        pick = [slice(0, rot, 2), slice(1, rot, 2)] if interleaved else [slice(0, rot // 2), slice(rot // 2, rot)]
+        a, b = x[:, :, pick[0]], x[:, :, pick[1]]
+        out[:, :, pick[0]], out[:, :, pick[1]] = a * cos - b * sin, b * cos + a * sin
+        da, db = dx[:, :, pick[0]], dx[:, :, pick[1]]
+        # float64's own angle: position * frequency is off by 2^-53 of itself
+        dturn = dturn + (angle.abs() * 2.0 ** -52 * abs(magnitude))[:, None, :]
+        both = (a.abs() + b.abs()) * dturn + abs(magnitude) * (da + db + 2 * EPS32 * (a.abs() + b.abs()))
+        dout[:, :, pick[0]], dout[:, :, pick[1]] = both, both
+    return out, dout
