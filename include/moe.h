@@ -505,6 +505,31 @@ moe_status_t moe_forward_few(const moe_problem_t* p, const moe_weights_t* w, con
  * themselves (moe_prompt_attention).  The conventions at the top hold; a
  * workspace serves one stream's calls at a time. */
 
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2, MOE_ACT_GELU_TANH = 3, MOE_ACT_RELU = 4 } moe_activation_t;
+
+/* M rows against N weight rows of depth K: M, N >= 0, K % 8 == 0, K >= 8. */
+typedef struct {
+  int32_t M, N, K;
+  int32_t dtype;      /* MOE_T_BF16 or MOE_T_F16, of x, w and bias */
+  int32_t out_dtype;  /* moe_dtype_t of out and residual */
+  int32_t activation; /* moe_activation_t */
+} moe_linear_t;
+
+/* 16-bit product with its epilogue (projections, dense layers):
+ *   out[m, n] = act(sum_k x[m, k] w[n, k] + bias[n]) + residual[m, n]
+ * in float, rounded once into out.  bias [N] and residual [M, N] or NULL
+ * (residual may be out with its stride).  act: silu(v) = v / (1 + exp(-v)), gelu(v)
+ * = v (1 + erf(v / sqrt 2)) / 2, its tanh form v (1 + tanh(sqrt(2 / pi) (v +
+ * 0.044715 v^3))) / 2, relu; a NaN stays one.  silu and the tanh form are
+ * within (8 + |y|) * 2^-22 of the value at their sum, y = v or 2 sqrt(2 / pi) (v +
+ * 0.044715 v^3), and zero where exp(-y) passes 8e37.
+ * x and w: 16-byte aligned, strides multiples of 8.  ws: 256 bytes (the error
+ * header). */
+moe_status_t moe_linear(const moe_linear_t* l, const void* x, int64_t x_stride, const void* w,
+                        int64_t w_stride, const void* bias, const void* residual,
+                        int64_t residual_stride, void* out, int64_t out_stride, void* ws,
+                        size_t ws_bytes, moe_stream_t stream);
+
 /* A paged cache of num_pages pages of page_size tokens (a power of two, 16 to
  * 1024), Hkv heads of D values each.  k and v point to [num_pages, page_size, Hkv,
  * D] values of the cache's type, with strides in elements between pages, tokens

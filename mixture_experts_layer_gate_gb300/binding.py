@@ -26,12 +26,13 @@ EXPORTED = ("moe_scratch_size", "moe_workspace_size", "moe_padded_capacity", "mo
             "moe_status_string", "moe_get_plan", "moe_get_plan_for_sms", "moe_align_permute_noalloc",
             "moe_dynamic_scales", "moe_launch_count", "moe_set_tuning", "moe_repack_int4",
             "moe_add_rms_norm", "moe_router_logits", "moe_gemm_fp8_block", "moe_gemm_fp8_block_swiglu",
-            "moe_few_workspace_size", "moe_forward_few", "moe_qk_norm_rope")
+            "moe_few_workspace_size", "moe_forward_few", "moe_qk_norm_rope", "moe_linear")
 
 DTYPES = {"bf16": 0, "f16": 1, "f32": 2}
 QUANTS = {"none": 0, "block": 1, "token": 2}
 OP_WORKSPACE_BYTES = 256 + 4096 + 4 * 8 * 16384
 FEW_MAX_TOKENS = 8
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4}
 LAYOUTS = {"half": 0, "interleaved": 1}
 
 
@@ -100,6 +101,10 @@ class KvStruct(ctypes.Structure):
                     "v_head_stride")]
 
 
+class LinearProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("M", "N", "K", "dtype", "out_dtype", "activation")]
+
+
 class RopeProblem(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "Hq", "Hkv", "D", "rot", "interleaved", "dtype", "weight_dtype",
                                              "cache_dtype", "page_size", "num_pages")] + [
@@ -150,6 +155,7 @@ def load(path: str = LIB_PATH):
                                            sz, vp]),
         "moe_few_workspace_size": (sz, [P]),
         "moe_forward_few": (st, [P, ctypes.POINTER(WeightsStruct), vp, vp, vp, vp, vp, sz, vp]),
+        "moe_linear": (st, [ctypes.POINTER(LinearProblem), vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, sz, vp]),
         "moe_qk_norm_rope": (st, [ctypes.POINTER(RopeProblem), vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp,
                                   i64, ctypes.POINTER(KvStruct), vp, vp, sz, vp]),
     }
@@ -394,7 +400,8 @@ def fp8_gemm_problem(M, N, K, out_dtype="bf16", accumulate=False) -> Fp8GemmProb
 
 
 def alloc_op_workspace(device):
-    """Zeroed workspace (error header and scratch) for router_logits and the gemm_fp8_block calls of one stream."""
+    """Zeroed workspace (error header and scratch) for router_logits, linear, qk_norm_rope and the gemm_fp8_block calls
+    of one stream."""
     import torch
     return torch.zeros(OP_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
 
@@ -464,6 +471,18 @@ def forward_few(p: Problem, w: Weights, x, logits, bias, out, ws, stream=None):
 # ------------------------------------------------- the attention half of a block
 
 
+def linear_problem(M, N, K, dtype="bf16", out_dtype=None, activation="none") -> LinearProblem:
+    """M rows, N output columns, depth K; out (and residual) of out_dtype, dtype without it; activation: "none", "silu",
+    "gelu", "gelu_tanh" or "relu"."""
+    return LinearProblem(int(M), int(N), int(K), DTYPES[dtype], DTYPES[out_dtype or dtype], ACTIVATIONS[activation])
+
+
+def linear(p: LinearProblem, x, w, out, ws, bias=None, residual=None, stream=None):
+    """moe_linear: out = act(x w^T + bias) + residual; x [M, K] and w [N, K] (rows may be strided), bias [N] of p's
+    dtype, residual [M, N] (may be out)."""
+    _check((_ops or _native()).linear(p, x, w, out, ws, bias, residual, stream), "moe_linear")
+
+
 def _cache_code(cache_dtype, dtype) -> int:
     """MOE_CACHE_SAME or MOE_CACHE_E4M3 of a cache of dtype's values or "e4m3"."""
     if cache_dtype == "e4m3":
@@ -520,7 +539,7 @@ def qk_norm_rope(r: RopeProblem, q, k, positions, turns, q_out, ws, k_out=None, 
     page_size, Hkv, D] of any order in memory with slots int32 [T], and for "e4m3" k_scale, v_scale float32 [num_pages,
     Hkv, page_size]."""
     _check((_ops or _native()).qk_norm_rope(r, q, k, v, positions, turns, q_weight, k_weight, q_out, k_out, k_cache,
-                                            v_cache, k_scale, v_scale, slots, ws, stream), "moe_qk_norm_rope")
+                                            v_cache, k_scale, v_scale, slots, ws, stream), "moe_qk_norm_rope", "moe_linear")
 
 
 def workspace_of(owner, name: str, n: int, allocate):

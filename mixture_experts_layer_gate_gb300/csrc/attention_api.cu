@@ -115,4 +115,38 @@ moe_status_t moe_qk_norm_rope(const moe_rope_t* r, const void* q, int64_t q_stri
   return cuda_status(launch_rope(a, r->dtype, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+moe_status_t moe_linear(const moe_linear_t* l, const void* x, int64_t x_stride, const void* w, int64_t w_stride,
+                        const void* bias, const void* residual, int64_t residual_stride, void* out, int64_t out_stride,
+                        void* ws, size_t ws_bytes, moe_stream_t stream) {
+  if (l == nullptr || l->M < 0 || l->N < 0 || l->K < 8 || l->K % 8 != 0) return MOE_ERR_INVALID_ARG;
+  if (!half_dtype(l->dtype) || !is_dtype(l->out_dtype)) return MOE_ERR_INVALID_ARG;
+  if (l->activation < MOE_ACT_NONE || l->activation > MOE_ACT_RELU) return MOE_ERR_INVALID_ARG;
+  if (l->M > (1 << 22) || l->N > (1 << 22)) return MOE_ERR_UNSUPPORTED;
+  MOE_TRY(check_header(ws, ws_bytes));
+  if (l->M == 0 || l->N == 0) return MOE_OK;
+  if (!wide_rows(x, x_stride, l->K) || !wide_rows(w, w_stride, l->K) || !aligned(bias, 2)) return MOE_ERR_INVALID_ARG;
+  const size_t b = size_of(l->out_dtype);
+  if (!rows_ok(out, out_stride, l->N, b)) return MOE_ERR_INVALID_ARG;
+  if (residual != nullptr && !rows_ok(residual, residual_stride, l->N, b)) return MOE_ERR_INVALID_ARG;
+  if (residual == out && residual_stride != out_stride) return MOE_ERR_INVALID_ARG;
+  LinearArgs a = {};
+  a.x = x;
+  a.w = w;
+  a.bias = bias;
+  a.residual = residual;
+  a.out = out;
+  a.x_stride = x_stride;
+  a.w_stride = w_stride;
+  a.residual_stride = residual_stride;
+  a.out_stride = out_stride;
+  a.M = l->M;
+  a.N = l->N;
+  a.K = l->K;
+  a.f16 = l->dtype == MOE_T_F16;
+  a.out_dtype = l->out_dtype;
+  a.act = l->activation;
+  a.err = static_cast<uint32_t*>(ws);
+  return cuda_status(launch_linear(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -306,9 +306,26 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* v, Py_ssize_t n) {
   });
 }
 
+// problem, x, w, out, ws, bias, residual, stream
+PyObject* linear(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return run(n, 8, [&] {
+    const moe_linear_t p = problem<moe_linear_t>(v[0]);
+    const Type b = type_of(p.dtype), ot = type_of(p.out_dtype);
+    const Rows x = rows(v[1], p.M, p.K, b, "x"), w = rows(v[2], p.N, p.K, b, "w");
+    const Rows o = rows(v[3], p.M, p.N, ot, "out"), r = rows(v[6], p.M, p.N, ot, "residual");
+    void* bias = flat(v[5], p.N, b, "bias");
+    const Workspace ws(v[4]);
+    const moe_stream_t s = stream_of(v[7]);
+    return unlocked([&] {
+      return moe_linear(&p, x.p, x.stride, w.p, w.stride, bias, r.p, r.stride, o.p, o.stride, ws.p, ws.bytes, s);
+    });
+  });
+}
+
 #define ENTRY(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(add_rms_norm), ENTRY(router_logits), ENTRY(gemm_fp8_block), ENTRY(gemm_fp8_block_swiglu),
-                         ENTRY(forward_few), ENTRY(qk_norm_rope), {nullptr, nullptr, 0, nullptr}};
+                         ENTRY(forward_few), ENTRY(qk_norm_rope), ENTRY(linear),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -66,7 +66,9 @@ struct Params {
   uint8_t* codes;        // SwiGLU
   float* scales;         // SwiGLU
   uint32_t* err;
-  int64_t a_scale_stride, out_stride;
+  const void* old;       // what the product is added to (accumulate): out, or a residual of its type
+  const void* bias;      // [N] of the operands' type, or null (EPI)
+  int64_t a_scale_stride, out_stride, old_stride;
   int M, N, KB;
   int group;             // k-blocks per accumulator
   int P;                 // CTAs of a cluster that split K (not PAIR)
@@ -76,14 +78,16 @@ struct Params {
   int fmt;               // 16-bit operands: 1 bf16, 0 f16
   int out_dtype;         // moe_dtype_t
   int accumulate;
-  int vec;               // out rows take 16-byte stores
+  int act;               // moe_activation_t (EPI 2, 3)
+  int vec_bias;          // bias takes 16-byte loads
+  int vec;               // rows of out (and old) take 16-byte accesses
   int tma_out;           // 256-column tiles are stored by TMA
   int boxes;             // of each joining warp, for that: 2 or 4
   int vec_scale;         // rows of a_scale take 16-byte loads at multiples of four blocks
 };
 
 struct Maps {
-  CUtensorMap a, w, out;
+  CUtensorMap a, w, out, old;
 };
 
 __host__ __device__ constexpr int wrows(int bn, bool pair) { return pair ? 128 : (bn < 128 ? bn : 128); }
@@ -243,22 +247,60 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, f
          (static_cast<uint32_t>(f32x2_to_e4m3x2(__fdiv_rn(c, scale), __fdiv_rn(d, scale))) << 16);
 }
 
+// What becomes of a sum before old is added: EPI 0 nothing, 1 the bias, 2 the bias
+// and an activation other than the error function's, 3 that one (kernels of their
+// own: its polynomial for 128 sums a thread is most of the code).
+template <int EPI>
+__device__ __forceinline__ float activated(float v, int act) {
+  if (EPI == 2) {
+    if (act == 4) return v < 0.f ? 0.f : v;
+    // silu(v) = v / (1 + exp(-v)), and (1 + tanh z) / 2 = 1 / (1 + exp(-2 z))
+    const float y = act == 1 ? v : v * fmaf(v * v, 0.044715f * 1.5957691216057308f, 1.5957691216057308f);
+    const float e = expf(-y);
+    return e > 8e37f ? v * 0.f : __fdividef(v, 1.0f + e);
+  }
+  if (EPI == 3) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+  return v;
+}
+__device__ __forceinline__ float bias_at(const Params& p, int col) {
+  const uint16_t b = static_cast<const uint16_t*>(p.bias)[col];
+  return p.fmt == 1 ? __uint_as_float(static_cast<uint32_t>(b) << 16) : __half2float(__ushort_as_half(b));
+}
+// of four columns, zero past N
+__device__ __forceinline__ float4 bias4(const Params& p, int col) {
+  if (p.vec_bias && col + 4 <= p.N) {
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.bias) + col);
+    if (p.fmt == 1) return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+  return make_float4(col < p.N ? bias_at(p, col) : 0.f, col + 1 < p.N ? bias_at(p, col + 1) : 0.f,
+                     col + 2 < p.N ? bias_at(p, col + 2) : 0.f, col + 3 < p.N ? bias_at(p, col + 3) : 0.f);
+}
+
 // out[row, col .. col + 3] of four sums
+template <int EPI>
 __device__ __forceinline__ void store4(const Params& p, int64_t row, int col, float4 v) {
-  const int64_t at = row * p.out_stride + col;
+  const int64_t at = row * p.out_stride + col, from = row * p.old_stride + col;
+  if (EPI > 0) {
+    const float4 b = p.bias != nullptr ? bias4(p, col) : make_float4(0.f, 0.f, 0.f, 0.f);
+    v = make_float4(activated<EPI>(v.x + b.x, p.act), activated<EPI>(v.y + b.y, p.act),
+                    activated<EPI>(v.z + b.z, p.act), activated<EPI>(v.w + b.w, p.act));
+  }
   float f[4] = {v.x, v.y, v.z, v.w};
   if (p.vec && col + 4 <= p.N) {
     if (p.out_dtype == 2) {
       float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
       if (p.accumulate) {
-        const float4 u = *o;
+        const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(p.old) + from);
         v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
       }
       *o = v;
     } else {
       uint2* o = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at);
       uint2 u = make_uint2(0, 0);
-      if (p.accumulate) u = *o;
+      if (p.accumulate) u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.old) + from);
       if (p.out_dtype == 0) {
         if (p.accumulate) {
           f[0] += bf16_lo(u.x);
@@ -288,13 +330,15 @@ __device__ __forceinline__ void store4(const Params& p, int64_t row, int col, fl
     if (col + j >= p.N) return;
     if (p.out_dtype == 0) {
       __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at + j;
-      *o = __float2bfloat16_rn(p.accumulate ? f[j] + __bfloat162float(*o) : f[j]);
+      const __nv_bfloat16* u = static_cast<const __nv_bfloat16*>(p.old) + from + j;
+      *o = __float2bfloat16_rn(p.accumulate ? f[j] + __bfloat162float(*u) : f[j]);
     } else if (p.out_dtype == 1) {
       __half* o = static_cast<__half*>(p.out) + at + j;
-      *o = __float2half_rn(p.accumulate ? f[j] + __half2float(*o) : f[j]);
+      const __half* u = static_cast<const __half*>(p.old) + from + j;
+      *o = __float2half_rn(p.accumulate ? f[j] + __half2float(*u) : f[j]);
     } else {
       float* o = static_cast<float*>(p.out) + at + j;
-      *o = p.accumulate ? f[j] + *o : f[j];
+      *o = p.accumulate ? f[j] + static_cast<const float*>(p.old)[from + j] : f[j];
     }
   }
 }
@@ -384,7 +428,7 @@ __device__ __forceinline__ void load_box(uint32_t leader, uint32_t dst, const vo
 // ADD: 256-column tiles that are added to what out holds (a kernel of its own: what
 // fetches the old values costs the storing one 51 -> 57 us at M = 4096, N = 7168,
 // K = 2048); of narrower tiles p.accumulate tells.
-template <int KIND, bool SWIGLU, bool PAIR, int BN, bool ADD>
+template <int KIND, bool SWIGLU, bool PAIR, int BN, bool ADD, int EPI>
 __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constant__ Maps maps, const Params p) {
   static_assert(!SWIGLU || BN == 256, "gate and up halves of 128 columns");
   static_assert(!PAIR || BN == 256, "a pair's halves are 128 weight rows");
@@ -439,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
     tma_prefetch_desc(&maps.a);
     tma_prefetch_desc(&maps.w);
     if (p.tma_out) tma_prefetch_desc(&maps.out);
+    if (ADD && p.tma_out) tma_prefetch_desc(&maps.old);
   }
   if (warp == 1) {
     if (PAIR) {
@@ -638,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
         const uint32_t slot = static_cast<uint32_t>(i & (p.boxes - 1));
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         expect_tx(lane == 0, BOX(slot), kBoxBytes);
-        load_box<false>(lane == 0, boxes0 + slot * kBoxBytes, &maps.out, BOX(slot), n0 + W * half + i * box_cols,
+        load_box<false>(lane == 0, boxes0 + slot * kBoxBytes, &maps.old, BOX(slot), n0 + W * half + i * box_cols,
                         m0 + 32 * quarter);
         box_loads |= 1u << slot;
       };
@@ -775,6 +820,16 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
         // What the sums are added to is there by then (fetch_box).  M = 4096, N =
         // 7168, K = 2048, bf16: 51 us, added 62; plain stores of the tile 62 and 130.
         if (live) {
+          auto finished = [&](int col, uint64_t a, uint64_t b) {  // two pairs of sums, of columns col ..
+            float2 u = unpair(a), v = unpair(b);
+            if (EPI > 0 && p.bias != nullptr) {
+              const float4 add = bias4(p, col);
+              u = make_float2(u.x + add.x, u.y + add.y);
+              v = make_float2(v.x + add.z, v.y + add.w);
+            }
+            return make_float4(activated<EPI>(u.x, p.act), activated<EPI>(u.y, p.act), activated<EPI>(v.x, p.act),
+                               activated<EPI>(v.y, p.act));
+          };
           auto box = [&](int i, auto&& piece) {  // piece(j, old): 16 bytes
             const uint32_t slot = static_cast<uint32_t>(i & (p.boxes - 1));
             const uint32_t dst = boxes0 + slot * kBoxBytes, mine = dst + static_cast<uint32_t>(lane * 64);
@@ -805,15 +860,15 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
 #pragma unroll
             for (int i = 0; i < W / 16; ++i)
               box(i, [&](int j, uint4 old) {
-                const float2 u = unpair(acc[8 * i + 2 * j]), v = unpair(acc[8 * i + 2 * j + 1]);
+                const float4 t = finished(n0 + W * half + 16 * i + 4 * j, acc[8 * i + 2 * j], acc[8 * i + 2 * j + 1]);
+                const float2 u = make_float2(t.x, t.y), v = make_float2(t.z, t.w);
                 if (!ADD) return make_uint4(__float_as_uint(u.x), __float_as_uint(u.y), __float_as_uint(v.x), __float_as_uint(v.y));
                 return make_uint4(__float_as_uint(u.x + __uint_as_float(old.x)), __float_as_uint(u.y + __uint_as_float(old.y)),
                                   __float_as_uint(v.x + __uint_as_float(old.z)), __float_as_uint(v.y + __uint_as_float(old.w)));
               });
           } else {
             const bool f16 = p.out_dtype == 1;
-            auto two = [&](uint64_t a, uint32_t old) {
-              float2 v = unpair(a);
+            auto two = [&](float2 v, uint32_t old) {
               if (ADD) {
                 const float2 o = f16 ? __half22float2(*reinterpret_cast<const __half2*>(&old))
                                      : make_float2(bf16_lo(old), bf16_hi(old));
@@ -826,7 +881,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
             for (int i = 0; i < W / 32; ++i)
               box(i, [&](int j, uint4 old) {
                 const uint64_t* q = acc + 16 * i + 4 * j;
-                return make_uint4(two(q[0], old.x), two(q[1], old.y), two(q[2], old.z), two(q[3], old.w));
+                const int col = n0 + W * half + 32 * i + 8 * j;
+                const float4 s = finished(col, q[0], q[1]), t = finished(col + 4, q[2], q[3]);
+                return make_uint4(two(make_float2(s.x, s.y), old.x), two(make_float2(s.z, s.w), old.y),
+                                  two(make_float2(t.x, t.y), old.z), two(make_float2(t.z, t.w), old.w));
               });
           }
         }
@@ -839,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
         const uint32_t mine = stage0 + static_cast<uint32_t>(4 * half + quarter) * out_stage_bytes(BN, p.boxes);
         const int to0 = m0 + 32 * quarter + (lane >> 2), col0 = n0 + W * half + 4 * (lane & 3);
         // a whole tile's columns, aligned stores (of 256-column tiles those are TMA's)
-        const bool fast = BN < 256 && p.vec && !p.accumulate && n0 + BN <= p.N;
+        const bool fast = EPI == 0 && BN < 256 && p.vec && !p.accumulate && n0 + BN <= p.N;
         const int64_t at = static_cast<int64_t>(to0) * p.out_stride + col0, eight = 8 * p.out_stride;
 #pragma unroll
         for (int c = 0; c < W / 16; ++c) {
@@ -855,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
           if (!fast) {
 #pragma unroll 1
             for (int i = 0; i < 4; ++i)
-              if (to0 + 8 * i < p.M) store4(p, to0 + 8 * i, col0 + col, lds_f4(from + static_cast<uint32_t>(8 * i * kStageRow)));
+              if (to0 + 8 * i < p.M) store4<EPI>(p, to0 + 8 * i, col0 + col, lds_f4(from + static_cast<uint32_t>(8 * i * kStageRow)));
           } else if (p.out_dtype == 2) {
             float* o = static_cast<float*>(p.out) + at + col;
 #pragma unroll
@@ -922,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
         if (lane == 0) p.scales[static_cast<int64_t>(m0 + r) * (p.N / 128) + n0 / 128] = scale;
         reinterpret_cast<uint32_t*>(p.codes + static_cast<int64_t>(m0 + r) * p.N + n0)[lane] = codes4(a, b, c, d, scale);
       } else {
-        for (int col = 4 * lane; col < BN; col += 128) store4(p, m0 + r, n0 + col, joined(col));
+        for (int col = 4 * lane; col < BN; col += 128) store4<EPI>(p, m0 + r, n0 + col, joined(col));
       }
     }
     cluster_sync_all();  // no CTA leaves while a peer reads its sums
@@ -951,13 +1009,13 @@ size_t smem_bytes(const Params& p, int bn, bool pair) {
   return std::max(kTensorMemorySmem, 1024 + fixed_bytes(KIND, SWIGLU, bn, p.boxes) + ring);
 }
 
-template <int KIND, bool SWIGLU, bool PAIR, int BN, bool ADD = false>
+template <int KIND, bool SWIGLU, bool PAIR, int BN, bool ADD = false, int EPI = 0>
 cudaError_t launch(const Maps& maps, const Params& p, int grid, cudaStream_t s) {
   static int configured[64] = {};
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
-  auto kernel = dense_kernel<KIND, SWIGLU, PAIR, BN, ADD>;
+  auto kernel = dense_kernel<KIND, SWIGLU, PAIR, BN, ADD, EPI>;
   if (dev < 0 || dev >= 64 || configured[dev] == 0) {
     err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxSmem));
     if (err != cudaSuccess) return err;
@@ -986,7 +1044,7 @@ struct Choice {
 // CTAs a cluster only for eight tiles at most: more such clusters do not all fit
 // on the SMs at once (one row, N = 2048, K = 7168 with SwiGLU: 24 us by eights,
 // 18 us by fours).
-inline Choice choose(int M, int N, int KB, bool swiglu, bool e4m3, int sms) {
+inline Choice choose(int M, int N, int KB, bool swiglu, bool e4m3, int sms, bool pairs_of_half = false) {
   Choice best{256, false, 1};
   double best_time = 1e30;
   const double arows = std::min(128, (M + 7) / 8 * 8);
@@ -995,7 +1053,7 @@ inline Choice choose(int M, int N, int KB, bool swiglu, bool e4m3, int sms) {
     constexpr double half_block[5] = {250, 340, 560, 1150, 1150}, e4m3_block[5] = {600, 690, 800, 1250, 950};
     const int bn = width[w];
     const bool pair = w == 4;
-    if ((swiglu && bn != 256) || (pair && (M <= 128 || !e4m3))) continue;
+    if ((swiglu && bn != 256) || (pair && (M <= 128 || !(e4m3 || pairs_of_half)))) continue;
     const int tm = pair ? 256 : 128, tn = swiglu ? 128 : bn;
     const long long tiles = static_cast<long long>((M + tm - 1) / tm) * ((N + tn - 1) / tn);
     for (int P = 1; P <= 8 && P <= KB; P *= 2) {
@@ -1016,7 +1074,7 @@ inline Choice choose(int M, int N, int KB, bool swiglu, bool e4m3, int sms) {
 // Descriptors, tile counts and ring depth, then the launch.  p: everything but
 // mt, nt, arows and stages.  a [M, K] and w [wrows_total, K] of 1-byte (kE4M3)
 // or 2-byte elements, strides in elements.
-template <int KIND>
+template <int KIND, int EPI = 0>
 cudaError_t plan_and_launch(Params p, int bn, bool pair, bool swiglu, const void* a, int64_t a_stride, const void* w,
                             int64_t w_stride, int64_t w_total, int64_t K, int sms, cudaStream_t s) {
   const uint64_t esz = KIND == kE4M3 ? 1 : 2;
@@ -1046,6 +1104,10 @@ cudaError_t plan_and_launch(Params p, int bn, bool pair, bool swiglu, const void
     if (!encode_map(&maps.out, osz == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.out,
                     dims, str, box, CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorInvalidValue;
+    const uint64_t old_str[1] = {static_cast<uint64_t>(p.old_stride) * osz};
+    if (p.accumulate && !encode_map(&maps.old, osz == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                                    2, p.old, dims, old_str, box, CU_TENSOR_MAP_SWIZZLE_64B))
+      return cudaErrorInvalidValue;
   }
   {
     const uint64_t dims[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(p.M)};
@@ -1068,21 +1130,26 @@ cudaError_t plan_and_launch(Params p, int bn, bool pair, bool swiglu, const void
       if (swiglu) return launch<KIND, true, true, 256>(maps, p, grid, s);
       return p.accumulate ? launch<KIND, false, true, 256, true>(maps, p, grid, s)
                           : launch<KIND, false, true, 256>(maps, p, grid, s);
+    } else if constexpr (EPI > 0) {
+      return p.accumulate ? launch<KIND, false, true, 256, true, EPI>(maps, p, grid, s)
+                          : launch<KIND, false, true, 256, false, EPI>(maps, p, grid, s);
     } else {
-      return cudaErrorInvalidValue;  // (choose() pairs CTAs for 8-bit operands only)
+      return cudaErrorInvalidValue;  // (the router's scores are no pair's: choose())
     }
   }
   if (p.P > 1) grid = static_cast<int>(tiles) * p.P;
   else grid = static_cast<int>(tiles < sms ? tiles : sms);
   if constexpr (KIND == kE4M3) {
     if (swiglu) return launch<KIND, true, false, 256>(maps, p, grid, s);
-    if (bn == 256 && p.accumulate) return launch<KIND, false, false, 256, true>(maps, p, grid, s);
+  }
+  if constexpr (KIND == kE4M3 || EPI > 0) {
+    if (bn == 256 && p.accumulate) return launch<KIND, false, false, 256, true, EPI>(maps, p, grid, s);
   }
   switch (bn) {
-    case 32: return launch<KIND, false, false, 32>(maps, p, grid, s);
-    case 64: return launch<KIND, false, false, 64>(maps, p, grid, s);
-    case 128: return launch<KIND, false, false, 128>(maps, p, grid, s);
-    default: return launch<KIND, false, false, 256>(maps, p, grid, s);
+    case 32: return launch<KIND, false, false, 32, false, EPI>(maps, p, grid, s);
+    case 64: return launch<KIND, false, false, 64, false, EPI>(maps, p, grid, s);
+    case 128: return launch<KIND, false, false, 128, false, EPI>(maps, p, grid, s);
+    default: return launch<KIND, false, false, 256, false, EPI>(maps, p, grid, s);
   }
 }
 

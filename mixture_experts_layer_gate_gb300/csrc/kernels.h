@@ -302,4 +302,22 @@ struct RopeArgs {
 };
 cudaError_t launch_rope(const RopeArgs& a, int dtype, cudaStream_t s);
 
+struct LinearArgs {
+  const void* x;          // [M, K]
+  const void* w;          // [N, K]
+  const void* bias;       // [N] or null
+  const void* residual;   // [M, N] or null
+  void* out;              // [M, N]
+  int64_t x_stride, w_stride, residual_stride, out_stride;
+  int M, N, K;
+  int f16;                // operands: f16, else bf16
+  int out_dtype;          // moe_dtype_t of out and residual
+  int act;                // moe_activation_t
+  uint32_t* err;
+};
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
+// The same for a few rows.
+constexpr int kLinearFewRows = 16;
+cudaError_t launch_linear_few(const LinearArgs& a, int sms, cudaStream_t s);
+
 }  // namespace moe

@@ -48,3 +48,29 @@ def norm_rotate(x, weight, positions, freq, interleaved, eps, magnitude):
         both = (a.abs() + b.abs()) * dturn + abs(magnitude) * (da + db + 2 * EPS32 * (a.abs() + b.abs()))
         dout[:, :, pick[0]], dout[:, :, pick[1]] = both, both
     return out, dout
+
+
+def linear(x, w, bias, act, residual):
+    """act(x w^T + bias) + residual in float64, and how far float arithmetic may be from it before the last rounding."""
+    x, w = x.cpu().double(), w.cpu().double()
+    v = x @ w.T
+    # 16 products a step and the joins of partial sums; the tensor core may truncate
+    dv = (x.shape[1] / 16 + 32) * 2 * EPS32 * (x.abs() @ w.abs().T)
+    if bias is not None:
+        v = v + bias.cpu().double()
+        dv = dv + EPS32 * v.abs()
+    y = 2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v ** 3) if act == "gelu_tanh" else v
+    if act in ("silu", "gelu_tanh"):
+        out = v / (1 + torch.exp(-y))
+        own = (8 + y.abs()) * 4 * EPS32 * out.abs() + 2.0 ** -100
+    elif act == "gelu":
+        out = v * torch.special.ndtr(v)
+        own = 8 * EPS32 * v.abs()  # erf is off by 2 ulp of 1 at most, then 1 + erf, and two products
+    else:
+        out = torch.where(v < 0, torch.zeros_like(v), v) if act == "relu" else v
+        own = torch.zeros_like(v)
+    dv = 1.13 * dv + own  # (no activation is steeper than 1.13)
+    if residual is not None:
+        out = out + residual.cpu().double()
+        dv = dv + EPS32 * out.abs()
+    return out, dv
