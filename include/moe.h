@@ -588,6 +588,51 @@ moe_status_t moe_qk_norm_rope(const moe_rope_t* r, const void* q, int64_t q_stri
                               const moe_kv_t* cache, const int32_t* slots, void* ws, size_t ws_bytes,
                               moe_stream_t stream);
 
+/* Attention of the new tokens of B sequences: T rows of queries (Hq heads of D
+ * values, D % 8 == 0, 8 <= D <= 128), Hkv key and value heads, Hq a multiple of
+ * Hkv.  Query head h reads key head h / (Hq / Hkv). */
+typedef struct {
+  int32_t T, B, Hq, Hkv, D;
+  int32_t max_q;       /* new tokens of a sequence, at most (>= 1; chooses the kernel) */
+  int32_t dtype;       /* MOE_T_BF16 or MOE_T_F16, of q, out and values that are no codes */
+  int32_t cache_dtype; /* MOE_CACHE_SAME or MOE_CACHE_E4M3 (paged) */
+  int32_t page_size;   /* paged: as moe_kv_t; else 0 */
+  int32_t num_pages;
+  int32_t max_pages;   /* columns of the page table */
+  float scale;         /* of the scores, > 0 */
+} moe_attention_t;
+
+/* Sequence b's new tokens are the rows cu_q[b] .. cu_q[b + 1] - 1 of q and out
+ * (int32 [B + 1], not decreasing, at most T), the last of its kv_len[b] tokens
+ * (int32 [B]; they are in the cache already).  Its key j is place j % page_size of
+ * page page_table[b, j / page_size] (int32 [B, max_pages] with its stride; entries
+ * past the length are not read).  New token i of n sees the keys j <= kv_len - n +
+ * i, and with x_j = scale * q . k_j
+ *   out = sum_j exp(x_j) v_j / sum_j exp(x_j),  lse[row, h] = log sum_j exp(x_j)
+ * (lse float [T, Hq] or NULL).  Rows that see no key (kv_len < n) get zeros and
+ * -inf; rows of no sequence stay as they were; keys and values that a row does not
+ * see do not reach it, whatever they hold.  Sums are float; each weight exp(x_j -
+ * max) is rounded to the 16-bit type that multiplies the values (f16 with an 8-bit
+ * cache).  A length beyond the table, a page outside the cache or rows outside T
+ * are recorded as MOE_ERR_DEVICE_BAD_INDEX; what they hold is not read and the
+ * sequence's results mean nothing.  All lengths are read on the device: a captured
+ * call follows them.  Results do not depend on timing (no atomics in sums).
+ * Rows are 16-byte aligned, strides multiples of 8.  The workspace holds
+ * moe_attention_workspace_size() bytes, zeroed when first used. */
+size_t moe_attention_workspace_size(const moe_attention_t* p);
+moe_status_t moe_paged_attention(const moe_attention_t* p, const void* q, int64_t q_stride,
+                                 const moe_kv_t* cache, const int32_t* page_table, int64_t table_stride,
+                                 const int32_t* cu_q, const int32_t* kv_len, void* out,
+                                 int64_t out_stride, float* lse, void* ws, size_t ws_bytes,
+                                 moe_stream_t stream);
+
+/* The same over whole prompts without a cache: keys and values are rows [T, Hkv *
+ * D] beside q's, token i of a sequence sees the sequence's tokens up to itself. */
+moe_status_t moe_prompt_attention(const moe_attention_t* p, const void* q, int64_t q_stride,
+                                  const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                  const int32_t* cu_q, void* out, int64_t out_stride, float* lse,
+                                  void* ws, size_t ws_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,5 +12,7 @@ from .binding import (MoEError, Problem, Plan, Weights, MoELayer, load, problem,
                       norm_problem, router_problem, fp8_gemm_problem, alloc_op_workspace, add_rms_norm,
                       router_logits, gemm_fp8_block, gemm_fp8_block_swiglu, few_workspace_size,
                       alloc_few_workspace, forward_few, FEW_MAX_TOKENS, RopeProblem, rope_problem, rope_table,
-                      qk_norm_rope, LinearProblem, linear_problem, linear)
+                      qk_norm_rope, LinearProblem, linear_problem, linear, AttentionProblem,
+                      attention_problem, attention_workspace_size, alloc_attention_workspace, paged_attention,
+                      prompt_attention)
 from .block import MoEBlock, SharedExpert

@@ -26,7 +26,8 @@ EXPORTED = ("moe_scratch_size", "moe_workspace_size", "moe_padded_capacity", "mo
             "moe_status_string", "moe_get_plan", "moe_get_plan_for_sms", "moe_align_permute_noalloc",
             "moe_dynamic_scales", "moe_launch_count", "moe_set_tuning", "moe_repack_int4",
             "moe_add_rms_norm", "moe_router_logits", "moe_gemm_fp8_block", "moe_gemm_fp8_block_swiglu",
-            "moe_few_workspace_size", "moe_forward_few", "moe_qk_norm_rope", "moe_linear")
+            "moe_few_workspace_size", "moe_forward_few", "moe_qk_norm_rope", "moe_linear",
+            "moe_attention_workspace_size", "moe_paged_attention", "moe_prompt_attention")
 
 DTYPES = {"bf16": 0, "f16": 1, "f32": 2}
 QUANTS = {"none": 0, "block": 1, "token": 2}
@@ -111,6 +112,11 @@ class RopeProblem(ctypes.Structure):
         ("eps", ctypes.c_float), ("magnitude", ctypes.c_float)]
 
 
+class AttentionProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "B", "Hq", "Hkv", "D", "max_q", "dtype", "cache_dtype", "page_size",
+                                             "num_pages", "max_pages")] + [("scale", ctypes.c_float)]
+
+
 TUNING_KNOBS = tuple(n for n, _ in Tuning._fields_)
 
 _lib = None
@@ -156,6 +162,11 @@ def load(path: str = LIB_PATH):
         "moe_few_workspace_size": (sz, [P]),
         "moe_forward_few": (st, [P, ctypes.POINTER(WeightsStruct), vp, vp, vp, vp, vp, sz, vp]),
         "moe_linear": (st, [ctypes.POINTER(LinearProblem), vp, i64, vp, i64, vp, vp, i64, vp, i64, vp, sz, vp]),
+        "moe_attention_workspace_size": (sz, [ctypes.POINTER(AttentionProblem)]),
+        "moe_paged_attention": (st, [ctypes.POINTER(AttentionProblem), vp, i64, ctypes.POINTER(KvStruct), vp, i64, vp,
+                                     vp, vp, i64, vp, vp, sz, vp]),
+        "moe_prompt_attention": (st, [ctypes.POINTER(AttentionProblem), vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, vp,
+                                      sz, vp]),
         "moe_qk_norm_rope": (st, [ctypes.POINTER(RopeProblem), vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp,
                                   i64, ctypes.POINTER(KvStruct), vp, vp, sz, vp]),
     }
@@ -539,7 +550,47 @@ def qk_norm_rope(r: RopeProblem, q, k, positions, turns, q_out, ws, k_out=None, 
     page_size, Hkv, D] of any order in memory with slots int32 [T], and for "e4m3" k_scale, v_scale float32 [num_pages,
     Hkv, page_size]."""
     _check((_ops or _native()).qk_norm_rope(r, q, k, v, positions, turns, q_weight, k_weight, q_out, k_out, k_cache,
-                                            v_cache, k_scale, v_scale, slots, ws, stream), "moe_qk_norm_rope", "moe_linear")
+                                            v_cache, k_scale, v_scale, slots, ws, stream), "moe_qk_norm_rope", "moe_linear",
+            "moe_attention_workspace_size", "moe_paged_attention", "moe_prompt_attention")
+
+
+def attention_problem(T, B, Hq, Hkv, D, max_q, dtype="bf16", cache_dtype=None, page_size=0, num_pages=0, max_pages=0,
+                      scale=None) -> AttentionProblem:
+    """T rows of Hq query heads of D values, the new tokens of B sequences (max_q of one at most), against Hkv key and
+    value heads.  For paged_attention with the cache's page_size, num_pages and type (dtype's values or "e4m3") and the
+    page table's columns max_pages; scale: of the scores, 1 / sqrt(D) without it."""
+    return AttentionProblem(int(T), int(B), int(Hq), int(Hkv), int(D), int(max_q), DTYPES[dtype],
+                            _cache_code(cache_dtype, dtype), int(page_size), int(num_pages), int(max_pages),
+                            float(D) ** -0.5 if scale is None else float(scale))
+
+
+def attention_workspace_size(p: AttentionProblem) -> int:
+    return int(load().moe_attention_workspace_size(ctypes.byref(p)))
+
+
+def alloc_attention_workspace(p: AttentionProblem, device):
+    """Zeroed workspace for the attention calls of one stream, of p and of problems with no longer heads and no more
+    new tokens a sequence."""
+    import torch
+    n = attention_workspace_size(p)
+    if n == 0:
+        raise MoEError(1, "attention workspace size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def paged_attention(p: AttentionProblem, q, k_cache, v_cache, page_table, cu_q, kv_len, out, ws, k_scale=None,
+                    v_scale=None, lse=None, stream=None):
+    """moe_paged_attention.  q, out [T, Hq * D] (rows may be strided); k_cache, v_cache [num_pages, page_size, Hkv, D] of
+    any order in memory, for "e4m3" with k_scale, v_scale float32 [num_pages, Hkv, page_size]; page_table int32 [B,
+    max_pages], cu_q int32 [B + 1], kv_len int32 [B]; lse float32 [T, Hq] or None."""
+    _check((_ops or _native()).paged_attention(p, q, k_cache, v_cache, k_scale, v_scale, page_table, cu_q, kv_len, out,
+                                               lse, ws, stream), "moe_paged_attention")
+
+
+def prompt_attention(p: AttentionProblem, q, k, v, cu_q, out, ws, lse=None, stream=None):
+    """moe_prompt_attention: q, out [T, Hq * D] and k, v [T, Hkv * D] (rows may be strided), cu_q int32 [B + 1], lse
+    float32 [T, Hq] or None."""
+    _check((_ops or _native()).prompt_attention(p, q, k, v, cu_q, out, lse, ws, stream), "moe_prompt_attention")
 
 
 def workspace_of(owner, name: str, n: int, allocate):

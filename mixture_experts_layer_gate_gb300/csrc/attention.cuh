@@ -1,0 +1,251 @@
+// How the attention kernels share out their work.  An item is a tile of rows (the
+// queries of one sequence and key head: row i G + g is query head g of the group,
+// new token i) and reads the keys up to its last row's, in tiles of KT keys.  All
+// items' tiles, in the order of sequences, key heads and row tiles, are cut into as
+// many runs of equal length as there are CTAs, whatever the sequences' lengths are: a
+// long context is spread over many SMs and short ones share one.  Lengths are read
+// on the device, so a captured call follows them.  An item that lies in several runs
+// is joined by the CTA that finishes last, in the order of the runs (the result does
+// not depend on which one that is).
+#pragma once
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace moe {
+namespace attn {
+
+// The live rows of a sequence: its last n new tokens see keys [0, past + i]; of a
+// sequence with fewer keys than new tokens the first `none` see nothing.
+struct Seq {
+  int row0;  // of the first live token
+  int n, L, past, none;
+};
+
+__device__ __forceinline__ Seq sequence(const AttnArgs& a, int b, bool report) {
+  const int q0 = a.cu_q[b], q1 = a.cu_q[b + 1];
+  Seq s;
+  int n = q1 - q0;
+  bool bad = false;
+  if (q0 < 0 || q1 < q0 || q1 > a.T) {
+    bad = true;
+    n = 0;
+  }
+  int L = a.kv_len != nullptr ? a.kv_len[b] : n;
+  if (a.kv_len != nullptr && (L < 0 || L > a.max_len)) {
+    bad = true;
+    L = L < 0 ? 0 : a.max_len;
+  }
+  if (bad && report) record_error(a.err, kErrBadIndex, static_cast<uint32_t>(b));
+  s.L = L;
+  s.n = min(n, L);
+  s.none = n - s.n;
+  s.row0 = q0 + s.none;
+  s.past = L - s.n;
+  return s;
+}
+
+// Row tiles of M rows, and the key tiles that row tile r reads.
+template <int M>
+__device__ __forceinline__ int row_tiles(const Seq& s, int G) {
+  return static_cast<int>((static_cast<int64_t>(s.n) * G + M - 1) / M);
+}
+template <int M, int KT>
+__device__ __forceinline__ int key_tiles(const Seq& s, int G, int r) {
+  const int64_t last = (static_cast<int64_t>(M) * (r + 1) - 1) / G;
+  const int keys = s.past + static_cast<int>(last < s.n ? last : s.n - 1) + 1;
+  return (keys + KT - 1) / KT;
+}
+// Key tiles of the row tiles before r.  But for the last tile, whose rows may end
+// early, tile i reads floor((M i + M - 1 + (past + KT) G) / (KT G)), which is u i / v
+// + const in whole numbers and repeats every v tiles up to a multiple of u.
+template <int M, int KT>
+__device__ __forceinline__ int64_t tiles_before(const Seq& s, int G, int r) {
+  constexpr int kUnit = M < KT ? M : KT;  // divides both
+  constexpr int u = M / kUnit;
+  const int64_t v = static_cast<int64_t>(KT / kUnit) * G;
+  const int64_t e = (M - 1 + (static_cast<int64_t>(s.past) + KT) * G) / kUnit;
+  int64_t sum = 0;
+  if (u == 1) {
+    // sum of floor(j / v) over j < x
+    auto below = [v](int64_t x) {
+      const int64_t q = x / v;
+      return v * (q * (q - 1) / 2) + q * (x - q * v);
+    };
+    sum = below(r + e) - below(e);
+  } else {
+    const int64_t whole = r / v, rest = r - whole * v;
+    int64_t period = 0;
+    const int64_t upto = whole > 0 ? v : rest;
+    for (int64_t i = 0; i < upto; ++i) {
+      const int64_t f = (u * i + e) / v;
+      period += f;
+      if (i < rest) sum += f;
+    }
+    // tile i + q v reads u q more than tile i
+    sum += whole * period + u * (v * (whole * (whole - 1) / 2) + whole * rest);
+  }
+  return sum;
+}
+template <int M, int KT>
+__device__ __forceinline__ int64_t head_tiles(const Seq& s, int G) {
+  const int R = row_tiles<M>(s, G);
+  return R == 0 ? 0 : tiles_before<M, KT>(s, G, R - 1) + key_tiles<M, KT>(s, G, R - 1);
+}
+
+// A CTA's place in its run of tiles.
+template <int M, int KT>
+struct Walk {
+  Seq s;
+  int b, h, r, R;
+  int t, end;        // key tiles of the item in this run
+  int len;           // the item's key tiles
+  int64_t at, left;  // tile t among all; tiles of the run from t on
+
+  __device__ __forceinline__ void enter(const AttnArgs& a) {
+    len = key_tiles<M, KT>(s, a.G, r);
+    end = left < len - t ? t + static_cast<int>(left) : len;
+  }
+  // to the next item; false at the run's end
+  __device__ __forceinline__ bool next(const AttnArgs& a) {
+    at += end - t;
+    left -= end - t;
+    if (left <= 0) return false;
+    if (++r == R) {
+      r = 0;
+      if (++h == a.Hkv) {
+        h = 0;
+        do {
+          if (++b >= a.B) {  // (lengths that changed under the call)
+            left = 0;
+            return false;
+          }
+          s = sequence(a, b, false);
+          R = row_tiles<M>(s, a.G);
+        } while (R == 0);
+      }
+    }
+    t = 0;
+    enter(a);
+    return true;
+  }
+};
+
+struct Shares {
+  int64_t total;
+  int n;  // CTAs with work
+  // the CTA whose run holds tile x
+  __device__ __forceinline__ int owner(int64_t x) const { return static_cast<int>(((x + 1) * n - 1) / total); }
+};
+
+// The run of this CTA; false where it has none.  Every thread calls it; `scratch`
+// holds THREADS / 32 + 4 words of 8 bytes.
+template <int M, int KT, int THREADS>
+__device__ __forceinline__ bool start(const AttnArgs& a, int64_t* scratch, Walk<M, KT>& w, Shares& sh) {
+  constexpr int kWarps = THREADS / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto scan = [&](int64_t v, int64_t& sum) {  // the threads' values before this one's; their sum
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[warp] = x;
+    __syncthreads();
+    int64_t before = x - v;
+    sum = 0;
+#pragma unroll 4
+    for (int i = 0; i < kWarps; ++i) {
+      const int64_t y = scratch[i];
+      if (i < warp) before += y;
+      sum += y;
+    }
+    return before;
+  };
+  auto tiles_of = [&](int b, bool report) {
+    return b < a.B ? head_tiles<M, KT>(sequence(a, b, report), a.G) * a.Hkv : static_cast<int64_t>(0);
+  };
+  int64_t total = 0, sum, mine = 0, before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += THREADS) {
+    mine = tiles_of(b0 + tid, blockIdx.x == 0);
+    before = scan(mine, sum);
+    total += sum;
+  }
+  sh.total = total;
+  sh.n = static_cast<int>(total < static_cast<int64_t>(gridDim.x) ? total : static_cast<int64_t>(gridDim.x));
+  if (static_cast<int>(blockIdx.x) >= sh.n) return false;
+  const int64_t lo = total * blockIdx.x / sh.n, hi = total * (blockIdx.x + 1) / sh.n;
+  int64_t base = 0;
+  for (int b0 = 0; b0 < a.B; b0 += THREADS) {
+    if (a.B > THREADS) {
+      mine = tiles_of(b0 + tid, false);
+      before = scan(mine, sum);
+    }
+    if (base + before <= lo && lo < base + before + mine) {
+      scratch[kWarps] = b0 + tid;
+      scratch[kWarps + 1] = lo - base - before;
+    }
+    base += sum;
+  }
+  __syncthreads();
+  w.b = static_cast<int>(scratch[kWarps]);
+  int64_t rest = scratch[kWarps + 1];
+  w.s = sequence(a, w.b, false);
+  w.R = row_tiles<M>(w.s, a.G);
+  const int64_t per_head = head_tiles<M, KT>(w.s, a.G);
+  w.h = static_cast<int>(rest / per_head);
+  rest -= w.h * per_head;
+  // the last row tile that starts at or before `rest`: 32 candidates at a time
+  int lo_r = 0, hi_r = w.R;  // in [lo_r, hi_r)
+  while (hi_r - lo_r > 1) {
+    const int step = (hi_r - lo_r + 31) / 32;
+    const int r = lo_r + lane * step;
+    const bool reached = r < hi_r && tiles_before<M, KT>(w.s, a.G, r) <= rest;
+    const int top = 31 - __clz(__ballot_sync(0xffffffffu, reached));
+    lo_r += top * step;
+    hi_r = min(hi_r, lo_r + step);
+  }
+  w.r = lo_r;
+  w.t = static_cast<int>(rest - tiles_before<M, KT>(w.s, a.G, lo_r));
+  w.at = lo;
+  w.left = hi - lo;
+  w.enter(a);
+  return true;
+}
+
+// Rows of tokens that see no key: zeros, and minus infinity as their logarithm.
+__device__ __forceinline__ void clear_empty_rows(const AttnArgs& a) {
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    const Seq s = sequence(a, b, false);
+    const int width = a.Hq * a.D;
+    for (int64_t i = threadIdx.x; i < static_cast<int64_t>(s.none) * width; i += blockDim.x)
+      a.out[(s.row0 - s.none + i / width) * a.out_stride + i % width] = 0;
+    if (a.lse != nullptr)
+      for (int64_t i = threadIdx.x; i < static_cast<int64_t>(s.none) * a.Hq; i += blockDim.x)
+        a.lse[static_cast<int64_t>(s.row0 - s.none) * a.Hq + i] = -INFINITY;
+  }
+}
+
+// 2^x; x = -inf gives 0
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float log2_fast(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// the maximum that scores are taken relative to: of rows without any score yet zero
+__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.f : m; }
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+}  // namespace attn
+}  // namespace moe

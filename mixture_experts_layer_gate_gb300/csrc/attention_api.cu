@@ -48,6 +48,55 @@ bool half_dtype(int d) { return d == MOE_T_BF16 || d == MOE_T_F16; }
 // 16-byte aligned rows of 16-bit values
 bool wide_rows(const void* p, int64_t stride, int64_t cols) { return rows_ok(p, stride, cols, 16) && stride % 8 == 0; }
 
+moe_status_t validate_attention(const moe_attention_t* p) {
+  if (p == nullptr || p->T < 0 || p->B < 0 || p->Hq < 1 || p->Hkv < 1 || p->Hq % p->Hkv != 0) return MOE_ERR_INVALID_ARG;
+  if (p->D < 8 || p->D % 8 != 0 || p->max_q < 1 || !half_dtype(p->dtype)) return MOE_ERR_INVALID_ARG;
+  if (p->cache_dtype < MOE_CACHE_SAME || p->cache_dtype > MOE_CACHE_E4M3) return MOE_ERR_INVALID_ARG;
+  if (!(p->scale > 0.f) || !std::isfinite(p->scale)) return MOE_ERR_INVALID_ARG;
+  if (p->D > 128 || p->Hq > 4096 || p->T > (1 << 28) || p->B > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t attention_workspace(const moe_attention_t& p) {
+  return kHeaderBytes + kAttnTicketBytes + 2 * kAttnMaxCtas * attn_piece_bytes(kAttnFewRows, p.D);
+}
+
+moe_status_t check_attention(const moe_attention_t* p, const void* q, int64_t q_stride, const int32_t* cu_q,
+                             const void* out, int64_t out_stride, const float* lse, const void* ws, size_t ws_bytes) {
+  MOE_TRY(check_header(ws, ws_bytes));
+  if (ws_bytes < attention_workspace(*p)) return MOE_ERR_WORKSPACE;
+  if (p->B == 0 || p->T == 0) return MOE_OK;
+  const int64_t nq = static_cast<int64_t>(p->Hq) * p->D;
+  if (!wide_rows(q, q_stride, nq) || !wide_rows(out, out_stride, nq)) return MOE_ERR_INVALID_ARG;
+  if (cu_q == nullptr || !aligned(cu_q, 4) || !aligned(lse, 4)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe_status_t attend(const moe_attention_t* p, AttnArgs& a, const void* q, int64_t q_stride, const int32_t* cu_q,
+                    void* out, int64_t out_stride, float* lse, void* ws, moe_stream_t stream) {
+  DeviceInfo di;
+  if (device_info(&di) != cudaSuccess) return MOE_ERR_CUDA;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  a.q = static_cast<const uint16_t*>(q);
+  a.cu_q = cu_q;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.err = reinterpret_cast<uint32_t*>(base);
+  a.tickets = reinterpret_cast<uint32_t*>(base + kHeaderBytes);
+  a.partial = reinterpret_cast<float*>(base + kHeaderBytes + kAttnTicketBytes);
+  a.q_stride = q_stride;
+  a.out_stride = out_stride;
+  a.T = p->T;
+  a.B = p->B;
+  a.Hq = p->Hq;
+  a.Hkv = p->Hkv;
+  a.D = p->D;
+  a.G = p->Hq / p->Hkv;
+  a.f16 = p->dtype == MOE_T_F16;
+  a.scale_log2 = p->scale * 1.4426950408889634f;
+  return cuda_status(launch_attention_few(a, di.sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -147,6 +196,54 @@ moe_status_t moe_linear(const moe_linear_t* l, const void* x, int64_t x_stride, 
   a.act = l->activation;
   a.err = static_cast<uint32_t*>(ws);
   return cuda_status(launch_linear(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_paged_attention(const moe_attention_t* p, const void* q, int64_t q_stride, const moe_kv_t* cache,
+                                 const int32_t* page_table, int64_t table_stride, const int32_t* cu_q,
+                                 const int32_t* kv_len, void* out, int64_t out_stride, float* lse, void* ws,
+                                 size_t ws_bytes, moe_stream_t stream) {
+  MOE_TRY(validate_attention(p));
+  AttnArgs a = {};
+  MOE_TRY(check_cache(cache, p->cache_dtype, p->Hkv, p->D, p->page_size, p->num_pages, &a.kv));
+  if (p->max_pages < 1) return MOE_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(p->max_pages) * p->page_size > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+  MOE_TRY(check_attention(p, q, q_stride, cu_q, out, out_stride, lse, ws, ws_bytes));
+  if (p->B == 0 || p->T == 0) return MOE_OK;
+  if (page_table == nullptr || !aligned(page_table, 4) || (p->B > 1 && table_stride < p->max_pages) ||
+      kv_len == nullptr || !aligned(kv_len, 4))
+    return MOE_ERR_INVALID_ARG;
+  a.page_table = page_table;
+  a.table_stride = table_stride;
+  a.kv_len = kv_len;
+  a.page_shift = shift_of(p->page_size);
+  a.num_pages = p->num_pages;
+  a.max_len = p->max_pages * p->page_size;
+  a.e4m3 = p->cache_dtype == MOE_CACHE_E4M3;
+  return attend(p, a, q, q_stride, cu_q, out, out_stride, lse, ws, stream);
+}
+
+moe_status_t moe_prompt_attention(const moe_attention_t* p, const void* q, int64_t q_stride, const void* k,
+                                  int64_t k_stride, const void* v, int64_t v_stride, const int32_t* cu_q, void* out,
+                                  int64_t out_stride, float* lse, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  MOE_TRY(validate_attention(p));
+  if (p->cache_dtype != MOE_CACHE_SAME || p->page_size != 0 || p->num_pages != 0 || p->max_pages != 0)
+    return MOE_ERR_INVALID_ARG;
+  MOE_TRY(check_attention(p, q, q_stride, cu_q, out, out_stride, lse, ws, ws_bytes));
+  if (p->B == 0 || p->T == 0) return MOE_OK;
+  const int64_t nk = static_cast<int64_t>(p->Hkv) * p->D;
+  if (!wide_rows(k, k_stride, nk) || !wide_rows(v, v_stride, nk)) return MOE_ERR_INVALID_ARG;
+  AttnArgs a = {};
+  a.kv.k = static_cast<uint8_t*>(const_cast<void*>(k));
+  a.kv.v = static_cast<uint8_t*>(const_cast<void*>(v));
+  a.kv.k_token = k_stride;
+  a.kv.v_token = v_stride;
+  a.kv.k_head = a.kv.v_head = p->D;
+  a.num_pages = 1;
+  return attend(p, a, q, q_stride, cu_q, out, out_stride, lse, ws, stream);
+}
+
+size_t moe_attention_workspace_size(const moe_attention_t* p) {
+  return validate_attention(p) == MOE_OK ? attention_workspace(*p) : 0;
 }
 
 }  // extern "C"

@@ -322,9 +322,55 @@ PyObject* linear(PyObject*, PyObject* const* v, Py_ssize_t n) {
   });
 }
 
+// [n, cols] of 32-bit integers with its stride
+Rows table(PyObject* o, int64_t n, int64_t cols, const char* what) { return rows(o, n, cols, kInt32, what); }
+
+// problem, q, k_cache, v_cache, k_scale, v_scale, page_table, cu_q, kv_len, out, lse, ws, stream
+PyObject* paged_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return run(n, 13, [&] {
+    const moe_attention_t p = problem<moe_attention_t>(v[0]);
+    const int64_t nq = static_cast<int64_t>(p.Hq) * p.D;
+    const Type b = type_of(p.dtype);
+    const Rows q = rows(v[1], p.T, nq, b, "q"), o = rows(v[9], p.T, nq, b, "out");
+    moe_kv_t c{};
+    const bool cached = cache_of(v + 2, p.dtype, p.cache_dtype, p.num_pages, p.page_size, p.Hkv, p.D, &c);
+    const Rows pages = table(v[6], p.B, p.max_pages, "page_table");
+    void* cu = flat(v[7], static_cast<int64_t>(p.B) + 1, kInt32, "cu_q");
+    void* len = flat(v[8], p.B, kInt32, "kv_len");
+    void* lse = flat(v[10], static_cast<int64_t>(p.T) * p.Hq, kFloat, "lse");
+    const Workspace ws(v[11]);
+    const moe_stream_t s = stream_of(v[12]);
+    return unlocked([&] {
+      return moe_paged_attention(&p, q.p, q.stride, cached ? &c : nullptr, static_cast<int32_t*>(pages.p), pages.stride,
+                                 static_cast<int32_t*>(cu), static_cast<int32_t*>(len), o.p, o.stride,
+                                 static_cast<float*>(lse), ws.p, ws.bytes, s);
+    });
+  });
+}
+
+// problem, q, k, v, cu_q, out, lse, ws, stream
+PyObject* prompt_attention(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return run(n, 9, [&] {
+    const moe_attention_t p = problem<moe_attention_t>(v[0]);
+    const int64_t nq = static_cast<int64_t>(p.Hq) * p.D, nk = static_cast<int64_t>(p.Hkv) * p.D;
+    const Type b = type_of(p.dtype);
+    const Rows q = rows(v[1], p.T, nq, b, "q"), o = rows(v[5], p.T, nq, b, "out");
+    const Rows k = rows(v[2], p.T, nk, b, "k"), val = rows(v[3], p.T, nk, b, "v");
+    void* cu = flat(v[4], static_cast<int64_t>(p.B) + 1, kInt32, "cu_q");
+    void* lse = flat(v[6], static_cast<int64_t>(p.T) * p.Hq, kFloat, "lse");
+    const Workspace ws(v[7]);
+    const moe_stream_t s = stream_of(v[8]);
+    return unlocked([&] {
+      return moe_prompt_attention(&p, q.p, q.stride, k.p, k.stride, val.p, val.stride, static_cast<int32_t*>(cu), o.p,
+                                  o.stride, static_cast<float*>(lse), ws.p, ws.bytes, s);
+    });
+  });
+}
+
 #define ENTRY(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(add_rms_norm), ENTRY(router_logits), ENTRY(gemm_fp8_block), ENTRY(gemm_fp8_block_swiglu),
-                         ENTRY(forward_few), ENTRY(qk_norm_rope), ENTRY(linear),
+                         ENTRY(forward_few), ENTRY(qk_norm_rope), ENTRY(linear), ENTRY(paged_attention),
+                         ENTRY(prompt_attention),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -320,4 +320,29 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
 constexpr int kLinearFewRows = 16;
 cudaError_t launch_linear_few(const LinearArgs& a, int sms, cudaStream_t s);
 
+struct AttnArgs {
+  const uint16_t* q;          // [T, Hq * D]
+  KvCache kv;                 // the cache, or packed rows (page_table null: one page, key j in row cu_q[b] + j)
+  const int32_t* page_table;  // [B, max_pages]
+  const int32_t* cu_q;        // [B + 1]
+  const int32_t* kv_len;      // [B], or null: as many keys as rows
+  uint16_t* out;              // [T, Hq * D]
+  float* lse;                 // [T, Hq] or null
+  uint32_t* err;
+  uint32_t* tickets;          // [kAttnMaxCtas], zero between calls
+  float* partial;             // [2 kAttnMaxCtas] pieces of split rows
+  int64_t q_stride, out_stride, table_stride;
+  int T, B, Hq, Hkv, D, G;
+  int page_shift, num_pages;
+  int max_len;                // keys that a row of the page table holds
+  int f16, e4m3;
+  float scale_log2;           // scale * log2(e)
+};
+constexpr int kAttnMaxCtas = 160;
+constexpr size_t kAttnTicketBytes = 1024;
+constexpr int kAttnFewRows = 16;
+// bytes of a piece's sums, maxima and totals
+constexpr size_t attn_piece_bytes(int rows, int D) { return static_cast<size_t>(rows) * ((D <= 64 ? 64 : 128) + 2) * 4; }
+cudaError_t launch_attention_few(const AttnArgs& a, int sms, cudaStream_t s);
+
 }  // namespace moe

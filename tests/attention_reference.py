@@ -74,3 +74,42 @@ def linear(x, w, bias, act, residual):
         out = out + residual.cpu().double()
         dv = dv + EPS32 * out.abs()
     return out, dv
+
+
+def attend(q, k, v, past, scale, p_half_step, unit=None):
+    """One sequence: q [n, Hq, D], k and v [L, Hkv, D] in float64; new token i sees keys [0, past + i].  Returns out,
+    lse and how far each may be from it before out's own rounding.  p_half_step: half a step of the type that weights
+    are rounded to; unit: what weights are relative to where not 1 (8-bit values' largest scale)."""
+    n, Hq, D = q.shape
+    L, Hkv, _ = k.shape
+    G = Hq // Hkv
+    out, dout = torch.zeros(n, Hq, D, dtype=torch.float64), torch.zeros(n, Hq, D, dtype=torch.float64)
+    lse, dlse = torch.full((n, Hq), -math.inf, dtype=torch.float64), torch.zeros(n, Hq, dtype=torch.float64)
+    for i in range(n):
+        seen = past + i + 1
+        if seen <= 0:
+            continue
+        for h in range(Hkv):
+            heads = slice(h * G, (h + 1) * G)
+            kk, vv = k[:seen, h], v[:seen, h]
+            x = q[i, heads] @ kk.T * scale
+            # a score: D products 16 at a time (the tensor core may truncate), then its factors
+            dx = ((D / 16 + 2) * 2 * EPS32 * (q[i, heads].abs() @ kk.abs().T) * scale + 4 * EPS32 * x.abs()).amax(dim=1)
+            top = x.amax(dim=1, keepdim=True)
+            w = torch.exp(x - top)
+            l = w.sum(dim=1, keepdim=True)
+            p = w / l
+            out[i, heads] = p @ vv
+            lse[i, heads] = (top + torch.log(l))[:, 0]
+            # a weight: its score's error, the exponent's argument (scores times log2 e, the subtraction) and exp2
+            dw = dx + 4 * EPS32 * (x - top).abs().amax(dim=1) + 8 * EPS32 + 4 * EPS32 * x.abs().amax(dim=1)
+            size = p @ vv.abs()
+            steps = seen / 16 + 64  # joins and rescalings of the sums
+            # weights under f16's normal range are off by 2^-25 of what they are relative to: 1, or the unit of the
+            # 8-bit values' scales (at most twice the largest) times codes of at most 448
+            small = (2.0 ** -25 * vv.abs().sum(dim=0)[None, :] if unit is None else
+                     torch.full_like(size, 2.0 ** -25 * 2 * unit * 448 * seen)) / l
+            dout[i, heads] = (2 * dw[:, None] + p_half_step + 2 * steps * 2 * EPS32) * size + small
+            dlse[i, heads] = dw + steps * 2 * EPS32 + 8 * EPS32 * (1 + lse[i, heads].abs())
+    return out, lse, dout, dlse
+
