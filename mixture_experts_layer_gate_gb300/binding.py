@@ -550,8 +550,7 @@ def qk_norm_rope(r: RopeProblem, q, k, positions, turns, q_out, ws, k_out=None, 
     page_size, Hkv, D] of any order in memory with slots int32 [T], and for "e4m3" k_scale, v_scale float32 [num_pages,
     Hkv, page_size]."""
     _check((_ops or _native()).qk_norm_rope(r, q, k, v, positions, turns, q_weight, k_weight, q_out, k_out, k_cache,
-                                            v_cache, k_scale, v_scale, slots, ws, stream), "moe_qk_norm_rope", "moe_linear",
-            "moe_attention_workspace_size", "moe_paged_attention", "moe_prompt_attention")
+                                            v_cache, k_scale, v_scale, slots, ws, stream), "moe_qk_norm_rope")
 
 
 def attention_problem(T, B, Hq, Hkv, D, max_q, dtype="bf16", cache_dtype=None, page_size=0, num_pages=0, max_pages=0,
