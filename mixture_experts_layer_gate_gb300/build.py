@@ -23,7 +23,7 @@ LIB = os.path.join(PKG, "libmoe_gb300.so")
 SOURCES = ["gemm.cu", "api.cu", "gate.cu", "align.cu", "route.cu", "reduce.cu", "noalloc.cu", "scale.cu",
            "repack.cu", "ops_api.cu", "norm.cu", "router.cu", "fp8_block.cu", "fp8_few.cu", "few.cu",
            "attention_api.cu", "rope.cu", "linear.cu", "linear_few.cu",
-           "attention_few.cu"]
+           "attention_few.cu", "attention.cu"]
 OPS = os.path.join(PKG, "_ops.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",

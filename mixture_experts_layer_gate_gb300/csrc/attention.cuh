@@ -45,16 +45,18 @@ __device__ __forceinline__ Seq sequence(const AttnArgs& a, int b, bool report) {
   return s;
 }
 
-// Row tiles of M rows, and the key tiles that row tile r reads.
+// Row tiles of M rows, and the key tiles that row tile r reads.  (A call's rows are
+// fewer than 2^30: 32-bit divisions, which are no function calls.)
 template <int M>
 __device__ __forceinline__ int row_tiles(const Seq& s, int G) {
-  return static_cast<int>((static_cast<int64_t>(s.n) * G + M - 1) / M);
+  return (s.n * G + M - 1) / M;
+}
+__device__ __forceinline__ int divided(int a, int b) {  // of numbers that are not negative
+  return static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
 }
 template <int M, int KT>
 __device__ __forceinline__ int key_tiles(const Seq& s, int G, int r) {
-  const int64_t last = (static_cast<int64_t>(M) * (r + 1) - 1) / G;
-  const int keys = s.past + static_cast<int>(last < s.n ? last : s.n - 1) + 1;
-  return (keys + KT - 1) / KT;
+  return (s.past + min(divided(M * (r + 1) - 1, G), s.n - 1) + KT) / KT;
 }
 // Key tiles of the row tiles before r.  But for the last tile, whose rows may end
 // early, tile i reads floor((M i + M - 1 + (past + KT) G) / (KT G)), which is u i / v
@@ -100,7 +102,7 @@ struct Walk {
   int b, h, r, R;
   int t, end;        // key tiles of the item in this run
   int len;           // the item's key tiles
-  int64_t at, left;  // tile t among all; tiles of the run from t on
+  int64_t left;      // tiles of the run from t on
 
   __device__ __forceinline__ void enter(const AttnArgs& a) {
     len = key_tiles<M, KT>(s, a.G, r);
@@ -108,7 +110,6 @@ struct Walk {
   }
   // to the next item; false at the run's end
   __device__ __forceinline__ bool next(const AttnArgs& a) {
-    at += end - t;
     left -= end - t;
     if (left <= 0) return false;
     if (++r == R) {
@@ -132,10 +133,17 @@ struct Walk {
 };
 
 struct Shares {
-  int64_t total;
-  int n;  // CTAs with work
-  // the CTA whose run holds tile x
-  __device__ __forceinline__ int owner(int64_t x) const { return static_cast<int>(((x + 1) * n - 1) / total); }
+  int64_t run;   // tiles of a CTA, and one more of the first `more` CTAs
+  int n, more;   // CTAs with work
+  int first;     // the CTA whose run holds the first tile of this run's first item
+  __device__ __forceinline__ int64_t run_of(int c) const { return run + (c < more); }
+  // CTAs up to the one that holds the last tile of an item of this CTA that begins
+  // in the run of `from`, `rest` tiles after this run
+  __device__ __forceinline__ int pieces(int from, int64_t rest) const {
+    int c = blockIdx.x + 1;
+    for (; rest > 0; ++c) rest -= run_of(c);
+    return c - from;
+  }
 };
 
 // The run of this CTA; false where it has none.  Every thread calls it; `scratch`
@@ -173,10 +181,12 @@ __device__ __forceinline__ bool start(const AttnArgs& a, int64_t* scratch, Walk<
     before = scan(mine, sum);
     total += sum;
   }
-  sh.total = total;
   sh.n = static_cast<int>(total < static_cast<int64_t>(gridDim.x) ? total : static_cast<int64_t>(gridDim.x));
-  if (static_cast<int>(blockIdx.x) >= sh.n) return false;
-  const int64_t lo = total * blockIdx.x / sh.n, hi = total * (blockIdx.x + 1) / sh.n;
+  const int cta = blockIdx.x;
+  if (cta >= sh.n) return false;
+  sh.run = total / sh.n;
+  sh.more = static_cast<int>(total - sh.run * sh.n);
+  const int64_t lo = sh.run * cta + min(cta, sh.more);
   int64_t base = 0;
   for (int b0 = 0; b0 < a.B; b0 += THREADS) {
     if (a.B > THREADS) {
@@ -209,8 +219,9 @@ __device__ __forceinline__ bool start(const AttnArgs& a, int64_t* scratch, Walk<
   }
   w.r = lo_r;
   w.t = static_cast<int>(rest - tiles_before<M, KT>(w.s, a.G, lo_r));
-  w.at = lo;
-  w.left = hi - lo;
+  w.left = sh.run_of(cta);
+  sh.first = cta;
+  for (int64_t rest_t = w.t; rest_t > 0;) rest_t -= sh.run_of(--sh.first);
   w.enter(a);
   return true;
 }

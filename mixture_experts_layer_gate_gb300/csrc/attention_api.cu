@@ -53,12 +53,16 @@ moe_status_t validate_attention(const moe_attention_t* p) {
   if (p->D < 8 || p->D % 8 != 0 || p->max_q < 1 || !half_dtype(p->dtype)) return MOE_ERR_INVALID_ARG;
   if (p->cache_dtype < MOE_CACHE_SAME || p->cache_dtype > MOE_CACHE_E4M3) return MOE_ERR_INVALID_ARG;
   if (!(p->scale > 0.f) || !std::isfinite(p->scale)) return MOE_ERR_INVALID_ARG;
-  if (p->D > 128 || p->Hq > 4096 || p->T > (1 << 28) || p->B > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+  if (p->D > 128 || p->Hq > 4096 || p->B > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(p->T) * p->Hq > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
+bool few_rows(const moe_attention_t& p) { return static_cast<int64_t>(p.max_q) * (p.Hq / p.Hkv) <= kAttnFewRows; }
+
 size_t attention_workspace(const moe_attention_t& p) {
-  return kHeaderBytes + kAttnTicketBytes + 2 * kAttnMaxCtas * attn_piece_bytes(kAttnFewRows, p.D);
+  return kHeaderBytes + kAttnTicketBytes +
+         2 * kAttnMaxCtas * attn_piece_bytes(few_rows(p) ? kAttnFewRows : kAttnRows, p.D);
 }
 
 moe_status_t check_attention(const moe_attention_t* p, const void* q, int64_t q_stride, const int32_t* cu_q,
@@ -94,7 +98,8 @@ moe_status_t attend(const moe_attention_t* p, AttnArgs& a, const void* q, int64_
   a.G = p->Hq / p->Hkv;
   a.f16 = p->dtype == MOE_T_F16;
   a.scale_log2 = p->scale * 1.4426950408889634f;
-  return cuda_status(launch_attention_few(a, di.sms, reinterpret_cast<cudaStream_t>(stream)));
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return cuda_status(few_rows(*p) ? launch_attention_few(a, di.sms, s) : launch_attention(a, di.sms, s));
 }
 
 }  // namespace

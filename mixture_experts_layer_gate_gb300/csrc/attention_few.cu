@@ -138,7 +138,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnAr
         more = iss.next(a);
       } else {
         ++iss.t;
-        ++iss.at;
         --iss.left;
       }
       if (more) page = page_of(iss);
@@ -153,17 +152,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnAr
   while (going) {
     // ---- an item: its rows g and g + 8
     const Seq s = cur.s;
-    const int64_t rows = static_cast<int64_t>(s.n) * a.G;
-    const int64_t row_a = static_cast<int64_t>(cur.r) * kRows + g;
-    const int live = static_cast<int>(rows - cur.r * kRows < kRows ? rows - cur.r * kRows : kRows);
+    const int live = min(s.n * a.G - cur.r * kRows, kRows);
     uint4 qf[2][DP / 32];  // of row g + 8 i
     int limit[2];          // the last key that the row sees
     float factor[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const bool there = g + 8 * i < live;
-      const int64_t R = there ? row_a + 8 * i : static_cast<int64_t>(cur.r) * kRows;
-      const int token = static_cast<int>(R / a.G), head = cur.h * a.G + static_cast<int>(R - static_cast<int64_t>(token) * a.G);
+      const int R = cur.r * kRows + (there ? g + 8 * i : 0);
+      const int token = divided(R, a.G), head = cur.h * a.G + R - token * a.G;
       limit[i] = there ? s.past + token : -1;
       factor[i] = a.scale_log2;
       const uint16_t* q = a.q + (s.row0 + token) * a.q_stride + static_cast<int64_t>(head) * a.D;
@@ -200,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnAr
         }
       }
     }
-    const int least = s.past + static_cast<int>(static_cast<int64_t>(cur.r) * kRows / a.G);  // of all rows' limits
+    const int least = s.past + divided(cur.r * kRows, a.G);  // of all rows' limits
     float o[kTiles][4];
 #pragma unroll
     for (int j = 0; j < kTiles; ++j)
@@ -498,8 +495,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnAr
     bool write = true;
     if (cur.end - cur.t < cur.len) {
       // the item lies in several runs: the last one to finish joins them
-      const int64_t item = cur.at - cur.t;
-      const int first = shares.owner(item), pieces = shares.owner(item + cur.len - 1) - first + 1;
+      const int first = cur.t > 0 ? shares.first : static_cast<int>(blockIdx.x);
+      const int pieces = shares.pieces(first, cur.len - cur.end);
       constexpr size_t kPiece = attn_piece_bytes(kRows, DP) / 4;
       auto piece = [&](int i) { return a.partial + (2 * (first + i) + (i == 0 ? 1 : 0)) * kPiece; };
       float* to = piece(static_cast<int>(blockIdx.x) - first);
@@ -545,8 +542,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnAr
       }
     }
     if (write && mine) {
-      const int64_t R = static_cast<int64_t>(cur.r) * kRows + row;
-      const int token = static_cast<int>(R / a.G), head = cur.h * a.G + static_cast<int>(R - static_cast<int64_t>(token) * a.G);
+      const int R = cur.r * kRows + row;
+      const int token = divided(R, a.G), head = cur.h * a.G + R - token * a.G;
       if (d0 < a.D) {
         uint32_t w[4];
 #pragma unroll
