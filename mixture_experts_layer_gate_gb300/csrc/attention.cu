@@ -8,9 +8,10 @@
 // its scores into weights, the other half's products run.
 //
 // Warps: 0-3 and 4-7 the halves' softmax (a thread a row: no exchange between
-// threads), 8 loads (16-bit: TMA, a box a page and 64 values) or scales (8-bit), 9
-// MMAs; 16-bit: 10 and 11 look at the values of tiles that some row does not wholly
-// see; 8-bit: 10 to 15 turn codes into f16 tiles.
+// threads), 8 loads (TMA, a box a page and 128 bytes of its rows), 9 MMAs; 16-bit: 10
+// and 11 look at the values of tiles that some row does not wholly see; 8-bit: 10
+// the tiles' scales, 12 to 15 turn codes, which TMA left in a ring of their own, into
+// f16 tiles.
 //
 // The running maximum is only raised, and O rescaled, when it grew by more than 8
 // (factors of 2^8 stay far inside the sums' and the weights' range), which is rare
@@ -31,10 +32,9 @@ using dense::commit;
 using dense::elect_one;
 using dense::expect_tx;
 using dense::mbar_arrive_cta;
-using dense::wait;
 
 constexpr int kHalf = 128, kRows = 2 * kHalf, kKeys = 128;
-constexpr int kMaxSlots = 8, kScaleSlots = 2, kDirty = 16;
+constexpr int kMaxSlots = 8, kCodeSlots = 4, kScaleSlots = 2, kDirty = 16;
 constexpr size_t kSmem = 232448;
 // Registers a thread of the softmax's warpgroups and of the others; 3 x 168 and 4 x
 // 128 at launch.
@@ -42,19 +42,20 @@ constexpr int kSoftRegs16 = 200, kLeanRegs16 = 104, kLaunchRegs16 = 168;
 constexpr int kSoftRegs8 = 192, kLeanRegs8 = 64, kLaunchRegs8 = 128;
 template <bool E4M3>
 constexpr int kThreads = E4M3 ? 512 : 384;
-constexpr int kGuards = 2, kConverters = 6;  // warps from 10 on
+constexpr int kGuards = 2, kConverters = 4;  // warps from 10, from 12 on
 constexpr uint32_t kTmemCols = 512, kOut = 256;  // scores of half i at 128 i, outputs at 256 + 128 i
 
 using BigWalk = Walk<kRows, kKeys>;
 
-// Barriers and small arrays, then (1024-byte aligned) Q's halves and the ring of key
-// and value tiles.
-constexpr int kBarBytes = 1024;
-constexpr int kScaleBytes = kScaleSlots * (2 * kKeys + 4) * 4;
+// Barriers and small arrays, then (1024-byte aligned) Q's halves, the ring of key and
+// value tiles and the ring of their codes.
+constexpr int kBarBytes = 512;
+constexpr int kScaleSlot = 2 * kKeys + 4;  // of 128 keys, of their values, unit, shrink
 template <bool E4M3>
-constexpr int kMiscBytes = E4M3 ? 4096 : kBarBytes;
-static_assert(kBarBytes + kScaleBytes <= kMiscBytes<true>, "scales lie between the barriers and Q");
+constexpr int kMiscBytes = E4M3 ? 3072 : 1024;
+static_assert(kBarBytes + kScaleSlots * kScaleSlot * 4 + 256 <= kMiscBytes<true>, "scales lie between the barriers and Q");
 __host__ __device__ constexpr int tile_bytes(int dp) { return kKeys * dp * 2; }
+__host__ __device__ constexpr int code_bytes(int dp) { return kKeys * dp; }
 
 struct Maps {
   CUtensorMap k, v;
@@ -88,6 +89,33 @@ __device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, 
       "@l tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], b, %5, p;\n\t}" ::"r"(leader),
       "r"(d), "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
+      " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// dense::wait in fewer instructions (there are many waits, and the code is long for
+// the instruction caches): a wait that runs out leaves `info` in the flag that ends
+// all waits, and it is recorded when the roles have ended.
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int info) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if ((i & 63u) != 0u) continue;
+    if (abort_flag != nullptr && *abort_flag != 0) return false;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitLimitNs) {
+      if (abort_flag != nullptr) *abort_flag = info;
+      return false;
+    }
+  }
+  return true;
 }
 
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
@@ -154,7 +182,8 @@ __device__ __forceinline__ bool locate(const AttnArgs& a, const Seq& s, int b, i
 }
 
 // DP: D rounded up to 64 or 128; the products are of that depth and width.
-template <bool E4M3, int DP>
+// F16: the products' type (8-bit: always), else bf16.
+template <bool E4M3, bool F16, int DP>
 __global__ void __launch_bounds__(kThreads<E4M3>, 1)
 attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a, const int slots, const int box_rows) {
   extern __shared__ __align__(1024) uint8_t attn_smem[];
@@ -162,25 +191,27 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
   constexpr uint32_t kTile = tile_bytes(DP);
   const uint32_t base = smem_u32(attn_smem);
   const uint32_t qbase = base + kMiscBytes<E4M3>, ring = qbase + 2u * kTile;
+  const uint32_t codes = ring + static_cast<uint32_t>(slots) * kTile;  // 8-bit
 #define FULL(s) (base + 8u * static_cast<uint32_t>(s))
 #define EMPTY(s) (base + 64u + 8u * static_cast<uint32_t>(s))
 #define QFULL(i) (base + 128u + 8u * static_cast<uint32_t>(i))
 #define SFULL(i) (base + 144u + 8u * static_cast<uint32_t>(i))
-#define PFULL(i) (base + 160u + 8u * static_cast<uint32_t>(i))
+#define PFULL(i, part) (base + 464u + 16u * static_cast<uint32_t>(i) + 8u * static_cast<uint32_t>(part))
 #define OFULL(i) (base + 176u + 8u * static_cast<uint32_t>(i))
 #define SCFULL(s) (base + 192u + 8u * static_cast<uint32_t>(s))
 #define SCEMPTY(s) (base + 208u + 8u * static_cast<uint32_t>(s))
 #define READY(s) (base + 320u + 8u * static_cast<uint32_t>(s))
+#define CFULL(s) (base + 400u + 8u * static_cast<uint32_t>(s))
+#define CEMPTY(s) (base + 432u + 8u * static_cast<uint32_t>(s))
   const uint32_t drain = base + 232u, join0 = base + 384u, join1 = base + 392u;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(attn_smem + 240);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(attn_smem + 244);
   volatile int* last_flag = reinterpret_cast<volatile int*>(attn_smem + 248);
   volatile int* dirty = reinterpret_cast<volatile int*>(attn_smem + 256);  // [kDirty]: the item that has such values
-  int64_t* scratch = reinterpret_cast<int64_t*>(attn_smem + 512);
-  float* scales = reinterpret_cast<float*>(attn_smem + kBarBytes);  // [slot]: of 128 keys, of their values, unit, shrink
-  constexpr int kScaleSlot = 2 * kKeys + 4;
+  int64_t* scratch = reinterpret_cast<int64_t*>(attn_smem + kBarBytes + (E4M3 ? kScaleSlots * kScaleSlot * 4 : 0));
+  float* scales = reinterpret_cast<float*>(attn_smem + kBarBytes);         // [slot]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool f16 = E4M3 || a.f16;  // of the products
+  static_assert(F16 || !E4M3, "codes become f16");
 
   if (tid == 0) {
     for (int s = 0; s < kMaxSlots; ++s) {
@@ -191,8 +222,13 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
     for (int i = 0; i < 2; ++i) {
       mbar_init(QFULL(i), 4u);
       mbar_init(SFULL(i), 1u);
-      mbar_init(PFULL(i), 4u);
+      mbar_init(PFULL(i, 0), 4u);
+      mbar_init(PFULL(i, 1), 4u);
       mbar_init(OFULL(i), 1u);
+    }
+    for (int s = 0; s < kCodeSlots; ++s) {
+      mbar_init(CFULL(s), 1u);
+      mbar_init(CEMPTY(s), kConverters);
     }
     for (int s = 0; s < kScaleSlots; ++s) {
       mbar_init(SCFULL(s), 1u);
@@ -204,10 +240,8 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
     for (int i = 0; i < kDirty; ++i) dirty[i] = -1;
     *abort_flag = 0;
     fence_mbar_init();
-    if (!E4M3) {
-      tma_prefetch_desc(&maps.k);
-      tma_prefetch_desc(&maps.v);
-    }
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
   }
   if (warp == 9) {
     tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), kTmemCols);
@@ -236,8 +270,12 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(E4M3 ? kLeanRegs8 : kLeanRegs16));
     bool ok = true;
-    if (some && warp == 8 && !E4M3) {
+    if (some && warp == 8) {
       // ------------------------------------------------------ TMA producer
+      // (8-bit: of codes, into their own ring)
+      const int my_slots = E4M3 ? kCodeSlots : slots;
+      constexpr uint32_t kMine = E4M3 ? code_bytes(DP) : kTile, kRowBytes = E4M3 ? DP : 128u;
+      constexpr int kBoxes = E4M3 ? 1 : kChunks;  // side by side
       const uint32_t leader = elect_one();
       const bool paged = a.page_table != nullptr;
       const int boxes = kKeys / box_rows, box_shift = 31 - __clz(box_rows);
@@ -270,20 +308,21 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
           const int key0 = t * kKeys, there = min(boxes, (s.L - key0 + box_rows - 1) >> box_shift);
 #pragma unroll 1
           for (int kv = 0; kv < 2 && ok; ++kv) {
-            ok = wait(EMPTY(st), ph ^ 1u, abort_flag, a.err, 0x700u);
+            const uint32_t full = E4M3 ? CFULL(st) : FULL(st);
+            ok = wait(E4M3 ? CEMPTY(st) : EMPTY(st), ph ^ 1u, abort_flag, 0x700);
             if (!ok) break;
-            const uint32_t dst = ring + static_cast<uint32_t>(st) * kTile;
-            expect_tx(leader, FULL(st), static_cast<uint32_t>(there * box_rows * 128 * kChunks));
+            const uint32_t dst = (E4M3 ? codes : ring) + static_cast<uint32_t>(st) * kMine;
+            expect_tx(leader, full, static_cast<uint32_t>(there * box_rows) * kRowBytes * kBoxes);
             for (int i = 0; i < there; ++i) {
               const int p = __shfl_sync(0xffffffffu, mine, i);
               const int row = paged ? (key0 + (i << box_shift)) & ((1 << a.page_shift) - 1) : s.row0 + key0;
 #pragma unroll
-              for (int c = 0; c < kChunks; ++c)
-                load_box4(leader, dst + static_cast<uint32_t>(c * 128 * 128 + ((i << box_shift) * 128)),
-                          kv == 0 ? &maps.k : &maps.v, FULL(st), 64 * c, row, b_h, p);
+              for (int c = 0; c < kBoxes; ++c)
+                load_box4(leader, dst + static_cast<uint32_t>(c * 128 * 128) + static_cast<uint32_t>(i << box_shift) * kRowBytes,
+                          kv == 0 ? &maps.k : &maps.v, full, 64 * c, row, b_h, p);
             }
             ++issued;
-            if (++st == slots) {
+            if (++st == my_slots) {
               st = 0;
               ph ^= 1u;
             }
@@ -292,19 +331,21 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
         w = next;
       }
       if (!ok) {  // after an abort the loads in flight land before the CTA leaves
-        for (int i = min(issued, slots); i > 0; --i) {
-          st = st == 0 ? slots - 1 : st - 1;
-          if (st == slots - 1) ph ^= 1u;
-          wait(FULL(st), ph, nullptr, a.err, 0x701u);
+        for (int i = min(issued, my_slots); i > 0; --i) {
+          st = st == 0 ? my_slots - 1 : st - 1;
+          if (st == my_slots - 1) ph ^= 1u;
+          wait(E4M3 ? CFULL(st) : FULL(st), ph, nullptr, 0x701);
         }
       }
-    } else if (some && warp == 8) {
+    } else if (E4M3 && some && warp == 10) {
       // ------------------------------------ 8-bit: scales of a tile's keys and values
       // four keys a lane; the values' relative to the largest so far, rounded up to
       // a power of two
       uint32_t n = 0;
-      for (bool more = true; more && ok;) {
+      int item = 0;
+      for (bool more = true; more && ok; ++item) {
         float unit = 0.f;
+        const int least = least_of(w);
         for (int t = w.t; t < w.end; ++t, ++n) {
           const uint32_t slot = n % kScaleSlots;
           const int key = t * kKeys + 4 * lane;
@@ -318,10 +359,19 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
             }
           }
           float most = 0.f;
-          const float each[4] = {vs.x, vs.y, vs.z, vs.w};
+          float* each = &vs.x;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (key + e < w.s.L && fabsf(each[e]) < INFINITY) most = fmaxf(most, fabsf(each[e]));
+          for (int e = 0; e < 4; ++e) {
+            const bool finite = fabsf(each[e]) < INFINITY;
+            if (key + e >= w.s.L) {
+              each[e] = 0.f;
+            } else if (finite) {
+              most = fmaxf(most, fabsf(each[e]));
+            } else if (t * kKeys + kKeys - 1 > least) {  // (as values that are not finite)
+              each[e] = 0.f;
+              dirty[item % kDirty] = item;
+            }
+          }
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
           float shrink = 1.f;
@@ -333,7 +383,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
             }
           }
           const float per = 1.f / unit;
-          ok = wait(SCEMPTY(slot), (n / kScaleSlots & 1u) ^ 1u, abort_flag, a.err, 0x710u);
+          ok = wait(SCEMPTY(slot), (n / kScaleSlots & 1u) ^ 1u, abort_flag, 0x710);
           if (!ok) break;
           float* to = scales + slot * kScaleSlot;
           *reinterpret_cast<float4*>(to + 4 * lane) = ks;
@@ -350,7 +400,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
     } else if (some && warp == 9) {
       // -------------------------------------------------------- MMA issuer
       const uint32_t leader = elect_one();
-      const uint32_t fmt = f16 ? 0u : 1u;
+      const uint32_t fmt = F16 ? 0u : 1u;
       const uint32_t idesc_s = make_idesc(128u, kKeys, fmt), idesc_o = make_idesc(128u, DP, fmt) | (1u << 16);
       const uint64_t kd = sw128_kmajor_desc(qbase);
       const uint32_t hi = static_cast<uint32_t>(kd >> 32);
@@ -368,9 +418,10 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
                    low | (addr(tile + c * 16384u) + 2u * k), hi, idesc_s, (c | k) != 0);
         commit<false>(leader, SFULL(i));
       };
-      auto outputs = [&](int i, uint32_t tile, bool first) {
+      // (a tile's keys in two parts: the first's products run while the second's weights are made)
+      auto outputs = [&](int i, int part, uint32_t tile, bool first) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 4 * part; k < 4 * part + 4; ++k)
           mma_ts(leader, tmem + kOut + 128u * i, tmem + 128u * i + 8u * k, v_low | (addr(tile) + 128u * k), hi, idesc_o,
                  !(first && k == 0));
       };
@@ -384,42 +435,46 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
         }
       };
       // a tile is there (16-bit: and looked at, in which the others' wait lies already)
-      auto there = [&](uint32_t info) {
-        return (E4M3 || wait(READY(st), ph, abort_flag, a.err, info)) && wait(FULL(st), ph, abort_flag, a.err, info);
+      auto there = [&](int info) {
+        return (E4M3 || wait(READY(st), ph, abort_flag, info)) && wait(FULL(st), ph, abort_flag, info);
       };
       auto tile_at = [&](int s) { return ring + static_cast<uint32_t>(s) * kTile; };
       for (bool more = true; more && ok;) {
         const int e[2] = {end_of(w, 0), end_of(w, 1)};
         for (int i = 0; i < 2 && ok; ++i)
           if (w.t < e[i]) {
-            ok = wait(QFULL(i), qph[i], abort_flag, a.err, 0x720u);
+            ok = wait(QFULL(i), qph[i], abort_flag, 0x720);
             qph[i] ^= 1u;
           }
-        ok = ok && there(0x721u);
+        ok = ok && there(0x721);
         if (!ok) break;
         tc_fence_after();
         any = true;
+#pragma unroll 1
         for (int i = 0; i < 2; ++i)
-          if (w.t < e[i]) scores(i, tile_at(st));
+          if (w.t < (i == 0 ? e[0] : e[1])) scores(i, tile_at(st));
         commit<false>(leader, EMPTY(st));
         step();
         for (int t = w.t; t < w.end && ok; ++t) {
           const int vs = st;
-          ok = there(0x722u);
+          ok = there(0x722);
           step();
           const int ks = st;
           const bool again = t + 1 < w.end;
           if (again) {
-            ok = ok && there(0x724u);
+            ok = ok && there(0x724);
             step();
           }
           for (int i = 0; i < 2 && ok; ++i) {
             if (t < e[i]) {
-              ok = wait(PFULL(i), pph[i], abort_flag, a.err, 0x725u);
+              for (int part = 0; part < 2 && ok; ++part) {
+                ok = wait(PFULL(i, part), pph[i], abort_flag, 0x725);
+                if (!ok) break;
+                tc_fence_after();
+                outputs(i, part, tile_at(vs), t == w.t);
+              }
               if (!ok) break;
               pph[i] ^= 1u;
-              tc_fence_after();
-              outputs(i, tile_at(vs), t == w.t);
               if (t + 1 >= e[i]) commit<false>(leader, OFULL(i));
             }
             if (i == 1) commit<false>(leader, EMPTY(vs));
@@ -431,7 +486,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
       }
       if (!ok && any) {  // MMAs in flight end before tensor memory is freed
         if (leader != 0u) mma_commit(drain);
-        wait(drain, 0u, nullptr, a.err, 0x730u);
+        wait(drain, 0u, nullptr, 0x730);
       }
     } else if (some && !E4M3) {
       // ------------------- 16-bit: values of tiles that some row does not wholly see
@@ -442,7 +497,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
         const int least = least_of(w);
         for (int u = 2 * w.t; u < 2 * w.end; ++u) {  // keys, values
           const int t = u >> 1;
-          ok = wait(FULL(st), ph, abort_flag, a.err, 0x740u);
+          ok = wait(FULL(st), ph, abort_flag, 0x740);
           if (!ok) break;
           if ((u & 1) != 0 && t * kKeys + kKeys - 1 > least) {
             const uint32_t tile = ring + static_cast<uint32_t>(st) * kTile;
@@ -457,7 +512,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
               } else {
                 const uint4 v = dense::lds_u4(at);
                 uint32_t bad = 0;
-                const uint4 x = make_uint4(tame(v.x, f16, bad), tame(v.y, f16, bad), tame(v.z, f16, bad), tame(v.w, f16, bad));
+                const uint4 x = make_uint4(tame(v.x, F16, bad), tame(v.y, F16, bad), tame(v.z, F16, bad), tame(v.w, F16, bad));
                 if (bad) dense::sts_u4(at, x);
                 odd |= bad;
               }
@@ -474,57 +529,29 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
         }
         more = ok && w.next(a);
       }
-    } else if (some) {
+    } else if (E4M3 && some && warp >= 12) {
       // ------------------------------------------- 8-bit: codes into f16 tiles
-      // Thread j takes 16-byte pieces j, j + 192, ... of a tile (lanes go along a
-      // row); a tile's codes are fetched before the wait for the place they go to.
-      constexpr int kPer = kKeys * DP / 16, kT = 32 * kConverters, kMine = (kPer + kT - 1) / kT, kRowPieces = DP / 16;
-      const int me = (warp - 10) * 32 + lane;
-      int st = 0, item = 0;
-      uint32_t ph = 0;
-      uint4 next[kMine];
-      auto fetch = [&](const BigWalk& x, int t, int kv) {
-        // lane i < 8: the page of keys 16 i .. of the tile
-        const int key0 = t * kKeys;
-        int p = 0;
-        if (lane < 8 && key0 + 16 * lane < x.s.L) {
-          p = a.page_table[x.b * a.table_stride + ((key0 + 16 * lane) >> a.page_shift)];
-          if (p < 0 || p >= a.num_pages) {
-            record_error(a.err, kErrBadIndex, static_cast<uint32_t>(x.b));
-            p = -1;
-          }
-        }
-        const uint8_t* from = kv == 0 ? a.kv.k : a.kv.v;
-        const int64_t ps = kv == 0 ? a.kv.k_page : a.kv.v_page, ts = kv == 0 ? a.kv.k_token : a.kv.v_token;
-        from += x.h * (kv == 0 ? a.kv.k_head : a.kv.v_head);
-#pragma unroll
-        for (int j = 0; j < kMine; ++j) {
-          const int i = me + j * kT, r = i / kRowPieces, c = i % kRowPieces;
-          const int page = __shfl_sync(0xffffffffu, p, (r >> 4) & 7);
-          const bool there = i < kPer && key0 + r < x.s.L && page >= 0 && 16 * c < a.D;
-          next[j] = there ? *reinterpret_cast<const uint4*>(from + page * ps +
-                                                            ((key0 + r) & ((1 << a.page_shift) - 1)) * ts + 16 * c)
-                          : make_uint4(0, 0, 0, 0);
-        }
-      };
-      fetch(w, w.t, 0);
+      // thread j takes 16-byte pieces j, j + 128, ... of a tile (lanes go along a row)
+      constexpr int kT = 32 * kConverters, kMine = kKeys * DP / 16 / kT, kRowPieces = DP / 16;
+      const int me = (warp - 12) * 32 + lane;
+      int st = 0, cs = 0, item = 0;
+      uint32_t ph = 0, cph = 0;
       for (bool more = true; more && ok; ++item) {
         const int least = least_of(w);
-        BigWalk after = w;
-        more = after.next(a);
 #pragma unroll 1
-        for (int u = 2 * w.t; u < 2 * w.end; ++u) {
-          const int t = u >> 1, kv = u & 1;
-          ok = wait(EMPTY(st), ph ^ 1u, abort_flag, a.err, 0x750u);
+        for (int u = 2 * w.t; u < 2 * w.end; ++u) {  // keys, values
+          const int t = u >> 1;
+          ok = wait(CFULL(cs), cph, abort_flag, 0x750) && wait(EMPTY(st), ph ^ 1u, abort_flag, 0x751);
           if (!ok) break;
-          const uint32_t tile = ring + static_cast<uint32_t>(st) * kTile;
-          const bool partly = kv == 1 && t * kKeys + kKeys - 1 > least;
+          const uint32_t from = codes + static_cast<uint32_t>(cs * code_bytes(DP)), tile = ring + static_cast<uint32_t>(st) * kTile;
+          const bool partly = (u & 1) != 0 && t * kKeys + kKeys - 1 > least;
+          const int there = w.s.L - t * kKeys;
           uint32_t odd = 0;
 #pragma unroll
           for (int j = 0; j < kMine; ++j) {
             const int i = me + j * kT, r = i / kRowPieces, c = i % kRowPieces;
-            if (i >= kPer) break;
-            const uint32_t q[4] = {next[j].x, next[j].y, next[j].z, next[j].w};
+            const uint4 v = dense::lds_u4(from + 16u * static_cast<uint32_t>(i));
+            const uint32_t q[4] = {v.x, v.y, v.z, v.w};
             uint32_t h[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -533,7 +560,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
             }
             if (partly) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) h[e] = tame(h[e], true, odd);
+              for (int e = 0; e < 8; ++e) h[e] = r < there ? tame(h[e], true, odd) : 0u;
             }
             // (lanes 4 to 7 of a row's eight begin with their second piece: other banks)
             const uint4 u0 = make_uint4(h[0], h[1], h[2], h[3]), u1 = make_uint4(h[4], h[5], h[6], h[7]);
@@ -544,15 +571,20 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
           if (odd) dirty[item % kDirty] = item;
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          if (lane == 0) mbar_arrive_cta(FULL(st));
+          if (lane == 0) {
+            mbar_arrive_cta(FULL(st));
+            mbar_arrive_cta(CEMPTY(cs));
+          }
           if (++st == slots) {
             st = 0;
             ph ^= 1u;
           }
-          if (u + 1 < 2 * w.end) fetch(w, (u + 1) >> 1, kv ^ 1);
-          else if (more) fetch(after, after.t, 0);
+          if (++cs == kCodeSlots) {
+            cs = 0;
+            cph ^= 1u;
+          }
         }
-        w = after;
+        more = ok && w.next(a);
       }
     }
     __syncwarp();
@@ -570,36 +602,41 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
     bool ok = true;
     int item = 0;
     // this thread's row of an item
-    struct Row {
-      bool live;
-      int limit;  // the last key that it sees
-      int64_t token;
-      int head;
+    auto live_of = [&](const BigWalk& x) { return half * kHalf + row < rows_of(x); };
+    auto token_of = [&](const BigWalk& x) { return divided(x.r * kRows + (live_of(x) ? half * kHalf + row : 0), a.G); };
+    auto head_of = [&](const BigWalk& x, int token) {
+      return x.h * a.G + x.r * kRows + (live_of(x) ? half * kHalf + row : 0) - token * a.G;
     };
-    auto row_of = [&](const BigWalk& x) {
-      Row y;
-      y.live = half * kHalf + row < rows_of(x);
-      const int R = x.r * kRows + (y.live ? half * kHalf + row : 0);
-      const int tok = divided(R, a.G);
-      y.limit = x.s.past + tok;
-      y.token = x.s.row0 + tok;
-      y.head = x.h * a.G + R - tok * a.G;
-      return y;
+    // The warp's queries into shared memory, a row over DP / 8 lanes.  16-bit: started
+    // here, there after queries_done.  8-bit: as f16, each row's largest brought to
+    // 2^14; returns what this thread's row's scores are multiplied with.
+    constexpr int kAcross = DP / 8, kTogether = 32 / kAcross;
+    auto queries = [&](const BigWalk& x) {
+      const int tok = token_of(x), hd = head_of(x, tok);
+      const uint64_t mine = live_of(x) ? reinterpret_cast<uint64_t>(a.q + (x.s.row0 + tok) * a.q_stride + static_cast<int64_t>(hd) * a.D) : 0;
+      const int c = lane % kAcross, base_row = 32 * (warp & 3);
+#pragma unroll 4
+      for (int i = 0; i < kAcross; ++i) {
+        const int r = i * kTogether + lane / kAcross;
+        const uint64_t from = __shfl_sync(0xffffffffu, mine, r);
+        const bool there = from != 0 && 8 * c < a.D;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(q_at + piece_at(base_row + r, c)),
+                     "l"(there ? from + 16 * c : reinterpret_cast<uint64_t>(a.q)), "r"(there ? 16u : 0u)
+                     : "memory");
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    // Its queries into shared memory; what their scores are multiplied with.  8-bit:
-    // as f16, the largest brought to 2^14.
-    auto put_queries = [&](const Row& y) {
-      const uint16_t* q = a.q + y.token * a.q_stride + static_cast<int64_t>(y.head) * a.D;
-      uint4 v[DP / 8];
-#pragma unroll
-      for (int c = 0; c < DP / 8; ++c)
-        v[c] = y.live && 8 * c < a.D ? *reinterpret_cast<const uint4*>(q + 8 * c) : make_uint4(0, 0, 0, 0);
+    // They are there; returns what this thread's row's scores are multiplied with.
+    auto queries_done = [&] {
       float factor = a.scale_log2;
-      if (E4M3) {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      if constexpr (E4M3) {
+        __syncwarp();
         float amax = 0.f;
-#pragma unroll
+#pragma unroll 2
         for (int c = 0; c < DP / 8; ++c) {
-          const uint32_t u[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+          const uint4 v = dense::lds_u4(q_at + piece_at(row, c));
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(f32_of(u[e] & 0xFFFFu, a.f16)), fabsf(f32_of(u[e] >> 16, a.f16))));
         }
@@ -607,43 +644,38 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
         const bool scaled = amax > 0.f && amax < INFINITY;
         const float up = scaled ? __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23) : 1.f;
         if (scaled) factor *= __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
-#pragma unroll
+#pragma unroll 2
         for (int c = 0; c < DP / 8; ++c) {
-          uint32_t* u = &v[c].x;
+          uint4 v = dense::lds_u4(q_at + piece_at(row, c));
+          uint32_t* u = &v.x;
 #pragma unroll
           for (int k = 0; k < 4; ++k) u[k] = pack_half(f32_of(u[k] & 0xFFFFu, a.f16) * up, f32_of(u[k] >> 16, a.f16) * up);
+          dense::sts_u4(q_at + piece_at(row, c), v);
         }
       }
-#pragma unroll
-      for (int c = 0; c < DP / 8; ++c) dense::sts_u4(q_at + piece_at(row, c), v[c]);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive_cta(QFULL(half));
       return factor;
     };
-    Row y{};
     float factor = a.scale_log2;
-    if (some) {
-      y = row_of(w);
-      if (w.t < end_of(w, half)) factor = put_queries(y);
-    }
-    for (bool more = some; more && ok; ++item) {
-      const int end = end_of(w, half), t0 = w.t;
-      // the first key that some row of this half does not see
+    // (the first turn has no item yet: it only asks for the first one's queries)
+    bool begun = false, more = some;
+    while (more || begun) {
+      const int end = begun ? end_of(w, half) : 0, t0 = begun ? w.t : 0;
+      // the first key that some row of this half does not see, and the last key that
+      // this row sees
       const int least = w.s.past + divided(w.r * kRows + half * kHalf, a.G);
+      const int limit = w.s.past + token_of(w);
       float top = -INFINITY;  // of the row's scores, what its weights are relative to
       float unit = 1.f;
       uint64_t sum = 0;
-      BigWalk next = w;
-      more = next.next(a);
-      Row y_next = y;
-      float factor_next = factor;
-      for (int t = t0; t < (E4M3 ? w.end : end) && ok; ++t) {
+      for (int t = t0; t < (E4M3 && begun ? w.end : end); ++t) {
         const float* sc = nullptr;
         uint32_t slot = 0;
         if (E4M3) {
           slot = scn % kScaleSlots;
-          ok = wait(SCFULL(slot), scn / kScaleSlots & 1u, abort_flag, a.err, 0x760u);
+          ok = wait(SCFULL(slot), scn / kScaleSlots & 1u, abort_flag, 0x760);
           ++scn;
           if (!ok) break;
           sc = scales + slot * kScaleSlot;
@@ -654,7 +686,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
           }
           unit = sc[2 * kKeys];
         }
-        ok = wait(SFULL(half), sph, abort_flag, a.err, 0x761u);
+        ok = wait(SFULL(half), sph, abort_flag, 0x761);
         if (!ok) break;
         sph ^= 1u;
         tc_fence_after();
@@ -668,14 +700,18 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
           for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const float4 k = *reinterpret_cast<const float4*>(sc + 32 * c + 4 * j);
-              const float kk[4] = {k.x, k.y, k.z, k.w};
+              const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(sc + 32 * c + 4 * j);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) s[c][4 * j + e] = __float_as_uint(__uint_as_float(s[c][4 * j + e]) * kk[e]);
+              for (int e = 0; e < 2; ++e) {
+                uint32_t* x = &s[c][4 * j + 2 * e];
+                const uint64_t z = mul2((static_cast<uint64_t>(x[1]) << 32) | x[0], e == 0 ? k.x : k.y);
+                x[0] = static_cast<uint32_t>(z);
+                x[1] = static_cast<uint32_t>(z >> 32);
+              }
             }
         }
         if (t * kKeys + kKeys - 1 > least) {
-          const int seen = y.limit - t * kKeys;
+          const int seen = limit - t * kKeys;
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -687,7 +723,9 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
         for (int c = 0; c < 4; ++c) {
           m4[c] = __uint_as_float(s[c][0]);
 #pragma unroll
-          for (int j = 1; j < 32; ++j) m4[c] = fmaxf(m4[c], __uint_as_float(s[c][j]));
+          for (int j = 1; j < 31; j += 2)
+            m4[c] = fmaxf(m4[c], fmaxf(__uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1])));
+          m4[c] = fmaxf(m4[c], __uint_as_float(s[c][31]));
         }
         const float now = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * factor;
         const float shrink = E4M3 ? sc[2 * kKeys + 1] : 1.f;
@@ -699,173 +737,208 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
           top = up;
           sum = mul2(sum, pack2(keep, keep));
           const float f = keep * shrink;
+#pragma unroll 1
+          for (int c = 0; c < DP / 16; ++c) {
+            uint32_t o[16];
+            dense::tmem_ld16_wait(O + 16u * c, o);
 #pragma unroll
-          for (int c = 0; c < DP / 32; ++c) {
-            uint32_t o[32];
-            dense::tmem_ld32(O + 32u * c, o);
-            dense::tmem_ld32_wait(o);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-            tmem_st32(O + 32u * c, o);
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_st16(O + 16u * c, o);
           }
         }
         const float r = reference(top);
         const uint64_t f2 = pack2(factor, factor), r2 = pack2(-r, -r);
         uint64_t sums[2] = {0, 0};
+        auto given = [&](int part) {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cta(PFULL(half, part));
+        };
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t p[32];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t p[16];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const uint32_t* x = &s[2 * c + (j >> 4)][2 * (j & 15)];
-            const uint64_t z = fma2((static_cast<uint64_t>(x[1]) << 32) | x[0], f2, r2);
+          for (int j = 0; j < 16; ++j) {
+            const uint64_t z = fma2((static_cast<uint64_t>(s[c][2 * j + 1]) << 32) | s[c][2 * j], f2, r2);
             uint64_t e = pack2(exp2_fast(lo2(z)), exp2_fast(hi2(z)));
             sums[j & 1] = add2(sums[j & 1], e);
             if (E4M3) {
-              const float2 v = *reinterpret_cast<const float2*>(sc + kKeys + 64 * c + 2 * j);
-              // (a weight of zero stays zero whatever its value's scale is)
-              e = pack2(lo2(e) == 0.f ? 0.f : lo2(e) * v.x, hi2(e) == 0.f ? 0.f : hi2(e) * v.y);
+              e = mul2(e, *reinterpret_cast<const uint64_t*>(sc + kKeys + 32 * c + 2 * j));
             }
-            p[j] = f16 ? pack_half(lo2(e), hi2(e)) : pack_bf16x2(lo2(e), hi2(e));
+            p[j] = F16 ? pack_half(lo2(e), hi2(e)) : pack_bf16x2(lo2(e), hi2(e));
           }
-          tmem_st32(S + 32u * c, p);
+          tmem_st16(S + 16u * c, p);
+          if (c == 1) given(0);
         }
+        given(1);
+        if (E4M3 && lane == 0) mbar_arrive_cta(SCEMPTY(slot));
         sum = add2(sum, add2(sums[0], sums[1]));
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_cta(PFULL(half));
-          if (E4M3) mbar_arrive_cta(SCEMPTY(slot));
-        }
-        // the item's last scores are read: the next item's queries may come
-        if (t + 1 == end && more) {
-          y_next = row_of(next);
-          if (next.t < end_of(next, half)) factor_next = put_queries(y_next);
-        }
       }
       if (!ok) break;
+      // ---- the item's end: its last scores are read, so the next one's queries come
       const bool has = t0 < end;
-      if (!has && more) {
-        y_next = row_of(next);
-        if (next.t < end_of(next, half)) factor_next = put_queries(y_next);
-      }
-      // ---- the item's end
-      float total = lo2(sum) + hi2(sum);
+      BigWalk next = w;
+      if (begun) more = next.next(a);
+      const bool ask = more && next.t < end_of(next, half);
+      if (ask) queries(next);
       if (has) {
-        ok = wait(OFULL(half), oph, abort_flag, a.err, 0x762u);
-        if (!ok) break;
+        ok = wait(OFULL(half), oph, abort_flag, 0x762);
         oph ^= 1u;
         tc_fence_after();
       }
-      const bool spoiled = dirty[item % kDirty] == item;
-      const bool whole = w.end - w.t == w.len;
-      const int first = t0 > 0 ? shares.first : static_cast<int>(blockIdx.x);
-      constexpr size_t kPiece = attn_piece_bytes(kRows, DP) / 4;
-      auto piece = [&](int i) { return a.partial + (2 * (first + i) + (i == 0 ? 1 : 0)) * kPiece + half * kHalf + row; };
-      uint16_t* to = a.out + y.token * a.out_stride + static_cast<int64_t>(y.head) * a.D;
-      auto write = [&](int c, const float (&v)[32], float inv) {  // 32 columns of the row
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (32 * c + 8 * j < a.D) {
-            uint32_t u[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              u[e] = a.f16 ? pack_half(v[8 * j + 2 * e] * inv, v[8 * j + 2 * e + 1] * inv)
-                           : pack_bf16x2(v[8 * j + 2 * e] * inv, v[8 * j + 2 * e + 1] * inv);
-            *reinterpret_cast<uint4*>(to + 32 * c + 8 * j) = make_uint4(u[0], u[1], u[2], u[3]);
-          }
-        }
-      };
-      float* mine = piece(static_cast<int>(blockIdx.x) - first);
-      const float inv = 1.f / total;
+      float factor_next = factor;
+      if (ask) factor_next = queries_done();
+      if (!ok) break;
+      if (begun) {
+        const float total = lo2(sum) + hi2(sum);
+        const bool spoiled = dirty[item % kDirty] == item, live = live_of(w);
+        const bool whole = w.end - w.t == w.len;
+        const int tok = token_of(w), hd = head_of(w, tok);
+        const int64_t out_row = w.s.row0 + tok;
+        const uint64_t to = live ? reinterpret_cast<uint64_t>(a.out + out_row * a.out_stride + static_cast<int64_t>(hd) * a.D) : 0;
+        // An item that lies in several runs leaves its sums in the workspace, and the
+        // last of its CTAs to finish joins them in the order of the runs.
+        const int first = t0 > 0 ? shares.first : static_cast<int>(blockIdx.x);
+        const int pieces = whole ? 1 : shares.pieces(first, w.len - w.end);
+        constexpr size_t kPiece = attn_piece_bytes(kRows, DP) / 4;
+        auto piece = [&](int i) { return a.partial + (2 * (first + i) + (i == 0 ? 1 : 0)) * kPiece + half * kHalf + row; };
+        float* mine = piece(static_cast<int>(blockIdx.x) - first);
+        float all_top = top, all_sum = total;
+        const int64_t at = live ? 0 : -static_cast<int64_t>(half * kHalf + row);  // (dead rows read the first one's)
 #pragma unroll 1
-      for (int c = 0; c < DP / 32; ++c) {
-        float v[32];
-        if (has) {
-          uint32_t o[32];
-          dense::tmem_ld32(O + 32u * c, o);
-          dense::tmem_ld32_wait(o);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * (E4M3 ? unit : 1.f);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0.f;
-        }
-        if (spoiled && y.live && has) {
-          // values that are not finite, of the keys that this row sees among those looked at
-          const int from = max(t0, (least_of(w) + 1) / kKeys) * kKeys;
-          for (int key = from; key <= min(y.limit, end * kKeys - 1); ++key) {
-            int64_t page, place;
-            if (!locate(a, w.s, w.b, key, page, place)) continue;
-            const int64_t in = page * a.kv.v_page + place * a.kv.v_token + w.h * a.kv.v_head + 32 * c;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              if (32 * c + j >= a.D) break;
-              const float x = E4M3 ? ((a.kv.v[in + j] & 0x7F) == 0x7F ? NAN : 0.f)
-                                   : f32_of(reinterpret_cast<const uint16_t*>(a.kv.v)[in + j], a.f16);
-              if (!(fabsf(x) < INFINITY)) v[j] += x;
-            }
-          }
-        }
-        if (whole) {
-          if (y.live) write(c, v, inv);
-        } else if (y.live) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) __stcg(mine + (32 * c + j) * kRows, v[j]);
-        }
-      }
-      tc_fence_before();  // (the next item's products write O after this half's weights)
-      if (whole) {
-        if (y.live && a.lse != nullptr) a.lse[y.token * a.Hq + y.head] = (top + log2_fast(total)) * 0.69314718055994531f;
-      } else {
-        // the item lies in several runs: the last one to finish joins them
-        if (y.live) {
-          __stcg(mine + DP * kRows, top);
-          __stcg(mine + (DP + 1) * kRows, total);
-        }
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cta(join0);
-        ok = wait(join0, jph, abort_flag, a.err, 0x770u);
-        if (!ok) break;
-        const int pieces = shares.pieces(first, w.len - w.end);
-        if (tid == 0) {
-          const bool last = atomicAdd(a.tickets + first, 1u) == static_cast<uint32_t>(pieces - 1);
-          if (last) a.tickets[first] = 0;
-          __threadfence();
-          *last_flag = last;
-          mbar_arrive_cta(join1);
-        }
-        ok = wait(join1, jph, abort_flag, a.err, 0x771u);
-        if (!ok) break;
-        jph ^= 1u;
-        if (*last_flag != 0 && y.live) {
-          __threadfence();
-          float m = -INFINITY;
-          for (int i = 0; i < pieces; ++i) m = fmaxf(m, __ldcg(piece(i) + DP * kRows));
-          const float r = reference(m);
-          float l = 0.f;
-          for (int i = 0; i < pieces; ++i) l = fmaf(__ldcg(piece(i) + (DP + 1) * kRows), exp2_fast(__ldcg(piece(i) + DP * kRows) - r), l);
+        for (int phase = whole ? 1 : 0; phase < 2; ++phase) {  // into the workspace; into out
+          const float inv = 1.f / all_sum;
 #pragma unroll 1
           for (int c = 0; c < DP / 32; ++c) {
             float v[32];
+            if (phase == 1 && !whole) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0.f;
-#pragma unroll 1
-            for (int i = 0; i < pieces; ++i) {
-              const float f = exp2_fast(__ldcg(piece(i) + DP * kRows) - r);
+              for (int j = 0; j < 32; ++j) v[j] = 0.f;
+#pragma unroll 2
+              for (int i = 0; i < pieces; ++i) {
+                const float* from = piece(i) + at;
+                const float f = exp2_fast(__ldcg(from + DP * kRows) - reference(all_top));
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = fmaf(__ldcg(piece(i) + (32 * c + j) * kRows), f, v[j]);
+                for (int j = 0; j < 32; ++j) v[j] = fmaf(__ldcg(from + (32 * c + j) * kRows), f, v[j]);
+              }
+            } else if (has) {
+              uint32_t o[32];
+              dense::tmem_ld32(O + 32u * c, o);
+              dense::tmem_ld32_wait(o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * (E4M3 ? unit : 1.f);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = 0.f;
             }
-            write(c, v, 1.f / l);
+            if (phase == 0) {
+              if (live)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) __stcg(mine + (32 * c + j) * kRows, v[j]);
+              continue;
+            }
+            // The rows of four lanes are turned so that the four store 64 adjacent bytes of
+            // one row at a time (a row a lane: 32 lines a store, 2 us an item).
+            uint4 u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t* x = &u[j].x;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float y = v[8 * j + 2 * e] * inv, z = v[8 * j + 2 * e + 1] * inv;
+                x[e] = (E4M3 ? a.f16 != 0 : F16) ? pack_half(y, z) : pack_bf16x2(y, z);
+              }
+            }
+            // lane l of four holds pieces 0 to 3 of row l; afterwards piece l of rows 0 to 3
+            auto turn = [&](uint4& p, uint4& q, int bit) {  // p of the lanes without the bit for q of those with it
+              const bool up = (lane & bit) != 0;
+              uint32_t *x = &p.x, *z = &q.x;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x[e] : z[e], bit);
+                if (up) x[e] = got;
+                else z[e] = got;
+              }
+            };
+            turn(u[0], u[1], 1);
+            turn(u[2], u[3], 1);
+            turn(u[0], u[2], 2);
+            turn(u[1], u[3], 2);
+            const int column = 32 * c + 8 * (lane & 3);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint64_t row_at = __shfl_sync(0xffffffffu, to, (lane & ~3) + j);
+              if (row_at != 0 && column < a.D) *reinterpret_cast<uint4*>(row_at + 2 * column) = u[j];
+            }
           }
-          if (a.lse != nullptr) a.lse[y.token * a.Hq + y.head] = (m + log2_fast(l)) * 0.69314718055994531f;
+          if (spoiled && has && (phase == 0 || whole)) {
+            // values that are not finite, of the keys that this row sees among those looked
+            // at, added to what was written
+            __syncwarp();
+            const int from = max(t0, divided(least_of(w) + 1, kKeys)) * kKeys;
+            const int upto = live ? min(limit, end * kKeys - 1) : -1;
+#pragma unroll 1
+            for (int key = from; key <= upto; ++key) {
+              int64_t page, place;
+              if (!locate(a, w.s, w.b, key, page, place)) continue;
+              const float vscale = E4M3 ? a.kv.v_scale[((page * a.Hkv + w.h) << a.page_shift) + place] : 1.f;
+              const int64_t in = page * a.kv.v_page + place * a.kv.v_token + w.h * a.kv.v_head;
+#pragma unroll 1
+              for (int d = 0; d < a.D; ++d) {
+                const float x = E4M3 ? __half2float(__ushort_as_half(static_cast<uint16_t>(e4m3x2_half2(a.kv.v[in + d])))) * vscale
+                                     : f32_of(reinterpret_cast<const uint16_t*>(a.kv.v)[in + d], F16);
+                if (fabsf(x) < INFINITY) continue;
+                if (phase == 0) {
+                  __stcg(mine + d * kRows, __ldcg(mine + d * kRows) + x);
+                } else {
+                  uint16_t* o = reinterpret_cast<uint16_t*>(to) + d;
+                  const float y = f32_of(*o, a.f16) + x;
+                  *o = static_cast<uint16_t>(a.f16 ? pack_half(y, 0.f) : pack_bf16x2(y, 0.f));
+                }
+              }
+            }
+          }
+          if (phase == 1) {
+            if (live && a.lse != nullptr) a.lse[out_row * a.Hq + hd] = (all_top + log2_fast(all_sum)) * 0.69314718055994531f;
+            break;
+          }
+          if (live) {
+            __stcg(mine + DP * kRows, top);
+            __stcg(mine + (DP + 1) * kRows, total);
+          }
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cta(join0);
+          ok = wait(join0, jph, abort_flag, 0x770);
+          if (!ok) break;
+          if (tid == 0) {
+            const bool last = atomicAdd(a.tickets + first, 1u) == static_cast<uint32_t>(pieces - 1);
+            if (last) a.tickets[first] = 0;
+            __threadfence();
+            *last_flag = last;
+            mbar_arrive_cta(join1);
+          }
+          ok = wait(join1, jph, abort_flag, 0x771);
+          jph ^= 1u;
+          if (!ok || *last_flag == 0) break;
+          __threadfence();
+          all_top = -INFINITY;
+#pragma unroll 4
+          for (int i = 0; i < pieces; ++i) all_top = fmaxf(all_top, __ldcg(piece(i) + at + DP * kRows));
+          all_sum = 0.f;
+#pragma unroll 4
+          for (int i = 0; i < pieces; ++i)
+            all_sum = fmaf(__ldcg(piece(i) + at + (DP + 1) * kRows), exp2_fast(__ldcg(piece(i) + at + DP * kRows) - reference(all_top)), all_sum);
         }
+        if (!ok) break;
+        tc_fence_before();  // (the next item's products write O after this half's weights)
+        ++item;
       }
+      if (!more) break;
       w = next;
-      y = y_next;
       factor = factor_next;
+      begun = true;
     }
     __syncwarp();
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(E4M3 ? kLaunchRegs8 : kLaunchRegs16));
@@ -881,15 +954,18 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
 #undef SCFULL
 #undef SCEMPTY
 #undef READY
+#undef CFULL
+#undef CEMPTY
+  if (tid == 0 && *abort_flag != 0) record_error(a.err, kErrTimeout, static_cast<uint32_t>(*abort_flag));
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
 }
 
-template <bool E4M3, int DP>
+template <bool E4M3, bool F16, int DP>
 cudaError_t launch(const AttnArgs& a, int sms, cudaStream_t s) {
-  auto kernel = attention_kernel<E4M3, DP>;
+  auto kernel = attention_kernel<E4M3, F16, DP>;
   static int configured[64] = {};
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
@@ -906,25 +982,30 @@ cudaError_t launch(const AttnArgs& a, int sms, cudaStream_t s) {
       return cudaErrorInvalidConfiguration;
     if (dev >= 0 && dev < 64) configured[dev] = 1;
   }
-  const int room = static_cast<int>((kSmem - kMiscBytes<E4M3>) / tile_bytes(DP)) - 2;
+  const size_t fixed = kMiscBytes<E4M3> + 2 * tile_bytes(DP) + (E4M3 ? kCodeSlots * code_bytes(DP) : 0);
+  const int room = static_cast<int>((kSmem - fixed) / tile_bytes(DP));
   const int slots = room < kMaxSlots ? room : kMaxSlots;
-  const size_t smem = std::max(kTensorMemorySmem, static_cast<size_t>(kMiscBytes<E4M3> + (2 + slots) * tile_bytes(DP)));
+  const size_t smem = std::max(kTensorMemorySmem, fixed + static_cast<size_t>(slots) * tile_bytes(DP));
   Maps maps = {};
   int box_rows = kKeys;
-  if (!E4M3) {
+  {
     const bool paged = a.page_table != nullptr;
     const uint64_t page = paged ? 1ull << a.page_shift : static_cast<uint64_t>(a.T);
     box_rows = paged && page < kKeys ? static_cast<int>(page) : kKeys;
-    const CUtensorMapDataType dt = a.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapDataType dt = E4M3    ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : a.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                           : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapSwizzle swizzle = E4M3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+    constexpr int64_t size = E4M3 ? 1 : 2;
     const uint64_t dims[4] = {static_cast<uint64_t>(a.D), page, static_cast<uint64_t>(a.Hkv), static_cast<uint64_t>(a.num_pages)};
-    const uint32_t box[4] = {64, static_cast<uint32_t>(box_rows), 1, 1};
+    const uint32_t box[4] = {E4M3 ? DP : 64, static_cast<uint32_t>(box_rows), 1, 1};
     const int64_t far = 16;  // (of one page: no stride)
-    const uint64_t ks[3] = {static_cast<uint64_t>(2 * a.kv.k_token), static_cast<uint64_t>(2 * a.kv.k_head),
-                            static_cast<uint64_t>(paged ? 2 * a.kv.k_page : far)};
-    const uint64_t vs[3] = {static_cast<uint64_t>(2 * a.kv.v_token), static_cast<uint64_t>(2 * a.kv.v_head),
-                            static_cast<uint64_t>(paged ? 2 * a.kv.v_page : far)};
-    if (!encode_map(&maps.k, dt, 4, a.kv.k, dims, ks, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_map(&maps.v, dt, 4, a.kv.v, dims, vs, box, CU_TENSOR_MAP_SWIZZLE_128B))
+    const uint64_t ks[3] = {static_cast<uint64_t>(size * a.kv.k_token), static_cast<uint64_t>(size * a.kv.k_head),
+                            static_cast<uint64_t>(paged ? size * a.kv.k_page : far)};
+    const uint64_t vs[3] = {static_cast<uint64_t>(size * a.kv.v_token), static_cast<uint64_t>(size * a.kv.v_head),
+                            static_cast<uint64_t>(paged ? size * a.kv.v_page : far)};
+    if (!encode_map(&maps.k, dt, 4, a.kv.k, dims, ks, box, swizzle) ||
+        !encode_map(&maps.v, dt, 4, a.kv.v, dims, vs, box, swizzle))
       return cudaErrorInvalidValue;
   }
   return launch_pdl(kernel, dim3(sms < kAttnMaxCtas ? sms : kAttnMaxCtas), dim3(kThreads<E4M3>), smem, s, maps, a, slots,
@@ -934,8 +1015,9 @@ cudaError_t launch(const AttnArgs& a, int sms, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_attention(const AttnArgs& a, int sms, cudaStream_t s) {
-  if (a.e4m3) return a.D <= 64 ? launch<true, 64>(a, sms, s) : launch<true, 128>(a, sms, s);
-  return a.D <= 64 ? launch<false, 64>(a, sms, s) : launch<false, 128>(a, sms, s);
+  if (a.e4m3) return a.D <= 64 ? launch<true, true, 64>(a, sms, s) : launch<true, true, 128>(a, sms, s);
+  if (a.f16) return a.D <= 64 ? launch<false, true, 64>(a, sms, s) : launch<false, true, 128>(a, sms, s);
+  return a.D <= 64 ? launch<false, false, 64>(a, sms, s) : launch<false, false, 128>(a, sms, s);
 }
 
 }  // namespace moe

@@ -59,33 +59,37 @@ __device__ __forceinline__ int key_tiles(const Seq& s, int G, int r) {
   return (s.past + min(divided(M * (r + 1) - 1, G), s.n - 1) + KT) / KT;
 }
 // Key tiles of the row tiles before r.  But for the last tile, whose rows may end
-// early, tile i reads floor((M i + M - 1 + (past + KT) G) / (KT G)), which is u i / v
-// + const in whole numbers and repeats every v tiles up to a multiple of u.
+// early, and with past = KT a + b, tile i reads a + 1 + floor((M i + M - 1 + b G) / (KT
+// G)) tiles, the last term being floor((u i + e) / v) in small whole numbers.
 template <int M, int KT>
 __device__ __forceinline__ int64_t tiles_before(const Seq& s, int G, int r) {
   constexpr int kUnit = M < KT ? M : KT;  // divides both
-  constexpr int u = M / kUnit;
-  const int64_t v = static_cast<int64_t>(KT / kUnit) * G;
-  const int64_t e = (M - 1 + (static_cast<int64_t>(s.past) + KT) * G) / kUnit;
-  int64_t sum = 0;
+  int u = M / kUnit, v = KT / kUnit * G, e = (M - 1 + s.past % KT * G) / kUnit;
+  int64_t sum = static_cast<int64_t>(s.past / KT + 1) * r;
+  static_assert(M / kUnit <= 2, "one or two");
+  if (u == 2 && v % 2 == 0) {
+    u = 1;
+    v /= 2;
+    e /= 2;
+  }
   if (u == 1) {
     // sum of floor(j / v) over j < x
-    auto below = [v](int64_t x) {
-      const int64_t q = x / v;
-      return v * (q * (q - 1) / 2) + q * (x - q * v);
+    auto below = [v](int x) {
+      const int q = divided(x, v);
+      return static_cast<int64_t>(v) * (static_cast<int64_t>(q) * (q - 1) / 2) + static_cast<int64_t>(q) * (x - q * v);
     };
-    sum = below(r + e) - below(e);
+    sum += below(r + e) - below(e);
   } else {
-    const int64_t whole = r / v, rest = r - whole * v;
+    // repeats every v tiles, u q more after q times
+    const int whole = divided(r, v), rest = r - whole * v, upto = whole > 0 ? v : rest;
     int64_t period = 0;
-    const int64_t upto = whole > 0 ? v : rest;
-    for (int64_t i = 0; i < upto; ++i) {
-      const int64_t f = (u * i + e) / v;
+    for (int i = 0; i < upto; ++i) {
+      const int f = divided(u * i + e, v);
       period += f;
       if (i < rest) sum += f;
     }
-    // tile i + q v reads u q more than tile i
-    sum += whole * period + u * (v * (whole * (whole - 1) / 2) + whole * rest);
+    sum += whole * period + static_cast<int64_t>(u) * (static_cast<int64_t>(v) * (static_cast<int64_t>(whole) * (whole - 1) / 2) +
+                                                      static_cast<int64_t>(whole) * rest);
   }
   return sum;
 }
@@ -147,7 +151,7 @@ struct Shares {
 };
 
 // The run of this CTA; false where it has none.  Every thread calls it; `scratch`
-// holds THREADS / 32 + 4 words of 8 bytes.
+// (read until the next barrier) holds THREADS / 32 + 4 words of 8 bytes.
 template <int M, int KT, int THREADS>
 __device__ __forceinline__ bool start(const AttnArgs& a, int64_t* scratch, Walk<M, KT>& w, Shares& sh) {
   constexpr int kWarps = THREADS / 32;
@@ -172,56 +176,70 @@ __device__ __forceinline__ bool start(const AttnArgs& a, int64_t* scratch, Walk<
     }
     return before;
   };
-  auto tiles_of = [&](int b, bool report) {
-    return b < a.B ? head_tiles<M, KT>(sequence(a, b, report), a.G) * a.Hkv : static_cast<int64_t>(0);
-  };
-  int64_t total = 0, sum, mine = 0, before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += THREADS) {
-    mine = tiles_of(b0 + tid, blockIdx.x == 0);
-    before = scan(mine, sum);
-    total += sum;
-  }
-  sh.n = static_cast<int>(total < static_cast<int64_t>(gridDim.x) ? total : static_cast<int64_t>(gridDim.x));
+  // (twice over the sequences, in one piece of code: their sum, then the one that
+  // holds the run's first tile; of few sequences the second time needs no reading)
   const int cta = blockIdx.x;
-  if (cta >= sh.n) return false;
-  sh.run = total / sh.n;
-  sh.more = static_cast<int>(total - sh.run * sh.n);
-  const int64_t lo = sh.run * cta + min(cta, sh.more);
-  int64_t base = 0;
-  for (int b0 = 0; b0 < a.B; b0 += THREADS) {
-    if (a.B > THREADS) {
-      mine = tiles_of(b0 + tid, false);
-      before = scan(mine, sum);
+  int64_t total = 0, mine = 0, before = 0, base = 0, lo = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.B; b0 += THREADS) {
+      int64_t sum = total;
+      if (pass == 0 || a.B > THREADS) {
+        const int b = b0 + tid;
+        mine = b < a.B ? head_tiles<M, KT>(sequence(a, b, pass == 0 && cta == 0), a.G) * a.Hkv : 0;
+        before = scan(mine, sum);
+      }
+      if (pass == 0) {
+        total += sum;
+      } else {
+        if (base + before <= lo && lo < base + before + mine) {
+          scratch[kWarps] = b0 + tid;
+          scratch[kWarps + 1] = lo - base - before;
+        }
+        base += sum;
+      }
     }
-    if (base + before <= lo && lo < base + before + mine) {
-      scratch[kWarps] = b0 + tid;
-      scratch[kWarps + 1] = lo - base - before;
+    if (pass == 0) {
+      sh.n = static_cast<int>(total < static_cast<int64_t>(gridDim.x) ? total : static_cast<int64_t>(gridDim.x));
+      if (cta >= sh.n) return false;
+      sh.run = total >> 31 == 0 ? static_cast<int64_t>(divided(static_cast<int>(total), sh.n)) : total / sh.n;
+      sh.more = static_cast<int>(total - sh.run * sh.n);
+      lo = sh.run * cta + min(cta, sh.more);
     }
-    base += sum;
   }
   __syncthreads();
   w.b = static_cast<int>(scratch[kWarps]);
   int64_t rest = scratch[kWarps + 1];
   w.s = sequence(a, w.b, false);
   w.R = row_tiles<M>(w.s, a.G);
-  const int64_t per_head = head_tiles<M, KT>(w.s, a.G);
-  w.h = static_cast<int>(rest / per_head);
-  rest -= w.h * per_head;
-  // the last row tile that starts at or before `rest`: 32 candidates at a time
+  w.h = 0;
+  // the last row tile that starts at or before `rest`: 32 candidates at a time, the
+  // first time with the whole head's tiles as one more
   int lo_r = 0, hi_r = w.R;  // in [lo_r, hi_r)
-  while (hi_r - lo_r > 1) {
+  int64_t skipped = 0;       // tiles before row tile lo_r
+  bool first = true;
+#pragma unroll 1
+  while (first || hi_r - lo_r > 1) {
     const int step = (hi_r - lo_r + 31) / 32;
-    const int r = lo_r + lane * step;
-    const bool reached = r < hi_r && tiles_before<M, KT>(w.s, a.G, r) <= rest;
-    const int top = 31 - __clz(__ballot_sync(0xffffffffu, reached));
+    const int r = first ? w.R - 1 : lo_r + lane * step;
+    const int64_t there = tiles_before<M, KT>(w.s, a.G, min(r, w.R - 1));
+    if (first) {
+      const int64_t per_head = there + key_tiles<M, KT>(w.s, a.G, w.R - 1);
+      for (; rest >= per_head; ++w.h) rest -= per_head;
+      first = false;
+      continue;
+    }
+    const int top = 31 - __clz(__ballot_sync(0xffffffffu, r < hi_r && there <= rest));
+    skipped = __shfl_sync(0xffffffffu, there, top);
     lo_r += top * step;
     hi_r = min(hi_r, lo_r + step);
   }
   w.r = lo_r;
-  w.t = static_cast<int>(rest - tiles_before<M, KT>(w.s, a.G, lo_r));
+  w.t = static_cast<int>(rest - skipped);
   w.left = sh.run_of(cta);
   sh.first = cta;
-  for (int64_t rest_t = w.t; rest_t > 0;) rest_t -= sh.run_of(--sh.first);
+  for (int64_t back = w.t; back > 0;) back -= sh.run_of(--sh.first);
   w.enter(a);
   return true;
 }
