@@ -49,11 +49,22 @@ using BigWalk = Walk<kRows, kKeys>;
 
 // Barriers and small arrays, then (1024-byte aligned) Q's halves, the ring of key and
 // value tiles and the ring of their codes.
-constexpr int kBarBytes = 512;
+constexpr int kBarBytes = 640;
 constexpr int kScaleSlot = 2 * kKeys + 4;  // of 128 keys, of their values, unit, shrink
+constexpr int kScratchBytes = 160;
+constexpr int kItems = 4;
+// An item as its warps see it: end is of its key tiles in this run, end0 that of the
+// first half's; least the last key that all rows see.
+struct Item {
+  int b, h, r, t, end, len, row0, L, past, rows, least, end0;
+};
 template <bool E4M3>
 constexpr int kMiscBytes = E4M3 ? 3072 : 1024;
-static_assert(kBarBytes + kScaleSlots * kScaleSlot * 4 + 256 <= kMiscBytes<true>, "scales lie between the barriers and Q");
+template <bool E4M3>
+constexpr int kScratchAt = kBarBytes + (E4M3 ? kScaleSlots * kScaleSlot * 4 : 0);
+static_assert(kScratchAt<true> + kScratchBytes + kItems * sizeof(Item) <= kMiscBytes<true> &&
+                  kScratchAt<false> + kScratchBytes + kItems * sizeof(Item) <= kMiscBytes<false>,
+              "all before Q");
 __host__ __device__ constexpr int tile_bytes(int dp) { return kKeys * dp * 2; }
 __host__ __device__ constexpr int code_bytes(int dp) { return kKeys * dp; }
 
@@ -169,10 +180,10 @@ __device__ __forceinline__ uint32_t tame(uint32_t w, bool f16, uint32_t& odd) {
 }
 
 // Where key j of sequence b lies: page and place in it; false for a page outside.
-__device__ __forceinline__ bool locate(const AttnArgs& a, const Seq& s, int b, int j, int64_t& page, int64_t& place) {
+__device__ __forceinline__ bool locate(const AttnArgs& a, int row0, int b, int j, int64_t& page, int64_t& place) {
   if (a.page_table == nullptr) {
     page = 0;
-    place = static_cast<int64_t>(s.row0) + j;
+    place = static_cast<int64_t>(row0) + j;
     return true;
   }
   const int p = a.page_table[b * a.table_stride + (j >> a.page_shift)];
@@ -203,12 +214,15 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
 #define READY(s) (base + 320u + 8u * static_cast<uint32_t>(s))
 #define CFULL(s) (base + 400u + 8u * static_cast<uint32_t>(s))
 #define CEMPTY(s) (base + 432u + 8u * static_cast<uint32_t>(s))
+#define IFULL(s) (base + 512u + 8u * static_cast<uint32_t>(s))
+#define IEMPTY(s) (base + 544u + 8u * static_cast<uint32_t>(s))
   const uint32_t drain = base + 232u, join0 = base + 384u, join1 = base + 392u;
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(attn_smem + 240);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(attn_smem + 244);
   volatile int* last_flag = reinterpret_cast<volatile int*>(attn_smem + 248);
   volatile int* dirty = reinterpret_cast<volatile int*>(attn_smem + 256);  // [kDirty]: the item that has such values
-  int64_t* scratch = reinterpret_cast<int64_t*>(attn_smem + kBarBytes + (E4M3 ? kScaleSlots * kScaleSlot * 4 : 0));
+  int64_t* scratch = reinterpret_cast<int64_t*>(attn_smem + kScratchAt<E4M3>);
+  Item* items = reinterpret_cast<Item*>(attn_smem + kScratchAt<E4M3> + kScratchBytes);
   float* scales = reinterpret_cast<float*>(attn_smem + kBarBytes);         // [slot]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   static_assert(F16 || !E4M3, "codes become f16");
@@ -225,6 +239,10 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
       mbar_init(PFULL(i, 0), 4u);
       mbar_init(PFULL(i, 1), 4u);
       mbar_init(OFULL(i), 1u);
+    }
+    for (int s = 0; s < kItems; ++s) {
+      mbar_init(IFULL(s), 1u);
+      mbar_init(IEMPTY(s), 9u + (E4M3 ? 1u + kConverters : kGuards));
     }
     for (int s = 0; s < kCodeSlots; ++s) {
       mbar_init(CFULL(s), 1u);
@@ -258,14 +276,14 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
   Shares shares;
   const bool some = start<kRows, kKeys, kThreads<E4M3>>(a, scratch, w, shares);
 
-  // rows of half i in an item, and the end of its key tiles in this run
-  auto rows_of = [&](const BigWalk& x) { return x.s.n * a.G - x.r * kRows; };
-  auto end_of = [&](const BigWalk& x, int i) {
-    if (rows_of(x) <= i * kHalf) return x.t;
-    return max(x.t, min(x.end, key_tiles<kHalf, kKeys>(x.s, a.G, 2 * x.r + i)));
+  // the n-th item (null after an abort; t < 0: there is none), and its release
+  auto take = [&](int n) -> const Item* {
+    return wait(IFULL(n % kItems), n / kItems & 1, abort_flag, 0x780) ? items + n % kItems : nullptr;
   };
-  // the last key that every row of the item sees
-  auto least_of = [&](const BigWalk& x) { return x.s.past + divided(x.r * kRows, a.G); };
+  auto leave = [&](int n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cta(IEMPTY(n % kItems));
+  };
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(E4M3 ? kLeanRegs8 : kLeanRegs16));
@@ -294,11 +312,19 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
         }
         return p;
       };
-      int page = page_of(w, w.t);
-      for (bool more = true; more && ok;) {
+      int page = page_of(w, w.t), n = 0;
+      for (bool more = true; more && ok; ++n) {
+        ok = wait(IEMPTY(n % kItems), (n / kItems & 1) ^ 1, abort_flag, 0x702);
+        if (!ok) break;
         int t = w.t;
         const int end = w.end, b_h = w.h;
         const Seq s = w.s;
+        if (lane == 0) {
+          const int rows = min(s.n * a.G - w.r * kRows, kRows);
+          items[n % kItems] = {w.b,    w.h, w.r,  t, end, w.len, s.row0, s.L, s.past, rows, s.past + divided(w.r * kRows, a.G),
+                               max(t, min(end, key_tiles<kHalf, kKeys>(s, a.G, 2 * w.r)))};
+          mbar_arrive_cta(IFULL(n % kItems));
+        }
         BigWalk next = w;
         more = next.next(a);
         for (; t < end && ok; ++t) {
@@ -330,6 +356,11 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
         }
         w = next;
       }
+      ok = ok && wait(IEMPTY(n % kItems), (n / kItems & 1) ^ 1, abort_flag, 0x703);
+      if (ok && lane == 0) {
+        items[n % kItems].t = -1;
+        mbar_arrive_cta(IFULL(n % kItems));
+      }
       if (!ok) {  // after an abort the loads in flight land before the CTA leaves
         for (int i = min(issued, my_slots); i > 0; --i) {
           st = st == 0 ? my_slots - 1 : st - 1;
@@ -339,21 +370,22 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
       }
     } else if (E4M3 && some && warp == 10) {
       // ------------------------------------ 8-bit: scales of a tile's keys and values
-      // four keys a lane; the values' relative to the largest so far, rounded up to
+      // four keys a lane; the values' relative to the item's largest so far, rounded up to
       // a power of two
       uint32_t n = 0;
-      int item = 0;
-      for (bool more = true; more && ok; ++item) {
+      for (int item = 0; ok; ++item) {
+        const Item* it = take(item);
+        if (it == nullptr || it->t < 0) break;
         float unit = 0.f;
-        const int least = least_of(w);
-        for (int t = w.t; t < w.end; ++t, ++n) {
+        const int end = it->end, L = it->L, least = it->least;
+        for (int t = it->t; t < end; ++t, ++n) {
           const uint32_t slot = n % kScaleSlots;
           const int key = t * kKeys + 4 * lane;
           float4 ks = make_float4(0.f, 0.f, 0.f, 0.f), vs = ks;
-          if (key < w.s.L) {
+          if (key < L) {
             int64_t page, place;
-            if (locate(a, w.s, w.b, key, page, place)) {
-              const int64_t at = ((page * a.Hkv + w.h) << a.page_shift) + place;
+            if (locate(a, it->row0, it->b, key, page, place)) {
+              const int64_t at = ((page * a.Hkv + it->h) << a.page_shift) + place;
               ks = *reinterpret_cast<const float4*>(a.kv.k_scale + at);
               vs = *reinterpret_cast<const float4*>(a.kv.v_scale + at);
             }
@@ -363,7 +395,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const bool finite = fabsf(each[e]) < INFINITY;
-            if (key + e >= w.s.L) {
+            if (key + e >= L) {
               each[e] = 0.f;
             } else if (finite) {
               most = fmaxf(most, fabsf(each[e]));
@@ -374,13 +406,11 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
           }
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+          const float power = __uint_as_float(min((__float_as_uint(most) & 0x7F800000u) + 0x00800000u, 0x7F000000u));
           float shrink = 1.f;
-          if (most >= unit) {
-            const float grown = __uint_as_float(min((__float_as_uint(most) & 0x7F800000u) + 0x00800000u, 0x7F000000u));
-            if (grown > unit) {
-              shrink = unit / grown;
-              unit = grown;
-            }
+          if (power > unit) {
+            shrink = unit / power;
+            unit = power;
           }
           const float per = 1.f / unit;
           ok = wait(SCEMPTY(slot), (n / kScaleSlots & 1u) ^ 1u, abort_flag, 0x710);
@@ -395,7 +425,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
           __syncwarp();
           if (lane == 0) mbar_arrive_cta(SCFULL(slot));
         }
-        more = ok && w.next(a);
+        leave(item);
       }
     } else if (some && warp == 9) {
       // -------------------------------------------------------- MMA issuer
@@ -421,12 +451,12 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
       // (a tile's keys in two parts: the first's products run while the second's weights are made)
       auto outputs = [&](int i, int part, uint32_t tile, bool first) {
 #pragma unroll
-        for (int k = 4 * part; k < 4 * part + 4; ++k)
-          mma_ts(leader, tmem + kOut + 128u * i, tmem + 128u * i + 8u * k, v_low | (addr(tile) + 128u * k), hi, idesc_o,
-                 !(first && k == 0));
+        for (int k = 0; k < 4; ++k)
+          mma_ts(leader, tmem + kOut + 128u * i, tmem + 128u * i + 32u * part + 8u * k,
+                 v_low | (addr(tile) + 512u * part + 128u * k), hi, idesc_o, !first || k > 0);
       };
       int st = 0;
-      uint32_t ph = 0, pph[2] = {0, 0}, qph[2] = {0, 0};
+      uint32_t ph = 0, pph = 0, qph = 0;  // (a bit a half)
       bool any = false;
       auto step = [&] {
         if (++st == slots) {
@@ -438,13 +468,19 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
       auto there = [&](int info) {
         return (E4M3 || wait(READY(st), ph, abort_flag, info)) && wait(FULL(st), ph, abort_flag, info);
       };
+      // (unrolled the issue is faster, but the 8-bit kernel outgrows the instruction caches)
+      constexpr int kUnrolled = E4M3 ? 1 : 2;
       auto tile_at = [&](int s) { return ring + static_cast<uint32_t>(s) * kTile; };
-      for (bool more = true; more && ok;) {
-        const int e[2] = {end_of(w, 0), end_of(w, 1)};
+      for (int item = 0; ok; ++item) {
+        const Item* it = take(item);
+        if (it == nullptr) ok = false;
+        if (!ok || it->t < 0) break;
+        const int t0 = it->t, end = it->end, e[2] = {it->end0, it->rows > kHalf ? end : t0};
+#pragma unroll 1
         for (int i = 0; i < 2 && ok; ++i)
-          if (w.t < e[i]) {
-            ok = wait(QFULL(i), qph[i], abort_flag, 0x720);
-            qph[i] ^= 1u;
+          if (t0 < (i == 0 ? e[0] : e[1])) {
+            ok = wait(QFULL(i), qph >> i & 1u, abort_flag, 0x720);
+            qph ^= 1u << i;
           }
         ok = ok && there(0x721);
         if (!ok) break;
@@ -452,37 +488,39 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
         any = true;
 #pragma unroll 1
         for (int i = 0; i < 2; ++i)
-          if (w.t < (i == 0 ? e[0] : e[1])) scores(i, tile_at(st));
+          if (t0 < (i == 0 ? e[0] : e[1])) scores(i, tile_at(st));
         commit<false>(leader, EMPTY(st));
         step();
-        for (int t = w.t; t < w.end && ok; ++t) {
+        for (int t = t0; t < end && ok; ++t) {
           const int vs = st;
           ok = there(0x722);
           step();
           const int ks = st;
-          const bool again = t + 1 < w.end;
+          const bool again = t + 1 < end;
           if (again) {
             ok = ok && there(0x724);
             step();
           }
-          for (int i = 0; i < 2 && ok; ++i) {
-            if (t < e[i]) {
+#pragma unroll kUnrolled
+          for (int i = 0; i < 2; ++i) {
+            const int ends = i == 0 ? e[0] : e[1];
+            if (ok && t < ends) {
+#pragma unroll kUnrolled
               for (int part = 0; part < 2 && ok; ++part) {
-                ok = wait(PFULL(i, part), pph[i], abort_flag, 0x725);
+                ok = wait(PFULL(i, part), pph >> i & 1u, abort_flag, 0x725);
                 if (!ok) break;
                 tc_fence_after();
-                outputs(i, part, tile_at(vs), t == w.t);
+                outputs(i, part, tile_at(vs), t == t0 && part == 0);
               }
-              if (!ok) break;
-              pph[i] ^= 1u;
-              if (t + 1 >= e[i]) commit<false>(leader, OFULL(i));
+              pph ^= 1u << i;
+              if (ok && t + 1 >= ends) commit<false>(leader, OFULL(i));
             }
-            if (i == 1) commit<false>(leader, EMPTY(vs));
-            if (t + 1 < e[i]) scores(i, tile_at(ks));
+            if (ok && i == 1) commit<false>(leader, EMPTY(vs));
+            if (ok && t + 1 < ends) scores(i, tile_at(ks));
           }
           if (again && ok) commit<false>(leader, EMPTY(ks));
         }
-        more = ok && w.next(a);
+        leave(item);
       }
       if (!ok && any) {  // MMAs in flight end before tensor memory is freed
         if (leader != 0u) mma_commit(drain);
@@ -491,17 +529,19 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
     } else if (some && !E4M3) {
       // ------------------- 16-bit: values of tiles that some row does not wholly see
       const int me = (warp - 10) * 32 + lane;
-      int st = 0, item = 0;
+      int st = 0;
       uint32_t ph = 0;
-      for (bool more = true; more && ok; ++item) {
-        const int least = least_of(w);
-        for (int u = 2 * w.t; u < 2 * w.end; ++u) {  // keys, values
+      for (int item = 0; ok; ++item) {
+        const Item* it = take(item);
+        if (it == nullptr || it->t < 0) break;
+        const int least = it->least, L = it->L, end = it->end;
+        for (int u = 2 * it->t; u < 2 * end; ++u) {  // keys, values
           const int t = u >> 1;
           ok = wait(FULL(st), ph, abort_flag, 0x740);
           if (!ok) break;
           if ((u & 1) != 0 && t * kKeys + kKeys - 1 > least) {
             const uint32_t tile = ring + static_cast<uint32_t>(st) * kTile;
-            const int there = min(kKeys, w.s.L - t * kKeys);
+            const int there = min(kKeys, L - t * kKeys);
             uint32_t odd = 0;
 #pragma unroll 4
             for (int i = me; i < kKeys * DP / 8; i += 32 * kGuards) {
@@ -527,37 +567,36 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
             ph ^= 1u;
           }
         }
-        more = ok && w.next(a);
+        leave(item);
       }
     } else if (E4M3 && some && warp >= 12) {
       // ------------------------------------------- 8-bit: codes into f16 tiles
       // thread j takes 16-byte pieces j, j + 128, ... of a tile (lanes go along a row)
       constexpr int kT = 32 * kConverters, kMine = kKeys * DP / 16 / kT, kRowPieces = DP / 16;
       const int me = (warp - 12) * 32 + lane;
-      int st = 0, cs = 0, item = 0;
+      int st = 0, cs = 0;
       uint32_t ph = 0, cph = 0;
-      for (bool more = true; more && ok; ++item) {
-        const int least = least_of(w);
+      for (int item = 0; ok; ++item) {
+        const Item* it = take(item);
+        if (it == nullptr || it->t < 0) break;
+        const int least = it->least, L = it->L, end = it->end;
 #pragma unroll 1
-        for (int u = 2 * w.t; u < 2 * w.end; ++u) {  // keys, values
+        for (int u = 2 * it->t; u < 2 * end; ++u) {  // keys, values
           const int t = u >> 1;
           ok = wait(CFULL(cs), cph, abort_flag, 0x750) && wait(EMPTY(st), ph ^ 1u, abort_flag, 0x751);
           if (!ok) break;
           const uint32_t from = codes + static_cast<uint32_t>(cs * code_bytes(DP)), tile = ring + static_cast<uint32_t>(st) * kTile;
           const bool partly = (u & 1) != 0 && t * kKeys + kKeys - 1 > least;
-          const int there = w.s.L - t * kKeys;
+          const int there = L - t * kKeys;
           uint32_t odd = 0;
-#pragma unroll
+#pragma unroll 2
           for (int j = 0; j < kMine; ++j) {
             const int i = me + j * kT, r = i / kRowPieces, c = i % kRowPieces;
             const uint4 v = dense::lds_u4(from + 16u * static_cast<uint32_t>(i));
             const uint32_t q[4] = {v.x, v.y, v.z, v.w};
             uint32_t h[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              h[2 * e] = e4m3x2_half2(q[e] & 0xFFFFu);
-              h[2 * e + 1] = e4m3x2_half2(q[e] >> 16);
-            }
+            for (int e = 0; e < 8; ++e) h[e] = e4m3x2_half2(e & 1 ? q[e >> 1] >> 16 : q[e >> 1] & 0xFFFFu);
             if (partly) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) h[e] = r < there ? tame(h[e], true, odd) : 0u;
@@ -584,7 +623,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
             cph ^= 1u;
           }
         }
-        more = ok && w.next(a);
+        leave(item);
       }
     }
     __syncwarp();
@@ -600,20 +639,17 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
     const uint32_t q_at = qbase + static_cast<uint32_t>(half) * kTile;
     uint32_t sph = 0, oph = 0, scn = 0, jph = 0;
     bool ok = true;
-    int item = 0;
     // this thread's row of an item
-    auto live_of = [&](const BigWalk& x) { return half * kHalf + row < rows_of(x); };
-    auto token_of = [&](const BigWalk& x) { return divided(x.r * kRows + (live_of(x) ? half * kHalf + row : 0), a.G); };
-    auto head_of = [&](const BigWalk& x, int token) {
-      return x.h * a.G + x.r * kRows + (live_of(x) ? half * kHalf + row : 0) - token * a.G;
-    };
+    auto live_of = [&](const Item* x) { return half * kHalf + row < x->rows; };
+    auto row_of = [&](const Item* x) { return x->r * kRows + (live_of(x) ? half * kHalf + row : 0); };
+    auto asks = [&](const Item* x) { return x->t < (half == 0 ? x->end0 : x->rows > kHalf ? x->end : x->t); };
     // The warp's queries into shared memory, a row over DP / 8 lanes.  16-bit: started
     // here, there after queries_done.  8-bit: as f16, each row's largest brought to
     // 2^14; returns what this thread's row's scores are multiplied with.
     constexpr int kAcross = DP / 8, kTogether = 32 / kAcross;
-    auto queries = [&](const BigWalk& x) {
-      const int tok = token_of(x), hd = head_of(x, tok);
-      const uint64_t mine = live_of(x) ? reinterpret_cast<uint64_t>(a.q + (x.s.row0 + tok) * a.q_stride + static_cast<int64_t>(hd) * a.D) : 0;
+    auto queries = [&](const Item* x) {
+      const int tok = divided(row_of(x), a.G), hd = x->h * a.G + row_of(x) - tok * a.G;
+      const uint64_t mine = live_of(x) ? reinterpret_cast<uint64_t>(a.q + (x->row0 + tok) * a.q_stride + static_cast<int64_t>(hd) * a.D) : 0;
       const int c = lane % kAcross, base_row = 32 * (warp & 3);
 #pragma unroll 4
       for (int i = 0; i < kAcross; ++i) {
@@ -660,17 +696,18 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
     };
     float factor = a.scale_log2;
     // (the first turn has no item yet: it only asks for the first one's queries)
-    bool begun = false, more = some;
-    while (more || begun) {
-      const int end = begun ? end_of(w, half) : 0, t0 = begun ? w.t : 0;
-      // the first key that some row of this half does not see, and the last key that
-      // this row sees
-      const int least = w.s.past + divided(w.r * kRows + half * kHalf, a.G);
-      const int limit = w.s.past + token_of(w);
+    const Item* w = nullptr;
+    for (int item = -1; some; ++item) {
+      const bool begun = item >= 0;
+      const int t0 = begun ? w->t : 0, w_end = begun ? w->end : 0;
+      const int end = !begun ? 0 : half == 0 ? w->end0 : w->rows > kHalf ? w_end : t0;
+      // the last key that every row of this half sees, and that this row sees
+      const int least = begun ? w->past + divided(w->r * kRows + half * kHalf, a.G) : 0;
+      const int limit = begun ? w->past + divided(row_of(w), a.G) : 0;
       float top = -INFINITY;  // of the row's scores, what its weights are relative to
       float unit = 1.f;
       uint64_t sum = 0;
-      for (int t = t0; t < (E4M3 && begun ? w.end : end); ++t) {
+      for (int t = t0; t < (E4M3 ? w_end : end); ++t) {
         const float* sc = nullptr;
         uint32_t slot = 0;
         if (E4M3) {
@@ -690,44 +727,50 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
         if (!ok) break;
         sph ^= 1u;
         tc_fence_after();
-        uint32_t s[4][32];
+        // Twice over the scores, some at a time: their maximum, then the weights.  (Held
+        // in registers in between, 128 of them unrolled, the code did not fit the
+        // instruction caches.)  Scores that are scaled or masked go back to tensor memory.
+        constexpr int kSome = E4M3 ? 32 : 64;
+        const bool masked = t * kKeys + kKeys - 1 > least;
+        float now = -INFINITY;
+#pragma unroll 1
+        for (int part = 0; part < kKeys / kSome; ++part) {
+          uint32_t s[kSome / 32][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) dense::tmem_ld32(S + 32u * c, s[c]);
+          for (int c = 0; c < kSome / 32; ++c) dense::tmem_ld32(S + static_cast<uint32_t>(kSome * part + 32 * c), s[c]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) dense::tmem_ld32_wait(s[c]);
-        if (E4M3) {
+          for (int c = 0; c < kSome / 32; ++c) dense::tmem_ld32_wait(s[c]);
+          if (E4M3) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(sc + 32 * c + 4 * j);
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                uint32_t* x = &s[c][4 * j + 2 * e];
-                const uint64_t z = mul2((static_cast<uint64_t>(x[1]) << 32) | x[0], e == 0 ? k.x : k.y);
-                x[0] = static_cast<uint32_t>(z);
-                x[1] = static_cast<uint32_t>(z >> 32);
-              }
+            for (int j = 0; j < kSome / 4; ++j) {
+              const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(sc + kSome * part + 4 * j);
+              uint32_t* x = &s[j >> 3][4 * (j & 7)];
+              const uint64_t y = mul2((static_cast<uint64_t>(x[1]) << 32) | x[0], k.x);
+              const uint64_t z = mul2((static_cast<uint64_t>(x[3]) << 32) | x[2], k.y);
+              x[0] = static_cast<uint32_t>(y);
+              x[1] = static_cast<uint32_t>(y >> 32);
+              x[2] = static_cast<uint32_t>(z);
+              x[3] = static_cast<uint32_t>(z >> 32);
             }
+          }
+          if (masked) {
+            const int seen = limit - t * kKeys - kSome * part;
+#pragma unroll
+            for (int j = 0; j < kSome; ++j)
+              if (j > seen) s[j >> 5][j & 31] = __float_as_uint(-INFINITY);
+          }
+          if (E4M3 || masked) {
+#pragma unroll
+            for (int c = 0; c < kSome / 32; ++c) tmem_st32(S + static_cast<uint32_t>(kSome * part + 32 * c), s[c]);
+          }
+          float m4[4] = {now, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < kSome; j += 2)
+            m4[j >> 1 & 3] = fmaxf(m4[j >> 1 & 3], fmaxf(__uint_as_float(s[j >> 5][j & 31]), __uint_as_float(s[j >> 5][(j & 31) + 1])));
+          now = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         }
-        if (t * kKeys + kKeys - 1 > least) {
-          const int seen = limit - t * kKeys;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (32 * c + j > seen) s[c][j] = __float_as_uint(-INFINITY);
-        }
-        float m4[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          m4[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-          for (int j = 1; j < 31; j += 2)
-            m4[c] = fmaxf(m4[c], fmaxf(__uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1])));
-          m4[c] = fmaxf(m4[c], __uint_as_float(s[c][31]));
-        }
-        const float now = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * factor;
+        if (E4M3 || masked) tmem_st_wait();
+        now *= factor;
         const float shrink = E4M3 ? sc[2 * kKeys + 1] : 1.f;
         if (t == t0) {
           top = fmaxf(top, now);  // (NaN leaves it)
@@ -748,39 +791,51 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
         }
         const float r = reference(top);
         const uint64_t f2 = pack2(factor, factor), r2 = pack2(-r, -r);
-        uint64_t sums[2] = {0, 0};
-        auto given = [&](int part) {
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cta(PFULL(half, part));
-        };
+#pragma unroll 1
+        for (int part = 0; part < kKeys / kSome; ++part) {
+          uint32_t s[kSome / 32][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t p[16];
+          for (int c = 0; c < kSome / 32; ++c) dense::tmem_ld32(S + static_cast<uint32_t>(kSome * part + 32 * c), s[c]);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const uint64_t z = fma2((static_cast<uint64_t>(s[c][2 * j + 1]) << 32) | s[c][2 * j], f2, r2);
-            uint64_t e = pack2(exp2_fast(lo2(z)), exp2_fast(hi2(z)));
-            sums[j & 1] = add2(sums[j & 1], e);
-            if (E4M3) {
-              e = mul2(e, *reinterpret_cast<const uint64_t*>(sc + kKeys + 32 * c + 2 * j));
+          for (int c = 0; c < kSome / 32; ++c) dense::tmem_ld32_wait(s[c]);
+          uint64_t sums[2] = {0, 0};
+#pragma unroll
+          for (int c = 0; c < kSome / 32; ++c) {
+            uint32_t p[16];
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              ulonglong2 v = make_ulonglong2(0, 0);
+              if (E4M3) v = *reinterpret_cast<const ulonglong2*>(sc + kKeys + kSome * part + 32 * c + 2 * j);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint64_t z = fma2((static_cast<uint64_t>(s[c][2 * (j + k) + 1]) << 32) | s[c][2 * (j + k)], f2, r2);
+                uint64_t e = pack2(exp2_fast(lo2(z)), exp2_fast(hi2(z)));
+                sums[k] = add2(sums[k], e);
+                if (E4M3) e = mul2(e, k == 0 ? v.x : v.y);
+                p[j + k] = F16 ? pack_half(lo2(e), hi2(e)) : pack_bf16x2(lo2(e), hi2(e));
+              }
             }
-            p[j] = F16 ? pack_half(lo2(e), hi2(e)) : pack_bf16x2(lo2(e), hi2(e));
+            tmem_st16(S + static_cast<uint32_t>(kSome / 2 * part + 16 * c), p);
           }
-          tmem_st16(S + 16u * c, p);
-          if (c == 1) given(0);
+          sum = add2(sum, add2(sums[0], sums[1]));
+          if (kSome * (part + 1) % 64 == 0) {  // half of the keys' weights
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cta(PFULL(half, kSome * part >= 64));
+          }
         }
-        given(1);
         if (E4M3 && lane == 0) mbar_arrive_cta(SCEMPTY(slot));
-        sum = add2(sum, add2(sums[0], sums[1]));
       }
       if (!ok) break;
       // ---- the item's end: its last scores are read, so the next one's queries come
       const bool has = t0 < end;
-      BigWalk next = w;
-      if (begun) more = next.next(a);
-      const bool ask = more && next.t < end_of(next, half);
+      const Item* next = take(item + 1);
+      if (next == nullptr) {
+        ok = false;
+        break;
+      }
+      const bool more = next->t >= 0, ask = more && asks(next);
       if (ask) queries(next);
       if (has) {
         ok = wait(OFULL(half), oph, abort_flag, 0x762);
@@ -793,14 +848,14 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
       if (begun) {
         const float total = lo2(sum) + hi2(sum);
         const bool spoiled = dirty[item % kDirty] == item, live = live_of(w);
-        const bool whole = w.end - w.t == w.len;
-        const int tok = token_of(w), hd = head_of(w, tok);
-        const int64_t out_row = w.s.row0 + tok;
+        const bool whole = w_end - t0 == w->len;
+        const int tok = limit - w->past, hd = w->h * a.G + row_of(w) - tok * a.G;
+        const int64_t out_row = w->row0 + tok;
         const uint64_t to = live ? reinterpret_cast<uint64_t>(a.out + out_row * a.out_stride + static_cast<int64_t>(hd) * a.D) : 0;
         // An item that lies in several runs leaves its sums in the workspace, and the
         // last of its CTAs to finish joins them in the order of the runs.
         const int first = t0 > 0 ? shares.first : static_cast<int>(blockIdx.x);
-        const int pieces = whole ? 1 : shares.pieces(first, w.len - w.end);
+        const int pieces = whole ? 1 : shares.pieces(first, w->len - w_end);
         constexpr size_t kPiece = attn_piece_bytes(kRows, DP) / 4;
         auto piece = [&](int i) { return a.partial + (2 * (first + i) + (i == 0 ? 1 : 0)) * kPiece + half * kHalf + row; };
         float* mine = piece(static_cast<int>(blockIdx.x) - first);
@@ -876,14 +931,14 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
             // values that are not finite, of the keys that this row sees among those looked
             // at, added to what was written
             __syncwarp();
-            const int from = max(t0, divided(least_of(w) + 1, kKeys)) * kKeys;
+            const int from = max(t0, divided(w->least + 1, kKeys)) * kKeys;
             const int upto = live ? min(limit, end * kKeys - 1) : -1;
 #pragma unroll 1
             for (int key = from; key <= upto; ++key) {
               int64_t page, place;
-              if (!locate(a, w.s, w.b, key, page, place)) continue;
-              const float vscale = E4M3 ? a.kv.v_scale[((page * a.Hkv + w.h) << a.page_shift) + place] : 1.f;
-              const int64_t in = page * a.kv.v_page + place * a.kv.v_token + w.h * a.kv.v_head;
+              if (!locate(a, w->row0, w->b, key, page, place)) continue;
+              const float vscale = E4M3 ? a.kv.v_scale[((page * a.Hkv + w->h) << a.page_shift) + place] : 1.f;
+              const int64_t in = page * a.kv.v_page + place * a.kv.v_token + w->h * a.kv.v_head;
 #pragma unroll 1
               for (int d = 0; d < a.D; ++d) {
                 const float x = E4M3 ? __half2float(__ushort_as_half(static_cast<uint16_t>(e4m3x2_half2(a.kv.v[in + d])))) * vscale
@@ -933,12 +988,11 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
         }
         if (!ok) break;
         tc_fence_before();  // (the next item's products write O after this half's weights)
-        ++item;
+        leave(item);
       }
       if (!more) break;
       w = next;
       factor = factor_next;
-      begun = true;
     }
     __syncwarp();
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(E4M3 ? kLaunchRegs8 : kLaunchRegs16));
@@ -956,6 +1010,8 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
 #undef READY
 #undef CFULL
 #undef CEMPTY
+#undef IFULL
+#undef IEMPTY
   if (tid == 0 && *abort_flag != 0) record_error(a.err, kErrTimeout, static_cast<uint32_t>(*abort_flag));
   if (warp == 9) {
     tc_fence_after();
