@@ -45,25 +45,24 @@ constexpr int kThreads = E4M3 ? 512 : 384;
 constexpr int kGuards = 2, kConverters = 4;  // warps from 10, from 12 on
 constexpr uint32_t kTmemCols = 512, kOut = 256;  // scores of half i at 128 i, outputs at 256 + 128 i
 
-using BigWalk = Walk<kRows, kKeys>;
+using BigWalk = Walk<Shape<kRows, kKeys, 3, 3, 4>>;
 
 // Barriers and small arrays, then (1024-byte aligned) Q's halves, the ring of key and
 // value tiles and the ring of their codes.
 constexpr int kBarBytes = 640;
 constexpr int kScaleSlot = 2 * kKeys + 4;  // of 128 keys, of their values, unit, shrink
-constexpr int kScratchBytes = 160;
 constexpr int kItems = 4;
 // An item as its warps see it: end is of its key tiles in this run, end0 that of the
 // first half's; least the last key that all rows see.
 struct Item {
-  int b, h, r, t, end, len, row0, L, past, rows, least, end0;
+  int b, h, r, t, end, len, row0, L, past, rows, least, end0, first, pieces;
 };
 template <bool E4M3>
 constexpr int kMiscBytes = E4M3 ? 3072 : 1024;
 template <bool E4M3>
-constexpr int kScratchAt = kBarBytes + (E4M3 ? kScaleSlots * kScaleSlot * 4 : 0);
-static_assert(kScratchAt<true> + kScratchBytes + kItems * sizeof(Item) <= kMiscBytes<true> &&
-                  kScratchAt<false> + kScratchBytes + kItems * sizeof(Item) <= kMiscBytes<false>,
+constexpr int kItemsAt = kBarBytes + (E4M3 ? kScaleSlots * kScaleSlot * 4 : 0);
+static_assert(kItemsAt<true> + kItems * sizeof(Item) <= kMiscBytes<true> &&
+                  kItemsAt<false> + kItems * sizeof(Item) <= kMiscBytes<false>,
               "all before Q");
 __host__ __device__ constexpr int tile_bytes(int dp) { return kKeys * dp * 2; }
 __host__ __device__ constexpr int code_bytes(int dp) { return kKeys * dp; }
@@ -221,8 +220,8 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
   volatile int* abort_flag = reinterpret_cast<volatile int*>(attn_smem + 244);
   volatile int* last_flag = reinterpret_cast<volatile int*>(attn_smem + 248);
   volatile int* dirty = reinterpret_cast<volatile int*>(attn_smem + 256);  // [kDirty]: the item that has such values
-  int64_t* scratch = reinterpret_cast<int64_t*>(attn_smem + kScratchAt<E4M3>);
-  Item* items = reinterpret_cast<Item*>(attn_smem + kScratchAt<E4M3> + kScratchBytes);
+  int64_t* scratch = reinterpret_cast<int64_t*>(attn_smem + kMiscBytes<E4M3>);  // (Q's place, until the roles begin)
+  Item* items = reinterpret_cast<Item*>(attn_smem + kItemsAt<E4M3>);
   float* scales = reinterpret_cast<float*>(attn_smem + kBarBytes);         // [slot]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   static_assert(F16 || !E4M3, "codes become f16");
@@ -273,8 +272,8 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
   const uint32_t tmem = *tmem_slot;
   clear_empty_rows(a);
   BigWalk w;
-  Shares shares;
-  const bool some = start<kRows, kKeys, kThreads<E4M3>>(a, scratch, w, shares);
+  const bool some = start<kThreads<E4M3>>(a, scratch, w);
+  __syncthreads();
 
   // the n-th item (null after an abort; t < 0: there is none), and its release
   auto take = [&](int n) -> const Item* {
@@ -322,7 +321,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
         if (lane == 0) {
           const int rows = min(s.n * a.G - w.r * kRows, kRows);
           items[n % kItems] = {w.b,    w.h, w.r,  t, end, w.len, s.row0, s.L, s.past, rows, s.past + divided(w.r * kRows, a.G),
-                               max(t, min(end, key_tiles<kHalf, kKeys>(s, a.G, 2 * w.r)))};
+                               max(t, min(end, key_tiles<kHalf, kKeys>(s, a.G, 2 * w.r))), w.first_cta(), w.cta_count()};
           mbar_arrive_cta(IFULL(n % kItems));
         }
         BigWalk next = w;
@@ -469,7 +468,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
         return (E4M3 || wait(READY(st), ph, abort_flag, info)) && wait(FULL(st), ph, abort_flag, info);
       };
       // (unrolled the issue is faster, but the 8-bit kernel outgrows the instruction caches)
-      constexpr int kUnrolled = E4M3 ? 1 : 2;
+      constexpr int kUnrolled = 2;
       auto tile_at = [&](int s) { return ring + static_cast<uint32_t>(s) * kTile; };
       for (int item = 0; ok; ++item) {
         const Item* it = take(item);
@@ -776,8 +775,10 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
           top = fmaxf(top, now);  // (NaN leaves it)
         } else if (__any_sync(0xffffffffu, now > top + 8.f) || shrink != 1.f) {
           // O of the tiles before is complete: their products precede these scores
-          const float up = fmaxf(top, now), keep = exp2_fast(top - reference(up));
-          top = up;
+          // (a row that did not grow so far keeps its bits, whatever its warp's others do)
+          const bool grown = now > top + 8.f;
+          const float keep = grown ? exp2_fast(top - reference(now)) : 1.f;
+          top = grown ? now : top;
           sum = mul2(sum, pack2(keep, keep));
           const float f = keep * shrink;
 #pragma unroll 1
@@ -854,8 +855,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
         const uint64_t to = live ? reinterpret_cast<uint64_t>(a.out + out_row * a.out_stride + static_cast<int64_t>(hd) * a.D) : 0;
         // An item that lies in several runs leaves its sums in the workspace, and the
         // last of its CTAs to finish joins them in the order of the runs.
-        const int first = t0 > 0 ? shares.first : static_cast<int>(blockIdx.x);
-        const int pieces = whole ? 1 : shares.pieces(first, w->len - w_end);
+        const int first = w->first, pieces = w->pieces;
         constexpr size_t kPiece = attn_piece_bytes(kRows, DP) / 4;
         auto piece = [&](int i) { return a.partial + (2 * (first + i) + (i == 0 ? 1 : 0)) * kPiece + half * kHalf + row; };
         float* mine = piece(static_cast<int>(blockIdx.x) - first);

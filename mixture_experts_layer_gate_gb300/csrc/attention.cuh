@@ -2,8 +2,8 @@
 // queries of one sequence and key head: row i G + g is query head g of the group,
 // new token i) and reads the keys up to its last row's, in tiles of KT keys.  All
 // items' tiles, in the order of sequences, key heads and row tiles, are cut into as
-// many runs of equal length as there are CTAs, whatever the sequences' lengths are: a
-// long context is spread over many SMs and short ones share one.  Lengths are read
+// many runs of about equal cost as there are CTAs, whatever the sequences' lengths are:
+// a long context is spread over many SMs and short ones share one.  Lengths are read
 // on the device, so a captured call follows them.  An item that lies in several runs
 // is joined by the CTA that finishes last, in the order of the runs (the result does
 // not depend on which one that is).
@@ -93,69 +93,66 @@ __device__ __forceinline__ int64_t tiles_before(const Seq& s, int G, int r) {
   }
   return sum;
 }
-template <int M, int KT>
-__device__ __forceinline__ int64_t head_tiles(const Seq& s, int G) {
-  const int R = row_tiles<M>(s, G);
-  return R == 0 ? 0 : tiles_before<M, KT>(s, G, R - 1) + key_tiles<M, KT>(s, G, R - 1);
-}
+// How a kernel shares out: rows and keys of a tile; what an item costs beside its
+// tiles, in tiles; runs are no shorter than `least`, and an item is not cut within
+// `slack` of its ends (a cut costs a join).
+template <int M_, int KT_, int COST_, int SLACK_, int LEAST_>
+struct Shape {
+  static constexpr int M = M_, KT = KT_, cost = COST_, slack = SLACK_, least = LEAST_;
+};
 
-// A CTA's place in its run of tiles.
-template <int M, int KT>
+// A place among all items' tiles.
+struct Place {
+  int b, h, r, t;
+};
+
+// A CTA's place in its run.
+template <typename S>
 struct Walk {
   Seq s;
   int b, h, r, R;
-  int t, end;        // key tiles of the item in this run
-  int len;           // the item's key tiles
-  int64_t left;      // tiles of the run from t on
+  int t, end;   // key tiles of the item in this run
+  int len;      // the item's key tiles
+  Place stop;   // where the run ends
+  int first, pieces, pieces_last;  // of an item that begins before the run: the CTA where it does, and its CTAs; of
+                                   // one that ends after it
 
   __device__ __forceinline__ void enter(const AttnArgs& a) {
-    len = key_tiles<M, KT>(s, a.G, r);
-    end = left < len - t ? t + static_cast<int>(left) : len;
+    len = key_tiles<S::M, S::KT>(s, a.G, r);
+    end = b == stop.b && h == stop.h && r == stop.r ? stop.t : len;
   }
+  // the item's first CTA, and how many it has
+  __device__ __forceinline__ int first_cta() const { return t > 0 ? first : static_cast<int>(blockIdx.x); }
+  __device__ __forceinline__ int cta_count() const { return t > 0 ? pieces : end < len ? pieces_last : 1; }
   // to the next item; false at the run's end
   __device__ __forceinline__ bool next(const AttnArgs& a) {
-    left -= end - t;
-    if (left <= 0) return false;
+    if (end < len) return false;
     if (++r == R) {
       r = 0;
       if (++h == a.Hkv) {
         h = 0;
         do {
-          if (++b >= a.B) {  // (lengths that changed under the call)
-            left = 0;
-            return false;
-          }
+          if (++b >= a.B) return false;
           s = sequence(a, b, false);
-          R = row_tiles<M>(s, a.G);
+          R = row_tiles<S::M>(s, a.G);
         } while (R == 0);
       }
     }
     t = 0;
     enter(a);
-    return true;
+    return end > 0;
   }
 };
 
-struct Shares {
-  int64_t run;   // tiles of a CTA, and one more of the first `more` CTAs
-  int n, more;   // CTAs with work
-  int first;     // the CTA whose run holds the first tile of this run's first item
-  __device__ __forceinline__ int64_t run_of(int c) const { return run + (c < more); }
-  // CTAs up to the one that holds the last tile of an item of this CTA that begins
-  // in the run of `from`, `rest` tiles after this run
-  __device__ __forceinline__ int pieces(int from, int64_t rest) const {
-    int c = blockIdx.x + 1;
-    for (; rest > 0; ++c) rest -= run_of(c);
-    return c - from;
-  }
-};
+constexpr int kScratchWords = 64;  // of 8 bytes, for start()
 
-// The run of this CTA; false where it has none.  Every thread calls it; `scratch`
-// (read until the next barrier) holds THREADS / 32 + 4 words of 8 bytes.
-template <int M, int KT, int THREADS>
-__device__ __forceinline__ bool start(const AttnArgs& a, int64_t* scratch, Walk<M, KT>& w, Shares& sh) {
-  constexpr int kWarps = THREADS / 32;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// The run of this CTA; false where it has none.  Every thread calls it; `scratch` (read
+// until the next barrier) holds kScratchWords.
+template <int THREADS, typename S>
+__device__ __forceinline__ bool start(const AttnArgs& a, int64_t* scratch, Walk<S>& w) {
+  constexpr int kWarps = THREADS / 32, M = S::M, KT = S::KT;
+  static_assert(kWarps <= 32 && kWarps >= 2, "one warp joins the warps' sums, two find the run's ends");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
   auto scan = [&](int64_t v, int64_t& sum) {  // the threads' values before this one's; their sum
     int64_t x = v;
 #pragma unroll
@@ -176,10 +173,11 @@ __device__ __forceinline__ bool start(const AttnArgs& a, int64_t* scratch, Walk<
     }
     return before;
   };
-  // (twice over the sequences, in one piece of code: their sum, then the one that
-  // holds the run's first tile; of few sequences the second time needs no reading)
-  const int cta = blockIdx.x;
-  int64_t total = 0, mine = 0, before = 0, base = 0, lo = 0;
+  // (twice over the sequences, in one piece of code: their sum, then those that hold
+  // the run's ends; of few sequences the second time needs no reading)
+  int64_t total = 0, mine = 0, before = 0, base = 0, cut[2] = {0, 0}, run = 0;
+  int n = 0, longer = 0;
+  auto run_of = [&](int c) { return run + (c < longer); };
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
@@ -187,59 +185,108 @@ __device__ __forceinline__ bool start(const AttnArgs& a, int64_t* scratch, Walk<
       int64_t sum = total;
       if (pass == 0 || a.B > THREADS) {
         const int b = b0 + tid;
-        mine = b < a.B ? head_tiles<M, KT>(sequence(a, b, pass == 0 && cta == 0), a.G) * a.Hkv : 0;
+        mine = 0;
+        if (b < a.B) {
+          const Seq s = sequence(a, b, pass == 0 && cta == 0);
+          const int R = row_tiles<M>(s, a.G);
+          if (R > 0)
+            mine = (tiles_before<M, KT>(s, a.G, R - 1) + key_tiles<M, KT>(s, a.G, R - 1) + static_cast<int64_t>(S::cost) * R) * a.Hkv;
+        }
         before = scan(mine, sum);
       }
       if (pass == 0) {
         total += sum;
       } else {
-        if (base + before <= lo && lo < base + before + mine) {
-          scratch[kWarps] = b0 + tid;
-          scratch[kWarps + 1] = lo - base - before;
-        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (base + before <= cut[i] && cut[i] < base + before + mine) {
+            scratch[32 + 2 * i] = b0 + tid;
+            scratch[33 + 2 * i] = cut[i] - base - before;
+          }
         base += sum;
       }
     }
     if (pass == 0) {
-      sh.n = static_cast<int>(total < static_cast<int64_t>(gridDim.x) ? total : static_cast<int64_t>(gridDim.x));
-      if (cta >= sh.n) return false;
-      sh.run = total >> 31 == 0 ? static_cast<int64_t>(divided(static_cast<int>(total), sh.n)) : total / sh.n;
-      sh.more = static_cast<int>(total - sh.run * sh.n);
-      lo = sh.run * cta + min(cta, sh.more);
+      const int64_t most = (total + S::least - 1) / S::least;
+      n = static_cast<int>(most < static_cast<int64_t>(gridDim.x) ? most : static_cast<int64_t>(gridDim.x));
+      if (cta >= n) return false;
+      run = total >> 31 == 0 ? static_cast<int64_t>(divided(static_cast<int>(total), n)) : total / n;
+      longer = static_cast<int>(total - run * n);
+      cut[0] = run * cta + min(cta, longer);
+      cut[1] = cut[0] + run_of(cta);
     }
   }
   __syncthreads();
-  w.b = static_cast<int>(scratch[kWarps]);
-  int64_t rest = scratch[kWarps + 1];
+  // warps 0 and 1: where the run's ends lie
+  int* found = reinterpret_cast<int*>(scratch + 40);
+  if (warp < 2) {
+    const int c = cta + warp;  // the CTA that begins here
+    Place p = {a.B, 0, 0, 0};
+    int first = cta, pieces = 1;
+    if (c < n) {
+      p.b = static_cast<int>(scratch[32 + 2 * warp]);
+      int64_t rest = scratch[33 + 2 * warp];
+      Seq s = sequence(a, p.b, false);
+      int R = row_tiles<M>(s, a.G);
+      // the last row tile that starts at or before `rest`: 32 candidates at a time, the
+      // first time with the whole head's cost as one more
+      int lo = 0, hi = R;    // in [lo, hi)
+      int64_t skipped = 0;   // what lies before row tile lo
+      bool whole = true;
+#pragma unroll 1
+      while (whole || hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, r = whole ? R - 1 : min(lo + lane * step, R - 1);
+        const int64_t there = tiles_before<M, KT>(s, a.G, r) + static_cast<int64_t>(S::cost) * r;
+        if (whole) {
+          const int64_t head = there + key_tiles<M, KT>(s, a.G, r) + S::cost;
+          for (; rest >= head; ++p.h) rest -= head;
+          whole = false;
+          continue;
+        }
+        const int top = 31 - __clz(__ballot_sync(0xffffffffu, lo + lane * step < hi && there <= rest));
+        skipped = __shfl_sync(0xffffffffu, there, top);
+        lo += top * step;
+        hi = min(hi, lo + step);
+      }
+      p.r = lo;
+      const int len = key_tiles<M, KT>(s, a.G, lo);
+      const int64_t at = rest - skipped;  // in the item, its cost first
+      const int64_t from = S::cost + S::slack, upto = S::cost + len - S::slack;
+      if (at < from) {
+        p.t = 0;
+      } else if (at > upto) {  // the next item's start
+        if (++p.r == R) {
+          p.r = 0;
+          if (++p.h == a.Hkv) {
+            p.h = 0;
+            do ++p.b;
+            while (p.b < a.B && row_tiles<M>(sequence(a, p.b, false), a.G) == 0);
+          }
+        }
+      } else {
+        p.t = static_cast<int>(at) - S::cost;
+        // the item's other cuts
+        int c0 = c, c1 = c;
+        for (int64_t x = at; c0 > 1 && x - run_of(c0 - 1) >= from; --c0) x -= run_of(c0 - 1);
+        for (int64_t x = at; c1 + 1 < n && x + run_of(c1) <= upto; ++c1) x += run_of(c1);
+        first = c0 - 1;
+        pieces = c1 - c0 + 2;
+      }
+    }
+    if (lane == 0) {
+      int* to = found + 6 * warp;
+      to[0] = p.b, to[1] = p.h, to[2] = p.r, to[3] = p.t, to[4] = first, to[5] = pieces;
+    }
+  }
+  __syncthreads();
+  w.b = found[0], w.h = found[1], w.r = found[2], w.t = found[3];
+  w.stop = {found[6], found[7], found[8], found[9]};
+  w.first = found[4];
+  w.pieces = found[5];
+  w.pieces_last = found[11];
+  if (w.b >= a.B || (w.b == w.stop.b && w.h == w.stop.h && w.r == w.stop.r && w.t == w.stop.t)) return false;
   w.s = sequence(a, w.b, false);
   w.R = row_tiles<M>(w.s, a.G);
-  w.h = 0;
-  // the last row tile that starts at or before `rest`: 32 candidates at a time, the
-  // first time with the whole head's tiles as one more
-  int lo_r = 0, hi_r = w.R;  // in [lo_r, hi_r)
-  int64_t skipped = 0;       // tiles before row tile lo_r
-  bool first = true;
-#pragma unroll 1
-  while (first || hi_r - lo_r > 1) {
-    const int step = (hi_r - lo_r + 31) / 32;
-    const int r = first ? w.R - 1 : lo_r + lane * step;
-    const int64_t there = tiles_before<M, KT>(w.s, a.G, min(r, w.R - 1));
-    if (first) {
-      const int64_t per_head = there + key_tiles<M, KT>(w.s, a.G, w.R - 1);
-      for (; rest >= per_head; ++w.h) rest -= per_head;
-      first = false;
-      continue;
-    }
-    const int top = 31 - __clz(__ballot_sync(0xffffffffu, r < hi_r && there <= rest));
-    skipped = __shfl_sync(0xffffffffu, there, top);
-    lo_r += top * step;
-    hi_r = min(hi_r, lo_r + step);
-  }
-  w.r = lo_r;
-  w.t = static_cast<int>(rest - skipped);
-  w.left = sh.run_of(cta);
-  sh.first = cta;
-  for (int64_t back = w.t; back > 0;) back -= sh.run_of(--sh.first);
   w.enter(a);
   return true;
 }

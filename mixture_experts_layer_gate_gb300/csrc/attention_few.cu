@@ -38,7 +38,7 @@ constexpr int kTile = kKeys * kWarps;
 constexpr int kMaxDepth = 8;
 constexpr size_t kSmem = 232448;
 
-using FewWalk = Walk<kRows, kTile>;
+using FewWalk = Walk<Shape<kRows, kTile, 1, 1, 1>>;
 
 __host__ __device__ constexpr int row_bytes(bool e4m3, int dp) { return e4m3 ? dp : 2 * dp; }
 // a step's keys and values, and their scales
@@ -46,7 +46,7 @@ __host__ __device__ constexpr int stage_bytes(bool e4m3, int dp) {
   return 2 * kKeys * row_bytes(e4m3, dp) + (e4m3 ? 2 * kKeys * 4 : 0);
 }
 __host__ __device__ constexpr int join_bytes(int dp) { return 4 * kRows * dp * 4; }
-constexpr int kMiscBytes = 2 * kWarps * kRows * 4 + (kWarps + 4) * 8 + 32;
+constexpr int kMiscBytes = 2 * kWarps * kRows * 4 + kScratchWords * 8;
 
 __device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16u : 0u) : "memory");
@@ -89,8 +89,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnAr
   pdl_trigger();
   clear_empty_rows(a);
   FewWalk cur;
-  Shares shares;
-  if (!start<kRows, kTile, kThreads>(a, scratch, cur, shares)) return;
+  if (!start<kThreads>(a, scratch, cur)) return;
 
   // ---- loads, ahead of the products
   FewWalk iss = cur;
@@ -134,12 +133,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnAr
           cp_async16_if(dst + static_cast<uint32_t>(2 * kKeys * kRow + 16 * lane), good ? s + at : s, good);
         }
       }
-      if (iss.t + 1 == iss.end) {
-        more = iss.next(a);
-      } else {
-        ++iss.t;
-        --iss.left;
-      }
+      if (++iss.t == iss.end) more = iss.next(a);
       if (more) page = page_of(iss);
     }
     cp_async_commit();
@@ -495,8 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnAr
     bool write = true;
     if (cur.end - cur.t < cur.len) {
       // the item lies in several runs: the last one to finish joins them
-      const int first = cur.t > 0 ? shares.first : static_cast<int>(blockIdx.x);
-      const int pieces = shares.pieces(first, cur.len - cur.end);
+      const int first = cur.first_cta(), pieces = cur.cta_count();
       constexpr size_t kPiece = attn_piece_bytes(kRows, DP) / 4;
       auto piece = [&](int i) { return a.partial + (2 * (first + i) + (i == 0 ? 1 : 0)) * kPiece; };
       float* to = piece(static_cast<int>(blockIdx.x) - first);
