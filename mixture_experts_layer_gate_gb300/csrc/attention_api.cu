@@ -99,7 +99,7 @@ moe_status_t attend(const moe_attention_t* p, AttnArgs& a, const void* q, int64_
   a.f16 = p->dtype == MOE_T_F16;
   a.scale_log2 = p->scale * 1.4426950408889634f;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return cuda_status(few_rows(*p) ? launch_attention_few(a, di.sms, s) : launch_attention(a, di.sms, s));
+  return cuda_status(few_rows(*p) ? launch_attention_few(a, p->max_q * a.G, di.sms, s) : launch_attention(a, di.sms, s));
 }
 
 }  // namespace

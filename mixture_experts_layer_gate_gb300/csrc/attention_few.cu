@@ -1,13 +1,13 @@
 // Attention of few rows (single tokens, drafted tokens: at most 16 rows of a key
-// head's queries): every key and value is read once and used by 16 rows, so the bound
-// is memory, and the products are mma.sync m16n8k16 (tcgen05's smallest M is 64
-// rows).  More rows go through tiles of 16, which is right but reads the keys once a
-// tile.
+// head's queries): every key and value is read once and used by all rows, so the bound
+// is memory, and the products are mma.sync m16n8k16 with 16 keys, or 16 places of the
+// head, as M and 8 rows as N (tcgen05's smallest M is 64).  More rows go through tiles
+// of 16, which is right but reads the keys once a tile.
 //
-// A tile of 128 keys is 16 keys for each of the eight warps.  A warp streams its
-// keys and values through a ring of its own (cp.async, several tiles ahead, across
-// items) and holds its own running maximum, sum and output, joined when the item
-// ends: no warp waits for another inside an item.
+// A tile is 16 keys for each warp.  A warp streams its keys and values through a ring
+// of its own (cp.async, some tiles ahead, across items) and holds its own running
+// maximum, sum and output, joined when the item ends: no warp waits for another inside
+// an item.
 //
 // One pass over the keys: with m the largest score so far, l = sum 2^(x - m) and O =
 // sum 2^(x - m) v, both multiplied by 2^(m - m') when it grows to m'.  Sums are float;
@@ -22,7 +22,9 @@
 //
 // K is permuted inside the head (any order gives the same product) so that a lane's
 // 16 adjacent bytes of a key are its fragment; 8-bit values are read along the head and
-// paired across keys by byte permutes, which leaves each lane 32 adjacent outputs.
+// paired across keys by byte permutes, which leaves each lane 16 adjacent outputs.
+// Weights, made with a key a lane, become the second product's fragment by one
+// transposition of 8 x 8 each.
 #include "attention.cuh"
 #include "stream.cuh"
 
@@ -31,25 +33,35 @@ namespace {
 
 using namespace attn;
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kRows = kAttnFewRows;
-constexpr int kKeys = 16;             // of a warp's step
-constexpr int kTile = kKeys * kWarps;
+constexpr int kMostRows = kAttnFewRows;
+constexpr int kKeys = 16;  // of a warp's step
 constexpr int kMaxDepth = 8;
-constexpr size_t kSmem = 232448;
+constexpr size_t kSmem = 232448 - 1024;
 
-using FewWalk = Walk<Shape<kRows, kTile, 1, 1, 1>>;
+// Warps of a CTA: 8-bit keys take more instructions a byte, and up to 8 rows leave the
+// registers for 16 warps.
+template <bool E4M3, int NT>
+constexpr int kWarpsOf = E4M3 && NT == 1 ? 16 : 8;
 
 __host__ __device__ constexpr int row_bytes(bool e4m3, int dp) { return e4m3 ? dp : 2 * dp; }
 // a step's keys and values, and their scales
 __host__ __device__ constexpr int stage_bytes(bool e4m3, int dp) {
   return 2 * kKeys * row_bytes(e4m3, dp) + (e4m3 ? 2 * kKeys * 4 : 0);
 }
-__host__ __device__ constexpr int join_bytes(int dp) { return 4 * kRows * dp * 4; }
-constexpr int kMiscBytes = 2 * kWarps * kRows * 4 + kScratchWords * 8;
+// 64 rows of sums: of 8 warps with 8 rows, or 4 with 16 (twice, where there are more)
+__host__ __device__ constexpr int join_bytes(int dp) { return 64 * dp * 4; }
+constexpr int kStatBytes = 2 * 64 * 4;
+constexpr int kMiscBytes = kStatBytes + kScratchWords * 8;
 
 __device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16u : 0u) : "memory");
+}
+// Of an 8 x 8 matrix of 16-bit values, (row g, columns 2 c and 2 c + 1) a lane: the
+// transposed one.
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 
 // Where the 16-byte pieces of a key or value row lie, so that a warp's reads fall into
@@ -69,19 +81,21 @@ __device__ __forceinline__ float f32_of(uint16_t v, bool f16) {
   return f16 ? __half2float(__ushort_as_half(v)) : __uint_as_float(static_cast<uint32_t>(v) << 16);
 }
 
-// F16: the products' type (8-bit caches: always), else bf16
-template <bool E4M3, bool F16, int DP>
-__global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnArgs a, const int depth) {
+// F16: the products' type (8-bit caches: always), else bf16.  NT: column tiles of 8 rows.
+template <bool E4M3, bool F16, int DP, int NT>
+__global__ void __launch_bounds__(32 * kWarpsOf<E4M3, NT>, 1) attention_few_kernel(const AttnArgs a, const int depth) {
   extern __shared__ __align__(128) uint8_t few_smem[];
+  constexpr int kWarps = kWarpsOf<E4M3, NT>, kThreads = 32 * kWarps, kTile = kKeys * kWarps, kRows = 8 * NT;
   constexpr int kRow = row_bytes(E4M3, DP), kPieces = kRow / 16, kStage = stage_bytes(E4M3, DP);
   constexpr int kPerLoad = 32 / kPieces;  // keys that a load of the warp covers
-  constexpr int kTiles = DP / 8;          // column tiles of the output
+  constexpr int MT = DP / 16;             // row tiles of the output: 16 places of the head
   constexpr int W = DP / 8;               // 8-bit: adjacent values a lane reads of a row
+  using FewWalk = Walk<Shape<kRows, kTile, 1, 1, 1>>;
   __shared__ int last;
-  float* join = reinterpret_cast<float*>(few_smem);  // [4 or 8][rows][DP]
-  float* ms = join + join_bytes(DP) / 4;             // [warp][row]
-  float* ls = ms + kWarps * kRows;
-  int64_t* scratch = reinterpret_cast<int64_t*>(ls + kWarps * kRows);
+  float* join = reinterpret_cast<float*>(few_smem);  // [buffer][row][DP]
+  float* ms = join + join_bytes(DP) / 4;             // [buffer][row]
+  float* ls = ms + 64;
+  int64_t* scratch = reinterpret_cast<int64_t*>(ls + 64);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const uint32_t ring = smem_u32(few_smem) + static_cast<uint32_t>((join_bytes(DP) + kMiscBytes + 127) / 128 * 128) +
                         static_cast<uint32_t>(warp * depth * kStage);
@@ -114,18 +128,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnAr
         const int64_t place = paged ? (key0 & page_mask) : static_cast<int64_t>(iss.s.row0 + key0);
         const int64_t from = good ? page : 0;
         constexpr int64_t size = E4M3 ? 1 : 2;
-        const uint8_t* k = a.kv.k + size * (from * a.kv.k_page + place * a.kv.k_token + iss.h * a.kv.k_head);
-        const uint8_t* v = a.kv.v + size * (from * a.kv.v_page + place * a.kv.v_token + iss.h * a.kv.v_head);
+        const uint8_t* k = a.kv.k + size * (from * a.kv.k_page + (place + my_key) * a.kv.k_token + iss.h * a.kv.k_head) + 16 * my_piece;
+        const uint8_t* v = a.kv.v + size * (from * a.kv.v_page + (place + my_key) * a.kv.v_token + iss.h * a.kv.v_head) + 16 * my_piece;
+        const int64_t k_step = size * kPerLoad * a.kv.k_token, v_step = size * kPerLoad * a.kv.v_token;
+        const int there = good && in_head ? iss.s.L - key0 - my_key : 0;  // keys of this lane's column of loads
 #pragma unroll
         for (int i = 0; i < kKeys / kPerLoad; ++i) {
           const int key = i * kPerLoad + my_key;
-          const bool there = good && in_head && key0 + key < iss.s.L;
-          const int64_t kt = there ? size * key * a.kv.k_token + 16 * my_piece : 0;
-          const int64_t vt = there ? size * key * a.kv.v_token + 16 * my_piece : 0;
-          cp_async16_if(dst + static_cast<uint32_t>(key * kRow + 16 * k_piece<E4M3, DP>(key, my_piece)),
-                        there ? k + kt : a.kv.k, there);
+          const bool in = i * kPerLoad < there;
+          cp_async16_if(dst + static_cast<uint32_t>(key * kRow + 16 * k_piece<E4M3, DP>(key, my_piece)), in ? k + i * k_step : a.kv.k, in);
           cp_async16_if(dst + static_cast<uint32_t>((kKeys + key) * kRow + 16 * v_piece<E4M3, DP>(key, my_piece)),
-                        there ? v + vt : a.kv.v, there);
+                        in ? v + i * v_step : a.kv.v, in);
         }
         if (E4M3 && lane < 8) {
           const float* s = lane < 4 ? a.kv.k_scale : a.kv.v_scale;
@@ -144,31 +157,32 @@ __global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnAr
   int slot = 0;
   bool going = true;
   while (going) {
-    // ---- an item: its rows g and g + 8
+    // ---- an item.  As fragments of the first product a lane holds row g (of each
+    // tile), everywhere else rows 2 c and 2 c + 1.
     const Seq s = cur.s;
     const int live = min(s.n * a.G - cur.r * kRows, kRows);
-    uint4 qf[2][DP / 32];  // of row g + 8 i
-    int limit[2];          // the last key that the row sees
-    float factor[2];
+    uint4 qf[NT][DP / 32];
+    int limit[NT][2];  // the last key that the row sees
+    float factor[NT][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const bool there = g + 8 * i < live;
-      const int R = cur.r * kRows + (there ? g + 8 * i : 0);
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool there = 8 * nt + g < live;
+      const int R = cur.r * kRows + (there ? 8 * nt + g : 0);
       const int token = divided(R, a.G), head = cur.h * a.G + R - token * a.G;
-      limit[i] = there ? s.past + token : -1;
-      factor[i] = a.scale_log2;
+      const int sees = there ? s.past + token : -1;
+      float f = a.scale_log2;
       const uint16_t* q = a.q + (s.row0 + token) * a.q_stride + static_cast<int64_t>(head) * a.D;
 #pragma unroll
       for (int j = 0; j < DP / 32; ++j) {
         // 16-bit: 8 values at 32 j + 8 c; 8-bit: of 16 values at 64 (j / 2) + 16 c the half j % 2
         const int d = E4M3 ? 64 * (j >> 1) + 16 * c + 8 * (j & 1) : 32 * j + 8 * c;
-        qf[i][j] = there && d < a.D ? *reinterpret_cast<const uint4*>(q + d) : make_uint4(0, 0, 0, 0);
+        qf[nt][j] = there && d < a.D ? *reinterpret_cast<const uint4*>(q + d) : make_uint4(0, 0, 0, 0);
       }
       if (E4M3) {
         float amax = 0.f;
 #pragma unroll
         for (int j = 0; j < DP / 32; ++j) {
-          const uint32_t w[4] = {qf[i][j].x, qf[i][j].y, qf[i][j].z, qf[i][j].w};
+          const uint32_t w[4] = {qf[nt][j].x, qf[nt][j].y, qf[nt][j].z, qf[nt][j].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             amax = fmaxf(amax, fmaxf(fabsf(f32_of(static_cast<uint16_t>(w[e]), a.f16)),
@@ -180,24 +194,38 @@ __global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnAr
         const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100), 126);
         const bool scaled = amax > 0.f && amax < INFINITY;
         const float up = scaled ? __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23) : 1.f;
-        factor[i] = scaled ? factor[i] * __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23) : factor[i];
+        if (scaled) f *= __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
 #pragma unroll
         for (int j = 0; j < DP / 32; ++j) {
-          uint32_t* w = &qf[i][j].x;
+          uint32_t* w = &qf[nt][j].x;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             w[k] = pack_half(f32_of(static_cast<uint16_t>(w[k]), a.f16) * up,
                              f32_of(static_cast<uint16_t>(w[k] >> 16), a.f16) * up);
         }
       }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {  // (row 2 c + i is row g of lane 4 (2 c + i))
+        limit[nt][i] = __shfl_sync(0xffffffffu, sees, 4 * (2 * c + i));
+        factor[nt][i] = __shfl_sync(0xffffffffu, f, 4 * (2 * c + i));
+      }
     }
     const int least = s.past + divided(cur.r * kRows, a.G);  // of all rows' limits
-    float o[kTiles][4];
+    float o[MT][NT][4];  // places (16-bit: 16 j + g, + 8; 8-bit: W g + 2 j, + 1) of rows 2 c, 2 c + 1
 #pragma unroll
-    for (int j = 0; j < kTiles; ++j)
+    for (int j = 0; j < MT; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[j][nt][e] = 0.f;
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        m[nt][i] = -INFINITY;
+        l[nt][i] = 0.f;
+      }
     float unit = 0.f, per_unit = 0.f;  // 8-bit: what the values' scales are relative to, and its inverse
 
     for (int t = cur.t; t < cur.end; ++t) {
@@ -208,78 +236,85 @@ __global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnAr
       const uint32_t src = ring + static_cast<uint32_t>(slot * kStage);
       if (++slot == depth) slot = 0;
       if (key0 >= s.L) continue;
-      // ---- scores of 16 keys
-      float x[2][4] = {};
+      // ---- scores of keys g and g + 8
+      float x[NT][4];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const uint32_t row = src + static_cast<uint32_t>((8 * nt + g) * kRow);
-        if (!E4M3) {
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < DP / 32; ++j) {
-            const uint4 b = lds128(row + 16u * static_cast<uint32_t>(k_piece<E4M3, DP>(g, 4 * j + c)));
-            mma16816<F16>(x[nt], qf[0][j].x, qf[1][j].x, qf[0][j].y, qf[1][j].y, b.x, b.y);
-            mma16816<F16>(x[nt], qf[0][j].z, qf[1][j].z, qf[0][j].w, qf[1][j].w, b.z, b.w);
+        for (int e = 0; e < 4; ++e) x[nt][e] = 0.f;
+      const uint32_t row_a = src + static_cast<uint32_t>(g * kRow), row_b = row_a + static_cast<uint32_t>(8 * kRow);
+      if (!E4M3) {
+#pragma unroll
+        for (int j = 0; j < DP / 32; ++j) {
+          const uint32_t at = 16u * static_cast<uint32_t>(k_piece<E4M3, DP>(g, 4 * j + c));
+          const uint4 u = lds128(row_a + at), v = lds128(row_b + at);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816<F16>(x[nt], u.x, v.x, u.y, v.y, qf[nt][j].x, qf[nt][j].y);
+            mma16816<F16>(x[nt], u.z, v.z, u.w, v.w, qf[nt][j].z, qf[nt][j].w);
           }
-        } else {
+        }
+      } else {
 #pragma unroll
-          for (int j = 0; j < DP / 64; ++j) {
-            const uint4 b = lds128(row + 16u * static_cast<uint32_t>(k_piece<E4M3, DP>(g, 4 * j + c)));
+        for (int j = 0; j < DP / 64; ++j) {
+          const uint32_t at = 16u * static_cast<uint32_t>(k_piece<E4M3, DP>(g, 4 * j + c));
+          const uint4 u = lds128(row_a + at), v = lds128(row_b + at);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t w = word(b, i);
-              const uint4 &u = qf[0][2 * j + (i >> 1)], &v = qf[1][2 * j + (i >> 1)];
-              mma16816<true>(x[nt], word(u, 2 * (i & 1)), word(v, 2 * (i & 1)), word(u, 2 * (i & 1) + 1),
-                             word(v, 2 * (i & 1) + 1), e4m3x2_f16x2(w & 0xFFFFu), e4m3x2_f16x2(w >> 16));
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t p = word(u, i), q = word(v, i);
+            const uint32_t a0 = e4m3x2_f16x2(p & 0xFFFFu), a1 = e4m3x2_f16x2(q & 0xFFFFu), a2 = e4m3x2_f16x2(p >> 16),
+                           a3 = e4m3x2_f16x2(q >> 16);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint4& b = qf[nt][2 * j + (i >> 1)];
+              mma16816<true>(x[nt], a0, a1, a2, a3, word(b, 2 * (i & 1)), word(b, 2 * (i & 1) + 1));
             }
           }
         }
       }
-      float vs[4] = {1.f, 1.f, 1.f, 1.f};  // 8-bit: scales of this lane's keys, 2 c, 2 c + 1, 2 c + 8, 2 c + 9
-      float ks[4] = {1.f, 1.f, 1.f, 1.f};
+      float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};  // 8-bit: scales of keys g, g + 8
       if (E4M3) {
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const uint2 u = lds64(src + static_cast<uint32_t>(2 * kKeys * kRow + 4 * (8 * nt + 2 * c)));
-          const uint2 v = lds64(src + static_cast<uint32_t>(2 * kKeys * kRow + 4 * (kKeys + 8 * nt + 2 * c)));
-          ks[2 * nt] = __uint_as_float(u.x);
-          ks[2 * nt + 1] = __uint_as_float(u.y);
-          vs[2 * nt] = __uint_as_float(v.x);
-          vs[2 * nt + 1] = __uint_as_float(v.y);
+        for (int i = 0; i < 2; ++i) {
+          uint32_t u, v;
+          const uint32_t at = src + static_cast<uint32_t>(2 * kKeys * kRow + 4 * (8 * i + g));
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(u) : "r"(at) : "memory");
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at + 4 * kKeys) : "memory");
+          ks[i] = __uint_as_float(u);
+          vs[i] = __uint_as_float(v);
         }
       }
       // ---- maxima
-      float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = e >> 1, key = key0 + 8 * nt + 2 * c + (e & 1);
-          float z = x[nt][e] * factor[i];
-          if (E4M3) z *= ks[2 * nt + (e & 1)];
-          x[nt][e] = key <= limit[i] ? z : -INFINITY;
-          top[i] = fmaxf(top[i], x[nt][e]);
-        }
       float grown = 0.f;  // 8-bit: the unit's new value
       if (E4M3) {
         float most = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (key0 + 8 * (e >> 1) + 2 * c + (e & 1) < s.L && fabsf(vs[e]) < INFINITY) most = fmaxf(most, fabsf(vs[e]));
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        for (int i = 0; i < 2; ++i)
+          if (key0 + 8 * i + g < s.L && fabsf(vs[i]) < INFINITY) most = fmaxf(most, fabsf(vs[i]));
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, w));
         if (most >= unit) grown = __uint_as_float(min((__float_as_uint(most) & 0x7F800000u) + 0x00800000u, 0x7F000000u));
       }
-      float keep[2];
+      float keep[NT][2];
       bool rescale = false;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
-        const float next = fmaxf(m[i], top[i]);
-        keep[i] = exp2_fast(m[i] - reference(next));
-        rescale = rescale || next != m[i];
-        m[i] = next;
-      }
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float z = x[nt][2 * k + i] * factor[nt][i];
+            if (E4M3) z *= ks[k];
+            x[nt][2 * k + i] = key0 + 8 * k + g <= limit[nt][i] ? z : -INFINITY;
+          }
+          float top = fmaxf(x[nt][i], x[nt][2 + i]);
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+          const float next = fmaxf(m[nt][i], top);
+          keep[nt][i] = exp2_fast(m[nt][i] - reference(next));
+          rescale = rescale || next != m[nt][i];
+          m[nt][i] = next;
+        }
       float shrink = 1.f;
       if (E4M3 && grown > unit) {
         shrink = unit / grown;
@@ -289,30 +324,34 @@ __global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnAr
       }
       if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          l[i] *= keep[i];
-          keep[i] *= shrink;
-        }
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j)
+          for (int i = 0; i < 2; ++i) {
+            l[nt][i] *= keep[nt][i];
+            keep[nt][i] *= shrink;
+          }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[j][e] *= keep[e >> 1];
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[j][nt][e] *= keep[nt][e & 1];
       }
       // ---- weights
-      uint32_t p[2][2];  // [key tile][row]
+      uint32_t p[NT][2];  // keys 2 c, 2 c + 1 (+ 8) of row g
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float r = reference(m[i]);
-          float u = exp2_fast(x[nt][2 * i] - r), v = exp2_fast(x[nt][2 * i + 1] - r);
-          l[i] += u + v;
+        for (int k = 0; k < 2; ++k) {
+          float u = exp2_fast(x[nt][2 * k] - reference(m[nt][0])), v = exp2_fast(x[nt][2 * k + 1] - reference(m[nt][1]));
+          l[nt][0] += u;
+          l[nt][1] += v;
           if (E4M3) {  // (a masked key's weight is zero whatever its scale is)
-            const int key = key0 + 8 * nt + 2 * c;
-            u = key <= limit[i] ? u * (vs[2 * nt] * per_unit) : 0.f;
-            v = key + 1 <= limit[i] ? v * (vs[2 * nt + 1] * per_unit) : 0.f;
+            const float f = vs[k] * per_unit;
+            u = key0 + 8 * k + g <= limit[nt][0] ? u * f : 0.f;
+            v = key0 + 8 * k + g <= limit[nt][1] ? v * f : 0.f;
           }
-          p[nt][i] = F16 ? pack_half(u, v) : pack_bf16x2(u, v);
+          p[nt][k] = transposed(F16 ? pack_half(u, v) : pack_bf16x2(u, v));
         }
       // ---- their sum of values
       const bool partly = key0 + kKeys - 1 > least;  // some row does not see some key
@@ -332,14 +371,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnAr
         }
         return w;
       };
-      if (!E4M3) {
-        const int row = (lane >> 3 & 1) * 8 + (lane & 7);
+      auto add = [&](int j, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+        if (partly) a0 = tame(a0), a1 = tame(a1), a2 = tame(a2), a3 = tame(a3);
 #pragma unroll
-        for (int j = 0; j < kTiles / 2; ++j) {
-          uint4 b = ldmatrix_x4_trans(values + static_cast<uint32_t>(row * kRow + 16 * v_piece<E4M3, DP>(row, 2 * j + (lane >> 4))));
-          if (partly) b = make_uint4(tame(b.x), tame(b.y), tame(b.z), tame(b.w));
-          mma16816<F16>(o[2 * j], p[0][0], p[0][1], p[1][0], p[1][1], b.x, b.y);
-          mma16816<F16>(o[2 * j + 1], p[0][0], p[0][1], p[1][0], p[1][1], b.z, b.w);
+        for (int nt = 0; nt < NT; ++nt) mma16816<F16>(o[j][nt], a0, a1, a2, a3, p[nt][0], p[nt][1]);
+      };
+      if (!E4M3) {
+        // matrices: places 0-7 and 8-15 of keys 0-7, then of keys 8-15
+        const int key = (lane >> 4) * 8 + (lane & 7);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          const uint4 b = ldmatrix_x4_trans(
+              values + static_cast<uint32_t>(key * kRow + 16 * v_piece<E4M3, DP>(key, 2 * j + (lane >> 3 & 1))));
+          add(j, b.x, b.y, b.z, b.w);
         }
       } else {
         uint32_t code[4][W / 4];  // rows 2 c, 2 c + 1, 2 c + 8, 2 c + 9 at W g
@@ -357,38 +401,30 @@ __global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnAr
           }
         }
 #pragma unroll
-        for (int i = 0; i < W / 4; ++i) {
-          const uint32_t lo[2] = {__byte_perm(code[0][i], code[1][i], 0x5140), __byte_perm(code[0][i], code[1][i], 0x7362)};
-          const uint32_t hi[2] = {__byte_perm(code[2][i], code[3][i], 0x5140), __byte_perm(code[2][i], code[3][i], 0x7362)};
+        for (int i = 0; i < W / 4; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t b0 = e4m3x2_f16x2(e & 1 ? lo[e >> 1] >> 16 : lo[e >> 1] & 0xFFFFu);
-            uint32_t b1 = e4m3x2_f16x2(e & 1 ? hi[e >> 1] >> 16 : hi[e >> 1] & 0xFFFFu);
-            if (partly) {
-              b0 = tame(b0);
-              b1 = tame(b1);
-            }
-            mma16816<true>(o[4 * i + e], p[0][0], p[0][1], p[1][0], p[1][1], b0, b1);
+          for (int e = 0; e < 2; ++e) {  // places W g + 4 i + 2 e and the next
+            const uint32_t sel = e == 0 ? 0x5140 : 0x7362;
+            const uint32_t lo = __byte_perm(code[0][i], code[1][i], sel), hi = __byte_perm(code[2][i], code[3][i], sel);
+            add(2 * i + e, e4m3x2_f16x2(lo & 0xFFFFu), e4m3x2_f16x2(lo >> 16), e4m3x2_f16x2(hi & 0xFFFFu), e4m3x2_f16x2(hi >> 16));
           }
-        }
       }
       if (partly && __any_sync(0xffffffffu, odd)) {
 #pragma unroll 1
         for (int key = 0; key < kKeys; ++key) {
 #pragma unroll
-          for (int j = 0; j < kTiles; ++j)
+          for (int j = 0; j < MT; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int d = E4M3 ? W * (2 * c + e) + j : 8 * j + 2 * c + e;
+              const int d = E4M3 ? W * g + 2 * j + e : 16 * j + 8 * e + g;
               float v;
+              uint16_t q;
               if (E4M3) {
                 const uint32_t at = values + static_cast<uint32_t>(
                     DP == 128 ? key * kRow + 16 * v_piece<E4M3, DP>(key, d >> 4) + (d & 15) : key * kRow + d);
-                uint16_t q;
                 asm volatile("ld.shared.u8 %0, [%1];" : "=h"(q) : "r"(at) : "memory");
                 v = (q & 0x7F) == 0x7F ? NAN : 0.f;
               } else {
-                uint16_t q;
                 asm volatile("ld.shared.u16 %0, [%1];"
                              : "=h"(q)
                              : "r"(values + static_cast<uint32_t>(key * kRow + 16 * v_piece<E4M3, DP>(key, d >> 3) + 2 * (d & 7)))
@@ -396,8 +432,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnAr
                 v = f32_of(q, F16);
               }
               if (!(fabsf(v) < INFINITY)) {
-                if (key0 + key <= limit[0]) o[j][e] += v;
-                if (key0 + key <= limit[1]) o[j][2 + e] += v;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int i = 0; i < 2; ++i)
+                    if (key0 + key <= limit[nt][i]) o[j][nt][2 * e + i] += v;
               }
             }
         }
@@ -406,82 +445,91 @@ __global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnAr
 
     // ---- the warps' sums joined
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-    }
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], w);
     if (E4M3) {
 #pragma unroll
-      for (int j = 0; j < kTiles; ++j)
+      for (int j = 0; j < MT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[j][e] *= unit;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[j][nt][e] *= unit;
     }
-    auto column = [&](int j, int e) { return E4M3 ? W * (2 * c + e) + j : 8 * j + 2 * c + e; };
-    // eight columns of a row stay adjacent; rows lie in different banks
-    auto place = [&](int buf, int row, int d, int per) { return join + (buf * per + row) * DP + (d ^ ((row & 3) << 3)); };
-    auto put = [&](int buf, int per) {
+    constexpr int kBufs = 64 / kRows;          // buffers of kRows rows
+    constexpr int kTurns = kWarps / kBufs;     // 1, or 2: the second half of the warps first
+    static_assert(kTurns == 1 || kTurns == 2, "each warp has a buffer, or half of them");
+    // eight places of a row stay adjacent; the rows of four lanes lie in different banks
+    auto at = [&](int buf, int row, int d) { return join + (buf * kRows + row) * DP + (d ^ ((row >> 1 & 3) << 3)); };
+    auto put = [&](int buf) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = g + 8 * i;
-        if (row < live) {
-#pragma unroll
-          for (int j = 0; j < kTiles; ++j) {
-            if (E4M3) {
-              *place(buf, row, column(j, 0), per) = o[j][2 * i];
-              *place(buf, row, column(j, 1), per) = o[j][2 * i + 1];
-            } else {
-              *reinterpret_cast<float2*>(place(buf, row, column(j, 0), per)) = make_float2(o[j][2 * i], o[j][2 * i + 1]);
-            }
-          }
-          if (c == 0) {
-            ms[buf * kRows + row] = m[i];
-            ls[buf * kRows + row] = l[i];
-          }
-        }
-      }
-    };
-    const bool two = live > 8;  // four buffers of 16 rows, or eight of 8
-    const int per = two ? 16 : 8, bufs = two ? 4 : 8;
-    __syncthreads();  // the last item's sums have been read
-    if (two) {
-      if (warp >= 4) put(warp - 4, per);
-      __syncthreads();
-      if (warp < 4) {
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int row = g + 8 * i;
+          const int row = 8 * nt + 2 * c + i;
           if (row < live) {
-            const float om = ms[warp * kRows + row], both = fmaxf(m[i], om), r = reference(both);
-            const float mine = exp2_fast(m[i] - r), other = exp2_fast(om - r);
-            l[i] = l[i] * mine + ls[warp * kRows + row] * other;
-            m[i] = both;
 #pragma unroll
-            for (int j = 0; j < kTiles; ++j)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                o[j][2 * i + e] = o[j][2 * i + e] * mine + *place(warp, row, column(j, e), per) * other;
+            for (int j = 0; j < MT; ++j) {
+              if (E4M3) {
+                *reinterpret_cast<float2*>(at(buf, row, W * g + 2 * j)) = make_float2(o[j][nt][i], o[j][nt][2 + i]);
+              } else {
+                *at(buf, row, 16 * j + g) = o[j][nt][i];
+                *at(buf, row, 16 * j + 8 + g) = o[j][nt][2 + i];
+              }
+            }
+            if (g == 0) {
+              ms[buf * kRows + row] = m[nt][i];
+              ls[buf * kRows + row] = l[nt][i];
+            }
           }
         }
+    };
+    __syncthreads();  // the last item's sums have been read
+    if (kTurns == 2) {
+      if (warp >= kBufs) put(warp - kBufs);
+      __syncthreads();
+      if (warp < kBufs) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int row = 8 * nt + 2 * c + i;
+            if (row < live) {
+              const float om = ms[warp * kRows + row], both = fmaxf(m[nt][i], om), r = reference(both);
+              const float mine = exp2_fast(m[nt][i] - r), other = exp2_fast(om - r);
+              l[nt][i] = l[nt][i] * mine + ls[warp * kRows + row] * other;
+              m[nt][i] = both;
+#pragma unroll
+              for (int j = 0; j < MT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int d = E4M3 ? W * g + 2 * j + e : 16 * j + 8 * e + g;
+                  o[j][nt][2 * e + i] = o[j][nt][2 * e + i] * mine + *at(warp, row, d) * other;
+                }
+            }
+          }
       }
       __syncthreads();
-      if (warp < 4) put(warp, per);
-    } else {
-      put(warp, per);
     }
+    if (warp < kBufs) put(warp);
     __syncthreads();
-    constexpr int kChunks = DP / 8;  // threads of a row, eight columns each
+    constexpr int kChunks = DP / 8;  // threads of a row, eight places each
     const int row = tid / kChunks, d0 = 8 * (tid % kChunks);
     const bool mine = row < live;
     float v[8], top = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 0.f;
     if (mine) {
-      for (int i = 0; i < bufs; ++i) top = fmaxf(top, ms[i * kRows + row]);
+#pragma unroll
+      for (int i = 0; i < kBufs; ++i) top = fmaxf(top, ms[i * kRows + row]);
       const float r = reference(top);
-      for (int i = 0; i < bufs; ++i) {
+#pragma unroll
+      for (int i = 0; i < kBufs; ++i) {
         const float f = exp2_fast(ms[i * kRows + row] - r);
         sum += ls[i * kRows + row] * f;
-        const float* from = place(i, row, d0, per);
+        const float* from = at(i, row, d0);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = fmaf(from[j], f, v[j]);
       }
@@ -490,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnAr
     if (cur.end - cur.t < cur.len) {
       // the item lies in several runs: the last one to finish joins them
       const int first = cur.first_cta(), pieces = cur.cta_count();
-      constexpr size_t kPiece = attn_piece_bytes(kRows, DP) / 4;
+      constexpr size_t kPiece = attn_piece_bytes(kMostRows, DP) / 4;
       auto piece = [&](int i) { return a.partial + (2 * (first + i) + (i == 0 ? 1 : 0)) * kPiece; };
       float* to = piece(static_cast<int>(blockIdx.x) - first);
       if (mine) {
@@ -498,8 +546,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnAr
         for (int j = 0; j < 2; ++j)
           __stcg(reinterpret_cast<float4*>(to + row * DP + d0) + j, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
         if (d0 == 0) {
-          __stcg(to + kRows * DP + 2 * row, top);
-          __stcg(to + kRows * DP + 2 * row + 1, sum);
+          __stcg(to + kMostRows * DP + 2 * row, top);
+          __stcg(to + kMostRows * DP + 2 * row + 1, sum);
         }
       }
       __threadfence();
@@ -513,24 +561,28 @@ __global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnAr
       write = last != 0;
       if (write && mine) {
         top = -INFINITY;
-        for (int i = 0; i < pieces; ++i) top = fmaxf(top, __ldcg(piece(i) + kRows * DP + 2 * row));
+#pragma unroll 8
+        for (int i = 0; i < pieces; ++i) top = fmaxf(top, __ldcg(piece(i) + kMostRows * DP + 2 * row));
         const float r = reference(top);
         sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = 0.f;
-#pragma unroll 2
+#pragma unroll 8
         for (int i = 0; i < pieces; ++i) {
           const float* from = piece(i);
-          const float f = exp2_fast(__ldcg(from + kRows * DP + 2 * row) - r);
-          sum = fmaf(__ldcg(from + kRows * DP + 2 * row + 1), f, sum);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float4 u = __ldcg(reinterpret_cast<const float4*>(from + row * DP + d0) + j);
-            v[4 * j] = fmaf(u.x, f, v[4 * j]);
-            v[4 * j + 1] = fmaf(u.y, f, v[4 * j + 1]);
-            v[4 * j + 2] = fmaf(u.z, f, v[4 * j + 2]);
-            v[4 * j + 3] = fmaf(u.w, f, v[4 * j + 3]);
-          }
+          const float2 stat = __ldcg(reinterpret_cast<const float2*>(from + kMostRows * DP + 2 * row));
+          const float4 u = __ldcg(reinterpret_cast<const float4*>(from + row * DP + d0));
+          const float4 z = __ldcg(reinterpret_cast<const float4*>(from + row * DP + d0) + 1);
+          const float f = exp2_fast(stat.x - r);
+          sum = fmaf(stat.y, f, sum);
+          v[0] = fmaf(u.x, f, v[0]);
+          v[1] = fmaf(u.y, f, v[1]);
+          v[2] = fmaf(u.z, f, v[2]);
+          v[3] = fmaf(u.w, f, v[3]);
+          v[4] = fmaf(z.x, f, v[4]);
+          v[5] = fmaf(z.y, f, v[5]);
+          v[6] = fmaf(z.z, f, v[6]);
+          v[7] = fmaf(z.w, f, v[7]);
         }
       }
     }
@@ -552,35 +604,41 @@ __global__ void __launch_bounds__(kThreads, 1) attention_few_kernel(const AttnAr
   }
 }
 
-template <bool E4M3, bool F16, int DP>
+template <bool E4M3, bool F16, int DP, int NT>
 cudaError_t launch(const AttnArgs& a, int sms, cudaStream_t s) {
-  auto kernel = attention_few_kernel<E4M3, F16, DP>;
+  auto kernel = attention_few_kernel<E4M3, F16, DP, NT>;
+  constexpr int kWarps = kWarpsOf<E4M3, NT>;
   static int configured[64] = {};
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev < 0 || dev >= 64 || configured[dev] == 0) {
-    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem) - 1024);
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
     if (err != cudaSuccess) return err;
     if (dev >= 0 && dev < 64) configured[dev] = 1;
   }
   const size_t fixed = (join_bytes(DP) + kMiscBytes + 127) / 128 * 128;
-  const int most = static_cast<int>((kSmem - 1024 - fixed) / (kWarps * stage_bytes(E4M3, DP)));
+  const int most = static_cast<int>((kSmem - fixed) / (kWarps * stage_bytes(E4M3, DP)));
   const int depth = most < kMaxDepth ? most : kMaxDepth;
-  return launch_pdl(kernel, dim3(sms < kAttnMaxCtas ? sms : kAttnMaxCtas), dim3(kThreads),
+  return launch_pdl(kernel, dim3(sms < kAttnMaxCtas ? sms : kAttnMaxCtas), dim3(32 * kWarps),
                     fixed + static_cast<size_t>(kWarps) * depth * stage_bytes(E4M3, DP), s, a, depth);
 }
 
+template <bool E4M3, bool F16, int DP>
+cudaError_t launch(const AttnArgs& a, int rows, int sms, cudaStream_t s) {
+  return rows <= 8 ? launch<E4M3, F16, DP, 1>(a, sms, s) : launch<E4M3, F16, DP, 2>(a, sms, s);
+}
+
 template <bool E4M3, bool F16>
-cudaError_t launch(const AttnArgs& a, int sms, cudaStream_t s) {
-  return a.D <= 64 ? launch<E4M3, F16, 64>(a, sms, s) : launch<E4M3, F16, 128>(a, sms, s);
+cudaError_t launch(const AttnArgs& a, int rows, int sms, cudaStream_t s) {
+  return a.D <= 64 ? launch<E4M3, F16, 64>(a, rows, sms, s) : launch<E4M3, F16, 128>(a, rows, sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_attention_few(const AttnArgs& a, int sms, cudaStream_t s) {
-  if (a.e4m3) return launch<true, true>(a, sms, s);
-  return a.f16 ? launch<false, true>(a, sms, s) : launch<false, false>(a, sms, s);
+cudaError_t launch_attention_few(const AttnArgs& a, int rows, int sms, cudaStream_t s) {
+  if (a.e4m3) return launch<true, true>(a, rows, sms, s);
+  return a.f16 ? launch<false, true>(a, rows, sms, s) : launch<false, false>(a, rows, sms, s);
 }
 
 }  // namespace moe

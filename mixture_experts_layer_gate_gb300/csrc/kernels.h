@@ -343,8 +343,8 @@ constexpr size_t kAttnTicketBytes = 1024;
 constexpr int kAttnFewRows = 16;
 // bytes of a piece's sums, maxima and totals
 constexpr size_t attn_piece_bytes(int rows, int D) { return static_cast<size_t>(rows) * ((D <= 64 ? 64 : 128) + 2) * 4; }
-// Rows of a key head's queries up to kAttnFewRows, and more of them (any number is right in both).
-cudaError_t launch_attention_few(const AttnArgs& a, int sms, cudaStream_t s);
+// `rows` of a key head's queries, up to kAttnFewRows, and more of them (any number is right in both).
+cudaError_t launch_attention_few(const AttnArgs& a, int rows, int sms, cudaStream_t s);
 constexpr int kAttnRows = 256;
 cudaError_t launch_attention(const AttnArgs& a, int sms, cudaStream_t s);
 
