@@ -4,10 +4,11 @@
 // 8-bit scale all come from registers).  Bound by memory.
 //
 // A head is held by LANES lanes of a warp, 8 values (16 bytes) each, so its mean
-// and its largest value are a few shuffles; a CTA takes heads of one token, whose
-// angles it computes once.  An angle is a fraction of a turn in 64 bits,
-// position * turns mod 2^64, which is exact, where position * frequency in float
-// is off by 0.06 radians at position 10^6.
+// and its largest value are a few shuffles; a warp takes some of a token's heads,
+// kAhead loads at a time, and computes the token's angles once, each lane some pairs,
+// handed on by shuffles (no shared memory, no barrier).  An angle is a fraction of a
+// turn in 64 bits, position * turns mod 2^64, which is exact, where position *
+// frequency in float is off by 0.06 radians at position 10^6.
 #include <algorithm>
 
 #include "common.cuh"
@@ -17,220 +18,297 @@ namespace moe {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kMaxPairs = 128;  // D <= 256
+constexpr int kAhead = 4;        // loads of a lane in flight
+constexpr int kWarpsPerSm = 48;
 
-template <typename T>
-__device__ __forceinline__ float2 two_f32(uint32_t v);
-template <>
-__device__ __forceinline__ float2 two_f32<__nv_bfloat16>(uint32_t v) {
-  return make_float2(bf16_lo(v), bf16_hi(v));
+// Eight values as four pairs of floats, which packed instructions take.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  return (static_cast<uint64_t>(__float_as_uint(b)) << 32) | __float_as_uint(a);
 }
-template <>
-__device__ __forceinline__ float2 two_f32<__half>(uint32_t v) {
-  return __half22float2(*reinterpret_cast<__half2*>(&v));
+__device__ __forceinline__ float lo(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
-template <typename T>
-__device__ __forceinline__ uint32_t two_from(float a, float b);
-template <>
-__device__ __forceinline__ uint32_t two_from<__nv_bfloat16>(float a, float b) {
-  return pack_bf16x2(a, b);
-}
-template <>
-__device__ __forceinline__ uint32_t two_from<__half>(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
-template <typename T>
-__device__ __forceinline__ void unpack8(const uint4& r, float (&x)[8]) {
+template <bool F16>
+__device__ __forceinline__ void unpack8(const uint4& r, uint64_t (&x)[4]) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 f = two_f32<T>(w[j]);
-    x[2 * j] = f.x;
-    x[2 * j + 1] = f.y;
+    if (F16) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+      x[j] = pair(f.x, f.y);
+    } else {
+      x[j] = pair(bf16_lo(w[j]), bf16_hi(w[j]));
+    }
   }
 }
-template <typename T>
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(two_from<T>(x[0], x[1]), two_from<T>(x[2], x[3]), two_from<T>(x[4], x[5]), two_from<T>(x[6], x[7]));
+template <bool F16>
+__device__ __forceinline__ uint4 pack8(const uint64_t (&x)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (F16) {
+      const __half2 h = __floats2half2_rn(lo(x[j]), hi(x[j]));
+      w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      w[j] = pack_bf16x2(lo(x[j]), hi(x[j]));
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // NaN wins, so that a head with one gets a NaN scale
 __device__ __forceinline__ float max_nan(float a, float b) { return (a > b || a != a) ? a : b; }
 
-template <typename T, int LANES>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
-  constexpr int kHeads = kRopeThreads / LANES;  // of a pass
-  __shared__ float2 turn[kMaxPairs];            // cos and sin, times the magnitude
+// A head's values as e4m3 codes with its scale; of the lanes of one head.
+template <int LANES>
+__device__ __forceinline__ void store_codes(const uint64_t (&x)[4], uint8_t* to, float* scale_to, int lane, bool live, bool first) {
+  float amax = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) amax = max_nan(amax, max_nan(fabsf(lo(x[j])), fabsf(hi(x[j]))));
+  // only the lanes of this head: others of the warp may have a query
+  const uint32_t members = LANES == 32 ? 0xffffffffu : ((1u << (LANES & 31)) - 1u) << (lane & ~(LANES - 1));
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(members, amax, o));
+  float scale = __fdiv_rn(amax, 448.0f);
+  if (scale == 0.f) scale = 1.0f;
+  if (!live) return;
+  if (first) *scale_to = scale;
+  uint32_t code[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) code[j] = f32x2_to_e4m3x2(__fdiv_rn(lo(x[j]), scale), __fdiv_rn(hi(x[j]), scale));
+  *reinterpret_cast<uint2*>(to) = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
+}
+
+template <bool F16, int LANES, bool NORM, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const RopeArgs a, const int groups) {
+  constexpr int kHeads = 32 / LANES;  // of a pass
+  constexpr int kPairs = LANES / 8;   // pairs whose angle a lane computes (D <= 8 LANES has 4 LANES pairs at most)
   __shared__ float spare[kRopeThreads / 32][32 * 9];
-  const int tid = threadIdx.x, lane = tid & 31, in_head = tid & (LANES - 1);
-  const int pairs = a.rot >> 1, chunks = a.D >> 3, heads = a.Hq + 2 * a.Hkv;
-  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x & 31, in_head = lane & (LANES - 1);
+  const int pairs = a.rot >> 1, chunks = a.D >> 3, D = a.D;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
+  const int64_t t = unit / groups;
+  if (t >= a.T) return;
+  const int group = static_cast<int>(unit - t * groups);
   const bool mine = in_head < chunks;
   const int e0 = in_head * 8;  // this lane's values
-  auto source = [&](int h) {   // of head h: queries, keys, values
-    const T* p = h < a.Hq            ? static_cast<const T*>(a.q) + t * a.q_stride + static_cast<int64_t>(h) * a.D
-                 : h < a.Hq + a.Hkv ? static_cast<const T*>(a.k) + t * a.k_stride + static_cast<int64_t>(h - a.Hq) * a.D
-                                    : static_cast<const T*>(a.v) + t * a.v_stride +
-                                          static_cast<int64_t>(h - a.Hq - a.Hkv) * a.D;
-    return reinterpret_cast<const uint4*>(p + e0);
-  };
-  // without a cache the value heads are nobody's
-  const int last = a.cache.k != nullptr ? heads : a.Hq + a.Hkv;
-  const int step = kHeads * gridDim.y;
-  int h = blockIdx.y * kHeads + tid / LANES;
+  const int turned = a.Hq + a.Hkv, step = kHeads * groups;
+  const int h_first = group * kHeads + lane / LANES;
+  // this lane's place in the token's rows (heads times D fit 32 bits)
+  const uint16_t* of_q = static_cast<const uint16_t*>(a.q) + t * a.q_stride + e0;
+  const uint16_t* of_k = static_cast<const uint16_t*>(a.k) + t * a.k_stride + e0 - a.Hq * D;
   pdl_wait();
   pdl_trigger();
-  uint4 next = mine && h < last ? *source(h) : make_uint4(0, 0, 0, 0);
+  uint4 raw[kAhead];
+  auto fetch = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i, h += step)
+      raw[i] = mine && h < turned ? *reinterpret_cast<const uint4*>((h < a.Hq ? of_q : of_k) + h * D) : make_uint4(0, 0, 0, 0);
+  };
+  fetch(h_first);
   int64_t slot = -1;
   if (a.cache.k != nullptr) {
     slot = a.slots[t];
     if (slot >= a.capacity) {
-      if (tid == 0 && blockIdx.y == 0) record_error(a.err, kErrBadIndex, static_cast<uint32_t>(t));
+      if (lane == 0 && group == 0) record_error(a.err, kErrBadIndex, static_cast<uint32_t>(t));
       slot = -1;
     }
   }
-  if (tid < pairs) {
-    const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(a.positions[t])) * a.turns[tid];
-    // the upper half as a signed fraction of a turn: within 2^-26 of a turn
-    const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
-    float s, c;
-    sincospif(half_turns, &s, &c);
-    turn[tid] = make_float2(c * a.magnitude, s * a.magnitude);
+  // the slot's keys and values, in bytes, and its place among the scales
+  const KvCache& cache = a.cache;
+  const int64_t page = slot < 0 ? 0 : slot >> a.page_shift, place = slot < 0 ? 0 : slot & ((1 << a.page_shift) - 1);
+  const int size = a.e4m3 ? 1 : 2;
+  const int64_t scale_at = ((page * a.Hkv) << a.page_shift) + place;
+  // cos and sin of this lane's values' pairs, times the magnitude
+  uint64_t co[4], si[4];
+  if (pairs > 0) {
+    const uint64_t position = static_cast<uint64_t>(static_cast<int64_t>(a.positions[t]));
+    float c[kPairs], s[kPairs];
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const int q = lane * kPairs + i;
+      const uint64_t phase = q < pairs ? position * a.turns[q] : 0;
+      // the upper half as a signed fraction of a turn: within 2^-26 of a turn
+      sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f, &s[i], &c[i]);
+      c[i] *= a.magnitude;
+      s[i] *= a.magnitude;
+    }
+    float co8[8], si8[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int e = e0 + j, q = INTERLEAVED ? e >> 1 : e < pairs ? e : e - pairs;
+      const int from = (q / kPairs) & 31;
+      co8[j] = si8[j] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const float u = __shfl_sync(0xffffffffu, c[i], from), v = __shfl_sync(0xffffffffu, s[i], from);
+        if (q % kPairs == i) {
+          co8[j] = u;
+          si8[j] = v;
+        }
+      }
+      if (INTERLEAVED ? (e & 1) == 0 : e < pairs) si8[j] = -si8[j];  // of the first of a pair
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      co[j] = pair(co8[2 * j], co8[2 * j + 1]);
+      si[j] = pair(si8[2 * j], si8[2 * j + 1]);
+    }
   }
-  __syncthreads();
+  const float per_d = 1.0f / static_cast<float>(D);
+  uint16_t* to_q = static_cast<uint16_t*>(a.q_out) + t * a.q_out_stride + e0;
+  uint16_t* to_k = a.k_out != nullptr ? static_cast<uint16_t*>(a.k_out) + t * a.k_out_stride + e0 - a.Hq * D : nullptr;
+  uint8_t* slot_k = cache.k + size * (page * cache.k_page + place * cache.k_token + e0);
 
-  // (every lane of a warp goes through the same number of passes)
-  for (int h0 = blockIdx.y * kHeads; h0 < last; h0 += step, h += step) {
-    const uint4 raw = next;
-    next = mine && h + step < last ? *source(h + step) : make_uint4(0, 0, 0, 0);
-    const bool live = mine && h < last, value = h >= a.Hq + a.Hkv, query = h < a.Hq;
-    const void* weight = value ? nullptr : query ? a.q_weight : a.k_weight;
-    float x[8];
-    unpack8<T>(raw, x);
-    float sum = 0.f;
+  // ---- queries and keys (every lane of a warp goes through the same number of passes)
+  int h = h_first;
+  for (int h0 = group * kHeads; h0 < turned; h0 += kAhead * step) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum = fmaf(x[j], x[j], sum);
+    for (int i = 0; i < kAhead; ++i, h += step) {
+      if (h0 + i * step >= turned) break;
+      const bool live = mine && h < turned, query = h < a.Hq;
+      uint64_t x[4];
+      unpack8<F16>(raw[i], x);
+      if (NORM) {
+        const void* weight = query ? a.q_weight : a.k_weight;
+        uint64_t sum2 = mul2(x[0], x[0]);
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (weight != nullptr && mine) {
-      const float r = 1.0f / sqrtf(sum / static_cast<float>(a.D) + a.eps);
-      float w[8];
-      if (a.weight_f32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(weight) + e0);
-        const float4 u = p[0], v = p[1];
-        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w, w[4] = v.x, w[5] = v.y, w[6] = v.z, w[7] = v.w;
-      } else {
-        unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(weight) + e0), w);
-      }
+        for (int j = 1; j < 4; ++j) sum2 = fma2(x[j], x[j], sum2);
+        float sum = lo(sum2) + hi(sum2);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = x[j] * r * w[j];
-    }
-    if (a.interleaved) {
-      if (!value) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (e0 + 2 * j < a.rot) {
-            const float2 f = turn[e0 / 2 + j];
-            const float u = x[2 * j], v = x[2 * j + 1];
-            x[2 * j] = fmaf(u, f.x, -v * f.y);
-            x[2 * j + 1] = fmaf(v, f.x, u * f.y);
+        for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (weight != nullptr && mine) {
+          const float r = rsqrtf(fmaf(sum, per_d, a.eps));
+          uint64_t w[4];
+          if (a.weight_f32) {
+            const ulonglong2* p = reinterpret_cast<const ulonglong2*>(static_cast<const float*>(weight) + e0);
+            w[0] = p[0].x, w[1] = p[0].y, w[2] = p[1].x, w[3] = p[1].y;
+          } else {
+            unpack8<F16>(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(weight) + e0), w);
           }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = mul2(mul2(x[j], pair(r, r)), w[j]);
         }
       }
-    } else if (pairs > 0) {
-      // the other half's values, from the lane that holds them (whole chunks), or
-      // through shared memory where the halves do not begin at a chunk
-      float y[8];
-      const bool front = e0 < pairs;
-      if ((pairs & 7) == 0) {
-        const int from = lane + (front ? pairs / 8 : -(pairs / 8));
+      if (pairs > 0) {
+        uint64_t y[4];  // the other of each value's pair
+        if (INTERLEAVED) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = __shfl_sync(0xffffffffu, x[j], from & 31);
-      } else {
-        float* buf = spare[tid >> 5];
+          for (int j = 0; j < 4; ++j) y[j] = pair(hi(x[j]), lo(x[j]));
+        } else if ((pairs & 7) == 0) {
+          // from the lane that holds the other half's chunk
+          const int from = lane + (e0 < pairs ? pairs / 8 : -(pairs / 8));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) buf[lane * 9 + j] = x[j];
-        __syncwarp();
+          for (int j = 0; j < 4; ++j) y[j] = __shfl_sync(0xffffffffu, x[j], from & 31);
+        } else {
+          // through shared memory where the halves do not begin at a chunk
+          float* buf = spare[threadIdx.x >> 5];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int e = e0 + j, other = e < pairs ? e + pairs : e < a.rot ? e - pairs : e;
-          y[j] = buf[((lane & ~(LANES - 1)) + (other >> 3)) * 9 + (other & 7)];
-        }
-        __syncwarp();
-      }
-      if (!value && mine) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int e = e0 + j;
-          if (e < a.rot) {
-            const bool first = e < pairs;
-            const float2 f = turn[first ? e : e - pairs];
-            x[j] = fmaf(x[j], f.x, first ? -y[j] * f.y : y[j] * f.y);
+          for (int j = 0; j < 4; ++j) {
+            buf[lane * 9 + 2 * j] = lo(x[j]);
+            buf[lane * 9 + 2 * j + 1] = hi(x[j]);
           }
+          __syncwarp();
+          float z[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int e = e0 + j, other = e < pairs ? e + pairs : e < a.rot ? e - pairs : e;
+            z[j] = buf[((lane & ~(LANES - 1)) + (other >> 3)) * 9 + (other & 7)];
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[j] = pair(z[2 * j], z[2 * j + 1]);
+          __syncwarp();
+        }
+        uint64_t z[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[j] = fma2(x[j], co[j], mul2(y[j], si[j]));
+        if (e0 + 8 <= a.rot) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = z[j];
+        } else {  // the end of the rotated part
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            x[j] = pair(e0 + 2 * j < a.rot ? lo(z[j]) : lo(x[j]), e0 + 2 * j + 1 < a.rot ? hi(z[j]) : hi(x[j]));
         }
       }
+      if (query) {
+        if (live) *reinterpret_cast<uint4*>(to_q + h * D) = pack8<F16>(x);
+        continue;
+      }
+      if (live && to_k != nullptr) *reinterpret_cast<uint4*>(to_k + h * D) = pack8<F16>(x);
+      if (slot < 0) continue;
+      uint8_t* to = slot_k + size * (h - a.Hq) * cache.k_head;
+      if (a.e4m3)
+        store_codes<LANES>(x, to, cache.k_scale + scale_at + (static_cast<int64_t>(h - a.Hq) << a.page_shift), lane, live, in_head == 0);
+      else if (live)
+        *reinterpret_cast<uint4*>(to) = pack8<F16>(x);
     }
-    if (query) {
-      if (live)
-        *reinterpret_cast<uint4*>(static_cast<T*>(a.q_out) + t * a.q_out_stride + static_cast<int64_t>(h) * a.D + e0) =
-            pack8<T>(x);
-      continue;
+    fetch(h);
+  }
+
+  // ---- values
+  if (slot < 0) return;
+  const uint16_t* of_v = static_cast<const uint16_t*>(a.v) + t * a.v_stride + e0;
+  uint8_t* slot_v = cache.v + size * (page * cache.v_page + place * cache.v_token + e0);
+  for (h = h_first; h - lane / LANES < a.Hkv; h += 2 * step) {
+    uint4 v[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      v[i] = mine && h + i * step < a.Hkv ? *reinterpret_cast<const uint4*>(of_v + (h + i * step) * D) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool live = mine && h + i * step < a.Hkv;
+      uint8_t* to = slot_v + size * (h + i * step) * cache.v_head;
+      if (a.e4m3) {
+        uint64_t x[4];
+        unpack8<F16>(v[i], x);
+        store_codes<LANES>(x, to, cache.v_scale + scale_at + (static_cast<int64_t>(h + i * step) << a.page_shift), lane, live, in_head == 0);
+      } else if (live) {
+        *reinterpret_cast<uint4*>(to) = v[i];
+      }
     }
-    const int hk = value ? h - a.Hq - a.Hkv : h - a.Hq;
-    if (live && !value && a.k_out != nullptr)
-      *reinterpret_cast<uint4*>(static_cast<T*>(a.k_out) + t * a.k_out_stride + static_cast<int64_t>(hk) * a.D + e0) =
-          pack8<T>(x);
-    if (slot < 0) continue;
-    const int64_t page = slot >> a.page_shift, place = slot & ((1 << a.page_shift) - 1);
-    const KvCache& c = a.cache;
-    const int64_t at = (value ? page * c.v_page + place * c.v_token + hk * c.v_head
-                              : page * c.k_page + place * c.k_token + hk * c.k_head) + e0;
-    uint8_t* to = value ? c.v : c.k;
-    if (!a.e4m3) {
-      if (live) *reinterpret_cast<uint4*>(to + 2 * at) = pack8<T>(x);
-      continue;
-    }
-    float amax = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(x[j]));
-    // only the lanes of this head: others of the warp may have left the pass for a query
-    const uint32_t group = LANES == 32 ? 0xffffffffu : ((1u << (LANES & 31)) - 1u) << (lane & ~(LANES - 1));
-#pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(group, amax, o));
-    float scale = __fdiv_rn(amax, 448.0f);
-    if (scale == 0.f) scale = 1.0f;
-    if (!live) continue;
-    if (in_head == 0)
-      (value ? c.v_scale : c.k_scale)[((page * a.Hkv + hk) << a.page_shift) + place] = scale;
-    uint32_t code[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) code[j] = f32x2_to_e4m3x2(__fdiv_rn(x[2 * j], scale), __fdiv_rn(x[2 * j + 1], scale));
-    *reinterpret_cast<uint2*>(to + at) = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
   }
 }
 
-template <typename T, int LANES>
+template <bool F16, int LANES, bool NORM, bool INTERLEAVED>
 cudaError_t launch(const RopeArgs& a, cudaStream_t s) {
-  // a token's heads in one CTA, or over several where the tokens leave SMs idle
-  constexpr int kHeads = kRopeThreads / LANES;
-  const int passes = (a.Hq + (a.cache.k != nullptr ? 2 : 1) * a.Hkv + kHeads - 1) / kHeads;
-  const int spread = std::max(1, std::min(passes, 2 * a.sms / a.T));
-  return launch_pdl(rope_kernel<T, LANES>, dim3(a.T, spread), dim3(kRopeThreads), 0, s, a);
+  // A token's heads by one warp, or by several where the tokens would leave SMs idle:
+  // kWarpsPerSm warps an SM.
+  constexpr int kHeads = 32 / LANES;
+  const int passes = (a.Hq + a.Hkv + kHeads - 1) / kHeads;
+  const int groups = std::max(1, std::min(passes, (kWarpsPerSm * a.sms + a.T - 1) / a.T));
+  const int64_t ctas = (static_cast<int64_t>(a.T) * groups + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+  return launch_pdl(rope_kernel<F16, LANES, NORM, INTERLEAVED>, dim3(static_cast<unsigned>(ctas)), dim3(kRopeThreads), 0, s, a, groups);
 }
 
-template <typename T>
+template <bool F16, int LANES>
 cudaError_t launch(const RopeArgs& a, cudaStream_t s) {
-  if (a.D <= 64) return launch<T, 8>(a, s);
-  if (a.D <= 128) return launch<T, 16>(a, s);
-  return launch<T, 32>(a, s);
+  const bool norm = a.q_weight != nullptr || a.k_weight != nullptr;
+  if (norm) return a.interleaved ? launch<F16, LANES, true, true>(a, s) : launch<F16, LANES, true, false>(a, s);
+  return a.interleaved ? launch<F16, LANES, false, true>(a, s) : launch<F16, LANES, false, false>(a, s);
+}
+
+template <bool F16>
+cudaError_t launch(const RopeArgs& a, cudaStream_t s) {
+  if (a.D <= 64) return launch<F16, 8>(a, s);
+  if (a.D <= 128) return launch<F16, 16>(a, s);
+  return launch<F16, 32>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const RopeArgs& a, int dtype, cudaStream_t s) {
-  return dtype == 0 ? launch<__nv_bfloat16>(a, s) : launch<__half>(a, s);
+  return dtype == 0 ? launch<false>(a, s) : launch<true>(a, s);
 }
 
 }  // namespace moe
