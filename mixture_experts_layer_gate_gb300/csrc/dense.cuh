@@ -46,7 +46,7 @@ constexpr uint32_t kScaleSlots = 4, kScaleSlotBytes = 2 * 4 * 128 * 4;
 // 80 bytes apart (eight lanes' 16-byte stores fall into different banks); of
 // 256-column tiles that TMA stores, two boxes of 32 rows by 64 bytes, or four
 // where it also fetches what the sums are added to and the ring keeps its stages
-// (CTA pairs).
+// (CTA pairs), or one (EPI).
 constexpr int kStageRow = 80, kBoxBytes = 32 * 64, kMaxBoxes = 4;
 __host__ __device__ constexpr int out_stage_bytes(int bn, int boxes) {
   return bn == 256 ? boxes * kBoxBytes : 32 * kStageRow;
@@ -82,7 +82,7 @@ struct Params {
   int vec_bias;          // bias takes 16-byte loads
   int vec;               // rows of out (and old) take 16-byte accesses
   int tma_out;           // 256-column tiles are stored by TMA
-  int boxes;             // of each joining warp, for that: 2 or 4
+  int boxes;             // of each joining warp, for that: 1, 2 or 4
   int vec_scale;         // rows of a_scale take 16-byte loads at multiples of four blocks
 };
 
@@ -839,7 +839,10 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
               box_phase ^= 1u << slot;
               box_loads &= ~(1u << slot);
             } else {
-              if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the last one but one is read
+              if (lane == 0) {
+                if (EPI > 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // (one box: it is read)
+                else asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the last one but one is read
+              }
               __syncwarp();
             }
 #pragma unroll
@@ -1050,7 +1053,7 @@ inline Choice choose(int M, int N, int KB, bool swiglu, bool e4m3, int sms, bool
   const double arows = std::min(128, (M + 7) / 8 * 8);
   for (int w = 0; w < 5; ++w) {
     constexpr int width[5] = {32, 64, 128, 256, 256};
-    constexpr double half_block[5] = {250, 340, 560, 1150, 1150}, e4m3_block[5] = {600, 690, 800, 1250, 950};
+    constexpr double half_block[5] = {250, 340, 560, 1150, 620}, e4m3_block[5] = {600, 690, 800, 1250, 950};
     const int bn = width[w];
     const bool pair = w == 4;
     if ((swiglu && bn != 256) || (pair && (M <= 128 || !(e4m3 || pairs_of_half)))) continue;
@@ -1087,7 +1090,9 @@ cudaError_t plan_and_launch(Params p, int bn, bool pair, bool swiglu, const void
   p.arows = pair || p.M >= 128 ? 128 : (p.M + 7) / 8 * 8;
   const int sb = stage_bytes(p.arows, bn, pair);
   p.tma_out = bn == 256 && !swiglu && p.P == 1 && p.vec;
-  p.boxes = p.tma_out && p.accumulate && pair ? kMaxBoxes : 2;
+  // 16-bit products with an epilogue take one: the ring's stages are worth more than boxes
+  // ahead (M = N = K = 4096 with a residual, one box 86 us, four 95)
+  p.boxes = EPI > 0 && p.tma_out ? 1 : p.tma_out && p.accumulate && pair ? kMaxBoxes : 2;
   const int fixed = fixed_bytes(KIND, swiglu, bn, p.boxes);
   const size_t room = kMaxSmem - 1024 - fixed - (kTileABytes - p.arows * 128);
   const int per_cta = pair ? p.KB : (p.KB + p.P - 1) / p.P;

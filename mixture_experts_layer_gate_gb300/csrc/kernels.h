@@ -317,8 +317,8 @@ struct LinearArgs {
 };
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
 // The same for a few rows.
-constexpr int kLinearFewRows = 16;
-cudaError_t launch_linear_few(const LinearArgs& a, int sms, cudaStream_t s);
+constexpr int kLinearFewRows = 8;
+cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t s);
 
 struct AttnArgs {
   const uint16_t* q;          // [T, Hq * D]

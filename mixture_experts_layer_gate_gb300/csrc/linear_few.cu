@@ -1,13 +1,13 @@
-// moe_linear for at most 16 rows of x (decode): bound by the rate at which the
+// moe_linear for at most 8 rows of x (decode): bound by the rate at which the
 // weights stream in, so no tile of 128 rows: a warp multiplies 16 weight rows with
-// all rows of x (the 8 columns of mma.sync m16n8k16, once or twice) over its part
-// of K, straight from global memory to registers.  K is permuted inside 32 values so
-// that the 16 adjacent bytes a lane loads are its fragment: lane (g, c) holds k = 8 c
-// .. 8 c + 7 of weight rows g and g + 8 and of row g of x, words 0 and 1 for one
-// product, 2 and 3 for the next.  The warps' sums are joined through shared memory in
-// a fixed order.
-#include <algorithm>
-
+// all rows of x (the 8 columns of mma.sync m16n8k16) over its part of K, straight
+// from global memory to registers.  K is permuted inside 32 values so that the 16
+// adjacent bytes a lane loads are its fragment: lane (g, c) holds k = 8 c .. 8 c + 7 of
+// weight rows g and g + 8 and of row g of x, words 0 and 1 for one product, 2 and 3 for
+// the next.  The warps' sums are joined through shared memory in a fixed order.  N =
+// 6144, K = 4096 in a graph, the weights from memory: one row 9.2 us = 5.5 TB/s, eight
+// 9.9; two CTAs an SM instead of three 11.1, six or eight steps ahead instead of four
+// 9.9 and 14 (their registers).  Sixteen rows took 15 us, the tensor cores' tiles 12.4.
 #include "common.cuh"
 #include "kernels.h"
 #include "stream.cuh"
@@ -42,18 +42,16 @@ __device__ __forceinline__ float value_at(const void* p, int64_t i, int dtype) {
                       : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
 }
 
-// NT: column groups of 8 rows of x.
-template <bool F16, int NT>
-__global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const LinearArgs a) {
-  __shared__ float red[kWarps][16][8 * NT + 1];
+template <bool F16>
+__global__ void __launch_bounds__(kThreads, 3) linear_few_kernel(const LinearArgs a) {
+  __shared__ float red[kWarps][16][9];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int n0 = blockIdx.x * 16;
   const int steps = (a.K + 31) / 32;
   const uint16_t* w0 = static_cast<const uint16_t*>(a.w) + static_cast<int64_t>(min(n0 + g, a.N - 1)) * a.w_stride;
   const uint16_t* w1 = static_cast<const uint16_t*>(a.w) + static_cast<int64_t>(min(n0 + g + 8, a.N - 1)) * a.w_stride;
-  const uint16_t* x0 = static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(min(g, a.M - 1)) * a.x_stride;
-  const uint16_t* x1 = static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(min(g + 8, a.M - 1)) * a.x_stride;
-  float acc[NT][4] = {};
+  const uint16_t* x = static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(min(g, a.M - 1)) * a.x_stride;
+  float acc[4] = {};
   const uint4 none = make_uint4(0, 0, 0, 0);
   uint4 p[kAhead], q[kAhead];
   pdl_wait();
@@ -72,23 +70,17 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const LinearArg
       const int s = s0 + i * kWarps, k = s * 32 + c * 8;
       const uint4 u = p[i], v = q[i];
       const bool there = s < steps && k < a.K;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        // (rows of x past M, and k past K, multiply nothing)
-        const uint4 b = there && g + 8 * t < a.M ? *reinterpret_cast<const uint4*>((t == 0 ? x0 : x1) + k) : none;
-        mma16816<F16>(acc[t], u.x, v.x, u.y, v.y, b.x, b.y);
-        mma16816<F16>(acc[t], u.z, v.z, u.w, v.w, b.z, b.w);
-      }
+      // (rows of x past M, and k past K, multiply nothing)
+      const uint4 b = there && g < a.M ? *reinterpret_cast<const uint4*>(x + k) : none;
+      mma16816<F16>(acc, u.x, v.x, u.y, v.y, b.x, b.y);
+      mma16816<F16>(acc, u.z, v.z, u.w, v.w, b.z, b.w);
       fetch(s + kWarps * kAhead, p[i], q[i]);
     }
   }
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    red[warp][g][8 * t + 2 * c] = acc[t][0];
-    red[warp][g][8 * t + 2 * c + 1] = acc[t][1];
-    red[warp][g + 8][8 * t + 2 * c] = acc[t][2];
-    red[warp][g + 8][8 * t + 2 * c + 1] = acc[t][3];
-  }
+  red[warp][g][2 * c] = acc[0];
+  red[warp][g][2 * c + 1] = acc[1];
+  red[warp][g + 8][2 * c] = acc[2];
+  red[warp][g + 8][2 * c + 1] = acc[3];
   __syncthreads();
   const int n = n0 + (tid & 15), m = tid >> 4;
   if (m < a.M && n < a.N) {
@@ -105,17 +97,12 @@ __global__ void __launch_bounds__(kThreads, 2) linear_few_kernel(const LinearArg
   }
 }
 
-template <bool F16>
-cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
-  const dim3 grid((a.N + 15) / 16), block(kThreads);
-  if (a.M <= 8) return launch_pdl(linear_few_kernel<F16, 1>, grid, block, 0, s, a);
-  return launch_pdl(linear_few_kernel<F16, 2>, grid, block, 0, s, a);
-}
-
 }  // namespace
 
-cudaError_t launch_linear_few(const LinearArgs& a, int, cudaStream_t s) {
-  return a.f16 ? launch<true>(a, s) : launch<false>(a, s);
+cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t s) {
+  const dim3 grid((a.N + 15) / 16), block(kThreads);
+  return a.f16 ? launch_pdl(linear_few_kernel<true>, grid, block, 0, s, a)
+               : launch_pdl(linear_few_kernel<false>, grid, block, 0, s, a);
 }
 
 }  // namespace moe
