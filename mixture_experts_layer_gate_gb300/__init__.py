@@ -15,4 +15,4 @@ from .binding import (MoEError, Problem, Plan, Weights, MoELayer, load, problem,
                       qk_norm_rope, LinearProblem, linear_problem, linear, AttentionProblem,
                       attention_problem, attention_workspace_size, alloc_attention_workspace, paged_attention,
                       prompt_attention)
-from .block import MoEBlock, SharedExpert
+from .block import AttentionBlock, DecoderLayer, KVCache, MoEBlock, SharedExpert
