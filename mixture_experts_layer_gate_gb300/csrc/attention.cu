@@ -570,9 +570,13 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
       }
     } else if (E4M3 && some && warp >= 12) {
       // ------------------------------------------- 8-bit: codes into f16 tiles
-      // thread j takes 16-byte pieces j, j + 128, ... of a tile (lanes go along a row)
-      constexpr int kT = 32 * kConverters, kMine = kKeys * DP / 16 / kT, kRowPieces = DP / 16;
-      const int me = (warp - 12) * 32 + lane;
+      // Eight lanes take half a row each of two neighbouring rows, 64 codes, whose swizzled
+      // f16 pieces lie in different banks; a thread's pieces are 32 rows and half a row
+      // apart, so that all its addresses are two plus constants.
+      static_assert(kConverters == 4, "32 rows at a time");
+      const int me = (warp - 12) * 32 + lane, my_row = (me >> 3) * 2 + (me >> 2 & 1), my_piece = me & 3;
+      const uint32_t my_codes = static_cast<uint32_t>(my_row * DP + 16 * my_piece);
+      const uint32_t my_f16[2] = {piece_at(my_row, 2 * my_piece), piece_at(my_row, 2 * my_piece + 1)};
       int st = 0, cs = 0;
       uint32_t ph = 0, cph = 0;
       for (int item = 0; ok; ++item) {
@@ -588,23 +592,33 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
           const bool partly = (u & 1) != 0 && t * kKeys + kKeys - 1 > least;
           const int there = L - t * kKeys;
           uint32_t odd = 0;
-#pragma unroll 2
-          for (int j = 0; j < kMine; ++j) {
-            const int i = me + j * kT, r = i / kRowPieces, c = i % kRowPieces;
-            const uint4 v = dense::lds_u4(from + 16u * static_cast<uint32_t>(i));
+          auto convert = [&](uint32_t src, uint32_t (&h)[8]) {
+            const uint4 v = dense::lds_u4(from + src);
             const uint32_t q[4] = {v.x, v.y, v.z, v.w};
-            uint32_t h[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[e] = e4m3x2_half2(e & 1 ? q[e >> 1] >> 16 : q[e >> 1] & 0xFFFFu);
-            if (partly) {
+          };
+          auto put = [&](uint32_t dst, const uint32_t (&h)[8]) {
+            dense::sts_u4(tile + my_f16[0] + dst, make_uint4(h[0], h[1], h[2], h[3]));
+            dense::sts_u4(tile + my_f16[1] + dst, make_uint4(h[4], h[5], h[6], h[7]));
+          };
+          if (!partly) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) h[e] = r < there ? tame(h[e], true, odd) : 0u;
+            for (int j = 0; j < 4 * kChunks; ++j) {
+              uint32_t h[8];
+              convert(my_codes + static_cast<uint32_t>((j / kChunks) * 32 * DP + (j % kChunks) * 64), h);
+              put(static_cast<uint32_t>((j / kChunks) * 32 * 128 + (j % kChunks) * 128 * 128), h);
             }
-            // (lanes 4 to 7 of a row's eight begin with their second piece: other banks)
-            const uint4 u0 = make_uint4(h[0], h[1], h[2], h[3]), u1 = make_uint4(h[4], h[5], h[6], h[7]);
-            const int swap = c >> 2 & 1;
-            dense::sts_u4(tile + piece_at(r, 2 * c + swap), swap ? u1 : u0);
-            dense::sts_u4(tile + piece_at(r, 2 * c + 1 - swap), swap ? u0 : u1);
+          } else {
+#pragma unroll 1
+            for (int j = 0; j < 4 * kChunks; ++j) {
+              uint32_t h[8];
+              convert(my_codes + static_cast<uint32_t>((j / kChunks) * 32 * DP + (j % kChunks) * 64), h);
+              const bool in = my_row + j / kChunks * 32 < there;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) h[e] = in ? tame(h[e], true, odd) : 0u;
+              put(static_cast<uint32_t>((j / kChunks) * 32 * 128 + (j % kChunks) * 128 * 128), h);
+            }
           }
           if (odd) dirty[item % kDirty] = item;
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -729,7 +743,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
         // Twice over the scores, some at a time: their maximum, then the weights.  (Held
         // in registers in between, 128 of them unrolled, the code did not fit the
         // instruction caches.)  Scores that are scaled or masked go back to tensor memory.
-        constexpr int kSome = E4M3 ? 32 : 64;
+        constexpr int kSome = 64;
         const bool masked = t * kKeys + kKeys - 1 > least;
         float now = -INFINITY;
 #pragma unroll 1

@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<E4M3, NT>, 1) attention_few_kern
   constexpr int kPerLoad = 32 / kPieces;  // keys that a load of the warp covers
   constexpr int MT = DP / 16;             // row tiles of the output: 16 places of the head
   constexpr int W = DP / 8;               // 8-bit: adjacent values a lane reads of a row
-  using FewWalk = Walk<Shape<kRows, kTile, 1, 1, 1>>;
+  using FewWalk = Walk<Shape<kRows, kTile, 1, 2, 4>>;
   __shared__ int last;
   float* join = reinterpret_cast<float*>(few_smem);  // [buffer][row][DP]
   float* ms = join + join_bytes(DP) / 4;             // [buffer][row]
