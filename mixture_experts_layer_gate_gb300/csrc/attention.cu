@@ -869,136 +869,167 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
         const uint64_t to = live ? reinterpret_cast<uint64_t>(a.out + out_row * a.out_stride + static_cast<int64_t>(hd) * a.D) : 0;
         // An item that lies in several runs leaves its sums in the workspace, and the
         // last of its CTAs to finish joins them in the order of the runs.
-        const int first = w->first, pieces = w->pieces;
+        const int first = w->first, pieces = w->pieces, me = static_cast<int>(blockIdx.x) - first;
         constexpr size_t kPiece = attn_piece_bytes(kRows, DP) / 4;
-        auto piece = [&](int i) { return a.partial + (2 * (first + i) + (i == 0 ? 1 : 0)) * kPiece + half * kHalf + row; };
-        float* mine = piece(static_cast<int>(blockIdx.x) - first);
-        float all_top = top, all_sum = total;
-        const int64_t at = live ? 0 : -static_cast<int64_t>(half * kHalf + row);  // (dead rows read the first one's)
+        auto piece = [&](int i) { return a.partial + (2 * (first + i) + (i == 0 ? 1 : 0)) * kPiece; };
+        float* mine = piece(me) + half * kHalf + row;
+        const float inv = 1.f / total;
 #pragma unroll 1
-        for (int phase = whole ? 1 : 0; phase < 2; ++phase) {  // into the workspace; into out
-          const float inv = 1.f / all_sum;
-#pragma unroll 1
-          for (int c = 0; c < DP / 32; ++c) {
-            float v[32];
-            if (phase == 1 && !whole) {
+        for (int c = 0; c < DP / 32; ++c) {
+          float v[32];
+          if (has) {
+            uint32_t o[32];
+            dense::tmem_ld32(O + 32u * c, o);
+            dense::tmem_ld32_wait(o);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = 0.f;
-#pragma unroll 2
-              for (int i = 0; i < pieces; ++i) {
-                const float* from = piece(i) + at;
-                const float f = exp2_fast(__ldcg(from + DP * kRows) - reference(all_top));
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * (E4M3 ? unit : 1.f);
+          } else {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = fmaf(__ldcg(from + (32 * c + j) * kRows), f, v[j]);
-              }
-            } else if (has) {
-              uint32_t o[32];
-              dense::tmem_ld32(O + 32u * c, o);
-              dense::tmem_ld32_wait(o);
+            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+          }
+          if (!whole) {
+            if (live)
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * (E4M3 ? unit : 1.f);
-            } else {
+              for (int j = 0; j < 32; ++j) __stcg(mine + (32 * c + j) * kRows, v[j]);
+            continue;
+          }
+          // The rows of four lanes are turned so that the four store 64 adjacent bytes of
+          // one row at a time (a row a lane: 32 lines a store, 2 us an item).
+          uint4 u[4];
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = 0.f;
-            }
-            if (phase == 0) {
-              if (live)
+          for (int j = 0; j < 4; ++j) {
+            uint32_t* x = &u[j].x;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) __stcg(mine + (32 * c + j) * kRows, v[j]);
-              continue;
-            }
-            // The rows of four lanes are turned so that the four store 64 adjacent bytes of
-            // one row at a time (a row a lane: 32 lines a store, 2 us an item).
-            uint4 u[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t* x = &u[j].x;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float y = v[8 * j + 2 * e] * inv, z = v[8 * j + 2 * e + 1] * inv;
-                x[e] = (E4M3 ? a.f16 != 0 : F16) ? pack_half(y, z) : pack_bf16x2(y, z);
-              }
-            }
-            // lane l of four holds pieces 0 to 3 of row l; afterwards piece l of rows 0 to 3
-            auto turn = [&](uint4& p, uint4& q, int bit) {  // p of the lanes without the bit for q of those with it
-              const bool up = (lane & bit) != 0;
-              uint32_t *x = &p.x, *z = &q.x;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x[e] : z[e], bit);
-                if (up) x[e] = got;
-                else z[e] = got;
-              }
-            };
-            turn(u[0], u[1], 1);
-            turn(u[2], u[3], 1);
-            turn(u[0], u[2], 2);
-            turn(u[1], u[3], 2);
-            const int column = 32 * c + 8 * (lane & 3);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint64_t row_at = __shfl_sync(0xffffffffu, to, (lane & ~3) + j);
-              if (row_at != 0 && column < a.D) *reinterpret_cast<uint4*>(row_at + 2 * column) = u[j];
+            for (int e = 0; e < 4; ++e) {
+              const float y = v[8 * j + 2 * e] * inv, z = v[8 * j + 2 * e + 1] * inv;
+              x[e] = (E4M3 ? a.f16 != 0 : F16) ? pack_half(y, z) : pack_bf16x2(y, z);
             }
           }
-          if (spoiled && has && (phase == 0 || whole)) {
-            // values that are not finite, of the keys that this row sees among those looked
-            // at, added to what was written
-            __syncwarp();
-            const int from = max(t0, divided(w->least + 1, kKeys)) * kKeys;
-            const int upto = live ? min(limit, end * kKeys - 1) : -1;
+          // lane l of four holds pieces 0 to 3 of row l; afterwards piece l of rows 0 to 3
+          auto turn = [&](uint4& p, uint4& q, int bit) {  // p of the lanes without the bit for q of those with it
+            const bool up = (lane & bit) != 0;
+            uint32_t *x = &p.x, *z = &q.x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x[e] : z[e], bit);
+              if (up) x[e] = got;
+              else z[e] = got;
+            }
+          };
+          turn(u[0], u[1], 1);
+          turn(u[2], u[3], 1);
+          turn(u[0], u[2], 2);
+          turn(u[1], u[3], 2);
+          const int column = 32 * c + 8 * (lane & 3);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint64_t row_at = __shfl_sync(0xffffffffu, to, (lane & ~3) + j);
+            if (row_at != 0 && column < a.D) *reinterpret_cast<uint4*>(row_at + 2 * column) = u[j];
+          }
+        }
+        if (spoiled && has) {
+          // values that are not finite, of the keys that this row sees among those looked
+          // at, added to what was written
+          __syncwarp();
+          const int from = max(t0, divided(w->least + 1, kKeys)) * kKeys;
+          const int upto = live ? min(limit, end * kKeys - 1) : -1;
 #pragma unroll 1
-            for (int key = from; key <= upto; ++key) {
-              int64_t page, place;
-              if (!locate(a, w->row0, w->b, key, page, place)) continue;
-              const float vscale = E4M3 ? a.kv.v_scale[((page * a.Hkv + w->h) << a.page_shift) + place] : 1.f;
-              const int64_t in = page * a.kv.v_page + place * a.kv.v_token + w->h * a.kv.v_head;
+          for (int key = from; key <= upto; ++key) {
+            int64_t page, place;
+            if (!locate(a, w->row0, w->b, key, page, place)) continue;
+            const float vscale = E4M3 ? a.kv.v_scale[((page * a.Hkv + w->h) << a.page_shift) + place] : 1.f;
+            const int64_t in = page * a.kv.v_page + place * a.kv.v_token + w->h * a.kv.v_head;
 #pragma unroll 1
-              for (int d = 0; d < a.D; ++d) {
-                const float x = E4M3 ? __half2float(__ushort_as_half(static_cast<uint16_t>(e4m3x2_half2(a.kv.v[in + d])))) * vscale
-                                     : f32_of(reinterpret_cast<const uint16_t*>(a.kv.v)[in + d], F16);
-                if (fabsf(x) < INFINITY) continue;
-                if (phase == 0) {
-                  __stcg(mine + d * kRows, __ldcg(mine + d * kRows) + x);
-                } else {
-                  uint16_t* o = reinterpret_cast<uint16_t*>(to) + d;
-                  const float y = f32_of(*o, a.f16) + x;
-                  *o = static_cast<uint16_t>(a.f16 ? pack_half(y, 0.f) : pack_bf16x2(y, 0.f));
-                }
+            for (int d = 0; d < a.D; ++d) {
+              const float x = E4M3 ? __half2float(__ushort_as_half(static_cast<uint16_t>(e4m3x2_half2(a.kv.v[in + d])))) * vscale
+                                   : f32_of(reinterpret_cast<const uint16_t*>(a.kv.v)[in + d], F16);
+              if (fabsf(x) < INFINITY) continue;
+              if (!whole) {
+                __stcg(mine + d * kRows, __ldcg(mine + d * kRows) + x);
+              } else {
+                uint16_t* o = reinterpret_cast<uint16_t*>(to) + d;
+                const float y = f32_of(*o, a.f16) + x;
+                *o = static_cast<uint16_t>(a.f16 ? pack_half(y, 0.f) : pack_bf16x2(y, 0.f));
               }
             }
           }
-          if (phase == 1) {
-            if (live && a.lse != nullptr) a.lse[out_row * a.Hq + hd] = (all_top + log2_fast(all_sum)) * 0.69314718055994531f;
-            break;
-          }
+        }
+        if (whole) {
+          if (live && a.lse != nullptr) a.lse[out_row * a.Hq + hd] = (top + log2_fast(total)) * 0.69314718055994531f;
+        } else {
           if (live) {
             __stcg(mine + DP * kRows, top);
             __stcg(mine + (DP + 1) * kRows, total);
           }
-          __threadfence();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cta(join0);
-          ok = wait(join0, jph, abort_flag, 0x770);
-          if (!ok) break;
-          if (tid == 0) {
-            const bool last = atomicAdd(a.tickets + first, 1u) == static_cast<uint32_t>(pieces - 1);
-            if (last) a.tickets[first] = 0;
+          // The warps share the live rows, 32 a warp, and where those are few also the
+          // columns (a row a thread with all its columns: 32 rows of 19 pieces took 40 us).
+          const int row_warps = (w->rows + 31) / 32;
+          const int groups = min(DP / 32, row_warps <= 2 ? 4 : row_warps <= 4 ? 2 : 1);
+          const int group = divided(warp, row_warps), join_row = 32 * (warp - group * row_warps) + lane;
+          const bool joins = group < groups && join_row < w->rows;
+          bool done = false;
+#pragma unroll 1
+          for (int level = 0; !done; ++level) {
+            const Join j = join_of(a, first, pieces, me, level);
             __threadfence();
-            *last_flag = last;
-            mbar_arrive_cta(join1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cta(join0);
+            ok = wait(join0, jph, abort_flag, 0x770);
+            if (!ok) break;
+            if (tid == 0) {
+              *last_flag = count_in(j);
+              mbar_arrive_cta(join1);
+            }
+            ok = wait(join1, jph, abort_flag, 0x771);
+            jph ^= 1u;
+            if (!ok || *last_flag == 0) break;
+            done = j.last;
+            if (!joins) continue;
+            // (a group's maxima and totals have a place of their own: warps read its first piece's)
+            auto stats = [&](int i) { return piece(j.base + i * j.stride) + (j.stride == 1 ? DP : DP + 2) * kRows + join_row; };
+            float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+            for (int i = 0; i < j.count; ++i) m = fmaxf(m, __ldcg(stats(i)));
+            const float r = reference(m);
+#pragma unroll 4
+            for (int i = 0; i < j.count; ++i) l = fmaf(__ldcg(stats(i) + kRows), exp2_fast(__ldcg(stats(i)) - r), l);
+            const int R = w->r * kRows + join_row, join_tok = divided(R, a.G), join_head = w->h * a.G + R - join_tok * a.G;
+            const int64_t join_out = w->row0 + join_tok;
+            uint16_t* out = a.out + join_out * a.out_stride + static_cast<int64_t>(join_head) * a.D;
+            const float per = 1.f / l;
+#pragma unroll 1
+            for (int c = group * (DP / 32) / groups; c < (group + 1) * (DP / 32) / groups; ++c) {
+              float v[32];
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] = 0.f;
+#pragma unroll 2
+              for (int i = 0; i < j.count; ++i) {
+                const float* from = piece(j.base + i * j.stride) + 32 * c * kRows + join_row;
+                const float f = exp2_fast(__ldcg(stats(i)) - r);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] = fmaf(__ldcg(from + k * kRows), f, v[k]);
+              }
+              if (!done) {  // a group's sum, into its first piece's place
+#pragma unroll
+                for (int k = 0; k < 32; ++k) __stcg(piece(j.base) + (32 * c + k) * kRows + join_row, v[k]);
+                continue;
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t u[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  u[e] = a.f16 ? pack_half(v[8 * k + 2 * e] * per, v[8 * k + 2 * e + 1] * per)
+                               : pack_bf16x2(v[8 * k + 2 * e] * per, v[8 * k + 2 * e + 1] * per);
+                if (32 * c + 8 * k < a.D) *reinterpret_cast<uint4*>(out + 32 * c + 8 * k) = make_uint4(u[0], u[1], u[2], u[3]);
+              }
+            }
+            if (done && group == 0 && a.lse != nullptr) a.lse[join_out * a.Hq + join_head] = (m + log2_fast(l)) * 0.69314718055994531f;
+            if (!done && group == 0) {
+              __stcg(piece(j.base) + (DP + 2) * kRows + join_row, m);
+              __stcg(piece(j.base) + (DP + 3) * kRows + join_row, l);
+            }
           }
-          ok = wait(join1, jph, abort_flag, 0x771);
-          jph ^= 1u;
-          if (!ok || *last_flag == 0) break;
-          __threadfence();
-          all_top = -INFINITY;
-#pragma unroll 4
-          for (int i = 0; i < pieces; ++i) all_top = fmaxf(all_top, __ldcg(piece(i) + at + DP * kRows));
-          all_sum = 0.f;
-#pragma unroll 4
-          for (int i = 0; i < pieces; ++i)
-            all_sum = fmaf(__ldcg(piece(i) + at + (DP + 1) * kRows), exp2_fast(__ldcg(piece(i) + at + DP * kRows) - reference(all_top)), all_sum);
         }
         if (!ok) break;
         tc_fence_before();  // (the next item's products write O after this half's weights)

@@ -291,6 +291,32 @@ __device__ __forceinline__ bool start(const AttnArgs& a, int64_t* scratch, Walk<
   return true;
 }
 
+// How an item's pieces are joined: all at once by the last CTA to finish, or, where
+// they are many, by the last one of each kGroup and then the last of those (152
+// pieces one after the other took 40 us).  Counters are zero between calls: of all
+// pieces or groups, of the first group and of the others, each by a CTA that has no
+// other item's (a CTA begins at most one cut item and continues at most one).
+constexpr int kDirect = 16, kGroup = 12;
+struct Join {
+  uint32_t* counter;
+  int base, stride, count;  // pieces base, base + stride, ...
+  bool last;                // of the item, else of a group
+};
+__device__ __forceinline__ Join join_of(const AttnArgs& a, int first, int pieces, int me, int level) {
+  if (pieces <= kDirect) return {a.tickets + first, 0, 1, pieces, true};
+  if (level > 0) return {a.tickets + first, 0, kGroup, (pieces + kGroup - 1) / kGroup, true};
+  const int group = me / kGroup, base = group * kGroup;
+  return {group == 0 ? a.tickets + kAttnMaxCtas + first : a.tickets + 2 * kAttnMaxCtas + first + base, base, 1,
+          min(kGroup, pieces - base), false};
+}
+// Counts one in; whether it was the last, with what the others wrote before visible.
+__device__ __forceinline__ bool count_in(const Join& j) {
+  const bool last = atomicAdd(j.counter, 1u) == static_cast<uint32_t>(j.count - 1);
+  if (last) *j.counter = 0;
+  __threadfence();
+  return last;
+}
+
 // Rows of tokens that see no key: zeros, and minus infinity as their logarithm.
 __device__ __forceinline__ void clear_empty_rows(const AttnArgs& a) {
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {

@@ -540,50 +540,54 @@ __global__ void __launch_bounds__(32 * kWarpsOf<E4M3, NT>, 1) attention_few_kern
       const int first = cur.first_cta(), pieces = cur.cta_count();
       constexpr size_t kPiece = attn_piece_bytes(kMostRows, DP) / 4;
       auto piece = [&](int i) { return a.partial + (2 * (first + i) + (i == 0 ? 1 : 0)) * kPiece; };
-      float* to = piece(static_cast<int>(blockIdx.x) - first);
-      if (mine) {
+      const int me = static_cast<int>(blockIdx.x) - first;
+      write = false;
+      int to = me;  // the piece that this CTA writes
+#pragma unroll 1
+      for (int level = 0; !write; ++level) {
+        float* p = piece(to);
+        if (mine) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          __stcg(reinterpret_cast<float4*>(to + row * DP + d0) + j, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
-        if (d0 == 0) {
-          __stcg(to + kMostRows * DP + 2 * row, top);
-          __stcg(to + kMostRows * DP + 2 * row + 1, sum);
+          for (int j = 0; j < 2; ++j)
+            __stcg(reinterpret_cast<float4*>(p + row * DP + d0) + j, make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+          if (d0 == 0) __stcg(reinterpret_cast<float2*>(p + kMostRows * DP + 2 * row), make_float2(top, sum));
         }
-      }
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        last = atomicAdd(a.tickets + first, 1u) == static_cast<uint32_t>(pieces - 1);
-        if (last) a.tickets[first] = 0;
+        const Join j = join_of(a, first, pieces, me, level);
         __threadfence();
-      }
-      __syncthreads();
-      write = last != 0;
-      if (write && mine) {
-        top = -INFINITY;
+        __syncthreads();
+        if (tid == 0) last = count_in(j);
+        __syncthreads();
+        if (last == 0) break;
+        if (mine) {
+          top = -INFINITY;
 #pragma unroll 8
-        for (int i = 0; i < pieces; ++i) top = fmaxf(top, __ldcg(piece(i) + kMostRows * DP + 2 * row));
-        const float r = reference(top);
-        sum = 0.f;
+          for (int i = 0; i < j.count; ++i)
+            top = fmaxf(top, __ldcg(piece(j.base + i * j.stride) + kMostRows * DP + 2 * row));
+          const float r = reference(top);
+          sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+          for (int i = 0; i < 8; ++i) v[i] = 0.f;
 #pragma unroll 8
-        for (int i = 0; i < pieces; ++i) {
-          const float* from = piece(i);
-          const float2 stat = __ldcg(reinterpret_cast<const float2*>(from + kMostRows * DP + 2 * row));
-          const float4 u = __ldcg(reinterpret_cast<const float4*>(from + row * DP + d0));
-          const float4 z = __ldcg(reinterpret_cast<const float4*>(from + row * DP + d0) + 1);
-          const float f = exp2_fast(stat.x - r);
-          sum = fmaf(stat.y, f, sum);
-          v[0] = fmaf(u.x, f, v[0]);
-          v[1] = fmaf(u.y, f, v[1]);
-          v[2] = fmaf(u.z, f, v[2]);
-          v[3] = fmaf(u.w, f, v[3]);
-          v[4] = fmaf(z.x, f, v[4]);
-          v[5] = fmaf(z.y, f, v[5]);
-          v[6] = fmaf(z.z, f, v[6]);
-          v[7] = fmaf(z.w, f, v[7]);
+          for (int i = 0; i < j.count; ++i) {
+            const float* from = piece(j.base + i * j.stride);
+            const float2 stat = __ldcg(reinterpret_cast<const float2*>(from + kMostRows * DP + 2 * row));
+            const float4 u = __ldcg(reinterpret_cast<const float4*>(from + row * DP + d0));
+            const float4 z = __ldcg(reinterpret_cast<const float4*>(from + row * DP + d0) + 1);
+            const float f = exp2_fast(stat.x - r);
+            sum = fmaf(stat.y, f, sum);
+            v[0] = fmaf(u.x, f, v[0]);
+            v[1] = fmaf(u.y, f, v[1]);
+            v[2] = fmaf(u.z, f, v[2]);
+            v[3] = fmaf(u.w, f, v[3]);
+            v[4] = fmaf(z.x, f, v[4]);
+            v[5] = fmaf(z.y, f, v[5]);
+            v[6] = fmaf(z.z, f, v[6]);
+            v[7] = fmaf(z.w, f, v[7]);
+          }
         }
+        write = j.last;
+        to = j.base;
+        __syncthreads();  // (all have read the group's pieces before its sum takes the first one's place)
       }
     }
     if (write && mine) {

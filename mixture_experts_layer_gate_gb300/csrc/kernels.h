@@ -329,7 +329,7 @@ struct AttnArgs {
   uint16_t* out;              // [T, Hq * D]
   float* lse;                 // [T, Hq] or null
   uint32_t* err;
-  uint32_t* tickets;          // [kAttnMaxCtas], zero between calls
+  uint32_t* tickets;          // [3 kAttnMaxCtas], zero between calls
   float* partial;             // [2 kAttnMaxCtas] pieces of split rows
   int64_t q_stride, out_stride, table_stride;
   int T, B, Hq, Hkv, D, G;
@@ -339,10 +339,10 @@ struct AttnArgs {
   float scale_log2;           // scale * log2(e)
 };
 constexpr int kAttnMaxCtas = 160;
-constexpr size_t kAttnTicketBytes = 1024;
+constexpr size_t kAttnTicketBytes = 2048;
 constexpr int kAttnFewRows = 16;
-// bytes of a piece's sums, maxima and totals
-constexpr size_t attn_piece_bytes(int rows, int D) { return static_cast<size_t>(rows) * ((D <= 64 ? 64 : 128) + 2) * 4; }
+// bytes of a piece's sums, maxima and totals (and of the last two for a group of pieces)
+constexpr size_t attn_piece_bytes(int rows, int D) { return static_cast<size_t>(rows) * ((D <= 64 ? 64 : 128) + 4) * 4; }
 // `rows` of a key head's queries, up to kAttnFewRows, and more of them (any number is right in both).
 cudaError_t launch_attention_few(const AttnArgs& a, int rows, int sms, cudaStream_t s);
 constexpr int kAttnRows = 256;

@@ -191,6 +191,11 @@ CASES = [  # new tokens, lengths, Hq, Hkv, D, dtype, cache, page, order
     ([260], [400], 5, 1, 128, "bf16", "bf16", 128, "token"),
     ([65, 64, 63], [65, 192, 511], 8, 1, 48, "bf16", "bf16", 16, "head"),
     ([129, 2], [129, 258], 3, 1, 112, "f16", "e4m3", 16, "head"),
+    # one item over many SMs: pieces joined in groups
+    ([1], [30000], 4, 1, 64, "bf16", "bf16", 64, "head"),
+    ([2, 1], [40000, 100], 8, 1, 64, "f16", "e4m3", 256, "head"),
+    ([3], [30011], 16, 1, 64, "bf16", "e4m3", 64, "token"),
+    ([7, 2], [29000, 5000], 13, 1, 128, "bf16", "bf16", 64, "head"),
 ]
 
 
