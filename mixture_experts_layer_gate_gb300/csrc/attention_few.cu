@@ -118,6 +118,15 @@ __global__ void __launch_bounds__(32 * kWarpsOf<E4M3, NT>, 1) attention_few_kern
     return paged && key < w.s.L ? a.page_table[w.b * a.table_stride + (key >> a.page_shift)] : 0;
   };
   int page = page_of(iss), slot_i = 0;
+  // this lane's first key and piece of the item's head
+  constexpr int64_t size = E4M3 ? 1 : 2;
+  const uint8_t *k_head, *v_head;
+  auto enter = [&] {
+    k_head = a.kv.k + size * (my_key * a.kv.k_token + iss.h * a.kv.k_head) + 16 * my_piece;
+    v_head = a.kv.v + size * (my_key * a.kv.v_token + iss.h * a.kv.v_head) + 16 * my_piece;
+  };
+  enter();
+  const int64_t k_step = size * kPerLoad * a.kv.k_token, v_step = size * kPerLoad * a.kv.v_token;
   auto issue = [&] {
     if (more) {
       const int key0 = iss.t * kTile + warp * kKeys;
@@ -127,18 +136,30 @@ __global__ void __launch_bounds__(32 * kWarpsOf<E4M3, NT>, 1) attention_few_kern
         if (!good && lane == 0) record_error(a.err, kErrBadIndex, static_cast<uint32_t>(iss.b));
         const int64_t place = paged ? (key0 & page_mask) : static_cast<int64_t>(iss.s.row0 + key0);
         const int64_t from = good ? page : 0;
-        constexpr int64_t size = E4M3 ? 1 : 2;
-        const uint8_t* k = a.kv.k + size * (from * a.kv.k_page + (place + my_key) * a.kv.k_token + iss.h * a.kv.k_head) + 16 * my_piece;
-        const uint8_t* v = a.kv.v + size * (from * a.kv.v_page + (place + my_key) * a.kv.v_token + iss.h * a.kv.v_head) + 16 * my_piece;
-        const int64_t k_step = size * kPerLoad * a.kv.k_token, v_step = size * kPerLoad * a.kv.v_token;
-        const int there = good && in_head ? iss.s.L - key0 - my_key : 0;  // keys of this lane's column of loads
-#pragma unroll
-        for (int i = 0; i < kKeys / kPerLoad; ++i) {
+        const uint8_t* k = k_head + size * (from * a.kv.k_page + place * a.kv.k_token);
+        const uint8_t* v = v_head + size * (from * a.kv.v_page + place * a.kv.v_token);
+        auto k_at = [&](int i) {
           const int key = i * kPerLoad + my_key;
-          const bool in = i * kPerLoad < there;
-          cp_async16_if(dst + static_cast<uint32_t>(key * kRow + 16 * k_piece<E4M3, DP>(key, my_piece)), in ? k + i * k_step : a.kv.k, in);
-          cp_async16_if(dst + static_cast<uint32_t>((kKeys + key) * kRow + 16 * v_piece<E4M3, DP>(key, my_piece)),
-                        in ? v + i * v_step : a.kv.v, in);
+          return dst + static_cast<uint32_t>(key * kRow + 16 * k_piece<E4M3, DP>(key, my_piece));
+        };
+        auto v_at = [&](int i) {
+          const int key = i * kPerLoad + my_key;
+          return dst + static_cast<uint32_t>((kKeys + key) * kRow + 16 * v_piece<E4M3, DP>(key, my_piece));
+        };
+        if (good && key0 + kKeys <= iss.s.L && a.D == DP) {
+#pragma unroll
+          for (int i = 0; i < kKeys / kPerLoad; ++i, k += k_step, v += v_step) {
+            cp_async16(k_at(i), k);
+            cp_async16(v_at(i), v);
+          }
+        } else {
+          const int there = good && in_head ? iss.s.L - key0 - my_key : 0;  // keys of this lane's column of loads
+#pragma unroll 1
+          for (int i = 0; i < kKeys / kPerLoad; ++i, k += k_step, v += v_step) {
+            const bool in = i * kPerLoad < there;
+            cp_async16_if(k_at(i), in ? k : a.kv.k, in);
+            cp_async16_if(v_at(i), in ? v : a.kv.v, in);
+          }
         }
         if (E4M3 && lane < 8) {
           const float* s = lane < 4 ? a.kv.k_scale : a.kv.v_scale;
@@ -146,7 +167,10 @@ __global__ void __launch_bounds__(32 * kWarpsOf<E4M3, NT>, 1) attention_few_kern
           cp_async16_if(dst + static_cast<uint32_t>(2 * kKeys * kRow + 16 * lane), good ? s + at : s, good);
         }
       }
-      if (++iss.t == iss.end) more = iss.next(a);
+      if (++iss.t == iss.end) {
+        more = iss.next(a);
+        enter();
+      }
       if (more) page = page_of(iss);
     }
     cp_async_commit();
