@@ -11,6 +11,8 @@ using namespace moe;
 
 namespace {
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 bool page_size_ok(int n) { return n >= 16 && n <= 1024 && (n & (n - 1)) == 0; }
 int shift_of(int n) {
   int s = 0;
@@ -52,7 +54,7 @@ moe_status_t validate_attention(const moe_attention_t* p) {
   if (p == nullptr || p->T < 0 || p->B < 0 || p->Hq < 1 || p->Hkv < 1 || p->Hq % p->Hkv != 0) return MOE_ERR_INVALID_ARG;
   if (p->D < 8 || p->D % 8 != 0 || p->max_q < 1 || !half_dtype(p->dtype)) return MOE_ERR_INVALID_ARG;
   if (p->cache_dtype < MOE_CACHE_SAME || p->cache_dtype > MOE_CACHE_E4M3) return MOE_ERR_INVALID_ARG;
-  if (!(p->scale > 0.f) || !std::isfinite(p->scale)) return MOE_ERR_INVALID_ARG;
+  if (!(p->scale > 0.f) || !std::isfinite(p->scale * kLog2e)) return MOE_ERR_INVALID_ARG;
   if (p->D > 128 || p->Hq > 4096 || p->B > (1 << 20)) return MOE_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(p->T) * p->Hq > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
@@ -97,7 +99,7 @@ moe_status_t attend(const moe_attention_t* p, AttnArgs& a, const void* q, int64_
   a.D = p->D;
   a.G = p->Hq / p->Hkv;
   a.f16 = p->dtype == MOE_T_F16;
-  a.scale_log2 = p->scale * 1.4426950408889634f;
+  a.scale_log2 = p->scale * kLog2e;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return cuda_status(few_rows(*p) ? launch_attention_few(a, p->max_q * a.G, di.sms, s) : launch_attention(a, di.sms, s));
 }

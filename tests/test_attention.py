@@ -55,7 +55,7 @@ def test_refuses_problems(lib):
     assert call(lib, None) == INVALID
     for bad in (dict(T=-1), dict(B=-1), dict(Hq=0), dict(Hkv=0), dict(Hq=6), dict(D=0), dict(D=60), dict(max_q=0),
                 dict(dtype=2), dict(cache_dtype=2), dict(page_size=8), dict(page_size=24), dict(num_pages=0),
-                dict(max_pages=0), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf)):
+                dict(max_pages=0), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf), dict(scale=3e38)):
         p = paged()
         for n, v in bad.items():
             setattr(p, n, v)
@@ -196,6 +196,11 @@ CASES = [  # new tokens, lengths, Hq, Hkv, D, dtype, cache, page, order
     ([2, 1], [40000, 100], 8, 1, 64, "f16", "e4m3", 256, "head"),
     ([3], [30011], 16, 1, 64, "bf16", "e4m3", 64, "token"),
     ([7, 2], [29000, 5000], 13, 1, 128, "bf16", "bf16", 64, "head"),
+    # the narrowest heads, and odd groups, in tiles of 128 rows
+    ([40, 3], [40, 200], 2, 2, 8, "bf16", "bf16", 16, "token"),
+    ([33], [150], 4, 2, 16, "f16", "e4m3", 32, "token"),
+    ([9, 5], [300, 77], 71, 1, 64, "bf16", "bf16", 16, "head"),
+    ([1, 3], [130, 60], 142, 2, 32, "f16", "e4m3", 16, "head"),
 ]
 
 
@@ -412,6 +417,30 @@ def test_captured_calls_follow_the_lengths(dev, cache, new):
         go(side.cuda_stream)
         side.synchronize()
         assert torch.equal(out, got)
+
+
+@gpu
+@pytest.mark.parametrize("new", [1, 20])
+def test_more_sequences_than_threads(dev, new):
+    B = 1100
+    case = ([new if i % 97 == 5 else 1 if i % 3 else 0 for i in range(B)], [i * 7 % 90 if i % 97 != 5 else 20 + i % 70 for i in range(B)],
+            2, 1, 16, "bf16", "bf16", 16, "token")
+    case[1][::3] = [n if m else 3 for n, m in zip(case[1][::3], case[0][::3])]
+    problem, args, q, keys, cu, _ = build(dev, *case)
+    out, lse, ws = run(problem, args, dev)
+    assert moe.get_device_error(ws) == 0
+    compare(problem, out, lse, q, keys, cu, "bf16", "bf16", None)
+
+
+@gpu
+def test_more_new_tokens_than_promised(dev):
+    """max_q chooses the kernel: one too small costs time, not results."""
+    case = ([40, 1], [90, 33], 4, 1, 64, "bf16", "bf16", 16, "token")
+    problem, args, q, keys, cu, _ = build(dev, *case)
+    problem.max_q = 1
+    out, lse, ws = run(problem, args, dev)
+    assert moe.get_device_error(ws) == 0
+    compare(problem, out, lse, q, keys, cu, "bf16", "bf16", None)
 
 
 @gpu
