@@ -270,7 +270,6 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
   pdl_wait();
   pdl_trigger();
   const uint32_t tmem = *tmem_slot;
-  clear_empty_rows(a);
   BigWalk w;
   const bool some = start<kThreads<E4M3>>(a, scratch, w);
   __syncthreads();
@@ -1057,6 +1056,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
 #undef CEMPTY
 #undef IFULL
 #undef IEMPTY
+  clear_empty_rows(a);
   if (tid == 0 && *abort_flag != 0) record_error(a.err, kErrTimeout, static_cast<uint32_t>(*abort_flag));
   if (warp == 9) {
     tc_fence_after();

@@ -222,11 +222,12 @@ __device__ __forceinline__ bool start(const AttnArgs& a, int64_t* scratch, Walk<
   if (warp < 2) {
     const int c = cta + warp;  // the CTA that begins here
     Place p = {a.B, 0, 0, 0};
-    int first = cta, pieces = 1;
+    int first = cta, pieces = 1, from_b = -1;
+    Seq s{};
     if (c < n) {
-      p.b = static_cast<int>(scratch[32 + 2 * warp]);
+      from_b = p.b = static_cast<int>(scratch[32 + 2 * warp]);
       int64_t rest = scratch[33 + 2 * warp];
-      Seq s = sequence(a, p.b, false);
+      s = sequence(a, p.b, false);
       int R = row_tiles<M>(s, a.G);
       // the last row tile that starts at or before `rest`: 32 candidates at a time, the
       // first time with the whole head's cost as one more
@@ -276,6 +277,7 @@ __device__ __forceinline__ bool start(const AttnArgs& a, int64_t* scratch, Walk<
     if (lane == 0) {
       int* to = found + 6 * warp;
       to[0] = p.b, to[1] = p.h, to[2] = p.r, to[3] = p.t, to[4] = first, to[5] = pieces;
+      if (warp == 0 && p.b < a.B) *reinterpret_cast<Seq*>(found + 12) = p.b == from_b ? s : sequence(a, p.b, false);
     }
   }
   __syncthreads();
@@ -285,7 +287,7 @@ __device__ __forceinline__ bool start(const AttnArgs& a, int64_t* scratch, Walk<
   w.pieces = found[5];
   w.pieces_last = found[11];
   if (w.b >= a.B || (w.b == w.stop.b && w.h == w.stop.h && w.r == w.stop.r && w.t == w.stop.t)) return false;
-  w.s = sequence(a, w.b, false);
+  w.s = *reinterpret_cast<const Seq*>(found + 12);
   w.R = row_tiles<M>(w.s, a.G);
   w.enter(a);
   return true;

@@ -101,9 +101,11 @@ __global__ void __launch_bounds__(32 * kWarpsOf<E4M3, NT>, 1) attention_few_kern
                         static_cast<uint32_t>(warp * depth * kStage);
   pdl_wait();
   pdl_trigger();
-  clear_empty_rows(a);
   FewWalk cur;
-  if (!start<kThreads>(a, scratch, cur)) return;
+  if (!start<kThreads>(a, scratch, cur)) {
+    clear_empty_rows(a);
+    return;
+  }
 
   // ---- loads, ahead of the products
   FewWalk iss = cur;
@@ -630,6 +632,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<E4M3, NT>, 1) attention_few_kern
     }
     going = cur.next(a);
   }
+  clear_empty_rows(a);
 }
 
 template <bool E4M3, bool F16, int DP, int NT>
