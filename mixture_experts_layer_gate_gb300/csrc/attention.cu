@@ -466,8 +466,6 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
       auto there = [&](int info) {
         return (E4M3 || wait(READY(st), ph, abort_flag, info)) && wait(FULL(st), ph, abort_flag, info);
       };
-      // (unrolled the issue is faster, but the 8-bit kernel outgrows the instruction caches)
-      constexpr int kUnrolled = 2;
       auto tile_at = [&](int s) { return ring + static_cast<uint32_t>(s) * kTile; };
       for (int item = 0; ok; ++item) {
         const Item* it = take(item);
@@ -499,11 +497,11 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
             ok = ok && there(0x724);
             step();
           }
-#pragma unroll kUnrolled
+#pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const int ends = i == 0 ? e[0] : e[1];
+            const int ends = e[i];
             if (ok && t < ends) {
-#pragma unroll kUnrolled
+#pragma unroll
               for (int part = 0; part < 2 && ok; ++part) {
                 ok = wait(PFULL(i, part), pph >> i & 1u, abort_flag, 0x725);
                 if (!ok) break;
