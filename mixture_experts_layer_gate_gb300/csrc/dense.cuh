@@ -78,7 +78,7 @@ struct Params {
   int fmt;               // 16-bit operands: 1 bf16, 0 f16
   int out_dtype;         // moe_dtype_t
   int accumulate;
-  int act;               // moe_activation_t (EPI 2, 3)
+  float act[2];          // of the activation (EPI 1, 2)
   int vec_bias;          // bias takes 16-byte loads
   int vec;               // rows of out (and old) take 16-byte accesses
   int tma_out;           // 256-column tiles are stored by TMA
@@ -247,17 +247,19 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, f
          (static_cast<uint32_t>(f32x2_to_e4m3x2(__fdiv_rn(c, scale), __fdiv_rn(d, scale))) << 16);
 }
 
-// What becomes of a sum before old is added: EPI 0 nothing, 1 the bias, 2 the bias
-// and an activation other than the error function's, 3 that one (kernels of their
-// own: its polynomial for 128 sums a thread is most of the code).
+// What becomes of a sum before old is added: EPI 0 nothing; 1 the bias, then zero where
+// it is below act[0] (minus infinity, or 0 for relu); 2 the bias, then v / (1 + exp(-v
+// (act[0] + act[1] v^2))), which is silu with (1, 0) and gelu's tanh form with (2 sqrt(2 /
+// pi), 0.044715 of that), as (1 + tanh z) / 2 = 1 / (1 + exp(-2 z)); 3 the bias and gelu.
+// Numbers instead of branches: one for each of 128 sums a thread took longer than the
+// activation (M = 2300, N = 2704, K = 1000, silu 42 us, none 20).
 template <int EPI>
-__device__ __forceinline__ float activated(float v, int act) {
+__device__ __forceinline__ float activated(const float (&act)[2], float v) {
+  if (EPI == 1) return v < act[0] ? 0.f : v;
   if (EPI == 2) {
-    if (act == 4) return v < 0.f ? 0.f : v;
-    // silu(v) = v / (1 + exp(-v)), and (1 + tanh z) / 2 = 1 / (1 + exp(-2 z))
-    const float y = act == 1 ? v : v * fmaf(v * v, 0.044715f * 1.5957691216057308f, 1.5957691216057308f);
-    const float e = expf(-y);
-    return e > 8e37f ? v * 0.f : __fdividef(v, 1.0f + e);
+    // (v^2 stays finite for the factor 0; where the denominator passes 2^126 the quotient is zero)
+    const float y = v * fmaf(fminf(v * v, 1e30f), act[1], act[0]);
+    return __fdividef(v, 1.0f + __expf(-y));
   }
   if (EPI == 3) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
   return v;
@@ -285,8 +287,8 @@ __device__ __forceinline__ void store4(const Params& p, int64_t row, int col, fl
   const int64_t at = row * p.out_stride + col, from = row * p.old_stride + col;
   if (EPI > 0) {
     const float4 b = p.bias != nullptr ? bias4(p, col) : make_float4(0.f, 0.f, 0.f, 0.f);
-    v = make_float4(activated<EPI>(v.x + b.x, p.act), activated<EPI>(v.y + b.y, p.act),
-                    activated<EPI>(v.z + b.z, p.act), activated<EPI>(v.w + b.w, p.act));
+    v = make_float4(activated<EPI>(p.act, v.x + b.x), activated<EPI>(p.act, v.y + b.y),
+                    activated<EPI>(p.act, v.z + b.z), activated<EPI>(p.act, v.w + b.w));
   }
   float f[4] = {v.x, v.y, v.z, v.w};
   if (p.vec && col + 4 <= p.N) {
@@ -325,21 +327,22 @@ __device__ __forceinline__ void store4(const Params& p, int64_t row, int col, fl
     }
     return;
   }
+  // (all loads before the first store, which might be to the same place for all the
+  // compiler knows: one after the other their latencies add up)
+  if (p.accumulate) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (col + j < p.N)
+        f[j] += p.out_dtype == 2   ? static_cast<const float*>(p.old)[from + j]
+                : p.out_dtype == 1 ? __half2float(static_cast<const __half*>(p.old)[from + j])
+                                   : __bfloat162float(static_cast<const __nv_bfloat16*>(p.old)[from + j]);
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (col + j >= p.N) return;
-    if (p.out_dtype == 0) {
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + at + j;
-      const __nv_bfloat16* u = static_cast<const __nv_bfloat16*>(p.old) + from + j;
-      *o = __float2bfloat16_rn(p.accumulate ? f[j] + __bfloat162float(*u) : f[j]);
-    } else if (p.out_dtype == 1) {
-      __half* o = static_cast<__half*>(p.out) + at + j;
-      const __half* u = static_cast<const __half*>(p.old) + from + j;
-      *o = __float2half_rn(p.accumulate ? f[j] + __half2float(*u) : f[j]);
-    } else {
-      float* o = static_cast<float*>(p.out) + at + j;
-      *o = p.accumulate ? f[j] + static_cast<const float*>(p.old)[from + j] : f[j];
-    }
+    if (p.out_dtype == 0) static_cast<__nv_bfloat16*>(p.out)[at + j] = __float2bfloat16_rn(f[j]);
+    else if (p.out_dtype == 1) static_cast<__half*>(p.out)[at + j] = __float2half_rn(f[j]);
+    else static_cast<float*>(p.out)[at + j] = f[j];
   }
 }
 
@@ -696,6 +699,13 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
       };
       if (fetch && live)
         for (int i = 0; i < p.boxes; ++i) fetch_box(i);
+      if (EPI > 0 && p.accumulate && !p.tma_out && row < p.M) {
+        // plain loads at the tile's end take what the sums are added to; it comes to L2 now
+        const int64_t size = p.out_dtype == 2 ? 4 : 2, at = row * p.old_stride + n0 + W * half;
+        const char* from = static_cast<const char*>(p.old) + size * at;
+        const int64_t bytes = size * min(W, p.N - n0 - W * half);
+        for (int64_t i = 0; i < bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i) : "memory");
+      }
       uint64_t acc[W / 2];
 #pragma unroll
       for (int i = 0; i < W / 2; ++i) acc[i] = 0;
@@ -827,8 +837,8 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
               u = make_float2(u.x + add.x, u.y + add.y);
               v = make_float2(v.x + add.z, v.y + add.w);
             }
-            return make_float4(activated<EPI>(u.x, p.act), activated<EPI>(u.y, p.act), activated<EPI>(v.x, p.act),
-                               activated<EPI>(v.y, p.act));
+            return make_float4(activated<EPI>(p.act, u.x), activated<EPI>(p.act, u.y), activated<EPI>(p.act, v.x),
+                               activated<EPI>(p.act, v.y));
           };
           auto box = [&](int i, auto&& piece) {  // piece(j, old): 16 bytes
             const uint32_t slot = static_cast<uint32_t>(i & (p.boxes - 1));

@@ -31,7 +31,9 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
   p.fmt = a.f16 ? 0 : 1;
   p.out_dtype = a.out_dtype;
   p.accumulate = a.residual != nullptr;
-  p.act = a.act;
+  constexpr float kTwice = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+  p.act[0] = a.act == 4 ? 0.f : a.act == 0 ? -INFINITY : a.act == 1 ? 1.f : kTwice;
+  p.act[1] = a.act == 3 ? 0.044715f * kTwice : 0.f;
   p.vec_bias = reinterpret_cast<uintptr_t>(a.bias) % 8 == 0;
   const int64_t osz = a.out_dtype == 2 ? 4 : 2;
   auto wide = [&](const void* q, int64_t stride) {
@@ -44,7 +46,7 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
     return dense::plan_and_launch<dense::kHalf, decltype(epi)::value>(p, c.bn, c.pair, false, a.x, a.x_stride, a.w,
                                                                       a.w_stride, a.N, a.K, di.sms, s);
   };
-  if (a.act == 0) return launch(std::integral_constant<int, 1>());
+  if (a.act == 0 || a.act == 4) return launch(std::integral_constant<int, 1>());
   if (a.act == 2) return launch(std::integral_constant<int, 3>());
   return launch(std::integral_constant<int, 2>());
 }
