@@ -21,6 +21,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -66,9 +67,7 @@ struct Params {
   uint8_t* codes;        // SwiGLU
   float* scales;         // SwiGLU
   uint32_t* err;
-  const void* old;       // what the product is added to (accumulate): out, or a residual of its type
-  const void* bias;      // [N] of the operands' type, or null (EPI)
-  int64_t a_scale_stride, out_stride, old_stride;
+  int64_t a_scale_stride, out_stride;
   int M, N, KB;
   int group;             // k-blocks per accumulator
   int P;                 // CTAs of a cluster that split K (not PAIR)
@@ -78,13 +77,28 @@ struct Params {
   int fmt;               // 16-bit operands: 1 bf16, 0 f16
   int out_dtype;         // moe_dtype_t
   int accumulate;
-  float act[2];          // of the activation (EPI 1, 2)
-  int vec_bias;          // bias takes 16-byte loads
   int vec;               // rows of out (and old) take 16-byte accesses
   int tma_out;           // 256-column tiles are stored by TMA
   int boxes;             // of each joining warp, for that: 1, 2 or 4
   int vec_scale;         // rows of a_scale take 16-byte loads at multiples of four blocks
 };
+
+// With an epilogue (EPI).  A struct of its own: one more word in Params and the SwiGLU
+// pair's kernel, which has not one register left, spills in its main loop (M = 4096,
+// I = 2048, K = 7168: 104 -> 124 us).
+struct EpilogueParams : Params {
+  const void* old;       // what the product is added to (accumulate): out, or a residual of its type
+  const void* bias;      // [N] of the operands' type, or null
+  int64_t old_stride;
+  float act[2];          // of the activation (EPI 1, 2)
+  int vec_bias;          // bias takes 16-byte loads
+};
+template <int EPI>
+using ParamsOf = std::conditional_t<(EPI > 0), EpilogueParams, Params>;
+__host__ __device__ __forceinline__ const void* old_of(const Params& p) { return p.out; }
+__host__ __device__ __forceinline__ const void* old_of(const EpilogueParams& p) { return p.old; }
+__host__ __device__ __forceinline__ int64_t old_stride_of(const Params& p) { return p.out_stride; }
+__host__ __device__ __forceinline__ int64_t old_stride_of(const EpilogueParams& p) { return p.old_stride; }
 
 struct Maps {
   CUtensorMap a, w, out, old;
@@ -247,7 +261,7 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, f
          (static_cast<uint32_t>(f32x2_to_e4m3x2(__fdiv_rn(c, scale), __fdiv_rn(d, scale))) << 16);
 }
 
-// What becomes of a sum before old is added: EPI 0 nothing; 1 the bias, then zero where
+// What becomes of a sum before old is added: EPI 1 the bias, then zero where
 // it is below act[0] (minus infinity, or 0 for relu); 2 the bias, then v / (1 + exp(-v
 // (act[0] + act[1] v^2))), which is silu with (1, 0) and gelu's tanh form with (2 sqrt(2 /
 // pi), 0.044715 of that), as (1 + tanh z) / 2 = 1 / (1 + exp(-2 z)); 3 the bias and gelu.
@@ -261,15 +275,14 @@ __device__ __forceinline__ float activated(const float (&act)[2], float v) {
     const float y = v * fmaf(fminf(v * v, 1e30f), act[1], act[0]);
     return __fdividef(v, 1.0f + __expf(-y));
   }
-  if (EPI == 3) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-  return v;
+  return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
 }
-__device__ __forceinline__ float bias_at(const Params& p, int col) {
+__device__ __forceinline__ float bias_at(const EpilogueParams& p, int col) {
   const uint16_t b = static_cast<const uint16_t*>(p.bias)[col];
   return p.fmt == 1 ? __uint_as_float(static_cast<uint32_t>(b) << 16) : __half2float(__ushort_as_half(b));
 }
 // of four columns, zero past N
-__device__ __forceinline__ float4 bias4(const Params& p, int col) {
+__device__ __forceinline__ float4 bias4(const EpilogueParams& p, int col) {
   if (p.vec_bias && col + 4 <= p.N) {
     const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.bias) + col);
     if (p.fmt == 1) return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
@@ -283,9 +296,9 @@ __device__ __forceinline__ float4 bias4(const Params& p, int col) {
 
 // out[row, col .. col + 3] of four sums
 template <int EPI>
-__device__ __forceinline__ void store4(const Params& p, int64_t row, int col, float4 v) {
-  const int64_t at = row * p.out_stride + col, from = row * p.old_stride + col;
-  if (EPI > 0) {
+__device__ __forceinline__ void store4(const ParamsOf<EPI>& p, int64_t row, int col, float4 v) {
+  const int64_t at = row * p.out_stride + col, from = row * old_stride_of(p) + col;
+  if constexpr (EPI > 0) {
     const float4 b = p.bias != nullptr ? bias4(p, col) : make_float4(0.f, 0.f, 0.f, 0.f);
     v = make_float4(activated<EPI>(p.act, v.x + b.x), activated<EPI>(p.act, v.y + b.y),
                     activated<EPI>(p.act, v.z + b.z), activated<EPI>(p.act, v.w + b.w));
@@ -295,14 +308,14 @@ __device__ __forceinline__ void store4(const Params& p, int64_t row, int col, fl
     if (p.out_dtype == 2) {
       float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
       if (p.accumulate) {
-        const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(p.old) + from);
+        const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(old_of(p)) + from);
         v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
       }
       *o = v;
     } else {
       uint2* o = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at);
       uint2 u = make_uint2(0, 0);
-      if (p.accumulate) u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.old) + from);
+      if (p.accumulate) u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(old_of(p)) + from);
       if (p.out_dtype == 0) {
         if (p.accumulate) {
           f[0] += bf16_lo(u.x);
@@ -333,9 +346,9 @@ __device__ __forceinline__ void store4(const Params& p, int64_t row, int col, fl
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (col + j < p.N)
-        f[j] += p.out_dtype == 2   ? static_cast<const float*>(p.old)[from + j]
-                : p.out_dtype == 1 ? __half2float(static_cast<const __half*>(p.old)[from + j])
-                                   : __bfloat162float(static_cast<const __nv_bfloat16*>(p.old)[from + j]);
+        f[j] += p.out_dtype == 2   ? static_cast<const float*>(old_of(p))[from + j]
+                : p.out_dtype == 1 ? __half2float(static_cast<const __half*>(old_of(p))[from + j])
+                                   : __bfloat162float(static_cast<const __nv_bfloat16*>(old_of(p))[from + j]);
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -432,7 +445,8 @@ __device__ __forceinline__ void load_box(uint32_t leader, uint32_t dst, const vo
 // fetches the old values costs the storing one 51 -> 57 us at M = 4096, N = 7168,
 // K = 2048); of narrower tiles p.accumulate tells.
 template <int KIND, bool SWIGLU, bool PAIR, int BN, bool ADD, int EPI>
-__global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constant__ Maps maps, const Params p) {
+__global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constant__ Maps maps,
+                                                             const ParamsOf<EPI> p) {
   static_assert(!SWIGLU || BN == 256, "gate and up halves of 128 columns");
   static_assert(!PAIR || BN == 256, "a pair's halves are 128 weight rows");
   static_assert(!ADD || (BN == 256 && !SWIGLU), "narrower tiles add at run time");
@@ -699,12 +713,14 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
       };
       if (fetch && live)
         for (int i = 0; i < p.boxes; ++i) fetch_box(i);
-      if (EPI > 0 && p.accumulate && !p.tma_out && row < p.M) {
-        // plain loads at the tile's end take what the sums are added to; it comes to L2 now
-        const int64_t size = p.out_dtype == 2 ? 4 : 2, at = row * p.old_stride + n0 + W * half;
-        const char* from = static_cast<const char*>(p.old) + size * at;
-        const int64_t bytes = size * min(W, p.N - n0 - W * half);
-        for (int64_t i = 0; i < bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i) : "memory");
+      if constexpr (EPI > 0) {
+        if (p.accumulate && !p.tma_out && row < p.M) {
+          // plain loads at the tile's end take what the sums are added to; it comes to L2 now
+          const int64_t size = p.out_dtype == 2 ? 4 : 2, at = row * p.old_stride + n0 + W * half;
+          const char* from = static_cast<const char*>(p.old) + size * at;
+          const int64_t bytes = size * min(W, p.N - n0 - W * half);
+          for (int64_t i = 0; i < bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i) : "memory");
+        }
       }
       uint64_t acc[W / 2];
 #pragma unroll
@@ -832,13 +848,16 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
         if (live) {
           auto finished = [&](int col, uint64_t a, uint64_t b) {  // two pairs of sums, of columns col ..
             float2 u = unpair(a), v = unpair(b);
-            if (EPI > 0 && p.bias != nullptr) {
-              const float4 add = bias4(p, col);
-              u = make_float2(u.x + add.x, u.y + add.y);
-              v = make_float2(v.x + add.z, v.y + add.w);
+            if constexpr (EPI > 0) {
+              if (p.bias != nullptr) {
+                const float4 add = bias4(p, col);
+                u = make_float2(u.x + add.x, u.y + add.y);
+                v = make_float2(v.x + add.z, v.y + add.w);
+              }
+              u = make_float2(activated<EPI>(p.act, u.x), activated<EPI>(p.act, u.y));
+              v = make_float2(activated<EPI>(p.act, v.x), activated<EPI>(p.act, v.y));
             }
-            return make_float4(activated<EPI>(p.act, u.x), activated<EPI>(p.act, u.y), activated<EPI>(p.act, v.x),
-                               activated<EPI>(p.act, v.y));
+            return make_float4(u.x, u.y, v.x, v.y);
           };
           auto box = [&](int i, auto&& piece) {  // piece(j, old): 16 bytes
             const uint32_t slot = static_cast<uint32_t>(i & (p.boxes - 1));
@@ -1023,7 +1042,7 @@ size_t smem_bytes(const Params& p, int bn, bool pair) {
 }
 
 template <int KIND, bool SWIGLU, bool PAIR, int BN, bool ADD = false, int EPI = 0>
-cudaError_t launch(const Maps& maps, const Params& p, int grid, cudaStream_t s) {
+cudaError_t launch(const Maps& maps, const ParamsOf<EPI>& p, int grid, cudaStream_t s) {
   static int configured[64] = {};
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
@@ -1088,7 +1107,7 @@ inline Choice choose(int M, int N, int KB, bool swiglu, bool e4m3, int sms, bool
 // mt, nt, arows and stages.  a [M, K] and w [wrows_total, K] of 1-byte (kE4M3)
 // or 2-byte elements, strides in elements.
 template <int KIND, int EPI = 0>
-cudaError_t plan_and_launch(Params p, int bn, bool pair, bool swiglu, const void* a, int64_t a_stride, const void* w,
+cudaError_t plan_and_launch(ParamsOf<EPI> p, int bn, bool pair, bool swiglu, const void* a, int64_t a_stride, const void* w,
                             int64_t w_stride, int64_t w_total, int64_t K, int sms, cudaStream_t s) {
   const uint64_t esz = KIND == kE4M3 ? 1 : 2;
   const CUtensorMapDataType dt = KIND == kE4M3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
@@ -1119,9 +1138,9 @@ cudaError_t plan_and_launch(Params p, int bn, bool pair, bool swiglu, const void
     if (!encode_map(&maps.out, osz == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.out,
                     dims, str, box, CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorInvalidValue;
-    const uint64_t old_str[1] = {static_cast<uint64_t>(p.old_stride) * osz};
+    const uint64_t old_str[1] = {static_cast<uint64_t>(old_stride_of(p)) * osz};
     if (p.accumulate && !encode_map(&maps.old, osz == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                                    2, p.old, dims, old_str, box, CU_TENSOR_MAP_SWIZZLE_64B))
+                                    2, old_of(p), dims, old_str, box, CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorInvalidValue;
   }
   {

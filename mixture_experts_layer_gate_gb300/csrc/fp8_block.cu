@@ -26,8 +26,6 @@ cudaError_t launch_fp8_block(const Fp8GemmArgs& g, cudaStream_t s) {
   p.err = g.err;
   p.a_scale_stride = g.a_scale_stride;
   p.out_stride = g.out_stride;
-  p.old = g.out;
-  p.old_stride = g.out_stride;
   p.M = g.M;
   p.N = g.N;
   p.KB = KB;

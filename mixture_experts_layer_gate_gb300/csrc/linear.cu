@@ -17,7 +17,7 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
   cudaError_t err = device_info(&di);
   if (err != cudaSuccess) return err;
   if (a.M <= kLinearFewRows) return launch_linear_few(a, s);
-  dense::Params p = {};
+  dense::EpilogueParams p = {};
   p.out = a.out;
   p.old = a.residual;
   p.bias = a.bias;
