@@ -8,12 +8,15 @@
 // (two per tensor-memory lane quarter: warp w holds rows 32 (w % 4) .. + 31,
 // one per lane, and one half of the columns) add the finished one, times the
 // scales of its block, to the tile's sums, which stay in registers.  The 8-bit
-// product joins every k-block, which is its scale block; the 16-bit one every
-// 16 (1024 values), which only bounds the length of the tensor core's own sums.
+// product joins every k-block, which is its scale block; the router's every 16
+// (1024 values), which only bounds the length of the tensor core's own sums, and
+// moe_linear's none before the tile's end.
 //
 // PAIR: two CTAs share MMAs of M = 256 (cta_group::2): each loads its own 128
 // rows and half of the columns' weights, which halves the weight traffic from
-// L2 per product.  Else P CTAs of a cluster take P ranges of K of one tile and
+// L2 per product.  Of 128 columns (16-bit, a few hundred rows) they read 24 KB a
+// k-block each where a CTA alone reads 32 (M = 512, N = K = 4096 18.7 -> 16.9 us, M =
+// 1024, N = 6144 42.0 -> 37.6).  Else P CTAs of a cluster take P ranges of K of one tile and
 // join their sums through distributed shared memory in rank order (no atomics:
 // the order is fixed).
 #pragma once
@@ -104,9 +107,9 @@ struct Maps {
   CUtensorMap a, w, out, old;
 };
 
-__host__ __device__ constexpr int wrows(int bn, bool pair) { return pair ? 128 : (bn < 128 ? bn : 128); }
+__host__ __device__ constexpr int wrows(int bn, bool pair) { return pair ? bn / 2 : (bn < 128 ? bn : 128); }
 __host__ __device__ constexpr int stage_bytes(int arows, int bn, bool pair) {
-  return arows * 128 + (pair ? 128 : bn) * 128;
+  return arows * 128 + (pair ? bn / 2 : bn) * 128;
 }
 // shared row of a split-K partial, padded so that 8 lanes' 16-byte stores of 8
 // rows fall into different banks
@@ -448,7 +451,7 @@ template <int KIND, bool SWIGLU, bool PAIR, int BN, bool ADD, int EPI>
 __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constant__ Maps maps,
                                                              const ParamsOf<EPI> p) {
   static_assert(!SWIGLU || BN == 256, "gate and up halves of 128 columns");
-  static_assert(!PAIR || BN == 256, "a pair's halves are 128 weight rows");
+  static_assert(!PAIR || BN == 256 || (BN == 128 && KIND == kHalf), "a pair's halves are 128 or 64 weight rows");
   static_assert(!ADD || (BN == 256 && !SWIGLU), "narrower tiles add at run time");
   constexpr int W = BN / 2;              // columns per joining warp
   constexpr int CH = W < 32 ? W : 32;    // columns per tensor-memory load
@@ -541,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) dense_kernel(const __grid_constan
         const int m0 = (t % p.mt) * kTileM + (PAIR ? 128 * static_cast<int>(rank) : 0);
         const int n0 = (t / p.mt) * (SWIGLU ? 128 : BN);
         // the weight rows: PAIR loads one half here, the peer the other
-        const int second = SWIGLU ? n0 + p.N : n0 + 128;
+        const int second = SWIGLU ? n0 + p.N : n0 + (PAIR ? BN / 2 : 128);
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait(EMPTY(st), ph ^ 1u, abort_flag, p.err, 0x600u)) {
             ok = false;
@@ -1072,7 +1075,8 @@ struct Choice {
 // The candidate with the least estimated time in cycles: rounds of the SMs times
 // (k-blocks of a CTA times a k-block's time, and the tile's end).  The k-block
 // times are measured ones of the whole loop (16-bit: H = 7168, 256 experts, 1 to
-// 4096 tokens; 8-bit: 1 to 4096 rows of the DeepSeek-V3 shared expert).  Eight
+// 4096 tokens, and pairs: moe_linear, 256 to 4096 rows, N and K of 1000 to 6144;
+// 8-bit: 1 to 4096 rows of the DeepSeek-V3 shared expert).  Eight
 // CTAs a cluster only for eight tiles at most: more such clusters do not all fit
 // on the SMs at once (one row, N = 2048, K = 7168 with SwiGLU: 24 us by eights,
 // 18 us by fours).
@@ -1080,12 +1084,12 @@ inline Choice choose(int M, int N, int KB, bool swiglu, bool e4m3, int sms, bool
   Choice best{256, false, 1};
   double best_time = 1e30;
   const double arows = std::min(128, (M + 7) / 8 * 8);
-  for (int w = 0; w < 5; ++w) {
-    constexpr int width[5] = {32, 64, 128, 256, 256};
-    constexpr double half_block[5] = {250, 340, 560, 1150, 620}, e4m3_block[5] = {600, 690, 800, 1250, 950};
+  for (int w = 0; w < 6; ++w) {
+    constexpr int width[6] = {32, 64, 128, 256, 256, 128};
+    constexpr double half_block[6] = {250, 340, 560, 1150, 620, 420}, e4m3_block[6] = {600, 690, 800, 1250, 950, 1e9};
     const int bn = width[w];
-    const bool pair = w == 4;
-    if ((swiglu && bn != 256) || (pair && (M <= 128 || !(e4m3 || pairs_of_half)))) continue;
+    const bool pair = w >= 4;
+    if ((swiglu && bn != 256) || (pair && (M <= 128 || !(e4m3 || pairs_of_half))) || (w == 5 && e4m3)) continue;
     const int tm = pair ? 256 : 128, tn = swiglu ? 128 : bn;
     const long long tiles = static_cast<long long>((M + tm - 1) / tm) * ((N + tn - 1) / tn);
     for (int P = 1; P <= 8 && P <= KB; P *= 2) {
@@ -1165,6 +1169,7 @@ cudaError_t plan_and_launch(ParamsOf<EPI> p, int bn, bool pair, bool swiglu, con
       return p.accumulate ? launch<KIND, false, true, 256, true>(maps, p, grid, s)
                           : launch<KIND, false, true, 256>(maps, p, grid, s);
     } else if constexpr (EPI > 0) {
+      if (bn == 128) return launch<KIND, false, true, 128, false, EPI>(maps, p, grid, s);
       return p.accumulate ? launch<KIND, false, true, 256, true, EPI>(maps, p, grid, s)
                           : launch<KIND, false, true, 256, false, EPI>(maps, p, grid, s);
     } else {

@@ -164,3 +164,18 @@ def test_python_refusals(dev):
         kw.update(bad)
         with pytest.raises(ValueError):
             moe.linear(p, kw["x"], kw["w"], kw["out"], ws, bias=kw["bias"], residual=kw["residual"])
+
+
+PAIR_CASES = [  # of CTA pairs that share 128 columns: a few hundred rows, last tiles of few rows and columns
+    (1000, 2300, 264, "bf16", "bf16", True, "silu", True, 0),
+    (1100, 1901, 520, "f16", "f32", True, "none", True, 8),
+    (700, 3001, 200, "bf16", "bf16", False, "gelu", False, 8),
+    (257, 4100, 136, "f16", "f16", True, "relu", True, 0),
+]
+
+
+@gpu
+@pytest.mark.parametrize("case", PAIR_CASES, ids=["-".join(map(str, c)) for c in PAIR_CASES])
+def test_pairs_of_narrow_tiles(dev, case):
+    for in_place in (False, True) if case[7] else (False,):
+        test_matches_plain(dev, case, in_place)
