@@ -613,7 +613,7 @@ typedef struct {
  * -inf; rows of no sequence stay as they were; keys and values that a row does not
  * see do not reach it, whatever they hold.  Sums are float; each weight exp(x_j -
  * max) is rounded to the 16-bit type that multiplies the values (f16 with an 8-bit
- * cache).  A length beyond the table, a page outside the cache or rows outside T
+ * cache; f16 weights under 2^-21 to steps of 2^-31 at most).  A length beyond the table, a page outside the cache or rows outside T
  * are recorded as MOE_ERR_DEVICE_BAD_INDEX; what they hold is not read and the
  * sequence's results mean nothing.  All lengths are read on the device: a captured
  * call follows them (they must not change while it runs).  Results do not depend on

@@ -15,7 +15,10 @@
 //
 // The running maximum is only raised, and O rescaled, when it grew by more than 8
 // (factors of 2^8 stay far inside the sums' and the weights' range), which is rare
-// after the first tiles.  A row's result does not depend on it but for roundings.
+// after the first tiles.  A row's result does not depend on it but for roundings.  f16
+// weights are 2^7 times those relative to it, so that they reach 2^15: those under f16's
+// normal range then weigh 2^-21 of the largest and less, where 2^-14 showed beside a key
+// that takes nearly all of the weight and adds nothing.
 //
 // Masked scores become -inf whatever they were.  Values behind the sequence's end
 // are zeroed in shared memory, and values that are not finite in a tile that some row
@@ -199,6 +202,10 @@ __device__ __forceinline__ bool locate(const AttnArgs& a, int row0, int b, int j
   place = j & ((1 << a.page_shift) - 1);
   return p >= 0 && p < a.num_pages;
 }
+
+// How far under the maximum f16 weights' reference lies.
+template <bool F16>
+constexpr float kLift = F16 ? 7.f : 0.f;
 
 // DP: D rounded up to 64 or 128; the products are of that depth and width.
 // F16: the products' type (8-bit: always), else bf16.
@@ -810,7 +817,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
             tmem_st16(O + 16u * c, o);
           }
         }
-        const float r = reference(top);
+        const float r = reference(top, kLift<F16>);
         const uint64_t f2 = pack2(factor, factor), r2 = pack2(-r, -r);
 #pragma unroll 1
         for (int part = 0; part < kKeys / kSome; ++part) {
@@ -961,7 +968,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
           }
         }
         if (whole) {
-          if (live && a.lse != nullptr) a.lse[out_row * a.Hq + hd] = (top + log2_fast(total)) * 0.69314718055994531f;
+          if (live && a.lse != nullptr) a.lse[out_row * a.Hq + hd] = (top - kLift<F16> + log2_fast(total)) * 0.69314718055994531f;
         } else {
           if (live) {
             __stcg(mine + DP * kRows, top);
@@ -1030,7 +1037,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
                 if (32 * c + 8 * k < a.D) *reinterpret_cast<uint4*>(out + 32 * c + 8 * k) = make_uint4(u[0], u[1], u[2], u[3]);
               }
             }
-            if (done && group == 0 && a.lse != nullptr) a.lse[join_out * a.Hq + join_head] = (m + log2_fast(l)) * 0.69314718055994531f;
+            if (done && group == 0 && a.lse != nullptr) a.lse[join_out * a.Hq + join_head] = (m - kLift<F16> + log2_fast(l)) * 0.69314718055994531f;
             if (!done && group == 0) {
               __stcg(piece(j.base) + (DP + 2) * kRows + join_row, m);
               __stcg(piece(j.base) + (DP + 3) * kRows + join_row, l);

@@ -345,8 +345,9 @@ __device__ __forceinline__ float log2_fast(float x) {
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// the maximum that scores are taken relative to: of rows without any score yet zero
-__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.f : m; }
+// What scores are taken relative to: the row's maximum, lowered where the weights' type
+// needs it; of rows without any score yet zero.
+__device__ __forceinline__ float reference(float m, float lift = 0.f) { return m == -INFINITY ? 0.f : m - lift; }
 
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);

@@ -12,7 +12,9 @@
 // One pass over the keys: with m the largest score so far, l = sum 2^(x - m) and O =
 // sum 2^(x - m) v, both multiplied by 2^(m - m') when it grows to m'.  Sums are float;
 // weights are rounded to the values' 16-bit type before they multiply them (half a
-// step of it, as the output's own rounding).
+// step of it, as the output's own rounding).  In f16 they are 2^14 times that: relative to
+// m itself those under 2^-14 lost bits and those under 2^-25 all of them, which shows
+// beside a key that takes nearly all of the weight and adds nothing.
 //
 // 8-bit cache: codes become f16, which is exact, and so do the queries after a
 // power of two brings each row's largest value to 2^14 (what falls below f16's steps is
@@ -42,6 +44,10 @@ constexpr int kMostRows = kAttnFewRows;
 constexpr int kKeys = 16;  // of a warp's step
 constexpr int kMaxDepth = 8;
 constexpr size_t kSmem = 232448 - 1024;
+
+// How far under the maximum f16 weights' reference lies: they reach 2^14.
+template <bool F16>
+constexpr float kLift = F16 ? 14.f : 0.f;
 
 // Warps of a CTA: 8-bit keys take more instructions a byte, and up to 8 rows leave the
 // registers for 16 warps.
@@ -374,7 +380,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<E4M3, NT>, 1) attention_few_kern
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float u = exp2_fast(x[nt][2 * k] - reference(m[nt][0])), v = exp2_fast(x[nt][2 * k + 1] - reference(m[nt][1]));
+          float u = exp2_fast(x[nt][2 * k] - reference(m[nt][0], kLift<F16>));
+          float v = exp2_fast(x[nt][2 * k + 1] - reference(m[nt][1], kLift<F16>));
           l[nt][0] += u;
           l[nt][1] += v;
           if (E4M3) {  // (a masked key's weight is zero whatever its scale is)
@@ -633,7 +640,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<E4M3, NT>, 1) attention_few_kern
             make_uint4(w[0], w[1], w[2], w[3]);
       }
       if (d0 == 0 && a.lse != nullptr)
-        a.lse[static_cast<int64_t>(s.row0 + token) * a.Hq + head] = (top + log2_fast(sum)) * 0.69314718055994531f;
+        a.lse[static_cast<int64_t>(s.row0 + token) * a.Hq + head] = (top - kLift<F16> + log2_fast(sum)) * 0.69314718055994531f;
     }
     going = cur.next(a);
   }
