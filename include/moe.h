@@ -612,8 +612,11 @@ typedef struct {
  * (lse float [T, Hq] or NULL).  Rows that see no key (kv_len < n) get zeros and
  * -inf; rows of no sequence stay as they were; keys and values that a row does not
  * see do not reach it, whatever they hold.  Sums are float; each weight exp(x_j -
- * max) is rounded to the 16-bit type that multiplies the values (f16 with an 8-bit
- * cache; f16 weights under 2^-21 to steps of 2^-31 at most).  A length beyond the table, a page outside the cache or rows outside T
+ * max) is rounded to the 16-bit type that multiplies the values (f16 weights under
+ * 2^-21 to steps of 2^-31 at most).  With an 8-bit cache weight times v_scale is
+ * rounded to f16, relative to the row's largest such product (those under 2^-17 of
+ * it to steps of 2^-27 of it at most), for scales of 2^-80 to 2^100; larger and
+ * smaller ones lose bits.  A length beyond the table, a page outside the cache or rows outside T
  * are recorded as MOE_ERR_DEVICE_BAD_INDEX; what they hold is not read and the
  * sequence's results mean nothing.  All lengths are read on the device: a captured
  * call follows them (they must not change while it runs).  Results do not depend on

@@ -10,15 +10,15 @@
 // Warps: 0-3 and 4-7 the halves' softmax (a thread a row: no exchange between
 // threads), 8 loads (TMA, a box a page and 128 bytes of its rows), 9 MMAs; 16-bit: 10
 // and 11 look at the values of tiles that some row does not wholly see; 8-bit: 10
-// the tiles' scales, 12 to 15 turn codes, which TMA left in a ring of their own, into
-// f16 tiles.
+// the tiles' scales (a value's counts in its row's maximum: scale_log2), 12 to 15 turn
+// codes, which TMA left in a ring of their own, into f16 tiles.
 //
 // The running maximum is only raised, and O rescaled, when it grew by more than 8
 // (factors of 2^8 stay far inside the sums' and the weights' range), which is rare
 // after the first tiles.  A row's result does not depend on it but for roundings.  f16
 // weights are 2^7 times those relative to it, so that they reach 2^15: those under f16's
-// normal range then weigh 2^-21 of the largest and less, where 2^-14 showed beside a key
-// that takes nearly all of the weight and adds nothing.
+// normal range then weigh 2^-21 of the largest and less (8-bit 2^-17, kClose), where 2^-14
+// showed beside a key that takes nearly all of the weight and adds nothing.
 //
 // Masked scores become -inf whatever they were.  Values behind the sequence's end
 // are zeroed in shared memory, and values that are not finite in a tile that some row
@@ -46,7 +46,7 @@ using dense::expect_tx;
 using dense::mbar_arrive_cta;
 
 constexpr int kHalf = 128, kRows = 2 * kHalf, kKeys = 128;
-constexpr int kMaxSlots = 8, kCodeSlots = 4, kScaleSlots = 2, kDirty = 16;
+constexpr int kMaxSlots = 8, kScaleSlots = 2, kDirty = 16;
 constexpr size_t kSmem = 232448;
 // Registers a thread of the softmax's warpgroups and of the others; 3 x 168 and 4 x
 // 128 at launch.
@@ -62,7 +62,7 @@ using BigWalk = Walk<Shape<kRows, kKeys, 3, 3, 4>>;
 // Barriers and small arrays, then (1024-byte aligned) Q's halves, the ring of key and
 // value tiles and the ring of their codes.
 constexpr int kBarBytes = 640;
-constexpr int kScaleSlot = 2 * kKeys + 4;  // of 128 keys, of their values, unit, shrink
+constexpr int kScaleSlot = 3 * kKeys + 4;  // of 128 keys, of their values, the latter's logarithms (scale_log2), the tile's
 constexpr int kItems = 4;
 // An item as its warps see it: end is of its key tiles in this run, end0 that of the
 // first half's; least the last key that all rows see.
@@ -70,7 +70,7 @@ struct Item {
   int b, h, r, t, end, len, row0, L, past, rows, least, end0, first, pieces;
 };
 template <bool E4M3>
-constexpr int kMiscBytes = E4M3 ? 3 * 1024 : 1024;
+constexpr int kMiscBytes = E4M3 ? 4 * 1024 : 1024;
 template <bool E4M3>
 constexpr int kItemsAt = kBarBytes + (E4M3 ? kScaleSlots * kScaleSlot * 4 : 0);
 static_assert(kItemsAt<true> + kItems * sizeof(Item) <= kMiscBytes<true> &&
@@ -78,6 +78,9 @@ static_assert(kItemsAt<true> + kItems * sizeof(Item) <= kMiscBytes<true> &&
               "all before Q");
 __host__ __device__ constexpr int tile_bytes(int dp) { return kKeys * dp * 2; }
 __host__ __device__ constexpr int code_bytes(int dp) { return kKeys * dp; }
+// the codes' ring: what three f16 tiles leave
+constexpr int kMaxCodeSlots = 4;
+__host__ __device__ constexpr int code_slots(int dp) { return dp == 64 ? 4 : 3; }
 
 struct Maps {
   CUtensorMap k, v;
@@ -203,9 +206,16 @@ __device__ __forceinline__ bool locate(const AttnArgs& a, int row0, int b, int j
   return p >= 0 && p < a.num_pages;
 }
 
-// How far under the maximum f16 weights' reference lies.
+// How far a row's maximum grows before it is raised, and how far under it f16 weights'
+// reference lies: they reach 2^15.  8-bit: where a half's rows all see a tile and its values'
+// scales' logarithms differ by at most kClose, the largest of these is added to the largest
+// score, at most kClose too much; else each to its key's score in another turn over the
+// scores (2048 tokens after 30000, 28 + 4 heads: 830 us, scales over a range of 2^12 1074).
+constexpr int kClose = 3;
+constexpr float kLag = 8.f;
 template <bool F16>
 constexpr float kLift = F16 ? 7.f : 0.f;
+static_assert(kLag + kLift<true> <= 15.f, "f16 ends below 2^16");
 
 // DP: D rounded up to 64 or 128; the products are of that depth and width.
 // F16: the products' type (8-bit: always), else bf16.
@@ -213,7 +223,7 @@ template <bool E4M3, bool F16, int DP>
 __global__ void __launch_bounds__(kThreads<E4M3>, 1)
 attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ AttnArgs a, const int slots, const int box_rows) {
   extern __shared__ __align__(1024) uint8_t attn_smem[];
-  constexpr int kChunks = DP / 64;
+  constexpr int kChunks = DP / 64, kCodeSlots = code_slots(DP);
   constexpr uint32_t kTile = tile_bytes(DP);
   const uint32_t base = smem_u32(attn_smem);
   const uint32_t qbase = base + kMiscBytes<E4M3>, ring = qbase + 2u * kTile;
@@ -259,7 +269,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
       mbar_init(IFULL(s), 1u);
       mbar_init(IEMPTY(s), 9u + (E4M3 ? 1u + kConverters : kGuards));
     }
-    for (int s = 0; s < kCodeSlots; ++s) {
+    for (int s = 0; s < kMaxCodeSlots; ++s) {
       mbar_init(CFULL(s), 1u);
       mbar_init(CEMPTY(s), kConverters);
     }
@@ -384,13 +394,11 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
       }
     } else if (E4M3 && some && warp == 10) {
       // ------------------------------------ 8-bit: scales of a tile's keys and values
-      // four keys a lane; the values' relative to the item's largest so far, rounded up to
-      // a power of two
+      // four keys a lane
       uint32_t n = 0;
       for (int item = 0; ok; ++item) {
         const Item* it = take(item);
         if (it == nullptr || it->t < 0) break;
-        float unit = 0.f;
         const int end = it->end, L = it->L, least = it->least;
         for (int t = it->t; t < end; ++t, ++n) {
           const uint32_t slot = n % kScaleSlots;
@@ -404,38 +412,27 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
               vs = *reinterpret_cast<const float4*>(a.kv.v_scale + at);
             }
           }
-          float most = 0.f;
           float* each = &vs.x;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const bool finite = fabsf(each[e]) < INFINITY;
             if (key + e >= L) {
               each[e] = 0.f;
-            } else if (finite) {
-              most = fmaxf(most, fabsf(each[e]));
-            } else if (t * kKeys + kKeys - 1 > least) {  // (as values that are not finite)
+            } else if (!(fabsf(each[e]) < INFINITY) && t * kKeys + kKeys - 1 > least) {  // (as values that are not finite)
               each[e] = 0.f;
               dirty[item % kDirty] = item;
             }
           }
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-          const float power = __uint_as_float(min((__float_as_uint(most) & 0x7F800000u) + 0x00800000u, 0x7F000000u));
-          float shrink = 1.f;
-          if (power > unit) {
-            shrink = unit / power;
-            unit = power;
-          }
-          const float per = 1.f / unit;
+          const float4 by = make_float4(scale_log2(vs.x), scale_log2(vs.y), scale_log2(vs.z), scale_log2(vs.w));
+          // (whole numbers)
+          const int most = __reduce_max_sync(0xffffffffu, static_cast<int>(fmaxf(fmaxf(by.x, by.y), fmaxf(by.z, by.w))));
+          const int fewest = __reduce_min_sync(0xffffffffu, static_cast<int>(fminf(fminf(by.x, by.y), fminf(by.z, by.w))));
           ok = wait(SCEMPTY(slot), (n / kScaleSlots & 1u) ^ 1u, abort_flag, 0x710);
           if (!ok) break;
           float* to = scales + slot * kScaleSlot;
           *reinterpret_cast<float4*>(to + 4 * lane) = ks;
-          *reinterpret_cast<float4*>(to + kKeys + 4 * lane) = make_float4(vs.x * per, vs.y * per, vs.z * per, vs.w * per);
-          if (lane == 0) {
-            to[2 * kKeys] = unit;
-            to[2 * kKeys + 1] = shrink;
-          }
+          *reinterpret_cast<float4*>(to + kKeys + 4 * lane) = vs;
+          *reinterpret_cast<float4*>(to + 2 * kKeys + 4 * lane) = by;
+          if (lane == 0) to[3 * kKeys] = most - fewest <= kClose ? static_cast<float>(most) : INFINITY;
           __syncwarp();
           if (lane == 0) mbar_arrive_cta(SCFULL(slot));
         }
@@ -731,7 +728,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
       const int least = begun ? w->past + divided(w->r * kRows + half * kHalf, a.G) : 0;
       const int limit = begun ? w->past + divided(row_of(w), a.G) : 0;
       float top = -INFINITY;  // of the row's scores, what its weights are relative to
-      float unit = 1.f;
+      const uint64_t f2 = pack2(factor, factor);
       uint64_t sum = 0;
       for (int t = t0; t < (E4M3 ? w_end : end); ++t) {
         const float* sc = nullptr;
@@ -747,7 +744,6 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
             if (lane == 0) mbar_arrive_cta(SCEMPTY(slot));
             continue;
           }
-          unit = sc[2 * kKeys];
         }
         ok = wait(SFULL(half), sph, abort_flag, 0x761);
         if (!ok) break;
@@ -758,6 +754,8 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
         // instruction caches.)  Scores that are scaled or masked go back to tensor memory.
         constexpr int kSome = 64;
         const bool masked = t * kKeys + kKeys - 1 > least;
+        const float by_tile = E4M3 ? sc[3 * kKeys] : 0.f;
+        const bool each = E4M3 && (masked || by_tile == INFINITY);
         float now = -INFINITY;
 #pragma unroll 1
         for (int part = 0; part < kKeys / kSome; ++part) {
@@ -796,18 +794,34 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
           now = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         }
         if (E4M3 || masked) tmem_st_wait();
-        now *= factor;
-        const float shrink = E4M3 ? sc[2 * kKeys + 1] : 1.f;
+        now = E4M3 ? fmaf(now, factor, by_tile) : now * factor;
+        if (E4M3 && each) {  // the maximum with what each value's scale adds
+          now = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < kKeys / 32; ++c) {
+            uint32_t s[32];
+            dense::tmem_ld32(S + 32u * c, s);
+            dense::tmem_ld32_wait(s);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const ulonglong2 by = *reinterpret_cast<const ulonglong2*>(sc + 2 * kKeys + 32 * c + 4 * j);
+              const uint64_t y = fma2((static_cast<uint64_t>(s[4 * j + 1]) << 32) | s[4 * j], f2, by.x);
+              const uint64_t z = fma2((static_cast<uint64_t>(s[4 * j + 3]) << 32) | s[4 * j + 2], f2, by.y);
+              now = fmaxf(fmaxf(now, fmaxf(lo2(y), hi2(y))), fmaxf(lo2(z), hi2(z)));
+            }
+          }
+        }
         if (t == t0) {
           top = fmaxf(top, now);  // (NaN leaves it)
-        } else if (__any_sync(0xffffffffu, now > top + 8.f) || shrink != 1.f) {
+        } else if (__any_sync(0xffffffffu, now > top + kLag)) {
           // O of the tiles before is complete: their products precede these scores
           // (a row that did not grow so far keeps its bits, whatever its warp's others do)
-          const bool grown = now > top + 8.f;
-          const float keep = grown ? exp2_fast(top - reference(now)) : 1.f;
+          const bool grown = now > top + kLag;
+          const float d = top - reference(now), keep = grown ? exp2_fast(E4M3 ? 0.5f * d : d) : 1.f;
           top = grown ? now : top;
           sum = mul2(sum, pack2(keep, keep));
-          const float f = keep * shrink;
+          if (E4M3) sum = mul2(sum, pack2(keep, keep));  // (moved)
+          const float f = E4M3 ? keep * keep : keep;
 #pragma unroll 1
           for (int c = 0; c < DP / 16; ++c) {
             uint32_t o[16];
@@ -818,7 +832,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
           }
         }
         const float r = reference(top, kLift<F16>);
-        const uint64_t f2 = pack2(factor, factor), r2 = pack2(-r, -r);
+        const uint64_t r2 = pack2(-r, -r);
 #pragma unroll 1
         for (int part = 0; part < kKeys / kSome; ++part) {
           uint32_t s[kSome / 32][32];
@@ -895,7 +909,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
             dense::tmem_ld32(O + 32u * c, o);
             dense::tmem_ld32_wait(o);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]) * (E4M3 ? unit : 1.f);
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(o[j]);
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = 0.f;
@@ -1005,7 +1019,10 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
             for (int i = 0; i < j.count; ++i) m = fmaxf(m, __ldcg(stats(i)));
             const float r = reference(m);
 #pragma unroll 4
-            for (int i = 0; i < j.count; ++i) l = fmaf(__ldcg(stats(i) + kRows), exp2_fast(__ldcg(stats(i)) - r), l);
+            for (int i = 0; i < j.count; ++i) {
+              const float d = __ldcg(stats(i)) - r;
+              l += moved<E4M3>(__ldcg(stats(i) + kRows), d, exp2_fast(d));
+            }
             const int R = w->r * kRows + join_row, join_tok = divided(R, a.G), join_head = w->h * a.G + R - join_tok * a.G;
             const int64_t join_out = w->row0 + join_tok;
             uint16_t* out = a.out + join_out * a.out_stride + static_cast<int64_t>(join_head) * a.D;
@@ -1097,7 +1114,7 @@ cudaError_t launch(const AttnArgs& a, int sms, cudaStream_t s) {
       return cudaErrorInvalidConfiguration;
     if (dev >= 0 && dev < 64) configured[dev] = 1;
   }
-  const size_t fixed = kMiscBytes<E4M3> + 2 * tile_bytes(DP) + (E4M3 ? kCodeSlots * code_bytes(DP) : 0);
+  const size_t fixed = kMiscBytes<E4M3> + 2 * tile_bytes(DP) + (E4M3 ? code_slots(DP) * code_bytes(DP) : 0);
   const int room = static_cast<int>((kSmem - fixed) / tile_bytes(DP));
   const int slots = room < kMaxSlots ? room : kMaxSlots;
   const size_t smem = std::max(kTensorMemorySmem, fixed + static_cast<size_t>(slots) * tile_bytes(DP));

@@ -349,6 +349,26 @@ __device__ __forceinline__ float log2_fast(float x) {
 // needs it; of rows without any score yet zero.
 __device__ __forceinline__ float reference(float m, float lift = 0.f) { return m == -INFINITY ? 0.f : m - lift; }
 
+// 8-bit caches: what a key's value scale adds to its score where a row's maximum is
+// taken, so that weight times scale, which is what becomes f16, is of the same size
+// whatever the scales are: the logarithm of the power of two above it.  Weights of small
+// scales are large numbers for that, hence at least -80: 2^30 keys' sum stays in float's
+// range.  (Scales that are not finite say nothing about the others.)
+constexpr float kLeastScale = -80.f;
+__device__ __forceinline__ float scale_log2(float v) {
+  const int e = static_cast<int>(__float_as_uint(v) >> 23 & 255u);
+  return e == 255 ? kLeastScale : fmaxf(static_cast<float>(e - 126), kLeastScale);
+}
+
+// A sum of weights times f = 2^d: of an 8-bit cache, which may be large where f
+// vanishes, twice by half of the exponent.
+template <bool E4M3>
+__device__ __forceinline__ float moved(float sum, float d, float f) {
+  if (!E4M3) return sum * f;
+  const float h = exp2_fast(0.5f * d);
+  return sum * h * h;
+}
+
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);

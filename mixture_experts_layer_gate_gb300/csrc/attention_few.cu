@@ -19,8 +19,10 @@
 // 8-bit cache: codes become f16, which is exact, and so do the queries after a
 // power of two brings each row's largest value to 2^14 (what falls below f16's steps is
 // under 2^-38 of that).  A key's scale multiplies its score.  A value's scale
-// multiplies its weight, relative to the largest one so far rounded up to a power of
-// two, so that weights stay in f16's range.
+// multiplies its weight, and m is then the largest score plus logarithm of the scale that
+// the row sees (scale_log2), so that their product stays in f16's range; l is relative to
+// the same m.  A largest scale of all keys instead took the weights of rows that do not
+// see it, or give it no weight, into f16's subnormals.
 //
 // K is permuted inside the head (any order gives the same product) so that a lane's
 // 16 adjacent bytes of a key are its fragment; 8-bit values are read along the head and
@@ -263,7 +265,6 @@ __global__ void __launch_bounds__(32 * kWarpsOf<E4M3, NT>, 1) attention_few_kern
         m[nt][i] = -INFINITY;
         l[nt][i] = 0.f;
       }
-    float unit = 0.f, per_unit = 0.f;  // 8-bit: what the values' scales are relative to, and its inverse
 
     for (int t = cur.t; t < cur.end; ++t) {
       cp_async_wait(depth - 2);
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<E4M3, NT>, 1) attention_few_kern
           }
         }
       }
-      float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};  // 8-bit: scales of keys g, g + 8
+      float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f}, more_by[2] = {0.f, 0.f};  // 8-bit: of keys g, g + 8
       if (E4M3) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -319,19 +320,10 @@ __global__ void __launch_bounds__(32 * kWarpsOf<E4M3, NT>, 1) attention_few_kern
           asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at + 4 * kKeys) : "memory");
           ks[i] = __uint_as_float(u);
           vs[i] = __uint_as_float(v);
+          more_by[i] = scale_log2(vs[i]);
         }
       }
       // ---- maxima
-      float grown = 0.f;  // 8-bit: the unit's new value
-      if (E4M3) {
-        float most = 0.f;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (key0 + 8 * i + g < s.L && fabsf(vs[i]) < INFINITY) most = fmaxf(most, fabsf(vs[i]));
-#pragma unroll
-        for (int w = 4; w < 32; w <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, w));
-        if (most >= unit) grown = __uint_as_float(min((__float_as_uint(most) & 0x7F800000u) + 0x00800000u, 0x7F000000u));
-      }
       float keep[NT][2];
       bool rescale = false;
 #pragma unroll
@@ -344,28 +336,25 @@ __global__ void __launch_bounds__(32 * kWarpsOf<E4M3, NT>, 1) attention_few_kern
             if (E4M3) z *= ks[k];
             x[nt][2 * k + i] = key0 + 8 * k + g <= limit[nt][i] ? z : -INFINITY;
           }
-          float top = fmaxf(x[nt][i], x[nt][2 + i]);
+          float top = E4M3 ? fmaxf(x[nt][i] + more_by[0], x[nt][2 + i] + more_by[1]) : fmaxf(x[nt][i], x[nt][2 + i]);
 #pragma unroll
           for (int w = 4; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
           const float next = fmaxf(m[nt][i], top);
-          keep[nt][i] = exp2_fast(m[nt][i] - reference(next));
+          const float shift = m[nt][i] - reference(next);
+          keep[nt][i] = exp2_fast(E4M3 ? 0.5f * shift : shift);
           rescale = rescale || next != m[nt][i];
           m[nt][i] = next;
         }
-      float shrink = 1.f;
-      if (E4M3 && grown > unit) {
-        shrink = unit / grown;
-        unit = grown;
-        per_unit = 1.f / grown;
-        rescale = true;
-      }
       if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             l[nt][i] *= keep[nt][i];
-            keep[nt][i] *= shrink;
+            if (E4M3) {  // (l may be large: twice half of the exponent)
+              l[nt][i] *= keep[nt][i];
+              keep[nt][i] *= keep[nt][i];
+            }
           }
 #pragma unroll
         for (int j = 0; j < MT; ++j)
@@ -385,9 +374,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<E4M3, NT>, 1) attention_few_kern
           l[nt][0] += u;
           l[nt][1] += v;
           if (E4M3) {  // (a masked key's weight is zero whatever its scale is)
-            const float f = vs[k] * per_unit;
-            u = key0 + 8 * k + g <= limit[nt][0] ? u * f : 0.f;
-            v = key0 + 8 * k + g <= limit[nt][1] ? v * f : 0.f;
+            u = key0 + 8 * k + g <= limit[nt][0] ? u * vs[k] : 0.f;
+            v = key0 + 8 * k + g <= limit[nt][1] ? v * vs[k] : 0.f;
           }
           p[nt][k] = transposed(F16 ? pack_half(u, v) : pack_bf16x2(u, v));
         }
@@ -488,14 +476,6 @@ __global__ void __launch_bounds__(32 * kWarpsOf<E4M3, NT>, 1) attention_few_kern
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], w);
-    if (E4M3) {
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[j][nt][e] *= unit;
-    }
     constexpr int kBufs = 64 / kRows;          // buffers of kRows rows
     constexpr int kTurns = kWarps / kBufs;     // 1, or 2: the second half of the warps first
     static_assert(kTurns == 1 || kTurns == 2, "each warp has a buffer, or half of them");
@@ -537,7 +517,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<E4M3, NT>, 1) attention_few_kern
             if (row < live) {
               const float om = ms[warp * kRows + row], both = fmaxf(m[nt][i], om), r = reference(both);
               const float mine = exp2_fast(m[nt][i] - r), other = exp2_fast(om - r);
-              l[nt][i] = l[nt][i] * mine + ls[warp * kRows + row] * other;
+              l[nt][i] = moved<E4M3>(l[nt][i], m[nt][i] - r, mine) + moved<E4M3>(ls[warp * kRows + row], om - r, other);
               m[nt][i] = both;
 #pragma unroll
               for (int j = 0; j < MT; ++j)
@@ -566,7 +546,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<E4M3, NT>, 1) attention_few_kern
 #pragma unroll
       for (int i = 0; i < kBufs; ++i) {
         const float f = exp2_fast(ms[i * kRows + row] - r);
-        sum += ls[i * kRows + row] * f;
+        sum += moved<E4M3>(ls[i * kRows + row], ms[i * kRows + row] - r, f);
         const float* from = at(i, row, d0);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = fmaf(from[j], f, v[j]);
@@ -612,7 +592,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<E4M3, NT>, 1) attention_few_kern
             const float4 u = __ldcg(reinterpret_cast<const float4*>(from + row * DP + d0));
             const float4 z = __ldcg(reinterpret_cast<const float4*>(from + row * DP + d0) + 1);
             const float f = exp2_fast(stat.x - r);
-            sum = fmaf(stat.y, f, sum);
+            sum += moved<E4M3>(stat.y, stat.x - r, f);
             v[0] = fmaf(u.x, f, v[0]);
             v[1] = fmaf(u.y, f, v[1]);
             v[2] = fmaf(u.z, f, v[2]);
