@@ -702,7 +702,8 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
         const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100), 126);
         const bool scaled = amax > 0.f && amax < INFINITY;
         const float up = scaled ? __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23) : 1.f;
-        if (scaled) factor *= __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
+        // (not zero, with which a masked score would be NaN)
+        if (scaled) factor = fmaxf(factor * __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23), 0x1p-126f);
 #pragma unroll 2
         for (int c = 0; c < DP / 8; ++c) {
           uint4 v = dense::lds_u4(q_at + piece_at(row, c));

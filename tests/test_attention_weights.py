@@ -1,6 +1,8 @@
 """What a row's weights are relative to when they are rounded to 16 bits: nothing that the row does not see reaches it
 through a value scale of an 8-bit cache, a seen key counts by its weight and its scale together, and small f16 weights
 keep their bits beside a key that takes nearly all of the weight."""
+import math
+
 import pytest
 import torch
 
@@ -170,3 +172,22 @@ def test_small_weights_beside_a_sink(dev, new, sink, dtype):
     rel, tiny = ref.half_step(DT[dtype])
     ref.check(out.reshape(new, Hq, D), want, dout + (want.abs() + dout) * rel + tiny, "out")
     ref.check(lse, wl, dl, "lse")
+
+
+@gpu
+@pytest.mark.parametrize("new", [3, 40])
+def test_scores_that_vanish(dev, new):
+    """Queries and a scale so small that their product is under float's range: every weight is the same, masked keys none."""
+    problem, args, q, keys, cu, _ = build(dev, [new], [300], 4, 2, 64, "bf16", "e4m3", 16, "token", spare=0)
+    problem.scale = 2.0 ** -60
+    q.mul_(2.0 ** -105)
+    args["q"] = q.to(dev)
+    out, lse, _ = run(problem, args, dev)
+    rel, tiny = ref.half_step(torch.bfloat16)
+    for i in range(new):
+        n = 300 - new + i + 1
+        want = keys[0][1][:n].mean(dim=0).repeat_interleave(2, dim=0)
+        size = keys[0][1][:n].abs().mean(dim=0).repeat_interleave(2, dim=0)
+        tol = size * (2.0 ** -11 + 2.0 ** -16) + want.abs() * rel + tiny  # a weight's rounding, the sums'
+        ref.check(out[i].reshape(4, 64), want, tol, "out")
+        assert bool(((lse[i].cpu().double() - math.log(n)).abs() < 2.0 ** -18).all())
