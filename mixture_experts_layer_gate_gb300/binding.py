@@ -213,15 +213,17 @@ def _stream(stream):
 def run_on(stream, call, *args):
     """call(*args) with the given raw stream as PyTorch's current one (None: as it is), for calls that allocate: what
     they allocate then belongs to the stream that their kernels run on.  Tensors that cross streams are kept from
-    reuse until both have done their work: the arguments on the given stream, the results on the caller's."""
+    reuse until both have done their work: the arguments (and what they hold as their `tensors`) on the given stream,
+    the results on the caller's."""
     if stream is None or int(stream) == _stream(None):
         return call(*args)
     import torch
     caller = torch.cuda.current_stream()
     side = torch.cuda.ExternalStream(0 if int(stream) == 1 else int(stream))  # (1: cudaStreamLegacy, the default one)
-    for t in args:
-        if isinstance(t, torch.Tensor):
-            t.record_stream(side)
+    for arg in args:
+        for t in getattr(arg, "tensors", (arg,)):
+            if isinstance(t, torch.Tensor):
+                t.record_stream(side)
     with torch.cuda.stream(side):
         results = call(*args)
     for t in results if isinstance(results, tuple) else (results,):

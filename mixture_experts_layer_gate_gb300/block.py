@@ -106,6 +106,10 @@ class KVCache:
             self.k_scale, self.v_scale = (torch.empty((num_pages, Hkv, page_size), dtype=torch.float32, device=device)
                                           for _ in range(2))
 
+    @property
+    def tensors(self):
+        return self.k, self.v, self.k_scale, self.v_scale
+
 
 class AttentionBlock:
     """`block(x, residual, positions, cu_q, max_q, ...)` -> (out, residual + x), both bf16 [T, H]; the next block adds
