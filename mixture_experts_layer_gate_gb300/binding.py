@@ -597,7 +597,7 @@ def prompt_attention(p: AttentionProblem, q, k, v, cu_q, out, ws, lse=None, stre
 def workspace_of(owner, name: str, n: int, allocate):
     """A workspace of at least n bytes for a call: owner's attribute `name`, which allocate() replaces where it is too
     small.  One that a captured graph uses stays alive in owner.kept, and one whose zero fill is being captured
-    serves that capture alone."""
+    serves that capture alone.  Of those that go owner.left keeps the error header, the first with an error if any."""
     import torch
     ws, capturing = getattr(owner, name), torch.cuda.is_current_stream_capturing()
     if ws is not None and n <= ws.numel():
@@ -609,6 +609,8 @@ def workspace_of(owner, name: str, n: int, allocate):
         owner.kept.append(new)
         return new
     if ws is not None and not any(w is ws for w in owner.kept):
+        header = ws[:256].clone()
+        owner.left = header if owner.left is None else torch.where(owner.left.view(torch.int32)[0] != 0, owner.left, header)
         ws.record_stream(torch.cuda.current_stream())  # its calls may still run there
     setattr(owner, name, new)
     return new
@@ -622,7 +624,7 @@ class MoELayer:
     def __init__(self, H, I, E, top_k, weights: Weights, max_tokens: int, device, **gate):
         self.shape = dict(H=H, I=I, E=E, top_k=top_k, **gate)
         self.weights = weights
-        self.kept = []  # workspaces that captured graphs use
+        self.kept, self.left = [], None  # workspaces that captured graphs use; the error header of those outgrown
         self.ws = alloc_workspace(problem(max_tokens, H, I, E, top_k, **gate), device)
 
     def problem(self, T: int) -> Problem:

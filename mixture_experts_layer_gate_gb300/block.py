@@ -12,6 +12,11 @@ from __future__ import annotations
 from . import binding as b
 
 
+def _first_error(stream, *workspaces) -> int:
+    found = [b.get_device_error(ws, stream) for ws in workspaces if ws is not None]
+    return next((e for e in found if e), 0)
+
+
 class SharedExpert:
     """Weights of the shared expert: w13 e4m3 [2I, H] and w2 e4m3 [H, I] with a float32 scale per 128 x 128 block."""
 
@@ -39,7 +44,7 @@ class MoEBlock:
         self.norm_weight, self.router_weight, self.router_bias = norm_weight, router_weight, router_bias
         self.shared, self.weights = shared, weights
         self.layer = b.MoELayer(H, I, E, top_k, weights, max_tokens, device, **gate)
-        self.few_ws, self.kept = None, []  # kept: workspaces that captured graphs use
+        self.few_ws, self.kept, self.left = None, [], None  # (kept, left: workspace_of)
         for T in range(min(max_tokens, b.FEW_MAX_TOKENS), 0, -1):
             if b.few_workspace_size(self.layer.problem(T)):
                 self.few_ws = b.alloc_few_workspace(self.layer.problem(T), device)
@@ -83,9 +88,8 @@ class MoEBlock:
 
     def device_error(self, stream=None) -> int:
         """First error that a kernel of the block recorded (0: none), cleared; synchronises the stream."""
-        all_ws = (self.op_ws, self.few_ws, self.layer.ws, *self.kept, *self.layer.kept)
-        found = [b.get_device_error(ws, stream) for ws in all_ws if ws is not None]
-        return next((e for e in found if e), 0)
+        return _first_error(stream, self.left, self.layer.left, self.op_ws, self.few_ws, self.layer.ws, *self.kept,
+                            *self.layer.kept)
 
 
 class KVCache:
@@ -132,7 +136,7 @@ class AttentionBlock:
         self.rope = dict(rot=D if rot is None else rot, layout=layout, magnitude=magnitude, eps=eps,
                          weight_dtype="f32" if norms and str(norms[0].dtype) == "torch.float32" else "bf16")
         self.op_ws = b.alloc_op_workspace(device)
-        self.attention_ws, self.kept = None, []  # kept: workspaces that captured graphs use
+        self.attention_ws, self.kept, self.left = None, [], None  # (kept, left: workspace_of)
 
     def __call__(self, x, residual, positions, cu_q, max_q, cache: KVCache | None = None, slots=None, page_table=None,
                  kv_len=None, stream=None):
@@ -178,8 +182,7 @@ class AttentionBlock:
 
     def device_error(self, stream=None) -> int:
         """First error that a kernel of the block recorded (0: none), cleared; synchronises the stream."""
-        found = [b.get_device_error(ws, stream) for ws in (self.op_ws, self.attention_ws, *self.kept) if ws is not None]
-        return next((e for e in found if e), 0)
+        return _first_error(stream, self.left, self.op_ws, self.attention_ws, *self.kept)
 
 
 class DecoderLayer:

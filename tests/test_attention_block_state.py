@@ -1,12 +1,16 @@
-"""AttentionBlock's memory between calls and across streams: its cache lives as long as a given stream's kernels need it."""
+"""AttentionBlock's memory between calls and across streams: its cache lives as long as a given stream's kernels need it,
+and errors of a workspace that was outgrown are not lost."""
 import pytest
 import torch
 
 import mixture_experts_layer_gate_gb300 as moe
 from mixture_experts_layer_gate_gb300 import binding
-from tests.test_attention_block import D, H, HKV, PAGE, make, weights
-from tests.test_block_streams import FakeStreams
-from tests.test_operators import gen, lib  # noqa: F401  (a fixture)
+from tests.test_attention_block import D, H, HKV, PAGE, Pages, make, weights
+from tests.test_block_streams import FakeStreams, cpu_block
+from tests.test_operators import dev, gen, lib, randn  # noqa: F401  (fixtures among them)
+
+gpu = pytest.mark.gpu
+BAD_INDEX, TIMEOUT = 5, 6
 
 
 def cpu_attention(monkeypatch, current=16):
@@ -20,6 +24,13 @@ def cpu_attention(monkeypatch, current=16):
                                         and t.dim() == 1 and t.numel() > 4096))
         monkeypatch.setattr(binding, name, op)
 
+    def error(ws, stream=None):  # a workspace's first word, cleared
+        head = ws[:8].view(torch.int32)
+        e = int(head[0])
+        head.zero_()
+        return e
+
+    monkeypatch.setattr(binding, "get_device_error", error)
     return block, fake
 
 
@@ -52,3 +63,39 @@ def test_cache_is_kept_by_a_decoder_layer(lib, monkeypatch):
     layer(x, x, i32(3), torch.tensor([0, 3], dtype=torch.int32), 3, stream=48, cache=cache, slots=i32(3),
           page_table=i32(1, 4), kv_len=i32(1))
     assert {(cache.k.data_ptr(), 48), (cache.v.data_ptr(), 48)} <= set(fake.recorded)
+
+
+def test_errors_of_an_outgrown_workspace_are_found(lib, monkeypatch):
+    cache = moe.KVCache(4, PAGE, HKV, D, "cpu")
+    block, fake = cpu_attention(monkeypatch)
+    step(block, 1, 1, cache)
+    fake.passed[-1][:8].view(torch.int32)[0] = BAD_INDEX
+    step(block, 90, 90, cache)
+    assert fake.passed[0] is not fake.passed[1]
+    assert block.device_error() == BAD_INDEX and block.device_error() == 0
+
+
+def test_errors_of_an_outgrown_expert_workspace_are_found(lib, monkeypatch):
+    """The same of MoEBlock, few tokens and many; of several outgrown ones the first error is the one that counts."""
+    for small, large in ((1, 3), (9, 40)):
+        with monkeypatch.context() as m:
+            block = cpu_block(small, shared=False)
+            _, fake = cpu_attention(m)
+            bf = lambda n: torch.zeros(n, 256, dtype=torch.bfloat16)  # noqa: E731
+            for i, n in enumerate((small, large, large + 2)):
+                block(bf(n))
+                fake.passed[-1][:8].view(torch.int32)[0] = (BAD_INDEX, TIMEOUT, 0)[i]
+            assert block.device_error() == BAD_INDEX and block.device_error() == 0, small
+
+
+@gpu
+def test_errors_of_an_outgrown_workspace_on_the_device(dev):
+    g = gen(21)
+    block = make(weights(g, dev), dev)
+    cache, pages = moe.KVCache(8, PAGE, HKV, D, dev), Pages(g, 8, 1)
+    i32 = lambda t: torch.tensor(t, dtype=torch.int32, device=dev)  # noqa: E731
+    x = randn(g, 40, H).bfloat16().to(dev)
+    slots = pages.append(0, 41)
+    block(x[:1], None, i32([0]), i32([0, 1]), 1, cache, i32(slots[:1]), i32([[-7] * 12]), i32([1]))
+    block(x, None, i32(list(range(1, 41))), i32([0, 40]), 40, cache, i32(slots[1:]), pages.table(dev), i32([41]))
+    assert block.device_error() == BAD_INDEX and block.device_error() == 0
