@@ -622,7 +622,8 @@ typedef struct {
  * call follows them (they must not change while it runs).  Results do not depend on
  * timing (no atomics in sums).  Rows are 16-byte aligned, strides multiples of 8,
  * T * Hq <= 2^30.  The workspace holds moe_attention_workspace_size() bytes, zeroed
- * when first used, and again after a call that recorded MOE_ERR_TIMEOUT in it. */
+ * when first used, and again after a call that ran into MOE_ERR_TIMEOUT (after any
+ * error in its header: that holds the first one only). */
 size_t moe_attention_workspace_size(const moe_attention_t* p);
 moe_status_t moe_paged_attention(const moe_attention_t* p, const void* q, int64_t q_stride,
                                  const moe_kv_t* cache, const int32_t* page_table, int64_t table_stride,

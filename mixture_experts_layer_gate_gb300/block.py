@@ -13,8 +13,13 @@ from . import binding as b
 
 
 def _first_error(stream, *workspaces) -> int:
-    found = [b.get_device_error(ws, stream) for ws in workspaces if ws is not None]
-    return next((e for e in found if e), 0)
+    found = 0
+    for ws in workspaces:
+        e = b.get_device_error(ws, stream) if ws is not None else 0
+        if e:  # a call that timed out, perhaps after this error, leaves counters that are zero between calls
+            b.run_on(stream, ws.zero_)
+        found = found or e
+    return found
 
 
 class SharedExpert:
@@ -87,7 +92,8 @@ class MoEBlock:
         return out, total if total is not None else x
 
     def device_error(self, stream=None) -> int:
-        """First error that a kernel of the block recorded (0: none), cleared; synchronises the stream."""
+        """First error that a kernel of the block recorded (0: none), cleared; synchronises the stream.  Then
+        the block can be used again."""
         return _first_error(stream, self.left, self.layer.left, self.op_ws, self.few_ws, self.layer.ws, *self.kept,
                             *self.layer.kept)
 
@@ -181,7 +187,8 @@ class AttentionBlock:
         return out, total if total is not None else x
 
     def device_error(self, stream=None) -> int:
-        """First error that a kernel of the block recorded (0: none), cleared; synchronises the stream."""
+        """First error that a kernel of the block recorded (0: none), cleared; synchronises the stream.  Then
+        the block can be used again."""
         return _first_error(stream, self.left, self.op_ws, self.attention_ws, *self.kept)
 
 

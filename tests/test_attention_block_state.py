@@ -1,11 +1,11 @@
 """AttentionBlock's memory between calls and across streams: its cache lives as long as a given stream's kernels need it,
-and errors of a workspace that was outgrown are not lost."""
+errors of a workspace that was outgrown are not lost, and one that an aborted call left is made usable again."""
 import pytest
 import torch
 
 import mixture_experts_layer_gate_gb300 as moe
 from mixture_experts_layer_gate_gb300 import binding
-from tests.test_attention_block import D, H, HKV, PAGE, Pages, make, weights
+from tests.test_attention_block import D, H, HKV, HQ, PAGE, Pages, make, weights
 from tests.test_block_streams import FakeStreams, cpu_block
 from tests.test_operators import dev, gen, lib, randn  # noqa: F401  (fixtures among them)
 
@@ -88,6 +88,20 @@ def test_errors_of_an_outgrown_expert_workspace_are_found(lib, monkeypatch):
             assert block.device_error() == BAD_INDEX and block.device_error() == 0, small
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_workspace_is_zeroed_after_an_error(lib, monkeypatch, captured):
+    cache = moe.KVCache(4, PAGE, HKV, D, "cpu")
+    block, fake = cpu_attention(monkeypatch)
+    fake.capturing = captured
+    step(block, 1, 1, cache)
+    fake.capturing = False
+    ws = fake.passed[-1]
+    for error in (TIMEOUT, BAD_INDEX):  # (a timeout after another error is not recorded)
+        ws.fill_(1)
+        ws[:8].view(torch.int32)[0] = error
+        assert block.device_error() == error and not bool(ws.any())
+
+
 @gpu
 def test_errors_of_an_outgrown_workspace_on_the_device(dev):
     g = gen(21)
@@ -99,3 +113,29 @@ def test_errors_of_an_outgrown_workspace_on_the_device(dev):
     block(x[:1], None, i32([0]), i32([0, 1]), 1, cache, i32(slots[:1]), i32([[-7] * 12]), i32([1]))
     block(x, None, i32(list(range(1, 41))), i32([0, 40]), 40, cache, i32(slots[1:]), pages.table(dev), i32([41]))
     assert block.device_error() == BAD_INDEX and block.device_error() == 0
+
+
+@gpu
+def test_results_after_a_timeout_was_reported(dev):
+    """The code and counters that an aborted call leaves, written by the host: once reported, calls are right again."""
+    g = gen(22)
+    w = weights(g, dev)
+    blocks = [make(w, dev) for _ in range(2)]
+    n = 3000
+    cache, pages = moe.KVCache(200, PAGE, HKV, D, dev), Pages(g, 200, 1)
+    slots = pages.append(0, n)
+    for t in (cache.k, cache.v):
+        t.copy_(randn(g, 200, PAGE, HKV, D))
+    i32 = lambda t: torch.tensor(t, dtype=torch.int32, device=dev)  # noqa: E731
+    x = randn(g, 1, H).bfloat16().to(dev)
+    call = lambda b: b(x, None, i32([n - 1]), i32([0, 1]), 1, cache, i32(slots[-1:]), pages.table(dev, 200), i32([n]))  # noqa: E731
+    want = call(blocks[0])[0]
+    call(blocks[1])
+    ws = blocks[1].attention_ws
+    ws[256:256 + 2048].view(torch.int32).fill_(77)
+    ws[:4].view(torch.int32).fill_(TIMEOUT)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    assert blocks[1].device_error(side.cuda_stream) == TIMEOUT
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(call(blocks[1])[0], want) and blocks[1].device_error() == 0
