@@ -522,7 +522,8 @@ typedef struct {
  * = v (1 + erf(v / sqrt 2)) / 2, its tanh form v (1 + tanh(sqrt(2 / pi) (v +
  * 0.044715 v^3))) / 2, relu; a NaN stays one.  silu and the tanh form are
  * within (8 + |y|) * 2^-22 of the value at their sum, y = v or 2 sqrt(2 / pi) (v +
- * 0.044715 v^3), and zero where exp(-y) passes 8e37.
+ * 0.044715 v^3), and zero where exp(-y) passes 8e37; gelu is within (10 + v^2) *
+ * 2^-23 of it, and zero below -13.1.
  * x and w: 16-byte aligned, strides multiples of 8.  ws: 256 bytes (the error
  * header). */
 moe_status_t moe_linear(const moe_linear_t* l, const void* x, int64_t x_stride, const void* w,

@@ -432,6 +432,30 @@ __device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float lo, float hi) {
       __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3));
 }
 
+// gelu, v Phi(v) with the normal distribution Phi, to within (10 + v^2) 2^-23 of it.
+// With a = |v| and t = 1 / (1 + 0.4 a), Phi(-a) = t 2^(P(t) - a^2 log2(e) / 2): what erfc
+// is without its exponential, over t, is smooth in t, and P its logarithm's Chebyshev
+// fit of degree 8 up to a = 14, off by 1.5 * 2^-24.  (1 + erf cancels below zero, 4%
+// off at -5.  moe_linear, M = N = K = 4096: 83 us, with erfcf 141.)
+__device__ __forceinline__ float gelu(float v) {
+  const float a = fabsf(v);
+  float t, e;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(fmaf(a, 0.4f, 1.0f)));
+  const float u = t - 0.6f;
+  float p = 0.276698917f;
+  p = fmaf(p, u, -0.0880540088f);
+  p = fmaf(p, u, -0.330344349f);
+  p = fmaf(p, u, 0.27729553f);
+  p = fmaf(p, u, 0.2349433f);
+  p = fmaf(p, u, -0.524225831f);
+  p = fmaf(p, u, -0.177062914f);
+  p = fmaf(p, u, 1.7519269f);
+  p = fmaf(p, u, -1.64642811f);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(a * a, -0.721347520f, p)));
+  const float below = t * e;  // Phi(-a)
+  return v * (v > 0.f ? 1.0f - below : below);
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 

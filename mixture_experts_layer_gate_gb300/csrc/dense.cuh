@@ -278,7 +278,7 @@ __device__ __forceinline__ float activated(const float (&act)[2], float v) {
     const float y = v * fmaf(fminf(v * v, 1e30f), act[1], act[0]);
     return __fdividef(v, 1.0f + __expf(-y));
   }
-  return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+  return gelu(v);
 }
 __device__ __forceinline__ float bias_at(const EpilogueParams& p, int col) {
   const uint16_t b = static_cast<const uint16_t*>(p.bias)[col];

@@ -29,7 +29,7 @@ __device__ __forceinline__ uint4 load_weights(const uint4* p) {
 __device__ __forceinline__ float activate(float v, int act) {
   switch (act) {
     case 1: return v / (1.0f + expf(-v));
-    case 2: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    case 2: return gelu(v);
     case 3: return v / (1.0f + expf(-v * fmaf(v * v, 0.044715f * 1.5957691216057308f, 1.5957691216057308f)));
     case 4: return v < 0.f ? 0.f : v;
     default: return v;

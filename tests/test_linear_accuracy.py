@@ -1,0 +1,33 @@
+"""moe_linear where float arithmetic is tried hardest: gelu's tail below zero."""
+import math
+
+import pytest
+import torch
+
+import mixture_experts_layer_gate_gb300 as moe
+from tests import op_reference as ref
+from tests.op_reference import EPS32
+from tests.test_operators import dev, lib  # noqa: F401  (fixtures)
+
+gpu = pytest.mark.gpu
+
+
+@gpu
+@pytest.mark.parametrize("M", [3, 200, 700])
+def test_gelu_keeps_its_bits_below_zero(dev, M):
+    """v Phi(v) to a relative bound, in steps of 2^-24.  Phi(-a) = t 2^(P(t) - a^2 log2(e) / 2) with t = 1 / (1 + 0.4 a):
+    t is off by 1 step (its denominator) and 2 (a reciprocal's ulp), which Phi(-a) takes at most twice (its logarithm's
+    slope over t's: 0.8 / 0.4 at a = 0, less beyond); P by 1.5 of its fit and 3 of its roundings; the exponent by those of
+    a^2, its factor and its sum (0.75 + 0.5 steps of v^2, and 1.8 of P); 2^x by 4 (2 ulp); two products by 1 each: 18.3 +
+    1.25 v^2."""
+    N, K = 256, 32
+    x, w = torch.zeros(M, K).bfloat16(), torch.zeros(N, K).bfloat16()
+    x[:, 0] = 1
+    w[:, 0] = torch.linspace(-12.5, 12.5, N).bfloat16()
+    w[3, 0], w[4, 0], w[5, 0] = -5.0, -5.5, -0.0
+    out = torch.empty(M, N, device=dev)
+    moe.linear(moe.linear_problem(M, N, K, out_dtype="f32", activation="gelu"), x.to(dev), w.to(dev), out,
+               moe.alloc_op_workspace(dev))
+    v = w[:, 0].double().expand(M, N)
+    want = v * torch.special.erfc(-v / math.sqrt(2.0)) / 2
+    ref.check(out, want, (2 * v * v + 20) * EPS32 * want.abs(), "gelu")
