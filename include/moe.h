@@ -517,7 +517,8 @@ typedef struct {
 
 /* 16-bit product with its epilogue (projections, dense layers):
  *   out[m, n] = act(sum_k x[m, k] w[n, k] + bias[n]) + residual[m, n]
- * in float, rounded once into out.  bias [N] and residual [M, N] or NULL
+ * in float (a tensor core's own sums take up to 2048 products), rounded once into
+ * out.  bias [N] and residual [M, N] or NULL
  * (residual may be out with its stride).  act: silu(v) = v / (1 + exp(-v)), gelu(v)
  * = v (1 + erf(v / sqrt 2)) / 2, its tanh form v (1 + tanh(sqrt(2 / pi) (v +
  * 0.044715 v^3))) / 2, relu; a NaN stays one.  silu and the tanh form are

@@ -10,7 +10,7 @@
 // scales of its block, to the tile's sums, which stay in registers.  The 8-bit
 // product joins every k-block, which is its scale block; the router's every 16
 // (1024 values), which only bounds the length of the tensor core's own sums, and
-// moe_linear's none before the tile's end.
+// moe_linear's every 32 (2048).
 //
 // PAIR: two CTAs share MMAs of M = 256 (cta_group::2): each loads its own 128
 // rows and half of the columns' weights, which halves the weight traffic from

@@ -316,6 +316,7 @@ struct LinearArgs {
   uint32_t* err;
 };
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
+constexpr int kLinearRun = 2048;  // values of K that a tensor core's sum takes before it is joined in float
 // The same for a few rows.
 constexpr int kLinearFewRows = 8;
 cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t s);

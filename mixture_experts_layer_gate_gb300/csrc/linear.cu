@@ -1,10 +1,11 @@
 // 16-bit product with bias, activation and residual in its epilogue (moe_linear):
 // out = act(x w^T + bias) + residual, on the dense kernel with 16-bit operands.
 // The sums are in registers when the tile ends, so bias and activation are applied
-// there, and the residual's boxes are fetched by TMA before that.  A tile's whole K is
-// one accumulator: nothing is joined before the tile's end, which the next tile's
-// products overlap (M = N = K = 4096 with a residual 104 us against 119 joined every
-// 1024 of K).  In a graph, M = N = K = 4096 78 us = 1.76 PFLOP/s, 91% of cuBLAS's rate
+// there, and the residual's boxes are fetched by TMA before that.  An accumulator takes
+// 2048 of K and is joined in float while the next one fills: the tensor core cuts off what
+// its own sum does not hold, so that sums of one sign are 2.4e-6 off after 2048, 7.9e-6
+// after 4096, 2.5e-5 after 8192 and 6.5e-5 after 16384 (f32 output; the times are the same).
+// In a graph, M = N = K = 4096 78 us = 1.76 PFLOP/s, 91% of cuBLAS's rate
 // alone, with a residual 83; N = 6144 114 us.  CTA pairs: single CTAs of 128 by 256
 // took 91 us, bound by their reads from L2.  Up to 8 rows go through a kernel that
 // streams the weights (linear_few.cu).
@@ -27,7 +28,7 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
   p.M = a.M;
   p.N = a.N;
   p.KB = (a.K + 63) / 64;
-  p.group = p.KB;
+  p.group = std::min(p.KB, kLinearRun / 64);
   p.fmt = a.f16 ? 0 : 1;
   p.out_dtype = a.out_dtype;
   p.accumulate = a.residual != nullptr;

@@ -51,7 +51,8 @@ __global__ void __launch_bounds__(kThreads, 3) linear_few_kernel(const LinearArg
   const uint16_t* w0 = static_cast<const uint16_t*>(a.w) + static_cast<int64_t>(min(n0 + g, a.N - 1)) * a.w_stride;
   const uint16_t* w1 = static_cast<const uint16_t*>(a.w) + static_cast<int64_t>(min(n0 + g + 8, a.N - 1)) * a.w_stride;
   const uint16_t* x = static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(min(g, a.M - 1)) * a.x_stride;
-  float acc[4] = {};
+  float acc[4] = {}, sum[4] = {};
+  int run = 0;
   const uint4 none = make_uint4(0, 0, 0, 0);
   uint4 p[kAhead], q[kAhead];
   pdl_wait();
@@ -76,11 +77,19 @@ __global__ void __launch_bounds__(kThreads, 3) linear_few_kernel(const LinearArg
       mma16816<F16>(acc, u.z, v.z, u.w, v.w, b.z, b.w);
       fetch(s + kWarps * kAhead, p[i], q[i]);
     }
+    if (++run == kLinearRun / (32 * kAhead)) {  // (a tensor core's sum is joined in float)
+      run = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sum[e] += acc[e];
+        acc[e] = 0.f;
+      }
+    }
   }
-  red[warp][g][2 * c] = acc[0];
-  red[warp][g][2 * c + 1] = acc[1];
-  red[warp][g + 8][2 * c] = acc[2];
-  red[warp][g + 8][2 * c + 1] = acc[3];
+  red[warp][g][2 * c] = sum[0] + acc[0];
+  red[warp][g][2 * c + 1] = sum[1] + acc[1];
+  red[warp][g + 8][2 * c] = sum[2] + acc[2];
+  red[warp][g + 8][2 * c + 1] = sum[3] + acc[3];
   __syncthreads();
   const int n = n0 + (tid & 15), m = tid >> 4;
   if (m < a.M && n < a.N) {

@@ -1,4 +1,4 @@
-"""moe_linear where float arithmetic is tried hardest: gelu's tail below zero."""
+"""moe_linear where float arithmetic is tried hardest: gelu's tail below zero, and long sums of one sign."""
 import math
 
 import pytest
@@ -6,8 +6,8 @@ import torch
 
 import mixture_experts_layer_gate_gb300 as moe
 from tests import op_reference as ref
-from tests.op_reference import EPS32
-from tests.test_operators import dev, lib  # noqa: F401  (fixtures)
+from tests.op_reference import EPS32, TRUNC32
+from tests.test_operators import dev, gen, lib  # noqa: F401  (fixtures among them)
 
 gpu = pytest.mark.gpu
 
@@ -31,3 +31,19 @@ def test_gelu_keeps_its_bits_below_zero(dev, M):
     v = w[:, 0].double().expand(M, N)
     want = v * torch.special.erfc(-v / math.sqrt(2.0)) / 2
     ref.check(out, want, (2 * v * v + 20) * EPS32 * want.abs(), "gelu")
+
+
+@gpu
+@pytest.mark.parametrize("K", [4096, 16384, 32768])
+@pytest.mark.parametrize("M", [5, 40, 2000])
+def test_long_sums_of_one_sign(dev, M, K):
+    """The tensor core's own sums, 16 products a step and each perhaps truncated, stay bounded however long K is: 2048
+    values (128 steps, each off by 2^-23 of the sum so far, which grows evenly: half of that of the whole on average).
+    Then they are joined in float, one after the other (2^-24 of the sum so far), and so are at most 8 parts of K."""
+    N, g = 300, gen(M + K)
+    x, w = ((torch.rand(n, K, generator=g) + 0.5).bfloat16() for n in (M, N))
+    out = torch.empty(M, N, device=dev)
+    moe.linear(moe.linear_problem(M, N, K, out_dtype="f32"), x.to(dev), w.to(dev), out, moe.alloc_op_workspace(dev))
+    want = x.double() @ w.double().T
+    steps = 128 / 2 + K / 2048 / 4 + 16
+    ref.check(out, want, steps * TRUNC32 * want.abs(), "out")
