@@ -507,7 +507,7 @@ moe_status_t moe_forward_few(const moe_problem_t* p, const moe_weights_t* w, con
 
 typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SILU = 1, MOE_ACT_GELU = 2, MOE_ACT_GELU_TANH = 3, MOE_ACT_RELU = 4 } moe_activation_t;
 
-/* M rows against N weight rows of depth K: M, N >= 0, K % 8 == 0, K >= 8. */
+/* M rows against N weight rows of depth K: 0 <= M, N <= 2^22, K % 8 == 0, 8 <= K <= 2^30. */
 typedef struct {
   int32_t M, N, K;
   int32_t dtype;      /* MOE_T_BF16 or MOE_T_F16, of x, w and bias */

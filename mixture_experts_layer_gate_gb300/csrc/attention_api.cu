@@ -177,7 +177,7 @@ moe_status_t moe_linear(const moe_linear_t* l, const void* x, int64_t x_stride, 
   if (l == nullptr || l->M < 0 || l->N < 0 || l->K < 8 || l->K % 8 != 0) return MOE_ERR_INVALID_ARG;
   if (!half_dtype(l->dtype) || !is_dtype(l->out_dtype)) return MOE_ERR_INVALID_ARG;
   if (l->activation < MOE_ACT_NONE || l->activation > MOE_ACT_RELU) return MOE_ERR_INVALID_ARG;
-  if (l->M > (1 << 22) || l->N > (1 << 22)) return MOE_ERR_UNSUPPORTED;
+  if (l->M > (1 << 22) || l->N > (1 << 22) || l->K > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   MOE_TRY(check_header(ws, ws_bytes));
   if (l->M == 0 || l->N == 0) return MOE_OK;
   if (!wide_rows(x, x_stride, l->K) || !wide_rows(w, w_stride, l->K) || !aligned(bias, 2)) return MOE_ERR_INVALID_ARG;

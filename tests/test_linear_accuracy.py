@@ -1,4 +1,5 @@
-"""moe_linear where float arithmetic is tried hardest: gelu's tail below zero, and long sums of one sign."""
+"""moe_linear where float arithmetic is tried hardest, gelu's tail below zero and long sums of one sign, and depths that
+its indexes do not take."""
 import math
 
 import pytest
@@ -7,6 +8,7 @@ import torch
 import mixture_experts_layer_gate_gb300 as moe
 from tests import op_reference as ref
 from tests.op_reference import EPS32, TRUNC32
+from tests.test_linear import UNSUPPORTED, call
 from tests.test_operators import dev, gen, lib  # noqa: F401  (fixtures among them)
 
 gpu = pytest.mark.gpu
@@ -47,3 +49,10 @@ def test_long_sums_of_one_sign(dev, M, K):
     want = x.double() @ w.double().T
     steps = 128 / 2 + K / 2048 / 4 + 16
     ref.check(out, want, steps * TRUNC32 * want.abs(), "out")
+
+
+def test_refuses_a_depth_past_32_bits(lib):
+    p = moe.linear_problem(5, 96, 64)
+    for K in (2 ** 31 - 8, (1 << 30) + 8):
+        p.K = K
+        assert call(lib, p) == UNSUPPORTED
