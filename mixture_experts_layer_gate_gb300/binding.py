@@ -519,7 +519,8 @@ def rope_table(rot, theta=10000.0, factor=1.0, original=0, low=1.0, high=1.0, in
     """The turns of qk_norm_rope (int64 [rot / 2], in 2^-64 of a turn a position): pair i turns theta^(-2 i / rot)
     radians a position (or inv_freq[i], float64), for a context stretched `factor` times as g f + (1 - g) f / factor.
     Without `original` g = 0: every frequency is divided.  With it, g goes from 0 for pairs of at most `low` turns over
-    the `original` positions to 1 for those of `high` and more."""
+    the `original` positions to 1 for those of `high` and more, in proportion to the turns; a model whose g is in
+    proportion to the pair's index gives its own inv_freq."""
     import math
 
     import torch
@@ -571,7 +572,7 @@ def attention_workspace_size(p: AttentionProblem) -> int:
 
 def alloc_attention_workspace(p: AttentionProblem, device):
     """Zeroed workspace for the attention calls of one stream, of p and of problems with no longer heads and no more
-    new tokens a sequence."""
+    rows a key head (max_q * Hq / Hkv)."""
     import torch
     n = attention_workspace_size(p)
     if n == 0:

@@ -29,12 +29,14 @@
 // weights back), which the other half's products overlap: tensor pipe 65%, issue slots
 // 42% busy.  In a graph, 32 query and 8 key heads of 128, bf16: one prompt of 8192
 // tokens 365 us = 1.5 PFLOP/s, a chunk of 2048 after 6000 tokens 170; over an e4m3
-// cache 250, where the converters' shared-memory traffic and the scales are added (28 + 4
-// heads, 2048 after 30000: 838 us = 1.09 PFLOP/s).  Tiles of 128 keys and two halves
+// cache 249, where the converters' shared-memory traffic and the scales are added (28 + 4
+// heads, 2048 after 30000: 830 us = 1.10 PFLOP/s; heads of 64, 8 key heads, 2048 after
+// 6000 219).  Tiles of 128 keys and two halves
 // fill tensor memory's 512 columns.  All code of an instance stays under 128 KB, what
 // the instruction cache holds: at 149 KB the e4m3 one took twice its time.
 #include "attention.cuh"
 #include "dense.cuh"
+#include "stream.cuh"
 
 namespace moe {
 namespace {
@@ -141,36 +143,6 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int
     }
   }
   return true;
-}
-
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  return (static_cast<uint64_t>(__float_as_uint(b)) << 32) | __float_as_uint(a);
-}
-__device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
-__device__ __forceinline__ float hi2(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
-
-__device__ __forceinline__ float f32_of(uint32_t v, bool f16) {
-  return f16 ? __half2float(__ushort_as_half(static_cast<uint16_t>(v))) : __uint_as_float(v << 16);
-}
-__device__ __forceinline__ uint32_t e4m3x2_half2(uint32_t v) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(v)));
-  return r;
 }
 
 // Byte offset of 16-byte piece c of row r in an operand tile: 64 values (128 bytes) of
@@ -606,7 +578,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
             const uint4 v = dense::lds_u4(from + src);
             const uint32_t q[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[e] = e4m3x2_half2(e & 1 ? q[e >> 1] >> 16 : q[e >> 1] & 0xFFFFu);
+            for (int e = 0; e < 8; ++e) h[e] = e4m3x2_f16x2(e & 1 ? q[e >> 1] >> 16 : q[e >> 1] & 0xFFFFu);
           };
           auto put = [&](uint32_t dst, const uint32_t (&h)[8]) {
             dense::sts_u4(tile + my_f16[0] + dst, make_uint4(h[0], h[1], h[2], h[3]));
@@ -861,12 +833,12 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
             tmem_st16(S + static_cast<uint32_t>(kSome / 2 * part + 16 * c), p);
           }
           sum = add2(sum, add2(sums[0], sums[1]));
-          if (kSome * (part + 1) % 64 == 0) {  // half of the keys' weights
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cta(PFULL(half, kSome * part >= 64));
-          }
+          // (half of the keys' weights)
+          static_assert(kSome == 64, "two parts");
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cta(PFULL(half, part));
         }
         if (E4M3 && lane == 0) mbar_arrive_cta(SCEMPTY(slot));
       }
@@ -969,7 +941,7 @@ attention_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Attn
             const int64_t in = page * a.kv.v_page + place * a.kv.v_token + w->h * a.kv.v_head;
 #pragma unroll 1
             for (int d = 0; d < a.D; ++d) {
-              const float x = E4M3 ? __half2float(__ushort_as_half(static_cast<uint16_t>(e4m3x2_half2(a.kv.v[in + d])))) * vscale
+              const float x = E4M3 ? __half2float(__ushort_as_half(static_cast<uint16_t>(e4m3x2_f16x2(a.kv.v[in + d])))) * vscale
                                    : f32_of(reinterpret_cast<const uint16_t*>(a.kv.v)[in + d], F16);
               if (fabsf(x) < INFINITY) continue;
               if (!whole) {

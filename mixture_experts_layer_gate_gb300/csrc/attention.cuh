@@ -96,8 +96,10 @@ __device__ __forceinline__ int64_t tiles_before(const Seq& s, int G, int r) {
   return sum;
 }
 // How a kernel shares out: rows and keys of a tile; what an item costs beside its
-// tiles, in tiles; runs are no shorter than `least`, and an item is not cut within
-// `slack` of its ends (a cut costs a join).
+// tiles, in tiles; there is a run for every `least` units or a part of them, at most, and
+// an item is not cut within `slack` of its ends (a cut costs a join).  `least` and `slack`
+// were chosen for batches that fill the SMs; of a few short sequences they leave most idle
+// (501 keys, 8 key heads: 10 runs).
 template <int M_, int KT_, int COST_, int SLACK_, int LEAST_>
 struct Shape {
   static constexpr int M = M_, KT = KT_, cost = COST_, slack = SLACK_, least = LEAST_;
@@ -369,6 +371,9 @@ __device__ __forceinline__ float moved(float sum, float d, float f) {
   return sum * h * h;
 }
 
+__device__ __forceinline__ float f32_of(uint16_t v, bool f16) {
+  return f16 ? __half2float(__ushort_as_half(v)) : __uint_as_float(static_cast<uint32_t>(v) << 16);
+}
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);

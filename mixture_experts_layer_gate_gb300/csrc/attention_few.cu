@@ -32,8 +32,8 @@
 //
 // In a graph, 32 query and 8 key heads of 128: 256 sequences of 2000 keys 317 us, 98%
 // of the measured copy's bandwidth; 64 sequences of 100 to 16384 142 us, 89%; with
-// queries as M (16 rows whatever there are) 343 and 155.  e4m3: 256 of 2000 241 us =
-// 4.5 TB/s, bound by the four instructions that a code's conversion takes.
+// queries as M (16 rows whatever there are) 343 and 155.  e4m3: 256 of 2000 232 us =
+// 4.7 TB/s, bound by the four instructions that a code's conversion takes.
 #include "attention.cuh"
 #include "stream.cuh"
 
@@ -88,10 +88,6 @@ template <bool E4M3, int DP>
 __device__ __forceinline__ int v_piece(int key, int piece) {
   if (!E4M3) return piece ^ (key & 7);
   return DP == 128 ? piece ^ (((key >> 1) & 3) << 1) : piece;
-}
-
-__device__ __forceinline__ float f32_of(uint16_t v, bool f16) {
-  return f16 ? __half2float(__ushort_as_half(v)) : __uint_as_float(static_cast<uint32_t>(v) << 16);
 }
 
 // F16: the products' type (8-bit caches: always), else bf16.  NT: column tiles of 8 rows.

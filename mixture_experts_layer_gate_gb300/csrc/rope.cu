@@ -23,25 +23,9 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kAhead = 4;        // loads of a lane in flight
-constexpr int kWarpsPerSm = 48;
+constexpr int kWarpsPerSm = 48;  // asked for; 24 of them run at a time (80 registers)
 
-// Eight values as four pairs of floats, which packed instructions take.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  return (static_cast<uint64_t>(__float_as_uint(b)) << 32) | __float_as_uint(a);
-}
-__device__ __forceinline__ float lo(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
-__device__ __forceinline__ float hi(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
+// (eight values of a head are four pairs of floats)
 template <bool F16>
 __device__ __forceinline__ void unpack8(const uint4& r, uint64_t (&x)[4]) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -49,9 +33,9 @@ __device__ __forceinline__ void unpack8(const uint4& r, uint64_t (&x)[4]) {
   for (int j = 0; j < 4; ++j) {
     if (F16) {
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-      x[j] = pair(f.x, f.y);
+      x[j] = pack2(f.x, f.y);
     } else {
-      x[j] = pair(bf16_lo(w[j]), bf16_hi(w[j]));
+      x[j] = pack2(bf16_lo(w[j]), bf16_hi(w[j]));
     }
   }
 }
@@ -61,10 +45,10 @@ __device__ __forceinline__ uint4 pack8(const uint64_t (&x)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (F16) {
-      const __half2 h = __floats2half2_rn(lo(x[j]), hi(x[j]));
+      const __half2 h = __floats2half2_rn(lo2(x[j]), hi2(x[j]));
       w[j] = *reinterpret_cast<const uint32_t*>(&h);
     } else {
-      w[j] = pack_bf16x2(lo(x[j]), hi(x[j]));
+      w[j] = pack_bf16x2(lo2(x[j]), hi2(x[j]));
     }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
@@ -78,7 +62,7 @@ template <int LANES>
 __device__ __forceinline__ void store_codes(const uint64_t (&x)[4], uint8_t* to, float* scale_to, int lane, bool live, bool first) {
   float amax = 0.f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) amax = max_nan(amax, max_nan(fabsf(lo(x[j])), fabsf(hi(x[j]))));
+  for (int j = 0; j < 4; ++j) amax = max_nan(amax, max_nan(fabsf(lo2(x[j])), fabsf(hi2(x[j]))));
   // only the lanes of this head: others of the warp may have a query
   const uint32_t members = LANES == 32 ? 0xffffffffu : ((1u << (LANES & 31)) - 1u) << (lane & ~(LANES - 1));
 #pragma unroll
@@ -89,7 +73,7 @@ __device__ __forceinline__ void store_codes(const uint64_t (&x)[4], uint8_t* to,
   if (first) *scale_to = scale;
   uint32_t code[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) code[j] = f32x2_to_e4m3x2(__fdiv_rn(lo(x[j]), scale), __fdiv_rn(hi(x[j]), scale));
+  for (int j = 0; j < 4; ++j) code[j] = f32x2_to_e4m3x2(__fdiv_rn(lo2(x[j]), scale), __fdiv_rn(hi2(x[j]), scale));
   *reinterpret_cast<uint2*>(to) = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
 }
 
@@ -165,8 +149,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const RopeArgs a,
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      co[j] = pair(co8[2 * j], co8[2 * j + 1]);
-      si[j] = pair(si8[2 * j], si8[2 * j + 1]);
+      co[j] = pack2(co8[2 * j], co8[2 * j + 1]);
+      si[j] = pack2(si8[2 * j], si8[2 * j + 1]);
     }
   }
   const float per_d = 1.0f / static_cast<float>(D);
@@ -188,7 +172,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const RopeArgs a,
         uint64_t sum2 = mul2(x[0], x[0]);
 #pragma unroll
         for (int j = 1; j < 4; ++j) sum2 = fma2(x[j], x[j], sum2);
-        float sum = lo(sum2) + hi(sum2);
+        float sum = lo2(sum2) + hi2(sum2);
 #pragma unroll
         for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         if (weight != nullptr && mine) {
@@ -201,14 +185,14 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const RopeArgs a,
             unpack8<F16>(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(weight) + e0), w);
           }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = mul2(mul2(x[j], pair(r, r)), w[j]);
+          for (int j = 0; j < 4; ++j) x[j] = mul2(mul2(x[j], pack2(r, r)), w[j]);
         }
       }
       if (pairs > 0) {
         uint64_t y[4];  // the other of each value's pair
         if (INTERLEAVED) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) y[j] = pair(hi(x[j]), lo(x[j]));
+          for (int j = 0; j < 4; ++j) y[j] = pack2(hi2(x[j]), lo2(x[j]));
         } else if ((pairs & 7) == 0) {
           // from the lane that holds the other half's chunk
           const int from = lane + (e0 < pairs ? pairs / 8 : -(pairs / 8));
@@ -219,8 +203,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const RopeArgs a,
           float* buf = spare[threadIdx.x >> 5];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            buf[lane * 9 + 2 * j] = lo(x[j]);
-            buf[lane * 9 + 2 * j + 1] = hi(x[j]);
+            buf[lane * 9 + 2 * j] = lo2(x[j]);
+            buf[lane * 9 + 2 * j + 1] = hi2(x[j]);
           }
           __syncwarp();
           float z[8];
@@ -230,7 +214,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const RopeArgs a,
             z[j] = buf[((lane & ~(LANES - 1)) + (other >> 3)) * 9 + (other & 7)];
           }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) y[j] = pair(z[2 * j], z[2 * j + 1]);
+          for (int j = 0; j < 4; ++j) y[j] = pack2(z[2 * j], z[2 * j + 1]);
           __syncwarp();
         }
         uint64_t z[4];
@@ -242,7 +226,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const RopeArgs a,
         } else {  // the end of the rotated part
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            x[j] = pair(e0 + 2 * j < a.rot ? lo(z[j]) : lo(x[j]), e0 + 2 * j + 1 < a.rot ? hi(z[j]) : hi(x[j]));
+            x[j] = pack2(e0 + 2 * j < a.rot ? lo2(z[j]) : lo2(x[j]), e0 + 2 * j + 1 < a.rot ? hi2(z[j]) : hi2(x[j]));
         }
       }
       if (query) {
@@ -286,7 +270,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const RopeArgs a,
 
 template <bool F16, int LANES, bool NORM, bool INTERLEAVED>
 cudaError_t launch(const RopeArgs& a, cudaStream_t s) {
-  // A token's heads by one warp, or by several where the tokens would leave SMs idle:
+  // A token's heads by one warp, or by several where there are fewer tokens than
   // kWarpsPerSm warps an SM.
   constexpr int kHeads = 32 / LANES;
   const int passes = (a.Hq + a.Hkv + kHeads - 1) / kHeads;
