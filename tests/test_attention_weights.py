@@ -51,7 +51,7 @@ def attend(q, k, codes, scales, past, scale, half, least=LEAST):
 
 
 def same(a, b):
-    return torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    return torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
 
 
 SIZES = [(4, 200), (8, 130), (3, 6000), (100, 300), (200, 200), (130, 5000)]
@@ -72,6 +72,24 @@ def test_unseen_value_scale(dev, new, L, power):
         out, lse, _ = run(problem, broken, dev)
         assert same(out[:first], clean[:first]) and same(lse[:first], clean_lse[:first])
         assert bool(torch.isfinite(out).all()) and not same(out[first:], clean[first:])
+
+
+@gpu
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("new,L", SIZES)
+def test_unseen_value_scale_that_is_not_finite(dev, new, L, bad):
+    problem, args, *_ = build(dev, [new], [L], 4, 2, 128, "bf16", "e4m3", 16, "head", spare=0)
+    clean, clean_lse, _ = run(problem, args, dev)
+    at, first = L - 1 - new // 2, new - 1 - new // 2
+    broken = dict(args, v_scale=args["v_scale"].clone())
+    broken["v_scale"][int(args["page_table"][0, at // 16]), 1, at % 16] = bad
+    out, lse, _ = run(problem, broken, dev)
+    assert same(out[:first], clean[:first]) and same(lse[:first], clean_lse[:first])
+    # heads 2 and 3 read value head 1, whose weights, and so the logarithm of their sum, do not depend on it
+    out, clean = out.view(new, 4, 128), clean.view(new, 4, 128)
+    assert same(out[:, :2], clean[:, :2]) and not bool(torch.isfinite(out[first:, 2:]).any())
+    assert same(lse[:, :2], clean_lse[:, :2])
+    assert bool(((lse - clean_lse).abs() <= 2.0 ** -17 * (1 + clean_lse.abs())).all())
 
 
 def scaled_case(dev, new, L, change):
